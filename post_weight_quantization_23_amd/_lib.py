@@ -1,4 +1,5 @@
-"""ctypes loader for libgptq_mi355x.so (the C ABI in include/gptq.h).
+"""ctypes loader for libgptq_mi355x.so (the C ABI in include/gptq.h and
+include/gptq_adapter.h).
 
 There is no fallback: if the library is missing or does not load, every entry
 point raises.  Build it with `python -m post_weight_quantization_23_amd.build`.
@@ -15,7 +16,7 @@ GPTQ_F32, GPTQ_BF16, GPTQ_F16 = 0, 1, 2
 STATUS = {0: "GPTQ_OK", 1: "GPTQ_EINVAL", 2: "GPTQ_EDTYPE", 3: "GPTQ_ESHAPE", 4: "GPTQ_EALIGN",
           5: "GPTQ_EUNSUPPORTED", 6: "GPTQ_EWORKSPACE", 7: "GPTQ_EHIP"}
 
-# name -> (restype, argtypes), mirroring include/gptq.h
+# name -> (restype, argtypes), mirroring include/gptq.h and include/gptq_adapter.h
 _P = C.c_void_p
 _I64 = C.c_int64
 _SZ = C.c_size_t
@@ -35,6 +36,19 @@ SIGNATURES = {
     "gptq_linear_forward": (C.c_int, [_P, C.c_int, _I64, _I64, _I64, _P, C.c_int, _I64, _I64, C.c_int, _P, _I64,
                                       _P, C.c_int, _I64, _P]),
     "gptq_round16": (C.c_int, [_P, _I64, _I64, _I64, C.c_int, _P, _I64, _P]),
+    # include/gptq_adapter.h
+    "gptq_packed_linear_workspace_size": (C.c_int, [_I64, _I64, _I64, C.c_int, _SZP]),
+    "gptq_packed_linear": (C.c_int, [_P, C.c_int, _I64, _I64, _P, _I64, _I64, C.c_int, _I64, _P, _P, _I64, _I64, _P,
+                                     _P, _P, _I64, _I64, _P, _P, _P, C.c_int, _I64, _P, _SZ, _P]),
+    "gptq_packed_linear_backward_workspace_size": (C.c_int, [_I64, _I64, _I64, _I64, _I64, _SZP]),
+    "gptq_packed_linear_backward": (C.c_int, [_P, C.c_int, _I64, _I64, _P, _I64, _I64, C.c_int, _I64, _P, _P, _I64,
+                                              _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, C.c_int, _I64, _P, _SZ, _P]),
+    "gptq_adapter_add_workspace_size": (C.c_int, [_I64, _I64, _SZP]),
+    "gptq_adapter_add": (C.c_int, [_P, C.c_int, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P, C.c_int, _I64,
+                                   _P, _I64, _P, _SZ, _P]),
+    "gptq_adapter_backward_workspace_size": (C.c_int, [_I64, _I64, _I64, _I64, _I64, _SZP]),
+    "gptq_adapter_backward": (C.c_int, [_P, _I64, _P, _I64, C.c_int, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P,
+                                        _P, _P, _P, C.c_int, _I64, _P, _SZ, _P]),
     "gptq_build_id": (C.c_char_p, []),
     "gptq_status_string": (C.c_char_p, [C.c_int]),
     "gptq_last_error": (C.c_char_p, []),

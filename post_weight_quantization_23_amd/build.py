@@ -28,7 +28,8 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 # slowest first: the pool starts them at once
 SOURCES = ["quantize.hip", "linear.hip", "gemm_f32.hip", "syrk.hip", "gemv.hip", "prepare.hip",
-           "hadamard.hip", "pack.hip", "gptq_api.hip", "workspace.hip"]
+           "hadamard.hip", "pack.hip", "packed_linear.hip", "packed_backward.hip", "adapter.hip", "gptq_api.hip",
+           "adapter_api.hip", "workspace.hip"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
@@ -39,14 +40,18 @@ COMMON_FLAGS = [
 
 
 HEADERS = [os.path.join(CSRC, "common.hpp"), os.path.join(CSRC, "kernels.hpp")]
-API_HEADER = os.path.join(ROOT, "include", "gptq.h")   # included by gptq_api.hip only
+API_HEADERS = [os.path.join(ROOT, "include", "gptq.h"), os.path.join(ROOT, "include", "gptq_adapter.h")]
+# headers that only some sources include
+MORE_HEADERS = {"gptq_api.hip": [os.path.join(CSRC, "api.hpp"), *API_HEADERS],
+                "adapter_api.hip": [os.path.join(CSRC, "api.hpp"), os.path.join(CSRC, "adapter.hpp"), *API_HEADERS],
+                **{f: [os.path.join(CSRC, "adapter.hpp")] for f in ("packed_linear.hip", "packed_backward.hip", "adapter.hip")}}
 
 
 def source_id() -> str:
     """SHA-256 over every file the library is built from (names and contents)."""
     h = hashlib.sha256()
     files = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hip", ".hpp")))
-    files.append(os.path.join(ROOT, "include", "gptq.h"))
+    files += API_HEADERS
     for path in files:
         h.update(os.path.relpath(path, ROOT).encode())
         with open(path, "rb") as f:
@@ -56,7 +61,7 @@ def source_id() -> str:
 
 def _object_key(src: str) -> str:
     h = hashlib.sha256(" ".join(COMMON_FLAGS).encode())
-    for path in [os.path.join(CSRC, src), *HEADERS, *([API_HEADER] if src == "gptq_api.hip" else [])]:
+    for path in [os.path.join(CSRC, src), *HEADERS, *MORE_HEADERS.get(src, [])]:
         with open(path, "rb") as f:
             h.update(f.read())
     return h.hexdigest()

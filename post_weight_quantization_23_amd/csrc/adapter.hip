@@ -1,0 +1,311 @@
+// Low-rank adapters of many requests beside a shared projection:
+//     delta[t, i] = alpha_a sum_p B_a[i, p] sum_k A_a[p, k] X[t, k],  a = index[t]
+// and their gradients
+//     gA_a[p, k] = alpha_a sum_t (dY B_a)[t, p] X[t, k]
+//     gB_a[i, p] = alpha_a sum_t dY[t, i] (A_a X)[t, p]     (t over a's tokens).
+// The product through the rank is two products: down (X to rank values per
+// token, fp32, alpha multiplied in) and up (rank values to the outputs).
+#include "adapter.hpp"
+
+namespace gptq {
+
+namespace {
+
+// ---------------------------------------------------------------- down
+// One wave per (token, rank row): 64 lanes x 8 elements a step, fp32 sums
+// folded over the wave in a fixed order.
+template <int DT>
+__global__ __launch_bounds__(256) void down_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t d, int64_t ldx,
+                                                   Adapters ad, const uint16_t* __restrict__ A, int64_t lda, bool vec,
+                                                   float* __restrict__ S) {
+  const int lane = threadIdx.x & 63;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t t = item / ad.rank;
+  const int p = (int)(item - t * ad.rank);
+  if (t >= n) return;
+  const int a = adapter_of(ad, t, n);
+  float sum = 0.f;
+  if (a >= 0) {
+    const uint16_t* x = X + t * ldx;
+    const uint16_t* w = A + ((int64_t)a * ad.rank + p) * lda;
+    for (int64_t k = 8 * lane; k < d; k += 512) {
+      const u32x4 xv = load8(x + k, (int)min((int64_t)8, d - k), vec);
+      const u32x4 wv = *reinterpret_cast<const u32x4*>(w + k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum = __builtin_fmaf(f16_to_f32<DT>(xv[i] & 0xFFFFu), f16_to_f32<DT>(wv[i] & 0xFFFFu), sum);
+        sum = __builtin_fmaf(f16_to_f32<DT>(xv[i] >> 16), f16_to_f32<DT>(wv[i] >> 16), sum);
+      }
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+    if (ad.alpha) sum *= ad.alpha[a];
+  }
+  if (lane == 0) S[item] = sum;
+}
+
+// ---------------------------------------------------------------- up
+// out = base + S B^T: a wave takes 16 tokens x 64 outputs.
+template <int DT, int YT>
+__global__ __launch_bounds__(256) void up_kernel(const float* __restrict__ S, int64_t n, Adapters ad,
+                                                 const uint16_t* __restrict__ B, int64_t rows, const void* base, int64_t ldb,
+                                                 void* out, int64_t ldo, int64_t col_tiles) {
+  const int lane = threadIdx.x & 63;
+  const int64_t tile = blockIdx.x / col_tiles, ct = blockIdx.x - tile * col_tiles;
+  const int64_t t0 = tile * 16, j0 = ct * 256 + 64 * (threadIdx.x >> 6);
+  int64_t row[4];
+  floatx4 acc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t j = j0 + 16 * q + (lane & 15);
+    row[q] = j < rows ? j : -1;
+    acc[q] = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
+  expand_add<DT, 4>(ad, B, rows, S, t0, n, row, acc);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + 4 * (lane >> 4) + i;
+      if (t >= n || row[q] < 0) continue;
+      float v = acc[q][i];
+      if (base) {
+        const int64_t at = t * ldb + row[q];
+        if constexpr (YT == 0) v += static_cast<const float*>(base)[at];
+        else v += f16_to_f32<YT>(static_cast<const uint16_t*>(base)[at]);
+      }
+      store_out<YT>(out, t * ldo + row[q], v);
+    }
+}
+
+// ---------------------------------------------------------------- transpose
+__global__ __launch_bounds__(256) void transpose16_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t cols,
+                                                          uint16_t* __restrict__ dst, int64_t ldd, int64_t row_tiles) {
+  __shared__ uint16_t tile[64][66];
+  const int64_t bt = blockIdx.x / row_tiles, rt = blockIdx.x - bt * row_tiles;
+  const int64_t ct_n = (cols + 63) / 64;
+  const int64_t a = bt / ct_n, ct = bt - a * ct_n;
+  const int64_t i0 = rt * 64, j0 = ct * 64;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int r = w; r < 64; r += 4) {
+    const int64_t i = i0 + r, j = j0 + lane;
+    tile[r][lane] = (i < rows && j < cols) ? src[(a * rows + i) * cols + j] : (uint16_t)0;
+  }
+  __syncthreads();
+  for (int r = w; r < 64; r += 4) {
+    const int64_t j = j0 + r, i = i0 + lane;
+    if (j < cols && i < ldd) dst[(a * cols + j) * ldd + i] = tile[lane][r];
+  }
+}
+
+// ---------------------------------------------------------------- token lists
+// Workgroup a lists its adapter's tokens in ascending order after the tokens
+// of the adapters before it: it counts those, then places its own by a prefix
+// over the workgroup.  No atomics, so the order is fixed.
+__global__ __launch_bounds__(1024) void token_lists_kernel(Adapters ad, int64_t n, int32_t* __restrict__ order,
+                                                           int32_t* __restrict__ start) {
+  __shared__ int below[16];
+  __shared__ int count[16];
+  const int a = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int less = 0;
+  for (int64_t t = threadIdx.x; t < n; t += 1024) {
+    const int v = adapter_of(ad, t, n);
+    less += v >= 0 && v < a;
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) less += __shfl_xor(less, m);
+  if (lane == 0) below[w] = less;
+  __syncthreads();
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) at += below[i];
+  if (threadIdx.x == 0) start[a] = at;
+  for (int64_t t0 = 0; t0 < n; t0 += 1024) {
+    const int64_t t = t0 + threadIdx.x;
+    const bool in = adapter_of(ad, t, n) == a;
+    const uint64_t mask = __ballot(in);
+    if (lane == 0) count[w] = __popcll(mask);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      before += i < w ? count[i] : 0;
+      all += count[i];
+    }
+    if (in) order[at + before + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)t;
+    at += all;
+    __syncthreads();
+  }
+  if (a == ad.m - 1 && threadIdx.x == 0) start[ad.m] = at;
+}
+
+// ---------------------------------------------------------------- gradients
+// G[p, j] = sum over the adapter's tokens of V[t, p] Z[t, j].  The contraction
+// runs over tokens, along which neither operand is contiguous.  A lane loads 8
+// columns of 8 tokens of Z; column u of them is its operand of the u-th of
+// eight products, whose 16 columns are j0 + 8 (lane & 15) + u: the transpose
+// happens in registers.  Tokens come through the adapter's list, so they may
+// lie in any order; places past its end multiply zeros by zeros.  V is split
+// in two bf16 terms (16 significant bits) and fp16 Z in two, so the gradient
+// keeps fp32's range and an error below 2^-16 of its terms.
+// Workgroup: 4 waves over the tokens of one 128-column block and 16 RT rank
+// rows, joined through LDS in wave order; token splits over the grid write
+// partial results that join_kernel adds in order.
+template <int DT, int RT>
+__global__ __launch_bounds__(256) void grad_kernel(const float* __restrict__ V, const uint16_t* __restrict__ Z, int64_t cols,
+                                                   int64_t ldz, bool vec, int rank, const int32_t* __restrict__ order,
+                                                   const int32_t* __restrict__ start, int up, float* __restrict__ G,
+                                                   int64_t per_split, int64_t col_blocks, int rank_blocks, int splits) {
+  __shared__ float red[16 * RT][128 + 4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, kq = lane >> 4;
+  int64_t b = blockIdx.x;
+  const int64_t cb = b % col_blocks;
+  b /= col_blocks;
+  const int rb = (int)(b % rank_blocks);
+  b /= rank_blocks;
+  const int split = (int)(b % splits);
+  const int a = (int)(b / splits);
+  const int first = start[a], count = start[a + 1] - first;
+  const int64_t j0 = cb * 128 + 8 * m;
+  const int valid = (int)max((int64_t)0, min((int64_t)8, cols - j0));
+  const int p0 = rb * 16 * RT;
+
+  floatx4 acc[RT][8];
+#pragma unroll
+  for (int p = 0; p < RT; ++p)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) acc[p][u] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  const int blocks = (count + 31) / 32;
+  const int each = (blocks + splits - 1) / splits;
+  const int b1 = min(blocks, (split + 1) * each);
+  for (int blk = split * each + wave; blk < b1; blk += 4) {
+    u32x4 z[8];
+    int64_t tok[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = 32 * blk + 8 * kq + e;
+      tok[e] = i < count ? (int64_t)order[first + i] : -1;
+      z[e] = u32x4{0u, 0u, 0u, 0u};
+      if (tok[e] >= 0 && valid > 0) z[e] = load8(Z + tok[e] * ldz + j0, valid, vec);
+    }
+    u32x4 vh[RT], vl[RT];
+#pragma unroll
+    for (int p = 0; p < RT; ++p) {
+      float v[8];
+      const int pr = p0 + 16 * p + m;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (tok[e] >= 0 && pr < rank) ? V[tok[e] * rank + pr] : 0.f;
+      split8(v, vh[p], vl[p]);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      u32x4 f, zh, zl;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        f[e] = __builtin_amdgcn_perm(z[2 * e + 1][u >> 1], z[2 * e][u >> 1], (u & 1) ? 0x07060302u : 0x05040100u);
+      to_bf16_terms<DT>(f, zh, zl);
+#pragma unroll
+      for (int p = 0; p < RT; ++p) acc[p][u] = mfma_split<DT>(vh[p], vl[p], zh, zl, acc[p][u]);
+    }
+  }
+
+  // waves in turn; row of the accumulator = rank, column = 8 (lane & 15) + u
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int p = 0; p < RT; ++p)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float& x = red[16 * p + 4 * kq + i][8 * m + u];
+            x = w == 0 ? acc[p][u][i] : x + acc[p][u][i];
+          }
+    }
+    __syncthreads();
+  }
+  const int64_t m_all = (int64_t)gridDim.x / (col_blocks * rank_blocks * splits);
+  float* g = G + ((int64_t)split * m_all + a) * rank * cols;
+  for (int i = threadIdx.x; i < 16 * RT * 128; i += 256) {
+    int pp, jj;
+    if (up) { jj = i / (16 * RT); pp = i - jj * (16 * RT); }
+    else { pp = i >> 7; jj = i & 127; }
+    const int64_t j = cb * 128 + jj;
+    const int p = p0 + pp;
+    if (j < cols && p < rank) g[up ? j * rank + p : (int64_t)p * cols + j] = red[pp][jj];
+  }
+}
+
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int64_t n, int splits,
+                                                   float* __restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  floatx4 v = *reinterpret_cast<const floatx4*>(part + i);
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const floatx4*>(part + s * n + i);
+  *reinterpret_cast<floatx4*>(out + i) = v;
+}
+
+bool rows_on_16(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+
+}  // namespace
+
+void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ldx, const Adapters& ad, const uint16_t* A,
+                         int64_t lda, float* S, hipStream_t s) {
+  const dim3 grid((unsigned)((n * ad.rank + 3) / 4)), block(256);
+  const bool vec = rows_on_16(X, ldx);
+  const auto* x = static_cast<const uint16_t*>(X);
+  if (xt == kBF16) hipLaunchKernelGGL((down_kernel<kBF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
+  else hipLaunchKernelGGL((down_kernel<kF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
+}
+
+void launch_adapter_up(const float* S, int64_t n, const Adapters& ad, int xt, const uint16_t* B, int64_t rows,
+                       const void* base, int64_t ldb, void* out, int yt, int64_t ldo, hipStream_t s) {
+  const int64_t ct = (rows + 255) / 256;
+  const dim3 grid((unsigned)((n + 15) / 16 * ct)), block(256);
+#define GPTQ_UP(D_, Y_) \
+  hipLaunchKernelGGL((up_kernel<D_, Y_>), grid, block, 0, s, S, n, ad, B, rows, base, ldb, out, ldo, ct)
+  if (xt == kBF16) { if (yt == 0) GPTQ_UP(kBF16, 0); else GPTQ_UP(kBF16, kBF16); }
+  else { if (yt == 0) GPTQ_UP(kF16, 0); else GPTQ_UP(kF16, kF16); }
+#undef GPTQ_UP
+}
+
+void launch_transpose16(const uint16_t* src, int m, int64_t rows, int64_t cols, uint16_t* dst, int64_t ldd, hipStream_t s) {
+  const int64_t rt = (ldd + 63) / 64;
+  hipLaunchKernelGGL(transpose16_kernel, dim3((unsigned)(rt * ((cols + 63) / 64) * m)), dim3(256), 0, s, src, rows, cols, dst,
+                     ldd, rt);
+}
+
+void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, hipStream_t s) {
+  hipLaunchKernelGGL(token_lists_kernel, dim3((unsigned)ad.m), dim3(1024), 0, s, ad, n, order, start);
+}
+
+int adapter_grad_splits(int64_t n, int m, int64_t cols) {
+  const int64_t groups = (cols + 127) / 128 * m;
+  int64_t splits = (512 + groups - 1) / groups;
+  splits = splits < (n + 127) / 128 ? splits : (n + 127) / 128;
+  return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
+}
+
+void launch_adapter_grad(const float* V, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz, const Adapters& ad,
+                         const int32_t* order, const int32_t* start, int up, float* G, float* part, int splits,
+                         hipStream_t s) {
+  const bool vec = rows_on_16(Z, ldz);
+  const int rt = ad.rank <= 16 ? 1 : (ad.rank <= 32 ? 2 : 4);
+  const int rb = (ad.rank + 16 * rt - 1) / (16 * rt);
+  const int64_t cb = (cols + 127) / 128;
+  const dim3 grid((unsigned)(cb * rb * splits * ad.m)), block(256);
+  float* dst = splits > 1 ? part : G;
+  const auto* z = static_cast<const uint16_t*>(Z);
+#define GPTQ_GRAD(D_, R_) \
+  hipLaunchKernelGGL((grad_kernel<D_, R_>), grid, block, 0, s, V, z, cols, ldz, vec, ad.rank, order, start, up, dst, (int64_t)0, cb, rb, splits)
+  if (zt == kBF16) { if (rt == 1) GPTQ_GRAD(kBF16, 1); else if (rt == 2) GPTQ_GRAD(kBF16, 2); else GPTQ_GRAD(kBF16, 4); }
+  else { if (rt == 1) GPTQ_GRAD(kF16, 1); else if (rt == 2) GPTQ_GRAD(kF16, 2); else GPTQ_GRAD(kF16, 4); }
+#undef GPTQ_GRAD
+  if (splits > 1) {
+    const int64_t all = (int64_t)ad.m * ad.rank * cols;   // rank is a multiple of 8: whole vectors
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)((all / 4 + 255) / 256)), dim3(256), 0, s, part, all, splits, G);
+  }
+}
+
+}  // namespace gptq

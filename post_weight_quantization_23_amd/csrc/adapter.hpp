@@ -1,0 +1,232 @@
+// Device helpers and launch interfaces shared by the packed products for many
+// tokens (packed_linear.hip, packed_backward.hip) and the low-rank adapters
+// beside them (adapter.hip).
+#pragma once
+#include "common.hpp"
+
+namespace gptq {
+
+// 16-bit element types: 1 bf16, 2 fp16 (the values of gptq_dtype).
+constexpr int kBF16 = 1, kF16 = 2;
+
+// Low-rank adapters of several requests: A [m][rank][d_in], B [m][d_out][rank],
+// both dense and of the activations' 16-bit type; token t uses adapter
+// index[t] (index null: 0), none when that lies outside 0 .. m-1.
+struct Adapters {
+  const uint16_t* A;
+  const uint16_t* B;
+  const float* alpha;     // null: 1
+  const int32_t* index;   // null: adapter 0 for every token
+  int m, rank;
+};
+
+// A packed layer as gptq_pack / gptq_quantize_layer write it.
+struct PackedLayer {
+  const uint32_t* words;
+  int64_t ldw;
+  const float* scales;
+  const int32_t* zeros;
+  int64_t ldg;
+  const int32_t* perm;    // null: packed column j is input j
+  int bits;
+  int r, c;
+  int cpg;                // 32-column chunks per group (all of them: one ruler per row)
+};
+
+// ---------------------------------------------------------------- 16-bit values
+template <int DT>
+GPTQ_DEV float f16_to_f32(uint32_t bits) {
+  if constexpr (DT == kBF16) return __uint_as_float(bits << 16);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+}
+
+// Round to nearest even; bf16 keeps NaN.
+template <int DT>
+GPTQ_DEV uint16_t f32_to_16(float v) {
+  if constexpr (DT == kBF16) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+template <int DT>
+GPTQ_DEV uint32_t pack2(float lo, float hi) {
+  return (uint32_t)f32_to_16<DT>(lo) | ((uint32_t)f32_to_16<DT>(hi) << 16);
+}
+
+// One output value to a matrix of type yt (0 fp32, 1 bf16, 2 fp16).
+template <int YT>
+GPTQ_DEV void store_out(void* Y, int64_t at, float v) {
+  if constexpr (YT == 0) static_cast<float*>(Y)[at] = v;
+  else static_cast<uint16_t*>(Y)[at] = f32_to_16<YT>(v);
+}
+
+// Eight consecutive 16-bit values of which the first `valid` exist (the rest
+// read as 0).  vec: the address is 16-byte aligned.
+GPTQ_DEV u32x4 load8(const uint16_t* p, int valid, bool vec) {
+  if (vec && valid >= 8) return *reinterpret_cast<const u32x4*>(p);
+  u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < valid) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+  return v;
+}
+
+// 16 x 16 x 32 matrix product: lane l holds A[l & 15][8 (l >> 4) + e] and
+// B[8 (l >> 4) + e][l & 15], and C[4 (l >> 4) + i][l & 15] in component i.
+template <int DT>
+GPTQ_DEV floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
+  if constexpr (DT == kBF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- adapters
+// Adapter of token t, or -1.
+GPTQ_DEV int adapter_of(const Adapters& ad, int64_t t, int64_t n) {
+  if (t >= n) return -1;
+  const int a = ad.index ? ad.index[t] : 0;
+  return (uint32_t)a < (uint32_t)ad.m ? a : -1;
+}
+
+// v = hi + lo + (an error below 2^-17 |v|), hi and lo bf16: an fp32 operand
+// of a bf16 matrix product as two of them.  Every fp16 value is such a sum
+// exactly (11 significant bits against 8 + 8).
+GPTQ_DEV void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = pack2<kBF16>(v0, v1);
+  lo = pack2<kBF16>(v0 - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xFFFF0000u));
+}
+
+GPTQ_DEV void split8(const float (&v)[8], u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h, l;
+    split2(v[2 * i], v[2 * i + 1], h, l);
+    hi[i] = h;
+    lo[i] = l;
+  }
+}
+
+// A 16-bit operand as one (bf16) or two (fp16) bf16 operands.
+template <int DT>
+GPTQ_DEV void to_bf16_terms(u32x4 v, u32x4& hi, u32x4& lo) {
+  if constexpr (DT == kBF16) {
+    hi = v;
+  } else {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = f16_to_f32<kF16>(v[i] & 0xFFFFu);
+      f[2 * i + 1] = f16_to_f32<kF16>(v[i] >> 16);
+    }
+    split8(f, hi, lo);
+  }
+}
+
+// c + V Z for an fp32 operand V = vh + vl and a 16-bit operand Z = zh (+ zl).
+// The terms left out (vl zl) are below 2^-18 of the product.
+template <int DT>
+GPTQ_DEV floatx4 mfma_split(u32x4 vh, u32x4 vl, u32x4 zh, u32x4 zl, floatx4 c) {
+  c = mfma16<kBF16>(vl, zh, c);
+  if constexpr (DT == kF16) c = mfma16<kBF16>(vh, zl, c);
+  return mfma16<kBF16>(vh, zh, c);
+}
+
+// Eight fp32 values (16-byte aligned).
+GPTQ_DEV void load8f(const float* p, float (&v)[8]) {
+  const floatx4 a = *reinterpret_cast<const floatx4*>(p), b = *reinterpret_cast<const floatx4*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+
+// out[q] += (S B_a^T) of 16 tokens t0 .. t0+15 and NT sets of 16 outputs, in
+// the accumulator layout of mfma16 (row = token): the low-rank product beside
+// a tile.  S [n][rank] fp32 already holds alpha; row[q] is this lane's output
+// row (column of the tile) in B [m][rows][rank], or -1.  The adapters that
+// occur among the 16 tokens are taken one after the other, each as a product
+// over all 16, of which only its own tokens' rows are kept: a value that is
+// not finite in one request's adapter or tokens stays in that request's rows.
+template <int DT, int NT>
+GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, const float* S, int64_t t0, int64_t n,
+                         const int64_t (&row)[NT], floatx4 (&out)[NT]) {
+  const int lane = threadIdx.x & 63, kq = lane >> 4;
+  const int64_t t = t0 + (lane & 15);
+  const int mine = adapter_of(ad, t, n);
+  uint32_t rest = (uint32_t)(__ballot(mine >= 0) & 0xFFFFu);
+  while (rest) {
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(rest));
+    const uint32_t members = (uint32_t)(__ballot(mine == a) & 0xFFFFu);
+    rest &= ~members;
+    floatx4 acc[NT];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) acc[q] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < ad.rank; k0 += 32) {
+      const int k = k0 + 8 * kq;
+      u32x4 sh = {0u, 0u, 0u, 0u}, sl = sh;
+      if (k < ad.rank && t < n) {
+        float v[8];
+        load8f(S + t * ad.rank + k, v);
+        split8(v, sh, sl);
+      }
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        u32x4 b = {0u, 0u, 0u, 0u}, bh, bl;
+        if (k < ad.rank && row[q] >= 0)
+          b = *reinterpret_cast<const u32x4*>(B + ((int64_t)a * rows + row[q]) * ad.rank + k);
+        to_bf16_terms<DT>(b, bh, bl);
+        acc[q] = mfma_split<DT>(sh, sl, bh, bl, acc[q]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((members >> (4 * kq + i)) & 1) out[q][i] += acc[q][i];
+  }
+}
+
+// ---------------------------------------------------------------- packed words
+// Eight consecutive codes of a row as one 32-bit block: the word itself (4
+// bits), or bits 24m .. 24m+23 of a chunk's 96 (3 bits).
+template <int BITS>
+GPTQ_DEV uint32_t code_block(const uint32_t* chunk, int m) {
+  if constexpr (BITS == 4) return chunk[m];
+  const int bit = 24 * m, w = bit >> 5;
+  return (__builtin_amdgcn_alignbit(chunk[w < 2 ? w + 1 : 2], chunk[w], bit & 31)) & 0xFFFFFFu;
+}
+
+// ---------------------------------------------------------------- launches
+// xt / dt: 1 bf16, 2 fp16; yt: 0 fp32, 1 bf16, 2 fp16.
+
+// S[t][p] = alpha sum_k X[t][k] A_a[p][k], A with row stride lda (a multiple
+// of 8, zero past d) -- adapter.hip.
+void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ldx, const Adapters& ad, const uint16_t* A,
+                         int64_t lda, float* S, hipStream_t s);
+// out = base + S B^T (base null: 0), out and base [n][rows] of type yt.
+void launch_adapter_up(const float* S, int64_t n, const Adapters& ad, int xt, const uint16_t* B, int64_t rows,
+                       const void* base, int64_t ldb, void* out, int yt, int64_t ldo, hipStream_t s);
+// dst[a][j][i] = src[a][i][j] of m matrices, src [rows][cols] dense, dst row
+// stride ldd >= rows, zero in columns rows .. ldd-1.
+void launch_transpose16(const uint16_t* src, int m, int64_t rows, int64_t cols, uint16_t* dst, int64_t ldd, hipStream_t s);
+// Token lists by adapter: order[start[a] .. start[a+1]) are the tokens of
+// adapter a, ascending.
+void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, hipStream_t s);
+// G[a][p][j] (up == 0) or G[a][j][p] (up == 1) = sum over a's tokens of
+// V[t][p] Z[t][j].  part: workspace of `splits` partial results (splits > 1).
+int adapter_grad_splits(int64_t n, int m, int64_t cols);
+void launch_adapter_grad(const float* V, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz, const Adapters& ad,
+                         const int32_t* order, const int32_t* start, int up, float* G, float* part, int splits,
+                         hipStream_t s);
+
+// Y = X W_hat^T (+ S B^T): packed_linear.hip.
+void launch_packed_linear(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad,
+                          const float* S, void* Y, int yt, int64_t ldy, hipStream_t s);
+// dst[t][j] = X[t][perm[j]] (entries outside 0 .. c-1 clamped), dst dense.
+void launch_gather_columns(const void* X, int64_t n, int64_t c, int64_t ldx, const int32_t* perm, void* dst, hipStream_t s);
+// dX = dY W_hat (+ T A): packed_backward.hip.  At: A transposed to [m][c][rank].
+void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, const PackedLayer& w, const Adapters& ad,
+                            const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, hipStream_t s);
+
+}  // namespace gptq

@@ -1,0 +1,395 @@
+// C ABI of the packed products for many tokens and of the low-rank adapters
+// (declared in include/gptq_adapter.h).  As in gptq_api.hip every argument is
+// validated on the host before anything is enqueued.
+#include <cstdio>
+#include <utility>
+
+#include "../../include/gptq_adapter.h"
+#include "adapter.hpp"
+#include "api.hpp"
+
+using namespace gptq::api;
+
+namespace {
+
+constexpr int64_t kMaxCols = int64_t(1) << 30;
+constexpr int64_t kMaxAdapters = int64_t(1) << 20;
+
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
+int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
+
+gptq_status need_ws(const char* fn, const void* ws, size_t have, int64_t need) {
+  char text[80];
+  snprintf(text, sizeof text, "workspace needs %lld bytes", (long long)need);
+  if (need > 0 && (!ws || have < (size_t)need)) return fail(GPTQ_EWORKSPACE, fn, text);
+  if (need > 0 && !aligned(ws, 256)) return fail(GPTQ_EALIGN, fn, "workspace not 256-byte aligned");
+  return GPTQ_OK;
+}
+
+// Pieces of a workspace, each 256-byte aligned.
+struct Carve {
+  char* at;
+  template <class T>
+  T* take(int64_t bytes) {
+    T* p = reinterpret_cast<T*>(at);
+    at += align256(bytes);
+    return p;
+  }
+};
+
+// Sizes that every call shares; keeps products of them inside 63 bits.
+gptq_status check_sizes(const char* fn, int64_t n, int64_t r, int64_t c, int64_t c_unit) {
+  if (n < 0 || r < 0 || c < 0) return fail(GPTQ_EINVAL, fn, "negative size");
+  if (n > kMaxRows || r > kMaxRows || c > kMaxCols) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (c == 0 || c % c_unit != 0)
+    return fail(GPTQ_ESHAPE, fn, c_unit == 32 ? "c must be a positive multiple of 32" : "c must be a positive multiple of 8");
+  return GPTQ_OK;
+}
+
+gptq_status check_rank(const char* fn, int64_t m, int64_t rank) {
+  if (m < 1) return fail(GPTQ_EINVAL, fn, "n_adapters must be positive");
+  if (m > kMaxAdapters) return fail(GPTQ_EUNSUPPORTED, fn, "too many adapters");
+  if (rank < 8 || rank > 128 || rank % 8 != 0) return fail(GPTQ_EUNSUPPORTED, fn, "rank must be a multiple of 8 in 8 .. 128");
+  return GPTQ_OK;
+}
+
+gptq_status check_adapters(const char* fn, const void* A, const void* B, int64_t m, int64_t rank, const int32_t* index,
+                           const float* alpha) {
+  if (gptq_status st = check_rank(fn, m, rank)) return st;
+  if (!A || !B) return fail(GPTQ_EINVAL, fn, "A or B is NULL");
+  if (!aligned(A, 16) || !aligned(B, 16)) return fail(GPTQ_EALIGN, fn, "A and B must be 16-byte aligned");
+  if (!aligned(index, 4) || !aligned(alpha, 4)) return fail(GPTQ_EALIGN, fn, "misaligned index or alpha");
+  return GPTQ_OK;
+}
+
+gptq::Adapters adapters(const void* A, const void* B, int64_t m, int64_t rank, const int32_t* index, const float* alpha) {
+  gptq::Adapters ad{};
+  if (A) {
+    ad.A = static_cast<const uint16_t*>(A);
+    ad.B = static_cast<const uint16_t*>(B);
+    ad.alpha = alpha;
+    ad.index = index;
+    ad.m = (int)m;
+    ad.rank = (int)rank;
+  }
+  return ad;
+}
+
+gptq_status check_packed(const char* fn, const uint32_t* packed, int64_t c, int bits, int64_t ld_words, const float* scales,
+                         const int32_t* zeros, int64_t ld_groups, int64_t groupsize, const int32_t* perm) {
+  if (bits != 3 && bits != 4) return fail(GPTQ_EUNSUPPORTED, fn, "bits must be 3 or 4");
+  const bool grouped = groupsize > 0 && groupsize < c;
+  if (grouped && groupsize % 32 != 0) return fail(GPTQ_EUNSUPPORTED, fn, "groupsize must be a multiple of 32");
+  if (ld_words < c / 32 * bits) return fail(GPTQ_ESHAPE, fn, "ld_words < c * bits / 32");
+  if (ld_groups < (grouped ? (c + groupsize - 1) / groupsize : 1)) return fail(GPTQ_ESHAPE, fn, "ld_groups < number of groups");
+  if (!packed || !scales || !zeros) return fail(GPTQ_EINVAL, fn, "a required pointer is NULL");
+  if (bits == 4 && (!aligned(packed, 16) || ld_words % 4 != 0))
+    return fail(GPTQ_EALIGN, fn, "4-bit words need a 16-byte aligned base and ld_words % 4 == 0");
+  if (!aligned(packed, 4) || !aligned(scales, 4) || !aligned(zeros, 4) || !aligned(perm, 4))
+    return fail(GPTQ_EALIGN, fn, "misaligned pointer");
+  return GPTQ_OK;
+}
+
+gptq::PackedLayer layer(const uint32_t* packed, int64_t r, int64_t c, int bits, int64_t ld_words, const float* scales,
+                        const int32_t* zeros, int64_t ld_groups, int64_t groupsize, const int32_t* perm) {
+  gptq::PackedLayer w;
+  w.words = packed;
+  w.ldw = ld_words;
+  w.scales = scales;
+  w.zeros = zeros;
+  w.ldg = ld_groups;
+  w.perm = perm;
+  w.bits = bits;
+  w.r = (int)r;
+  w.c = (int)c;
+  w.cpg = groupsize > 0 && groupsize < c ? (int)(groupsize / 32) : (int)(c / 32);
+  return w;
+}
+
+// `out` against one input: -1 extent too large, 1 overlap, 0 apart.
+int clash(const void* out, int64_t eo, const void* in, int64_t rows, int64_t ld, int64_t cols, int64_t elem) {
+  const int64_t e = extent_bytes(rows, ld, cols, elem);
+  if (eo < 0 || e < 0) return -1;
+  return eo > 0 && e > 0 && overlaps(out, eo, in, e) ? 1 : 0;
+}
+
+gptq_status check_clash(const char* fn, int c) {
+  if (c < 0) return fail(GPTQ_EUNSUPPORTED, fn, "matrix extent exceeds 2^63 bytes");
+  if (c > 0) return fail(GPTQ_EINVAL, fn, "an output overlaps an input");
+  return GPTQ_OK;
+}
+
+int64_t low_bytes(int64_t n, int64_t rank) { return align256(n * rank * 4); }
+
+// Every launch's grid, at the launch helpers' workgroup shapes.
+bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
+  return groups_for(n * (rank > 0 ? rank : 1), 4) <= kMaxGroups256 &&                    // down: a wave per value
+         groups_for(n, 16) * groups_for(r, 16) <= kMaxGroups256 / 2 &&                   // forward: 512 threads per 16 rows
+         groups_for(n, 16) * groups_for(r > c ? r : c, 256) <= kMaxGroups256 &&          // up
+         groups_for(n, 128) * groups_for(c, 128) <= kMaxGroups256 &&                     // backward
+         groups_for(n * (c / 8), 256) <= kMaxGroups256 &&                                // gather
+         m * groups_for(r > c ? r : c, 64) * 2 <= kMaxGroups256 &&                       // transpose (rank <= 128)
+         m * groups_for(r > c ? r : c, 128) * 2 * 16 <= kMaxGroups256 &&                 // gradients (16 splits)
+         groups_for(m * rank * (r > c ? r : c), 1024) <= kMaxGroups256;                  // join
+}
+
+struct GradSizes {
+  int sa, sb;                       // token splits of gA and gB
+  int64_t part, lists, total;
+};
+
+GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
+  GradSizes z;
+  z.sa = gptq::adapter_grad_splits(n, (int)m, c);
+  z.sb = gptq::adapter_grad_splits(n, (int)m, r);
+  const int64_t pa = z.sa > 1 ? z.sa * m * rank * c * 4 : 0, pb = z.sb > 1 ? z.sb * m * rank * r * 4 : 0;
+  z.part = align256(pa > pb ? pa : pb);
+  z.lists = align256(n * 4) + align256((m + 1) * 4);
+  z.total = align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + 2 * low_bytes(n, rank) + z.lists + z.part;
+  return z;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------------ packed product
+gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t c, int64_t rank, int has_perm, size_t* bytes) {
+  const char* fn = "gptq_packed_linear_workspace_size";
+  if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
+  if (has_perm != 0 && has_perm != 1) return fail(GPTQ_EINVAL, fn, "has_perm must be 0 or 1");
+  if (gptq_status st = check_sizes(fn, n, 0, c, 32)) return st;
+  if (rank != 0)
+    if (gptq_status st = check_rank(fn, 1, rank)) return st;
+  *bytes = (size_t)((has_perm ? align256(n * c * 2) : 0) + low_bytes(n, rank));
+  return ok();
+}
+
+gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t ldx, const uint32_t* packed, int64_t r,
+                               int64_t c, int bits, int64_t ld_words, const float* scales, const int32_t* zeros,
+                               int64_t ld_groups, int64_t groupsize, const int32_t* perm, const void* A, const void* B,
+                               int64_t m, int64_t rank, const int32_t* index, const float* alpha, void* Y, gptq_dtype yt,
+                               int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "gptq_packed_linear";
+  const bool low = A || B;
+  if (!low) m = rank = 0;
+  if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
+  if (!valid_dtype(xt) || !valid_dtype(yt)) return fail(GPTQ_EINVAL, fn, "xt and yt must be gptq_dtype values");
+  if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "X must be GPTQ_BF16 or GPTQ_F16");
+  if (yt != GPTQ_F32 && yt != xt) return fail(GPTQ_EDTYPE, fn, "Y must be GPTQ_F32 or of X's type");
+  if (low)
+    if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
+  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (n == 0 || r == 0) return ok();
+  if (gptq_status st = check_packed(fn, packed, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm)) return st;
+  if (ldx < c || ldy < r) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
+  if (!X || !Y) return fail(GPTQ_EINVAL, fn, "a required pointer is NULL");
+  if (perm ? !aligned(X, 2) : (!aligned(X, 16) || ldx % 8 != 0)) return fail(GPTQ_EALIGN, fn, "rows of X must start on 16 bytes");
+  if (!aligned(Y, elem_size(yt))) return fail(GPTQ_EALIGN, fn, "Y misaligned");
+  const int64_t ey = extent_bytes(n, ldy, r, (int64_t)elem_size(yt));
+  if (gptq_status st = check_clash(fn, clash(Y, ey, X, n, ldx, c, 2))) return st;
+  if (gptq_status st = check_clash(fn, clash(Y, ey, packed, r, ld_words, c / 32 * bits, 4))) return st;
+  if (low) {
+    if (gptq_status st = check_clash(fn, clash(Y, ey, A, m * rank, c, c, 2))) return st;
+    if (gptq_status st = check_clash(fn, clash(Y, ey, B, m * r, rank, rank, 2))) return st;
+  }
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, (perm ? align256(n * c * 2) : 0) + low_bytes(n, rank))) return st;
+  Carve carve{static_cast<char*>(ws)};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
+  const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
+  const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
+  const void* xp = X;
+  int64_t ldp = ldx;
+  if (perm) {
+    void* g = carve.take<uint16_t>(n * c * 2);
+    gptq::launch_gather_columns(X, n, c, ldx, perm, g, s);
+    xp = g;
+    ldp = c;
+  }
+  float* S = nullptr;
+  if (low) {
+    S = carve.take<float>(n * rank * 4);
+    gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
+  }
+  gptq::launch_packed_linear(xp, xi, n, ldp, w, ad, S, Y, yt == GPTQ_F32 ? 0 : xi, ldy, s);
+  return check_launch(fn);
+}
+
+// ------------------------------------------------------------------ its input gradient
+gptq_status gptq_packed_linear_backward_workspace_size(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank,
+                                                       size_t* bytes) {
+  const char* fn = "gptq_packed_linear_backward_workspace_size";
+  if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
+  if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
+  if (m != 0 || rank != 0)
+    if (gptq_status st = check_rank(fn, m, rank)) return st;
+  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  *bytes = (size_t)(align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, rank));
+  return ok();
+}
+
+gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n, int64_t ldy, const uint32_t* packed,
+                                        int64_t r, int64_t c, int bits, int64_t ld_words, const float* scales,
+                                        const int32_t* zeros, int64_t ld_groups, int64_t groupsize, const int32_t* perm,
+                                        const void* A, const void* B, int64_t m, int64_t rank, const int32_t* index,
+                                        const float* alpha, void* dX, gptq_dtype ot, int64_t ldx, void* ws, size_t ws_bytes,
+                                        void* stream) {
+  const char* fn = "gptq_packed_linear_backward";
+  const bool low = A || B;
+  if (!low) m = rank = 0;
+  if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
+  if (!valid_dtype(xt) || !valid_dtype(ot)) return fail(GPTQ_EINVAL, fn, "xt and ot must be gptq_dtype values");
+  if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "dY must be GPTQ_BF16 or GPTQ_F16");
+  if (ot != GPTQ_F32 && ot != xt) return fail(GPTQ_EDTYPE, fn, "dX must be GPTQ_F32 or of dY's type");
+  if (low)
+    if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
+  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (r == 0) return fail(GPTQ_ESHAPE, fn, "r must be positive");
+  if (n == 0) return ok();
+  if (gptq_status st = check_packed(fn, packed, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm)) return st;
+  if (ldx < c || ldy < r) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
+  if (!dY || !dX) return fail(GPTQ_EINVAL, fn, "a required pointer is NULL");
+  if (!aligned(dY, 2) || !aligned(dX, elem_size(ot))) return fail(GPTQ_EALIGN, fn, "misaligned pointer");
+  const int64_t ex = extent_bytes(n, ldx, c, (int64_t)elem_size(ot));
+  if (gptq_status st = check_clash(fn, clash(dX, ex, dY, n, ldy, r, 2))) return st;
+  if (gptq_status st = check_clash(fn, clash(dX, ex, packed, r, ld_words, c / 32 * bits, 4))) return st;
+  if (low) {
+    if (gptq_status st = check_clash(fn, clash(dX, ex, A, m * rank, c, c, 2))) return st;
+    if (gptq_status st = check_clash(fn, clash(dX, ex, B, m * r, rank, rank, 2))) return st;
+  }
+  const int64_t need = align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, rank);
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, low ? need : 0)) return st;
+  Carve carve{static_cast<char*>(ws)};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
+  const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
+  const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
+  uint16_t* At = nullptr;
+  float* T = nullptr;
+  if (low) {
+    At = carve.take<uint16_t>(m * c * rank * 2);
+    uint16_t* Bt = carve.take<uint16_t>(m * rank * pad8(r) * 2);
+    T = carve.take<float>(n * rank * 4);
+    gptq::launch_transpose16(ad.A, (int)m, rank, c, At, rank, s);
+    gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
+    gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);
+  }
+  gptq::launch_packed_backward(dY, xi, n, ldy, w, ad, At, T, dX, ot == GPTQ_F32 ? 0 : xi, ldx, s);
+  return check_launch(fn);
+}
+
+// ------------------------------------------------------------------ adapters beside any projection
+gptq_status gptq_adapter_add_workspace_size(int64_t n, int64_t rank, size_t* bytes) {
+  const char* fn = "gptq_adapter_add_workspace_size";
+  if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
+  if (gptq_status st = check_sizes(fn, n, 0, 8, 8)) return st;
+  if (gptq_status st = check_rank(fn, 1, rank)) return st;
+  *bytes = (size_t)low_bytes(n, rank);
+  return ok();
+}
+
+gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n, int64_t c, int64_t ldx, const void* A, const void* B,
+                             int64_t m, int64_t rank, int64_t r, const int32_t* index, const float* alpha, const void* Y,
+                             gptq_dtype yt, int64_t ldy, void* out, int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "gptq_adapter_add";
+  if (gptq_status st = check_sizes(fn, n, r, c, 8)) return st;
+  if (!valid_dtype(xt) || !valid_dtype(yt)) return fail(GPTQ_EINVAL, fn, "xt and yt must be gptq_dtype values");
+  if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "X must be GPTQ_BF16 or GPTQ_F16");
+  if (yt != GPTQ_F32 && yt != xt) return fail(GPTQ_EDTYPE, fn, "Y must be GPTQ_F32 or of X's type");
+  if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
+  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (n == 0 || r == 0) return ok();
+  if (ldx < c || ldy < r || ldo < r) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
+  if (!X || !Y || !out) return fail(GPTQ_EINVAL, fn, "a required pointer is NULL");
+  const int64_t el = (int64_t)elem_size(yt);
+  if (!aligned(X, 2) || !aligned(Y, el) || !aligned(out, el)) return fail(GPTQ_EALIGN, fn, "misaligned pointer");
+  const int64_t eo = extent_bytes(n, ldo, r, el);
+  if (gptq_status st = check_clash(fn, clash(out, eo, X, n, ldx, c, 2))) return st;
+  if (gptq_status st = check_clash(fn, clash(out, eo, A, m * rank, c, c, 2))) return st;
+  if (gptq_status st = check_clash(fn, clash(out, eo, B, m * r, rank, rank, 2))) return st;
+  if (!(out == Y && ldo == ldy))
+    if (gptq_status st = check_clash(fn, clash(out, eo, Y, n, ldy, r, el))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, low_bytes(n, rank))) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
+  const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
+  float* S = static_cast<float*>(ws);
+  gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
+  gptq::launch_adapter_up(S, n, ad, xi, ad.B, r, Y, ldy, out, yt == GPTQ_F32 ? 0 : xi, ldo, s);
+  return check_launch(fn);
+}
+
+// ------------------------------------------------------------------ their gradients
+gptq_status gptq_adapter_backward_workspace_size(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank, size_t* bytes) {
+  const char* fn = "gptq_adapter_backward_workspace_size";
+  if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
+  if (gptq_status st = check_sizes(fn, n, r, c, 8)) return st;
+  if (gptq_status st = check_rank(fn, m, rank)) return st;
+  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  *bytes = (size_t)grad_sizes(n, r, c, m, rank).total;
+  return ok();
+}
+
+gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, int64_t ldx, gptq_dtype xt, int64_t n,
+                                  int64_t r, int64_t c, const void* A, const void* B, int64_t m, int64_t rank,
+                                  const int32_t* index, const float* alpha, float* gA, float* gB, const void* base, void* dX,
+                                  gptq_dtype ot, int64_t ldd, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "gptq_adapter_backward";
+  if (gptq_status st = check_sizes(fn, n, r, c, 8)) return st;
+  if (!valid_dtype(xt) || !valid_dtype(ot)) return fail(GPTQ_EINVAL, fn, "xt and ot must be gptq_dtype values");
+  if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "dY and X must be GPTQ_BF16 or GPTQ_F16");
+  if (ot != GPTQ_F32 && ot != xt) return fail(GPTQ_EDTYPE, fn, "dX must be GPTQ_F32 or of X's type");
+  if (r == 0) return fail(GPTQ_ESHAPE, fn, "r must be positive");
+  if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
+  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (ldy < r || ldx < c || (dX && ldd < c)) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
+  if (!gA || !gB) return fail(GPTQ_EINVAL, fn, "gA or gB is NULL");
+  if (n > 0 && (!dY || !X)) return fail(GPTQ_EINVAL, fn, "dY or X is NULL");
+  if (base && !dX) return fail(GPTQ_EINVAL, fn, "base without dX");
+  const int64_t el = (int64_t)elem_size(ot);
+  if (!aligned(dY, 2) || !aligned(X, 2) || !aligned(dX, el) || !aligned(base, el))
+    return fail(GPTQ_EALIGN, fn, "misaligned pointer");
+  if (!aligned(gA, 16) || !aligned(gB, 16)) return fail(GPTQ_EALIGN, fn, "gA and gB must be 16-byte aligned");
+  const int64_t ea = extent_bytes(m * rank, c, c, 4), eb = extent_bytes(m * r, rank, rank, 4);
+  const int64_t ed = dX ? extent_bytes(n, ldd, c, el) : 0;
+  struct { const void* p; int64_t rows, ld, cols, elem; } in[] = {
+      {dY, n, ldy, r, 2}, {X, n, ldx, c, 2}, {A, m * rank, c, c, 2}, {B, m * r, rank, rank, 2}};
+  for (const auto& v : in)
+    for (const auto& o : {std::pair<const void*, int64_t>{gA, ea}, {gB, eb}, {dX, ed}})
+      if (o.first)
+        if (gptq_status st = check_clash(fn, clash(o.first, o.second, v.p, v.rows, v.ld, v.cols, v.elem))) return st;
+  if (overlaps(gA, ea, gB, eb) || (dX && ed > 0 && (overlaps(dX, ed, gA, ea) || overlaps(dX, ed, gB, eb))))
+    return fail(GPTQ_EINVAL, fn, "outputs overlap");
+  if (base && base != dX)
+    for (const auto& o : {std::pair<const void*, int64_t>{gA, ea}, {gB, eb}, {dX, ed}})
+      if (gptq_status st = check_clash(fn, clash(o.first, o.second, base, n, ldd, c, el))) return st;
+  const GradSizes z = grad_sizes(n, r, c, m, rank);
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, z.total)) return st;
+  Carve carve{static_cast<char*>(ws)};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
+  const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
+  uint16_t* Bt = carve.take<uint16_t>(m * rank * pad8(r) * 2);
+  uint16_t* At = carve.take<uint16_t>(m * c * rank * 2);
+  float* S = carve.take<float>(n * rank * 4);
+  float* T = carve.take<float>(n * rank * 4);
+  int32_t* order = carve.take<int32_t>(n * 4);
+  int32_t* start = carve.take<int32_t>((m + 1) * 4);
+  float* part = carve.take<float>(z.part);
+  gptq::launch_token_lists(ad, n, order, start, s);
+  if (n > 0) {
+    gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
+    gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
+    gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);
+  }
+  gptq::launch_adapter_grad(T, X, xi, n, c, ldx, ad, order, start, 0, gA, part, z.sa, s);
+  gptq::launch_adapter_grad(S, dY, xi, n, r, ldy, ad, order, start, 1, gB, part, z.sb, s);
+  if (dX && n > 0) {
+    gptq::launch_transpose16(ad.A, (int)m, rank, c, At, rank, s);
+    gptq::launch_adapter_up(T, n, ad, xi, At, c, base, ldd, dX, ot == GPTQ_F32 ? 0 : xi, ldd, s);
+  }
+  return check_launch(fn);
+}
+
+}  // extern "C"

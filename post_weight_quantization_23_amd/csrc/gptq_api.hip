@@ -8,59 +8,19 @@
 #include <mutex>
 #include <string>
 
-#include "../../include/gptq.h"
+#include "api.hpp"
 #include "kernels.hpp"
+
+std::string& gptq::api::last_error() {
+  static thread_local std::string text;
+  return text;
+}
+
+using namespace gptq::api;
 
 namespace {
 
-thread_local std::string g_last_error;
-
-gptq_status fail(gptq_status st, const char* fn, const std::string& what) {
-  g_last_error = std::string(fn) + ": " + what;
-  return st;
-}
-
-gptq_status ok() {
-  g_last_error.clear();
-  return GPTQ_OK;
-}
-
-gptq_status check_launch(const char* fn) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(GPTQ_EHIP, fn, hipGetErrorString(e));
-  return ok();
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 constexpr int64_t kMaxDim = 65535;       // H / U edge (grid y limit, int kernels)
-constexpr int64_t kMaxRows = INT_MAX / 2; // rows of W, tokens of X
-// A launch's grid.x times its 256 threads per workgroup must fit in 32 bits.
-constexpr int64_t kMaxGroups256 = ((int64_t(1) << 32) - 1) / 256;
-
-// Workgroups of 256 threads needed for n items at `per` items per workgroup.
-int64_t groups_for(int64_t n, int64_t per) { return (n + per - 1) / per; }
-
-// Bytes spanned by a rows x cols matrix with row stride ld (elements of
-// `elem` bytes), or -1 when that does not fit in 63 bits.
-int64_t extent_bytes(int64_t rows, int64_t ld, int64_t cols, int64_t elem) {
-  int64_t e = 0;
-  if (rows <= 0 || cols <= 0) return 0;
-  if (__builtin_mul_overflow(rows - 1, ld, &e) || __builtin_add_overflow(e, cols, &e) ||
-      __builtin_mul_overflow(e, elem, &e))
-    return -1;
-  return e;
-}
-
-// Whether [p, p + bytes) and [q, q + bytes_q) overlap (extents already known to fit).
-bool overlaps(const void* p, int64_t bytes, const void* q, int64_t bytes_q) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + (uint64_t)bytes_q && b < a + (uint64_t)bytes;
-}
-
-size_t elem_size(gptq_dtype t) { return t == GPTQ_F32 ? 4 : 2; }
-bool valid_dtype(int t) { return t == GPTQ_F32 || t == GPTQ_BF16 || t == GPTQ_F16; }
-
 // Scratch of gptq_prepare_noalloc: one array per GPU, as large as
 // gptq_prepare's workspace at the largest supported d.  In host code the
 // name `scratch` is only a stand-in; its device address on the current
@@ -108,7 +68,7 @@ const char* gptq_status_string(gptq_status s) {
   return "unknown gptq_status";
 }
 
-const char* gptq_last_error(void) { return g_last_error.c_str(); }
+const char* gptq_last_error(void) { return last_error().c_str(); }
 
 // ------------------------------------------------------------------ Hessian
 gptq_status gptq_hessian_workspace_size(int64_t d, int64_t n_tok, gptq_dtype xt, size_t* bytes) {

@@ -1,0 +1,232 @@
+// Product of many tokens with a packed layer, with the low-rank adapters of
+// their requests beside it:
+//     Y[t, i] = sum_j s[i, g(j)] (q[i, j] - z[i, g(j)]) X[t, perm[j]] + (S B_a^T)[t, i].
+//
+// Codes enter the matrix cores as whole numbers: a b-bit code shifted to the
+// top of a 16-bit float's mantissa under the exponent of 2^b reads as 2^b + q
+// exactly, one shift and one and-or for two codes.  With P = sum (2^b + q) x and
+// X_g = sum x over a group (a product with ones, on the matrix cores too), the
+// group's part is s (P - (2^b + z) X_g): the weights are never rounded, and
+// every sum is fp32.  The subtraction costs a factor below 8 in the error of
+// the fp32 sums, three bits of 24.
+#include "adapter.hpp"
+
+namespace gptq {
+
+namespace {
+
+struct FwdArgs {
+  const uint16_t* X;
+  int64_t ldx, n;
+  PackedLayer w;
+  Adapters ad;
+  const float* S;    // null: no adapters
+  void* Y;
+  int64_t ldy;
+  int row_tiles;
+};
+
+// Codes t and t + 4 of a block of eight, t = 0 .. 3, as pairs of 16-bit floats
+// 2^BITS + q.
+template <int BITS, int DT>
+GPTQ_DEV u32x4 code_pairs(uint32_t blk) {
+  constexpr int P = (DT == kBF16 ? 7 : 10) - BITS;   // lowest bit of the code in the mantissa
+  constexpr uint32_t one = DT == kBF16 ? (0x3F80u + (BITS << 7)) : (0x3C00u + (BITS << 10));
+  constexpr uint32_t mask = (((1u << BITS) - 1) << P) * 0x10001u, magic = one * 0x10001u;
+  if constexpr (BITS == 3) blk = (blk & 0xFFFu) | ((blk & 0xFFF000u) << 4);   // codes 4 .. 7 to the high half
+  u32x4 v;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    constexpr int B = BITS;
+    const int sh = P - B * t;
+    v[t] = ((sh >= 0 ? blk << sh : blk >> -sh) & mask) | magic;
+  }
+  return v;
+}
+
+// Eight consecutive activations in the order of code_pairs.
+GPTQ_DEV u32x4 pair_order(u32x4 v) {
+  u32x4 p;
+  p[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100u);
+  p[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302u);
+  p[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100u);
+  p[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);
+  return p;
+}
+
+constexpr int kWaves = 8;
+
+// 16 MT tokens x 16 rows per workgroup.  The waves split the columns in steps
+// of 128 (lane (m, kq): row m, chunk kq of the step's four) and are joined
+// through LDS in wave order.
+// WIDE: groups hold whole steps, and the step's four products take word j of
+// every lane's chunk (columns 32 kq + 8 j).  Otherwise the lanes' words are
+// transposed so that product j holds chunk j alone, and rulers apply per chunk.
+template <int BITS, int DT, int YT, int MT, bool WIDE>
+__global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
+  __shared__ float red[kWaves][MT][4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, kq = lane >> 4;
+  const int64_t tile = blockIdx.x / a.row_tiles;
+  const int64_t t0 = tile * 16 * MT;
+  const int row0 = (int)(blockIdx.x - tile * a.row_tiles) * 16;
+  const int row = min(row0 + m, a.w.r - 1);
+  const int nch = a.w.c >> 5, steps = (nch + 3) >> 2;
+  const uint32_t* words = a.w.words + (int64_t)row * a.w.ldw;
+  const float* srow = a.w.scales + (int64_t)row * a.w.ldg;
+  const int32_t* zrow = a.w.zeros + (int64_t)row * a.w.ldg;
+  const uint32_t one = DT == kBF16 ? 0x3F803F80u : 0x3C003C00u;
+  const u32x4 ones = {one, one, one, one};
+  const floatx4 zero4 = {0.f, 0.f, 0.f, 0.f};
+
+  floatx4 tot[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) tot[i] = zero4;
+
+  for (int s = wave; s < steps; s += kWaves) {
+    const int ch = min(4 * s + kq, nch - 1);
+    uint32_t chunk[BITS];
+    if constexpr (BITS == 4) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(words + 4 * (int64_t)ch);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) chunk[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) chunk[i] = words[3 * (int64_t)ch + i];
+    }
+    uint32_t blk[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) blk[j] = code_block<BITS>(chunk, j);
+    if constexpr (!WIDE) {
+      // register j of lane (m, kq) <-> register kq of lane (m, j)
+      auto swap16 = [](uint32_t& x, uint32_t& y) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+        x = r[0];
+        y = r[1];
+      };
+      auto swap32 = [](uint32_t& x, uint32_t& y) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        x = r[0];
+        y = r[1];
+      };
+      swap16(blk[0], blk[1]);
+      swap16(blk[2], blk[3]);
+      swap32(blk[0], blk[2]);
+      swap32(blk[1], blk[3]);
+    }
+    floatx4 p[MT], xs[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) p[i] = xs[i] = zero4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 w = code_pairs<BITS, DT>(blk[j]);
+      const int xc = WIDE ? 4 * s + kq : 4 * s + j;            // chunk of this lane's activations
+      const int64_t col = 32 * (int64_t)xc + 8 * (WIDE ? j : kq);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int64_t t = t0 + 16 * i + m;
+        u32x4 x = {0u, 0u, 0u, 0u};
+        if (xc < nch && t < a.n) x = pair_order(*reinterpret_cast<const u32x4*>(a.X + t * a.ldx + col));
+        p[i] = mfma16<DT>(x, w, p[i]);
+        xs[i] = mfma16<DT>(x, ones, xs[i]);
+      }
+      if (!WIDE || j == 3) {
+        const int g = min(4 * s + (WIDE ? 0 : j), nch - 1) / a.w.cpg;
+        const float sc = srow[g], off = (float)(1 << BITS) + (float)zrow[g];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tot[i][e] = __builtin_fmaf(sc, __builtin_fmaf(-off, xs[i][e], p[i][e]), tot[i][e]);
+          p[i] = xs[i] = zero4;
+        }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[wave][i][e][lane] = tot[i][e];
+  __syncthreads();
+  if (wave < MT) {
+    const int i = wave;
+    floatx4 y[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v = red[0][i][e][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += red[w][i][e][lane];
+      y[0][e] = v;
+    }
+    const int64_t rows[1] = {row0 + m < a.w.r ? row0 + m : -1};
+    if (a.S) expand_add<DT, 1>(a.ad, a.ad.B, a.w.r, a.S, t0 + 16 * i, a.n, rows, y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t t = t0 + 16 * i + 4 * kq + e;
+      if (t < a.n && rows[0] >= 0) store_out<YT>(a.Y, t * a.ldy + rows[0], y[0][e]);
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void gather_columns_kernel(const uint16_t* __restrict__ X, int64_t c, int64_t ldx,
+                                                             const int32_t* __restrict__ perm, uint16_t* __restrict__ dst,
+                                                             int64_t items) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // eight columns of one token
+  if (i >= items) return;
+  const int64_t per = c >> 3, t = i / per, j = (i - t * per) * 8;
+  const uint16_t* x = X + t * ldx;
+  u32x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int p0 = min(max(perm[j + 2 * e], 0), (int)c - 1), p1 = min(max(perm[j + 2 * e + 1], 0), (int)c - 1);
+    v[e] = (uint32_t)x[p0] | ((uint32_t)x[p1] << 16);
+  }
+  *reinterpret_cast<u32x4*>(dst + t * c + j) = v;
+}
+
+template <int BITS, int DT, int YT, int MT>
+void launch_rows16(const FwdArgs& a, hipStream_t s) {
+  const int64_t tiles = (a.n + 16 * MT - 1) / (16 * MT);
+  const dim3 grid((unsigned)(tiles * a.row_tiles)), block(64 * kWaves);
+  if (a.w.cpg % 4 == 0 || a.w.cpg >= (a.w.c >> 5)) hipLaunchKernelGGL((rows16_kernel<BITS, DT, YT, MT, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((rows16_kernel<BITS, DT, YT, MT, false>), grid, block, 0, s, a);
+}
+
+template <int BITS, int DT, int YT>
+void launch_forward(const FwdArgs& a, hipStream_t s) {
+  if (a.n <= 16) launch_rows16<BITS, DT, YT, 1>(a, s);
+  else if (a.n <= 32) launch_rows16<BITS, DT, YT, 2>(a, s);
+  else launch_rows16<BITS, DT, YT, 4>(a, s);
+}
+
+}  // namespace
+
+void launch_gather_columns(const void* X, int64_t n, int64_t c, int64_t ldx, const int32_t* perm, void* dst, hipStream_t s) {
+  const int64_t items = n * (c >> 3);
+  hipLaunchKernelGGL(gather_columns_kernel, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, s,
+                     static_cast<const uint16_t*>(X), c, ldx, perm, static_cast<uint16_t*>(dst), items);
+}
+
+void launch_packed_linear(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad,
+                          const float* S, void* Y, int yt, int64_t ldy, hipStream_t s) {
+  FwdArgs a;
+  a.X = static_cast<const uint16_t*>(X);
+  a.ldx = ldx;
+  a.n = n;
+  a.w = w;
+  a.ad = ad;
+  a.S = S;
+  a.Y = Y;
+  a.ldy = ldy;
+  a.row_tiles = (w.r + 15) / 16;
+#define GPTQ_FWD(B_)                                                                          \
+  do {                                                                                        \
+    if (xt == kBF16) { if (yt == 0) launch_forward<B_, kBF16, 0>(a, s); else launch_forward<B_, kBF16, kBF16>(a, s); } \
+    else { if (yt == 0) launch_forward<B_, kF16, 0>(a, s); else launch_forward<B_, kF16, kF16>(a, s); }                \
+  } while (0)
+  if (w.bits == 4) GPTQ_FWD(4);
+  else GPTQ_FWD(3);
+#undef GPTQ_FWD
+}
+
+}  // namespace gptq
