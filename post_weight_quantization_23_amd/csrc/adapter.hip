@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void up_kernel(const float* __restrict__ S, in
     row[q] = j < rows ? j : -1;
     acc[q] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
-  expand_add<DT, 4>(ad, B, rows, S, t0, n, row, acc);
+  expand_add<DT, YT == 0 ? 3 : 2, 4>(ad, B, rows, S, t0, n, row, acc);
 #pragma unroll
   for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -146,8 +146,8 @@ __global__ __launch_bounds__(1024) void token_lists_kernel(Adapters ad, int64_t 
 // eight products, whose 16 columns are j0 + 8 (lane & 15) + u: the transpose
 // happens in registers.  Tokens come through the adapter's list, so they may
 // lie in any order; places past its end multiply zeros by zeros.  V is split
-// in two bf16 terms (16 significant bits) and fp16 Z in two, so the gradient
-// keeps fp32's range and an error below 2^-16 of its terms.
+// in three bf16 terms (24 significant bits) and fp16 Z in two, so the gradient
+// keeps fp32's range and precision.
 // Workgroup: 4 waves over the tokens of one 128-column block and 16 RT rank
 // rows, joined through LDS in wave order; token splits over the grid write
 // partial results that join_kernel adds in order.
@@ -189,24 +189,24 @@ __global__ __launch_bounds__(256) void grad_kernel(const float* __restrict__ V, 
       z[e] = u32x4{0u, 0u, 0u, 0u};
       if (tok[e] >= 0 && valid > 0) z[e] = load8(Z + tok[e] * ldz + j0, valid, vec);
     }
-    u32x4 vh[RT], vl[RT];
+    u32x4 vt[RT][3];
 #pragma unroll
     for (int p = 0; p < RT; ++p) {
       float v[8];
       const int pr = p0 + 16 * p + m;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = (tok[e] >= 0 && pr < rank) ? V[tok[e] * rank + pr] : 0.f;
-      split8(v, vh[p], vl[p]);
+      split8<3>(v, vt[p]);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      u32x4 f, zh, zl;
+      u32x4 f;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         f[e] = __builtin_amdgcn_perm(z[2 * e + 1][u >> 1], z[2 * e][u >> 1], (u & 1) ? 0x07060302u : 0x05040100u);
-      to_bf16_terms<DT>(f, zh, zl);
+      const Terms16<DT> zt(f);
 #pragma unroll
-      for (int p = 0; p < RT; ++p) acc[p][u] = mfma_split<DT>(vh[p], vl[p], zh, zl, acc[p][u]);
+      for (int p = 0; p < RT; ++p) acc[p][u] = mfma_terms<DT, 3>(vt[p], zt, acc[p][u]);
     }
   }
 

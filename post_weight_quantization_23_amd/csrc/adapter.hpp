@@ -80,6 +80,32 @@ GPTQ_DEV floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// 32 x 32 x 16: lane l holds A[l & 31][8 (l >> 5) + e] and B[8 (l >> 5) + e][l & 31],
+// and C[8 (i >> 2) + 4 (l >> 5) + (i & 3)][l & 31] in component i.
+template <int DT>
+GPTQ_DEV floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c) {
+  if constexpr (DT == kBF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Tile shapes of the two: E x E outputs, K of the contraction, the lane's
+// position in an operand (row l % E, K offset 8 (l / E)) and the row of
+// accumulator component i.
+template <class Acc>
+struct TileShape;
+template <>
+struct TileShape<floatx4> {
+  static constexpr int E = 16, K = 32, C = 4;
+  static GPTQ_DEV int acc_row(int lane, int i) { return 4 * (lane >> 4) + i; }
+};
+template <>
+struct TileShape<floatx16> {
+  static constexpr int E = 32, K = 16, C = 16;
+  static GPTQ_DEV int acc_row(int lane, int i) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+};
+
 // ---------------------------------------------------------------- adapters
 // Adapter of token t, or -1.
 GPTQ_DEV int adapter_of(const Adapters& ad, int64_t t, int64_t n) {
@@ -88,47 +114,67 @@ GPTQ_DEV int adapter_of(const Adapters& ad, int64_t t, int64_t n) {
   return (uint32_t)a < (uint32_t)ad.m ? a : -1;
 }
 
-// v = hi + lo + (an error below 2^-17 |v|), hi and lo bf16: an fp32 operand
-// of a bf16 matrix product as two of them.  Every fp16 value is such a sum
-// exactly (11 significant bits against 8 + 8).
-GPTQ_DEV void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  hi = pack2<kBF16>(v0, v1);
-  lo = pack2<kBF16>(v0 - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xFFFF0000u));
-}
-
-GPTQ_DEV void split8(const float (&v)[8], u32x4& hi, u32x4& lo) {
+// An fp32 operand of a bf16 matrix product as TERMS of them, v = v1 + v2 (+ v3):
+// each term holds 8 more significant bits, so the rest is below 2^-17 |v| with
+// two terms and 2^-25 |v| with three.
+template <int TERMS>
+GPTQ_DEV void split8(const float (&v)[8], u32x4 (&t)[TERMS]) {
+  float r[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h, l;
-    split2(v[2 * i], v[2 * i + 1], h, l);
-    hi[i] = h;
-    lo[i] = l;
-  }
-}
-
-// A 16-bit operand as one (bf16) or two (fp16) bf16 operands.
-template <int DT>
-GPTQ_DEV void to_bf16_terms(u32x4 v, u32x4& hi, u32x4& lo) {
-  if constexpr (DT == kBF16) {
-    hi = v;
-  } else {
-    float f[8];
+  for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+  for (int k = 0; k < TERMS; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f[2 * i] = f16_to_f32<kF16>(v[i] & 0xFFFFu);
-      f[2 * i + 1] = f16_to_f32<kF16>(v[i] >> 16);
+      const uint32_t w = pack2<kBF16>(r[2 * i], r[2 * i + 1]);
+      t[k][i] = w;
+      r[2 * i] -= __uint_as_float(w << 16);
+      r[2 * i + 1] -= __uint_as_float(w & 0xFFFF0000u);
     }
-    split8(f, hi, lo);
-  }
 }
 
-// c + V Z for an fp32 operand V = vh + vl and a 16-bit operand Z = zh (+ zl).
-// The terms left out (vl zl) are below 2^-18 of the product.
+// A 16-bit operand in bf16: itself, or two terms for fp16 (exact: 11
+// significant bits against 8 + 8).
 template <int DT>
-GPTQ_DEV floatx4 mfma_split(u32x4 vh, u32x4 vl, u32x4 zh, u32x4 zl, floatx4 c) {
-  c = mfma16<kBF16>(vl, zh, c);
-  if constexpr (DT == kF16) c = mfma16<kBF16>(vh, zl, c);
-  return mfma16<kBF16>(vh, zh, c);
+struct Terms16 {
+  static constexpr int N = DT == kBF16 ? 1 : 2;
+  u32x4 t[N];
+  GPTQ_DEV explicit Terms16(u32x4 v) {
+    if constexpr (DT == kBF16) {
+      t[0] = v;
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = f16_to_f32<kF16>(v[i] & 0xFFFFu);
+        f[2 * i + 1] = f16_to_f32<kF16>(v[i] >> 16);
+      }
+      split8<2>(f, t);
+    }
+  }
+};
+
+// c + V Z of an fp32 operand in TERMS terms and a 16-bit one, smallest products
+// first; those below the first term left out of V are left out.
+template <int DT, int TERMS>
+GPTQ_DEV floatx4 mfma_terms(const u32x4 (&v)[TERMS], const Terms16<DT>& z, floatx4 c) {
+  if constexpr (TERMS == 3) {
+    c = mfma16<kBF16>(v[2], z.t[0], c);
+    if constexpr (DT == kF16) c = mfma16<kBF16>(v[1], z.t[1], c);
+  }
+  c = mfma16<kBF16>(v[1], z.t[0], c);
+  if constexpr (DT == kF16) c = mfma16<kBF16>(v[0], z.t[1], c);
+  return mfma16<kBF16>(v[0], z.t[0], c);
+}
+template <int DT, int TERMS>
+GPTQ_DEV floatx16 mfma_terms(const u32x4 (&v)[TERMS], const Terms16<DT>& z, floatx16 c) {
+  if constexpr (TERMS == 3) {
+    c = mfma32<kBF16>(v[2], z.t[0], c);
+    if constexpr (DT == kF16) c = mfma32<kBF16>(v[1], z.t[1], c);
+  }
+  c = mfma32<kBF16>(v[1], z.t[0], c);
+  if constexpr (DT == kF16) c = mfma32<kBF16>(v[0], z.t[1], c);
+  return mfma32<kBF16>(v[0], z.t[0], c);
 }
 
 // Eight fp32 values (16-byte aligned).
@@ -141,49 +187,46 @@ GPTQ_DEV void load8f(const float* p, float (&v)[8]) {
   }
 }
 
-// out[q] += (S B_a^T) of 16 tokens t0 .. t0+15 and NT sets of 16 outputs, in
-// the accumulator layout of mfma16 (row = token): the low-rank product beside
-// a tile.  S [n][rank] fp32 already holds alpha; row[q] is this lane's output
-// row (column of the tile) in B [m][rows][rank], or -1.  The adapters that
-// occur among the 16 tokens are taken one after the other, each as a product
-// over all 16, of which only its own tokens' rows are kept: a value that is
-// not finite in one request's adapter or tokens stays in that request's rows.
-template <int DT, int NT>
+// out[q] += (S B_a^T) of the tile's tokens t0 .. and NT sets of its outputs, in
+// the accumulator layout (row = token): the low-rank product beside a tile.
+// S [n][rank] fp32 already holds alpha; row[q] is this lane's output row
+// (column of the tile) in B [m][rows][rank], or -1.  The adapters that occur
+// among the tokens are taken one after the other, each as a product over all of
+// them, of which only its own tokens' rows are kept: a value that is not finite
+// in one request's adapter or tokens stays in that request's rows.
+// fp32 results take S in three terms, 16-bit ones in two.
+template <int DT, int TERMS, int NT, class Acc>
 GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, const float* S, int64_t t0, int64_t n,
-                         const int64_t (&row)[NT], floatx4 (&out)[NT]) {
-  const int lane = threadIdx.x & 63, kq = lane >> 4;
-  const int64_t t = t0 + (lane & 15);
+                         const int64_t (&row)[NT], Acc (&out)[NT]) {
+  using Tile = TileShape<Acc>;
+  const int lane = threadIdx.x & 63, kq = lane / Tile::E;
+  const int64_t t = t0 + lane % Tile::E;
   const int mine = adapter_of(ad, t, n);
-  uint32_t rest = (uint32_t)(__ballot(mine >= 0) & 0xFFFFu);
+  uint32_t rest = (uint32_t)(__ballot(mine >= 0) & ((1ull << Tile::E) - 1));
   while (rest) {
     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(rest));
-    const uint32_t members = (uint32_t)(__ballot(mine == a) & 0xFFFFu);
+    const uint32_t members = (uint32_t)(__ballot(mine == a) & ((1ull << Tile::E) - 1));
     rest &= ~members;
-    floatx4 acc[NT];
-#pragma unroll
-    for (int q = 0; q < NT; ++q) acc[q] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int k0 = 0; k0 < ad.rank; k0 += 32) {
+    Acc acc[NT] = {};
+    for (int k0 = 0; k0 < ad.rank; k0 += Tile::K) {
       const int k = k0 + 8 * kq;
-      u32x4 sh = {0u, 0u, 0u, 0u}, sl = sh;
-      if (k < ad.rank && t < n) {
-        float v[8];
-        load8f(S + t * ad.rank + k, v);
-        split8(v, sh, sl);
-      }
+      float v[8] = {};
+      if (k < ad.rank && t < n) load8f(S + t * ad.rank + k, v);
+      u32x4 s[TERMS];
+      split8<TERMS>(v, s);
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
-        u32x4 b = {0u, 0u, 0u, 0u}, bh, bl;
+        u32x4 b = {0u, 0u, 0u, 0u};
         if (k < ad.rank && row[q] >= 0)
           b = *reinterpret_cast<const u32x4*>(B + ((int64_t)a * rows + row[q]) * ad.rank + k);
-        to_bf16_terms<DT>(b, bh, bl);
-        acc[q] = mfma_split<DT>(sh, sl, bh, bl, acc[q]);
+        acc[q] = mfma_terms<DT, TERMS>(s, Terms16<DT>(b), acc[q]);
       }
     }
 #pragma unroll
     for (int q = 0; q < NT; ++q)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((members >> (4 * kq + i)) & 1) out[q][i] += acc[q][i];
+      for (int i = 0; i < Tile::C; ++i)
+        if ((members >> Tile::acc_row(lane, i)) & 1) out[q][i] += acc[q][i];
   }
 }
 
@@ -195,6 +238,34 @@ GPTQ_DEV uint32_t code_block(const uint32_t* chunk, int m) {
   if constexpr (BITS == 4) return chunk[m];
   const int bit = 24 * m, w = bit >> 5;
   return (__builtin_amdgcn_alignbit(chunk[w < 2 ? w + 1 : 2], chunk[w], bit & 31)) & 0xFFFFFFu;
+}
+
+// Codes t and t + 4 of a block of eight, t = 0 .. 3, as pairs of 16-bit floats
+// 2^BITS + q.
+template <int BITS, int DT>
+GPTQ_DEV u32x4 code_pairs(uint32_t blk) {
+  constexpr int P = (DT == kBF16 ? 7 : 10) - BITS;   // lowest bit of the code in the mantissa
+  constexpr uint32_t one = DT == kBF16 ? (0x3F80u + (BITS << 7)) : (0x3C00u + (BITS << 10));
+  constexpr uint32_t mask = (((1u << BITS) - 1) << P) * 0x10001u, magic = one * 0x10001u;
+  if constexpr (BITS == 3) blk = (blk & 0xFFFu) | ((blk & 0xFFF000u) << 4);   // codes 4 .. 7 to the high half
+  u32x4 v;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    constexpr int B = BITS;
+    const int sh = P - B * t;
+    v[t] = ((sh >= 0 ? blk << sh : blk >> -sh) & mask) | magic;
+  }
+  return v;
+}
+
+// Eight consecutive activations in the order of code_pairs.
+GPTQ_DEV u32x4 pair_order(u32x4 v) {
+  u32x4 p;
+  p[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100u);
+  p[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302u);
+  p[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100u);
+  p[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);
+  return p;
 }
 
 // ---------------------------------------------------------------- launches
@@ -225,6 +296,14 @@ void launch_packed_linear(const void* X, int xt, int64_t n, int64_t ldx, const P
                           const float* S, void* Y, int yt, int64_t ldy, hipStream_t s);
 // dst[t][j] = X[t][perm[j]] (entries outside 0 .. c-1 clamped), dst dense.
 void launch_gather_columns(const void* X, int64_t n, int64_t c, int64_t ldx, const int32_t* perm, void* dst, hipStream_t s);
+// The same on tiles for many tokens: packed_tiles.hip.  prepare_tokens writes
+// n x tiles_width(c) 16-bit values and n exponents.
+bool packed_tiles(int64_t n, int64_t c);
+int64_t tiles_width(int64_t c);
+void launch_prepare_tokens(const void* X, int xt, int64_t n, int64_t ldx, int64_t c, const int32_t* perm, void* dst, int32_t* ex,
+                           hipStream_t s);
+void launch_packed_tiles(const void* X, const int32_t* ex, int xt, int64_t n, const PackedLayer& w, const Adapters& ad, const float* S,
+                         void* Y, int yt, int64_t ldy, hipStream_t s);
 // dX = dY W_hat (+ T A): packed_backward.hip.  At: A transposed to [m][c][rank].
 void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, const PackedLayer& w, const Adapters& ad,
                             const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, hipStream_t s);

@@ -119,6 +119,13 @@ gptq_status check_clash(const char* fn, int c) {
   return GPTQ_OK;
 }
 
+// Activations of the packed product as its kernels take them: a gathered copy
+// for a few tokens of an act-order layer, a prepared copy for many.
+int64_t token_bytes(int64_t n, int64_t c, bool perm) {
+  if (gptq::packed_tiles(n, c)) return align256(n * gptq::tiles_width(c) * 2) + align256(n * 4);
+  return perm ? align256(n * c * 2) : 0;
+}
+
 int64_t low_bytes(int64_t n, int64_t rank) { return align256(n * rank * 4); }
 
 // Every launch's grid, at the launch helpers' workgroup shapes.
@@ -161,7 +168,7 @@ gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t c, int64_t rank
   if (gptq_status st = check_sizes(fn, n, 0, c, 32)) return st;
   if (rank != 0)
     if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  *bytes = (size_t)((has_perm ? align256(n * c * 2) : 0) + low_bytes(n, rank));
+  *bytes = (size_t)(token_bytes(n, c, has_perm != 0) + low_bytes(n, rank));
   return ok();
 }
 
@@ -193,26 +200,32 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
     if (gptq_status st = check_clash(fn, clash(Y, ey, A, m * rank, c, c, 2))) return st;
     if (gptq_status st = check_clash(fn, clash(Y, ey, B, m * r, rank, rank, 2))) return st;
   }
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, (perm ? align256(n * c * 2) : 0) + low_bytes(n, rank))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, token_bytes(n, c, perm != nullptr) + low_bytes(n, rank))) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
   const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
-  const void* xp = X;
-  int64_t ldp = ldx;
-  if (perm) {
-    void* g = carve.take<uint16_t>(n * c * 2);
-    gptq::launch_gather_columns(X, n, c, ldx, perm, g, s);
-    xp = g;
-    ldp = c;
-  }
+  const int yi = yt == GPTQ_F32 ? 0 : xi;
   float* S = nullptr;
   if (low) {
     S = carve.take<float>(n * rank * 4);
     gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
   }
-  gptq::launch_packed_linear(xp, xi, n, ldp, w, ad, S, Y, yt == GPTQ_F32 ? 0 : xi, ldy, s);
+  if (gptq::packed_tiles(n, c)) {
+    uint16_t* xp = carve.take<uint16_t>(n * gptq::tiles_width(c) * 2);
+    int32_t* ex = carve.take<int32_t>(n * 4);
+    gptq::launch_prepare_tokens(X, xi, n, ldx, c, perm, xp, ex, s);
+    gptq::launch_packed_tiles(xp, ex, xi, n, w, ad, S, Y, yi, ldy, s);
+  } else {
+    const void* xp = X;
+    if (perm) {
+      uint16_t* g = carve.take<uint16_t>(n * c * 2);
+      gptq::launch_gather_columns(X, n, c, ldx, perm, g, s);
+      xp = g;
+    }
+    gptq::launch_packed_linear(xp, xi, n, perm ? c : ldx, w, ad, S, Y, yi, ldy, s);
+  }
   return check_launch(fn);
 }
 

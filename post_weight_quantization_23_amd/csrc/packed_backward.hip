@@ -155,7 +155,7 @@ __global__ __launch_bounds__(128 * MW) void backward_kernel(BwdArgs a) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t ti = t0 + wm + 16 * i;
-    if (a.T) expand_add<DT, 4>(a.ad, a.At, a.w.c, a.T, ti, a.n, col, acc[i]);
+    if (a.T) expand_add<DT, OT == 0 ? 3 : 2, 4>(a.ad, a.At, a.w.c, a.T, ti, a.n, col, acc[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll

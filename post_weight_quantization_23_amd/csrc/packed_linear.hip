@@ -26,34 +26,6 @@ struct FwdArgs {
   int row_tiles;
 };
 
-// Codes t and t + 4 of a block of eight, t = 0 .. 3, as pairs of 16-bit floats
-// 2^BITS + q.
-template <int BITS, int DT>
-GPTQ_DEV u32x4 code_pairs(uint32_t blk) {
-  constexpr int P = (DT == kBF16 ? 7 : 10) - BITS;   // lowest bit of the code in the mantissa
-  constexpr uint32_t one = DT == kBF16 ? (0x3F80u + (BITS << 7)) : (0x3C00u + (BITS << 10));
-  constexpr uint32_t mask = (((1u << BITS) - 1) << P) * 0x10001u, magic = one * 0x10001u;
-  if constexpr (BITS == 3) blk = (blk & 0xFFFu) | ((blk & 0xFFF000u) << 4);   // codes 4 .. 7 to the high half
-  u32x4 v;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    constexpr int B = BITS;
-    const int sh = P - B * t;
-    v[t] = ((sh >= 0 ? blk << sh : blk >> -sh) & mask) | magic;
-  }
-  return v;
-}
-
-// Eight consecutive activations in the order of code_pairs.
-GPTQ_DEV u32x4 pair_order(u32x4 v) {
-  u32x4 p;
-  p[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100u);
-  p[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302u);
-  p[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100u);
-  p[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);
-  return p;
-}
-
 constexpr int kWaves = 8;
 
 // 16 MT tokens x 16 rows per workgroup.  The waves split the columns in steps
@@ -159,7 +131,7 @@ __global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
       y[0][e] = v;
     }
     const int64_t rows[1] = {row0 + m < a.w.r ? row0 + m : -1};
-    if (a.S) expand_add<DT, 1>(a.ad, a.ad.B, a.w.r, a.S, t0 + 16 * i, a.n, rows, y);
+    if (a.S) expand_add<DT, YT == 0 ? 3 : 2, 1>(a.ad, a.ad.B, a.w.r, a.S, t0 + 16 * i, a.n, rows, y);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t t = t0 + 16 * i + 4 * kq + e;

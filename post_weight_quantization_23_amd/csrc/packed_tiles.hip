@@ -1,0 +1,359 @@
+// Product of many tokens (prompts, batches) with a packed layer on tiles of the
+// matrix cores, with the low-rank adapters beside it.
+//
+// Codes become fp16 values q - z exactly: a code shifted under the exponent of
+// 2^b reads as 2^b + q, and 2^b + z is subtracted two at a time (12 operations
+// for 8 codes).  Activations become fp16 once per call (prepare_tokens): bf16
+// ones are scaled by a power of two per token, which keeps every value within
+// 2^-29 of the token's largest exactly and the others to 2^-40 of it.  A
+// group's products are then whole-number weights times activations with fp32
+// sums, and its scale multiplies the sum: the weights are never rounded.
+//
+// Work split: 4 waves of 32 MT tokens x 32 NT rows over the same tokens, so a
+// workgroup is 32 MT x 128 NT.  Activations of 128 columns come into LDS by
+// loads that write it (double buffered; 16-byte chunks permuted by the row, so
+// that operand reads spread over the banks); words go straight into the
+// registers of the one wave that needs them, which dequantizes them once and
+// uses them for all MT token tiles.
+#include "adapter.hpp"
+
+namespace gptq {
+
+namespace {
+
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+
+constexpr int STEP = 128, ROWB = STEP * 2;   // columns of a step, bytes of an LDS row
+
+struct TileArgs {
+  const uint16_t* X;   // prepared activations [n][ldx]
+  const int32_t* ex;   // their exponents
+  int64_t n;
+  int ldx, row_tiles, tok_tiles;
+  PackedLayer w;
+  Adapters ad;
+  const float* S;      // null: no adapters
+  void* Y;
+  int64_t ldy;
+};
+
+// Tile of workgroup b.  Panels of 8 token tiles are walked row tile by row
+// tile; the dispatcher deals workgroups round robin to the 8 XCDs, so within
+// 256 workgroups XCD x is given 32 consecutive places of that walk: 8 token
+// tiles x 4 row tiles, whose activations and words its L2 shares.
+GPTQ_DEV void tile_of(int64_t b, int tok_tiles, int row_tiles, int& tok, int& row) {
+  const int64_t all = (int64_t)tok_tiles * row_tiles;
+  if (b < (all & ~(int64_t)255)) b = (b & ~(int64_t)255) | ((b & 7) << 5) | ((b & 255) >> 3);
+  const int64_t per = (int64_t)8 * row_tiles;
+  const int panel = (int)(b / per), in = (int)(b - panel * per);
+  const int h = min(8, tok_tiles - 8 * panel);
+  row = in / h;
+  tok = 8 * panel + in - row * h;
+}
+
+template <int BITS>
+struct Chunk {
+  uint32_t w[BITS];
+};
+
+template <int BITS>
+GPTQ_DEV Chunk<BITS> load_chunk(const uint32_t* words, int ch) {
+  Chunk<BITS> c;
+  const uint32_t* p = words + (int64_t)BITS * ch;
+  if constexpr (BITS == 4) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) c.w[i] = p[i];
+  }
+  return c;
+}
+
+// Codes (t, t + 4) of a block as fp16 pairs q - z; off is the pair of 2^BITS + z.
+template <int BITS>
+GPTQ_DEV u32x4 centered(uint32_t blk, half2_t off) {
+  u32x4 v = code_pairs<BITS, kF16>(blk);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t pair = v[t];   // (a bit cast of the vector's element itself would read element 0)
+    v[t] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, pair) - off);
+  }
+  return v;
+}
+
+// CPS: chunks of 32 columns that share a ruler within a step (4, 2 or 1).
+template <int BITS, int YT, int DT, int MT, int NT, int CPS>
+GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 31, h = lane >> 5;
+  int tt, rt;
+  tile_of(blockIdx.x, a.tok_tiles, a.row_tiles, tt, rt);
+  const int64_t t0 = (int64_t)tt * 32 * MT;
+  const int row0 = rt * 128 * NT + wave * 32 * NT;
+  const int nch = a.w.c >> 5, steps = (nch + 3) >> 2;
+
+  const uint32_t* words[NT];
+  const float* srow[NT];
+  const int32_t* zrow[NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int row = min(row0 + 32 * q + m, a.w.r - 1);
+    words[q] = a.w.words + (int64_t)row * a.w.ldw;
+    srow[q] = a.w.scales + (int64_t)row * a.w.ldg;
+    zrow[q] = a.w.zeros + (int64_t)row * a.w.ldg;
+  }
+
+  // activations: an instruction of a wave moves 4 rows of 256 bytes; rows past
+  // the last token lie outside the descriptor's records and read as zero
+  int off[2 * MT];
+#pragma unroll
+  for (int q = 0; q < 2 * MT; ++q) {
+    const int row = 4 * (wave * 2 * MT + q) + (lane >> 4);
+    off[q] = (row * a.ldx + 8 * ((lane & 15) ^ (row & 15))) * 2;
+  }
+  const int records = (int)(min(a.n - t0, (int64_t)32 * MT) * a.ldx * 2);
+  lds_u8* lbase = (lds_u8*)xs;
+  auto load_x = [&](int s) {
+    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)(a.X + t0 * a.ldx + s * STEP), (short)0,
+                                                                        records - s * ROWB, 0x00020000);
+#pragma unroll
+    for (int q = 0; q < 2 * MT; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, lbase + (s & 1) * (32 * MT * ROWB) + (wave * 2 * MT + q) * 1024, 16, off[q], 0,
+                                               0, 0);
+  };
+
+  constexpr int RU = 4 / CPS;   // rulers per step
+  Chunk<BITS> cw[NT][2];
+  float sc[NT][RU];
+  int ze[NT][RU];
+  auto load_w = [&](int s) {
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      cw[q][0] = load_chunk<BITS>(words[q], min(4 * s + 2 * h, nch - 1));
+      cw[q][1] = load_chunk<BITS>(words[q], min(4 * s + 2 * h + 1, nch - 1));
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        const int g = min(4 * s + CPS * u, nch - 1) / a.w.cpg;
+        sc[q][u] = srow[q][g];
+        ze[q][u] = zrow[q][g];
+      }
+    }
+  };
+
+  floatx16 tot[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) tot[i][q] = floatx16{};
+
+  load_x(0);
+  load_w(0);
+  for (int s = 0; s < steps; ++s) {
+    // this step's operands.  CPS == 4: product j takes words j of the lane's
+    // two chunks, columns 64 h + 8 j.  Otherwise the halves exchange words, so
+    // that products 2 ch and 2 ch + 1 are chunk ch alone, columns 32 ch + 8 h
+    // and + 16.
+    u32x4 wf[NT][8];
+    float scale[NT][RU];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      half2_t o[RU];
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        scale[q][u] = sc[q][u];
+        const _Float16 z = (_Float16)(float)((1 << BITS) + ze[q][u]);
+        o[u] = half2_t{z, z};
+      }
+      uint32_t blk[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) blk[j] = code_block<BITS>(cw[q][j >> 2].w, j & 3);
+      if constexpr (CPS < 4) {
+        uint32_t x[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const auto r = __builtin_amdgcn_permlane32_swap(blk[j], blk[j + 1], false, false);
+          const int c = j >> 2, u = (j >> 1) & 1;   // chunk of the half's two, product of the chunk
+          x[2 * c + u] = r[0];                      // chunk c (held by half 0)
+          x[2 * (2 + c) + u] = r[1];                // chunk 2 + c (held by half 1)
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) blk[j] = x[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wf[q][j] = centered<BITS>(blk[j], o[CPS == 4 ? 0 : (j >> 1) / CPS]);
+    }
+    // own loads have landed; with every wave here, the other buffer is free
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (s + 1 < steps) {
+      load_x(s + 1);
+      load_w(s + 1);
+    }
+    const unsigned char* xb = xs + (s & 1) * (32 * MT * ROWB);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      u32x4 x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int chunk = CPS == 4 ? 8 * h + j : 4 * (j >> 1) + 2 * (j & 1) + h;
+        x[j] = *reinterpret_cast<const u32x4*>(xb + (32 * i + m) * ROWB + ((chunk ^ (m & 15)) << 4));
+      }
+#pragma unroll
+      for (int u = 0; u < RU; ++u)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          floatx16 p = floatx16{};
+#pragma unroll
+          for (int j = 2 * CPS * u; j < 2 * CPS * (u + 1); ++j) p = mfma32<kF16>(x[j], wf[q][j], p);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) tot[i][q][e] = __builtin_fmaf(scale[q][u], p[e], tot[i][q][e]);
+        }
+    }
+  }
+
+  int64_t row[NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int at = row0 + 32 * q + m;
+    row[q] = at < a.w.r ? at : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t ti = t0 + 32 * i;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int64_t t = ti + TileShape<floatx16>::acc_row(lane, e);
+      const int ex = a.ex[min(t, a.n - 1)];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) tot[i][q][e] = __builtin_ldexpf(tot[i][q][e], ex);
+    }
+    if (a.S) expand_add<DT, YT == 0 ? 3 : 2, NT>(a.ad, a.ad.B, a.w.r, a.S, ti, a.n, row, tot[i]);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int64_t t = ti + TileShape<floatx16>::acc_row(lane, e);
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+        if (t < a.n && row[q] >= 0) store_out<YT>(a.Y, t * a.ldy + row[q], tot[i][q][e]);
+    }
+  }
+}
+
+template <int BITS, int YT, int DT, int MT, int NT, int CPS>
+__global__ __launch_bounds__(256, 2) void tiles_kernel(TileArgs a) {
+  __shared__ __align__(16) unsigned char xs[2 * 32 * MT * ROWB];
+  tiles_body<BITS, YT, DT, MT, NT, CPS>(a, xs);
+}
+
+// Activations for tiles_kernel: fp16 in the order of code_pairs, columns
+// gathered through perm, zero up to whole steps, and the token's exponent
+// (the value is X' 2^ex).  One workgroup per token.
+template <int DT>
+__global__ __launch_bounds__(256) void prepare_tokens_kernel(const uint16_t* __restrict__ X, int64_t ldx, bool vec, int c,
+                                                             const int32_t* __restrict__ perm, uint16_t* __restrict__ dst,
+                                                             int ldd, int32_t* __restrict__ exps) {
+  __shared__ float wave_max[4];
+  const int64_t t = blockIdx.x;
+  const uint16_t* x = X + t * ldx;
+  auto load = [&](int j) {
+    if (!perm) return load8(x + j, 8, vec);
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p0 = min(max(perm[j + 2 * e], 0), c - 1), p1 = min(max(perm[j + 2 * e + 1], 0), c - 1);
+      v[e] = (uint32_t)x[p0] | ((uint32_t)x[p1] << 16);
+    }
+    return v;
+  };
+  int shift = 0;
+  if constexpr (DT == kBF16) {
+    float top = 0.f;
+    for (int j = 8 * threadIdx.x; j < c; j += 2048) {
+      const u32x4 v = load8(x + j, 8, vec);   // any order will do
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        top = fmaxf(top, fabsf(__uint_as_float(v[e] << 16)));
+        top = fmaxf(top, fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
+      }
+    }
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
+    if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wave_max[0], wave_max[1]), fmaxf(wave_max[2], wave_max[3]));
+    shift = top > 0.f && top < __builtin_inff() ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+  }
+  if (threadIdx.x == 0) exps[t] = -shift;
+  for (int j = 8 * threadIdx.x; j < ldd; j += 2048) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (j < c) v = load(j);
+    if constexpr (DT == kBF16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = pack2<kF16>(__builtin_ldexpf(__uint_as_float(v[e] << 16), shift),
+                           __builtin_ldexpf(__uint_as_float(v[e] & 0xFFFF0000u), shift));
+    }
+    *reinterpret_cast<u32x4*>(dst + t * ldd + j) = pair_order(v);
+  }
+}
+
+template <int BITS, int YT, int DT, int MT, int NT>
+void launch_tiles(TileArgs a, hipStream_t s) {
+  a.row_tiles = (a.w.r + 128 * NT - 1) / (128 * NT);
+  a.tok_tiles = (int)((a.n + 32 * MT - 1) / (32 * MT));
+  const dim3 grid((unsigned)((int64_t)a.tok_tiles * a.row_tiles)), block(256);
+  if (a.w.cpg % 4 == 0 || a.w.cpg >= (a.w.c >> 5)) hipLaunchKernelGGL((tiles_kernel<BITS, YT, DT, MT, NT, 4>), grid, block, 0, s, a);
+  else if (a.w.cpg % 2 == 0) hipLaunchKernelGGL((tiles_kernel<BITS, YT, DT, MT, NT, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((tiles_kernel<BITS, YT, DT, MT, NT, 1>), grid, block, 0, s, a);
+}
+
+template <int BITS, int YT, int DT>
+void choose_tiles(const TileArgs& a, hipStream_t s) {
+#ifdef PROBE_MT
+  launch_tiles<BITS, YT, DT, PROBE_MT, PROBE_NT>(a, s);
+#else
+  launch_tiles<BITS, YT, DT, 4, 1>(a, s);
+#endif
+}
+
+}  // namespace
+
+int64_t tiles_width(int64_t c) { return (c + STEP - 1) / STEP * STEP; }
+
+bool packed_tiles(int64_t n, int64_t c) { return n > 64 && c <= (int64_t(1) << 22); }
+
+void launch_prepare_tokens(const void* X, int xt, int64_t n, int64_t ldx, int64_t c, const int32_t* perm, void* dst, int32_t* ex,
+                           hipStream_t s) {
+  const auto* x = static_cast<const uint16_t*>(X);
+  auto* d = static_cast<uint16_t*>(dst);
+  const int ldd = (int)tiles_width(c);
+  const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
+  if (xt == kBF16) hipLaunchKernelGGL((prepare_tokens_kernel<kBF16>), dim3((unsigned)n), dim3(256), 0, s, x, ldx, vec, (int)c, perm, d, ldd, ex);
+  else hipLaunchKernelGGL((prepare_tokens_kernel<kF16>), dim3((unsigned)n), dim3(256), 0, s, x, ldx, vec, (int)c, perm, d, ldd, ex);
+}
+
+void launch_packed_tiles(const void* X, const int32_t* ex, int xt, int64_t n, const PackedLayer& w, const Adapters& ad, const float* S,
+                         void* Y, int yt, int64_t ldy, hipStream_t s) {
+  TileArgs a{};
+  a.X = static_cast<const uint16_t*>(X);
+  a.ex = ex;
+  a.n = n;
+  a.ldx = (int)tiles_width(w.c);
+  a.w = w;
+  a.ad = ad;
+  a.S = S;
+  a.Y = Y;
+  a.ldy = ldy;
+#define GPTQ_TILES(B_)                                                                                     \
+  do {                                                                                                     \
+    if (xt == kBF16) { if (yt == 0) choose_tiles<B_, 0, kBF16>(a, s); else choose_tiles<B_, kBF16, kBF16>(a, s); } \
+    else { if (yt == 0) choose_tiles<B_, 0, kF16>(a, s); else choose_tiles<B_, kF16, kF16>(a, s); }        \
+  } while (0)
+  if (w.bits == 4) GPTQ_TILES(4);
+  else GPTQ_TILES(3);
+#undef GPTQ_TILES
+}
+
+}  // namespace gptq
