@@ -26,9 +26,10 @@
  * Packed layer arguments (packed, r, c, bits, ld_words, scales, zeros,
  * ld_groups, groupsize, col_perm) are those of gptq_dequant_gemv, with its
  * requirements, except that c is a positive multiple of 32 of any size up to
- * 2^30 and col_perm has to be a permutation of 0 .. c-1 in the backward call
- * (an input column that it leaves out keeps its old content; entries outside
- * the range are clamped; both stay inside the buffers).
+ * 2^30, zeros lie in -1000 .. 1000 (a ruler's lie in 0 .. 2^bits - 1), and
+ * col_perm has to be a permutation of 0 .. c-1 in the backward call (an input
+ * column that it leaves out or names twice has no defined gradient; entries
+ * outside the range are clamped; both stay inside the buffers).
  *
  * Adapter arguments:
  * A       : n_adapters x rank x c, B: n_adapters x r x rank, both dense, 16-byte
@@ -81,16 +82,20 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n_tok, int6
  *                           + alpha sum_p (sum_i dY[t, i] B_a[i, p]) A_a[p, src(j)] ),
  * the gradient of gptq_packed_linear for its input.  W_hat is rounded once to
  * dY's type, as gptq_linear_forward does, when dX is of that type; with ot =
- * GPTQ_F32 it enters as the sum of two such values (an error of 2^-17).
+ * GPTQ_F32 it enters as a sum of such values that holds fp32's precision
+ * (for GPTQ_F16: down to 2^-25).
  *
  * dY : n_tok x r of type xt, 2-byte aligned, ldy >= r (rows that start on 16
  *      bytes take the fast load path).
  * dX : n_tok x c of type ot (GPTQ_F32 or xt), row stride ldx; overlaps no input.
+ * r  : 1 .. 2^22 - 64.
  * ws : gptq_packed_linear_backward_workspace_size() bytes (n_adapters = rank
- *      = 0 without adapters; may be NULL when that is 0).
+ *      = 0 without adapters): it holds a dequantized copy of the layer, 2 r c
+ *      bytes (4 r c or 6 r c for fp32 results), while the call runs.
  * ------------------------------------------------------------------------ */
-gptq_status gptq_packed_linear_backward_workspace_size(int64_t n_tok, int64_t r, int64_t c, int64_t n_adapters,
-                                                       int64_t rank, size_t* bytes);
+gptq_status gptq_packed_linear_backward_workspace_size(int64_t n_tok, int64_t r, int64_t c, gptq_dtype xt,
+                                                       gptq_dtype ot, int64_t n_adapters, int64_t rank,
+                                                       size_t* bytes);
 gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n_tok, int64_t ldy,
                                         const uint32_t* packed, int64_t r, int64_t c, int bits, int64_t ld_words,
                                         const float* scales, const int32_t* zeros, int64_t ld_groups,

@@ -163,9 +163,7 @@ def packed_linear_backward(dY: torch.Tensor, packed: torch.Tensor, scales: torch
     ot = _out_type(out, out_dtype, dY.dtype)
     _check_out(out, "out", n, c, ot)
     dev = _device(dY, packed, scales, zeros, perm, A, B, index, alpha, out)
-    buf, nb = None, 0
-    if m:
-        buf, nb = _ws(ws, _lib.query("gptq_packed_linear_backward_workspace_size", n, r, c, m, rank), dev)
+    buf, nb = _ws(ws, _lib.query("gptq_packed_linear_backward_workspace_size", n, r, c, _DT[dY.dtype], _DT[ot], m, rank), dev)
     out = torch.empty((n, c), dtype=ot, device=dev) if out is None else out
     _lib.call("gptq_packed_linear_backward", _ptr(dY), _DT[dY.dtype], n, _ld(dY), _ptr(packed), r, c, int(bits), _ld(packed),
               _ptr(scales), _ptr(zeros), _ld(scales), int(groupsize), _ptr(perm), _ptr(A), _ptr(B), m, rank, _ptr(index),

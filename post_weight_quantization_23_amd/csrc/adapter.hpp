@@ -230,6 +230,21 @@ GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, co
   }
 }
 
+// ---------------------------------------------------------------- tile order
+// Tile of workgroup b.  Panels of 8 token tiles are walked row tile by row
+// tile; the dispatcher deals workgroups round robin to the 8 XCDs, so within
+// 256 workgroups XCD x is given 32 consecutive places of that walk: 8 token
+// tiles x 4 row tiles, whose activations and words its L2 shares.
+GPTQ_DEV void tile_of(int64_t b, int tok_tiles, int row_tiles, int& tok, int& row) {
+  const int64_t all = (int64_t)tok_tiles * row_tiles;
+  if (b < (all & ~(int64_t)255)) b = (b & ~(int64_t)255) | ((b & 7) << 5) | ((b & 255) >> 3);
+  const int64_t per = (int64_t)8 * row_tiles;
+  const int panel = (int)(b / per), in = (int)(b - panel * per);
+  const int h = min(8, tok_tiles - 8 * panel);
+  row = in / h;
+  tok = 8 * panel + in - row * h;
+}
+
 // ---------------------------------------------------------------- packed words
 // Eight consecutive codes of a row as one 32-bit block: the word itself (4
 // bits), or bits 24m .. 24m+23 of a chunk's 96 (3 bits).
@@ -304,8 +319,12 @@ void launch_prepare_tokens(const void* X, int xt, int64_t n, int64_t ldx, int64_
                            hipStream_t s);
 void launch_packed_tiles(const void* X, const int32_t* ex, int xt, int64_t n, const PackedLayer& w, const Adapters& ad, const float* S,
                          void* Y, int yt, int64_t ldy, hipStream_t s);
-// dX = dY W_hat (+ T A): packed_backward.hip.  At: A transposed to [m][c][rank].
+// dX = dY W_hat (+ T A): packed_backward.hip.  At: A transposed to [m][c][rank];
+// Wt: backward_terms x c x backward_depth(r) values, rows: n x backward_depth(r).
+constexpr int backward_terms(int xt, int ot) { return ot != 0 ? 1 : (xt == kBF16 ? 3 : 2); }
+int64_t backward_depth(int64_t r);
 void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, const PackedLayer& w, const Adapters& ad,
-                            const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, hipStream_t s);
+                            const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, uint16_t* Wt, uint16_t* rows,
+                            hipStream_t s);
 
 }  // namespace gptq

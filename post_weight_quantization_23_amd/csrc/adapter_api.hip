@@ -13,6 +13,7 @@ using namespace gptq::api;
 namespace {
 
 constexpr int64_t kMaxCols = int64_t(1) << 30;
+constexpr int64_t kMaxDepth = (int64_t(1) << 22) - 64;   // rows of the layer in the input gradient
 constexpr int64_t kMaxAdapters = int64_t(1) << 20;
 
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -133,11 +134,18 @@ bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
   return groups_for(n * (rank > 0 ? rank : 1), 4) <= kMaxGroups256 &&                    // down: a wave per value
          groups_for(n, 16) * groups_for(r, 16) <= kMaxGroups256 / 2 &&                   // forward: 512 threads per 16 rows
          groups_for(n, 16) * groups_for(r > c ? r : c, 256) <= kMaxGroups256 &&          // up
-         groups_for(n, 128) * groups_for(c, 128) <= kMaxGroups256 &&                     // backward
+         groups_for(n, 32) * groups_for(r > c ? r : c, 128) <= kMaxGroups256 / 2 &&      // tiles
+         groups_for(r, 64) * groups_for(c, 256) <= kMaxGroups256 &&                      // dequantized copy
+         groups_for(n * (r / 8 + 8), 256) <= kMaxGroups256 &&                            // padded rows
          groups_for(n * (c / 8), 256) <= kMaxGroups256 &&                                // gather
          m * groups_for(r > c ? r : c, 64) * 2 <= kMaxGroups256 &&                       // transpose (rank <= 128)
          m * groups_for(r > c ? r : c, 128) * 2 * 16 <= kMaxGroups256 &&                 // gradients (16 splits)
          groups_for(m * rank * (r > c ? r : c), 1024) <= kMaxGroups256;                  // join
+}
+
+// The input gradient's dequantized weights and padded rows of dY.
+int64_t backward_bytes(int64_t n, int64_t r, int64_t c, int terms) {
+  return align256(terms * c * gptq::backward_depth(r) * 2) + align256(n * gptq::backward_depth(r) * 2);
 }
 
 struct GradSizes {
@@ -230,15 +238,19 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
 }
 
 // ------------------------------------------------------------------ its input gradient
-gptq_status gptq_packed_linear_backward_workspace_size(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank,
-                                                       size_t* bytes) {
+gptq_status gptq_packed_linear_backward_workspace_size(int64_t n, int64_t r, int64_t c, gptq_dtype xt, gptq_dtype ot, int64_t m,
+                                                       int64_t rank, size_t* bytes) {
   const char* fn = "gptq_packed_linear_backward_workspace_size";
   if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
+  if (!valid_dtype(xt) || !valid_dtype(ot)) return fail(GPTQ_EINVAL, fn, "xt and ot must be gptq_dtype values");
+  if (xt == GPTQ_F32 || (ot != GPTQ_F32 && ot != xt)) return fail(GPTQ_EDTYPE, fn, "xt must be 16-bit, ot GPTQ_F32 or xt");
   if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
   if (m != 0 || rank != 0)
     if (gptq_status st = check_rank(fn, m, rank)) return st;
   if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
-  *bytes = (size_t)(align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, rank));
+  if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
+  *bytes = (size_t)(backward_bytes(n, r, c, gptq::backward_terms((int)xt, (int)ot)) + align256(m * c * rank * 2) +
+                    align256(m * rank * pad8(r) * 2) + low_bytes(n, rank));
   return ok();
 }
 
@@ -259,6 +271,7 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
     if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
   if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (r == 0) return fail(GPTQ_ESHAPE, fn, "r must be positive");
+  if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
   if (n == 0) return ok();
   if (gptq_status st = check_packed(fn, packed, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm)) return st;
   if (ldx < c || ldy < r) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
@@ -271,13 +284,16 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
     if (gptq_status st = check_clash(fn, clash(dX, ex, A, m * rank, c, c, 2))) return st;
     if (gptq_status st = check_clash(fn, clash(dX, ex, B, m * r, rank, rank, 2))) return st;
   }
-  const int64_t need = align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, rank);
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, low ? need : 0)) return st;
+  const int terms = gptq::backward_terms((int)xt, (int)ot);
+  const int64_t need = backward_bytes(n, r, c, terms) + align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, rank);
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, need)) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
   const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
+  uint16_t* Wt = carve.take<uint16_t>(terms * c * gptq::backward_depth(r) * 2);
+  uint16_t* rows = carve.take<uint16_t>(n * gptq::backward_depth(r) * 2);
   uint16_t* At = nullptr;
   float* T = nullptr;
   if (low) {
@@ -288,7 +304,7 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
     gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
     gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);
   }
-  gptq::launch_packed_backward(dY, xi, n, ldy, w, ad, At, T, dX, ot == GPTQ_F32 ? 0 : xi, ldx, s);
+  gptq::launch_packed_backward(dY, xi, n, ldy, w, ad, At, T, dX, ot == GPTQ_F32 ? 0 : xi, ldx, Wt, rows, s);
   return check_launch(fn);
 }
 

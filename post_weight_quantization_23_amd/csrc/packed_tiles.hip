@@ -38,20 +38,6 @@ struct TileArgs {
   int64_t ldy;
 };
 
-// Tile of workgroup b.  Panels of 8 token tiles are walked row tile by row
-// tile; the dispatcher deals workgroups round robin to the 8 XCDs, so within
-// 256 workgroups XCD x is given 32 consecutive places of that walk: 8 token
-// tiles x 4 row tiles, whose activations and words its L2 shares.
-GPTQ_DEV void tile_of(int64_t b, int tok_tiles, int row_tiles, int& tok, int& row) {
-  const int64_t all = (int64_t)tok_tiles * row_tiles;
-  if (b < (all & ~(int64_t)255)) b = (b & ~(int64_t)255) | ((b & 7) << 5) | ((b & 255) >> 3);
-  const int64_t per = (int64_t)8 * row_tiles;
-  const int panel = (int)(b / per), in = (int)(b - panel * per);
-  const int h = min(8, tok_tiles - 8 * panel);
-  row = in / h;
-  tok = 8 * panel + in - row * h;
-}
-
 template <int BITS>
 struct Chunk {
   uint32_t w[BITS];

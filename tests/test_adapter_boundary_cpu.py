@@ -49,9 +49,12 @@ def test_workspace_queries(lib):
     assert f(16, 48, 0, 0, C.byref(out)) == 3 and f(16, 0, 0, 0, C.byref(out)) == 3
     assert f(16, 4096, 12, 0, C.byref(out)) == 5 and f(16, 4096, 136, 0, C.byref(out)) == 5
     f = lib.gptq_packed_linear_backward_workspace_size
-    assert f(16, 100, 4096, 0, 0, C.byref(out)) == 0
-    assert f(16, 100, 4096, 2, 8, C.byref(out)) == 0 and out.value >= 2 * 8 * (4096 + 100) * 2
-    assert f(16, 100, 4096, 0, 8, C.byref(out)) == 1 and f(16, 100, 4096, 2, 0, C.byref(out)) == 5
+    assert f(16, 100, 4096, 1, 1, 0, 0, C.byref(out)) == 0 and out.value >= 100 * 4096 * 2
+    assert f(16, 100, 4096, 1, 0, 0, 0, C.byref(out)) == 0 and out.value >= 3 * 100 * 4096 * 2
+    assert f(16, 100, 4096, 2, 2, 2, 8, C.byref(out)) == 0 and out.value >= 100 * 4096 * 2 + 2 * 8 * (4096 + 100) * 2
+    assert f(16, 100, 4096, 1, 1, 0, 8, C.byref(out)) == 1 and f(16, 100, 4096, 1, 1, 2, 0, C.byref(out)) == 5
+    assert f(16, 100, 4096, 0, 0, 0, 0, C.byref(out)) == 2 and f(16, 100, 4096, 1, 2, 0, 0, C.byref(out)) == 2
+    assert f(16, 1 << 22, 4096, 1, 1, 0, 0, C.byref(out)) == 5
     f = lib.gptq_adapter_add_workspace_size
     assert f(16, 8, C.byref(out)) == 0 and out.value >= 16 * 8 * 4 and f(16, 0, C.byref(out)) == 5
     f = lib.gptq_adapter_backward_workspace_size
@@ -107,7 +110,7 @@ def test_packed_linear_backward_argument_errors(lib):
     assert f(n=0, X=None) == 0 and f(r=0) == 3
     assert f(n=-1) == 1 and f(xt=0) == 2 and f(yt=2) == 2 and f(c=100) == 3 and f(bits=5) == 5
     assert f(ldx=255) == 3 and f(ldy=7) == 3 and f(X=None) == 1 and f(Y=None) == 1
-    assert f(X=at(P(0), 1)) == 4 and f(Y=at(P(8), 1)) == 4
+    assert f(X=at(P(0), 1)) == 4 and f(Y=at(P(8), 1)) == 4 and f() == 6
     assert f(Y=P(0)) == 1 and f(Y=P(1)) == 1
     assert f(A=P(5), B=P(6), m=2, rank=8) == 6 and f(A=P(5), B=P(6), m=2, rank=4) == 5
 
