@@ -57,8 +57,9 @@ extern "C" {
 
 /* ------------------------------------------------------------------------
  * Y[t, i] = round_yt( sum_j W_hat[i, j] X[t, src(j)] + delta[t, i] ),
- * src(j) = col_perm[j], or j.  Codes are multiplied as whole numbers and the
- * rulers applied to each group's fp32 sum, so the weights are not rounded:
+ * src(j) = col_perm[j], or j.  Up to 1023 tokens, and for fp32 results of any
+ * number, codes are multiplied as whole numbers and the rulers applied to each
+ * group's fp32 sum, so the weights are not rounded:
  * the fp32 result is within about 2^-16 sum_j scale (2 * 2^bits + q + zero)
  * |x_j| of the exact product (a bound; usual errors are far smaller).  |X| must stay below 2^115 (larger bf16 values can
  * overflow a group's sum); a token that holds an infinity or NaN gives NaN.
@@ -69,7 +70,8 @@ extern "C" {
  * ws : gptq_packed_linear_workspace_size(n_tok, c, rank, col_perm != NULL)
  *      bytes, rank 0 without adapters (NULL when that is 0).
  * ------------------------------------------------------------------------ */
-gptq_status gptq_packed_linear_workspace_size(int64_t n_tok, int64_t c, int64_t rank, int has_perm, size_t* bytes);
+gptq_status gptq_packed_linear_workspace_size(int64_t n_tok, int64_t r, int64_t c, gptq_dtype yt, int64_t rank,
+                                              int has_perm, size_t* bytes);
 gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n_tok, int64_t ldx, const uint32_t* packed,
                                int64_t r, int64_t c, int bits, int64_t ld_words, const float* scales,
                                const int32_t* zeros, int64_t ld_groups, int64_t groupsize, const int32_t* col_perm,

@@ -37,7 +37,7 @@ SIGNATURES = {
                                       _P, C.c_int, _I64, _P]),
     "gptq_round16": (C.c_int, [_P, _I64, _I64, _I64, C.c_int, _P, _I64, _P]),
     # include/gptq_adapter.h
-    "gptq_packed_linear_workspace_size": (C.c_int, [_I64, _I64, _I64, C.c_int, _SZP]),
+    "gptq_packed_linear_workspace_size": (C.c_int, [_I64, _I64, _I64, C.c_int, _I64, C.c_int, _SZP]),
     "gptq_packed_linear": (C.c_int, [_P, C.c_int, _I64, _I64, _P, _I64, _I64, C.c_int, _I64, _P, _P, _I64, _I64, _P,
                                      _P, _P, _I64, _I64, _P, _P, _P, C.c_int, _I64, _P, _SZ, _P]),
     "gptq_packed_linear_backward_workspace_size": (C.c_int, [_I64, _I64, _I64, C.c_int, C.c_int, _I64, _I64, _SZP]),

@@ -133,7 +133,7 @@ def packed_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, z
     yt = _out_type(out, out_dtype, X.dtype)
     _check_out(out, "out", n, r, yt)
     dev = _device(X, packed, scales, zeros, perm, A, B, index, alpha, out)
-    buf, nb = _ws(ws, _lib.query("gptq_packed_linear_workspace_size", n, c, rank, int(perm is not None)), dev)
+    buf, nb = _ws(ws, _lib.query("gptq_packed_linear_workspace_size", n, r, c, _DT[yt], rank, int(perm is not None)), dev)
     out = torch.empty((n, r), dtype=yt, device=dev) if out is None else out
     _lib.call("gptq_packed_linear", _ptr(X), _DT[X.dtype], n, _ld(X), _ptr(packed), r, c, int(bits), _ld(packed),
               _ptr(scales), _ptr(zeros), _ld(scales), int(groupsize), _ptr(perm), _ptr(A), _ptr(B), m, rank, _ptr(index),

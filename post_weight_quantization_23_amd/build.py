@@ -28,8 +28,8 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 # slowest first: the pool starts them at once
 SOURCES = ["quantize.hip", "linear.hip", "gemm_f32.hip", "syrk.hip", "gemv.hip", "prepare.hip",
-           "hadamard.hip", "pack.hip", "packed_linear.hip", "packed_tiles.hip", "packed_backward.hip", "adapter.hip",
-           "gptq_api.hip", "adapter_api.hip", "workspace.hip"]
+           "hadamard.hip", "pack.hip", "packed_linear.hip", "packed_tiles.hip", "packed_backward.hip", "gemm16.hip",
+           "adapter.hip", "gptq_api.hip", "adapter_api.hip", "workspace.hip"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
@@ -44,7 +44,8 @@ API_HEADERS = [os.path.join(ROOT, "include", "gptq.h"), os.path.join(ROOT, "incl
 # headers that only some sources include
 MORE_HEADERS = {"gptq_api.hip": [os.path.join(CSRC, "api.hpp"), *API_HEADERS],
                 "adapter_api.hip": [os.path.join(CSRC, "api.hpp"), os.path.join(CSRC, "adapter.hpp"), *API_HEADERS],
-                **{f: [os.path.join(CSRC, "adapter.hpp")] for f in ("packed_linear.hip", "packed_tiles.hip", "packed_backward.hip", "adapter.hip")}}
+                **{f: [os.path.join(CSRC, "adapter.hpp")] for f in ("packed_linear.hip", "packed_tiles.hip", "packed_backward.hip", "gemm16.hip",
+                                                            "adapter.hip")}}
 
 
 def source_id() -> str:

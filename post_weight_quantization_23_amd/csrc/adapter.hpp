@@ -230,6 +230,53 @@ GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, co
   }
 }
 
+// ---------------------------------------------------------------- tile results
+// Stores a wave's 32 tokens x 32 NT outputs (accumulators of mfma32) to out,
+// turned through the wave's own 32 x (32 NT + 4) floats of LDS so that a row
+// leaves in whole runs of eight outputs per lane (single stores of two bytes
+// took a tenth of a 256 x 256 tile's time at 4096 columns).  vec: rows of out
+// start on 16 bytes.
+template <int OT, int NT>
+GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], void* out, int64_t t0, int64_t n, int64_t j0, int64_t cols, int64_t ldo,
+                         bool vec) {
+  constexpr int W = 32 * NT, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) lds[TileShape<floatx16>::acc_row(lane, e) * LD + 32 * q + (lane & 31)] = acc[q][e];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+  for (int k = 0; k < 32 / RPP; ++k) {
+    const int r = RPP * k + lane / LPR, c = 8 * (lane % LPR);
+    const int64_t t = t0 + r, j = j0 + c;
+    float v[8];
+    load8f(lds + r * LD + c, v);
+    if (t >= n || j >= cols) continue;
+    if (vec && j + 8 <= cols) {
+      if constexpr (OT == 0) {
+        float* o = static_cast<float*>(out) + t * ldo + j;
+        *reinterpret_cast<floatx4*>(o) = floatx4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<floatx4*>(o + 4) = floatx4{v[4], v[5], v[6], v[7]};
+      } else {
+        const u32x4 o = {pack2<OT>(v[0], v[1]), pack2<OT>(v[2], v[3]), pack2<OT>(v[4], v[5]), pack2<OT>(v[6], v[7])};
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + t * ldo + j) = o;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e < cols) store_out<OT>(out, t * ldo + j + e, v[e]);
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// Whether rows of a result of type ot (0 fp32) start on 16 bytes.
+inline bool rows_on_16(const void* p, int64_t ld, int ot) {
+  const int64_t e = ot == 0 ? 4 : 2;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * e % 16 == 0;
+}
+
 // ---------------------------------------------------------------- tile order
 // Tile of workgroup b.  Panels of 8 token tiles are walked row tile by row
 // tile; the dispatcher deals workgroups round robin to the 8 XCDs, so within
@@ -253,6 +300,13 @@ GPTQ_DEV uint32_t code_block(const uint32_t* chunk, int m) {
   if constexpr (BITS == 4) return chunk[m];
   const int bit = 24 * m, w = bit >> 5;
   return (__builtin_amdgcn_alignbit(chunk[w < 2 ? w + 1 : 2], chunk[w], bit & 31)) & 0xFFFFFFu;
+}
+
+// Block b of a 3-bit row (its bits 24 .. 31 are not the block's).
+GPTQ_DEV uint32_t straddling_block(const uint32_t* words, int b) {
+  const uint32_t* c = words + 3 * (int64_t)(b >> 2);
+  const int bit = 24 * (b & 3), at = bit >> 5;
+  return __builtin_amdgcn_alignbit(c[at < 2 ? at + 1 : 2], c[at], bit & 31);
 }
 
 // Codes t and t + 4 of a block of eight, t = 0 .. 3, as pairs of 16-bit floats
@@ -306,23 +360,44 @@ void launch_adapter_grad(const float* V, const void* Z, int zt, int64_t n, int64
                          const int32_t* order, const int32_t* start, int up, float* G, float* part, int splits,
                          hipStream_t s);
 
+// out = X W^T (+ S B^T): gemm16.hip.  The contraction has kp columns, a
+// multiple of its step, with zeros in W past the last one (and finite values
+// in X).
+constexpr int kGemm16Step = 64;
+inline int64_t gemm16_depth(int64_t k) { return (k + kGemm16Step - 1) / kGemm16Step * kGemm16Step; }
+struct Gemm16 {
+  const uint16_t* X;      // [n][ldx], rows on 16 bytes, ldx < 2^22
+  const uint16_t* W;      // [terms][cols][kp], kp < 2^22
+  int64_t n, ldx, kp;
+  int cols, tok_tiles, col_tiles;
+  Adapters ad;
+  const uint16_t* B;      // [m][cols][rank]
+  const float* S;         // null: no adapters
+  void* out;
+  int64_t ldo;
+  bool vec;               // set by launch_gemm16
+};
+// dt: type of X, W and B; ot: of out.  fp32 results take W in as many terms of
+// its type as fp32 has bits.
+constexpr int gemm16_terms(int dt, int ot) { return ot != 0 ? 1 : (dt == kBF16 ? 3 : 2); }
+void launch_gemm16(const Gemm16& a, int dt, int ot, hipStream_t s);
+// Whether rows of d values can be its X as they are, and a copy (n x
+// gemm16_depth(d)) that can.
+bool gemm16_takes(const void* X, int64_t d, int64_t ldx);
+void launch_pad_rows(const void* X, int64_t n, int64_t d, int64_t ldx, const int32_t* perm, uint16_t* dst, hipStream_t s);
+
 // Y = X W_hat^T (+ S B^T): packed_linear.hip.
 void launch_packed_linear(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad,
                           const float* S, void* Y, int yt, int64_t ldy, hipStream_t s);
 // dst[t][j] = X[t][perm[j]] (entries outside 0 .. c-1 clamped), dst dense.
 void launch_gather_columns(const void* X, int64_t n, int64_t c, int64_t ldx, const int32_t* perm, void* dst, hipStream_t s);
-// The same on tiles for many tokens: packed_tiles.hip.  prepare_tokens writes
-// n x tiles_width(c) 16-bit values and n exponents.
+// The same for many tokens: packed_tiles.hip.  ws: packed_tiles_bytes().
 bool packed_tiles(int64_t n, int64_t c);
-int64_t tiles_width(int64_t c);
-void launch_prepare_tokens(const void* X, int xt, int64_t n, int64_t ldx, int64_t c, const int32_t* perm, void* dst, int32_t* ex,
-                           hipStream_t s);
-void launch_packed_tiles(const void* X, const int32_t* ex, int xt, int64_t n, const PackedLayer& w, const Adapters& ad, const float* S,
-                         void* Y, int yt, int64_t ldy, hipStream_t s);
+int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt);
+void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad, const float* S,
+                         void* Y, int yt, int64_t ldy, void* ws, hipStream_t s);
 // dX = dY W_hat (+ T A): packed_backward.hip.  At: A transposed to [m][c][rank];
-// Wt: backward_terms x c x backward_depth(r) values, rows: n x backward_depth(r).
-constexpr int backward_terms(int xt, int ot) { return ot != 0 ? 1 : (xt == kBF16 ? 3 : 2); }
-int64_t backward_depth(int64_t r);
+// Wt: gemm16_terms x c x gemm16_depth(r) values, rows: n x gemm16_depth(r).
 void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, const PackedLayer& w, const Adapters& ad,
                             const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, uint16_t* Wt, uint16_t* rows,
                             hipStream_t s);

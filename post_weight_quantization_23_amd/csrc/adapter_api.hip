@@ -120,10 +120,10 @@ gptq_status check_clash(const char* fn, int c) {
   return GPTQ_OK;
 }
 
-// Activations of the packed product as its kernels take them: a gathered copy
-// for a few tokens of an act-order layer, a prepared copy for many.
-int64_t token_bytes(int64_t n, int64_t c, bool perm) {
-  if (gptq::packed_tiles(n, c)) return align256(n * gptq::tiles_width(c) * 2) + align256(n * 4);
+// What the packed product's kernels prepare: the gathered activations of a few
+// tokens of an act-order layer, or what many tokens need.
+int64_t forward_bytes(int64_t n, int64_t r, int64_t c, bool perm, int yt) {
+  if (gptq::packed_tiles(n, c)) return gptq::packed_tiles_bytes(n, r, c, yt);
   return perm ? align256(n * c * 2) : 0;
 }
 
@@ -145,7 +145,7 @@ bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
 
 // The input gradient's dequantized weights and padded rows of dY.
 int64_t backward_bytes(int64_t n, int64_t r, int64_t c, int terms) {
-  return align256(terms * c * gptq::backward_depth(r) * 2) + align256(n * gptq::backward_depth(r) * 2);
+  return align256(terms * c * gptq::gemm16_depth(r) * 2) + align256(n * gptq::gemm16_depth(r) * 2);
 }
 
 struct GradSizes {
@@ -169,14 +169,16 @@ GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
 extern "C" {
 
 // ------------------------------------------------------------------ packed product
-gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t c, int64_t rank, int has_perm, size_t* bytes) {
+gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t r, int64_t c, gptq_dtype yt, int64_t rank, int has_perm,
+                                              size_t* bytes) {
   const char* fn = "gptq_packed_linear_workspace_size";
   if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
   if (has_perm != 0 && has_perm != 1) return fail(GPTQ_EINVAL, fn, "has_perm must be 0 or 1");
-  if (gptq_status st = check_sizes(fn, n, 0, c, 32)) return st;
+  if (!valid_dtype(yt)) return fail(GPTQ_EINVAL, fn, "yt must be a gptq_dtype value");
+  if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
   if (rank != 0)
     if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  *bytes = (size_t)(token_bytes(n, c, has_perm != 0) + low_bytes(n, rank));
+  *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, rank));
   return ok();
 }
 
@@ -208,7 +210,7 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
     if (gptq_status st = check_clash(fn, clash(Y, ey, A, m * rank, c, c, 2))) return st;
     if (gptq_status st = check_clash(fn, clash(Y, ey, B, m * r, rank, rank, 2))) return st;
   }
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, token_bytes(n, c, perm != nullptr) + low_bytes(n, rank))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, forward_bytes(n, r, c, perm != nullptr, (int)yt) + low_bytes(n, rank))) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
@@ -221,10 +223,7 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
     gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
   }
   if (gptq::packed_tiles(n, c)) {
-    uint16_t* xp = carve.take<uint16_t>(n * gptq::tiles_width(c) * 2);
-    int32_t* ex = carve.take<int32_t>(n * 4);
-    gptq::launch_prepare_tokens(X, xi, n, ldx, c, perm, xp, ex, s);
-    gptq::launch_packed_tiles(xp, ex, xi, n, w, ad, S, Y, yi, ldy, s);
+    gptq::launch_packed_tiles(X, xi, n, ldx, w, ad, S, Y, yi, ldy, carve.at, s);
   } else {
     const void* xp = X;
     if (perm) {
@@ -249,7 +248,7 @@ gptq_status gptq_packed_linear_backward_workspace_size(int64_t n, int64_t r, int
     if (gptq_status st = check_rank(fn, m, rank)) return st;
   if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
-  *bytes = (size_t)(backward_bytes(n, r, c, gptq::backward_terms((int)xt, (int)ot)) + align256(m * c * rank * 2) +
+  *bytes = (size_t)(backward_bytes(n, r, c, gptq::gemm16_terms((int)xt, (int)ot)) + align256(m * c * rank * 2) +
                     align256(m * rank * pad8(r) * 2) + low_bytes(n, rank));
   return ok();
 }
@@ -284,7 +283,7 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
     if (gptq_status st = check_clash(fn, clash(dX, ex, A, m * rank, c, c, 2))) return st;
     if (gptq_status st = check_clash(fn, clash(dX, ex, B, m * r, rank, rank, 2))) return st;
   }
-  const int terms = gptq::backward_terms((int)xt, (int)ot);
+  const int terms = gptq::gemm16_terms((int)xt, (int)ot);
   const int64_t need = backward_bytes(n, r, c, terms) + align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, rank);
   if (gptq_status st = need_ws(fn, ws, ws_bytes, need)) return st;
   Carve carve{static_cast<char*>(ws)};
@@ -292,8 +291,8 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
   const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
   const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
-  uint16_t* Wt = carve.take<uint16_t>(terms * c * gptq::backward_depth(r) * 2);
-  uint16_t* rows = carve.take<uint16_t>(n * gptq::backward_depth(r) * 2);
+  uint16_t* Wt = carve.take<uint16_t>(terms * c * gptq::gemm16_depth(r) * 2);
+  uint16_t* rows = carve.take<uint16_t>(n * gptq::gemm16_depth(r) * 2);
   uint16_t* At = nullptr;
   float* T = nullptr;
   if (low) {

@@ -1,0 +1,180 @@
+// out = X W^T (+ S B^T) with 16-bit operands that are both contiguous along the
+// contraction, on tiles of the matrix cores: the product behind the input
+// gradient (packed_backward.hip) and behind the packed product of many tokens
+// (packed_tiles.hip), each of which prepares its operands first.
+#include "adapter.hpp"
+
+namespace gptq {
+
+namespace {
+
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+
+// ---------------------------------------------------------------- product
+constexpr int LK = kGemm16Step, ROWB = LK * 2;   // contraction step, bytes of an LDS row
+
+// Chunk c (16 bytes) of LDS row f lies at place c ^ swz(f).
+GPTQ_DEV int swz(int f) { return (f ^ (f >> 3)) & 7; }
+
+// WM x WN waves of 32 MT tokens x 32 NT columns.  Both operands come from
+// memory straight into LDS (double buffered, one barrier per step), each lane
+// fetching the chunk that belongs at its place; rows past the end lie outside
+// the descriptors' records and read as zero.
+template <int DT, int OT, int TERMS, int MT, int NT, int WM, int WN>
+GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
+  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, NW = WM * WN, BUF = (TM + TN) * ROWB;
+  constexpr int QX = TM / 8 / NW, QW = TN / 8 / NW;   // load instructions per wave: 8 rows each
+  static_assert(QX * 8 * NW == TM && QW * 8 * NW == TN, "tiles divide over the waves");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 31, h = lane >> 5;
+  int tt, ct;
+  tile_of(blockIdx.x, a.tok_tiles, a.col_tiles, tt, ct);
+  const int64_t t0 = (int64_t)tt * TM;
+  const int j0 = ct * TN;
+  const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
+  lds_u8* lbase = (lds_u8*)smem;
+
+  int offx[QX], offw[QW];
+#pragma unroll
+  for (int q = 0; q < QX; ++q) {
+    const int row = 8 * (wave * QX + q) + (lane >> 3);
+    offx[q] = (row * (int)a.ldx + 8 * ((lane & 7) ^ swz(row))) * 2;
+  }
+#pragma unroll
+  for (int q = 0; q < QW; ++q) {
+    const int row = 8 * (wave * QW + q) + (lane >> 3);
+    offw[q] = (row * (int)a.kp + 8 * ((lane & 7) ^ swz(row))) * 2;
+  }
+  const int xrec = (int)(min(a.n - t0, (int64_t)TM) * a.ldx * 2), wrec = (int)(min(a.cols - j0, TN) * a.kp * 2);
+  const int steps = (int)(a.kp / LK), all = TERMS * steps;
+  auto load = [&](int s) {
+    const int term = TERMS == 1 ? 0 : s / steps, k0 = (s - term * steps) * LK;
+    const __amdgpu_buffer_rsrc_t rx =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(a.X + t0 * a.ldx + k0), (short)0, xrec - 2 * k0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(a.W + ((int64_t)term * a.cols + j0) * a.kp + k0), (short)0, wrec - 2 * k0, 0x00020000);
+    lds_u8* to = lbase + (s & 1) * BUF;
+#pragma unroll
+    for (int q = 0; q < QX; ++q) __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to + (wave * QX + q) * 1024, 16, offx[q], 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < QW; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to + TM * ROWB + (wave * QW + q) * 1024, 16, offw[q], 0, 0, 0);
+  };
+
+  floatx16 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) acc[i][q] = floatx16{};
+
+  load(0);
+  for (int s = 0; s < all; ++s) {
+    // own loads have landed; with every wave here, the other buffer is free
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (s + 1 < all) load(s + 1);
+    const unsigned char* xb = smem + (s & 1) * BUF;
+    const unsigned char* wb = xb + TM * ROWB;
+#pragma unroll
+    for (int k = 0; k < LK / 16; ++k) {
+      u32x4 x[MT], w[NT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int f = wm + 32 * i + m;
+        x[i] = *reinterpret_cast<const u32x4*>(xb + f * ROWB + (((2 * k + h) ^ swz(f)) << 4));
+      }
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const int f = wn + 32 * q + m;
+        w[q] = *reinterpret_cast<const u32x4*>(wb + f * ROWB + (((2 * k + h) ^ swz(f)) << 4));
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[i][q] = mfma32<DT>(x[i], w[q], acc[i][q]);
+    }
+  }
+
+  static_assert(NW * 32 * (32 * NT + 4) * 4 <= 2 * BUF, "tile results fit the operands' LDS");
+  float* own = reinterpret_cast<float*>(smem) + wave * 32 * (32 * NT + 4);
+  __syncthreads();   // the last step's operands have been read
+  int64_t col[NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int at = j0 + wn + 32 * q + m;
+    col[q] = at < a.cols ? at : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t ti = t0 + wm + 32 * i;
+    if (a.S) expand_add<DT, OT == 0 ? 3 : 2, NT>(a.ad, a.B, a.cols, a.S, ti, a.n, col, acc[i]);
+    store_tile<OT, NT>(own, acc[i], a.out, ti, a.n, j0 + wn, a.cols, a.ldo, a.vec);
+  }
+}
+
+template <int DT, int OT, int TERMS, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(Gemm16 a) {
+  extern __shared__ __align__(16) unsigned char gsm[];
+  gemm_body<DT, OT, TERMS, MT, NT, WM, WN>(a, gsm);
+}
+
+template <int DT, int OT, int TERMS, int MT, int NT, int WM, int WN>
+void launch_gemm(Gemm16 a, hipStream_t s) {
+  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, LDS = 2 * (TM + TN) * ROWB;
+  static const bool set = [] {   // once, thread-safe
+    (void)hipFuncSetAttribute((const void*)gemm_kernel<DT, OT, TERMS, MT, NT, WM, WN>, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+    return true;
+  }();
+  (void)set;
+  a.tok_tiles = (int)((a.n + TM - 1) / TM);
+  a.col_tiles = (a.cols + TN - 1) / TN;
+  hipLaunchKernelGGL((gemm_kernel<DT, OT, TERMS, MT, NT, WM, WN>), dim3((unsigned)((int64_t)a.tok_tiles * a.col_tiles)),
+                     dim3(64 * WM * WN), LDS, s, a);
+}
+
+template <int DT, int OT, int TERMS>
+void choose_gemm(const Gemm16& a, hipStream_t s) {
+  const int64_t big = (a.n + 255) / 256 * ((a.cols + 255) / 256);
+  if (big >= 192) launch_gemm<DT, OT, TERMS, 4, 2, 2, 4>(a, s);
+  else launch_gemm<DT, OT, TERMS, 2, 2, 2, 2>(a, s);
+}
+
+// dst[t][0 .. kp) = src[t][0 .. d) (through perm, entries outside 0 .. d-1
+// clamped) and zeros: rows for the product where the given ones do not start on
+// 16 bytes, do not end on a whole step, or lie in another order.
+__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t n, int64_t d, int64_t lds, bool vec,
+                                                       const int32_t* __restrict__ perm, uint16_t* __restrict__ dst, int64_t kp) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = kp >> 3, t = i / per, k = (i - t * per) * 8;
+  if (t >= n) return;
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (k < d && perm) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < d) v[e >> 1] |= (uint32_t)src[t * lds + min(max((int64_t)perm[k + e], (int64_t)0), d - 1)] << (16 * (e & 1));
+  } else if (k < d) {
+    v = load8(src + t * lds + k, (int)min((int64_t)8, d - k), vec);
+  }
+  *reinterpret_cast<u32x4*>(dst + t * kp + k) = v;
+}
+
+}  // namespace
+
+void launch_gemm16(const Gemm16& g, int dt, int ot, hipStream_t s) {
+  Gemm16 a = g;
+  a.vec = rows_on_16(a.out, a.ldo, ot);
+  if (dt == kBF16) { if (ot == 0) choose_gemm<kBF16, 0, gemm16_terms(kBF16, 0)>(a, s); else choose_gemm<kBF16, kBF16, 1>(a, s); }
+  else { if (ot == 0) choose_gemm<kF16, 0, gemm16_terms(kF16, 0)>(a, s); else choose_gemm<kF16, kF16, 1>(a, s); }
+}
+
+bool gemm16_takes(const void* X, int64_t d, int64_t ldx) {
+  return reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0 && ldx < (int64_t(1) << 22) && d % LK == 0;
+}
+
+void launch_pad_rows(const void* X, int64_t n, int64_t d, int64_t ldx, const int32_t* perm, uint16_t* dst, hipStream_t s) {
+  const int64_t kp = gemm16_depth(d);
+  const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
+  hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)((n * (kp / 8) + 255) / 256)), dim3(256), 0, s, static_cast<const uint16_t*>(X), n,
+                     d, ldx, vec, perm, dst, kp);
+}
+
+}  // namespace gptq

@@ -1,9 +1,8 @@
 // Product of many tokens (prompts, batches) with a packed layer on tiles of the
 // matrix cores, with the low-rank adapters beside it.
 //
-// Codes become fp16 values q - z exactly: a code shifted under the exponent of
-// 2^b reads as 2^b + q, and 2^b + z is subtracted two at a time (12 operations
-// for 8 codes).  Activations become fp16 once per call (prepare_tokens): bf16
+// Codes become fp16 values q - z exactly, in about nine operations for eight
+// codes (centered).  Activations become fp16 once per call (prepare_tokens): bf16
 // ones are scaled by a power of two per token, which keeps every value within
 // 2^-29 of the token's largest exactly and the others to 2^-40 of it.  A
 // group's products are then whole-number weights times activations with fp32
@@ -25,6 +24,7 @@ typedef __attribute__((address_space(3))) unsigned char lds_u8;
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 
 constexpr int STEP = 128, ROWB = STEP * 2;   // columns of a step, bytes of an LDS row
+constexpr int64_t kCopyTokens = 1024;         // see dequant_first
 
 struct TileArgs {
   const uint16_t* X;   // prepared activations [n][ldx]
@@ -36,6 +36,7 @@ struct TileArgs {
   const float* S;      // null: no adapters
   void* Y;
   int64_t ldy;
+  bool vec;            // rows of Y start on 16 bytes
 };
 
 template <int BITS>
@@ -58,14 +59,41 @@ GPTQ_DEV Chunk<BITS> load_chunk(const uint32_t* words, int ch) {
   return c;
 }
 
-// Codes (t, t + 4) of a block as fp16 pairs q - z; off is the pair of 2^BITS + z.
+// What turns a block's codes into fp16 values q - z, a pair at a time: a field
+// at bit p of each half, under the exponent of 1024, reads as 1024 + 2^p q;
+// times 2^-p, minus 2^(10-p) + z, it is q - z, every step exact.  The fields
+// that a half's ten mantissa bits hold need no shift (two of four at 4 bits,
+// three at 3 bits).
 template <int BITS>
-GPTQ_DEV u32x4 centered(uint32_t blk, half2_t off) {
-  u32x4 v = code_pairs<BITS, kF16>(blk);
+struct Center {
+  static constexpr int FIT = BITS == 4 ? 2 : 3;   // fields read in place
+  half2_t off[FIT];                               // 2^(10 - BITS f) + z
+  GPTQ_DEV void set(int zero) {
+#pragma unroll
+    for (int f = 0; f < FIT; ++f) {
+      const _Float16 o = (_Float16)(float)((1 << (10 - BITS * f)) + zero);
+      off[f] = half2_t{o, o};
+    }
+  }
+};
+
+// Codes (t, t + 4) of a block as fp16 pairs q - z.  magic is 0x64006400 in a
+// vector register, so that mask and exponent are one instruction (its other
+// constant, the mask, takes the one scalar operand).
+template <int BITS>
+GPTQ_DEV u32x4 centered(uint32_t blk, const Center<BITS>& c, uint32_t magic) {
+  if constexpr (BITS == 3) blk = (blk & 0xFFFu) | ((blk & 0xFFF000u) << 4);   // codes 4 .. 7 to the high half
+  u32x4 v;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const uint32_t pair = v[t];   // (a bit cast of the vector's element itself would read element 0)
-    v[t] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, pair) - off);
+    constexpr int FIT = Center<BITS>::FIT;
+    const int f = t % FIT;
+    const uint32_t w = t < FIT ? blk : blk >> (BITS * FIT);
+    const uint32_t pair = (w & ((((1u << BITS) - 1) << (BITS * f)) * 0x10001u)) | magic;
+    const _Float16 k = (_Float16)(1.0f / (float)(1 << (BITS * f)));
+    const half2_t h = __builtin_bit_cast(half2_t, pair);
+    const half2_t d = f == 0 ? h - c.off[0] : h * half2_t{k, k} - c.off[f];
+    v[t] = __builtin_bit_cast(uint32_t, d);
   }
   return v;
 }
@@ -135,6 +163,8 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
 #pragma unroll
     for (int q = 0; q < NT; ++q) tot[i][q] = floatx16{};
 
+  uint32_t magic = 0x64006400u;
+  asm volatile("" : "+v"(magic));
   load_x(0);
   load_w(0);
   for (int s = 0; s < steps; ++s) {
@@ -146,12 +176,11 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
     float scale[NT][RU];
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-      half2_t o[RU];
+      Center<BITS> o[RU];
 #pragma unroll
       for (int u = 0; u < RU; ++u) {
         scale[q][u] = sc[q][u];
-        const _Float16 z = (_Float16)(float)((1 << BITS) + ze[q][u]);
-        o[u] = half2_t{z, z};
+        o[u].set(ze[q][u]);
       }
       uint32_t blk[8];
 #pragma unroll
@@ -169,7 +198,7 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
         for (int j = 0; j < 8; ++j) blk[j] = x[j];
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wf[q][j] = centered<BITS>(blk[j], o[CPS == 4 ? 0 : (j >> 1) / CPS]);
+      for (int j = 0; j < 8; ++j) wf[q][j] = centered<BITS>(blk[j], o[CPS == 4 ? 0 : (j >> 1) / CPS], magic);
     }
     // own loads have landed; with every wave here, the other buffer is free
     __builtin_amdgcn_s_waitcnt(0);
@@ -200,6 +229,9 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
     }
   }
 
+  static_assert(4 * 32 * (32 * NT + 4) * 4 <= 2 * 32 * MT * ROWB + 1024 * (MT == 1), "tile results fit the operands' LDS");
+  float* own = reinterpret_cast<float*>(xs) + wave * 32 * (32 * NT + 4);
+  __syncthreads();   // the last step's operands have been read
   int64_t row[NT];
 #pragma unroll
   for (int q = 0; q < NT; ++q) {
@@ -217,13 +249,7 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
       for (int q = 0; q < NT; ++q) tot[i][q][e] = __builtin_ldexpf(tot[i][q][e], ex);
     }
     if (a.S) expand_add<DT, YT == 0 ? 3 : 2, NT>(a.ad, a.ad.B, a.w.r, a.S, ti, a.n, row, tot[i]);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int64_t t = ti + TileShape<floatx16>::acc_row(lane, e);
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
-        if (t < a.n && row[q] >= 0) store_out<YT>(a.Y, t * a.ldy + row[q], tot[i][q][e]);
-    }
+    store_tile<YT, NT>(own, tot[i], a.Y, ti, a.n, row0, a.w.r, a.ldy, a.vec);
   }
 }
 
@@ -304,34 +330,100 @@ void choose_tiles(const TileArgs& a, hipStream_t s) {
 #endif
 }
 
-}  // namespace
-
-int64_t tiles_width(int64_t c) { return (c + STEP - 1) / STEP * STEP; }
-
-bool packed_tiles(int64_t n, int64_t c) { return n > 64 && c <= (int64_t(1) << 22); }
-
-void launch_prepare_tokens(const void* X, int xt, int64_t n, int64_t ldx, int64_t c, const int32_t* perm, void* dst, int32_t* ex,
-                           hipStream_t s) {
-  const auto* x = static_cast<const uint16_t*>(X);
-  auto* d = static_cast<uint16_t*>(dst);
-  const int ldd = (int)tiles_width(c);
-  const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
-  if (xt == kBF16) hipLaunchKernelGGL((prepare_tokens_kernel<kBF16>), dim3((unsigned)n), dim3(256), 0, s, x, ldx, vec, (int)c, perm, d, ldd, ex);
-  else hipLaunchKernelGGL((prepare_tokens_kernel<kF16>), dim3((unsigned)n), dim3(256), 0, s, x, ldx, vec, (int)c, perm, d, ldd, ex);
+// The layer as 16-bit rows in packed column order, zero from column c to kp.
+// One wave per row, a block of eight columns per lane.
+template <int BITS, int DT>
+__global__ __launch_bounds__(256) void dequant_rows_kernel(PackedLayer w, uint16_t* __restrict__ W, int kp) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= w.r) return;
+  const float* srow = w.scales + row * w.ldg;
+  const int32_t* zrow = w.zeros + row * w.ldg;
+  const uint32_t* words = w.words + row * w.ldw;
+  for (int b = threadIdx.x & 63; 8 * b < kp; b += 64) {
+    u32x4 o = {0u, 0u, 0u, 0u};
+    if (8 * b < w.c) {
+      const int g = (b >> 2) / w.cpg;
+      const float z = (float)zrow[g], sc = srow[g];
+      const uint32_t blk = BITS == 4 ? words[b] : straddling_block(words, b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w0 = ((float)((blk >> (2 * BITS * e)) & ((1u << BITS) - 1)) - z) * sc;
+        const float w1 = ((float)((blk >> (2 * BITS * e + BITS)) & ((1u << BITS) - 1)) - z) * sc;
+        o[e] = pack2<DT>(w0, w1);
+      }
+    }
+    *reinterpret_cast<u32x4*>(W + row * kp + 8 * b) = o;
+  }
 }
 
-void launch_packed_tiles(const void* X, const int32_t* ex, int xt, int64_t n, const PackedLayer& w, const Adapters& ad, const float* S,
-                         void* Y, int yt, int64_t ldy, hipStream_t s) {
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
+int64_t tiles_width(int64_t c) { return (c + STEP - 1) / STEP * STEP; }
+
+// 16-bit results of many tokens: the layer is dequantized once into 16-bit rows
+// (each weight rounded to the activations' type, as gptq_linear_forward does)
+// and multiplied by gemm16.  Its product runs at 1.25 PFLOP/s where the tiles
+// here, which also multiply scales and dequantize for every 128 tokens, reach
+// 0.83, and the copy costs 30 us for 45 million weights: even at about 800
+// tokens, and 0.62 against 0.89 ms for 8192 tokens of 11008 x 4096.
+bool dequant_first(int64_t n, int yt) { return yt != 0 && n >= kCopyTokens; }
+
+}  // namespace
+
+bool packed_tiles(int64_t n, int64_t c) { return n > 64 && c < (int64_t(1) << 22) - STEP; }
+
+int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt) {
+  if (dequant_first(n, yt)) return align256(n * gemm16_depth(c) * 2) + align256(r * gemm16_depth(c) * 2);
+  return align256(n * tiles_width(c) * 2) + align256(n * 4);
+}
+
+void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad, const float* S,
+                         void* Y, int yt, int64_t ldy, void* ws, hipStream_t s) {
+  auto* xp = static_cast<uint16_t*>(ws);
+  const dim3 block(256);
+  if (dequant_first(n, yt)) {
+    Gemm16 g{};
+    g.kp = gemm16_depth(w.c);
+    g.X = static_cast<const uint16_t*>(X);
+    g.ldx = ldx;
+    if (w.perm || !gemm16_takes(X, w.c, ldx)) {
+      launch_pad_rows(X, n, w.c, ldx, w.perm, xp, s);
+      g.X = xp;
+      g.ldx = g.kp;
+    }
+    uint16_t* W = xp + align256(n * g.kp * 2) / 2;
+    const dim3 dgrid((unsigned)((w.r + 3) / 4));
+#define GPTQ_DEQ(B_, D_) hipLaunchKernelGGL((dequant_rows_kernel<B_, D_>), dgrid, block, 0, s, w, W, (int)g.kp)
+    if (w.bits == 4) { if (xt == kBF16) GPTQ_DEQ(4, kBF16); else GPTQ_DEQ(4, kF16); }
+    else { if (xt == kBF16) GPTQ_DEQ(3, kBF16); else GPTQ_DEQ(3, kF16); }
+#undef GPTQ_DEQ
+    g.W = W;
+    g.n = n;
+    g.cols = w.r;
+    g.ad = ad;
+    g.B = ad.B;
+    g.S = S;
+    g.out = Y;
+    g.ldo = ldy;
+    launch_gemm16(g, xt, yt, s);
+    return;
+  }
+  const int ldp = (int)tiles_width(w.c);
+  auto* ex = reinterpret_cast<int32_t*>(xp + align256(n * ldp * 2) / 2);
+  const auto* x = static_cast<const uint16_t*>(X);
+  const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
+  if (xt == kBF16) hipLaunchKernelGGL((prepare_tokens_kernel<kBF16>), dim3((unsigned)n), block, 0, s, x, ldx, vec, w.c, w.perm, xp, ldp, ex);
+  else hipLaunchKernelGGL((prepare_tokens_kernel<kF16>), dim3((unsigned)n), block, 0, s, x, ldx, vec, w.c, w.perm, xp, ldp, ex);
   TileArgs a{};
-  a.X = static_cast<const uint16_t*>(X);
+  a.X = xp;
   a.ex = ex;
   a.n = n;
-  a.ldx = (int)tiles_width(w.c);
+  a.ldx = ldp;
   a.w = w;
   a.ad = ad;
   a.S = S;
   a.Y = Y;
   a.ldy = ldy;
+  a.vec = rows_on_16(Y, ldy, yt);
 #define GPTQ_TILES(B_)                                                                                     \
   do {                                                                                                     \
     if (xt == kBF16) { if (yt == 0) choose_tiles<B_, 0, kBF16>(a, s); else choose_tiles<B_, kBF16, kBF16>(a, s); } \

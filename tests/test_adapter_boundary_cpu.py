@@ -41,13 +41,14 @@ def test_header_symbols_are_exported(lib):
 def test_workspace_queries(lib):
     out = C.c_size_t(7)
     f = lib.gptq_packed_linear_workspace_size
-    assert f(16, 4096, 0, 0, C.byref(out)) == 0 and out.value == 0
-    assert f(16, 4096, 16, 0, C.byref(out)) == 0 and out.value >= 16 * 16 * 4
-    assert f(16, 4096, 0, 1, C.byref(out)) == 0 and out.value >= 16 * 4096 * 2
-    assert f(-1, 4096, 0, 0, C.byref(out)) == 1 and f(16, 4096, 0, 2, C.byref(out)) == 1
-    assert f(16, 4096, 0, 0, None) == 1
-    assert f(16, 48, 0, 0, C.byref(out)) == 3 and f(16, 0, 0, 0, C.byref(out)) == 3
-    assert f(16, 4096, 12, 0, C.byref(out)) == 5 and f(16, 4096, 136, 0, C.byref(out)) == 5
+    assert f(16, 100, 4096, 1, 0, 0, C.byref(out)) == 0 and out.value == 0
+    assert f(16, 100, 4096, 1, 16, 0, C.byref(out)) == 0 and out.value >= 16 * 16 * 4
+    assert f(16, 100, 4096, 1, 0, 1, C.byref(out)) == 0 and out.value >= 16 * 4096 * 2
+    assert f(1 << 30, 1 << 30, 1 << 30, 0, 128, 1, C.byref(out)) in (0, 5)
+    assert f(-1, 100, 4096, 1, 0, 0, C.byref(out)) == 1 and f(16, 100, 4096, 1, 0, 2, C.byref(out)) == 1
+    assert f(16, 100, 4096, 1, 0, 0, None) == 1 and f(16, 100, 4096, 7, 0, 0, C.byref(out)) == 1
+    assert f(16, 100, 48, 1, 0, 0, C.byref(out)) == 3 and f(16, 100, 0, 1, 0, 0, C.byref(out)) == 3
+    assert f(16, 100, 4096, 1, 12, 0, C.byref(out)) == 5 and f(16, 100, 4096, 1, 136, 0, C.byref(out)) == 5
     f = lib.gptq_packed_linear_backward_workspace_size
     assert f(16, 100, 4096, 1, 1, 0, 0, C.byref(out)) == 0 and out.value >= 100 * 4096 * 2
     assert f(16, 100, 4096, 1, 0, 0, 0, C.byref(out)) == 0 and out.value >= 3 * 100 * 4096 * 2

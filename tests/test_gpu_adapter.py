@@ -8,6 +8,8 @@ sum of magnitudes:
   packed forward   a group's sums see at most 128 columns in a chain, then one
                    addition per 128 columns and 16 across waves:
                    (128 + c/128 + 32) 2 eps sum_j s (2 2^b + q + z) |x_j|
+                   16-bit results of 1024 tokens or more: each weight rounded
+                   once and a chain over the c columns, (c 2 eps + u) sum |W x|
   input gradient   a chain over the r rows; each weight rounded once (u) or
                    held in two terms (2^-16, and 2^-24 for fp16's smallest):
                    (r 2 eps + u) sum |dY W|
@@ -109,10 +111,12 @@ def check(name, got, want, bound):
     assert torch.isfinite(got).all() and worst <= 1.0, (name, worst)
 
 
-def forward64(L, X, ad):
+def forward64(L, X, ad, out_dtype=torch.float32):
     X64 = X.double()
     want = X64 @ L.W.T
     bound = (128 + L.c / 128 + 32) * 2 * EPS * (X64.abs() @ L.mag.T)
+    if out_dtype != torch.float32 and X.shape[0] >= 1024:
+        bound += (L.c * 2 * EPS + U[out_dtype]) * (X64.abs() @ L.W.abs().T)
     if ad:
         v, b = low64(ad, X, ad["A"], ad["B"].transpose(1, 2))
         want, bound = want + v, bound + b
@@ -133,6 +137,10 @@ FORWARD = [
     (300, 96, 768, 4, 32, True, "fp16", "fp32", (3, 64, "runs")),
     (515, 200, 256, 4, 128, False, "bf16", "fp32", (1, 16, "all")),
     (2050, 65, 128, 3, 128, False, "fp16", "fp16", (2, 32, "mixed")),
+    (1024, 300, 416, 4, 96, True, "bf16", "bf16", (3, 16, "runs")),
+    (1300, 257, 96, 4, -1, False, "fp16", "fp16", None),
+    (1500, 129, 544, 3, 32, True, "bf16", "bf16", (6, 8, "mixed")),
+    (1111, 140, 320, 4, 64, False, "bf16", "fp32", (2, 24, "mixed")),
 ]
 
 
@@ -147,7 +155,7 @@ def test_packed_linear(n, r, c, bits, gs, act, dt, out, low):
     Y = gq().packed_linear(X, *L.args(), perm=L.perm, out_dtype=DT[out], **ad)
     torch.cuda.synchronize()
     assert Y.shape == (n, r) and Y.dtype == DT[out]
-    check("Y", Y, *forward64(L, X, ad))
+    check("Y", Y, *forward64(L, X, ad, DT[out]))
 
 
 def backward64(L, dY, ad, out_dtype):
