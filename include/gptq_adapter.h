@@ -116,7 +116,7 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
  *       stride); any other overlap with Y or X is GPTQ_EINVAL.
  * ws  : gptq_adapter_add_workspace_size() bytes.
  * ------------------------------------------------------------------------ */
-gptq_status gptq_adapter_add_workspace_size(int64_t n_tok, int64_t rank, size_t* bytes);
+gptq_status gptq_adapter_add_workspace_size(int64_t n_tok, int64_t c, int64_t rank, size_t* bytes);
 gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n_tok, int64_t c, int64_t ldx, const void* A,
                              const void* B, int64_t n_adapters, int64_t rank, int64_t r, const int32_t* index,
                              const float* alpha, const void* Y, gptq_dtype yt, int64_t ldy, void* out, int64_t ldo,

@@ -43,7 +43,7 @@ SIGNATURES = {
     "gptq_packed_linear_backward_workspace_size": (C.c_int, [_I64, _I64, _I64, C.c_int, C.c_int, _I64, _I64, _SZP]),
     "gptq_packed_linear_backward": (C.c_int, [_P, C.c_int, _I64, _I64, _P, _I64, _I64, C.c_int, _I64, _P, _P, _I64,
                                               _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, C.c_int, _I64, _P, _SZ, _P]),
-    "gptq_adapter_add_workspace_size": (C.c_int, [_I64, _I64, _SZP]),
+    "gptq_adapter_add_workspace_size": (C.c_int, [_I64, _I64, _I64, _SZP]),
     "gptq_adapter_add": (C.c_int, [_P, C.c_int, _I64, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P, C.c_int, _I64,
                                    _P, _I64, _P, _SZ, _P]),
     "gptq_adapter_backward_workspace_size": (C.c_int, [_I64, _I64, _I64, _I64, _I64, _SZP]),

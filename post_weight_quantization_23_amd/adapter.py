@@ -189,7 +189,7 @@ def adapter_add(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tens
     m, rank = _adapters(A, B, index, alpha, X.dtype, n, r, c)
     _check_out(out, "out", n, r, Y.dtype)
     dev = _device(X, Y, A, B, index, alpha, out)
-    buf, nb = _ws(ws, _lib.query("gptq_adapter_add_workspace_size", n, rank), dev)
+    buf, nb = _ws(ws, _lib.query("gptq_adapter_add_workspace_size", n, c, rank), dev)
     out = torch.empty((n, r), dtype=Y.dtype, device=dev) if out is None else out
     _lib.call("gptq_adapter_add", _ptr(X), _DT[X.dtype], n, c, _ld(X), _ptr(A), _ptr(B), m, rank, r, _ptr(index),
               _ptr(alpha), _ptr(Y), _DT[Y.dtype], _ld(Y), _ptr(out), _ld(out), _ptr(buf), nb, _stream())

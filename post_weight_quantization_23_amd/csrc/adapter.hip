@@ -12,8 +12,9 @@ namespace gptq {
 namespace {
 
 // ---------------------------------------------------------------- down
-// One wave per (token, rank row): 64 lanes x 8 elements a step, fp32 sums
-// folded over the wave in a fixed order.
+// A few tokens: one wave per (token, rank row), 64 lanes x 8 elements a load, four
+// loads of each operand in flight (a chain of single ones waits for memory once
+// per 512 elements).  fp32 sums, folded over the wave in a fixed order.
 template <int DT>
 __global__ __launch_bounds__(256) void down_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t d, int64_t ldx,
                                                    Adapters ad, const uint16_t* __restrict__ A, int64_t lda, bool vec,
@@ -24,24 +25,125 @@ __global__ __launch_bounds__(256) void down_kernel(const uint16_t* __restrict__ 
   const int p = (int)(item - t * ad.rank);
   if (t >= n) return;
   const int a = adapter_of(ad, t, n);
-  float sum = 0.f;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
   if (a >= 0) {
     const uint16_t* x = X + t * ldx;
     const uint16_t* w = A + ((int64_t)a * ad.rank + p) * lda;
-    for (int64_t k = 8 * lane; k < d; k += 512) {
-      const u32x4 xv = load8(x + k, (int)min((int64_t)8, d - k), vec);
-      const u32x4 wv = *reinterpret_cast<const u32x4*>(w + k);
+    for (int64_t k0 = 8 * lane; k0 < d; k0 += 2048) {
+      u32x4 xv[4], wv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t k = k0 + 512 * u;
+        xv[u] = wv[u] = u32x4{0u, 0u, 0u, 0u};
+        if (k < d) {
+          xv[u] = load8(x + k, (int)min((int64_t)8, d - k), vec);
+          wv[u] = *reinterpret_cast<const u32x4*>(w + k);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[u] = __builtin_fmaf(f16_to_f32<DT>(xv[u][i] & 0xFFFFu), f16_to_f32<DT>(wv[u][i] & 0xFFFFu), sum[u]);
+          sum[u] = __builtin_fmaf(f16_to_f32<DT>(xv[u][i] >> 16), f16_to_f32<DT>(wv[u][i] >> 16), sum[u]);
+        }
+    }
+  }
+  float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) all += __shfl_xor(all, m);
+  if (lane == 0) S[item] = a >= 0 && ad.alpha ? all * ad.alpha[a] : all;
+}
+
+// Many tokens: a workgroup takes 64 tokens and one of `splits` parts of the
+// contraction, its four waves every fourth step of 32 of that part, all 16 RT
+// rank rows (operands come from memory in the layout of the product, which
+// reads X once).  The adapters that occur among the tokens are taken in turn;
+// each writes its own tokens' rows.  Waves are joined through LDS in wave
+// order, parts by scale_join_kernel.
+template <int DT, int RT>
+__global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t d, int64_t ldx, Adapters ad,
+                                                         const uint16_t* __restrict__ A, int64_t lda, bool vec, float* __restrict__ S,
+                                                         int splits) {
+  __shared__ float red[64][16 * RT + 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, kq = lane >> 4;
+  const int64_t tile = blockIdx.x / splits;
+  const int split = (int)(blockIdx.x - tile * splits);
+  const int64_t t0 = tile * 64;
+  const int64_t steps = (d + 31) / 32, per = (steps + splits - 1) / splits;
+  const int64_t s1 = min(steps, (split + 1) * per);
+  float* out = S + (int64_t)split * n * ad.rank;
+  const int mine = adapter_of(ad, t0 + lane, n);
+  uint64_t rest = __ballot(mine >= 0);
+  const uint64_t none = ~rest;
+  for (int i = threadIdx.x; i < 64 * ad.rank; i += 256) {
+    const int tok = i / ad.rank;
+    if (((none >> tok) & 1) && t0 + tok < n) out[t0 * ad.rank + i] = 0.f;
+  }
+  while (rest) {
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rest));
+    const uint64_t members = __ballot(mine == a);
+    rest &= ~members;
+    const uint16_t* w = A + (int64_t)a * ad.rank * lda;
+    floatx4 acc[4][RT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int p = 0; p < RT; ++p) acc[i][p] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int64_t s = split * per + wave; s < s1; s += 4) {
+      const int64_t k = 32 * s + 8 * kq;
+      u32x4 x[4], b[RT];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        sum = __builtin_fmaf(f16_to_f32<DT>(xv[i] & 0xFFFFu), f16_to_f32<DT>(wv[i] & 0xFFFFu), sum);
-        sum = __builtin_fmaf(f16_to_f32<DT>(xv[i] >> 16), f16_to_f32<DT>(wv[i] >> 16), sum);
+        const int64_t t = t0 + 16 * i + m;
+        x[i] = u32x4{0u, 0u, 0u, 0u};
+        if (t < n && k < d) x[i] = load8(X + t * ldx + k, (int)min((int64_t)8, d - k), vec);
       }
-    }
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-    if (ad.alpha) sum *= ad.alpha[a];
+      for (int p = 0; p < RT; ++p) {
+        b[p] = u32x4{0u, 0u, 0u, 0u};
+        if (16 * p + m < ad.rank && k < d) b[p] = *reinterpret_cast<const u32x4*>(w + (int64_t)(16 * p + m) * lda + k);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < RT; ++p) acc[i][p] = mfma16<DT>(x[i], b[p], acc[i][p]);
+    }
+    for (int v = 0; v < 4; ++v) {
+      if (wave == v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int p = 0; p < RT; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& r = red[16 * i + 4 * kq + e][16 * p + m];
+              r = v == 0 ? acc[i][p][e] : r + acc[i][p][e];
+            }
+      }
+      __syncthreads();
+    }
+    const float f = splits == 1 && ad.alpha ? ad.alpha[a] : 1.f;
+    for (int i = threadIdx.x; i < 64 * ad.rank; i += 256) {
+      const int tok = i / ad.rank, p = i - tok * ad.rank;
+      if ((members >> tok) & 1) out[t0 * ad.rank + i] = f * red[tok][p];
+    }
+    __syncthreads();
   }
-  if (lane == 0) S[item] = sum;
+}
+
+// S[t][p] = alpha_a (sum of the parts), four values per thread.
+__global__ __launch_bounds__(256) void scale_join_kernel(const float* __restrict__ part, int64_t n, Adapters ad, int splits,
+                                                         float* __restrict__ S) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, all = n * ad.rank;
+  if (i >= all) return;
+  floatx4 v = *reinterpret_cast<const floatx4*>(part + i);
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const floatx4*>(part + s * all + i);
+  const int a = adapter_of(ad, i / ad.rank, n);
+  if (a >= 0 && ad.alpha) v *= ad.alpha[a];
+  *reinterpret_cast<floatx4*>(S + i) = v;
 }
 
 // ---------------------------------------------------------------- up
@@ -246,17 +348,54 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   *reinterpret_cast<floatx4*>(out + i) = v;
 }
 
-bool rows_on_16(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+// Parts of the contraction of down_tiles_kernel: enough workgroups for the
+// chip, each wave left with four steps at least.
+int down_splits(int64_t n, int64_t d) {
+  const int64_t tiles = (n + 63) / 64, steps = (d + 31) / 32;
+  int64_t splits = 512 / tiles;
+  splits = splits < steps / 16 ? splits : steps / 16;
+  return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
+}
+
+// Tokens from which down_tiles_kernel is faster than a wave per value.
+constexpr int64_t kDownTiles = 64;
 
 }  // namespace
 
+int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank) {
+  const int64_t one = (n * rank + 63) / 64 * 64;
+  const int splits = n < kDownTiles ? 1 : down_splits(n, d);
+  return splits == 1 ? one : one + splits * n * rank;
+}
+
 void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ldx, const Adapters& ad, const uint16_t* A,
                          int64_t lda, float* S, hipStream_t s) {
-  const dim3 grid((unsigned)((n * ad.rank + 3) / 4)), block(256);
-  const bool vec = rows_on_16(X, ldx);
+  const dim3 block(256);
+  const bool vec = rows_on_16(X, ldx, xt);
   const auto* x = static_cast<const uint16_t*>(X);
-  if (xt == kBF16) hipLaunchKernelGGL((down_kernel<kBF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
-  else hipLaunchKernelGGL((down_kernel<kF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
+  if (n < kDownTiles) {
+    const dim3 grid((unsigned)((n * ad.rank + 3) / 4));
+    if (xt == kBF16) hipLaunchKernelGGL((down_kernel<kBF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
+    else hipLaunchKernelGGL((down_kernel<kF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
+    return;
+  }
+  const int splits = down_splits(n, d);
+  float* out = splits == 1 ? S : S + (n * ad.rank + 63) / 64 * 64;
+  const dim3 grid((unsigned)((n + 63) / 64 * splits));
+#define GPTQ_DOWN(D_, R_) hipLaunchKernelGGL((down_tiles_kernel<D_, R_>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits)
+#define GPTQ_DOWN_R(D_)                     \
+  do {                                      \
+    if (ad.rank <= 16) GPTQ_DOWN(D_, 1);    \
+    else if (ad.rank <= 32) GPTQ_DOWN(D_, 2); \
+    else if (ad.rank <= 64) GPTQ_DOWN(D_, 4); \
+    else GPTQ_DOWN(D_, 8);                  \
+  } while (0)
+  if (xt == kBF16) GPTQ_DOWN_R(kBF16);
+  else GPTQ_DOWN_R(kF16);
+#undef GPTQ_DOWN_R
+#undef GPTQ_DOWN
+  if (splits > 1)
+    hipLaunchKernelGGL(scale_join_kernel, dim3((unsigned)((n * ad.rank / 4 + 255) / 256)), block, 0, s, out, n, ad, splits, S);
 }
 
 void launch_adapter_up(const float* S, int64_t n, const Adapters& ad, int xt, const uint16_t* B, int64_t rows,
@@ -290,7 +429,7 @@ int adapter_grad_splits(int64_t n, int m, int64_t cols) {
 void launch_adapter_grad(const float* V, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz, const Adapters& ad,
                          const int32_t* order, const int32_t* start, int up, float* G, float* part, int splits,
                          hipStream_t s) {
-  const bool vec = rows_on_16(Z, ldz);
+  const bool vec = rows_on_16(Z, ldz, zt);
   const int rt = ad.rank <= 16 ? 1 : (ad.rank <= 32 ? 2 : 4);
   const int rb = (ad.rank + 16 * rt - 1) / (16 * rt);
   const int64_t cb = (cols + 127) / 128;

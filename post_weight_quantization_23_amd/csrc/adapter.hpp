@@ -341,7 +341,9 @@ GPTQ_DEV u32x4 pair_order(u32x4 v) {
 // xt / dt: 1 bf16, 2 fp16; yt: 0 fp32, 1 bf16, 2 fp16.
 
 // S[t][p] = alpha sum_k X[t][k] A_a[p][k], A with row stride lda (a multiple
-// of 8, zero past d) -- adapter.hip.
+// of 8, zero past d) -- adapter.hip.  S: n x rank results (on 16 bytes) in
+// adapter_down_floats() of workspace.
+int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank);
 void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ldx, const Adapters& ad, const uint16_t* A,
                          int64_t lda, float* S, hipStream_t s);
 // out = base + S B^T (base null: 0), out and base [n][rows] of type yt.

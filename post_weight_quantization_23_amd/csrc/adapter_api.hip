@@ -127,7 +127,8 @@ int64_t forward_bytes(int64_t n, int64_t r, int64_t c, bool perm, int yt) {
   return perm ? align256(n * c * 2) : 0;
 }
 
-int64_t low_bytes(int64_t n, int64_t rank) { return align256(n * rank * 4); }
+// The rank values of n tokens of d features, with what computing them takes.
+int64_t low_bytes(int64_t n, int64_t d, int64_t rank) { return rank > 0 ? align256(gptq::adapter_down_floats(n, d, rank) * 4) : 0; }
 
 // Every launch's grid, at the launch helpers' workgroup shapes.
 bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
@@ -160,7 +161,7 @@ GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
   const int64_t pa = z.sa > 1 ? z.sa * m * rank * c * 4 : 0, pb = z.sb > 1 ? z.sb * m * rank * r * 4 : 0;
   z.part = align256(pa > pb ? pa : pb);
   z.lists = align256(n * 4) + align256((m + 1) * 4);
-  z.total = align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + 2 * low_bytes(n, rank) + z.lists + z.part;
+  z.total = align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + low_bytes(n, c, rank) + low_bytes(n, r, rank) + z.lists + z.part;
   return z;
 }
 
@@ -178,7 +179,7 @@ gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t r, int64_t c, g
   if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
   if (rank != 0)
     if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, rank));
+  *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, c, rank));
   return ok();
 }
 
@@ -210,7 +211,7 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
     if (gptq_status st = check_clash(fn, clash(Y, ey, A, m * rank, c, c, 2))) return st;
     if (gptq_status st = check_clash(fn, clash(Y, ey, B, m * r, rank, rank, 2))) return st;
   }
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, forward_bytes(n, r, c, perm != nullptr, (int)yt) + low_bytes(n, rank))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, forward_bytes(n, r, c, perm != nullptr, (int)yt) + low_bytes(n, c, rank))) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
@@ -219,7 +220,7 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
   const int yi = yt == GPTQ_F32 ? 0 : xi;
   float* S = nullptr;
   if (low) {
-    S = carve.take<float>(n * rank * 4);
+    S = carve.take<float>(low_bytes(n, c, rank));
     gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
   }
   if (gptq::packed_tiles(n, c)) {
@@ -249,7 +250,7 @@ gptq_status gptq_packed_linear_backward_workspace_size(int64_t n, int64_t r, int
   if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
   *bytes = (size_t)(backward_bytes(n, r, c, gptq::gemm16_terms((int)xt, (int)ot)) + align256(m * c * rank * 2) +
-                    align256(m * rank * pad8(r) * 2) + low_bytes(n, rank));
+                    align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank));
   return ok();
 }
 
@@ -284,7 +285,7 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
     if (gptq_status st = check_clash(fn, clash(dX, ex, B, m * r, rank, rank, 2))) return st;
   }
   const int terms = gptq::gemm16_terms((int)xt, (int)ot);
-  const int64_t need = backward_bytes(n, r, c, terms) + align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, rank);
+  const int64_t need = backward_bytes(n, r, c, terms) + align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank);
   if (gptq_status st = need_ws(fn, ws, ws_bytes, need)) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -298,7 +299,7 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
   if (low) {
     At = carve.take<uint16_t>(m * c * rank * 2);
     uint16_t* Bt = carve.take<uint16_t>(m * rank * pad8(r) * 2);
-    T = carve.take<float>(n * rank * 4);
+    T = carve.take<float>(low_bytes(n, r, rank));
     gptq::launch_transpose16(ad.A, (int)m, rank, c, At, rank, s);
     gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
     gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);
@@ -308,12 +309,12 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
 }
 
 // ------------------------------------------------------------------ adapters beside any projection
-gptq_status gptq_adapter_add_workspace_size(int64_t n, int64_t rank, size_t* bytes) {
+gptq_status gptq_adapter_add_workspace_size(int64_t n, int64_t c, int64_t rank, size_t* bytes) {
   const char* fn = "gptq_adapter_add_workspace_size";
   if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
-  if (gptq_status st = check_sizes(fn, n, 0, 8, 8)) return st;
+  if (gptq_status st = check_sizes(fn, n, 0, c, 8)) return st;
   if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  *bytes = (size_t)low_bytes(n, rank);
+  *bytes = (size_t)low_bytes(n, c, rank);
   return ok();
 }
 
@@ -338,7 +339,7 @@ gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n, int64_t c,
   if (gptq_status st = check_clash(fn, clash(out, eo, B, m * r, rank, rank, 2))) return st;
   if (!(out == Y && ldo == ldy))
     if (gptq_status st = check_clash(fn, clash(out, eo, Y, n, ldy, r, el))) return st;
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, low_bytes(n, rank))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, low_bytes(n, c, rank))) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
@@ -400,8 +401,8 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
   uint16_t* Bt = carve.take<uint16_t>(m * rank * pad8(r) * 2);
   uint16_t* At = carve.take<uint16_t>(m * c * rank * 2);
-  float* S = carve.take<float>(n * rank * 4);
-  float* T = carve.take<float>(n * rank * 4);
+  float* S = carve.take<float>(low_bytes(n, c, rank));
+  float* T = carve.take<float>(low_bytes(n, r, rank));
   int32_t* order = carve.take<int32_t>(n * 4);
   int32_t* start = carve.take<int32_t>((m + 1) * 4);
   float* part = carve.take<float>(z.part);

@@ -57,7 +57,8 @@ def test_workspace_queries(lib):
     assert f(16, 100, 4096, 0, 0, 0, 0, C.byref(out)) == 2 and f(16, 100, 4096, 1, 2, 0, 0, C.byref(out)) == 2
     assert f(16, 1 << 22, 4096, 1, 1, 0, 0, C.byref(out)) == 5
     f = lib.gptq_adapter_add_workspace_size
-    assert f(16, 8, C.byref(out)) == 0 and out.value >= 16 * 8 * 4 and f(16, 0, C.byref(out)) == 5
+    assert f(16, 64, 8, C.byref(out)) == 0 and out.value >= 16 * 8 * 4 and f(16, 64, 0, C.byref(out)) == 5
+    assert f(16, 60, 8, C.byref(out)) == 3
     f = lib.gptq_adapter_backward_workspace_size
     assert f(16, 100, 64, 2, 8, C.byref(out)) == 0 and f(16, 100, 60, 2, 8, C.byref(out)) == 3
     # sizes whose byte counts would pass 63 bits are refused, not wrapped
