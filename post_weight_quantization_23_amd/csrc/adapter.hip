@@ -61,7 +61,10 @@ __global__ __launch_bounds__(256) void down_kernel(const uint16_t* __restrict__ 
 // reads X once).  The adapters that occur among the tokens are taken in turn;
 // each writes its own tokens' rows.  Waves are joined through LDS in wave
 // order, parts by scale_join_kernel.
-template <int DT, int RT>
+// FAST: rows of X start on 16 bytes and hold whole steps; then every load is
+// unconditional (tokens and rank rows past the end repeat the last one, whose
+// results are dropped), so that several steps' loads are in flight.
+template <int DT, int RT, bool FAST>
 __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t d, int64_t ldx, Adapters ad,
                                                          const uint16_t* __restrict__ A, int64_t lda, bool vec, float* __restrict__ S,
                                                          int splits) {
@@ -91,7 +94,7 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int p = 0; p < RT; ++p) acc[i][p] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+#pragma unroll FAST ? (RT > 4 ? 2 : 4) : 1
     for (int64_t s = split * per + wave; s < s1; s += 4) {
       const int64_t k = 32 * s + 8 * kq;
       u32x4 x[4], b[RT];
@@ -99,12 +102,14 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
       for (int i = 0; i < 4; ++i) {
         const int64_t t = t0 + 16 * i + m;
         x[i] = u32x4{0u, 0u, 0u, 0u};
-        if (t < n && k < d) x[i] = load8(X + t * ldx + k, (int)min((int64_t)8, d - k), vec);
+        if constexpr (FAST) x[i] = *reinterpret_cast<const u32x4*>(X + min(t, n - 1) * ldx + k);
+        else if (t < n && k < d) x[i] = load8(X + t * ldx + k, (int)min((int64_t)8, d - k), vec);
       }
 #pragma unroll
       for (int p = 0; p < RT; ++p) {
         b[p] = u32x4{0u, 0u, 0u, 0u};
-        if (16 * p + m < ad.rank && k < d) b[p] = *reinterpret_cast<const u32x4*>(w + (int64_t)(16 * p + m) * lda + k);
+        if constexpr (FAST) b[p] = *reinterpret_cast<const u32x4*>(w + (int64_t)min(16 * p + m, ad.rank - 1) * lda + k);
+        else if (16 * p + m < ad.rank && k < d) b[p] = *reinterpret_cast<const u32x4*>(w + (int64_t)(16 * p + m) * lda + k);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -147,37 +152,83 @@ __global__ __launch_bounds__(256) void scale_join_kernel(const float* __restrict
 }
 
 // ---------------------------------------------------------------- up
-// out = base + S B^T: a wave takes 16 tokens x 64 outputs.
-template <int DT, int YT>
-__global__ __launch_bounds__(256) void up_kernel(const float* __restrict__ S, int64_t n, Adapters ad,
-                                                 const uint16_t* __restrict__ B, int64_t rows, const void* base, int64_t ldb,
-                                                 void* out, int64_t ldo, int64_t col_tiles) {
-  const int lane = threadIdx.x & 63;
-  const int64_t tile = blockIdx.x / col_tiles, ct = blockIdx.x - tile * col_tiles;
-  const int64_t t0 = tile * 16, j0 = ct * 256 + 64 * (threadIdx.x >> 6);
-  int64_t row[4];
-  floatx4 acc[4];
+// What the low-rank product is added to, k <= 8 outputs from column j of token t.
+template <int YT>
+GPTQ_DEV void add_base(const UpArgs& u, float (&v)[8], int64_t t, int64_t j, int k) {
+  if (u.part) {
+    float sum[8] = {};
+    const int64_t at = t * u.rows + j;
+    for (int s = 0; s < u.splits; ++s) {
+      const float* p = u.part + s * u.n * u.rows + at;
+      if (k == 8 && u.vec_base) {
+        float w[8];
+        load8f(p, w);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t j = j0 + 16 * q + (lane & 15);
-    row[q] = j < rows ? j : -1;
-    acc[q] = floatx4{0.f, 0.f, 0.f, 0.f};
-  }
-  expand_add<DT, YT == 0 ? 3 : 2, 4>(ad, B, rows, S, t0, n, row, acc);
+        for (int e = 0; e < 8; ++e) sum[e] += w[e];
+      } else {
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + 4 * (lane >> 4) + i;
-      if (t >= n || row[q] < 0) continue;
-      float v = acc[q][i];
-      if (base) {
-        const int64_t at = t * ldb + row[q];
-        if constexpr (YT == 0) v += static_cast<const float*>(base)[at];
-        else v += f16_to_f32<YT>(static_cast<const uint16_t*>(base)[at]);
+        for (int e = 0; e < 8; ++e)
+          if (e < k) sum[e] += p[e];
       }
-      store_out<YT>(out, t * ldo + row[q], v);
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += __builtin_ldexpf(sum[e], u.ex[t]);
+  } else if (u.base) {
+    if constexpr (YT == 0) {
+      const float* p = static_cast<const float*>(u.base) + t * u.ldb + j;
+      if (k == 8 && u.vec_base) {
+        float w[8];
+        load8f(p, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += w[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < k) v[e] += p[e];
+      }
+    } else {
+      const u32x4 w = load8(static_cast<const uint16_t*>(u.base) + t * u.ldb + j, k, u.vec_base);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] += f16_to_f32<YT>(w[e] & 0xFFFFu);
+        v[2 * e + 1] += f16_to_f32<YT>(w[e] >> 16);
+      }
+    }
+  }
+}
+
+// Many tokens: a wave takes 32 tokens x 64 outputs on the matrix cores.
+template <int DT, int YT>
+__global__ __launch_bounds__(256) void up_tiles_kernel(UpArgs u) {
+  __shared__ float turn[4][32 * 68];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t tile = blockIdx.x / u.col_tiles, ct = blockIdx.x - tile * u.col_tiles;
+  const int64_t t0 = tile * 32, j0 = ct * 256 + 64 * wave;
+  int64_t row[2];
+  floatx16 acc[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int64_t j = j0 + 32 * q + (lane & 31);
+    row[q] = j < u.rows ? j : -1;
+    acc[q] = floatx16{};
+  }
+  if (u.S) expand_add<DT, YT == 0 ? 3 : 2, 2>(u.ad, u.B, u.rows, u.S, t0, u.n, row, acc);
+  store_tile<YT, 2>(turn[wave], acc, u.out, t0, u.n, j0, u.rows, u.ldo, u.vec_out,
+                    [&](float (&v)[8], int64_t t, int64_t j, int k) { add_base<YT>(u, v, t, j, k); });
+}
+
+// A few tokens: a thread takes one output of one token, and its row of that
+// token's adapter (a tile of 32 tokens would take 32 adapters in turn).
+template <int DT, int YT>
+__global__ __launch_bounds__(256) void up_kernel(UpArgs u) {
+  const int64_t t = blockIdx.x / u.col_tiles, ct = blockIdx.x - t * u.col_tiles;
+  const int64_t j = ct * 256 + threadIdx.x;
+  if (j >= u.rows) return;
+  float v[8] = {};
+  const int a = u.S ? adapter_of(u.ad, t, u.n) : -1;
+  if (a >= 0) v[0] = rank_dot<DT>(u.S + t * u.ad.rank, u.B + ((int64_t)a * u.rows + j) * u.ad.rank, u.ad.rank);
+  add_base<YT>(u, v, t, j, 1);
+  store_out<YT>(u.out, t * u.ldo + j, v[0]);
 }
 
 // ---------------------------------------------------------------- transpose
@@ -201,11 +252,12 @@ __global__ __launch_bounds__(256) void transpose16_kernel(const uint16_t* __rest
 }
 
 // ---------------------------------------------------------------- token lists
-// Workgroup a lists its adapter's tokens in ascending order after the tokens
-// of the adapters before it: it counts those, then places its own by a prefix
-// over the workgroup.  No atomics, so the order is fixed.
+// Workgroup a lists its adapter's tokens in ascending order.  It counts the
+// tokens of the adapters before it (c) and starts at 32 (ceil(c / 32) + a): the
+// next one starts at least count + 1 places further and on a multiple of 32.
+// No atomics, so the order is fixed.
 __global__ __launch_bounds__(1024) void token_lists_kernel(Adapters ad, int64_t n, int32_t* __restrict__ order,
-                                                           int32_t* __restrict__ start) {
+                                                           int32_t* __restrict__ start, int32_t* __restrict__ counts) {
   __shared__ int below[16];
   __shared__ int count[16];
   const int a = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -218,10 +270,11 @@ __global__ __launch_bounds__(1024) void token_lists_kernel(Adapters ad, int64_t 
   for (int m = 1; m < 64; m <<= 1) less += __shfl_xor(less, m);
   if (lane == 0) below[w] = less;
   __syncthreads();
-  int at = 0;
+  int before_all = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) at += below[i];
-  if (threadIdx.x == 0) start[a] = at;
+  for (int i = 0; i < 16; ++i) before_all += below[i];
+  const int64_t first = 32 * ((int64_t)(before_all + 31) / 32 + a);
+  int64_t at = first;
   for (int64_t t0 = 0; t0 < n; t0 += 1024) {
     const int64_t t = t0 + threadIdx.x;
     const bool in = adapter_of(ad, t, n) == a;
@@ -238,26 +291,55 @@ __global__ __launch_bounds__(1024) void token_lists_kernel(Adapters ad, int64_t 
     at += all;
     __syncthreads();
   }
-  if (a == ad.m - 1 && threadIdx.x == 0) start[ad.m] = at;
+  const int mine = (int)(at - first);
+  const int64_t next = 32 * ((int64_t)(before_all + mine + 31) / 32 + a + 1);
+  for (int64_t i = at + threadIdx.x; i < next; i += 1024) order[i] = -1;
+  if (threadIdx.x == 0) {
+    start[a] = (int32_t)first;
+    counts[a] = mine;
+    if (a == ad.m - 1) start[a + 1] = (int32_t)next;
+  }
+}
+
+// The rank values in list order, transposed and split into three bf16 terms: the
+// gradients' operand as it is loaded.  One thread per rank row and eight places.
+__global__ __launch_bounds__(256) void sorted_terms_kernel(const float* __restrict__ V, int rank, const int32_t* __restrict__ order,
+                                                           const int32_t* __restrict__ used, int64_t places,
+                                                           uint16_t* __restrict__ terms) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t p8 = i / rank * 8;
+  const int p = (int)(i % rank);
+  if (p8 >= *used) return;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int t = order[p8 + e];
+    v[e] = t >= 0 ? V[(int64_t)t * rank + p] : 0.f;
+  }
+  u32x4 k[3];
+  split8<3>(v, k);
+#pragma unroll
+  for (int u = 0; u < 3; ++u) *reinterpret_cast<u32x4*>(terms + ((int64_t)u * rank + p) * places + p8) = k[u];
 }
 
 // ---------------------------------------------------------------- gradients
 // G[p, j] = sum over the adapter's tokens of V[t, p] Z[t, j].  The contraction
-// runs over tokens, along which neither operand is contiguous.  A lane loads 8
-// columns of 8 tokens of Z; column u of them is its operand of the u-th of
-// eight products, whose 16 columns are j0 + 8 (lane & 15) + u: the transpose
-// happens in registers.  Tokens come through the adapter's list, so they may
-// lie in any order; places past its end multiply zeros by zeros.  V is split
-// in three bf16 terms (24 significant bits) and fp16 Z in two, so the gradient
-// keeps fp32's range and precision.
+// runs over tokens, along which Z is not contiguous.  A lane loads 8 columns of
+// 8 tokens of Z; column u of them is its operand of the u-th of eight products,
+// whose 16 columns are j0 + 8 (lane & 15) + u: the transpose happens in
+// registers.  Tokens come through the adapter's list, so they may lie in any
+// order; places past its end repeat its first token and multiply zeros.  V
+// comes in three bf16 terms (24 significant bits) and fp16 Z is split in two,
+// so the gradient keeps fp32's range and precision.
 // Workgroup: 4 waves over the tokens of one 128-column block and 16 RT rank
 // rows, joined through LDS in wave order; token splits over the grid write
-// partial results that join_kernel adds in order.
+// partial results that join_kernel adds in order.  The next block's Z is
+// loaded before the current one is multiplied.
 template <int DT, int RT>
-__global__ __launch_bounds__(256) void grad_kernel(const float* __restrict__ V, const uint16_t* __restrict__ Z, int64_t cols,
-                                                   int64_t ldz, bool vec, int rank, const int32_t* __restrict__ order,
-                                                   const int32_t* __restrict__ start, int up, float* __restrict__ G,
-                                                   int64_t per_split, int64_t col_blocks, int rank_blocks, int splits) {
+__global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ terms, int64_t places, const uint16_t* __restrict__ Z,
+                                                   int64_t cols, int64_t ldz, bool vec, int rank, const int32_t* __restrict__ order,
+                                                   const int32_t* __restrict__ start, const int32_t* __restrict__ counts, int up,
+                                                   float* __restrict__ G, int64_t col_blocks, int rank_blocks, int splits) {
   __shared__ float red[16 * RT][128 + 4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, kq = lane >> 4;
   int64_t b = blockIdx.x;
@@ -267,8 +349,13 @@ __global__ __launch_bounds__(256) void grad_kernel(const float* __restrict__ V, 
   b /= rank_blocks;
   const int split = (int)(b % splits);
   const int a = (int)(b / splits);
-  const int first = start[a], count = start[a + 1] - first;
-  const int64_t j0 = cb * 128 + 8 * m;
+  const int64_t first = start[a];
+  const int count = counts[a];
+  // whole 16-byte loads where rows allow them: columns past the end repeat the
+  // last eight, whose results are dropped
+  const int64_t jv = cb * 128 + 8 * m;
+  const bool whole = vec && cols % 8 == 0;
+  const int64_t j0 = whole ? min(jv, cols - 8) : jv;
   const int valid = (int)max((int64_t)0, min((int64_t)8, cols - j0));
   const int p0 = rb * 16 * RT;
 
@@ -280,26 +367,27 @@ __global__ __launch_bounds__(256) void grad_kernel(const float* __restrict__ V, 
 
   const int blocks = (count + 31) / 32;
   const int each = (blocks + splits - 1) / splits;
-  const int b1 = min(blocks, (split + 1) * each);
-  for (int blk = split * each + wave; blk < b1; blk += 4) {
-    u32x4 z[8];
-    int64_t tok[8];
+  const int b0 = split * each + wave, b1 = min(blocks, (split + 1) * each);
+  auto load_z = [&](int blk, u32x4 (&z)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int i = 32 * blk + 8 * kq + e;
-      tok[e] = i < count ? (int64_t)order[first + i] : -1;
-      z[e] = u32x4{0u, 0u, 0u, 0u};
-      if (tok[e] >= 0 && valid > 0) z[e] = load8(Z + tok[e] * ldz + j0, valid, vec);
+      int t = order[first + 32 * blk + 8 * kq + e];
+      if (t < 0) t = order[first];
+      if (whole) z[e] = *reinterpret_cast<const u32x4*>(Z + (int64_t)t * ldz + j0);
+      else z[e] = load8(Z + (int64_t)t * ldz + j0, valid, vec);
     }
-    u32x4 vt[RT][3];
+  };
+  u32x4 z[8];
+  if (b0 < b1) load_z(b0, z);
+  for (int blk = b0; blk < b1; blk += 4) {
+    u32x4 vt[RT][3], next[8];
 #pragma unroll
-    for (int p = 0; p < RT; ++p) {
-      float v[8];
-      const int pr = p0 + 16 * p + m;
+    for (int p = 0; p < RT; ++p)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (tok[e] >= 0 && pr < rank) ? V[tok[e] * rank + pr] : 0.f;
-      split8<3>(v, vt[p]);
-    }
+      for (int k = 0; k < 3; ++k)
+        vt[p][k] = *reinterpret_cast<const u32x4*>(terms + ((int64_t)k * rank + min(p0 + 16 * p + m, rank - 1)) * places + first +
+                                                   32 * blk + 8 * kq);
+    if (blk + 4 < b1) load_z(blk + 4, next);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       u32x4 f;
@@ -310,6 +398,8 @@ __global__ __launch_bounds__(256) void grad_kernel(const float* __restrict__ V, 
 #pragma unroll
       for (int p = 0; p < RT; ++p) acc[p][u] = mfma_terms<DT, 3>(vt[p], zt, acc[p][u]);
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = next[e];
   }
 
   // waves in turn; row of the accumulator = rank, column = 8 (lane & 15) + u
@@ -360,6 +450,9 @@ int down_splits(int64_t n, int64_t d) {
 // Tokens from which down_tiles_kernel is faster than a wave per value.
 constexpr int64_t kDownTiles = 64;
 
+// Tokens up to which up_kernel is faster than tiles.
+constexpr int64_t kUpTokens = 64;
+
 }  // namespace
 
 int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank) {
@@ -382,7 +475,11 @@ void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ld
   const int splits = down_splits(n, d);
   float* out = splits == 1 ? S : S + (n * ad.rank + 63) / 64 * 64;
   const dim3 grid((unsigned)((n + 63) / 64 * splits));
-#define GPTQ_DOWN(D_, R_) hipLaunchKernelGGL((down_tiles_kernel<D_, R_>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits)
+#define GPTQ_DOWN(D_, R_)                                                                                                          \
+  do {                                                                                                                             \
+    if (vec && d % 32 == 0) hipLaunchKernelGGL((down_tiles_kernel<D_, R_, true>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits); \
+    else hipLaunchKernelGGL((down_tiles_kernel<D_, R_, false>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits);     \
+  } while (0)
 #define GPTQ_DOWN_R(D_)                     \
   do {                                      \
     if (ad.rank <= 16) GPTQ_DOWN(D_, 1);    \
@@ -398,12 +495,18 @@ void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ld
     hipLaunchKernelGGL(scale_join_kernel, dim3((unsigned)((n * ad.rank / 4 + 255) / 256)), block, 0, s, out, n, ad, splits, S);
 }
 
-void launch_adapter_up(const float* S, int64_t n, const Adapters& ad, int xt, const uint16_t* B, int64_t rows,
-                       const void* base, int64_t ldb, void* out, int yt, int64_t ldo, hipStream_t s) {
-  const int64_t ct = (rows + 255) / 256;
-  const dim3 grid((unsigned)((n + 15) / 16 * ct)), block(256);
-#define GPTQ_UP(D_, Y_) \
-  hipLaunchKernelGGL((up_kernel<D_, Y_>), grid, block, 0, s, S, n, ad, B, rows, base, ldb, out, ldo, ct)
+void launch_adapter_up(const UpArgs& given, int xt, int yt, hipStream_t s) {
+  UpArgs u = given;
+  u.col_tiles = (u.rows + 255) / 256;
+  u.vec_base = u.part ? rows_on_16(u.part, u.rows, 0) : rows_on_16(u.base, u.ldb, yt);
+  u.vec_out = rows_on_16(u.out, u.ldo, yt);
+  const bool few = u.n <= kUpTokens;
+  const dim3 grid((unsigned)((few ? u.n : (u.n + 31) / 32) * u.col_tiles)), block(256);
+#define GPTQ_UP(D_, Y_)                                                                \
+  do {                                                                                 \
+    if (few) hipLaunchKernelGGL((up_kernel<D_, Y_>), grid, block, 0, s, u);            \
+    else hipLaunchKernelGGL((up_tiles_kernel<D_, Y_>), grid, block, 0, s, u);          \
+  } while (0)
   if (xt == kBF16) { if (yt == 0) GPTQ_UP(kBF16, 0); else GPTQ_UP(kBF16, kBF16); }
   else { if (yt == 0) GPTQ_UP(kF16, 0); else GPTQ_UP(kF16, kF16); }
 #undef GPTQ_UP
@@ -415,8 +518,14 @@ void launch_transpose16(const uint16_t* src, int m, int64_t rows, int64_t cols, 
                      ldd, rt);
 }
 
-void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, hipStream_t s) {
-  hipLaunchKernelGGL(token_lists_kernel, dim3((unsigned)ad.m), dim3(1024), 0, s, ad, n, order, start);
+void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, int32_t* count, hipStream_t s) {
+  hipLaunchKernelGGL(token_lists_kernel, dim3((unsigned)ad.m), dim3(1024), 0, s, ad, n, order, start, count);
+}
+
+void launch_sorted_terms(const float* V, int rank, const int32_t* order, const int32_t* used, int64_t places, uint16_t* terms,
+                         hipStream_t s) {
+  hipLaunchKernelGGL(sorted_terms_kernel, dim3((unsigned)((places / 8 * rank + 255) / 256)), dim3(256), 0, s, V, rank, order, used, places,
+                     terms);
 }
 
 int adapter_grad_splits(int64_t n, int m, int64_t cols) {
@@ -426,9 +535,9 @@ int adapter_grad_splits(int64_t n, int m, int64_t cols) {
   return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
 }
 
-void launch_adapter_grad(const float* V, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz, const Adapters& ad,
-                         const int32_t* order, const int32_t* start, int up, float* G, float* part, int splits,
-                         hipStream_t s) {
+void launch_adapter_grad(const uint16_t* terms, int64_t places, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz,
+                         const Adapters& ad, const int32_t* order, const int32_t* start, const int32_t* count, int up, float* G,
+                         float* part, int splits, hipStream_t s) {
   const bool vec = rows_on_16(Z, ldz, zt);
   const int rt = ad.rank <= 16 ? 1 : (ad.rank <= 32 ? 2 : 4);
   const int rb = (ad.rank + 16 * rt - 1) / (16 * rt);
@@ -436,8 +545,9 @@ void launch_adapter_grad(const float* V, const void* Z, int zt, int64_t n, int64
   const dim3 grid((unsigned)(cb * rb * splits * ad.m)), block(256);
   float* dst = splits > 1 ? part : G;
   const auto* z = static_cast<const uint16_t*>(Z);
-#define GPTQ_GRAD(D_, R_) \
-  hipLaunchKernelGGL((grad_kernel<D_, R_>), grid, block, 0, s, V, z, cols, ldz, vec, ad.rank, order, start, up, dst, (int64_t)0, cb, rb, splits)
+#define GPTQ_GRAD(D_, R_)                                                                                                       \
+  hipLaunchKernelGGL((grad_kernel<D_, R_>), grid, block, 0, s, terms, places, z, cols, ldz, vec, ad.rank, order, start, count, up, dst, cb, \
+                     rb, splits)
   if (zt == kBF16) { if (rt == 1) GPTQ_GRAD(kBF16, 1); else if (rt == 2) GPTQ_GRAD(kBF16, 2); else GPTQ_GRAD(kBF16, 4); }
   else { if (rt == 1) GPTQ_GRAD(kF16, 1); else if (rt == 2) GPTQ_GRAD(kF16, 2); else GPTQ_GRAD(kF16, 4); }
 #undef GPTQ_GRAD

@@ -187,6 +187,23 @@ GPTQ_DEV void load8f(const float* p, float (&v)[8]) {
   }
 }
 
+// sum_p S[p] b[p] of one output: its row b of 16-bit values.
+template <int DT>
+GPTQ_DEV float rank_dot(const float* S, const uint16_t* b, int rank) {
+  float sum = 0.f;
+  for (int p = 0; p < rank; p += 8) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(b + p);
+    float v[8];
+    load8f(S + p, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sum = __builtin_fmaf(v[2 * e], f16_to_f32<DT>(w[e] & 0xFFFFu), sum);
+      sum = __builtin_fmaf(v[2 * e + 1], f16_to_f32<DT>(w[e] >> 16), sum);
+    }
+  }
+  return sum;
+}
+
 // out[q] += (S B_a^T) of the tile's tokens t0 .. and NT sets of its outputs, in
 // the accumulator layout (row = token): the low-rank product beside a tile.
 // S [n][rank] fp32 already holds alpha; row[q] is this lane's output row
@@ -235,10 +252,13 @@ GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, co
 // turned through the wave's own 32 x (32 NT + 4) floats of LDS so that a row
 // leaves in whole runs of eight outputs per lane (single stores of two bytes
 // took a tenth of a 256 x 256 tile's time at 4096 columns).  vec: rows of out
-// start on 16 bytes.
-template <int OT, int NT>
+// start on 16 bytes.  more(v, t, j, k): adds to the first k <= 8 outputs from j.
+struct NoMore {
+  GPTQ_DEV void operator()(float (&)[8], int64_t, int64_t, int) const {}
+};
+template <int OT, int NT, class More = NoMore>
 GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], void* out, int64_t t0, int64_t n, int64_t j0, int64_t cols, int64_t ldo,
-                         bool vec) {
+                         bool vec, const More& more = More()) {
   constexpr int W = 32 * NT, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;
   const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -253,6 +273,7 @@ GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], void* out, int64
     float v[8];
     load8f(lds + r * LD + c, v);
     if (t >= n || j >= cols) continue;
+    more(v, t, j, (int)min((int64_t)8, cols - j));
     if (vec && j + 8 <= cols) {
       if constexpr (OT == 0) {
         float* o = static_cast<float*>(out) + t * ldo + j;
@@ -309,6 +330,27 @@ GPTQ_DEV uint32_t straddling_block(const uint32_t* words, int b) {
   return __builtin_amdgcn_alignbit(c[at < 2 ? at + 1 : 2], c[at], bit & 31);
 }
 
+// 32 consecutive codes of a row.
+template <int BITS>
+struct Chunk {
+  uint32_t w[BITS];
+};
+
+template <int BITS>
+GPTQ_DEV Chunk<BITS> load_chunk(const uint32_t* words, int ch) {
+  Chunk<BITS> c;
+  const uint32_t* p = words + (int64_t)BITS * ch;
+  if constexpr (BITS == 4) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) c.w[i] = p[i];
+  }
+  return c;
+}
+
 // Codes t and t + 4 of a block of eight, t = 0 .. 3, as pairs of 16-bit floats
 // 2^BITS + q.
 template <int BITS, int DT>
@@ -346,21 +388,42 @@ GPTQ_DEV u32x4 pair_order(u32x4 v) {
 int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank);
 void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ldx, const Adapters& ad, const uint16_t* A,
                          int64_t lda, float* S, hipStream_t s);
-// out = base + S B^T (base null: 0), out and base [n][rows] of type yt.
-void launch_adapter_up(const float* S, int64_t n, const Adapters& ad, int xt, const uint16_t* B, int64_t rows,
-                       const void* base, int64_t ldb, void* out, int yt, int64_t ldo, hipStream_t s);
+// out = base + S B^T, of type yt.  base: of the same type (null: 0), or the sum of
+// `splits` parts [n][rows] fp32 times 2^ex[t].  S null: no adapters.
+struct UpArgs {
+  const float* S;
+  int64_t n, rows;
+  Adapters ad;
+  const uint16_t* B;      // [m][rows][rank] of type xt
+  const void* base;
+  int64_t ldb;
+  const float* part;
+  int splits;
+  const int32_t* ex;
+  void* out;
+  int64_t ldo;
+  int64_t col_tiles;      // set by the launch
+  bool vec_base, vec_out;
+};
+void launch_adapter_up(const UpArgs& u, int xt, int yt, hipStream_t s);
 // dst[a][j][i] = src[a][i][j] of m matrices, src [rows][cols] dense, dst row
 // stride ldd >= rows, zero in columns rows .. ldd-1.
 void launch_transpose16(const uint16_t* src, int m, int64_t rows, int64_t cols, uint16_t* dst, int64_t ldd, hipStream_t s);
-// Token lists by adapter: order[start[a] .. start[a+1]) are the tokens of
-// adapter a, ascending.
-void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, hipStream_t s);
-// G[a][p][j] (up == 0) or G[a][j][p] (up == 1) = sum over a's tokens of
-// V[t][p] Z[t][j].  part: workspace of `splits` partial results (splits > 1).
-int adapter_grad_splits(int64_t n, int m, int64_t cols);
-void launch_adapter_grad(const float* V, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz, const Adapters& ad,
-                         const int32_t* order, const int32_t* start, int up, float* G, float* part, int splits,
+// Token lists by adapter: order[start[a]] .. are the count[a] tokens of adapter a,
+// ascending, then -1 up to start[a + 1]; starts are multiples of 32.
+inline int64_t list_places(int64_t n, int64_t m) { return (n + 31) / 32 * 32 + 32 * m; }
+void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, int32_t* count, hipStream_t s);
+// terms[k][p][i] = k-th bf16 term of V[order[i]][p] (0 where order[i] is -1).
+// used: start[m], on the device.
+void launch_sorted_terms(const float* V, int rank, const int32_t* order, const int32_t* used, int64_t places, uint16_t* terms,
                          hipStream_t s);
+// G[a][p][j] (up == 0) or G[a][j][p] (up == 1) = sum over a's tokens of
+// V[t][p] Z[t][j], V as sorted terms.  part: workspace of `splits` partial
+// results (splits > 1).
+int adapter_grad_splits(int64_t n, int m, int64_t cols);
+void launch_adapter_grad(const uint16_t* terms, int64_t places, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz,
+                         const Adapters& ad, const int32_t* order, const int32_t* start, const int32_t* count, int up, float* G,
+                         float* part, int splits, hipStream_t s);
 
 // out = X W^T (+ S B^T): gemm16.hip.  The contraction has kp columns, a
 // multiple of its step, with zeros in W past the last one (and finite values

@@ -139,6 +139,8 @@ bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
          groups_for(r, 64) * groups_for(c, 256) <= kMaxGroups256 &&                      // dequantized copy
          groups_for(n * (r / 8 + 8), 256) <= kMaxGroups256 &&                            // padded rows
          groups_for(n * (c / 8), 256) <= kMaxGroups256 &&                                // gather
+         n * groups_for(r > c ? r : c, 256) <= kMaxGroups256 * (n > 64 ? 32 : 1) &&      // up
+         groups_for(gptq::list_places(n, m) / 8 * (rank > 0 ? rank : 1), 256) <= kMaxGroups256 && gptq::list_places(n, m) < INT_MAX &&  // lists
          m * groups_for(r > c ? r : c, 64) * 2 <= kMaxGroups256 &&                       // transpose (rank <= 128)
          m * groups_for(r > c ? r : c, 128) * 2 * 16 <= kMaxGroups256 &&                 // gradients (16 splits)
          groups_for(m * rank * (r > c ? r : c), 1024) <= kMaxGroups256;                  // join
@@ -151,7 +153,7 @@ int64_t backward_bytes(int64_t n, int64_t r, int64_t c, int terms) {
 
 struct GradSizes {
   int sa, sb;                       // token splits of gA and gB
-  int64_t part, lists, total;
+  int64_t places, part, lists, terms, total;
 };
 
 GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
@@ -160,8 +162,10 @@ GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
   z.sb = gptq::adapter_grad_splits(n, (int)m, r);
   const int64_t pa = z.sa > 1 ? z.sa * m * rank * c * 4 : 0, pb = z.sb > 1 ? z.sb * m * rank * r * 4 : 0;
   z.part = align256(pa > pb ? pa : pb);
-  z.lists = align256(n * 4) + align256((m + 1) * 4);
-  z.total = align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + low_bytes(n, c, rank) + low_bytes(n, r, rank) + z.lists + z.part;
+  z.places = gptq::list_places(n, m);
+  z.lists = align256(z.places * 4) + align256((m + 1) * 4) + align256(m * 4);
+  z.terms = align256(3 * rank * z.places * 2);
+  z.total = align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + low_bytes(n, c, rank) + low_bytes(n, r, rank) + z.lists + 2 * z.terms + z.part;
   return z;
 }
 
@@ -345,7 +349,9 @@ gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n, int64_t c,
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
   float* S = static_cast<float*>(ws);
   gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
-  gptq::launch_adapter_up(S, n, ad, xi, ad.B, r, Y, ldy, out, yt == GPTQ_F32 ? 0 : xi, ldo, s);
+  gptq::UpArgs u{};
+  u.S = S; u.n = n; u.rows = r; u.ad = ad; u.B = ad.B; u.base = Y; u.ldb = ldy; u.out = out; u.ldo = ldo;
+  gptq::launch_adapter_up(u, xi, yt == GPTQ_F32 ? 0 : xi, s);
   return check_launch(fn);
 }
 
@@ -403,20 +409,27 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   uint16_t* At = carve.take<uint16_t>(m * c * rank * 2);
   float* S = carve.take<float>(low_bytes(n, c, rank));
   float* T = carve.take<float>(low_bytes(n, r, rank));
-  int32_t* order = carve.take<int32_t>(n * 4);
+  int32_t* order = carve.take<int32_t>(z.places * 4);
   int32_t* start = carve.take<int32_t>((m + 1) * 4);
+  int32_t* count = carve.take<int32_t>(m * 4);
+  uint16_t* Sx = carve.take<uint16_t>(z.terms);
+  uint16_t* Tx = carve.take<uint16_t>(z.terms);
   float* part = carve.take<float>(z.part);
-  gptq::launch_token_lists(ad, n, order, start, s);
+  gptq::launch_token_lists(ad, n, order, start, count, s);
   if (n > 0) {
     gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
     gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
     gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);
+    gptq::launch_sorted_terms(S, (int)rank, order, start + m, z.places, Sx, s);
+    gptq::launch_sorted_terms(T, (int)rank, order, start + m, z.places, Tx, s);
   }
-  gptq::launch_adapter_grad(T, X, xi, n, c, ldx, ad, order, start, 0, gA, part, z.sa, s);
-  gptq::launch_adapter_grad(S, dY, xi, n, r, ldy, ad, order, start, 1, gB, part, z.sb, s);
+  gptq::launch_adapter_grad(Tx, z.places, X, xi, n, c, ldx, ad, order, start, count, 0, gA, part, z.sa, s);
+  gptq::launch_adapter_grad(Sx, z.places, dY, xi, n, r, ldy, ad, order, start, count, 1, gB, part, z.sb, s);
   if (dX && n > 0) {
     gptq::launch_transpose16(ad.A, (int)m, rank, c, At, rank, s);
-    gptq::launch_adapter_up(T, n, ad, xi, At, c, base, ldd, dX, ot == GPTQ_F32 ? 0 : xi, ldd, s);
+    gptq::UpArgs u{};
+    u.S = T; u.n = n; u.rows = c; u.ad = ad; u.B = At; u.base = base; u.ldb = ldd; u.out = dX; u.ldo = ldd;
+    gptq::launch_adapter_up(u, xi, ot == GPTQ_F32 ? 0 : xi, s);
   }
   return check_launch(fn);
 }

@@ -27,10 +27,13 @@ struct FwdArgs {
 };
 
 constexpr int kWaves = 8;
+constexpr int kAhead = 4;   // steps of a wave whose words are requested together
 
 // 16 MT tokens x 16 rows per workgroup.  The waves split the columns in steps
 // of 128 (lane (m, kq): row m, chunk kq of the step's four) and are joined
-// through LDS in wave order.
+// through LDS in wave order; each wave requests the words and rulers of four
+// of its steps before it uses the first (one step at a time waited for memory
+// four times in a row at 4096 columns).
 // WIDE: groups hold whole steps, and the step's four products take word j of
 // every lane's chunk (columns 32 kq + 8 j).  Otherwise the lanes' words are
 // transposed so that product j holds chunk j alone, and rulers apply per chunk.
@@ -50,66 +53,75 @@ __global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
   const uint32_t one = DT == kBF16 ? 0x3F803F80u : 0x3C003C00u;
   const u32x4 ones = {one, one, one, one};
   const floatx4 zero4 = {0.f, 0.f, 0.f, 0.f};
+  constexpr int RU = WIDE ? 1 : 4;   // rulers per step
 
   floatx4 tot[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) tot[i] = zero4;
 
-  for (int s = wave; s < steps; s += kWaves) {
-    const int ch = min(4 * s + kq, nch - 1);
-    uint32_t chunk[BITS];
-    if constexpr (BITS == 4) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(words + 4 * (int64_t)ch);
+  for (int s0 = wave; s0 < steps; s0 += kWaves * kAhead) {
+    Chunk<BITS> cw[kAhead];
+    float sc[kAhead][RU];
+    int ze[kAhead][RU];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) chunk[i] = v[i];
-    } else {
+    for (int d = 0; d < kAhead; ++d) {
+      const int s = s0 + d * kWaves;
+      cw[d] = load_chunk<BITS>(words, min(4 * s + kq, nch - 1));
 #pragma unroll
-      for (int i = 0; i < 3; ++i) chunk[i] = words[3 * (int64_t)ch + i];
-    }
-    uint32_t blk[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) blk[j] = code_block<BITS>(chunk, j);
-    if constexpr (!WIDE) {
-      // register j of lane (m, kq) <-> register kq of lane (m, j)
-      auto swap16 = [](uint32_t& x, uint32_t& y) {
-        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-        x = r[0];
-        y = r[1];
-      };
-      auto swap32 = [](uint32_t& x, uint32_t& y) {
-        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-        x = r[0];
-        y = r[1];
-      };
-      swap16(blk[0], blk[1]);
-      swap16(blk[2], blk[3]);
-      swap32(blk[0], blk[2]);
-      swap32(blk[1], blk[3]);
-    }
-    floatx4 p[MT], xs[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) p[i] = xs[i] = zero4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const u32x4 w = code_pairs<BITS, DT>(blk[j]);
-      const int xc = WIDE ? 4 * s + kq : 4 * s + j;            // chunk of this lane's activations
-      const int64_t col = 32 * (int64_t)xc + 8 * (WIDE ? j : kq);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int64_t t = t0 + 16 * i + m;
-        u32x4 x = {0u, 0u, 0u, 0u};
-        if (xc < nch && t < a.n) x = pair_order(*reinterpret_cast<const u32x4*>(a.X + t * a.ldx + col));
-        p[i] = mfma16<DT>(x, w, p[i]);
-        xs[i] = mfma16<DT>(x, ones, xs[i]);
+      for (int u = 0; u < RU; ++u) {
+        const int g = min(4 * s + u, nch - 1) / a.w.cpg;
+        sc[d][u] = srow[g];
+        ze[d][u] = zrow[g];
       }
-      if (!WIDE || j == 3) {
-        const int g = min(4 * s + (WIDE ? 0 : j), nch - 1) / a.w.cpg;
-        const float sc = srow[g], off = (float)(1 << BITS) + (float)zrow[g];
+    }
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const int s = s0 + d * kWaves;
+      if (s >= steps) break;
+      uint32_t blk[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) blk[j] = code_block<BITS>(cw[d].w, j);
+      if constexpr (!WIDE) {
+        // register j of lane (m, kq) <-> register kq of lane (m, j)
+        auto swap16 = [](uint32_t& x, uint32_t& y) {
+          const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+          x = r[0];
+          y = r[1];
+        };
+        auto swap32 = [](uint32_t& x, uint32_t& y) {
+          const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+          x = r[0];
+          y = r[1];
+        };
+        swap16(blk[0], blk[1]);
+        swap16(blk[2], blk[3]);
+        swap32(blk[0], blk[2]);
+        swap32(blk[1], blk[3]);
+      }
+      floatx4 p[MT], xs[MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) p[i] = xs[i] = zero4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const u32x4 w = code_pairs<BITS, DT>(blk[j]);
+        const int xc = WIDE ? 4 * s + kq : 4 * s + j;            // chunk of this lane's activations
+        const int64_t col = 32 * (int64_t)xc + 8 * (WIDE ? j : kq);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
+          const int64_t t = t0 + 16 * i + m;
+          u32x4 x = {0u, 0u, 0u, 0u};
+          if (xc < nch && t < a.n) x = pair_order(*reinterpret_cast<const u32x4*>(a.X + t * a.ldx + col));
+          p[i] = mfma16<DT>(x, w, p[i]);
+          xs[i] = mfma16<DT>(x, ones, xs[i]);
+        }
+        if (!WIDE || j == 3) {
+          const float scale = sc[d][WIDE ? 0 : j], off = (float)(1 << BITS) + (float)ze[d][WIDE ? 0 : j];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) tot[i][e] = __builtin_fmaf(sc, __builtin_fmaf(-off, xs[i][e], p[i][e]), tot[i][e]);
-          p[i] = xs[i] = zero4;
+          for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tot[i][e] = __builtin_fmaf(scale, __builtin_fmaf(-off, xs[i][e], p[i][e]), tot[i][e]);
+            p[i] = xs[i] = zero4;
+          }
         }
       }
     }
@@ -120,23 +132,19 @@ __global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) red[wave][i][e][lane] = tot[i][e];
   __syncthreads();
-  if (wave < MT) {
-    const int i = wave;
-    floatx4 y[1];
+  // an output per thread: 16 tokens x 16 rows of the accumulators' layout
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v = red[0][i][e][lane];
+  for (int o = threadIdx.x; o < 256 * MT; o += 64 * kWaves) {
+    const int tok = o >> 4, i = tok >> 4, e = tok & 3, l = ((tok >> 2) & 3) * 16 + (o & 15);
+    const int64_t t = t0 + tok;
+    const int out = row0 + (o & 15);
+    if (t >= a.n || out >= a.w.r) continue;
+    float v = red[0][i][e][l];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += red[w][i][e][lane];
-      y[0][e] = v;
-    }
-    const int64_t rows[1] = {row0 + m < a.w.r ? row0 + m : -1};
-    if (a.S) expand_add<DT, YT == 0 ? 3 : 2, 1>(a.ad, a.ad.B, a.w.r, a.S, t0 + 16 * i, a.n, rows, y);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t t = t0 + 16 * i + 4 * kq + e;
-      if (t < a.n && rows[0] >= 0) store_out<YT>(a.Y, t * a.ldy + rows[0], y[0][e]);
-    }
+    for (int w = 1; w < kWaves; ++w) v += red[w][i][e][l];
+    const int ad = a.S ? adapter_of(a.ad, t, a.n) : -1;
+    if (ad >= 0) v += rank_dot<DT>(a.S + t * a.ad.rank, a.ad.B + ((int64_t)ad * a.w.r + out) * a.ad.rank, a.ad.rank);
+    store_out<YT>(a.Y, t * a.ldy + out, v);
   }
 }
 

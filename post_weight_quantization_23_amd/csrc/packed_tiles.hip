@@ -32,32 +32,11 @@ struct TileArgs {
   int64_t n;
   int ldx, row_tiles, tok_tiles;
   PackedLayer w;
-  Adapters ad;
-  const float* S;      // null: no adapters
-  void* Y;
-  int64_t ldy;
-  bool vec;            // rows of Y start on 16 bytes
+  int splits;          // parts of the contraction
+  float* out;          // parts [splits][n][r], to be summed and times 2^ex; or the
+  int64_t ldo;         //   results themselves (one part, rows of ldo)
+  bool direct, vec;    // results; rows of out start on 16 bytes
 };
-
-template <int BITS>
-struct Chunk {
-  uint32_t w[BITS];
-};
-
-template <int BITS>
-GPTQ_DEV Chunk<BITS> load_chunk(const uint32_t* words, int ch) {
-  Chunk<BITS> c;
-  const uint32_t* p = words + (int64_t)BITS * ch;
-  if constexpr (BITS == 4) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c.w[i] = v[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) c.w[i] = p[i];
-  }
-  return c;
-}
 
 // What turns a block's codes into fp16 values q - z, a pair at a time: a field
 // at bit p of each half, under the exponent of 1024, reads as 1024 + 2^p q;
@@ -99,15 +78,19 @@ GPTQ_DEV u32x4 centered(uint32_t blk, const Center<BITS>& c, uint32_t magic) {
 }
 
 // CPS: chunks of 32 columns that share a ruler within a step (4, 2 or 1).
-template <int BITS, int YT, int DT, int MT, int NT, int CPS>
+template <int BITS, int MT, int CPS>
 GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
+  constexpr int NT = 1;   // 32-row tiles per wave (two need more registers than two waves a SIMD have: 1.09 against 0.89 ms)
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 31, h = lane >> 5;
   int tt, rt;
-  tile_of(blockIdx.x, a.tok_tiles, a.row_tiles, tt, rt);
+  const int64_t tile = blockIdx.x / a.splits;
+  const int split = (int)(blockIdx.x - tile * a.splits);
+  tile_of(tile, a.tok_tiles, a.row_tiles, tt, rt);
   const int64_t t0 = (int64_t)tt * 32 * MT;
   const int row0 = rt * 128 * NT + wave * 32 * NT;
-  const int nch = a.w.c >> 5, steps = (nch + 3) >> 2;
+  const int nch = a.w.c >> 5, all = (nch + 3) >> 2, each = (all + a.splits - 1) / a.splits;
+  const int s0 = split * each, steps = min(all, s0 + each);
 
   const uint32_t* words[NT];
   const float* srow[NT];
@@ -165,9 +148,9 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
 
   uint32_t magic = 0x64006400u;
   asm volatile("" : "+v"(magic));
-  load_x(0);
-  load_w(0);
-  for (int s = 0; s < steps; ++s) {
+  load_x(s0);
+  load_w(s0);
+  for (int s = s0; s < steps; ++s) {
     // this step's operands.  CPS == 4: product j takes words j of the lane's
     // two chunks, columns 64 h + 8 j.  Otherwise the halves exchange words, so
     // that products 2 ch and 2 ch + 1 are chunk ch alone, columns 32 ch + 8 h
@@ -229,34 +212,29 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
     }
   }
 
-  static_assert(4 * 32 * (32 * NT + 4) * 4 <= 2 * 32 * MT * ROWB + 1024 * (MT == 1), "tile results fit the operands' LDS");
   float* own = reinterpret_cast<float*>(xs) + wave * 32 * (32 * NT + 4);
   __syncthreads();   // the last step's operands have been read
-  int64_t row[NT];
-#pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    const int at = row0 + 32 * q + m;
-    row[q] = at < a.w.r ? at : -1;
-  }
+  float* out = a.out + (int64_t)split * a.n * a.w.r;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t ti = t0 + 32 * i;
+    if (a.direct) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int64_t t = ti + TileShape<floatx16>::acc_row(lane, e);
-      const int ex = a.ex[min(t, a.n - 1)];
+      for (int e = 0; e < 16; ++e) {
+        const int ex = a.ex[min(ti + TileShape<floatx16>::acc_row(lane, e), a.n - 1)];
 #pragma unroll
-      for (int q = 0; q < NT; ++q) tot[i][q][e] = __builtin_ldexpf(tot[i][q][e], ex);
+        for (int q = 0; q < NT; ++q) tot[i][q][e] = __builtin_ldexpf(tot[i][q][e], ex);
+      }
     }
-    if (a.S) expand_add<DT, YT == 0 ? 3 : 2, NT>(a.ad, a.ad.B, a.w.r, a.S, ti, a.n, row, tot[i]);
-    store_tile<YT, NT>(own, tot[i], a.Y, ti, a.n, row0, a.w.r, a.ldy, a.vec);
+    store_tile<0, NT>(own, tot[i], out, ti, a.n, row0, a.w.r, a.ldo, a.vec);
   }
 }
 
-template <int BITS, int YT, int DT, int MT, int NT, int CPS>
+template <int BITS, int MT, int CPS>
 __global__ __launch_bounds__(256, 2) void tiles_kernel(TileArgs a) {
-  __shared__ __align__(16) unsigned char xs[2 * 32 * MT * ROWB];
-  tiles_body<BITS, YT, DT, MT, NT, CPS>(a, xs);
+  // the operands of two steps, and then four waves' results
+  __shared__ __align__(16) unsigned char xs[2 * 32 * MT * ROWB > 4 * 32 * 36 * 4 ? 2 * 32 * MT * ROWB : 4 * 32 * 36 * 4];
+  tiles_body<BITS, MT, CPS>(a, xs);
 }
 
 // Activations for tiles_kernel: fp16 in the order of code_pairs, columns
@@ -311,23 +289,12 @@ __global__ __launch_bounds__(256) void prepare_tokens_kernel(const uint16_t* __r
   }
 }
 
-template <int BITS, int YT, int DT, int MT, int NT>
-void launch_tiles(TileArgs a, hipStream_t s) {
-  a.row_tiles = (a.w.r + 128 * NT - 1) / (128 * NT);
-  a.tok_tiles = (int)((a.n + 32 * MT - 1) / (32 * MT));
-  const dim3 grid((unsigned)((int64_t)a.tok_tiles * a.row_tiles)), block(256);
-  if (a.w.cpg % 4 == 0 || a.w.cpg >= (a.w.c >> 5)) hipLaunchKernelGGL((tiles_kernel<BITS, YT, DT, MT, NT, 4>), grid, block, 0, s, a);
-  else if (a.w.cpg % 2 == 0) hipLaunchKernelGGL((tiles_kernel<BITS, YT, DT, MT, NT, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((tiles_kernel<BITS, YT, DT, MT, NT, 1>), grid, block, 0, s, a);
-}
-
-template <int BITS, int YT, int DT>
-void choose_tiles(const TileArgs& a, hipStream_t s) {
-#ifdef PROBE_MT
-  launch_tiles<BITS, YT, DT, PROBE_MT, PROBE_NT>(a, s);
-#else
-  launch_tiles<BITS, YT, DT, 4, 1>(a, s);
-#endif
+template <int BITS, int MT>
+void launch_tiles(const TileArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)a.tok_tiles * a.row_tiles * a.splits)), block(256);
+  if (a.w.cpg % 4 == 0 || a.w.cpg >= (a.w.c >> 5)) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 4>), grid, block, 0, s, a);
+  else if (a.w.cpg % 2 == 0) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((tiles_kernel<BITS, MT, 1>), grid, block, 0, s, a);
 }
 
 // The layer as 16-bit rows in packed column order, zero from column c to kp.
@@ -356,6 +323,29 @@ __global__ __launch_bounds__(256) void dequant_rows_kernel(PackedLayer w, uint16
   }
 }
 
+// Tiles of 32 mt tokens x 128 rows, the contraction in `splits` parts.
+struct TilePlan {
+  int mt, splits;
+};
+
+TilePlan plan_tiles(int64_t n, int64_t r, int64_t c) {
+#ifdef PROBE_MT
+  return {PROBE_MT, PROBE_KS};
+#endif
+  const int64_t steps = (c + STEP - 1) / STEP, row_tiles = (r + 127) / 128;
+  TilePlan best{4, 1};
+  double least = 1e30;
+  for (int mt = 1; mt <= 4; mt *= 2)
+    for (int64_t splits = 1; splits <= 16 && 2 * splits <= steps; ++splits) {
+      const int64_t groups = (n + 32 * mt - 1) / (32 * mt) * row_tiles * splits, each = (steps + splits - 1) / splits;
+      const int64_t rounds = (groups + 511) / 512;
+      double us = rounds * (3 + each * (0.66 + 0.48 * mt));
+      if (splits > 1) us += 4 + splits * n * r * 8 / 4e6;
+      if (us < least) least = us, best = {mt, (int)splits};
+    }
+  return best;
+}
+
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 int64_t tiles_width(int64_t c) { return (c + STEP - 1) / STEP * STEP; }
 
@@ -373,7 +363,9 @@ bool packed_tiles(int64_t n, int64_t c) { return n > 64 && c < (int64_t(1) << 22
 
 int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt) {
   if (dequant_first(n, yt)) return align256(n * gemm16_depth(c) * 2) + align256(r * gemm16_depth(c) * 2);
-  return align256(n * tiles_width(c) * 2) + align256(n * 4);
+  const TilePlan p = plan_tiles(n, r, c);
+  const bool direct = yt == 0 && p.splits == 1;
+  return align256(n * tiles_width(c) * 2) + align256(n * 4) + (direct ? 0 : align256(p.splits * n * r * 4));
 }
 
 void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad, const float* S,
@@ -413,25 +405,43 @@ void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const Pa
   const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
   if (xt == kBF16) hipLaunchKernelGGL((prepare_tokens_kernel<kBF16>), dim3((unsigned)n), block, 0, s, x, ldx, vec, w.c, w.perm, xp, ldp, ex);
   else hipLaunchKernelGGL((prepare_tokens_kernel<kF16>), dim3((unsigned)n), block, 0, s, x, ldx, vec, w.c, w.perm, xp, ldp, ex);
+  const TilePlan p = plan_tiles(n, w.r, w.c);
   TileArgs a{};
   a.X = xp;
   a.ex = ex;
   a.n = n;
   a.ldx = ldp;
   a.w = w;
-  a.ad = ad;
-  a.S = S;
-  a.Y = Y;
-  a.ldy = ldy;
-  a.vec = rows_on_16(Y, ldy, yt);
-#define GPTQ_TILES(B_)                                                                                     \
-  do {                                                                                                     \
-    if (xt == kBF16) { if (yt == 0) choose_tiles<B_, 0, kBF16>(a, s); else choose_tiles<B_, kBF16, kBF16>(a, s); } \
-    else { if (yt == 0) choose_tiles<B_, 0, kF16>(a, s); else choose_tiles<B_, kF16, kF16>(a, s); }        \
-  } while (0)
+  a.tok_tiles = (int)((n + 32 * p.mt - 1) / (32 * p.mt));
+  a.row_tiles = (w.r + 127) / 128;
+  a.splits = p.splits;
+  a.direct = yt == 0 && p.splits == 1;
+  a.out = a.direct ? static_cast<float*>(Y) : reinterpret_cast<float*>(ex + align256(n * 4) / 4);
+  a.ldo = a.direct ? ldy : w.r;
+  a.vec = rows_on_16(a.out, a.ldo, 0) && (p.splits == 1 || n * w.r % 4 == 0);
+#define GPTQ_TILES(B_) (p.mt == 4 ? launch_tiles<B_, 4>(a, s) : p.mt == 2 ? launch_tiles<B_, 2>(a, s) : launch_tiles<B_, 1>(a, s))
   if (w.bits == 4) GPTQ_TILES(4);
   else GPTQ_TILES(3);
 #undef GPTQ_TILES
+  if (a.direct && !S) return;
+  // the parts joined, the adapters added, one rounding
+  UpArgs u{};
+  u.S = S;
+  u.n = n;
+  u.rows = w.r;
+  u.ad = ad;
+  u.B = ad.B;
+  if (a.direct) {
+    u.base = Y;
+    u.ldb = ldy;
+  } else {
+    u.part = a.out;
+    u.splits = p.splits;
+    u.ex = ex;
+  }
+  u.out = Y;
+  u.ldo = ldy;
+  launch_adapter_up(u, xt, yt, s);
 }
 
 }  // namespace gptq
