@@ -56,7 +56,8 @@ __global__ __launch_bounds__(256) void down_kernel(const uint16_t* __restrict__ 
 }
 
 // Many tokens: a workgroup takes 64 tokens and one of `splits` parts of the
-// contraction, its four waves every fourth step of 32 of that part, all 16 RT
+// contraction, its four waves every fourth step of 64 of that part (a whole
+// line of memory per row), all 16 RT
 // rank rows (operands come from memory in the layout of the product, which
 // reads X once).  The adapters that occur among the tokens are taken in turn;
 // each writes its own tokens' rows.  Waves are joined through LDS in wave
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
   const int64_t tile = blockIdx.x / splits;
   const int split = (int)(blockIdx.x - tile * splits);
   const int64_t t0 = tile * 64;
-  const int64_t steps = (d + 31) / 32, per = (steps + splits - 1) / splits;
+  const int64_t steps = (d + 63) / 64, per = (steps + splits - 1) / splits;
   const int64_t s1 = min(steps, (split + 1) * per);
   float* out = S + (int64_t)split * n * ad.rank;
   const int mine = adapter_of(ad, t0 + lane, n);
@@ -94,9 +95,7 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int p = 0; p < RT; ++p) acc[i][p] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll FAST ? (RT > 4 ? 2 : 4) : 1
-    for (int64_t s = split * per + wave; s < s1; s += 4) {
-      const int64_t k = 32 * s + 8 * kq;
+    auto step = [&](int64_t k) __attribute__((always_inline)) {
       u32x4 x[4], b[RT];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -115,6 +114,11 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int p = 0; p < RT; ++p) acc[i][p] = mfma16<DT>(x[i], b[p], acc[i][p]);
+    };
+#pragma unroll FAST && RT <= 4 ? 2 : 1
+    for (int64_t s = split * per + wave; s < s1; s += 4) {
+      step(64 * s + 8 * kq);
+      step(64 * s + 32 + 8 * kq);
     }
     for (int v = 0; v < 4; ++v) {
       if (wave == v) {
@@ -331,18 +335,18 @@ __global__ __launch_bounds__(256) void sorted_terms_kernel(const float* __restri
 // order; places past its end repeat its first token and multiply zeros.  V
 // comes in three bf16 terms (24 significant bits) and fp16 Z is split in two,
 // so the gradient keeps fp32's range and precision.
-// Workgroup: 4 waves over the tokens of one 128-column block and 16 RT rank
-// rows, joined through LDS in wave order; token splits over the grid write
-// partial results that join_kernel adds in order.  The next block's Z is
-// loaded before the current one is multiplied.
+// A wave takes 128 columns x 16 RT rank rows and one of `splits` parts of the
+// adapter's tokens, by itself (four waves joined through LDS spent more time
+// there than on their five blocks of tokens); parts are added in order by
+// join_kernel.  The next block's Z is requested before the current one is used.
 template <int DT, int RT>
 __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ terms, int64_t places, const uint16_t* __restrict__ Z,
                                                    int64_t cols, int64_t ldz, bool vec, int rank, const int32_t* __restrict__ order,
                                                    const int32_t* __restrict__ start, const int32_t* __restrict__ counts, int up,
-                                                   float* __restrict__ G, int64_t col_blocks, int rank_blocks, int splits) {
-  __shared__ float red[16 * RT][128 + 4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, kq = lane >> 4;
-  int64_t b = blockIdx.x;
+                                                   float* __restrict__ G, int64_t items, int64_t col_blocks, int rank_blocks, int splits) {
+  const int lane = threadIdx.x & 63, m = lane & 15, kq = lane >> 4;
+  int64_t b = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (b >= items) return;
   const int64_t cb = b % col_blocks;
   b /= col_blocks;
   const int rb = (int)(b % rank_blocks);
@@ -367,7 +371,7 @@ __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ 
 
   const int blocks = (count + 31) / 32;
   const int each = (blocks + splits - 1) / splits;
-  const int b0 = split * each + wave, b1 = min(blocks, (split + 1) * each);
+  const int b0 = split * each, b1 = min(blocks, (split + 1) * each);
   auto load_z = [&](int blk, u32x4 (&z)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -379,7 +383,7 @@ __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ 
   };
   u32x4 z[8];
   if (b0 < b1) load_z(b0, z);
-  for (int blk = b0; blk < b1; blk += 4) {
+  for (int blk = b0; blk < b1; ++blk) {
     u32x4 vt[RT][3], next[8];
 #pragma unroll
     for (int p = 0; p < RT; ++p)
@@ -387,7 +391,7 @@ __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ 
       for (int k = 0; k < 3; ++k)
         vt[p][k] = *reinterpret_cast<const u32x4*>(terms + ((int64_t)k * rank + min(p0 + 16 * p + m, rank - 1)) * places + first +
                                                    32 * blk + 8 * kq);
-    if (blk + 4 < b1) load_z(blk + 4, next);
+    if (blk + 1 < b1) load_z(blk + 1, next);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       u32x4 f;
@@ -402,30 +406,31 @@ __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ 
     for (int e = 0; e < 8; ++e) z[e] = next[e];
   }
 
-  // waves in turn; row of the accumulator = rank, column = 8 (lane & 15) + u
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
-#pragma unroll
-      for (int p = 0; p < RT; ++p)
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float& x = red[16 * p + 4 * kq + i][8 * m + u];
-            x = w == 0 ? acc[p][u][i] : x + acc[p][u][i];
-          }
-    }
-    __syncthreads();
-  }
-  const int64_t m_all = (int64_t)gridDim.x / (col_blocks * rank_blocks * splits);
+  // row of the accumulator = rank, column = 8 (lane & 15) + u
+  const int64_t m_all = items / (col_blocks * rank_blocks * splits);
   float* g = G + ((int64_t)split * m_all + a) * rank * cols;
-  for (int i = threadIdx.x; i < 16 * RT * 128; i += 256) {
-    int pp, jj;
-    if (up) { jj = i / (16 * RT); pp = i - jj * (16 * RT); }
-    else { pp = i >> 7; jj = i & 127; }
-    const int64_t j = cb * 128 + jj;
-    const int p = p0 + pp;
-    if (j < cols && p < rank) g[up ? j * rank + p : (int64_t)p * cols + j] = red[pp][jj];
+#pragma unroll
+  for (int p = 0; p < RT; ++p) {
+    const int pr = p0 + 16 * p + 4 * kq;
+    if (up) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (jv + u < cols && pr < rank) *reinterpret_cast<floatx4*>(g + (jv + u) * rank + pr) = acc[p][u];   // rank % 8 == 0
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (pr + i >= rank) continue;
+        float* o = g + (int64_t)(pr + i) * cols + jv;
+        if (jv + 8 <= cols && cols % 4 == 0) {
+          *reinterpret_cast<floatx4*>(o) = floatx4{acc[p][0][i], acc[p][1][i], acc[p][2][i], acc[p][3][i]};
+          *reinterpret_cast<floatx4*>(o + 4) = floatx4{acc[p][4][i], acc[p][5][i], acc[p][6][i], acc[p][7][i]};
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (jv + u < cols) o[u] = acc[p][u][i];
+        }
+      }
+    }
   }
 }
 
@@ -439,11 +444,11 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 }
 
 // Parts of the contraction of down_tiles_kernel: enough workgroups for the
-// chip, each wave left with four steps at least.
+// chip, each wave left with two steps at least.
 int down_splits(int64_t n, int64_t d) {
-  const int64_t tiles = (n + 63) / 64, steps = (d + 31) / 32;
+  const int64_t tiles = (n + 63) / 64, steps = (d + 63) / 64;
   int64_t splits = 512 / tiles;
-  splits = splits < steps / 16 ? splits : steps / 16;
+  splits = splits < steps / 8 ? splits : steps / 8;
   return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
 }
 
@@ -477,7 +482,7 @@ void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ld
   const dim3 grid((unsigned)((n + 63) / 64 * splits));
 #define GPTQ_DOWN(D_, R_)                                                                                                          \
   do {                                                                                                                             \
-    if (vec && d % 32 == 0) hipLaunchKernelGGL((down_tiles_kernel<D_, R_, true>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits); \
+    if (vec && d % 64 == 0) hipLaunchKernelGGL((down_tiles_kernel<D_, R_, true>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits); \
     else hipLaunchKernelGGL((down_tiles_kernel<D_, R_, false>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits);     \
   } while (0)
 #define GPTQ_DOWN_R(D_)                     \
@@ -528,10 +533,14 @@ void launch_sorted_terms(const float* V, int rank, const int32_t* order, const i
                      terms);
 }
 
-int adapter_grad_splits(int64_t n, int m, int64_t cols) {
-  const int64_t groups = (cols + 127) / 128 * m;
-  int64_t splits = (512 + groups - 1) / groups;
-  splits = splits < (n + 127) / 128 ? splits : (n + 127) / 128;
+// Rank rows of a gradient wave: 32 (64 would leave one wave per SIMD).
+int grad_rows(int rank) { return rank <= 16 ? 16 : 32; }
+
+int adapter_grad_splits(int64_t n, int m, int64_t cols, int rank) {
+  const int64_t waves = (cols + 127) / 128 * m * ((rank + grad_rows(rank) - 1) / grad_rows(rank));
+  int64_t splits = (2048 + waves - 1) / waves;
+  const int64_t most = n / m / (32 * 4);   // four blocks of tokens at least
+  splits = splits < most ? splits : most;
   return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
 }
 
@@ -539,17 +548,17 @@ void launch_adapter_grad(const uint16_t* terms, int64_t places, const void* Z, i
                          const Adapters& ad, const int32_t* order, const int32_t* start, const int32_t* count, int up, float* G,
                          float* part, int splits, hipStream_t s) {
   const bool vec = rows_on_16(Z, ldz, zt);
-  const int rt = ad.rank <= 16 ? 1 : (ad.rank <= 32 ? 2 : 4);
-  const int rb = (ad.rank + 16 * rt - 1) / (16 * rt);
-  const int64_t cb = (cols + 127) / 128;
-  const dim3 grid((unsigned)(cb * rb * splits * ad.m)), block(256);
+  const int rt = grad_rows(ad.rank);
+  const int rb = (ad.rank + rt - 1) / rt;
+  const int64_t cb = (cols + 127) / 128, items = cb * rb * splits * ad.m;
+  const dim3 grid((unsigned)((items + 3) / 4)), block(256);
   float* dst = splits > 1 ? part : G;
   const auto* z = static_cast<const uint16_t*>(Z);
 #define GPTQ_GRAD(D_, R_)                                                                                                       \
-  hipLaunchKernelGGL((grad_kernel<D_, R_>), grid, block, 0, s, terms, places, z, cols, ldz, vec, ad.rank, order, start, count, up, dst, cb, \
-                     rb, splits)
-  if (zt == kBF16) { if (rt == 1) GPTQ_GRAD(kBF16, 1); else if (rt == 2) GPTQ_GRAD(kBF16, 2); else GPTQ_GRAD(kBF16, 4); }
-  else { if (rt == 1) GPTQ_GRAD(kF16, 1); else if (rt == 2) GPTQ_GRAD(kF16, 2); else GPTQ_GRAD(kF16, 4); }
+  hipLaunchKernelGGL((grad_kernel<D_, R_>), grid, block, 0, s, terms, places, z, cols, ldz, vec, ad.rank, order, start, count, up, dst, \
+                     items, cb, rb, splits)
+  if (zt == kBF16) { if (rt == 16) GPTQ_GRAD(kBF16, 1); else GPTQ_GRAD(kBF16, 2); }
+  else { if (rt == 16) GPTQ_GRAD(kF16, 1); else GPTQ_GRAD(kF16, 2); }
 #undef GPTQ_GRAD
   if (splits > 1) {
     const int64_t all = (int64_t)ad.m * ad.rank * cols;   // rank is a multiple of 8: whole vectors

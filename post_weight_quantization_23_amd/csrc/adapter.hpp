@@ -420,7 +420,7 @@ void launch_sorted_terms(const float* V, int rank, const int32_t* order, const i
 // G[a][p][j] (up == 0) or G[a][j][p] (up == 1) = sum over a's tokens of
 // V[t][p] Z[t][j], V as sorted terms.  part: workspace of `splits` partial
 // results (splits > 1).
-int adapter_grad_splits(int64_t n, int m, int64_t cols);
+int adapter_grad_splits(int64_t n, int m, int64_t cols, int rank);
 void launch_adapter_grad(const uint16_t* terms, int64_t places, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz,
                          const Adapters& ad, const int32_t* order, const int32_t* start, const int32_t* count, int up, float* G,
                          float* part, int splits, hipStream_t s);

@@ -142,7 +142,7 @@ bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
          n * groups_for(r > c ? r : c, 256) <= kMaxGroups256 * (n > 64 ? 32 : 1) &&      // up
          groups_for(gptq::list_places(n, m) / 8 * (rank > 0 ? rank : 1), 256) <= kMaxGroups256 && gptq::list_places(n, m) < INT_MAX &&  // lists
          m * groups_for(r > c ? r : c, 64) * 2 <= kMaxGroups256 &&                       // transpose (rank <= 128)
-         m * groups_for(r > c ? r : c, 128) * 2 * 16 <= kMaxGroups256 &&                 // gradients (16 splits)
+         m * groups_for(r > c ? r : c, 128) * 16 <= kMaxGroups256 &&                     // gradients (16 splits of 4 rank blocks, 4 a group)
          groups_for(m * rank * (r > c ? r : c), 1024) <= kMaxGroups256;                  // join
 }
 
@@ -158,8 +158,8 @@ struct GradSizes {
 
 GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
   GradSizes z;
-  z.sa = gptq::adapter_grad_splits(n, (int)m, c);
-  z.sb = gptq::adapter_grad_splits(n, (int)m, r);
+  z.sa = gptq::adapter_grad_splits(n, (int)m, c, (int)rank);
+  z.sb = gptq::adapter_grad_splits(n, (int)m, r, (int)rank);
   const int64_t pa = z.sa > 1 ? z.sa * m * rank * c * 4 : 0, pb = z.sb > 1 ? z.sb * m * rank * r * 4 : 0;
   z.part = align256(pa > pb ? pa : pb);
   z.places = gptq::list_places(n, m);

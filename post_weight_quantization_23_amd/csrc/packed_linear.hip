@@ -32,11 +32,12 @@ constexpr int kAhead = 4;   // steps of a wave whose words are requested togethe
 // 16 MT tokens x 16 rows per workgroup.  The waves split the columns in steps
 // of 128 (lane (m, kq): row m, chunk kq of the step's four) and are joined
 // through LDS in wave order; each wave requests the words and rulers of four
-// of its steps before it uses the first (one step at a time waited for memory
-// four times in a row at 4096 columns).
-// WIDE: groups hold whole steps, and the step's four products take word j of
-// every lane's chunk (columns 32 kq + 8 j).  Otherwise the lanes' words are
-// transposed so that product j holds chunk j alone, and rulers apply per chunk.
+// of its steps before it uses the first.  The lanes' blocks of codes are then
+// transposed, so that product j holds chunk j alone and a row's activations are
+// read in runs of 64 bytes.  There are no branches on the way: steps, tokens and
+// rows past the end repeat the last ones, under a scale of zero or with results
+// that are dropped (conditional loads waited for memory one after the other).
+// WIDE: groups hold whole steps, so that rulers apply per step, else per chunk.
 template <int BITS, int DT, int YT, int MT, bool WIDE>
 __global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
   __shared__ float red[kWaves][MT][4][64];
@@ -55,9 +56,13 @@ __global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
   const floatx4 zero4 = {0.f, 0.f, 0.f, 0.f};
   constexpr int RU = WIDE ? 1 : 4;   // rulers per step
 
+  const uint16_t* xrow[MT];
   floatx4 tot[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) tot[i] = zero4;
+  for (int i = 0; i < MT; ++i) {
+    xrow[i] = a.X + min(t0 + 16 * i + m, a.n - 1) * a.ldx;
+    tot[i] = zero4;
+  }
 
   for (int s0 = wave; s0 < steps; s0 += kWaves * kAhead) {
     Chunk<BITS> cw[kAhead];
@@ -70,47 +75,46 @@ __global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
 #pragma unroll
       for (int u = 0; u < RU; ++u) {
         const int g = min(4 * s + u, nch - 1) / a.w.cpg;
-        sc[d][u] = srow[g];
+        const bool in = 4 * s + u < nch;
+        const float v = srow[g];
+        sc[d][u] = in ? v : 0.f;
         ze[d][u] = zrow[g];
       }
     }
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
       const int s = s0 + d * kWaves;
-      if (s >= steps) break;
       uint32_t blk[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) blk[j] = code_block<BITS>(cw[d].w, j);
-      if constexpr (!WIDE) {
-        // register j of lane (m, kq) <-> register kq of lane (m, j)
-        auto swap16 = [](uint32_t& x, uint32_t& y) {
-          const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-          x = r[0];
-          y = r[1];
-        };
-        auto swap32 = [](uint32_t& x, uint32_t& y) {
-          const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-          x = r[0];
-          y = r[1];
-        };
-        swap16(blk[0], blk[1]);
-        swap16(blk[2], blk[3]);
-        swap32(blk[0], blk[2]);
-        swap32(blk[1], blk[3]);
-      }
+      // register j of lane (m, kq) <-> register kq of lane (m, j)
+      auto swap16 = [](uint32_t& x, uint32_t& y) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+        x = r[0];
+        y = r[1];
+      };
+      auto swap32 = [](uint32_t& x, uint32_t& y) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        x = r[0];
+        y = r[1];
+      };
+      swap16(blk[0], blk[1]);
+      swap16(blk[2], blk[3]);
+      swap32(blk[0], blk[2]);
+      swap32(blk[1], blk[3]);
       floatx4 p[MT], xs[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i) p[i] = xs[i] = zero4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const u32x4 w = code_pairs<BITS, DT>(blk[j]);
-        const int xc = WIDE ? 4 * s + kq : 4 * s + j;            // chunk of this lane's activations
-        const int64_t col = 32 * (int64_t)xc + 8 * (WIDE ? j : kq);
+        const bool in = 4 * s + j < nch;
+        const int64_t col = 32 * (int64_t)min(4 * s + j, nch - 1) + 8 * kq;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          const int64_t t = t0 + 16 * i + m;
-          u32x4 x = {0u, 0u, 0u, 0u};
-          if (xc < nch && t < a.n) x = pair_order(*reinterpret_cast<const u32x4*>(a.X + t * a.ldx + col));
+          u32x4 x = *reinterpret_cast<const u32x4*>(xrow[i] + col);
+          if (WIDE && !in) x = u32x4{0u, 0u, 0u, 0u};   // a step's last chunks (wave-uniform)
+          x = pair_order(x);
           p[i] = mfma16<DT>(x, w, p[i]);
           xs[i] = mfma16<DT>(x, ones, xs[i]);
         }
