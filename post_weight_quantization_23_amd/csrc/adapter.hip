@@ -61,7 +61,8 @@ __global__ __launch_bounds__(256) void down_kernel(const uint16_t* __restrict__ 
 // rank rows (operands come from memory in the layout of the product, which
 // reads X once).  The adapters that occur among the tokens are taken in turn;
 // each writes its own tokens' rows.  Waves are joined through LDS in wave
-// order, parts by scale_join_kernel.
+// order (each has a slot there: adding them up in one, wave after wave, took
+// longer than the product), parts by scale_join_kernel.
 // FAST: rows of X start on 16 bytes and hold whole steps; then every load is
 // unconditional (tokens and rank rows past the end repeat the last one, whose
 // results are dropped), so that several steps' loads are in flight.
@@ -69,7 +70,8 @@ template <int DT, int RT, bool FAST>
 __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t d, int64_t ldx, Adapters ad,
                                                          const uint16_t* __restrict__ A, int64_t lda, bool vec, float* __restrict__ S,
                                                          int splits) {
-  __shared__ float red[64][16 * RT + 1];
+  constexpr int LD = 16 * RT + 4;   // floats of a token's row in a slot
+  extern __shared__ __align__(16) float slots[];   // [4][64][LD]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kq = lane >> 4;
   const int64_t tile = blockIdx.x / splits;
@@ -80,11 +82,12 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
   float* out = S + (int64_t)split * n * ad.rank;
   const int mine = adapter_of(ad, t0 + lane, n);
   uint64_t rest = __ballot(mine >= 0);
-  const uint64_t none = ~rest;
-  for (int i = threadIdx.x; i < 64 * ad.rank; i += 256) {
-    const int tok = i / ad.rank;
-    if (((none >> tok) & 1) && t0 + tok < n) out[t0 * ad.rank + i] = 0.f;
-  }
+  // this thread's four rank values of every (64 / RT)-th token
+  const int col = 4 * (threadIdx.x % (4 * RT)), tok0 = threadIdx.x / (4 * RT);
+#pragma unroll
+  for (int tok = tok0; tok < 64; tok += 64 / RT)
+    if (!((rest >> tok) & 1) && t0 + tok < n && col < ad.rank)
+      *reinterpret_cast<floatx4*>(out + (t0 + tok) * ad.rank + col) = floatx4{0.f, 0.f, 0.f, 0.f};
   while (rest) {
     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rest));
     const uint64_t members = __ballot(mine == a);
@@ -120,24 +123,22 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
       step(64 * s + 8 * kq);
       step(64 * s + 32 + 8 * kq);
     }
-    for (int v = 0; v < 4; ++v) {
-      if (wave == v) {
+    float* slot = slots + wave * 64 * LD;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int p = 0; p < RT; ++p)
+      for (int p = 0; p < RT; ++p)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float& r = red[16 * i + 4 * kq + e][16 * p + m];
-              r = v == 0 ? acc[i][p][e] : r + acc[i][p][e];
-            }
-      }
-      __syncthreads();
-    }
+        for (int e = 0; e < 4; ++e) slot[(16 * i + 4 * kq + e) * LD + 16 * p + m] = acc[i][p][e];
+    __syncthreads();
     const float f = splits == 1 && ad.alpha ? ad.alpha[a] : 1.f;
-    for (int i = threadIdx.x; i < 64 * ad.rank; i += 256) {
-      const int tok = i / ad.rank, p = i - tok * ad.rank;
-      if ((members >> tok) & 1) out[t0 * ad.rank + i] = f * red[tok][p];
+#pragma unroll
+    for (int tok = tok0; tok < 64; tok += 64 / RT) {
+      const float* at = slots + tok * LD + col;
+      floatx4 v = *reinterpret_cast<const floatx4*>(at);
+#pragma unroll
+      for (int u = 1; u < 4; ++u) v += *reinterpret_cast<const floatx4*>(at + u * 64 * LD);
+      if (((members >> tok) & 1) && col < ad.rank) *reinterpret_cast<floatx4*>(out + (t0 + tok) * ad.rank + col) = f * v;
     }
     __syncthreads();
   }
@@ -338,7 +339,7 @@ __global__ __launch_bounds__(256) void sorted_terms_kernel(const float* __restri
 // A wave takes 128 columns x 16 RT rank rows and one of `splits` parts of the
 // adapter's tokens, by itself (four waves joined through LDS spent more time
 // there than on their five blocks of tokens); parts are added in order by
-// join_kernel.  The next block's Z is requested before the current one is used.
+// join_kernel.
 template <int DT, int RT>
 __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ terms, int64_t places, const uint16_t* __restrict__ Z,
                                                    int64_t cols, int64_t ldz, bool vec, int rank, const int32_t* __restrict__ order,
@@ -372,38 +373,58 @@ __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ 
   const int blocks = (count + 31) / 32;
   const int each = (blocks + splits - 1) / splits;
   const int b0 = split * each, b1 = min(blocks, (split + 1) * each);
-  auto load_z = [&](int blk, u32x4 (&z)[8]) {
+  // tokens two blocks ahead, their rows of Z and the terms one block ahead
+  struct Operands {
+    u32x4 z[8], v[RT][3];
+  } f0, f1;
+  typedef int int4_t __attribute__((ext_vector_type(4)));
+  int4_t tok[2];
+  const int spare = b0 < b1 ? order[first] : 0;
+  auto load_tokens = [&](int blk) __attribute__((always_inline)) {
+    const int4_t* p = reinterpret_cast<const int4_t*>(order + first + 32 * (int64_t)blk + 8 * kq);   // 32-byte aligned
+    tok[0] = p[0];
+    tok[1] = p[1];
+  };
+  auto load = [&](Operands& f, int blk) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      int t = order[first + 32 * blk + 8 * kq + e];
-      if (t < 0) t = order[first];
-      if (whole) z[e] = *reinterpret_cast<const u32x4*>(Z + (int64_t)t * ldz + j0);
-      else z[e] = load8(Z + (int64_t)t * ldz + j0, valid, vec);
+      int t = tok[e >> 2][e & 3];
+      if (t < 0) t = spare;
+      if (whole) f.z[e] = *reinterpret_cast<const u32x4*>(Z + (int64_t)t * ldz + j0);
+      else f.z[e] = load8(Z + (int64_t)t * ldz + j0, valid, vec);
     }
-  };
-  u32x4 z[8];
-  if (b0 < b1) load_z(b0, z);
-  for (int blk = b0; blk < b1; ++blk) {
-    u32x4 vt[RT][3], next[8];
 #pragma unroll
     for (int p = 0; p < RT; ++p)
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        vt[p][k] = *reinterpret_cast<const u32x4*>(terms + ((int64_t)k * rank + min(p0 + 16 * p + m, rank - 1)) * places + first +
-                                                   32 * blk + 8 * kq);
-    if (blk + 1 < b1) load_z(blk + 1, next);
+        f.v[p][k] = *reinterpret_cast<const u32x4*>(terms + ((int64_t)k * rank + min(p0 + 16 * p + m, rank - 1)) * places + first +
+                                                    32 * (int64_t)blk + 8 * kq);
+    if (blk + 1 < b1) load_tokens(blk + 1);
+  };
+  auto use = [&](const Operands& f) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      u32x4 f;
+      u32x4 c;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        f[e] = __builtin_amdgcn_perm(z[2 * e + 1][u >> 1], z[2 * e][u >> 1], (u & 1) ? 0x07060302u : 0x05040100u);
-      const Terms16<DT> zt(f);
+        c[e] = __builtin_amdgcn_perm(f.z[2 * e + 1][u >> 1], f.z[2 * e][u >> 1], (u & 1) ? 0x07060302u : 0x05040100u);
+      const Terms16<DT> zt(c);
 #pragma unroll
-      for (int p = 0; p < RT; ++p) acc[p][u] = mfma_terms<DT, 3>(vt[p], zt, acc[p][u]);
+      for (int p = 0; p < RT; ++p) acc[p][u] = mfma_terms<DT, 3>(f.v[p], zt, acc[p][u]);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = next[e];
+  };
+  int blk = b0;
+  if (blk < b1) {
+    load_tokens(blk);
+    load(f0, blk);
+  }
+  while (blk < b1) {
+    if (blk + 1 < b1) load(f1, blk + 1);
+    use(f0);
+    if (++blk >= b1) break;
+    if (blk + 1 < b1) load(f0, blk + 1);
+    use(f1);
+    ++blk;
   }
 
   // row of the accumulator = rank, column = 8 (lane & 15) + u
@@ -460,6 +481,17 @@ constexpr int64_t kUpTokens = 64;
 
 }  // namespace
 
+template <int DT, int RT, bool FAST, class... Args>
+static void launch_down_tiles(dim3 grid, hipStream_t s, Args... args) {
+  constexpr int LDS = 4 * 64 * (16 * RT + 4) * 4;
+  static const bool set = [] {   // once, thread-safe
+    (void)hipFuncSetAttribute((const void*)down_tiles_kernel<DT, RT, FAST>, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+    return true;
+  }();
+  (void)set;
+  hipLaunchKernelGGL((down_tiles_kernel<DT, RT, FAST>), grid, dim3(256), LDS, s, args...);
+}
+
 int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank) {
   const int64_t one = (n * rank + 63) / 64 * 64;
   const int splits = n < kDownTiles ? 1 : down_splits(n, d);
@@ -480,11 +512,9 @@ void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ld
   const int splits = down_splits(n, d);
   float* out = splits == 1 ? S : S + (n * ad.rank + 63) / 64 * 64;
   const dim3 grid((unsigned)((n + 63) / 64 * splits));
-#define GPTQ_DOWN(D_, R_)                                                                                                          \
-  do {                                                                                                                             \
-    if (vec && d % 64 == 0) hipLaunchKernelGGL((down_tiles_kernel<D_, R_, true>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits); \
-    else hipLaunchKernelGGL((down_tiles_kernel<D_, R_, false>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, out, splits);     \
-  } while (0)
+#define GPTQ_DOWN(D_, R_)                                                                                                    \
+  (vec && d % 64 == 0 ? launch_down_tiles<D_, R_, true>(grid, s, x, n, d, ldx, ad, A, lda, vec, out, splits)                 \
+                      : launch_down_tiles<D_, R_, false>(grid, s, x, n, d, ldx, ad, A, lda, vec, out, splits))
 #define GPTQ_DOWN_R(D_)                     \
   do {                                      \
     if (ad.rank <= 16) GPTQ_DOWN(D_, 1);    \
@@ -539,7 +569,7 @@ int grad_rows(int rank) { return rank <= 16 ? 16 : 32; }
 int adapter_grad_splits(int64_t n, int m, int64_t cols, int rank) {
   const int64_t waves = (cols + 127) / 128 * m * ((rank + grad_rows(rank) - 1) / grad_rows(rank));
   int64_t splits = (2048 + waves - 1) / waves;
-  const int64_t most = n / m / (32 * 4);   // four blocks of tokens at least
+  const int64_t most = (n + m - 1) / m / 64;   // two blocks of tokens each
   splits = splits < most ? splits : most;
   return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
 }
