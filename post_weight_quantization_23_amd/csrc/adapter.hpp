@@ -31,6 +31,10 @@ struct PackedLayer {
   int bits;
   int r, c;
   int cpg;                // 32-column chunks per group (all of them: one ruler per row)
+  int shift;              // log2 of cpg, 31 for one group, -1 where it is neither
+
+  // Group of a chunk (a division by a variable is some twenty instructions).
+  GPTQ_DEV int group(int chunk) const { return shift >= 0 ? chunk >> shift : chunk / cpg; }
 };
 
 // ---------------------------------------------------------------- 16-bit values
@@ -353,18 +357,25 @@ GPTQ_DEV Chunk<BITS> load_chunk(const uint32_t* words, int ch) {
 
 // Codes t and t + 4 of a block of eight, t = 0 .. 3, as pairs of 16-bit floats
 // 2^BITS + q.
+// exponent: code_exponent() in a vector register, so that mask and exponent are
+// one instruction (its other constant, the mask, takes the one scalar operand).
 template <int BITS, int DT>
-GPTQ_DEV u32x4 code_pairs(uint32_t blk) {
+GPTQ_DEV uint32_t code_exponent() {
+  uint32_t v = (DT == kBF16 ? 0x3F80u + (BITS << 7) : 0x3C00u + (BITS << 10)) * 0x10001u;
+  asm volatile("" : "+v"(v));
+  return v;
+}
+template <int BITS, int DT>
+GPTQ_DEV u32x4 code_pairs(uint32_t blk, uint32_t exponent) {
   constexpr int P = (DT == kBF16 ? 7 : 10) - BITS;   // lowest bit of the code in the mantissa
-  constexpr uint32_t one = DT == kBF16 ? (0x3F80u + (BITS << 7)) : (0x3C00u + (BITS << 10));
-  constexpr uint32_t mask = (((1u << BITS) - 1) << P) * 0x10001u, magic = one * 0x10001u;
+  constexpr uint32_t mask = (((1u << BITS) - 1) << P) * 0x10001u;
   if constexpr (BITS == 3) blk = (blk & 0xFFFu) | ((blk & 0xFFF000u) << 4);   // codes 4 .. 7 to the high half
   u32x4 v;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     constexpr int B = BITS;
     const int sh = P - B * t;
-    v[t] = ((sh >= 0 ? blk << sh : blk >> -sh) & mask) | magic;
+    v[t] = ((sh >= 0 ? blk << sh : blk >> -sh) & mask) | exponent;
   }
   return v;
 }

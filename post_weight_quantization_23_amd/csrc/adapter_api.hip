@@ -104,6 +104,7 @@ gptq::PackedLayer layer(const uint32_t* packed, int64_t r, int64_t c, int bits, 
   w.r = (int)r;
   w.c = (int)c;
   w.cpg = groupsize > 0 && groupsize < c ? (int)(groupsize / 32) : (int)(c / 32);
+  w.shift = w.cpg == c / 32 ? 31 : ((w.cpg & (w.cpg - 1)) == 0 ? __builtin_ctz((unsigned)w.cpg) : -1);
   return w;
 }
 

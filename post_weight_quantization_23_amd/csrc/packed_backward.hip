@@ -28,7 +28,7 @@ __global__ __launch_bounds__(256) void dequant_t_kernel(PackedLayer w, uint16_t*
   const int64_t i0 = rt * 64 + 8 * (threadIdx.x & 7);
   const int gb = (int)ct * 32 + (threadIdx.x >> 3);      // block of eight columns
   if (gb * 8 >= w.c) return;
-  const int g = (gb >> 2) / w.cpg;
+  const int g = w.group(gb >> 2);
   uint32_t blk[8];
   float sc[8], ze[8];
 #pragma unroll

@@ -15,6 +15,8 @@ namespace gptq {
 
 namespace {
 
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+
 struct FwdArgs {
   const uint16_t* X;
   int64_t ldx, n;
@@ -24,132 +26,189 @@ struct FwdArgs {
   void* Y;
   int64_t ldy;
   int row_tiles;
+  int quads;         // tokens of a workgroup in fours, at most four
 };
 
-constexpr int kWaves = 8;
-constexpr int kAhead = 4;   // steps of a wave whose words are requested together
+// Register j of lane (m, kq) <-> register kq of lane (m, j), lane = m + 16 kq.
+GPTQ_DEV void transpose4(uint32_t (&v)[4]) {
+  auto swap16 = [](uint32_t& x, uint32_t& y) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    x = r[0];
+    y = r[1];
+  };
+  auto swap32 = [](uint32_t& x, uint32_t& y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    x = r[0];
+    y = r[1];
+  };
+  swap16(v[0], v[1]);
+  swap16(v[2], v[3]);
+  swap32(v[0], v[2]);
+  swap32(v[1], v[3]);
+}
 
-// 16 MT tokens x 16 rows per workgroup.  The waves split the columns in steps
-// of 128 (lane (m, kq): row m, chunk kq of the step's four) and are joined
-// through LDS in wave order; each wave requests the words and rulers of four
-// of its steps before it uses the first.  The lanes' blocks of codes are then
-// transposed, so that product j holds chunk j alone and a row's activations are
-// read in runs of 64 bytes.  There are no branches on the way: steps, tokens and
-// rows past the end repeat the last ones, under a scale of zero or with results
-// that are dropped (conditional loads waited for memory one after the other).
-// WIDE: groups hold whole steps, so that rulers apply per step, else per chunk.
-template <int BITS, int DT, int YT, int MT, bool WIDE>
-__global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
-  __shared__ float red[kWaves][MT][4][64];
+constexpr int kWaves = 8, kAhead = 2;   // waves of a workgroup, steps of a run
+
+// LDS bytes of a step of one wave: 16 rows of words, then 4 ceil(n / 4) tokens of
+// 256 bytes.
+template <int BITS>
+constexpr int step_bytes(int quads) { return 256 * BITS + 1024 * quads; }
+
+// 16 tokens x 16 rows per workgroup.  The waves split the columns in runs of two
+// steps of 128 and are joined through LDS in wave order.
+//
+// What a run reads comes through the wave's own part of LDS, by loads that write
+// it.  The operand layout gives consecutive lanes consecutive rows, so loading
+// operands straight into registers touches 64 places of 16 bytes per
+// instruction, and the L1 cache takes them one a cycle: that, not memory, set the
+// pace (16 tokens of 11008 x 4096 at 3 bits: 22 us, and 40 thousand accesses
+// per CU).  The loads into LDS give 4 (words) or 16 (activations) consecutive
+// lanes one row.
+//
+// A lane then holds chunk kq of row m (lane = m + 16 kq); the blocks of codes are
+// transposed, so that product j takes chunk j alone.  Steps, tokens and rows past
+// the end repeat the last ones, under a scale of zero or with results that are
+// dropped.  WIDE: groups hold whole steps, so that rulers apply per step;
+// otherwise each lane reads its own chunk's ruler, and the transpose spreads
+// them as well.
+template <int BITS, int DT, int YT, bool WIDE>
+GPTQ_DEV void rows16_body(const FwdArgs& a, unsigned char* smem) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kq = lane >> 4;
   const int64_t tile = blockIdx.x / a.row_tiles;
-  const int64_t t0 = tile * 16 * MT;
+  const int64_t t0 = tile * 16;
   const int row0 = (int)(blockIdx.x - tile * a.row_tiles) * 16;
-  const int row = min(row0 + m, a.w.r - 1);
   const int nch = a.w.c >> 5, steps = (nch + 3) >> 2;
-  const uint32_t* words = a.w.words + (int64_t)row * a.w.ldw;
+  const int row = min(row0 + m, a.w.r - 1);
   const float* srow = a.w.scales + (int64_t)row * a.w.ldg;
   const int32_t* zrow = a.w.zeros + (int64_t)row * a.w.ldg;
   const uint32_t one = DT == kBF16 ? 0x3F803F80u : 0x3C003C00u;
   const u32x4 ones = {one, one, one, one};
+  const uint32_t exponent = code_exponent<BITS, DT>();
   const floatx4 zero4 = {0.f, 0.f, 0.f, 0.f};
-  constexpr int RU = WIDE ? 1 : 4;   // rulers per step
 
-  const uint16_t* xrow[MT];
-  floatx4 tot[MT];
+  const int sb = step_bytes<BITS>(a.quads);
+  unsigned char* own = smem + wave * kAhead * sb;
+  lds_u8* lown = (lds_u8*)own;
+
+  // Global sources of this lane: words (4 bits: piece lane & 3 of row lane >> 2;
+  // 3 bits: dwords lane, lane + 64, lane + 128 of the step's 16 x 12), tokens
+  // (piece lane & 15 of tokens lane >> 4, + 4, ...).  Pieces are permuted by the
+  // row, so that operand reads spread over the banks.
+  constexpr int WL = BITS == 4 ? 1 : 3;
+  const uint32_t* wsrc[WL];
+  int wcol[WL];    // chunk of the step (4 bits), dword of the step (3 bits)
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    xrow[i] = a.X + min(t0 + 16 * i + m, a.n - 1) * a.ldx;
-    tot[i] = zero4;
+  for (int i = 0; i < WL; ++i) {
+    const int at = lane + 64 * i, rr = BITS == 4 ? at >> 2 : at / 12;
+    wsrc[i] = a.w.words + (int64_t)min(row0 + rr, a.w.r - 1) * a.w.ldw;
+    wcol[i] = BITS == 4 ? (at & 3) ^ ((rr >> 2) & 3) : at % 12;
+  }
+  const uint16_t* xsrc[4];
+  int xpiece[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rr = 4 * i + (lane >> 4);
+    xsrc[i] = a.X + min(t0 + rr, a.n - 1) * a.ldx;
+    xpiece[i] = (lane & 15) ^ (rr & 15);
   }
 
-  for (int s0 = wave; s0 < steps; s0 += kWaves * kAhead) {
-    Chunk<BITS> cw[kAhead];
-    float sc[kAhead][RU];
-    int ze[kAhead][RU];
+  floatx4 tot = zero4;
+  for (int s0 = kAhead * wave; s0 < steps; s0 += kWaves * kAhead) {
+    float sc[kAhead];
+    int ze[kAhead];
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
-      const int s = s0 + d * kWaves;
-      cw[d] = load_chunk<BITS>(words, min(4 * s + kq, nch - 1));
+      const int s = s0 + d;
+      lds_u8* to = lown + d * sb;
 #pragma unroll
-      for (int u = 0; u < RU; ++u) {
-        const int g = min(4 * s + u, nch - 1) / a.w.cpg;
-        const bool in = 4 * s + u < nch;
-        const float v = srow[g];
-        sc[d][u] = in ? v : 0.f;
-        ze[d][u] = zrow[g];
+      for (int i = 0; i < WL; ++i) {
+        if constexpr (BITS == 4)
+          __builtin_amdgcn_global_load_lds((const void __attribute__((address_space(1)))*)(wsrc[i] + 4 * (int64_t)min(4 * s + wcol[i], nch - 1)),
+                                           (void __attribute__((address_space(3)))*)to, 16, 0, 0);
+        else
+          __builtin_amdgcn_global_load_lds((const void __attribute__((address_space(1)))*)(wsrc[i] + min(12 * (int64_t)s + wcol[i], 3 * (int64_t)nch - 1)),
+                                           (void __attribute__((address_space(3)))*)(to + 256 * i), 4, 0, 0);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < a.quads)
+          __builtin_amdgcn_global_load_lds((const void __attribute__((address_space(1)))*)(xsrc[i] + 8 * (int64_t)min(16 * s + xpiece[i], 4 * nch - 1)),
+                                           (void __attribute__((address_space(3)))*)(to + 256 * BITS + 1024 * i), 16, 0, 0);
+      const int g = a.w.group(min(4 * s + (WIDE ? 0 : kq), nch - 1));
+      sc[d] = srow[g];
+      ze[d] = zrow[g];
     }
+    __builtin_amdgcn_s_waitcnt(0);   // the wave reads only what it has loaded itself
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
-      const int s = s0 + d * kWaves;
-      uint32_t blk[4];
+      const int s = s0 + d;
+      const unsigned char* from = own + d * sb;
+      uint32_t chunk[BITS], blk[4], scs[4], zes[4];
+      if constexpr (BITS == 4) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(from + m * 64 + ((kq ^ ((m >> 2) & 3)) << 4));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) blk[j] = code_block<BITS>(cw[d].w, j);
-      // register j of lane (m, kq) <-> register kq of lane (m, j)
-      auto swap16 = [](uint32_t& x, uint32_t& y) {
-        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-        x = r[0];
-        y = r[1];
-      };
-      auto swap32 = [](uint32_t& x, uint32_t& y) {
-        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-        x = r[0];
-        y = r[1];
-      };
-      swap16(blk[0], blk[1]);
-      swap16(blk[2], blk[3]);
-      swap32(blk[0], blk[2]);
-      swap32(blk[1], blk[3]);
-      floatx4 p[MT], xs[MT];
+        for (int i = 0; i < 4; ++i) chunk[i] = v[i];
+      } else {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) p[i] = xs[i] = zero4;
+        for (int i = 0; i < 3; ++i) chunk[i] = *reinterpret_cast<const uint32_t*>(from + m * 48 + kq * 12 + 4 * i);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const u32x4 w = code_pairs<BITS, DT>(blk[j]);
+        blk[j] = code_block<BITS>(chunk, j);
+        scs[j] = __float_as_uint(sc[d]);
+        zes[j] = (uint32_t)ze[d];
+      }
+      transpose4(blk);
+      if constexpr (!WIDE) {
+        transpose4(scs);
+        transpose4(zes);
+      }
+      floatx4 p = zero4, xs = zero4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
         const bool in = 4 * s + j < nch;
-        const int64_t col = 32 * (int64_t)min(4 * s + j, nch - 1) + 8 * kq;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          u32x4 x = *reinterpret_cast<const u32x4*>(xrow[i] + col);
-          if (WIDE && !in) x = u32x4{0u, 0u, 0u, 0u};   // a step's last chunks (wave-uniform)
-          x = pair_order(x);
-          p[i] = mfma16<DT>(x, w, p[i]);
-          xs[i] = mfma16<DT>(x, ones, xs[i]);
-        }
+        u32x4 x = *reinterpret_cast<const u32x4*>(from + 256 * BITS + m * 256 + (((4 * j + kq) ^ m) << 4));
+        if (WIDE && !in) x = u32x4{0u, 0u, 0u, 0u};   // a step's last chunks
+        x = pair_order(x);
+        xs = mfma16<DT>(x, ones, xs);
+        p = mfma16<DT>(x, code_pairs<BITS, DT>(blk[j], exponent), p);
         if (!WIDE || j == 3) {
-          const float scale = sc[d][WIDE ? 0 : j], off = (float)(1 << BITS) + (float)ze[d][WIDE ? 0 : j];
+          const float scale = (WIDE ? 4 * s < nch : in) ? __uint_as_float(scs[j]) : 0.f;
+          const float off = (float)(1 << BITS) + (float)(int)zes[j];
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) tot[i][e] = __builtin_fmaf(scale, __builtin_fmaf(-off, xs[i][e], p[i][e]), tot[i][e]);
-            p[i] = xs[i] = zero4;
-          }
+          for (int e = 0; e < 4; ++e) tot[e] = __builtin_fmaf(scale, __builtin_fmaf(-off, xs[e], p[e]), tot[e]);
+          p = xs = zero4;
         }
       }
     }
   }
 
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[wave][i][e][lane] = tot[i][e];
   __syncthreads();
-  // an output per thread: 16 tokens x 16 rows of the accumulators' layout
+  float* red = reinterpret_cast<float*>(smem);   // [wave][e][lane]
 #pragma unroll
-  for (int o = threadIdx.x; o < 256 * MT; o += 64 * kWaves) {
-    const int tok = o >> 4, i = tok >> 4, e = tok & 3, l = ((tok >> 2) & 3) * 16 + (o & 15);
+  for (int e = 0; e < 4; ++e) red[(wave * 4 + e) * 64 + lane] = tot[e];
+  __syncthreads();
+  // an output per thread of the first four waves: 16 tokens x 16 rows of the accumulators' layout
+  if (threadIdx.x < 256) {
+    const int tok = threadIdx.x >> 4, l = (tok >> 2) * 16 + (threadIdx.x & 15);
     const int64_t t = t0 + tok;
-    const int out = row0 + (o & 15);
-    if (t >= a.n || out >= a.w.r) continue;
-    float v = red[0][i][e][l];
+    const int out = row0 + (threadIdx.x & 15);
+    if (t >= a.n || out >= a.w.r) return;
+    float v = red[(tok & 3) * 64 + l];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += red[w][i][e][l];
+    for (int w = 1; w < kWaves; ++w) v += red[(w * 4 + (tok & 3)) * 64 + l];
     const int ad = a.S ? adapter_of(a.ad, t, a.n) : -1;
     if (ad >= 0) v += rank_dot<DT>(a.S + t * a.ad.rank, a.ad.B + ((int64_t)ad * a.w.r + out) * a.ad.rank, a.ad.rank);
     store_out<YT>(a.Y, t * a.ldy + out, v);
   }
+}
+
+template <int BITS, int DT, int YT, bool WIDE>
+__global__ __launch_bounds__(64 * kWaves) void rows16_kernel(FwdArgs a) {
+  extern __shared__ __align__(16) unsigned char rsm[];
+  rows16_body<BITS, DT, YT, WIDE>(a, rsm);
 }
 
 __global__ __launch_bounds__(256) void gather_columns_kernel(const uint16_t* __restrict__ X, int64_t c, int64_t ldx,
@@ -168,19 +227,22 @@ __global__ __launch_bounds__(256) void gather_columns_kernel(const uint16_t* __r
   *reinterpret_cast<u32x4*>(dst + t * c + j) = v;
 }
 
-template <int BITS, int DT, int YT, int MT>
+template <int BITS, int DT, int YT, bool WIDE>
 void launch_rows16(const FwdArgs& a, hipStream_t s) {
-  const int64_t tiles = (a.n + 16 * MT - 1) / (16 * MT);
-  const dim3 grid((unsigned)(tiles * a.row_tiles)), block(64 * kWaves);
-  if (a.w.cpg % 4 == 0 || a.w.cpg >= (a.w.c >> 5)) hipLaunchKernelGGL((rows16_kernel<BITS, DT, YT, MT, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((rows16_kernel<BITS, DT, YT, MT, false>), grid, block, 0, s, a);
+  static const bool set = [] {   // once, thread-safe
+    (void)hipFuncSetAttribute((const void*)rows16_kernel<BITS, DT, YT, WIDE>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                              kWaves * kAhead * step_bytes<BITS>(4));
+    return true;
+  }();
+  (void)set;
+  hipLaunchKernelGGL((rows16_kernel<BITS, DT, YT, WIDE>), dim3((unsigned)((a.n + 15) / 16 * a.row_tiles)), dim3(64 * kWaves),
+                     kWaves * kAhead * step_bytes<BITS>(a.quads), s, a);
 }
 
 template <int BITS, int DT, int YT>
 void launch_forward(const FwdArgs& a, hipStream_t s) {
-  if (a.n <= 16) launch_rows16<BITS, DT, YT, 1>(a, s);
-  else if (a.n <= 32) launch_rows16<BITS, DT, YT, 2>(a, s);
-  else launch_rows16<BITS, DT, YT, 4>(a, s);
+  if (a.w.cpg % 4 == 0 || a.w.shift == 31) launch_rows16<BITS, DT, YT, true>(a, s);
+  else launch_rows16<BITS, DT, YT, false>(a, s);
 }
 
 }  // namespace
@@ -203,6 +265,7 @@ void launch_packed_linear(const void* X, int xt, int64_t n, int64_t ldx, const P
   a.Y = Y;
   a.ldy = ldy;
   a.row_tiles = (w.r + 15) / 16;
+  a.quads = n >= 16 ? 4 : (int)((n + 3) / 4);
 #define GPTQ_FWD(B_)                                                                          \
   do {                                                                                        \
     if (xt == kBF16) { if (yt == 0) launch_forward<B_, kBF16, 0>(a, s); else launch_forward<B_, kBF16, kBF16>(a, s); } \

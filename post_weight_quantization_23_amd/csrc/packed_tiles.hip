@@ -133,7 +133,7 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
       cw[q][1] = load_chunk<BITS>(words[q], min(4 * s + 2 * h + 1, nch - 1));
 #pragma unroll
       for (int u = 0; u < RU; ++u) {
-        const int g = min(4 * s + CPS * u, nch - 1) / a.w.cpg;
+        const int g = a.w.group(min(4 * s + CPS * u, nch - 1));
         sc[q][u] = srow[q][g];
         ze[q][u] = zrow[q][g];
       }
@@ -292,7 +292,7 @@ __global__ __launch_bounds__(256) void prepare_tokens_kernel(const uint16_t* __r
 template <int BITS, int MT>
 void launch_tiles(const TileArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.tok_tiles * a.row_tiles * a.splits)), block(256);
-  if (a.w.cpg % 4 == 0 || a.w.cpg >= (a.w.c >> 5)) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 4>), grid, block, 0, s, a);
+  if (a.w.cpg % 4 == 0 || a.w.shift == 31) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 4>), grid, block, 0, s, a);
   else if (a.w.cpg % 2 == 0) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 2>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((tiles_kernel<BITS, MT, 1>), grid, block, 0, s, a);
 }
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(256) void dequant_rows_kernel(PackedLayer w, uint16
   for (int b = threadIdx.x & 63; 8 * b < kp; b += 64) {
     u32x4 o = {0u, 0u, 0u, 0u};
     if (8 * b < w.c) {
-      const int g = (b >> 2) / w.cpg;
+      const int g = w.group(b >> 2);
       const float z = (float)zrow[g], sc = srow[g];
       const uint32_t blk = BITS == 4 ? words[b] : straddling_block(words, b);
 #pragma unroll
