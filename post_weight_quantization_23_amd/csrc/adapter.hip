@@ -80,14 +80,18 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
   const int64_t steps = (d + 63) / 64, per = (steps + splits - 1) / splits;
   const int64_t s1 = min(steps, (split + 1) * per);
   float* out = S + (int64_t)split * n * ad.rank;
-  const int mine = adapter_of(ad, t0 + lane, n);
+  const int64_t lane_token = ad.token(t0 + lane, n);
+  const int mine = adapter_of(ad, lane_token, n);
   uint64_t rest = __ballot(mine >= 0);
   // this thread's four rank values of every (64 / RT)-th token
   const int col = 4 * (threadIdx.x % (4 * RT)), tok0 = threadIdx.x / (4 * RT);
 #pragma unroll
   for (int tok = tok0; tok < 64; tok += 64 / RT)
     if (!((rest >> tok) & 1) && t0 + tok < n && col < ad.rank)
-      *reinterpret_cast<floatx4*>(out + (t0 + tok) * ad.rank + col) = floatx4{0.f, 0.f, 0.f, 0.f};
+      *reinterpret_cast<floatx4*>(out + ad.token(t0 + tok, n) * ad.rank + col) = floatx4{0.f, 0.f, 0.f, 0.f};
+  const uint16_t* xrow[4];   // tokens past the end repeat the last one
+#pragma unroll
+  for (int i = 0; i < 4; ++i) xrow[i] = X + ad.token(min(t0 + 16 * i + m, n - 1), n) * ldx;
   while (rest) {
     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rest));
     const uint64_t members = __ballot(mine == a);
@@ -102,10 +106,9 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
       u32x4 x[4], b[RT];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t t = t0 + 16 * i + m;
         x[i] = u32x4{0u, 0u, 0u, 0u};
-        if constexpr (FAST) x[i] = *reinterpret_cast<const u32x4*>(X + min(t, n - 1) * ldx + k);
-        else if (t < n && k < d) x[i] = load8(X + t * ldx + k, (int)min((int64_t)8, d - k), vec);
+        if constexpr (FAST) x[i] = *reinterpret_cast<const u32x4*>(xrow[i] + k);
+        else if (k < d) x[i] = load8(xrow[i] + k, (int)min((int64_t)8, d - k), vec);
       }
 #pragma unroll
       for (int p = 0; p < RT; ++p) {
@@ -138,7 +141,7 @@ __global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restr
       floatx4 v = *reinterpret_cast<const floatx4*>(at);
 #pragma unroll
       for (int u = 1; u < 4; ++u) v += *reinterpret_cast<const floatx4*>(at + u * 64 * LD);
-      if (((members >> tok) & 1) && col < ad.rank) *reinterpret_cast<floatx4*>(out + (t0 + tok) * ad.rank + col) = f * v;
+      if (((members >> tok) & 1) && col < ad.rank) *reinterpret_cast<floatx4*>(out + ad.token(t0 + tok, n) * ad.rank + col) = f * v;
     }
     __syncthreads();
   }
@@ -177,7 +180,7 @@ GPTQ_DEV void add_base(const UpArgs& u, float (&v)[8], int64_t t, int64_t j, int
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += __builtin_ldexpf(sum[e], u.ex[t]);
+    for (int e = 0; e < 8; ++e) v[e] += u.ex ? __builtin_ldexpf(sum[e], u.ex[t]) : sum[e];
   } else if (u.base) {
     if constexpr (YT == 0) {
       const float* p = static_cast<const float*>(u.base) + t * u.ldb + j;
@@ -218,7 +221,7 @@ __global__ __launch_bounds__(256) void up_tiles_kernel(UpArgs u) {
     acc[q] = floatx16{};
   }
   if (u.S) expand_add<DT, YT == 0 ? 3 : 2, 2>(u.ad, u.B, u.rows, u.S, t0, u.n, row, acc);
-  store_tile<YT, 2>(turn[wave], acc, u.out, t0, u.n, j0, u.rows, u.ldo, u.vec_out,
+  store_tile<YT, 2>(turn[wave], acc, u.ad, u.out, t0, u.n, j0, u.rows, u.ldo, u.vec_out,
                     [&](float (&v)[8], int64_t t, int64_t j, int k) { add_base<YT>(u, v, t, j, k); });
 }
 
@@ -303,6 +306,41 @@ __global__ __launch_bounds__(1024) void token_lists_kernel(Adapters ad, int64_t 
     start[a] = (int32_t)first;
     counts[a] = mine;
     if (a == ad.m - 1) start[a + 1] = (int32_t)next;
+  }
+}
+
+// All tokens by adapter, ascending, those without one last: workgroup a places the
+// tokens of adapter a (a == m: without) after those of the adapters before it.
+__global__ __launch_bounds__(1024) void token_order_kernel(Adapters ad, int64_t n, int32_t* __restrict__ order) {
+  __shared__ int below[16];
+  __shared__ int count[16];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const uint32_t a = blockIdx.x;   // as the unsigned adapter of a token, none being m
+  auto key = [&](int64_t t) { return min((uint32_t)adapter_of(ad, t, n), (uint32_t)ad.m); };
+  int less = 0;
+  for (int64_t t = threadIdx.x; t < n; t += 1024) less += key(t) < a;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) less += __shfl_xor(less, m);
+  if (lane == 0) below[w] = less;
+  __syncthreads();
+  int64_t at = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) at += below[i];
+  for (int64_t t0 = 0; t0 < n; t0 += 1024) {
+    const int64_t t = t0 + threadIdx.x;
+    const bool in = t < n && key(t) == a;
+    const uint64_t mask = __ballot(in);
+    if (lane == 0) count[w] = __popcll(mask);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      before += i < w ? count[i] : 0;
+      all += count[i];
+    }
+    if (in) order[at + before + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)t;
+    at += all;
+    __syncthreads();
   }
 }
 
@@ -473,11 +511,9 @@ int down_splits(int64_t n, int64_t d) {
   return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
 }
 
-// Tokens from which down_tiles_kernel is faster than a wave per value.
-constexpr int64_t kDownTiles = 64;
-
-// Tokens up to which up_kernel is faster than tiles.
-constexpr int64_t kUpTokens = 64;
+// Whether each token is taken by itself: a few of them, or so many adapters that a
+// tile would hold ten and more.
+bool by_token(int64_t n, int m) { return n <= 64 || n <= 4 * (int64_t)m; }
 
 }  // namespace
 
@@ -494,7 +530,7 @@ static void launch_down_tiles(dim3 grid, hipStream_t s, Args... args) {
 
 int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank) {
   const int64_t one = (n * rank + 63) / 64 * 64;
-  const int splits = n < kDownTiles ? 1 : down_splits(n, d);
+  const int splits = n <= 64 ? 1 : down_splits(n, d);
   return splits == 1 ? one : one + splits * n * rank;
 }
 
@@ -503,7 +539,7 @@ void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ld
   const dim3 block(256);
   const bool vec = rows_on_16(X, ldx, xt);
   const auto* x = static_cast<const uint16_t*>(X);
-  if (n < kDownTiles) {
+  if (by_token(n, ad.m)) {
     const dim3 grid((unsigned)((n * ad.rank + 3) / 4));
     if (xt == kBF16) hipLaunchKernelGGL((down_kernel<kBF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
     else hipLaunchKernelGGL((down_kernel<kF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
@@ -535,7 +571,7 @@ void launch_adapter_up(const UpArgs& given, int xt, int yt, hipStream_t s) {
   u.col_tiles = (u.rows + 255) / 256;
   u.vec_base = u.part ? rows_on_16(u.part, u.rows, 0) : rows_on_16(u.base, u.ldb, yt);
   u.vec_out = rows_on_16(u.out, u.ldo, yt);
-  const bool few = u.n <= kUpTokens;
+  const bool few = u.n <= 64 || (u.S && by_token(u.n, u.ad.m));
   const dim3 grid((unsigned)((few ? u.n : (u.n + 31) / 32) * u.col_tiles)), block(256);
 #define GPTQ_UP(D_, Y_)                                                                \
   do {                                                                                 \
@@ -553,6 +589,12 @@ void launch_transpose16(const uint16_t* src, int m, int64_t rows, int64_t cols, 
                      ldd, rt);
 }
 
+bool adapters_want_order(int64_t n, int m, const int32_t* index) { return index && m > 1 && !by_token(n, m); }
+
+void launch_token_order(const Adapters& ad, int64_t n, int32_t* order, hipStream_t s) {
+  hipLaunchKernelGGL(token_order_kernel, dim3((unsigned)ad.m + 1), dim3(1024), 0, s, ad, n, order);
+}
+
 void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, int32_t* count, hipStream_t s) {
   hipLaunchKernelGGL(token_lists_kernel, dim3((unsigned)ad.m), dim3(1024), 0, s, ad, n, order, start, count);
 }
@@ -567,6 +609,7 @@ void launch_sorted_terms(const float* V, int rank, const int32_t* order, const i
 int grad_rows(int rank) { return rank <= 16 ? 16 : 32; }
 
 int adapter_grad_splits(int64_t n, int m, int64_t cols, int rank) {
+  if (n == 0 || cols == 0) return 1;
   const int64_t waves = (cols + 127) / 128 * m * ((rank + grad_rows(rank) - 1) / grad_rows(rank));
   int64_t splits = (2048 + waves - 1) / waves;
   const int64_t most = (n + m - 1) / m / 64;   // two blocks of tokens each

@@ -18,6 +18,10 @@ struct Adapters {
   const float* alpha;     // null: 1
   const int32_t* index;   // null: adapter 0 for every token
   int m, rank;
+  const int32_t* order;   // null, or all tokens in the order of their adapters
+
+  // Token at a place of a tile; the places past the last token have none (-1).
+  GPTQ_DEV int64_t token(int64_t place, int64_t n) const { return place >= n ? -1 : (order ? (int64_t)order[place] : place); }
 };
 
 // A packed layer as gptq_pack / gptq_quantize_layer write it.
@@ -113,7 +117,7 @@ struct TileShape<floatx16> {
 // ---------------------------------------------------------------- adapters
 // Adapter of token t, or -1.
 GPTQ_DEV int adapter_of(const Adapters& ad, int64_t t, int64_t n) {
-  if (t >= n) return -1;
+  if (t < 0 || t >= n) return -1;
   const int a = ad.index ? ad.index[t] : 0;
   return (uint32_t)a < (uint32_t)ad.m ? a : -1;
 }
@@ -208,20 +212,21 @@ GPTQ_DEV float rank_dot(const float* S, const uint16_t* b, int rank) {
   return sum;
 }
 
-// out[q] += (S B_a^T) of the tile's tokens t0 .. and NT sets of its outputs, in
-// the accumulator layout (row = token): the low-rank product beside a tile.
+// out[q] += (S B_a^T) of the tokens at places t0 .. and NT sets of a tile's outputs, in
+// the accumulator layout (row = place): the low-rank product beside a tile.
 // S [n][rank] fp32 already holds alpha; row[q] is this lane's output row
 // (column of the tile) in B [m][rows][rank], or -1.  The adapters that occur
 // among the tokens are taken one after the other, each as a product over all of
 // them, of which only its own tokens' rows are kept: a value that is not finite
-// in one request's adapter or tokens stays in that request's rows.
+// in one request's adapter or tokens stays in that request's rows.  Places in the
+// order of adapters leave one or two of them to a tile.
 // fp32 results take S in three terms, 16-bit ones in two.
 template <int DT, int TERMS, int NT, class Acc>
 GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, const float* S, int64_t t0, int64_t n,
                          const int64_t (&row)[NT], Acc (&out)[NT]) {
   using Tile = TileShape<Acc>;
   const int lane = threadIdx.x & 63, kq = lane / Tile::E;
-  const int64_t t = t0 + lane % Tile::E;
+  const int64_t t = ad.token(t0 + lane % Tile::E, n);
   const int mine = adapter_of(ad, t, n);
   uint32_t rest = (uint32_t)(__ballot(mine >= 0) & ((1ull << Tile::E) - 1));
   while (rest) {
@@ -232,7 +237,7 @@ GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, co
     for (int k0 = 0; k0 < ad.rank; k0 += Tile::K) {
       const int k = k0 + 8 * kq;
       float v[8] = {};
-      if (k < ad.rank && t < n) load8f(S + t * ad.rank + k, v);
+      if (k < ad.rank && mine >= 0) load8f(S + t * ad.rank + k, v);
       u32x4 s[TERMS];
       split8<TERMS>(v, s);
 #pragma unroll
@@ -252,8 +257,8 @@ GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, co
 }
 
 // ---------------------------------------------------------------- tile results
-// Stores a wave's 32 tokens x 32 NT outputs (accumulators of mfma32) to out,
-// turned through the wave's own 32 x (32 NT + 4) floats of LDS so that a row
+// Stores the 32 tokens at places t0 .. x 32 NT outputs of a wave (accumulators of
+// mfma32) to out, turned through the wave's own 32 x (32 NT + 4) floats of LDS so that a row
 // leaves in whole runs of eight outputs per lane (single stores of two bytes
 // took a tenth of a 256 x 256 tile's time at 4096 columns).  vec: rows of out
 // start on 16 bytes.  more(v, t, j, k): adds to the first k <= 8 outputs from j.
@@ -261,8 +266,8 @@ struct NoMore {
   GPTQ_DEV void operator()(float (&)[8], int64_t, int64_t, int) const {}
 };
 template <int OT, int NT, class More = NoMore>
-GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], void* out, int64_t t0, int64_t n, int64_t j0, int64_t cols, int64_t ldo,
-                         bool vec, const More& more = More()) {
+GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], const Adapters& ad, void* out, int64_t t0, int64_t n, int64_t j0,
+                         int64_t cols, int64_t ldo, bool vec, const More& more = More()) {
   constexpr int W = 32 * NT, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;
   const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -273,10 +278,10 @@ GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], void* out, int64
 #pragma unroll
   for (int k = 0; k < 32 / RPP; ++k) {
     const int r = RPP * k + lane / LPR, c = 8 * (lane % LPR);
-    const int64_t t = t0 + r, j = j0 + c;
+    const int64_t t = ad.token(t0 + r, n), j = j0 + c;
     float v[8];
     load8f(lds + r * LD + c, v);
-    if (t >= n || j >= cols) continue;
+    if (t < 0 || j >= cols) continue;
     more(v, t, j, (int)min((int64_t)8, cols - j));
     if (vec && j + 8 <= cols) {
       if constexpr (OT == 0) {
@@ -397,10 +402,14 @@ GPTQ_DEV u32x4 pair_order(u32x4 v) {
 // of 8, zero past d) -- adapter.hip.  S: n x rank results (on 16 bytes) in
 // adapter_down_floats() of workspace.
 int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank);
+// Whether tokens are to be taken adapter by adapter (ad.order, below), and that order:
+// all n tokens by adapter, ascending, those without one last.
+bool adapters_want_order(int64_t n, int m, const int32_t* index);
+void launch_token_order(const Adapters& ad, int64_t n, int32_t* order, hipStream_t s);
 void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ldx, const Adapters& ad, const uint16_t* A,
                          int64_t lda, float* S, hipStream_t s);
 // out = base + S B^T, of type yt.  base: of the same type (null: 0), or the sum of
-// `splits` parts [n][rows] fp32 times 2^ex[t].  S null: no adapters.
+// `splits` parts [n][rows] fp32 times 2^ex[t] (ex null: 1).  S null: no adapters.
 struct UpArgs {
   const float* S;
   int64_t n, rows;
@@ -451,12 +460,15 @@ struct Gemm16 {
   const float* S;         // null: no adapters
   void* out;
   int64_t ldo;
-  bool vec;               // set by launch_gemm16
+  bool vec;               // set by launch_gemm16, as splits
+  int splits;
+  float* part;            // gemm16_part_floats() of workspace (null where that is 0)
 };
 // dt: type of X, W and B; ot: of out.  fp32 results take W in as many terms of
 // its type as fp32 has bits.
 constexpr int gemm16_terms(int dt, int ot) { return ot != 0 ? 1 : (dt == kBF16 ? 3 : 2); }
 void launch_gemm16(const Gemm16& a, int dt, int ot, hipStream_t s);
+int64_t gemm16_part_floats(int64_t n, int64_t cols, int64_t kp, int dt, int ot);
 // Whether rows of d values can be its X as they are, and a copy (n x
 // gemm16_depth(d)) that can.
 bool gemm16_takes(const void* X, int64_t d, int64_t ldx);
@@ -473,9 +485,10 @@ int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt);
 void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad, const float* S,
                          void* Y, int yt, int64_t ldy, void* ws, hipStream_t s);
 // dX = dY W_hat (+ T A): packed_backward.hip.  At: A transposed to [m][c][rank];
-// Wt: gemm16_terms x c x gemm16_depth(r) values, rows: n x gemm16_depth(r).
+// Wt: gemm16_terms x c x gemm16_depth(r) values, rows: n x gemm16_depth(r), part: as
+// Gemm16's.
 void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, const PackedLayer& w, const Adapters& ad,
                             const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, uint16_t* Wt, uint16_t* rows,
-                            hipStream_t s);
+                            float* part, hipStream_t s);
 
 }  // namespace gptq

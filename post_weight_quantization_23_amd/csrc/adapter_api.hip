@@ -130,17 +130,25 @@ int64_t forward_bytes(int64_t n, int64_t r, int64_t c, bool perm, int yt) {
 
 // The rank values of n tokens of d features, with what computing them takes.
 int64_t low_bytes(int64_t n, int64_t d, int64_t rank) { return rank > 0 ? align256(gptq::adapter_down_floats(n, d, rank) * 4) : 0; }
+int64_t order_bytes(int64_t n, int64_t rank) { return rank > 0 ? align256(n * 4) : 0; }
+
+// Adapters with their tokens' order, where that helps.
+void set_order(gptq::Adapters& ad, int64_t n, int32_t* place, hipStream_t s) {
+  if (!gptq::adapters_want_order(n, ad.m, ad.index)) return;
+  gptq::launch_token_order(ad, n, place, s);
+  ad.order = place;
+}
 
 // Every launch's grid, at the launch helpers' workgroup shapes.
 bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
   return groups_for(n * (rank > 0 ? rank : 1), 4) <= kMaxGroups256 &&                    // down: a wave per value
          groups_for(n, 16) * groups_for(r, 16) <= kMaxGroups256 / 2 &&                   // forward: 512 threads per 16 rows
          groups_for(n, 16) * groups_for(r > c ? r : c, 256) <= kMaxGroups256 &&          // up
-         groups_for(n, 32) * groups_for(r > c ? r : c, 128) <= kMaxGroups256 / 2 &&      // tiles
+         groups_for(n, 32) * groups_for(r > c ? r : c, 128) <= kMaxGroups256 / 16 &&     // tiles, in up to 16 parts
          groups_for(r, 64) * groups_for(c, 256) <= kMaxGroups256 &&                      // dequantized copy
          groups_for(n * (r / 8 + 8), 256) <= kMaxGroups256 &&                            // padded rows
          groups_for(n * (c / 8), 256) <= kMaxGroups256 &&                                // gather
-         n * groups_for(r > c ? r : c, 256) <= kMaxGroups256 * (n > 64 ? 32 : 1) &&      // up
+         n * groups_for(r > c ? r : c, 256) <= kMaxGroups256 * (n > 64 && n > 4 * m ? 32 : 1) &&   // up
          groups_for(gptq::list_places(n, m) / 8 * (rank > 0 ? rank : 1), 256) <= kMaxGroups256 && gptq::list_places(n, m) < INT_MAX &&  // lists
          m * groups_for(r > c ? r : c, 64) * 2 <= kMaxGroups256 &&                       // transpose (rank <= 128)
          m * groups_for(r > c ? r : c, 128) * 16 <= kMaxGroups256 &&                     // gradients (16 splits of 4 rank blocks, 4 a group)
@@ -148,8 +156,10 @@ bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
 }
 
 // The input gradient's dequantized weights and padded rows of dY.
-int64_t backward_bytes(int64_t n, int64_t r, int64_t c, int terms) {
-  return align256(terms * c * gptq::gemm16_depth(r) * 2) + align256(n * gptq::gemm16_depth(r) * 2);
+int64_t backward_bytes(int64_t n, int64_t r, int64_t c, int xt, int ot) {
+  const int64_t depth = gptq::gemm16_depth(r);
+  return align256(gptq::gemm16_terms(xt, ot) * c * depth * 2) + align256(n * depth * 2) +
+         align256(gptq::gemm16_part_floats(n, c, depth, xt, ot) * 4);
 }
 
 struct GradSizes {
@@ -166,7 +176,7 @@ GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
   z.places = gptq::list_places(n, m);
   z.lists = align256(z.places * 4) + align256((m + 1) * 4) + align256(m * 4);
   z.terms = align256(3 * rank * z.places * 2);
-  z.total = align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + low_bytes(n, c, rank) + low_bytes(n, r, rank) + z.lists + 2 * z.terms + z.part;
+  z.total = order_bytes(n, rank) + align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + low_bytes(n, c, rank) + low_bytes(n, r, rank) + z.lists + 2 * z.terms + z.part;
   return z;
 }
 
@@ -184,7 +194,7 @@ gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t r, int64_t c, g
   if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
   if (rank != 0)
     if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, c, rank));
+  *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank));
   return ok();
 }
 
@@ -216,16 +226,17 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
     if (gptq_status st = check_clash(fn, clash(Y, ey, A, m * rank, c, c, 2))) return st;
     if (gptq_status st = check_clash(fn, clash(Y, ey, B, m * r, rank, rank, 2))) return st;
   }
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, forward_bytes(n, r, c, perm != nullptr, (int)yt) + low_bytes(n, c, rank))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, forward_bytes(n, r, c, perm != nullptr, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank))) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
-  const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
+  gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
   const int yi = yt == GPTQ_F32 ? 0 : xi;
   float* S = nullptr;
   if (low) {
     S = carve.take<float>(low_bytes(n, c, rank));
+    set_order(ad, n, carve.take<int32_t>(n * 4), s);
     gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
   }
   if (gptq::packed_tiles(n, c)) {
@@ -254,8 +265,8 @@ gptq_status gptq_packed_linear_backward_workspace_size(int64_t n, int64_t r, int
     if (gptq_status st = check_rank(fn, m, rank)) return st;
   if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
-  *bytes = (size_t)(backward_bytes(n, r, c, gptq::gemm16_terms((int)xt, (int)ot)) + align256(m * c * rank * 2) +
-                    align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank));
+  *bytes = (size_t)(backward_bytes(n, r, c, (int)xt, (int)ot) + align256(m * c * rank * 2) +
+                    align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank) + order_bytes(n, rank));
   return ok();
 }
 
@@ -290,26 +301,29 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
     if (gptq_status st = check_clash(fn, clash(dX, ex, B, m * r, rank, rank, 2))) return st;
   }
   const int terms = gptq::gemm16_terms((int)xt, (int)ot);
-  const int64_t need = backward_bytes(n, r, c, terms) + align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank);
+  const int64_t need = backward_bytes(n, r, c, (int)xt, (int)ot) + align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank) +
+                       order_bytes(n, rank);
   if (gptq_status st = need_ws(fn, ws, ws_bytes, need)) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
-  const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
+  gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
   uint16_t* Wt = carve.take<uint16_t>(terms * c * gptq::gemm16_depth(r) * 2);
   uint16_t* rows = carve.take<uint16_t>(n * gptq::gemm16_depth(r) * 2);
+  float* part = carve.take<float>(gptq::gemm16_part_floats(n, c, gptq::gemm16_depth(r), (int)xt, (int)ot) * 4);
   uint16_t* At = nullptr;
   float* T = nullptr;
   if (low) {
     At = carve.take<uint16_t>(m * c * rank * 2);
     uint16_t* Bt = carve.take<uint16_t>(m * rank * pad8(r) * 2);
     T = carve.take<float>(low_bytes(n, r, rank));
+    set_order(ad, n, carve.take<int32_t>(n * 4), s);
     gptq::launch_transpose16(ad.A, (int)m, rank, c, At, rank, s);
     gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
     gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);
   }
-  gptq::launch_packed_backward(dY, xi, n, ldy, w, ad, At, T, dX, ot == GPTQ_F32 ? 0 : xi, ldx, Wt, rows, s);
+  gptq::launch_packed_backward(dY, xi, n, ldy, w, ad, At, T, dX, ot == GPTQ_F32 ? 0 : xi, ldx, Wt, rows, part, s);
   return check_launch(fn);
 }
 
@@ -319,7 +333,7 @@ gptq_status gptq_adapter_add_workspace_size(int64_t n, int64_t c, int64_t rank, 
   if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
   if (gptq_status st = check_sizes(fn, n, 0, c, 8)) return st;
   if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  *bytes = (size_t)low_bytes(n, c, rank);
+  *bytes = (size_t)(low_bytes(n, c, rank) + order_bytes(n, rank));
   return ok();
 }
 
@@ -344,11 +358,13 @@ gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n, int64_t c,
   if (gptq_status st = check_clash(fn, clash(out, eo, B, m * r, rank, rank, 2))) return st;
   if (!(out == Y && ldo == ldy))
     if (gptq_status st = check_clash(fn, clash(out, eo, Y, n, ldy, r, el))) return st;
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, low_bytes(n, c, rank))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, low_bytes(n, c, rank) + order_bytes(n, rank))) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
+  gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
-  float* S = static_cast<float*>(ws);
+  Carve carve{static_cast<char*>(ws)};
+  float* S = carve.take<float>(low_bytes(n, c, rank));
+  set_order(ad, n, carve.take<int32_t>(n * 4), s);
   gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
   gptq::UpArgs u{};
   u.S = S; u.n = n; u.rows = r; u.ad = ad; u.B = ad.B; u.base = Y; u.ldb = ldy; u.out = out; u.ldo = ldo;
@@ -404,8 +420,9 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   if (gptq_status st = need_ws(fn, ws, ws_bytes, z.total)) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
+  gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
+  int32_t* by_adapter = carve.take<int32_t>(n * 4);
   uint16_t* Bt = carve.take<uint16_t>(m * rank * pad8(r) * 2);
   uint16_t* At = carve.take<uint16_t>(m * c * rank * 2);
   float* S = carve.take<float>(low_bytes(n, c, rank));
@@ -418,6 +435,7 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   float* part = carve.take<float>(z.part);
   gptq::launch_token_lists(ad, n, order, start, count, s);
   if (n > 0) {
+    set_order(ad, n, by_adapter, s);
     gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
     gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
     gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);

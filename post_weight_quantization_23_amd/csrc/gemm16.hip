@@ -18,9 +18,11 @@ GPTQ_DEV int swz(int f) { return (f ^ (f >> 3)) & 7; }
 
 // WM x WN waves of 32 MT tokens x 32 NT columns.  Both operands come from
 // memory straight into LDS (double buffered, one barrier per step), each lane
-// fetching the chunk that belongs at its place; rows past the end lie outside
-// the descriptors' records and read as zero.
-template <int DT, int OT, int TERMS, int MT, int NT, int WM, int WN>
+// fetching the chunk that belongs at its place; tokens past the end repeat the
+// last one, columns past the end lie outside the descriptor's records and read
+// as zero.  ORDER: tokens by adapter (ad.order).  PARTS: the workgroup takes one of
+// `splits` parts of the contraction and writes its fp32 sums to part.
+template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
 GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
   constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, NW = WM * WN, BUF = (TM + TN) * ROWB;
   constexpr int QX = TM / 8 / NW, QW = TN / 8 / NW;   // load instructions per wave: 8 rows each
@@ -28,17 +30,21 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 31, h = lane >> 5;
   int tt, ct;
-  tile_of(blockIdx.x, a.tok_tiles, a.col_tiles, tt, ct);
+  const int64_t tile = PARTS ? blockIdx.x / a.splits : blockIdx.x;
+  const int split = PARTS ? (int)(blockIdx.x - tile * a.splits) : 0;
+  tile_of(tile, a.tok_tiles, a.col_tiles, tt, ct);
   const int64_t t0 = (int64_t)tt * TM;
   const int j0 = ct * TN;
   const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
   lds_u8* lbase = (lds_u8*)smem;
 
   int offx[QX], offw[QW];
+  const uint16_t* fromx[QX];
 #pragma unroll
   for (int q = 0; q < QX; ++q) {
-    const int row = 8 * (wave * QX + q) + (lane >> 3);
-    offx[q] = (row * (int)a.ldx + 8 * ((lane & 7) ^ swz(row))) * 2;
+    const int row = 8 * (wave * QX + q) + (lane >> 3), piece = 8 * ((lane & 7) ^ swz(row));
+    if constexpr (ORDER) fromx[q] = a.X + (int64_t)a.ad.order[min(t0 + row, a.n - 1)] * a.ldx + piece;
+    else offx[q] = (row * (int)a.ldx + piece) * 2;
   }
 #pragma unroll
   for (int q = 0; q < QW; ++q) {
@@ -46,7 +52,8 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
     offw[q] = (row * (int)a.kp + 8 * ((lane & 7) ^ swz(row))) * 2;
   }
   const int xrec = (int)(min(a.n - t0, (int64_t)TM) * a.ldx * 2), wrec = (int)(min(a.cols - j0, TN) * a.kp * 2);
-  const int steps = (int)(a.kp / LK), all = TERMS * steps;
+  const int steps = (int)(a.kp / LK), total = TERMS * steps, each = PARTS ? (total + a.splits - 1) / a.splits : total;
+  const int first = split * each, all = min(total, first + each);
   auto load = [&](int s) {
     const int term = TERMS == 1 ? 0 : s / steps, k0 = (s - term * steps) * LK;
     const __amdgpu_buffer_rsrc_t rx =
@@ -55,7 +62,13 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
         (void*)(a.W + ((int64_t)term * a.cols + j0) * a.kp + k0), (short)0, wrec - 2 * k0, 0x00020000);
     lds_u8* to = lbase + (s & 1) * BUF;
 #pragma unroll
-    for (int q = 0; q < QX; ++q) __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to + (wave * QX + q) * 1024, 16, offx[q], 0, 0, 0);
+    for (int q = 0; q < QX; ++q) {
+      if constexpr (ORDER)
+        __builtin_amdgcn_global_load_lds((const void __attribute__((address_space(1)))*)(fromx[q] + k0),
+                                         (void __attribute__((address_space(3)))*)(to + (wave * QX + q) * 1024), 16, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to + (wave * QX + q) * 1024, 16, offx[q], 0, 0, 0);
+    }
 #pragma unroll
     for (int q = 0; q < QW; ++q)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to + TM * ROWB + (wave * QW + q) * 1024, 16, offw[q], 0, 0, 0);
@@ -67,8 +80,8 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
 #pragma unroll
     for (int q = 0; q < NT; ++q) acc[i][q] = floatx16{};
 
-  load(0);
-  for (int s = 0; s < all; ++s) {
+  load(first);
+  for (int s = first; s < all; ++s) {
     // own loads have landed; with every wave here, the other buffer is free
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
@@ -98,6 +111,13 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
   static_assert(NW * 32 * (32 * NT + 4) * 4 <= 2 * BUF, "tile results fit the operands' LDS");
   float* own = reinterpret_cast<float*>(smem) + wave * 32 * (32 * NT + 4);
   __syncthreads();   // the last step's operands have been read
+  if constexpr (PARTS) {
+    float* part = a.part + (int64_t)split * a.n * a.cols;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      store_tile<0, NT>(own, acc[i], a.ad, part, t0 + wm + 32 * i, a.n, j0 + wn, a.cols, a.cols, a.vec);
+    return;
+  }
   int64_t col[NT];
 #pragma unroll
   for (int q = 0; q < NT; ++q) {
@@ -108,35 +128,49 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
   for (int i = 0; i < MT; ++i) {
     const int64_t ti = t0 + wm + 32 * i;
     if (a.S) expand_add<DT, OT == 0 ? 3 : 2, NT>(a.ad, a.B, a.cols, a.S, ti, a.n, col, acc[i]);
-    store_tile<OT, NT>(own, acc[i], a.out, ti, a.n, j0 + wn, a.cols, a.ldo, a.vec);
+    store_tile<OT, NT>(own, acc[i], a.ad, a.out, ti, a.n, j0 + wn, a.cols, a.ldo, a.vec);
   }
 }
 
-template <int DT, int OT, int TERMS, int MT, int NT, int WM, int WN>
+template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(Gemm16 a) {
   extern __shared__ __align__(16) unsigned char gsm[];
-  gemm_body<DT, OT, TERMS, MT, NT, WM, WN>(a, gsm);
+  gemm_body<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>(a, gsm);
 }
 
-template <int DT, int OT, int TERMS, int MT, int NT, int WM, int WN>
+template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
 void launch_gemm(Gemm16 a, hipStream_t s) {
   constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, LDS = 2 * (TM + TN) * ROWB;
   static const bool set = [] {   // once, thread-safe
-    (void)hipFuncSetAttribute((const void*)gemm_kernel<DT, OT, TERMS, MT, NT, WM, WN>, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+    (void)hipFuncSetAttribute((const void*)gemm_kernel<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>,
+                              hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     return true;
   }();
   (void)set;
   a.tok_tiles = (int)((a.n + TM - 1) / TM);
   a.col_tiles = (a.cols + TN - 1) / TN;
-  hipLaunchKernelGGL((gemm_kernel<DT, OT, TERMS, MT, NT, WM, WN>), dim3((unsigned)((int64_t)a.tok_tiles * a.col_tiles)),
-                     dim3(64 * WM * WN), LDS, s, a);
+  hipLaunchKernelGGL((gemm_kernel<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>),
+                     dim3((unsigned)((int64_t)a.tok_tiles * a.col_tiles * a.splits)), dim3(64 * WM * WN), LDS, s, a);
+}
+
+// Tiles of 256 x 256 (8 waves) from 192 of them on, else 128 x 128 (4 waves), and
+// those in parts while they are too few for the chip.
+bool big_tiles(int64_t n, int64_t cols) { return (n + 255) / 256 * ((cols + 255) / 256) >= 192; }
+
+int gemm16_splits(int64_t n, int64_t cols, int64_t steps) {
+  if (n == 0 || cols == 0 || big_tiles(n, cols)) return 1;
+  const int64_t tiles = (n + 127) / 128 * ((cols + 127) / 128);
+  int64_t splits = 384 / tiles;
+  splits = splits < steps / 8 ? splits : steps / 8;
+  return splits < 2 ? 1 : (splits > 16 ? 16 : (int)splits);
 }
 
 template <int DT, int OT, int TERMS>
 void choose_gemm(const Gemm16& a, hipStream_t s) {
-  const int64_t big = (a.n + 255) / 256 * ((a.cols + 255) / 256);
-  if (big >= 192) launch_gemm<DT, OT, TERMS, 4, 2, 2, 4>(a, s);
-  else launch_gemm<DT, OT, TERMS, 2, 2, 2, 2>(a, s);
+  const bool order = a.ad.order != nullptr;
+  if (a.splits > 1) launch_gemm<DT, 0, TERMS, false, true, 2, 2, 2, 2>(a, s);
+  else if (big_tiles(a.n, a.cols)) order ? launch_gemm<DT, OT, TERMS, true, false, 4, 2, 2, 4>(a, s) : launch_gemm<DT, OT, TERMS, false, false, 4, 2, 2, 4>(a, s);
+  else order ? launch_gemm<DT, OT, TERMS, true, false, 2, 2, 2, 2>(a, s) : launch_gemm<DT, OT, TERMS, false, false, 2, 2, 2, 2>(a, s);
 }
 
 // dst[t][0 .. kp) = src[t][0 .. d) (through perm, entries outside 0 .. d-1
@@ -161,9 +195,28 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
 
 void launch_gemm16(const Gemm16& g, int dt, int ot, hipStream_t s) {
   Gemm16 a = g;
-  a.vec = rows_on_16(a.out, a.ldo, ot);
+  a.splits = gemm16_splits(a.n, a.cols, gemm16_terms(dt, ot) * (a.kp / LK));
+  a.vec = a.splits > 1 ? rows_on_16(a.part, a.cols, 0) && a.n * a.cols % 4 == 0 : rows_on_16(a.out, a.ldo, ot);
+  if (a.splits > 1) a.ad.order = nullptr;   // the adapters follow where the parts are joined
   if (dt == kBF16) { if (ot == 0) choose_gemm<kBF16, 0, gemm16_terms(kBF16, 0)>(a, s); else choose_gemm<kBF16, kBF16, 1>(a, s); }
   else { if (ot == 0) choose_gemm<kF16, 0, gemm16_terms(kF16, 0)>(a, s); else choose_gemm<kF16, kF16, 1>(a, s); }
+  if (a.splits == 1) return;
+  UpArgs u{};
+  u.S = g.S;
+  u.n = g.n;
+  u.rows = g.cols;
+  u.ad = g.ad;
+  u.B = g.B;
+  u.part = a.part;
+  u.splits = a.splits;
+  u.out = g.out;
+  u.ldo = g.ldo;
+  launch_adapter_up(u, dt, ot, s);
+}
+
+int64_t gemm16_part_floats(int64_t n, int64_t cols, int64_t kp, int dt, int ot) {
+  const int splits = gemm16_splits(n, cols, gemm16_terms(dt, ot) * (kp / LK));
+  return splits > 1 ? splits * n * cols : 0;
 }
 
 bool gemm16_takes(const void* X, int64_t d, int64_t ldx) {

@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256) void dequant_t_kernel(PackedLayer w, uint16_t*
 
 void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, const PackedLayer& w, const Adapters& ad,
                             const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, uint16_t* Wt, uint16_t* rows,
-                            hipStream_t s) {
+                            float* part, hipStream_t s) {
   const int64_t kp = gemm16_depth(w.r);
   const int64_t rt = kp / 64;
   const dim3 dgrid((unsigned)(rt * ((w.c + 255) / 256)));
@@ -97,6 +97,7 @@ void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, cons
     a.ldx = kp;
   }
   a.W = Wt;
+  a.part = part;
   a.kp = kp;
   a.cols = w.c;
   a.ad = ad;

@@ -226,7 +226,7 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
         for (int q = 0; q < NT; ++q) tot[i][q][e] = __builtin_ldexpf(tot[i][q][e], ex);
       }
     }
-    store_tile<0, NT>(own, tot[i], out, ti, a.n, row0, a.w.r, a.ldo, a.vec);
+    store_tile<0, NT>(own, tot[i], Adapters{}, out, ti, a.n, row0, a.w.r, a.ldo, a.vec);
   }
 }
 
@@ -362,7 +362,8 @@ bool dequant_first(int64_t n, int yt) { return yt != 0 && n >= kCopyTokens; }
 bool packed_tiles(int64_t n, int64_t c) { return n > 64 && c < (int64_t(1) << 22) - STEP; }
 
 int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt) {
-  if (dequant_first(n, yt)) return align256(n * gemm16_depth(c) * 2) + align256(r * gemm16_depth(c) * 2);
+  if (dequant_first(n, yt))
+    return align256(n * gemm16_depth(c) * 2) + align256(r * gemm16_depth(c) * 2) + 4 * gemm16_part_floats(n, r, gemm16_depth(c), yt, yt);
   const TilePlan p = plan_tiles(n, r, c);
   const bool direct = yt == 0 && p.splits == 1;
   return align256(n * tiles_width(c) * 2) + align256(n * 4) + (direct ? 0 : align256(p.splits * n * r * 4));
@@ -389,6 +390,7 @@ void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const Pa
     else { if (xt == kBF16) GPTQ_DEQ(3, kBF16); else GPTQ_DEQ(3, kF16); }
 #undef GPTQ_DEQ
     g.W = W;
+    g.part = reinterpret_cast<float*>(W + align256((int64_t)w.r * g.kp * 2) / 2);
     g.n = n;
     g.cols = w.r;
     g.ad = ad;

@@ -61,6 +61,12 @@ def test_workspace_queries(lib):
     assert f(16, 60, 8, C.byref(out)) == 3
     f = lib.gptq_adapter_backward_workspace_size
     assert f(16, 100, 64, 2, 8, C.byref(out)) == 0 and f(16, 100, 60, 2, 8, C.byref(out)) == 3
+    assert f(0, 100, 64, 2, 8, C.byref(out)) == 0 and f(16, 0, 64, 2, 8, C.byref(out)) == 0
+    assert lib.gptq_packed_linear_workspace_size(0, 0, 64, 1, 8, 1, C.byref(out)) == 0
+    assert lib.gptq_packed_linear_workspace_size(2000, 0, 64, 1, 8, 1, C.byref(out)) == 0
+    assert lib.gptq_packed_linear_backward_workspace_size(0, 100, 64, 1, 0, 2, 8, C.byref(out)) == 0
+    assert lib.gptq_packed_linear_backward_workspace_size(16, 0, 64, 1, 1, 2, 8, C.byref(out)) == 0
+    assert lib.gptq_adapter_add_workspace_size(0, 64, 8, C.byref(out)) == 0
     # sizes whose byte counts would pass 63 bits are refused, not wrapped
     assert f(1 << 30, 1 << 30, 1 << 30, 1 << 20, 128, C.byref(out)) == 5
 

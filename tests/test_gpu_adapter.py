@@ -141,6 +141,9 @@ FORWARD = [
     (1300, 257, 96, 4, -1, False, "fp16", "fp16", None),
     (1500, 129, 544, 3, 32, True, "bf16", "bf16", (6, 8, "mixed")),
     (1111, 140, 320, 4, 64, False, "bf16", "fp32", (2, 24, "mixed")),
+    (103, 41, 192, 3, -1, True, "bf16", "bf16", (32, 128, "mixed")),   # few tokens for each of many adapters
+    (300, 90, 256, 4, 128, False, "fp16", "fp32", (40, 8, "mixed")),
+    (1200, 530, 128, 4, 128, False, "bf16", "bf16", (32, 16, "mixed")),
 ]
 
 
@@ -178,6 +181,8 @@ BACKWARD = [
     (200, 130, 1056, 3, 128, False, "bf16", "fp32", None),
     (257, 72, 640, 4, 256, True, "fp16", "fp32", (5, 40, "mixed")),
     (1030, 100, 160, 4, 32, False, "bf16", "bf16", (2, 64, "runs")),
+    (20, 1030, 96, 4, 32, False, "bf16", "fp32", (3, 8, "mixed")),     # few tiles, a long contraction
+    (300, 900, 160, 3, 32, True, "fp16", "fp16", (9, 16, "mixed")),
 ]
 
 
@@ -201,6 +206,8 @@ ADD = [
     (100, 64, 1000, "fp16", "fp16", (9, 128, "mixed")),
     (530, 130, 256, "bf16", "fp32", (3, 64, "runs")),
     (2049, 40, 128, "fp16", "fp32", (2, 40, "mixed")),
+    (200, 70, 64, "bf16", "bf16", (64, 8, "mixed")),
+    (700, 33, 320, "fp16", "fp16", (32, 72, "mixed")),
 ]
 
 
@@ -227,6 +234,8 @@ GRAD = [
     (333, 136, 520, "bf16", "fp32", (5, 40, "mixed")),
     (700, 200, 96, "fp16", "fp32", (1, 128, "all")),
     (1500, 72, 200, "bf16", "bf16", (3, 64, "runs")),
+    (128, 34, 64, "fp16", "fp16", (32, 40, "runs")),
+    (900, 45, 136, "bf16", "fp32", (24, 8, "mixed")),
 ]
 
 
