@@ -13,11 +13,19 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .gptq import _DT, Workspace, _need, _ptr, _stream, _ws
+from .gptq import _DT, Workspace, _need, _ws
 
 __all__ = ["packed_linear", "packed_linear_backward", "adapter_add", "adapter_backward"]
 
 _16 = (torch.bfloat16, torch.float16)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _rows16(t, name, n=None, d=None, dtype=None):
@@ -137,7 +145,7 @@ def packed_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, z
     out = torch.empty((n, r), dtype=yt, device=dev) if out is None else out
     _lib.call("gptq_packed_linear", _ptr(X), _DT[X.dtype], n, _ld(X), _ptr(packed), r, c, int(bits), _ld(packed),
               _ptr(scales), _ptr(zeros), _ld(scales), int(groupsize), _ptr(perm), _ptr(A), _ptr(B), m, rank, _ptr(index),
-              _ptr(alpha), _ptr(out), _DT[yt], _ld(out), _ptr(buf), nb, _stream())
+              _ptr(alpha), _ptr(out), _DT[yt], _ld(out), _ptr(buf), nb, _stream(dev))
     return out
 
 
@@ -167,7 +175,7 @@ def packed_linear_backward(dY: torch.Tensor, packed: torch.Tensor, scales: torch
     out = torch.empty((n, c), dtype=ot, device=dev) if out is None else out
     _lib.call("gptq_packed_linear_backward", _ptr(dY), _DT[dY.dtype], n, _ld(dY), _ptr(packed), r, c, int(bits), _ld(packed),
               _ptr(scales), _ptr(zeros), _ld(scales), int(groupsize), _ptr(perm), _ptr(A), _ptr(B), m, rank, _ptr(index),
-              _ptr(alpha), _ptr(out), _DT[ot], _ld(out), _ptr(buf), nb, _stream())
+              _ptr(alpha), _ptr(out), _DT[ot], _ld(out), _ptr(buf), nb, _stream(dev))
     return out
 
 
@@ -192,7 +200,7 @@ def adapter_add(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tens
     buf, nb = _ws(ws, _lib.query("gptq_adapter_add_workspace_size", n, c, rank), dev)
     out = torch.empty((n, r), dtype=Y.dtype, device=dev) if out is None else out
     _lib.call("gptq_adapter_add", _ptr(X), _DT[X.dtype], n, c, _ld(X), _ptr(A), _ptr(B), m, rank, r, _ptr(index),
-              _ptr(alpha), _ptr(Y), _DT[Y.dtype], _ld(Y), _ptr(out), _ld(out), _ptr(buf), nb, _stream())
+              _ptr(alpha), _ptr(Y), _DT[Y.dtype], _ld(Y), _ptr(out), _ld(out), _ptr(buf), nb, _stream(dev))
     return out
 
 
@@ -243,5 +251,5 @@ def adapter_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torc
         if base is not None and n > 1 and _ld(base) != ldd:
             raise ValueError("base and out['dX'] must have the same row stride")
     _lib.call("gptq_adapter_backward", _ptr(dY), _ld(dY), _ptr(X), _ld(X), _DT[X.dtype], n, r, c, _ptr(A), _ptr(B), m, rank,
-              _ptr(index), _ptr(alpha), _ptr(gA), _ptr(gB), _ptr(base), _ptr(dX), _DT[ot], ldd, _ptr(buf), nb, _stream())
+              _ptr(index), _ptr(alpha), _ptr(gA), _ptr(gB), _ptr(base), _ptr(dX), _DT[ot], ldd, _ptr(buf), nb, _stream(dev))
     return {"A": gA, "B": gB, "dX": dX}

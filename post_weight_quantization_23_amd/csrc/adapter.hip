@@ -11,32 +11,43 @@ namespace gptq {
 
 namespace {
 
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+
+// fp32 sums of split gradients: out = parts added in order, for up to two of them.
+struct JoinArgs {
+  const float* part[2];
+  float* out[2];
+  int64_t n[2];
+  int splits[2];
+};
+
 // ---------------------------------------------------------------- down
 // A few tokens: one wave per (token, rank row), 64 lanes x 8 elements a load, four
 // loads of each operand in flight (a chain of single ones waits for memory once
 // per 512 elements).  fp32 sums, folded over the wave in a fixed order.
 template <int DT>
-__global__ __launch_bounds__(256) void down_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t d, int64_t ldx,
-                                                   Adapters ad, const uint16_t* __restrict__ A, int64_t lda, bool vec,
-                                                   float* __restrict__ S) {
+__global__ __launch_bounds__(256) void down_kernel(DownArgs g) {
   const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t t = item / ad.rank;
-  const int p = (int)(item - t * ad.rank);
-  if (t >= n) return;
-  const int a = adapter_of(ad, t, n);
+  int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t per = g.n * g.ad.rank;
+  const DownProblem& q = g.p[item < per ? 0 : 1];
+  if (item >= per) item -= per;
+  const int64_t t = item / g.ad.rank;
+  const int p = (int)(item - t * g.ad.rank);
+  if (t >= g.n || !q.X) return;
+  const int a = adapter_of(g.ad, t, g.n);
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   if (a >= 0) {
-    const uint16_t* x = X + t * ldx;
-    const uint16_t* w = A + ((int64_t)a * ad.rank + p) * lda;
-    for (int64_t k0 = 8 * lane; k0 < d; k0 += 2048) {
+    const uint16_t* x = q.X + t * q.ldx;
+    const uint16_t* w = q.A + ((int64_t)a * g.ad.rank + p) * q.lda;
+    for (int64_t k0 = 8 * lane; k0 < q.d; k0 += 2048) {
       u32x4 xv[4], wv[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t k = k0 + 512 * u;
         xv[u] = wv[u] = u32x4{0u, 0u, 0u, 0u};
-        if (k < d) {
-          xv[u] = load8(x + k, (int)min((int64_t)8, d - k), vec);
+        if (k < q.d) {
+          xv[u] = load8(x + k, (int)min((int64_t)8, q.d - k), q.vec);
           wv[u] = *reinterpret_cast<const u32x4*>(w + k);
         }
       }
@@ -52,106 +63,126 @@ __global__ __launch_bounds__(256) void down_kernel(const uint16_t* __restrict__ 
   float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) all += __shfl_xor(all, m);
-  if (lane == 0) S[item] = a >= 0 && ad.alpha ? all * ad.alpha[a] : all;
+  if (lane == 0) q.S[item] = a >= 0 && g.ad.alpha ? all * g.ad.alpha[a] : all;
 }
 
-// Many tokens: a workgroup takes 64 tokens and one of `splits` parts of the
-// contraction, its four waves every fourth step of 64 of that part (a whole
-// line of memory per row), all 16 RT
-// rank rows (operands come from memory in the layout of the product, which
-// reads X once).  The adapters that occur among the tokens are taken in turn;
-// each writes its own tokens' rows.  Waves are joined through LDS in wave
-// order (each has a slot there: adding them up in one, wave after wave, took
-// longer than the product), parts by scale_join_kernel.
-// FAST: rows of X start on 16 bytes and hold whole steps; then every load is
-// unconditional (tokens and rank rows past the end repeat the last one, whose
-// results are dropped), so that several steps' loads are in flight.
-template <int DT, int RT, bool FAST>
-__global__ __launch_bounds__(256) void down_tiles_kernel(const uint16_t* __restrict__ X, int64_t n, int64_t d, int64_t ldx, Adapters ad,
-                                                         const uint16_t* __restrict__ A, int64_t lda, bool vec, float* __restrict__ S,
-                                                         int splits) {
-  constexpr int LD = 16 * RT + 4;   // floats of a token's row in a slot
-  extern __shared__ __align__(16) float slots[];   // [4][64][LD]
+// Many tokens: a workgroup takes the 64 tokens at 64 places and one of `splits`
+// parts of the contraction, each wave 16 of the tokens and all 16 RT rank rows.
+// Steps of 64 come into LDS by loads that write it (double buffered): loading
+// operands straight into registers touches 64 places of 16 bytes per
+// instruction, which the L1 cache takes one a cycle, against 16 here (4096
+// tokens of 11008, rank 64: 37 us, memory's share is 18).  The adapters that
+// occur among the tokens are taken in turn; each writes its own tokens' rows.
+// Parts are added by the kernels that read them.
+template <int DT, int RT>
+GPTQ_DEV void down_tiles_body(const DownArgs& g, unsigned char* smem) {
+  constexpr int ROWB = 128, XB = 64 * ROWB, BUF = XB + 16 * RT * ROWB;
+  constexpr int QW = 16 * RT / 8;   // load instructions of a step for the rank rows (8 rows each); the tokens take 8
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, kq = lane >> 4;
-  const int64_t tile = blockIdx.x / splits;
-  const int split = (int)(blockIdx.x - tile * splits);
+  const Adapters& ad = g.ad;
+  int64_t b = blockIdx.x;
+  const bool second = b >= g.blocks0;
+  const DownProblem& q = g.p[second ? 1 : 0];
+  if (second) b -= g.blocks0;
+  const int64_t tile = b / q.splits;
+  const int split = (int)(b - tile * q.splits);
   const int64_t t0 = tile * 64;
-  const int64_t steps = (d + 63) / 64, per = (steps + splits - 1) / splits;
-  const int64_t s1 = min(steps, (split + 1) * per);
-  float* out = S + (int64_t)split * n * ad.rank;
-  const int64_t lane_token = ad.token(t0 + lane, n);
-  const int mine = adapter_of(ad, lane_token, n);
+  const int64_t steps = (q.d + 63) / 64, per = (steps + q.splits - 1) / q.splits;
+  const int64_t sa = split * per, s1 = min(steps, sa + per);
+  float* out = q.splits == 1 ? q.S : q.S + down_values(g.n, ad.rank) + (int64_t)split * g.n * ad.rank;
+  const int mine = adapter_of(ad, ad.token(t0 + lane, g.n), g.n);
   uint64_t rest = __ballot(mine >= 0);
-  // this thread's four rank values of every (64 / RT)-th token
+  // rows of tokens without an adapter: this thread's four rank values of every (64 / RT)-th token
   const int col = 4 * (threadIdx.x % (4 * RT)), tok0 = threadIdx.x / (4 * RT);
 #pragma unroll
   for (int tok = tok0; tok < 64; tok += 64 / RT)
-    if (!((rest >> tok) & 1) && t0 + tok < n && col < ad.rank)
-      *reinterpret_cast<floatx4*>(out + ad.token(t0 + tok, n) * ad.rank + col) = floatx4{0.f, 0.f, 0.f, 0.f};
-  const uint16_t* xrow[4];   // tokens past the end repeat the last one
+    if (!((rest >> tok) & 1) && t0 + tok < g.n && col < ad.rank)
+      *reinterpret_cast<floatx4*>(out + ad.token(t0 + tok, g.n) * ad.rank + col) = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  // sources of this lane: piece (16 bytes) lane & 7 of row lane >> 3, permuted by
+  // the row; tokens past the end repeat the last one, pieces past the end of a
+  // row its last one
+  lds_u8* lbase = (lds_u8*)smem;
+  const uint16_t* xsrc[2];
+  int xpiece[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) xrow[i] = X + ad.token(min(t0 + 16 * i + m, n - 1), n) * ldx;
+  for (int i = 0; i < 2; ++i) {
+    const int row = 8 * (2 * wave + i) + (lane >> 3);
+    xsrc[i] = q.X + ad.token(min(t0 + row, g.n - 1), g.n) * q.ldx;
+    xpiece[i] = (lane & 7) ^ (row & 7);
+  }
+  const int64_t xlast = q.d / 8 - 1, wlast = q.lda / 8 - 1;
   while (rest) {
     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(rest));
     const uint64_t members = __ballot(mine == a);
     rest &= ~members;
-    const uint16_t* w = A + (int64_t)a * ad.rank * lda;
-    floatx4 acc[4][RT];
+    const uint16_t* w = q.A + (int64_t)a * ad.rank * q.lda;
+    auto load = [&](int64_t s) __attribute__((always_inline)) {
+      lds_u8* to = lbase + ((s - sa) & 1) * BUF;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
+        __builtin_amdgcn_global_load_lds((const void __attribute__((address_space(1)))*)(xsrc[i] + 8 * min(8 * s + xpiece[i], xlast)),
+                                         (void __attribute__((address_space(3)))*)(to + (2 * wave + i) * 1024), 16, 0, 0);
 #pragma unroll
-      for (int p = 0; p < RT; ++p) acc[i][p] = floatx4{0.f, 0.f, 0.f, 0.f};
-    auto step = [&](int64_t k) __attribute__((always_inline)) {
-      u32x4 x[4], b[RT];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = u32x4{0u, 0u, 0u, 0u};
-        if constexpr (FAST) x[i] = *reinterpret_cast<const u32x4*>(xrow[i] + k);
-        else if (k < d) x[i] = load8(xrow[i] + k, (int)min((int64_t)8, d - k), vec);
+      for (int i = wave; i < QW; i += 4) {
+        const int row = 8 * i + (lane >> 3);
+        __builtin_amdgcn_global_load_lds(
+            (const void __attribute__((address_space(1)))*)(w + (int64_t)min(row, ad.rank - 1) * q.lda + 8 * min(8 * s + ((lane & 7) ^ (row & 7)), wlast)),
+            (void __attribute__((address_space(3)))*)(to + XB + i * 1024), 16, 0, 0);
       }
-#pragma unroll
-      for (int p = 0; p < RT; ++p) {
-        b[p] = u32x4{0u, 0u, 0u, 0u};
-        if constexpr (FAST) b[p] = *reinterpret_cast<const u32x4*>(w + (int64_t)min(16 * p + m, ad.rank - 1) * lda + k);
-        else if (16 * p + m < ad.rank && k < d) b[p] = *reinterpret_cast<const u32x4*>(w + (int64_t)(16 * p + m) * lda + k);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int p = 0; p < RT; ++p) acc[i][p] = mfma16<DT>(x[i], b[p], acc[i][p]);
     };
-#pragma unroll FAST && RT <= 4 ? 2 : 1
-    for (int64_t s = split * per + wave; s < s1; s += 4) {
-      step(64 * s + 8 * kq);
-      step(64 * s + 32 + 8 * kq);
-    }
-    float* slot = slots + wave * 64 * LD;
+    floatx4 acc[RT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int p = 0; p < RT; ++p) acc[p] = floatx4{0.f, 0.f, 0.f, 0.f};
+    if (sa < s1) load(sa);
+    for (int64_t s = sa; s < s1; ++s) {
+      __builtin_amdgcn_s_waitcnt(0);   // own loads have landed; with every wave here, the other buffer is free
+      unsigned char* at = smem + ((s - sa) & 1) * BUF;
+      if (8 * s + 8 > q.d / 8) {       // the last step's places past the end, of the tokens that this wave loaded
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (8 * s + xpiece[i] > xlast) *reinterpret_cast<u32x4*>(at + (2 * wave + i) * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+      }
+      __syncthreads();
+      if (s + 1 < s1) load(s + 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int xr = 16 * wave + m;
+        const u32x4 x = *reinterpret_cast<const u32x4*>(at + xr * ROWB + (((4 * h + kq) ^ (xr & 7)) << 4));
+#pragma unroll
+        for (int p = 0; p < RT; ++p) {
+          const int wr = 16 * p + m;
+          const u32x4 v = *reinterpret_cast<const u32x4*>(at + XB + wr * ROWB + (((4 * h + kq) ^ (wr & 7)) << 4));
+          acc[p] = mfma16<DT>(x, v, acc[p]);
+        }
+      }
+    }
+    const float f = q.splits == 1 && ad.alpha ? ad.alpha[a] : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int tok = 16 * wave + 4 * kq + e;
+      if (!((members >> tok) & 1)) continue;
+      float* o = out + ad.token(t0 + tok, g.n) * ad.rank;
 #pragma unroll
       for (int p = 0; p < RT; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) slot[(16 * i + 4 * kq + e) * LD + 16 * p + m] = acc[i][p][e];
-    __syncthreads();
-    const float f = splits == 1 && ad.alpha ? ad.alpha[a] : 1.f;
-#pragma unroll
-    for (int tok = tok0; tok < 64; tok += 64 / RT) {
-      const float* at = slots + tok * LD + col;
-      floatx4 v = *reinterpret_cast<const floatx4*>(at);
-#pragma unroll
-      for (int u = 1; u < 4; ++u) v += *reinterpret_cast<const floatx4*>(at + u * 64 * LD);
-      if (((members >> tok) & 1) && col < ad.rank) *reinterpret_cast<floatx4*>(out + ad.token(t0 + tok, n) * ad.rank + col) = f * v;
+        if (16 * p + m < ad.rank) o[16 * p + m] = f * acc[p][e];
     }
-    __syncthreads();
+    __syncthreads();   // every wave has read the last step
   }
 }
 
+template <int DT, int RT>
+__global__ __launch_bounds__(256) void down_tiles_kernel(DownArgs g) {
+  __shared__ __align__(16) unsigned char smem[2 * (64 + 16 * RT) * 128];
+  down_tiles_body<DT, RT>(g, smem);
+}
+
 // S[t][p] = alpha_a (sum of the parts), four values per thread.
-__global__ __launch_bounds__(256) void scale_join_kernel(const float* __restrict__ part, int64_t n, Adapters ad, int splits,
-                                                         float* __restrict__ S) {
+__global__ __launch_bounds__(256) void scale_join_kernel(float* __restrict__ S, int64_t n, Adapters ad, int splits) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, all = n * ad.rank;
   if (i >= all) return;
+  const float* part = S + down_values(n, ad.rank);
   floatx4 v = *reinterpret_cast<const floatx4*>(part + i);
   for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const floatx4*>(part + s * all + i);
   const int a = adapter_of(ad, i / ad.rank, n);
@@ -239,97 +270,44 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs u) {
   store_out<YT>(u.out, t * u.ldo + j, v[0]);
 }
 
-// ---------------------------------------------------------------- transpose
-__global__ __launch_bounds__(256) void transpose16_kernel(const uint16_t* __restrict__ src, int64_t rows, int64_t cols,
-                                                          uint16_t* __restrict__ dst, int64_t ldd, int64_t row_tiles) {
-  __shared__ uint16_t tile[64][66];
-  const int64_t bt = blockIdx.x / row_tiles, rt = blockIdx.x - bt * row_tiles;
-  const int64_t ct_n = (cols + 63) / 64;
-  const int64_t a = bt / ct_n, ct = bt - a * ct_n;
+// ---------------------------------------------------------------- preparation
+// Everything that has to be laid out before the products, in one launch of
+// workgroups that each do one piece: they are small, and a launch each took
+// longer than the work.
+
+GPTQ_DEV void transpose_piece(const TransposeArgs& v, int64_t b, uint16_t (&tile)[64][66]) {
+  const int64_t row_tiles = (v.ldd + 63) / 64, ct_n = (v.cols + 63) / 64;
+  const int64_t bt = b / row_tiles, rt = b - bt * row_tiles, a = bt / ct_n, ct = bt - a * ct_n;
   const int64_t i0 = rt * 64, j0 = ct * 64;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int r = w; r < 64; r += 4) {
+  for (int r = w; r < 64; r += 16) {
     const int64_t i = i0 + r, j = j0 + lane;
-    tile[r][lane] = (i < rows && j < cols) ? src[(a * rows + i) * cols + j] : (uint16_t)0;
+    tile[r][lane] = (i < v.rows && j < v.cols) ? v.src[(a * v.rows + i) * v.cols + j] : (uint16_t)0;
   }
   __syncthreads();
-  for (int r = w; r < 64; r += 4) {
+  for (int r = w; r < 64; r += 16) {
     const int64_t j = j0 + r, i = i0 + lane;
-    if (j < cols && i < ldd) dst[(a * cols + j) * ldd + i] = tile[lane][r];
+    if (j < v.cols && i < v.ldd) v.dst[(a * v.cols + j) * v.ldd + i] = tile[lane][r];
   }
 }
 
-// ---------------------------------------------------------------- token lists
-// Workgroup a lists its adapter's tokens in ascending order.  It counts the
-// tokens of the adapters before it (c) and starts at 32 (ceil(c / 32) + a): the
-// next one starts at least count + 1 places further and on a multiple of 32.
-// No atomics, so the order is fixed.
-__global__ __launch_bounds__(1024) void token_lists_kernel(Adapters ad, int64_t n, int32_t* __restrict__ order,
-                                                           int32_t* __restrict__ start, int32_t* __restrict__ counts) {
-  __shared__ int below[16];
-  __shared__ int count[16];
-  const int a = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int less = 0;
-  for (int64_t t = threadIdx.x; t < n; t += 1024) {
-    const int v = adapter_of(ad, t, n);
-    less += v >= 0 && v < a;
-  }
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) less += __shfl_xor(less, m);
-  if (lane == 0) below[w] = less;
-  __syncthreads();
-  int before_all = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) before_all += below[i];
-  const int64_t first = 32 * ((int64_t)(before_all + 31) / 32 + a);
-  int64_t at = first;
-  for (int64_t t0 = 0; t0 < n; t0 += 1024) {
-    const int64_t t = t0 + threadIdx.x;
-    const bool in = adapter_of(ad, t, n) == a;
-    const uint64_t mask = __ballot(in);
-    if (lane == 0) count[w] = __popcll(mask);
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      before += i < w ? count[i] : 0;
-      all += count[i];
-    }
-    if (in) order[at + before + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)t;
-    at += all;
-    __syncthreads();
-  }
-  const int mine = (int)(at - first);
-  const int64_t next = 32 * ((int64_t)(before_all + mine + 31) / 32 + a + 1);
-  for (int64_t i = at + threadIdx.x; i < next; i += 1024) order[i] = -1;
-  if (threadIdx.x == 0) {
-    start[a] = (int32_t)first;
-    counts[a] = mine;
-    if (a == ad.m - 1) start[a + 1] = (int32_t)next;
-  }
+GPTQ_DEV void pad_piece(const PadArgs& v, int64_t n, int64_t b) {
+  const int64_t i = b * 1024 + threadIdx.x, per = v.kp >> 3, t = i / per, k = (i - t * per) * 8;
+  if (t >= n) return;
+  u32x4 x = {0u, 0u, 0u, 0u};
+  if (k < v.d) x = load8(v.src + t * v.lds + k, (int)min((int64_t)8, v.d - k), false);
+  *reinterpret_cast<u32x4*>(v.dst + t * v.kp + k) = x;
 }
 
-// All tokens by adapter, ascending, those without one last: workgroup a places the
-// tokens of adapter a (a == m: without) after those of the adapters before it.
-__global__ __launch_bounds__(1024) void token_order_kernel(Adapters ad, int64_t n, int32_t* __restrict__ order) {
-  __shared__ int below[16];
-  __shared__ int count[16];
+// Tokens of one adapter placed in ascending order from `at` on; `in` says whose.
+// Returns the place after the last.  No atomics, so the order is fixed.
+template <class In>
+GPTQ_DEV int64_t place_tokens(int64_t n, int64_t at, int32_t* order, int (&count)[16], const In& in) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const uint32_t a = blockIdx.x;   // as the unsigned adapter of a token, none being m
-  auto key = [&](int64_t t) { return min((uint32_t)adapter_of(ad, t, n), (uint32_t)ad.m); };
-  int less = 0;
-  for (int64_t t = threadIdx.x; t < n; t += 1024) less += key(t) < a;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) less += __shfl_xor(less, m);
-  if (lane == 0) below[w] = less;
-  __syncthreads();
-  int64_t at = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) at += below[i];
   for (int64_t t0 = 0; t0 < n; t0 += 1024) {
     const int64_t t = t0 + threadIdx.x;
-    const bool in = t < n && key(t) == a;
-    const uint64_t mask = __ballot(in);
+    const bool mine = t < n && in(t);
+    const uint64_t mask = __ballot(mine);
     if (lane == 0) count[w] = __popcll(mask);
     __syncthreads();
     int before = 0, all = 0;
@@ -338,31 +316,115 @@ __global__ __launch_bounds__(1024) void token_order_kernel(Adapters ad, int64_t 
       before += i < w ? count[i] : 0;
       all += count[i];
     }
-    if (in) order[at + before + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)t;
+    if (mine) order[at + before + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)t;
     at += all;
     __syncthreads();
+  }
+  return at;
+}
+
+// Tokens for which `in` holds, counted by the workgroup.
+template <class In>
+GPTQ_DEV int64_t count_tokens(int64_t n, int (&count)[16], const In& in) {
+  int c = 0;
+  for (int64_t t = threadIdx.x; t < n; t += 1024) c += in(t);
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) c += __shfl_xor(c, m);
+  if ((threadIdx.x & 63) == 0) count[threadIdx.x >> 6] = c;
+  __syncthreads();
+  int64_t all = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) all += count[i];
+  __syncthreads();
+  return all;
+}
+
+__global__ __launch_bounds__(1024) void prepare_adapters_kernel(PrepareArgs g) {
+  __shared__ uint16_t tile[64][66];
+  __shared__ int count[16];
+  const Adapters& ad = g.ad;
+  const int64_t n = g.n;
+  // an adapter as an unsigned number, m where a token has none
+  auto key = [&](int64_t t) { return min((uint32_t)adapter_of(ad, t, n), (uint32_t)ad.m); };
+  int64_t b = blockIdx.x;
+  if (b < g.order_blocks) {
+    // all tokens by adapter, ascending, those without one last
+    const uint32_t a = (uint32_t)b;
+    const int64_t at = count_tokens(n, count, [&](int64_t t) { return key(t) < a; });
+    place_tokens(n, at, g.order, count, [&](int64_t t) { return key(t) == a; });
+    return;
+  }
+  b -= g.order_blocks;
+  if (b < g.list_blocks) {
+    // an adapter's tokens from a multiple of 32 on: with c tokens of the adapters
+    // before it, list a starts at 32 (ceil(c / 32) + a), and the next one starts
+    // at least count + 1 places further
+    const uint32_t a = (uint32_t)b;
+    const int64_t c = count_tokens(n, count, [&](int64_t t) { return key(t) < a; });
+    const int64_t first = 32 * ((c + 31) / 32 + a);
+    const int64_t at = place_tokens(n, first, g.list, count, [&](int64_t t) { return key(t) == a; });
+    const int64_t next = 32 * ((c + at - first + 31) / 32 + a + 1);
+    for (int64_t i = at + threadIdx.x; i < next; i += 1024) g.list[i] = -1;
+    if (threadIdx.x == 0) {
+      g.start[a] = (int32_t)first;
+      g.count[a] = (int32_t)(at - first);
+      if ((int)a == ad.m - 1) g.start[a + 1] = (int32_t)next;
+    }
+    return;
+  }
+  b -= g.list_blocks;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (b < g.turn[i].blocks) return transpose_piece(g.turn[i], b, tile);
+    b -= g.turn[i].blocks;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (b < g.pad[i].blocks) return pad_piece(g.pad[i], n, b);
+    b -= g.pad[i].blocks;
   }
 }
 
 // The rank values in list order, transposed and split into three bf16 terms: the
-// gradients' operand as it is loaded.  One thread per rank row and eight places.
-__global__ __launch_bounds__(256) void sorted_terms_kernel(const float* __restrict__ V, int rank, const int32_t* __restrict__ order,
-                                                           const int32_t* __restrict__ used, int64_t places,
-                                                           uint16_t* __restrict__ terms) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// gradients' operand as it is loaded.  One thread per rank row and eight places;
+// it joins the parts that down_tiles_kernel left, and keeps the joined values
+// where `keep` says so.
+__global__ __launch_bounds__(256) void sorted_terms_kernel(TermsArgs g) {
+  const int rank = g.ad.rank;
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t one = g.places / 8 * rank;
+  const int which = i < one ? 0 : 1;
+  if (which) i -= one;
   const int64_t p8 = i / rank * 8;
   const int p = (int)(i % rank);
-  if (p8 >= *used) return;
-  float v[8];
+  if (p8 >= g.start[g.ad.m]) return;
+  float* S = g.S[which];
+  const int splits = g.splits[which];
+  const float* part = S + down_values(g.n, rank);
+  // every load unconditional (places without a token read token 0)
+  int tok[8];
+  float v[8], f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) tok[e] = g.list[p8 + e];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int t = order[p8 + e];
-    v[e] = t >= 0 ? V[(int64_t)t * rank + p] : 0.f;
+    const int64_t t = max(tok[e], 0);
+    v[e] = splits == 1 ? S[t * rank + p] : part[t * rank + p];
+    const int a = splits == 1 || !g.ad.alpha ? -1 : adapter_of(g.ad, t, g.n);
+    f[e] = a >= 0 ? g.ad.alpha[a] : 1.f;
+  }
+  for (int s = 1; s < splits; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += part[((int64_t)s * g.n + max(tok[e], 0)) * rank + p];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = tok[e] >= 0 ? v[e] * f[e] : 0.f;
+    if (splits > 1 && g.keep[which] && tok[e] >= 0) S[(int64_t)tok[e] * rank + p] = v[e];
   }
   u32x4 k[3];
   split8<3>(v, k);
 #pragma unroll
-  for (int u = 0; u < 3; ++u) *reinterpret_cast<u32x4*>(terms + ((int64_t)u * rank + p) * places + p8) = k[u];
+  for (int u = 0; u < 3; ++u) *reinterpret_cast<u32x4*>(g.terms[which] + ((int64_t)u * rank + p) * g.places + p8) = k[u];
 }
 
 // ---------------------------------------------------------------- gradients
@@ -379,27 +441,29 @@ __global__ __launch_bounds__(256) void sorted_terms_kernel(const float* __restri
 // there than on their five blocks of tokens); parts are added in order by
 // join_kernel.
 template <int DT, int RT>
-__global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ terms, int64_t places, const uint16_t* __restrict__ Z,
-                                                   int64_t cols, int64_t ldz, bool vec, int rank, const int32_t* __restrict__ order,
-                                                   const int32_t* __restrict__ start, const int32_t* __restrict__ counts, int up,
-                                                   float* __restrict__ G, int64_t items, int64_t col_blocks, int rank_blocks, int splits) {
+__global__ __launch_bounds__(256) void grad_kernel(GradArgs g) {
   const int lane = threadIdx.x & 63, m = lane & 15, kq = lane >> 4;
   int64_t b = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (b >= items) return;
-  const int64_t cb = b % col_blocks;
-  b /= col_blocks;
-  const int rb = (int)(b % rank_blocks);
-  b /= rank_blocks;
+  const GradProblem& q = g.p[b < g.p[0].items ? 0 : 1];
+  if (b >= g.p[0].items) b -= g.p[0].items;
+  if (b >= q.items) return;
+  const int rank = g.ad.rank, splits = q.splits;
+  const int64_t places = g.places, cols = q.cols, ldz = q.ldz;
+  const uint16_t* terms = q.terms;
+  const uint16_t* Z = q.Z;
+  const int32_t* order = g.list;
+  const int64_t cb = b % q.col_blocks;
+  b /= q.col_blocks;
+  const int rb = (int)(b % g.rank_blocks);
+  b /= g.rank_blocks;
   const int split = (int)(b % splits);
   const int a = (int)(b / splits);
-  const int64_t first = start[a];
-  const int count = counts[a];
-  // whole 16-byte loads where rows allow them: columns past the end repeat the
-  // last eight, whose results are dropped
+  const int64_t first = g.start[a];
+  const int count = g.count[a];
+  // columns past the end of Z's rows (a multiple of 8) repeat the last eight, whose
+  // results are dropped
   const int64_t jv = cb * 128 + 8 * m;
-  const bool whole = vec && cols % 8 == 0;
-  const int64_t j0 = whole ? min(jv, cols - 8) : jv;
-  const int valid = (int)max((int64_t)0, min((int64_t)8, cols - j0));
+  const int64_t j0 = min(jv, q.width - 8);
   const int p0 = rb * 16 * RT;
 
   floatx4 acc[RT][8];
@@ -428,8 +492,7 @@ __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ 
     for (int e = 0; e < 8; ++e) {
       int t = tok[e >> 2][e & 3];
       if (t < 0) t = spare;
-      if (whole) f.z[e] = *reinterpret_cast<const u32x4*>(Z + (int64_t)t * ldz + j0);
-      else f.z[e] = load8(Z + (int64_t)t * ldz + j0, valid, vec);
+      f.z[e] = *reinterpret_cast<const u32x4*>(Z + (int64_t)t * ldz + j0);
     }
 #pragma unroll
     for (int p = 0; p < RT; ++p)
@@ -466,20 +529,19 @@ __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ 
   }
 
   // row of the accumulator = rank, column = 8 (lane & 15) + u
-  const int64_t m_all = items / (col_blocks * rank_blocks * splits);
-  float* g = G + ((int64_t)split * m_all + a) * rank * cols;
+  float* to = q.G + ((int64_t)split * g.ad.m + a) * rank * cols;
 #pragma unroll
   for (int p = 0; p < RT; ++p) {
     const int pr = p0 + 16 * p + 4 * kq;
-    if (up) {
+    if (q.up) {
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (jv + u < cols && pr < rank) *reinterpret_cast<floatx4*>(g + (jv + u) * rank + pr) = acc[p][u];   // rank % 8 == 0
+        if (jv + u < cols && pr < rank) *reinterpret_cast<floatx4*>(to + (jv + u) * rank + pr) = acc[p][u];   // rank % 8 == 0
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (pr + i >= rank) continue;
-        float* o = g + (int64_t)(pr + i) * cols + jv;
+        float* o = to + (int64_t)(pr + i) * cols + jv;
         if (jv + 8 <= cols && cols % 4 == 0) {
           *reinterpret_cast<floatx4*>(o) = floatx4{acc[p][0][i], acc[p][1][i], acc[p][2][i], acc[p][3][i]};
           *reinterpret_cast<floatx4*>(o + 4) = floatx4{acc[p][4][i], acc[p][5][i], acc[p][6][i], acc[p][7][i]};
@@ -493,83 +555,121 @@ __global__ __launch_bounds__(256) void grad_kernel(const uint16_t* __restrict__ 
   }
 }
 
-__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int64_t n, int splits,
-                                                   float* __restrict__ out) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs g) {
+  int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int which = i < g.n[0] ? 0 : 1;
+  if (which) i -= g.n[0];
+  const int64_t n = g.n[which];
   if (i >= n) return;
+  const float* part = g.part[which];
   floatx4 v = *reinterpret_cast<const floatx4*>(part + i);
-  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const floatx4*>(part + s * n + i);
-  *reinterpret_cast<floatx4*>(out + i) = v;
+  for (int s = 1; s < g.splits[which]; ++s) v += *reinterpret_cast<const floatx4*>(part + s * n + i);
+  *reinterpret_cast<floatx4*>(g.out[which] + i) = v;
 }
 
 // Parts of the contraction of down_tiles_kernel: enough workgroups for the
-// chip, each wave left with two steps at least.
+// chip, two steps of 64 at least in each.
 int down_splits(int64_t n, int64_t d) {
   const int64_t tiles = (n + 63) / 64, steps = (d + 63) / 64;
-  int64_t splits = 512 / tiles;
-  splits = splits < steps / 8 ? splits : steps / 8;
-  return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
+  int64_t splits = 768 / tiles;
+  splits = splits < steps / 2 ? splits : steps / 2;
+  return splits < 1 ? 1 : (splits > 8 ? 8 : (int)splits);
 }
 
 // Whether each token is taken by itself: a few of them, or so many adapters that a
 // tile would hold ten and more.
 bool by_token(int64_t n, int m) { return n <= 64 || n <= 4 * (int64_t)m; }
 
+// Rank rows of a gradient wave: 32 (64 would leave one wave per SIMD).
+int grad_rows(int rank) { return rank <= 16 ? 16 : 32; }
+
+int grad_splits(int64_t n, int m, int64_t cols, int rank) {
+  if (n == 0 || cols == 0) return 1;
+  const int64_t waves = (cols + 127) / 128 * m * ((rank + grad_rows(rank) - 1) / grad_rows(rank));
+  int64_t splits = (2048 + waves - 1) / waves;
+  const int64_t most = (n + m - 1) / m / 64;   // two blocks of tokens each
+  splits = splits < most ? splits : most;
+  return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
+}
+
+int64_t align64(int64_t floats) { return (floats + 63) / 64 * 64; }
+
 }  // namespace
 
-template <int DT, int RT, bool FAST, class... Args>
-static void launch_down_tiles(dim3 grid, hipStream_t s, Args... args) {
-  constexpr int LDS = 4 * 64 * (16 * RT + 4) * 4;
-  static const bool set = [] {   // once, thread-safe
-    (void)hipFuncSetAttribute((const void*)down_tiles_kernel<DT, RT, FAST>, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
-    return true;
-  }();
-  (void)set;
-  hipLaunchKernelGGL((down_tiles_kernel<DT, RT, FAST>), grid, dim3(256), LDS, s, args...);
-}
-
+// ---------------------------------------------------------------- launches
 int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank) {
-  const int64_t one = (n * rank + 63) / 64 * 64;
   const int splits = n <= 64 ? 1 : down_splits(n, d);
-  return splits == 1 ? one : one + splits * n * rank;
+  return splits == 1 ? down_values(n, rank) : down_values(n, rank) + splits * n * rank;
 }
 
-void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ldx, const Adapters& ad, const uint16_t* A,
-                         int64_t lda, float* S, hipStream_t s) {
-  const dim3 block(256);
-  const bool vec = rows_on_16(X, ldx, xt);
-  const auto* x = static_cast<const uint16_t*>(X);
-  if (by_token(n, ad.m)) {
-    const dim3 grid((unsigned)((n * ad.rank + 3) / 4));
-    if (xt == kBF16) hipLaunchKernelGGL((down_kernel<kBF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
-    else hipLaunchKernelGGL((down_kernel<kF16>), grid, block, 0, s, x, n, d, ldx, ad, A, lda, vec, S);
-    return;
+int adapter_down_parts(int64_t n, int m, int64_t d) { return by_token(n, m) ? 1 : down_splits(n, d); }
+
+bool adapter_rows_direct(const void* X, int64_t n, int64_t d, int64_t ldx, int m) {
+  return (reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0 && d % 8 == 0) || by_token(n, m);
+}
+
+void launch_prepare_adapters(const PrepareArgs& given, hipStream_t s) {
+  PrepareArgs g = given;
+  g.order_blocks = g.order ? g.ad.m + 1 : 0;
+  g.list_blocks = g.list ? g.ad.m : 0;
+  int64_t blocks = (int64_t)g.order_blocks + g.list_blocks;
+  for (auto& v : g.turn) {
+    v.blocks = v.src ? (v.ldd + 63) / 64 * ((v.cols + 63) / 64) * g.ad.m : 0;
+    blocks += v.blocks;
   }
-  const int splits = down_splits(n, d);
-  float* out = splits == 1 ? S : S + (n * ad.rank + 63) / 64 * 64;
-  const dim3 grid((unsigned)((n + 63) / 64 * splits));
-#define GPTQ_DOWN(D_, R_)                                                                                                    \
-  (vec && d % 64 == 0 ? launch_down_tiles<D_, R_, true>(grid, s, x, n, d, ldx, ad, A, lda, vec, out, splits)                 \
-                      : launch_down_tiles<D_, R_, false>(grid, s, x, n, d, ldx, ad, A, lda, vec, out, splits))
-#define GPTQ_DOWN_R(D_)                     \
-  do {                                      \
-    if (ad.rank <= 16) GPTQ_DOWN(D_, 1);    \
-    else if (ad.rank <= 32) GPTQ_DOWN(D_, 2); \
-    else if (ad.rank <= 64) GPTQ_DOWN(D_, 4); \
-    else GPTQ_DOWN(D_, 8);                  \
+  for (auto& v : g.pad) {
+    v.kp = gemm16_depth(v.d);
+    v.blocks = v.src ? (g.n * (v.kp / 8) + 1023) / 1024 : 0;
+    blocks += v.blocks;
+  }
+  if (blocks) hipLaunchKernelGGL(prepare_adapters_kernel, dim3((unsigned)blocks), dim3(1024), 0, s, g);
+}
+
+bool adapters_want_order(int64_t n, int m, const int32_t* index) { return index && m > 1 && !by_token(n, m); }
+
+int launch_adapter_down(const DownArgs& given, int xt, bool join, hipStream_t s) {
+  DownArgs g = given;
+  const dim3 block(256);
+  const int problems = g.p[1].X ? 2 : 1;
+  for (auto& q : g.p) {
+    q.splits = 1;
+    q.vec = rows_on_16(q.X, q.ldx, kBF16);
+  }
+  if (by_token(g.n, g.ad.m)) {
+    const dim3 grid((unsigned)((problems * g.n * g.ad.rank + 3) / 4));
+    if (xt == kBF16) hipLaunchKernelGGL((down_kernel<kBF16>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((down_kernel<kF16>), grid, block, 0, s, g);
+    return 1;
+  }
+  int64_t blocks = 0;
+  for (int i = 0; i < problems; ++i) {
+    g.p[i].splits = down_splits(g.n, g.p[i].d);
+    blocks += (g.n + 63) / 64 * g.p[i].splits;
+    if (i == 0) g.blocks0 = blocks;
+  }
+  const dim3 grid((unsigned)blocks);
+#define GPTQ_DOWN(D_)                                                                              \
+  do {                                                                                             \
+    if (g.ad.rank <= 16) hipLaunchKernelGGL((down_tiles_kernel<D_, 1>), grid, block, 0, s, g);     \
+    else if (g.ad.rank <= 32) hipLaunchKernelGGL((down_tiles_kernel<D_, 2>), grid, block, 0, s, g); \
+    else if (g.ad.rank <= 64) hipLaunchKernelGGL((down_tiles_kernel<D_, 4>), grid, block, 0, s, g); \
+    else hipLaunchKernelGGL((down_tiles_kernel<D_, 8>), grid, block, 0, s, g);                     \
   } while (0)
-  if (xt == kBF16) GPTQ_DOWN_R(kBF16);
-  else GPTQ_DOWN_R(kF16);
-#undef GPTQ_DOWN_R
+  if (xt == kBF16) GPTQ_DOWN(kBF16);
+  else GPTQ_DOWN(kF16);
 #undef GPTQ_DOWN
-  if (splits > 1)
-    hipLaunchKernelGGL(scale_join_kernel, dim3((unsigned)((n * ad.rank / 4 + 255) / 256)), block, 0, s, out, n, ad, splits, S);
+  if (join && g.p[0].splits > 1) {
+    hipLaunchKernelGGL(scale_join_kernel, dim3((unsigned)((g.n * g.ad.rank / 4 + 255) / 256)), block, 0, s, g.p[0].S, g.n, g.ad,
+                       g.p[0].splits);
+    return 1;
+  }
+  return g.p[0].splits;
 }
 
 void launch_adapter_up(const UpArgs& given, int xt, int yt, hipStream_t s) {
   UpArgs u = given;
   u.col_tiles = (u.rows + 255) / 256;
-  u.vec_base = u.part ? rows_on_16(u.part, u.rows, 0) : rows_on_16(u.base, u.ldb, yt);
+  u.vec_base = u.part ? rows_on_16(u.part, u.rows, 0) && u.n * u.rows % 4 == 0 : rows_on_16(u.base, u.ldb, yt);
   u.vec_out = rows_on_16(u.out, u.ldo, yt);
   const bool few = u.n <= 64 || (u.S && by_token(u.n, u.ad.m));
   const dim3 grid((unsigned)((few ? u.n : (u.n + 31) / 32) * u.col_tiles)), block(256);
@@ -583,60 +683,50 @@ void launch_adapter_up(const UpArgs& given, int xt, int yt, hipStream_t s) {
 #undef GPTQ_UP
 }
 
-void launch_transpose16(const uint16_t* src, int m, int64_t rows, int64_t cols, uint16_t* dst, int64_t ldd, hipStream_t s) {
-  const int64_t rt = (ldd + 63) / 64;
-  hipLaunchKernelGGL(transpose16_kernel, dim3((unsigned)(rt * ((cols + 63) / 64) * m)), dim3(256), 0, s, src, rows, cols, dst,
-                     ldd, rt);
-}
-
-bool adapters_want_order(int64_t n, int m, const int32_t* index) { return index && m > 1 && !by_token(n, m); }
-
-void launch_token_order(const Adapters& ad, int64_t n, int32_t* order, hipStream_t s) {
-  hipLaunchKernelGGL(token_order_kernel, dim3((unsigned)ad.m + 1), dim3(1024), 0, s, ad, n, order);
-}
-
-void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, int32_t* count, hipStream_t s) {
-  hipLaunchKernelGGL(token_lists_kernel, dim3((unsigned)ad.m), dim3(1024), 0, s, ad, n, order, start, count);
-}
-
-void launch_sorted_terms(const float* V, int rank, const int32_t* order, const int32_t* used, int64_t places, uint16_t* terms,
-                         hipStream_t s) {
-  hipLaunchKernelGGL(sorted_terms_kernel, dim3((unsigned)((places / 8 * rank + 255) / 256)), dim3(256), 0, s, V, rank, order, used, places,
-                     terms);
-}
-
-// Rank rows of a gradient wave: 32 (64 would leave one wave per SIMD).
-int grad_rows(int rank) { return rank <= 16 ? 16 : 32; }
-
-int adapter_grad_splits(int64_t n, int m, int64_t cols, int rank) {
-  if (n == 0 || cols == 0) return 1;
-  const int64_t waves = (cols + 127) / 128 * m * ((rank + grad_rows(rank) - 1) / grad_rows(rank));
-  int64_t splits = (2048 + waves - 1) / waves;
-  const int64_t most = (n + m - 1) / m / 64;   // two blocks of tokens each
-  splits = splits < most ? splits : most;
-  return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
-}
-
-void launch_adapter_grad(const uint16_t* terms, int64_t places, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz,
-                         const Adapters& ad, const int32_t* order, const int32_t* start, const int32_t* count, int up, float* G,
-                         float* part, int splits, hipStream_t s) {
-  const bool vec = rows_on_16(Z, ldz, zt);
-  const int rt = grad_rows(ad.rank);
-  const int rb = (ad.rank + rt - 1) / rt;
-  const int64_t cb = (cols + 127) / 128, items = cb * rb * splits * ad.m;
-  const dim3 grid((unsigned)((items + 3) / 4)), block(256);
-  float* dst = splits > 1 ? part : G;
-  const auto* z = static_cast<const uint16_t*>(Z);
-#define GPTQ_GRAD(D_, R_)                                                                                                       \
-  hipLaunchKernelGGL((grad_kernel<D_, R_>), grid, block, 0, s, terms, places, z, cols, ldz, vec, ad.rank, order, start, count, up, dst, \
-                     items, cb, rb, splits)
-  if (zt == kBF16) { if (rt == 16) GPTQ_GRAD(kBF16, 1); else GPTQ_GRAD(kBF16, 2); }
-  else { if (rt == 16) GPTQ_GRAD(kF16, 1); else GPTQ_GRAD(kF16, 2); }
-#undef GPTQ_GRAD
-  if (splits > 1) {
-    const int64_t all = (int64_t)ad.m * ad.rank * cols;   // rank is a multiple of 8: whole vectors
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)((all / 4 + 255) / 256)), dim3(256), 0, s, part, all, splits, G);
+int64_t adapter_grad_floats(int64_t n, int m, int64_t r, int64_t c, int rank) {
+  int64_t floats = 0;
+  for (const int64_t cols : {c, r}) {
+    const int splits = grad_splits(n, m, cols, rank);
+    if (splits > 1) floats += align64(splits * m * rank * cols);
   }
+  return floats;
+}
+
+void launch_adapter_grads(const TermsArgs& terms, const GradArgs& given, int zt, float* gA, float* gB, float* part, hipStream_t s) {
+  const dim3 block(256);
+  if (terms.n > 0)
+    hipLaunchKernelGGL(sorted_terms_kernel, dim3((unsigned)((2 * (terms.places / 8) * terms.ad.rank + 255) / 256)), block, 0, s, terms);
+  GradArgs g = given;
+  const int rt = grad_rows(g.ad.rank);
+  g.rank_blocks = (g.ad.rank + rt - 1) / rt;
+  JoinArgs j{};
+  for (int i = 0; i < 2; ++i) {
+    GradProblem& q = g.p[i];
+    float* out = i == 0 ? gA : gB;
+    q.splits = grad_splits(terms.n, g.ad.m, q.cols, g.ad.rank);
+    q.col_blocks = (q.cols + 127) / 128;
+    q.items = q.col_blocks * g.rank_blocks * q.splits * g.ad.m;
+    q.G = out;
+    if (q.splits > 1) {
+      const int64_t all = (int64_t)g.ad.m * g.ad.rank * q.cols;   // rank is a multiple of 8: whole vectors
+      const int k = j.n[0] ? 1 : 0;
+      q.G = part;
+      j.part[k] = part;
+      j.out[k] = out;
+      j.n[k] = all;
+      j.splits[k] = q.splits;
+      part += align64(q.splits * all);
+    }
+  }
+  const dim3 grid((unsigned)((g.p[0].items + g.p[1].items + 3) / 4));
+  if (zt == kBF16) {
+    if (rt == 16) hipLaunchKernelGGL((grad_kernel<kBF16, 1>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((grad_kernel<kBF16, 2>), grid, block, 0, s, g);
+  } else {
+    if (rt == 16) hipLaunchKernelGGL((grad_kernel<kF16, 1>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((grad_kernel<kF16, 2>), grid, block, 0, s, g);
+  }
+  if (j.n[0]) hipLaunchKernelGGL(join_kernel, dim3((unsigned)(((j.n[0] + j.n[1]) / 4 + 255) / 256)), block, 0, s, j);
 }
 
 }  // namespace gptq

@@ -398,16 +398,66 @@ GPTQ_DEV u32x4 pair_order(u32x4 v) {
 // ---------------------------------------------------------------- launches
 // xt / dt: 1 bf16, 2 fp16; yt: 0 fp32, 1 bf16, 2 fp16.
 
-// S[t][p] = alpha sum_k X[t][k] A_a[p][k], A with row stride lda (a multiple
-// of 8, zero past d) -- adapter.hip.  S: n x rank results (on 16 bytes) in
-// adapter_down_floats() of workspace.
+// S[t][p] = alpha sum_k X[t][k] A_a[p][k]: X [n][ldx] (d columns), A [m][rank][lda]
+// on 16 bytes, lda a multiple of 8 and zero past d.  S: n x rank results in
+// adapter_down_floats() of workspace, in which the parts of a split contraction
+// follow the results.  Up to two such problems in one launch (p[1].X null: one);
+// X as adapter_rows_direct says.  join: the one problem's parts are joined (else
+// the reader joins them).  Returns the parts of p[0], 1 once joined.
+inline __host__ __device__ int64_t down_values(int64_t n, int64_t rank) { return (n * rank + 63) / 64 * 64; }
+struct DownProblem {
+  const uint16_t* X;
+  int64_t d, ldx;
+  const uint16_t* A;
+  int64_t lda;
+  float* S;
+  bool vec;        // set by the launch, as splits
+  int splits;
+};
+struct DownArgs {
+  Adapters ad;
+  int64_t n;
+  DownProblem p[2];
+  int64_t blocks0; // set by the launch
+};
 int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank);
-// Whether tokens are to be taken adapter by adapter (ad.order, below), and that order:
-// all n tokens by adapter, ascending, those without one last.
+int launch_adapter_down(const DownArgs& g, int xt, bool join, hipStream_t s);
+// The parts that a launch leaves of a problem.
+int adapter_down_parts(int64_t n, int m, int64_t d);
+// Whether rows can be a down problem's X as they are (else padded, see below).
+bool adapter_rows_direct(const void* X, int64_t n, int64_t d, int64_t ldx, int m);
+
+// What is laid out before the products, each piece where its pointer is set:
+// order: all n tokens by adapter (adapters_want_order);
+// list: tokens by adapter: list[start[a]] .. are the count[a] tokens of adapter a,
+//   ascending, then -1 up to start[a + 1]; starts are multiples of 32;
+// turn: dst[a][j][i] = src[a][i][j] of m matrices, src [rows][cols] dense, dst row
+//   stride ldd >= rows, zero in columns rows .. ldd-1;
+// pad: dst[t][0 .. gemm16_depth(d)) = src[t][0 .. d) and zeros.
 bool adapters_want_order(int64_t n, int m, const int32_t* index);
-void launch_token_order(const Adapters& ad, int64_t n, int32_t* order, hipStream_t s);
-void launch_adapter_down(const void* X, int xt, int64_t n, int64_t d, int64_t ldx, const Adapters& ad, const uint16_t* A,
-                         int64_t lda, float* S, hipStream_t s);
+inline int64_t list_places(int64_t n, int64_t m) { return (n + 31) / 32 * 32 + 32 * m; }
+struct TransposeArgs {
+  const uint16_t* src;
+  int64_t rows, cols;
+  uint16_t* dst;
+  int64_t ldd, blocks;
+};
+struct PadArgs {
+  const uint16_t* src;
+  int64_t d, lds;
+  uint16_t* dst;
+  int64_t kp, blocks;
+};
+struct PrepareArgs {
+  Adapters ad;
+  int64_t n;
+  int32_t *order, *list, *start, *count;
+  int order_blocks, list_blocks;   // set by the launch, as blocks and kp
+  TransposeArgs turn[2];
+  PadArgs pad[2];
+};
+void launch_prepare_adapters(const PrepareArgs& g, hipStream_t s);
+
 // out = base + S B^T, of type yt.  base: of the same type (null: 0), or the sum of
 // `splits` parts [n][rows] fp32 times 2^ex[t] (ex null: 1).  S null: no adapters.
 struct UpArgs {
@@ -426,24 +476,36 @@ struct UpArgs {
   bool vec_base, vec_out;
 };
 void launch_adapter_up(const UpArgs& u, int xt, int yt, hipStream_t s);
-// dst[a][j][i] = src[a][i][j] of m matrices, src [rows][cols] dense, dst row
-// stride ldd >= rows, zero in columns rows .. ldd-1.
-void launch_transpose16(const uint16_t* src, int m, int64_t rows, int64_t cols, uint16_t* dst, int64_t ldd, hipStream_t s);
-// Token lists by adapter: order[start[a]] .. are the count[a] tokens of adapter a,
-// ascending, then -1 up to start[a + 1]; starts are multiples of 32.
-inline int64_t list_places(int64_t n, int64_t m) { return (n + 31) / 32 * 32 + 32 * m; }
-void launch_token_lists(const Adapters& ad, int64_t n, int32_t* order, int32_t* start, int32_t* count, hipStream_t s);
-// terms[k][p][i] = k-th bf16 term of V[order[i]][p] (0 where order[i] is -1).
-// used: start[m], on the device.
-void launch_sorted_terms(const float* V, int rank, const int32_t* order, const int32_t* used, int64_t places, uint16_t* terms,
-                         hipStream_t s);
-// G[a][p][j] (up == 0) or G[a][j][p] (up == 1) = sum over a's tokens of
-// V[t][p] Z[t][j], V as sorted terms.  part: workspace of `splits` partial
-// results (splits > 1).
-int adapter_grad_splits(int64_t n, int m, int64_t cols, int rank);
-void launch_adapter_grad(const uint16_t* terms, int64_t places, const void* Z, int zt, int64_t n, int64_t cols, int64_t ldz,
-                         const Adapters& ad, const int32_t* order, const int32_t* start, const int32_t* count, int up, float* G,
-                         float* part, int splits, hipStream_t s);
+// gA[a][p][k] = sum over a's tokens of T[t][p] X[t][k] and gB[a][i][p] = ... S[t][p]
+// dY[t][i], from the rank values S[0] = T and S[1] = S in list order: terms[w][k][p][i]
+// is the k-th bf16 term of S[w][list[i]][p] (0 where list[i] is -1).
+struct TermsArgs {
+  Adapters ad;
+  int64_t n, places;
+  const int32_t *list, *start;
+  float* S[2];
+  int splits[2];       // parts that down left
+  bool keep[2];        // joined values are written to S
+  uint16_t* terms[2];
+};
+struct GradProblem {
+  const uint16_t* terms;
+  const uint16_t* Z;   // rows on 16 bytes
+  int64_t cols, ldz, width;   // width: columns that can be read, a multiple of 8
+  int up;              // 0: G[a][p][j], 1: G[a][j][p]
+  float* G;            // set by the launch, as what follows
+  int splits;
+  int64_t col_blocks, items;
+};
+struct GradArgs {
+  Adapters ad;
+  int64_t places;
+  const int32_t *list, *start, *count;
+  int rank_blocks;     // set by the launch
+  GradProblem p[2];    // gA, gB
+};
+int64_t adapter_grad_floats(int64_t n, int m, int64_t r, int64_t c, int rank);
+void launch_adapter_grads(const TermsArgs& terms, const GradArgs& g, int zt, float* gA, float* gB, float* part, hipStream_t s);
 
 // out = X W^T (+ S B^T): gemm16.hip.  The contraction has kp columns, a
 // multiple of its step, with zeros in W past the last one (and finite values

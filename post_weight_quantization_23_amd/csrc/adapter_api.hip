@@ -132,11 +132,37 @@ int64_t forward_bytes(int64_t n, int64_t r, int64_t c, bool perm, int yt) {
 int64_t low_bytes(int64_t n, int64_t d, int64_t rank) { return rank > 0 ? align256(gptq::adapter_down_floats(n, d, rank) * 4) : 0; }
 int64_t order_bytes(int64_t n, int64_t rank) { return rank > 0 ? align256(n * 4) : 0; }
 
-// Adapters with their tokens' order, where that helps.
-void set_order(gptq::Adapters& ad, int64_t n, int32_t* place, hipStream_t s) {
-  if (!gptq::adapters_want_order(n, ad.m, ad.index)) return;
-  gptq::launch_token_order(ad, n, place, s);
-  ad.order = place;
+// A padded copy of n rows of d values for the rank values' product, where the
+// rows themselves will not do.
+int64_t rows_bytes(int64_t n, int64_t d, int64_t rank) { return rank > 0 ? align256(n * gptq::gemm16_depth(d) * 2) : 0; }
+
+// Lays out what the adapters need (g's other pieces with it) and sets their order.
+void prepare(gptq::PrepareArgs& g, gptq::Adapters& ad, int32_t* order, hipStream_t s) {
+  g.ad = ad;
+  if (gptq::adapters_want_order(g.n, ad.m, ad.index)) g.order = order;
+  gptq::launch_prepare_adapters(g, s);
+  ad.order = g.order;
+}
+
+// One side of the rank values: rows of X or their padded copy.
+gptq::DownProblem down_problem(const void* X, int64_t n, int64_t d, int64_t ldx, const uint16_t* A, int64_t lda, float* S,
+                               uint16_t* rows, int m, gptq::PadArgs& pad) {
+  gptq::DownProblem q{};
+  q.X = static_cast<const uint16_t*>(X);
+  q.d = d;
+  q.ldx = ldx;
+  if (!gptq::adapter_rows_direct(X, n, d, ldx, m)) {
+    pad.src = q.X;
+    pad.d = d;
+    pad.lds = ldx;
+    pad.dst = rows;
+    q.X = rows;
+    q.d = q.ldx = gptq::gemm16_depth(d);
+  }
+  q.A = A;
+  q.lda = lda;
+  q.S = S;
+  return q;
 }
 
 // Every launch's grid, at the launch helpers' workgroup shapes.
@@ -150,7 +176,7 @@ bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
          groups_for(n * (c / 8), 256) <= kMaxGroups256 &&                                // gather
          n * groups_for(r > c ? r : c, 256) <= kMaxGroups256 * (n > 64 && n > 4 * m ? 32 : 1) &&   // up
          groups_for(gptq::list_places(n, m) / 8 * (rank > 0 ? rank : 1), 256) <= kMaxGroups256 && gptq::list_places(n, m) < INT_MAX &&  // lists
-         m * groups_for(r > c ? r : c, 64) * 2 <= kMaxGroups256 &&                       // transpose (rank <= 128)
+         m * groups_for(r > c ? r : c, 64) * 5 + groups_for(n * (r + c) / 8 + 16, 1024) <= kMaxGroups256 / 4 &&   // preparation (1024 threads)
          m * groups_for(r > c ? r : c, 128) * 16 <= kMaxGroups256 &&                     // gradients (16 splits of 4 rank blocks, 4 a group)
          groups_for(m * rank * (r > c ? r : c), 1024) <= kMaxGroups256;                  // join
 }
@@ -163,20 +189,16 @@ int64_t backward_bytes(int64_t n, int64_t r, int64_t c, int xt, int ot) {
 }
 
 struct GradSizes {
-  int sa, sb;                       // token splits of gA and gB
   int64_t places, part, lists, terms, total;
 };
 
 GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
   GradSizes z;
-  z.sa = gptq::adapter_grad_splits(n, (int)m, c, (int)rank);
-  z.sb = gptq::adapter_grad_splits(n, (int)m, r, (int)rank);
-  const int64_t pa = z.sa > 1 ? z.sa * m * rank * c * 4 : 0, pb = z.sb > 1 ? z.sb * m * rank * r * 4 : 0;
-  z.part = align256(pa > pb ? pa : pb);
+  z.part = align256(gptq::adapter_grad_floats(n, (int)m, r, c, (int)rank) * 4);
   z.places = gptq::list_places(n, m);
   z.lists = align256(z.places * 4) + align256((m + 1) * 4) + align256(m * 4);
   z.terms = align256(3 * rank * z.places * 2);
-  z.total = order_bytes(n, rank) + align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + low_bytes(n, c, rank) + low_bytes(n, r, rank) + z.lists + 2 * z.terms + z.part;
+  z.total = order_bytes(n, rank) + rows_bytes(n, r, rank) + rows_bytes(n, c, rank) + align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + low_bytes(n, c, rank) + low_bytes(n, r, rank) + z.lists + 2 * z.terms + z.part;
   return z;
 }
 
@@ -194,7 +216,7 @@ gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t r, int64_t c, g
   if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
   if (rank != 0)
     if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank));
+  *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank) + rows_bytes(n, c, rank));
   return ok();
 }
 
@@ -226,7 +248,7 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
     if (gptq_status st = check_clash(fn, clash(Y, ey, A, m * rank, c, c, 2))) return st;
     if (gptq_status st = check_clash(fn, clash(Y, ey, B, m * r, rank, rank, 2))) return st;
   }
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, forward_bytes(n, r, c, perm != nullptr, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, forward_bytes(n, r, c, perm != nullptr, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank) + rows_bytes(n, c, rank))) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const gptq::PackedLayer w = layer(packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm);
@@ -236,8 +258,16 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
   float* S = nullptr;
   if (low) {
     S = carve.take<float>(low_bytes(n, c, rank));
-    set_order(ad, n, carve.take<int32_t>(n * 4), s);
-    gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
+    int32_t* order = carve.take<int32_t>(n * 4);
+    uint16_t* rows = carve.take<uint16_t>(rows_bytes(n, c, rank));
+    gptq::PrepareArgs g{};
+    g.n = n;
+    gptq::DownArgs d{};
+    d.n = n;
+    d.p[0] = down_problem(X, n, c, ldx, ad.A, c, S, rows, ad.m, g.pad[0]);
+    prepare(g, ad, order, s);
+    d.ad = ad;
+    gptq::launch_adapter_down(d, xi, true, s);
   }
   if (gptq::packed_tiles(n, c)) {
     gptq::launch_packed_tiles(X, xi, n, ldx, w, ad, S, Y, yi, ldy, carve.at, s);
@@ -266,7 +296,7 @@ gptq_status gptq_packed_linear_backward_workspace_size(int64_t n, int64_t r, int
   if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
   *bytes = (size_t)(backward_bytes(n, r, c, (int)xt, (int)ot) + align256(m * c * rank * 2) +
-                    align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank) + order_bytes(n, rank));
+                    align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank) + order_bytes(n, rank) + rows_bytes(n, r, rank));
   return ok();
 }
 
@@ -302,7 +332,7 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
   }
   const int terms = gptq::gemm16_terms((int)xt, (int)ot);
   const int64_t need = backward_bytes(n, r, c, (int)xt, (int)ot) + align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank) +
-                       order_bytes(n, rank);
+                       order_bytes(n, rank) + rows_bytes(n, r, rank);
   if (gptq_status st = need_ws(fn, ws, ws_bytes, need)) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -318,10 +348,18 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
     At = carve.take<uint16_t>(m * c * rank * 2);
     uint16_t* Bt = carve.take<uint16_t>(m * rank * pad8(r) * 2);
     T = carve.take<float>(low_bytes(n, r, rank));
-    set_order(ad, n, carve.take<int32_t>(n * 4), s);
-    gptq::launch_transpose16(ad.A, (int)m, rank, c, At, rank, s);
-    gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
-    gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);
+    int32_t* order = carve.take<int32_t>(n * 4);
+    uint16_t* padded = carve.take<uint16_t>(rows_bytes(n, r, rank));
+    gptq::PrepareArgs g{};
+    g.n = n;
+    g.turn[0] = {ad.A, rank, c, At, rank, 0};
+    g.turn[1] = {ad.B, r, rank, Bt, pad8(r), 0};
+    gptq::DownArgs d{};
+    d.n = n;
+    d.p[0] = down_problem(dY, n, r, ldy, Bt, pad8(r), T, padded, ad.m, g.pad[0]);
+    prepare(g, ad, order, s);
+    d.ad = ad;
+    gptq::launch_adapter_down(d, xi, true, s);
   }
   gptq::launch_packed_backward(dY, xi, n, ldy, w, ad, At, T, dX, ot == GPTQ_F32 ? 0 : xi, ldx, Wt, rows, part, s);
   return check_launch(fn);
@@ -333,7 +371,7 @@ gptq_status gptq_adapter_add_workspace_size(int64_t n, int64_t c, int64_t rank, 
   if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
   if (gptq_status st = check_sizes(fn, n, 0, c, 8)) return st;
   if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  *bytes = (size_t)(low_bytes(n, c, rank) + order_bytes(n, rank));
+  *bytes = (size_t)(low_bytes(n, c, rank) + order_bytes(n, rank) + rows_bytes(n, c, rank));
   return ok();
 }
 
@@ -358,14 +396,22 @@ gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n, int64_t c,
   if (gptq_status st = check_clash(fn, clash(out, eo, B, m * r, rank, rank, 2))) return st;
   if (!(out == Y && ldo == ldy))
     if (gptq_status st = check_clash(fn, clash(out, eo, Y, n, ldy, r, el))) return st;
-  if (gptq_status st = need_ws(fn, ws, ws_bytes, low_bytes(n, c, rank) + order_bytes(n, rank))) return st;
+  if (gptq_status st = need_ws(fn, ws, ws_bytes, low_bytes(n, c, rank) + order_bytes(n, rank) + rows_bytes(n, c, rank))) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
   Carve carve{static_cast<char*>(ws)};
   float* S = carve.take<float>(low_bytes(n, c, rank));
-  set_order(ad, n, carve.take<int32_t>(n * 4), s);
-  gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
+  int32_t* order = carve.take<int32_t>(n * 4);
+  uint16_t* rows = carve.take<uint16_t>(rows_bytes(n, c, rank));
+  gptq::PrepareArgs g{};
+  g.n = n;
+  gptq::DownArgs d{};
+  d.n = n;
+  d.p[0] = down_problem(X, n, c, ldx, ad.A, c, S, rows, ad.m, g.pad[0]);
+  prepare(g, ad, order, s);
+  d.ad = ad;
+  gptq::launch_adapter_down(d, xi, true, s);
   gptq::UpArgs u{};
   u.S = S; u.n = n; u.rows = r; u.ad = ad; u.B = ad.B; u.base = Y; u.ldb = ldy; u.out = out; u.ldo = ldo;
   gptq::launch_adapter_up(u, xi, yt == GPTQ_F32 ? 0 : xi, s);
@@ -423,29 +469,67 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   gptq::Adapters ad = adapters(A, B, m, rank, index, alpha);
   const int xi = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
   int32_t* by_adapter = carve.take<int32_t>(n * 4);
+  uint16_t* rows_y = carve.take<uint16_t>(rows_bytes(n, r, rank));
+  uint16_t* rows_x = carve.take<uint16_t>(rows_bytes(n, c, rank));
   uint16_t* Bt = carve.take<uint16_t>(m * rank * pad8(r) * 2);
   uint16_t* At = carve.take<uint16_t>(m * c * rank * 2);
   float* S = carve.take<float>(low_bytes(n, c, rank));
   float* T = carve.take<float>(low_bytes(n, r, rank));
-  int32_t* order = carve.take<int32_t>(z.places * 4);
-  int32_t* start = carve.take<int32_t>((m + 1) * 4);
-  int32_t* count = carve.take<int32_t>(m * 4);
+  gptq::PrepareArgs g{};
+  g.n = n;
+  g.list = carve.take<int32_t>(z.places * 4);
+  g.start = carve.take<int32_t>((m + 1) * 4);
+  g.count = carve.take<int32_t>(m * 4);
   uint16_t* Sx = carve.take<uint16_t>(z.terms);
   uint16_t* Tx = carve.take<uint16_t>(z.terms);
   float* part = carve.take<float>(z.part);
-  gptq::launch_token_lists(ad, n, order, start, count, s);
-  if (n > 0) {
-    set_order(ad, n, by_adapter, s);
-    gptq::launch_transpose16(ad.B, (int)m, r, rank, Bt, pad8(r), s);
-    gptq::launch_adapter_down(X, xi, n, c, ldx, ad, ad.A, c, S, s);
-    gptq::launch_adapter_down(dY, xi, n, r, ldy, ad, Bt, pad8(r), T, s);
-    gptq::launch_sorted_terms(S, (int)rank, order, start + m, z.places, Sx, s);
-    gptq::launch_sorted_terms(T, (int)rank, order, start + m, z.places, Tx, s);
-  }
-  gptq::launch_adapter_grad(Tx, z.places, X, xi, n, c, ldx, ad, order, start, count, 0, gA, part, z.sa, s);
-  gptq::launch_adapter_grad(Sx, z.places, dY, xi, n, r, ldy, ad, order, start, count, 1, gB, part, z.sb, s);
+  g.turn[0] = {ad.B, r, rank, Bt, pad8(r), 0};
+  if (dX) g.turn[1] = {ad.A, rank, c, At, rank, 0};
+  gptq::DownArgs d{};
+  d.n = n;
+  d.p[0] = down_problem(dY, n, r, ldy, Bt, pad8(r), T, rows_y, ad.m, g.pad[0]);
+  d.p[1] = down_problem(X, n, c, ldx, ad.A, c, S, rows_x, ad.m, g.pad[1]);
+  // the gradients read dY and X eight columns at a time in any case
+  gptq::GradArgs w{};
+  auto side = [&](gptq::GradProblem& q, const void* Z, int64_t cols, int64_t ldz, uint16_t* rows, gptq::PadArgs& pad,
+                  const uint16_t* terms, int up) {
+    q.cols = cols;
+    q.up = up;
+    q.terms = terms;
+    if (aligned(Z, 16) && ldz % 8 == 0 && cols % 8 == 0) {
+      q.Z = static_cast<const uint16_t*>(Z);
+      q.ldz = ldz;
+      q.width = cols;
+    } else {
+      pad.src = static_cast<const uint16_t*>(Z);
+      pad.d = cols;
+      pad.lds = ldz;
+      pad.dst = rows;
+      q.Z = rows;
+      q.ldz = q.width = gptq::gemm16_depth(cols);
+    }
+  };
+  side(w.p[0], X, c, ldx, rows_x, g.pad[1], Tx, 0);
+  side(w.p[1], dY, r, ldy, rows_y, g.pad[0], Sx, 1);
+  prepare(g, ad, by_adapter, s);
+  w.ad = d.ad = ad;
+  if (n > 0) gptq::launch_adapter_down(d, xi, false, s);
+  gptq::TermsArgs v{};
+  v.ad = ad;
+  v.n = n;
+  v.places = w.places = z.places;
+  v.list = w.list = g.list;
+  v.start = w.start = g.start;
+  w.count = g.count;
+  v.S[0] = T;
+  v.S[1] = S;
+  v.splits[0] = gptq::adapter_down_parts(n, ad.m, d.p[0].d);
+  v.splits[1] = gptq::adapter_down_parts(n, ad.m, d.p[1].d);
+  v.keep[0] = dX != nullptr;
+  v.terms[0] = Tx;
+  v.terms[1] = Sx;
+  gptq::launch_adapter_grads(v, w, xi, gA, gB, part, s);
   if (dX && n > 0) {
-    gptq::launch_transpose16(ad.A, (int)m, rank, c, At, rank, s);
     gptq::UpArgs u{};
     u.S = T; u.n = n; u.rows = c; u.ad = ad; u.B = At; u.base = base; u.ldb = ldd; u.out = dX; u.ldo = ldd;
     gptq::launch_adapter_up(u, xi, ot == GPTQ_F32 ? 0 : xi, s);
