@@ -191,27 +191,40 @@ __global__ __launch_bounds__(256) void scale_join_kernel(float* __restrict__ S, 
 }
 
 // ---------------------------------------------------------------- up
-// What the low-rank product is added to, k <= 8 outputs from column j of token t.
+// Sum of the parts of eight outputs (their rows are padded to whole eights), two
+// chains of adds so that four loads are in flight.
+GPTQ_DEV void join_parts(const UpArgs& u, int64_t t, int64_t j, float (&v)[8]) {
+  const float* p = u.part + t * u.ldp + j;
+  const int64_t step = u.n * u.ldp;
+  float a[8], b[8] = {};
+  load8f(p, a);
+  int s = 1;
+  for (; s + 1 < u.splits; s += 2) {
+    float x[8], y[8];
+    load8f(p + s * step, x);
+    load8f(p + (s + 1) * step, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] += x[e];
+      b[e] += y[e];
+    }
+  }
+  if (s < u.splits) {
+    float x[8];
+    load8f(p + s * step, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] += x[e];
+  }
+  const int ex = u.ex ? u.ex[t] : 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] += __builtin_ldexpf(a[e] + b[e], ex);
+}
+
+// What the low-rank product is added to, k <= 8 outputs from column j (a multiple of 8) of token t.
 template <int YT>
 GPTQ_DEV void add_base(const UpArgs& u, float (&v)[8], int64_t t, int64_t j, int k) {
   if (u.part) {
-    float sum[8] = {};
-    const int64_t at = t * u.rows + j;
-    for (int s = 0; s < u.splits; ++s) {
-      const float* p = u.part + s * u.n * u.rows + at;
-      if (k == 8 && u.vec_base) {
-        float w[8];
-        load8f(p, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += w[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < k) sum[e] += p[e];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += u.ex ? __builtin_ldexpf(sum[e], u.ex[t]) : sum[e];
+    join_parts(u, t, j, v);
   } else if (u.base) {
     if constexpr (YT == 0) {
       const float* p = static_cast<const float*>(u.base) + t * u.ldb + j;
@@ -251,7 +264,7 @@ __global__ __launch_bounds__(256) void up_tiles_kernel(UpArgs u) {
     row[q] = j < u.rows ? j : -1;
     acc[q] = floatx16{};
   }
-  if (u.S) expand_add<DT, YT == 0 ? 3 : 2, 2>(u.ad, u.B, u.rows, u.S, t0, u.n, row, acc);
+  expand_add<DT, YT == 0 ? 3 : 2, 2>(u.ad, u.B, u.rows, u.S, t0, u.n, row, acc);
   store_tile<YT, 2>(turn[wave], acc, u.ad, u.out, t0, u.n, j0, u.rows, u.ldo, u.vec_out,
                     [&](float (&v)[8], int64_t t, int64_t j, int k) { add_base<YT>(u, v, t, j, k); });
 }
@@ -264,11 +277,31 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs u) {
   const int64_t j = ct * 256 + threadIdx.x;
   if (j >= u.rows) return;
   float v[8] = {};
-  const int a = u.S ? adapter_of(u.ad, t, u.n) : -1;
+  const int a = adapter_of(u.ad, t, u.n);
   if (a >= 0) v[0] = rank_dot<DT>(u.S + t * u.ad.rank, u.B + ((int64_t)a * u.rows + j) * u.ad.rank, u.ad.rank);
-  add_base<YT>(u, v, t, j, 1);
+  if (u.part) {
+    float w[8] = {};
+    join_parts(u, t, j & ~(int64_t)7, w);
+    float mine = w[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) mine = (j & 7) == e ? w[e] : mine;
+    v[0] += mine;
+  } else {
+    add_base<YT>(u, v, t, j, 1);
+  }
   store_out<YT>(u.out, t * u.ldo + j, v[0]);
 }
+
+// Parts joined without adapters: a thread takes eight outputs of one token.
+template <int YT>
+__global__ __launch_bounds__(256) void join_rows_kernel(UpArgs u) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = u.ldp >> 3, t = i / per, j = (i - t * per) * 8;
+  if (t >= u.n) return;
+  float v[8] = {};
+  join_parts(u, t, j, v);
+  store8<YT>(u.out, t * u.ldo + j, v, (int)min((int64_t)8, u.rows - j), u.vec_out);
+}
+
 
 // ---------------------------------------------------------------- preparation
 // Everything that has to be laid out before the products, in one launch of
@@ -669,9 +702,16 @@ int launch_adapter_down(const DownArgs& given, int xt, bool join, hipStream_t s)
 void launch_adapter_up(const UpArgs& given, int xt, int yt, hipStream_t s) {
   UpArgs u = given;
   u.col_tiles = (u.rows + 255) / 256;
-  u.vec_base = u.part ? rows_on_16(u.part, u.rows, 0) && u.n * u.rows % 4 == 0 : rows_on_16(u.base, u.ldb, yt);
+  u.vec_base = rows_on_16(u.base, u.ldb, yt);
   u.vec_out = rows_on_16(u.out, u.ldo, yt);
-  const bool few = u.n <= 64 || (u.S && by_token(u.n, u.ad.m));
+  if (!u.S) {
+    const dim3 flat((unsigned)((u.n * (u.ldp / 8) + 255) / 256));
+    if (yt == 0) hipLaunchKernelGGL((join_rows_kernel<0>), flat, dim3(256), 0, s, u);
+    else if (yt == kBF16) hipLaunchKernelGGL((join_rows_kernel<kBF16>), flat, dim3(256), 0, s, u);
+    else hipLaunchKernelGGL((join_rows_kernel<kF16>), flat, dim3(256), 0, s, u);
+    return;
+  }
+  const bool few = by_token(u.n, u.ad.m);
   const dim3 grid((unsigned)((few ? u.n : (u.n + 31) / 32) * u.col_tiles)), block(256);
 #define GPTQ_UP(D_, Y_)                                                                \
   do {                                                                                 \

@@ -212,6 +212,36 @@ GPTQ_DEV float rank_dot(const float* S, const uint16_t* b, int rank) {
   return sum;
 }
 
+// out[q] += S B_a^T of one adapter's tokens among the Tile::E of a tile (accumulator
+// layout, row = place): a product over all of them, of which only the members'
+// rows are kept.  t: the token of the lane's place, or -1.
+template <int DT, int TERMS, int NT, class Acc>
+GPTQ_DEV void expand_shared(const Adapters& ad, int a, uint32_t members, const uint16_t* B, int64_t rows, const float* S, int64_t t,
+                            const int64_t (&row)[NT], Acc (&out)[NT]) {
+  using Tile = TileShape<Acc>;
+  const int lane = threadIdx.x & 63, kq = lane / Tile::E;
+  Acc acc[NT] = {};
+  for (int k0 = 0; k0 < ad.rank; k0 += Tile::K) {
+    const int k = k0 + 8 * kq;
+    float v[8] = {};
+    if (k < ad.rank && t >= 0) load8f(S + t * ad.rank + k, v);
+    u32x4 s[TERMS];
+    split8<TERMS>(v, s);
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      u32x4 b = {0u, 0u, 0u, 0u};
+      if (k < ad.rank && row[q] >= 0)
+        b = *reinterpret_cast<const u32x4*>(B + ((int64_t)a * rows + row[q]) * ad.rank + k);
+      acc[q] = mfma_terms<DT, TERMS>(s, Terms16<DT>(b), acc[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int i = 0; i < Tile::C; ++i)
+      if ((members >> Tile::acc_row(lane, i)) & 1) out[q][i] += acc[q][i];
+}
+
 // out[q] += (S B_a^T) of the tokens at places t0 .. and NT sets of a tile's outputs, in
 // the accumulator layout (row = place): the low-rank product beside a tile.
 // S [n][rank] fp32 already holds alpha; row[q] is this lane's output row
@@ -225,34 +255,33 @@ template <int DT, int TERMS, int NT, class Acc>
 GPTQ_DEV void expand_add(const Adapters& ad, const uint16_t* B, int64_t rows, const float* S, int64_t t0, int64_t n,
                          const int64_t (&row)[NT], Acc (&out)[NT]) {
   using Tile = TileShape<Acc>;
-  const int lane = threadIdx.x & 63, kq = lane / Tile::E;
-  const int64_t t = ad.token(t0 + lane % Tile::E, n);
+  const int64_t t = ad.token(t0 + (threadIdx.x & 63) % Tile::E, n);
   const int mine = adapter_of(ad, t, n);
   uint32_t rest = (uint32_t)(__ballot(mine >= 0) & ((1ull << Tile::E) - 1));
   while (rest) {
     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(rest));
     const uint32_t members = (uint32_t)(__ballot(mine == a) & ((1ull << Tile::E) - 1));
     rest &= ~members;
-    Acc acc[NT] = {};
-    for (int k0 = 0; k0 < ad.rank; k0 += Tile::K) {
-      const int k = k0 + 8 * kq;
-      float v[8] = {};
-      if (k < ad.rank && mine >= 0) load8f(S + t * ad.rank + k, v);
-      u32x4 s[TERMS];
-      split8<TERMS>(v, s);
-#pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        u32x4 b = {0u, 0u, 0u, 0u};
-        if (k < ad.rank && row[q] >= 0)
-          b = *reinterpret_cast<const u32x4*>(B + ((int64_t)a * rows + row[q]) * ad.rank + k);
-        acc[q] = mfma_terms<DT, TERMS>(s, Terms16<DT>(b), acc[q]);
-      }
+    expand_shared<DT, TERMS, NT>(ad, a, members, B, rows, S, t, row, out);
+  }
+}
+
+// The first k of eight outputs from `at`.  vec: eight start on 16 bytes there.
+template <int OT>
+GPTQ_DEV void store8(void* out, int64_t at, const float (&v)[8], int k, bool vec) {
+  if (vec && k == 8) {
+    if constexpr (OT == 0) {
+      float* o = static_cast<float*>(out) + at;
+      *reinterpret_cast<floatx4*>(o) = floatx4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<floatx4*>(o + 4) = floatx4{v[4], v[5], v[6], v[7]};
+    } else {
+      const u32x4 o = {pack2<OT>(v[0], v[1]), pack2<OT>(v[2], v[3]), pack2<OT>(v[4], v[5]), pack2<OT>(v[6], v[7])};
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + at) = o;
     }
+  } else {
 #pragma unroll
-    for (int q = 0; q < NT; ++q)
-#pragma unroll
-      for (int i = 0; i < Tile::C; ++i)
-        if ((members >> Tile::acc_row(lane, i)) & 1) out[q][i] += acc[q][i];
+    for (int e = 0; e < 8; ++e)
+      if (e < k) store_out<OT>(out, at + e, v[e]);
   }
 }
 
@@ -283,20 +312,7 @@ GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], const Adapters& 
     load8f(lds + r * LD + c, v);
     if (t < 0 || j >= cols) continue;
     more(v, t, j, (int)min((int64_t)8, cols - j));
-    if (vec && j + 8 <= cols) {
-      if constexpr (OT == 0) {
-        float* o = static_cast<float*>(out) + t * ldo + j;
-        *reinterpret_cast<floatx4*>(o) = floatx4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<floatx4*>(o + 4) = floatx4{v[4], v[5], v[6], v[7]};
-      } else {
-        const u32x4 o = {pack2<OT>(v[0], v[1]), pack2<OT>(v[2], v[3]), pack2<OT>(v[4], v[5]), pack2<OT>(v[6], v[7])};
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(out) + t * ldo + j) = o;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (j + e < cols) store_out<OT>(out, t * ldo + j + e, v[e]);
-    }
+    store8<OT>(out, t * ldo + j, v, (int)min((int64_t)8, cols - j), vec);
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
@@ -459,7 +475,9 @@ struct PrepareArgs {
 void launch_prepare_adapters(const PrepareArgs& g, hipStream_t s);
 
 // out = base + S B^T, of type yt.  base: of the same type (null: 0), or the sum of
-// `splits` parts [n][rows] fp32 times 2^ex[t] (ex null: 1).  S null: no adapters.
+// `splits` parts [n][ldp] fp32 times 2^ex[t] (ex null: 1), ldp = part_width(rows).
+// S null: no adapters, and parts to join.
+inline int64_t part_width(int64_t rows) { return (rows + 7) / 8 * 8; }
 struct UpArgs {
   const float* S;
   int64_t n, rows;
@@ -468,6 +486,7 @@ struct UpArgs {
   const void* base;
   int64_t ldb;
   const float* part;
+  int64_t ldp;
   int splits;
   const int32_t* ex;
   void* out;

@@ -112,10 +112,11 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
   float* own = reinterpret_cast<float*>(smem) + wave * 32 * (32 * NT + 4);
   __syncthreads();   // the last step's operands have been read
   if constexpr (PARTS) {
-    float* part = a.part + (int64_t)split * a.n * a.cols;
+    const int64_t ldp = (a.cols + 7) & ~7;
+    float* part = a.part + (int64_t)split * a.n * ldp;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      store_tile<0, NT>(own, acc[i], a.ad, part, t0 + wm + 32 * i, a.n, j0 + wn, a.cols, a.cols, a.vec);
+      store_tile<0, NT>(own, acc[i], a.ad, part, t0 + wm + 32 * i, a.n, j0 + wn, ldp, ldp, true);
     return;
   }
   int64_t col[NT];
@@ -153,24 +154,52 @@ void launch_gemm(Gemm16 a, hipStream_t s) {
                      dim3((unsigned)((int64_t)a.tok_tiles * a.col_tiles * a.splits)), dim3(64 * WM * WN), LDS, s, a);
 }
 
-// Tiles of 256 x 256 (8 waves) from 192 of them on, else 128 x 128 (4 waves), and
-// those in parts while they are too few for the chip.
-bool big_tiles(int64_t n, int64_t cols) { return (n + 255) / 256 * ((cols + 255) / 256) >= 192; }
+// Tiles: 256 x 256 (8 waves of 128 x 64), 128 x 128 (4 of 64 x 64), 96 and 64 x 128 (4 of
+// 96 or 64 x 32).  A launch takes as long as its fullest CU, ceil(tiles / 256) of
+// them, and a large tile reads less of LDS for each product.  A call of 1024 tokens
+// of 4096 x 4096 took 101, 59, 60 and 57 us in this order, of 2085 tokens 108, 116, 107
+// and 109, of 8192 254, 302, 331 and 340; the choice was within 12 % of the best
+// on 44 sizes (512 to 8192 tokens, four layers).
+enum Shape { k256, k128, k96, k64 };
 
+Shape choose_shape(int64_t n, int64_t cols) {
+  const int64_t tm[4] = {256, 128, 96, 64}, tn[4] = {256, 128, 128, 128};
+  const double cost[4] = {0.83, 1.0, 1.08, 1.15};
+  Shape best = k256;
+  double least = 1e30;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t tiles = (n + tm[i] - 1) / tm[i] * ((cols + tn[i] - 1) / tn[i]);
+    const double us = cost[i] * tm[i] * tn[i] * (double)((tiles + 255) / 256);
+    if (us < least) least = us, best = (Shape)i;
+  }
+  return best;
+}
+
+// Parts of the contraction, while the tiles are too few for the chip (128 x 128
+// then).
 int gemm16_splits(int64_t n, int64_t cols, int64_t steps) {
-  if (n == 0 || cols == 0 || big_tiles(n, cols)) return 1;
+  if (n == 0 || cols == 0) return 1;
   const int64_t tiles = (n + 127) / 128 * ((cols + 127) / 128);
   int64_t splits = 384 / tiles;
   splits = splits < steps / 8 ? splits : steps / 8;
-  return splits < 2 ? 1 : (splits > 16 ? 16 : (int)splits);
+  return splits < 3 ? 1 : (splits > 16 ? 16 : (int)splits);
+}
+
+template <int DT, int OT, int TERMS, bool ORDER>
+void launch_shape(const Gemm16& a, hipStream_t s) {
+  switch (choose_shape(a.n, a.cols)) {
+    case k256: return launch_gemm<DT, OT, TERMS, ORDER, false, 4, 2, 2, 4>(a, s);
+    case k128: return launch_gemm<DT, OT, TERMS, ORDER, false, 2, 2, 2, 2>(a, s);
+    case k96: return launch_gemm<DT, OT, TERMS, ORDER, false, 3, 1, 1, 4>(a, s);
+    case k64: return launch_gemm<DT, OT, TERMS, ORDER, false, 2, 1, 1, 4>(a, s);
+  }
 }
 
 template <int DT, int OT, int TERMS>
 void choose_gemm(const Gemm16& a, hipStream_t s) {
-  const bool order = a.ad.order != nullptr;
   if (a.splits > 1) launch_gemm<DT, 0, TERMS, false, true, 2, 2, 2, 2>(a, s);
-  else if (big_tiles(a.n, a.cols)) order ? launch_gemm<DT, OT, TERMS, true, false, 4, 2, 2, 4>(a, s) : launch_gemm<DT, OT, TERMS, false, false, 4, 2, 2, 4>(a, s);
-  else order ? launch_gemm<DT, OT, TERMS, true, false, 2, 2, 2, 2>(a, s) : launch_gemm<DT, OT, TERMS, false, false, 2, 2, 2, 2>(a, s);
+  else if (a.ad.order) launch_shape<DT, OT, TERMS, true>(a, s);
+  else launch_shape<DT, OT, TERMS, false>(a, s);
 }
 
 // dst[t][0 .. kp) = src[t][0 .. d) (through perm, entries outside 0 .. d-1
@@ -196,7 +225,7 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
 void launch_gemm16(const Gemm16& g, int dt, int ot, hipStream_t s) {
   Gemm16 a = g;
   a.splits = gemm16_splits(a.n, a.cols, gemm16_terms(dt, ot) * (a.kp / LK));
-  a.vec = a.splits > 1 ? rows_on_16(a.part, a.cols, 0) && a.n * a.cols % 4 == 0 : rows_on_16(a.out, a.ldo, ot);
+  a.vec = rows_on_16(a.out, a.ldo, ot);
   if (a.splits > 1) a.ad.order = nullptr;   // the adapters follow where the parts are joined
   if (dt == kBF16) { if (ot == 0) choose_gemm<kBF16, 0, gemm16_terms(kBF16, 0)>(a, s); else choose_gemm<kBF16, kBF16, 1>(a, s); }
   else { if (ot == 0) choose_gemm<kF16, 0, gemm16_terms(kF16, 0)>(a, s); else choose_gemm<kF16, kF16, 1>(a, s); }
@@ -208,6 +237,7 @@ void launch_gemm16(const Gemm16& g, int dt, int ot, hipStream_t s) {
   u.ad = g.ad;
   u.B = g.B;
   u.part = a.part;
+  u.ldp = part_width(g.cols);
   u.splits = a.splits;
   u.out = g.out;
   u.ldo = g.ldo;
@@ -216,7 +246,7 @@ void launch_gemm16(const Gemm16& g, int dt, int ot, hipStream_t s) {
 
 int64_t gemm16_part_floats(int64_t n, int64_t cols, int64_t kp, int dt, int ot) {
   const int splits = gemm16_splits(n, cols, gemm16_terms(dt, ot) * (kp / LK));
-  return splits > 1 ? splits * n * cols : 0;
+  return splits > 1 ? splits * n * part_width(cols) : 0;
 }
 
 bool gemm16_takes(const void* X, int64_t d, int64_t ldx) {

@@ -214,7 +214,8 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
 
   float* own = reinterpret_cast<float*>(xs) + wave * 32 * (32 * NT + 4);
   __syncthreads();   // the last step's operands have been read
-  float* out = a.out + (int64_t)split * a.n * a.w.r;
+  const int64_t width = a.direct ? a.w.r : a.ldo;   // the columns between r and a part's width are sums of the last row
+  float* out = a.out + (int64_t)split * a.n * a.ldo;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t ti = t0 + 32 * i;
@@ -226,7 +227,7 @@ GPTQ_DEV void tiles_body(const TileArgs& a, unsigned char* xs) {
         for (int q = 0; q < NT; ++q) tot[i][q][e] = __builtin_ldexpf(tot[i][q][e], ex);
       }
     }
-    store_tile<0, NT>(own, tot[i], Adapters{}, out, ti, a.n, row0, a.w.r, a.ldo, a.vec);
+    store_tile<0, NT>(own, tot[i], Adapters{}, out, ti, a.n, row0, width, a.ldo, a.vec);
   }
 }
 
@@ -289,11 +290,15 @@ __global__ __launch_bounds__(256) void prepare_tokens_kernel(const uint16_t* __r
   }
 }
 
+// Chunks of a step that share a ruler (CPS of tiles_kernel).
+int chunks_per_ruler(const PackedLayer& w) { return w.cpg % 4 == 0 || w.shift == 31 ? 4 : (w.cpg % 2 == 0 ? 2 : 1); }
+
 template <int BITS, int MT>
 void launch_tiles(const TileArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.tok_tiles * a.row_tiles * a.splits)), block(256);
-  if (a.w.cpg % 4 == 0 || a.w.shift == 31) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 4>), grid, block, 0, s, a);
-  else if (a.w.cpg % 2 == 0) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 2>), grid, block, 0, s, a);
+  const int chunks = chunks_per_ruler(a.w);
+  if (chunks == 4) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 4>), grid, block, 0, s, a);
+  else if (chunks == 2) hipLaunchKernelGGL((tiles_kernel<BITS, MT, 2>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((tiles_kernel<BITS, MT, 1>), grid, block, 0, s, a);
 }
 
@@ -323,24 +328,27 @@ __global__ __launch_bounds__(256) void dequant_rows_kernel(PackedLayer w, uint16
   }
 }
 
-// Tiles of 32 mt tokens x 128 rows, the contraction in `splits` parts.
+// Tiles of 32 mt tokens x 128 rows, the contraction in `splits` parts, as a model of
+// the measured times has it: microseconds of a step for one workgroup alone on
+// a CU and for two, by the chunks that share a ruler (a scale for every 32
+// columns takes four times the multiplications), and parts written and read
+// back at 8 TB/s (they stay in the caches).  On 30 sizes (65 to 1000 tokens, six
+// layers) the choice was within 19 % of the best of 24, half of them within 4 %.
 struct TilePlan {
   int mt, splits;
 };
 
-TilePlan plan_tiles(int64_t n, int64_t r, int64_t c) {
-#ifdef PROBE_MT
-  return {PROBE_MT, PROBE_KS};
-#endif
+TilePlan plan_tiles(int64_t n, int64_t r, int64_t c, int chunks) {
+  const double alone0 = chunks == 4 ? 0.85 : (chunks == 2 ? 1.1 : 1.45), alone1 = chunks == 4 ? 0.14 : (chunks == 2 ? 0.17 : 0.21);
+  const double two0 = chunks == 4 ? 0.66 : (chunks == 2 ? 1.0 : 1.9), two1 = chunks == 4 ? 0.48 : (chunks == 2 ? 0.55 : 0.7);
   const int64_t steps = (c + STEP - 1) / STEP, row_tiles = (r + 127) / 128;
   TilePlan best{4, 1};
   double least = 1e30;
   for (int mt = 1; mt <= 4; mt *= 2)
-    for (int64_t splits = 1; splits <= 16 && 2 * splits <= steps; ++splits) {
+    for (int64_t splits = 1; splits <= 16 && (splits == 1 || 2 * splits <= steps); ++splits) {
       const int64_t groups = (n + 32 * mt - 1) / (32 * mt) * row_tiles * splits, each = (steps + splits - 1) / splits;
-      const int64_t rounds = (groups + 511) / 512;
-      double us = rounds * (3 + each * (0.66 + 0.48 * mt));
-      if (splits > 1) us += 4 + splits * n * r * 8 / 4e6;
+      const int64_t per_cu = (groups + 255) / 256;
+      const double us = each * (per_cu / 2 * (two0 + two1 * mt) + per_cu % 2 * (alone0 + alone1 * mt)) + splits * n * r * 8 / 8e6;
       if (us < least) least = us, best = {mt, (int)splits};
     }
   return best;
@@ -359,14 +367,19 @@ bool dequant_first(int64_t n, int yt) { return yt != 0 && n >= kCopyTokens; }
 
 }  // namespace
 
-bool packed_tiles(int64_t n, int64_t c) { return n > 64 && c < (int64_t(1) << 22) - STEP; }
+// From 49 tokens on: 64 tokens of 11008 x 4096 take 26 us so and 40 by sixteen at a
+// time, of 4096 x 11008 33 and 37, of 4096 x 4096 20 and 16.
+bool packed_tiles(int64_t n, int64_t c) { return n > 48 && c < (int64_t(1) << 22) - STEP; }
 
 int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt) {
   if (dequant_first(n, yt))
     return align256(n * gemm16_depth(c) * 2) + align256(r * gemm16_depth(c) * 2) + 4 * gemm16_part_floats(n, r, gemm16_depth(c), yt, yt);
-  const TilePlan p = plan_tiles(n, r, c);
-  const bool direct = yt == 0 && p.splits == 1;
-  return align256(n * tiles_width(c) * 2) + align256(n * 4) + (direct ? 0 : align256(p.splits * n * r * 4));
+  int64_t splits = yt == 0 ? 0 : 1;   // one part of fp32 results is the results
+  for (const int chunks : {4, 2, 1}) {
+    const int k = plan_tiles(n, r, c, chunks).splits;
+    splits = k > 1 && k > splits ? k : splits;
+  }
+  return align256(n * tiles_width(c) * 2) + align256(n * 4) + align256(splits * n * part_width(r) * 4);
 }
 
 void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad, const float* S,
@@ -407,7 +420,7 @@ void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const Pa
   const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0;
   if (xt == kBF16) hipLaunchKernelGGL((prepare_tokens_kernel<kBF16>), dim3((unsigned)n), block, 0, s, x, ldx, vec, w.c, w.perm, xp, ldp, ex);
   else hipLaunchKernelGGL((prepare_tokens_kernel<kF16>), dim3((unsigned)n), block, 0, s, x, ldx, vec, w.c, w.perm, xp, ldp, ex);
-  const TilePlan p = plan_tiles(n, w.r, w.c);
+  const TilePlan p = plan_tiles(n, w.r, w.c, chunks_per_ruler(w));
   TileArgs a{};
   a.X = xp;
   a.ex = ex;
@@ -419,8 +432,8 @@ void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const Pa
   a.splits = p.splits;
   a.direct = yt == 0 && p.splits == 1;
   a.out = a.direct ? static_cast<float*>(Y) : reinterpret_cast<float*>(ex + align256(n * 4) / 4);
-  a.ldo = a.direct ? ldy : w.r;
-  a.vec = rows_on_16(a.out, a.ldo, 0) && (p.splits == 1 || n * w.r % 4 == 0);
+  a.ldo = a.direct ? ldy : part_width(w.r);
+  a.vec = rows_on_16(a.out, a.ldo, 0);
 #define GPTQ_TILES(B_) (p.mt == 4 ? launch_tiles<B_, 4>(a, s) : p.mt == 2 ? launch_tiles<B_, 2>(a, s) : launch_tiles<B_, 1>(a, s))
   if (w.bits == 4) GPTQ_TILES(4);
   else GPTQ_TILES(3);
@@ -438,6 +451,7 @@ void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const Pa
     u.ldb = ldy;
   } else {
     u.part = a.out;
+    u.ldp = a.ldo;
     u.splits = p.splits;
     u.ex = ex;
   }
