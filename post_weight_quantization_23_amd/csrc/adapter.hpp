@@ -286,32 +286,35 @@ GPTQ_DEV void store8(void* out, int64_t at, const float (&v)[8], int k, bool vec
 }
 
 // ---------------------------------------------------------------- tile results
-// Stores the 32 tokens at places t0 .. x 32 NT outputs of a wave (accumulators of
-// mfma32) to out, turned through the wave's own 32 x (32 NT + 4) floats of LDS so that a row
-// leaves in whole runs of eight outputs per lane (single stores of two bytes
-// took a tenth of a 256 x 256 tile's time at 4096 columns).  vec: rows of out
-// start on 16 bytes.  more(v, t, j, k): adds to the first k <= 8 outputs from j.
-struct NoMore {
-  GPTQ_DEV void operator()(float (&)[8], int64_t, int64_t, int) const {}
-};
-template <int OT, int NT, class More = NoMore>
-GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], const Adapters& ad, void* out, int64_t t0, int64_t n, int64_t j0,
-                         int64_t cols, int64_t ldo, bool vec, const More& more = More()) {
-  constexpr int W = 32 * NT, LD = W + 4, LPR = W / 8, RPP = 64 / LPR;
+// A wave's 32 x 32 NT accumulators into its own 32 x (32 NT + 4) floats of LDS, rows
+// of places.
+template <int NT>
+GPTQ_DEV void turn_tile(float* lds, const floatx16 (&acc)[NT]) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int q = 0; q < NT; ++q)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) lds[TileShape<floatx16>::acc_row(lane, e) * LD + 32 * q + (lane & 31)] = acc[q][e];
+    for (int e = 0; e < 16; ++e) lds[TileShape<floatx16>::acc_row(lane, e) * (32 * NT + 4) + 32 * q + (lane & 31)] = acc[q][e];
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// Stores the 32 tokens at places t0 .. x 32 NT outputs of a wave (accumulators of
+// mfma32) to out, turned through LDS so that a row leaves in whole runs of eight
+// outputs per lane (single stores of two bytes took a tenth of a 256 x 256
+// tile's time at 4096 columns).  vec: rows of out start on 16 bytes.
+template <int OT, int NT>
+GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], const Adapters& ad, void* out, int64_t t0, int64_t n, int64_t j0,
+                         int64_t cols, int64_t ldo, bool vec) {
+  constexpr int W = 32 * NT, LPR = W / 8, RPP = 64 / LPR;
+  const int lane = threadIdx.x & 63;
+  turn_tile<NT>(lds, acc);
 #pragma unroll
   for (int k = 0; k < 32 / RPP; ++k) {
     const int r = RPP * k + lane / LPR, c = 8 * (lane % LPR);
     const int64_t t = ad.token(t0 + r, n), j = j0 + c;
-    float v[8];
-    load8f(lds + r * LD + c, v);
     if (t < 0 || j >= cols) continue;
-    more(v, t, j, (int)min((int64_t)8, cols - j));
+    float v[8];
+    load8f(lds + r * (W + 4) + c, v);
     store8<OT>(out, t * ldo + j, v, (int)min((int64_t)8, cols - j), vec);
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -561,7 +564,8 @@ void launch_packed_linear(const void* X, int xt, int64_t n, int64_t ldx, const P
 // dst[t][j] = X[t][perm[j]] (entries outside 0 .. c-1 clamped), dst dense.
 void launch_gather_columns(const void* X, int64_t n, int64_t c, int64_t ldx, const int32_t* perm, void* dst, hipStream_t s);
 // The same for many tokens: packed_tiles.hip.  ws: packed_tiles_bytes().
-bool packed_tiles(int64_t n, int64_t c);
+bool packed_tiles(int64_t n, int64_t r, int64_t c);
+double packed_rows_us(int64_t n, int64_t r, int64_t c);   // launch_packed_linear's time, as its model has it
 int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt);
 void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad, const float* S,
                          void* Y, int yt, int64_t ldy, void* ws, hipStream_t s);

@@ -124,7 +124,7 @@ gptq_status check_clash(const char* fn, int c) {
 // What the packed product's kernels prepare: the gathered activations of a few
 // tokens of an act-order layer, or what many tokens need.
 int64_t forward_bytes(int64_t n, int64_t r, int64_t c, bool perm, int yt) {
-  if (gptq::packed_tiles(n, c)) return gptq::packed_tiles_bytes(n, r, c, yt);
+  if (gptq::packed_tiles(n, r, c)) return gptq::packed_tiles_bytes(n, r, c, yt);
   return perm ? align256(n * c * 2) : 0;
 }
 
@@ -269,7 +269,7 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
     d.ad = ad;
     gptq::launch_adapter_down(d, xi, true, s);
   }
-  if (gptq::packed_tiles(n, c)) {
+  if (gptq::packed_tiles(n, r, c)) {
     gptq::launch_packed_tiles(X, xi, n, ldx, w, ad, S, Y, yi, ldy, carve.at, s);
   } else {
     const void* xp = X;

@@ -336,20 +336,20 @@ __global__ __launch_bounds__(256) void dequant_rows_kernel(PackedLayer w, uint16
 // layers) the choice was within 19 % of the best of 24, half of them within 4 %.
 struct TilePlan {
   int mt, splits;
+  double us;
 };
 
 TilePlan plan_tiles(int64_t n, int64_t r, int64_t c, int chunks) {
   const double alone0 = chunks == 4 ? 0.85 : (chunks == 2 ? 1.1 : 1.45), alone1 = chunks == 4 ? 0.14 : (chunks == 2 ? 0.17 : 0.21);
   const double two0 = chunks == 4 ? 0.66 : (chunks == 2 ? 1.0 : 1.9), two1 = chunks == 4 ? 0.48 : (chunks == 2 ? 0.55 : 0.7);
   const int64_t steps = (c + STEP - 1) / STEP, row_tiles = (r + 127) / 128;
-  TilePlan best{4, 1};
-  double least = 1e30;
+  TilePlan best{4, 1, 1e30};
   for (int mt = 1; mt <= 4; mt *= 2)
     for (int64_t splits = 1; splits <= 16 && (splits == 1 || 2 * splits <= steps); ++splits) {
       const int64_t groups = (n + 32 * mt - 1) / (32 * mt) * row_tiles * splits, each = (steps + splits - 1) / splits;
       const int64_t per_cu = (groups + 255) / 256;
       const double us = each * (per_cu / 2 * (two0 + two1 * mt) + per_cu % 2 * (alone0 + alone1 * mt)) + splits * n * r * 8 / 8e6;
-      if (us < least) least = us, best = {mt, (int)splits};
+      if (us < best.us) best = {mt, (int)splits, us};
     }
   return best;
 }
@@ -367,9 +367,14 @@ bool dequant_first(int64_t n, int yt) { return yt != 0 && n >= kCopyTokens; }
 
 }  // namespace
 
-// From 49 tokens on: 64 tokens of 11008 x 4096 take 26 us so and 40 by sixteen at a
-// time, of 4096 x 11008 33 and 37, of 4096 x 4096 20 and 16.
-bool packed_tiles(int64_t n, int64_t c) { return n > 48 && c < (int64_t(1) << 22) - STEP; }
+// Below the tokens of a copy, the kernel for few tokens as long as the models of both
+// say so; tiles take three launches, with what these leave between them in memory
+// (10 us).  By that kernel and in tiles: 512 tokens of 1024 x 4096 16 and 28 us, 128 of
+// 4096 x 4096 16 and 27, 512 of them 54 and 42, 65 tokens of 12288 x 8192 55 and 46.
+bool packed_tiles(int64_t n, int64_t r, int64_t c) {
+  if (n <= 64 || c >= (int64_t(1) << 22) - STEP) return false;
+  return n >= kCopyTokens || packed_rows_us(n, r, c) > 10 + plan_tiles(n, r, c, 4).us;
+}
 
 int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt) {
   if (dequant_first(n, yt))

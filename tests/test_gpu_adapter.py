@@ -161,6 +161,32 @@ def test_packed_linear(n, r, c, bits, gs, act, dt, out, low):
     check("Y", Y, *forward64(L, X, ad, DT[out]))
 
 
+# Rows enough for two and three row tiles to a workgroup, with token groups that end
+# early; many tokens with fp32 results, and the tiles in front of 16-bit ones.
+SHAPES = [
+    (17, 4001, 160, 4, 32, False, "bf16", "bf16", (2, 8, "mixed")),
+    (24, 8003, 256, 4, 128, False, "fp16", "fp32", None),
+    (13, 8016, 544, 3, 64, True, "bf16", "bf16", (13, 16, "runs")),
+    (31, 12001, 288, 3, 96, True, "bf16", "bf16", (3, 24, "mixed")),
+    (41, 4000, 640, 3, -1, False, "fp16", "fp16", (2, 16, "mixed")),
+    (48, 7999, 192, 4, 64, False, "bf16", "fp32", None),
+    (35, 12007, 128, 4, 128, True, "fp16", "fp16", (5, 8, "runs")),
+    (60, 8190, 320, 3, 32, False, "bf16", "bf16", (60, 8, "runs")),
+    (450, 100, 256, 4, 128, False, "bf16", "bf16", (3, 32, "runs")),
+    (1030, 300, 544, 4, 96, False, "fp16", "fp32", (3, 16, "mixed")),
+    (1100, 130, 1024, 3, 64, True, "bf16", "fp32", None),
+    (1024, 257, 640, 3, -1, False, "bf16", "fp32", (7, 8, "runs")),
+    (1151, 1030, 96, 4, 32, True, "fp16", "fp32", (1, 64, "all")),
+    (520, 4100, 4128, 4, 128, False, "bf16", "bf16", (3, 16, "runs")),
+    (77, 6001, 8224, 3, 32, True, "fp16", "fp16", (2, 40, "mixed")),
+]
+
+
+@pytest.mark.parametrize("n,r,c,bits,gs,act,dt,out,low", SHAPES)
+def test_packed_linear_shapes(n, r, c, bits, gs, act, dt, out, low):
+    test_packed_linear(n, r, c, bits, gs, act, dt, out, low)
+
+
 def backward64(L, dY, ad, out_dtype):
     dY64 = dY.double()
     want = dY64 @ L.W
