@@ -16,6 +16,92 @@ constexpr int LK = kGemm16Step, ROWB = LK * 2;   // contraction step, bytes of a
 // Chunk c (16 bytes) of LDS row f lies at place c ^ swz(f).
 GPTQ_DEV int swz(int f) { return (f ^ (f >> 3)) & 7; }
 
+// What the adapters' part of a tile keeps in LDS behind the operands: token and
+// adapter of each place.
+template <int TM>
+struct Places {
+  int tok[TM], who[TM];
+};
+
+// acc[i][q] += S B_a^T for the tile's adapters (S in TERMS bf16 terms).  S and, for one
+// adapter after the other, the tile's rows of B come into the operands' LDS in
+// whole runs, 64 ranks at a time: operands loaded straight into registers would
+// touch 32 rows per instruction, at a place a cycle (2085 tokens of 4096 x 4096
+// with rank 64: 110 us, 116 so).  Sets of 32 places that one adapter has to itself take
+// its products onto their sums; the others follow by expand_shared, so that a
+// value that is not finite in one request stays there.
+template <int DT, int TERMS, int MT, int NT, int WM, int WN>
+GPTQ_DEV void expand_staged(const Gemm16& a, const Places<32 * MT * WM>* pl, unsigned char* smem, int j0, int wm, int wn,
+                            const int64_t (&col)[NT], floatx16 (&acc)[MT][NT]) {
+  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, RANKS = 64;
+  constexpr int QS = TM / 4 / (WM * WN), QB = TN / 8 / WN;   // load instructions per wave: 4 rows of S, 8 of B
+  static_assert(QS * 4 * WM * WN == TM && QB * 8 * WN == TN, "rows divide over the waves");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31, h = lane >> 5;
+  const int rank = a.ad.rank;
+  unsigned char* bs = smem + TM * 256 + (wave / WN) * TN * 128;   // B of the waves with these tokens
+  lds_u8 *ls = (lds_u8*)smem, *lb = (lds_u8*)bs;
+  for (int k0 = 0; k0 < rank; k0 += RANKS) {
+    const int ranks = min(RANKS, rank - k0);
+#pragma unroll 2
+    for (int q = 0; q < QS; ++q) {
+      const int row = 4 * (wave * QS + q) + (lane >> 4), piece = (lane & 15) ^ (row & 15);
+      const float* from = a.S + (int64_t)max(pl->tok[row], 0) * rank + k0 + (4 * piece < ranks ? 4 * piece : 0);
+      __builtin_amdgcn_global_load_lds((const void __attribute__((address_space(1)))*)from,
+                                       (void __attribute__((address_space(3)))*)(ls + (wave * QS + q) * 1024), 16, 0, 0);
+    }
+    int held = -1;   // the adapter whose B lies in bs
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int at = wm + 32 * i + m, tok = pl->tok[at], mine = pl->who[at], first = __builtin_amdgcn_readfirstlane(mine);
+      const bool whole = first >= 0 && (uint32_t)__ballot(mine == first) == (uint32_t)__ballot(tok >= 0);
+      if (whole && first != held) {
+        held = first;
+#pragma unroll 2
+        for (int q = 0; q < QB; ++q) {
+          const int row = 8 * ((wave % WN) * QB + q) + (lane >> 3), piece = (lane & 7) ^ (row & 7);
+          const uint16_t* from = a.B + ((int64_t)first * a.cols + min(j0 + row, a.cols - 1)) * rank + k0 + (8 * piece < ranks ? 8 * piece : 0);
+          __builtin_amdgcn_global_load_lds((const void __attribute__((address_space(1)))*)from,
+                                           (void __attribute__((address_space(3)))*)(lb + ((wave % WN) * QB + q) * 1024), 16, 0, 0);
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (whole) {
+        for (int k1 = 0; k1 < ranks; k1 += 16) {
+          const int k = k1 + 8 * h;
+          const bool in = k < ranks;
+          const floatx4 lo = *reinterpret_cast<const floatx4*>(smem + at * 256 + (((k >> 2) ^ (at & 15)) << 4));
+          const floatx4 hi = *reinterpret_cast<const floatx4*>(smem + at * 256 + ((((k >> 2) + 1) ^ (at & 15)) << 4));
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = in ? lo[e] : 0.f;
+            v[4 + e] = in ? hi[e] : 0.f;
+          }
+          u32x4 s[TERMS];
+          split8<TERMS>(v, s);
+#pragma unroll
+          for (int q = 0; q < NT; ++q) {
+            const int f = wn + 32 * q + m;
+            u32x4 b = *reinterpret_cast<const u32x4*>(bs + f * 128 + (((k >> 3) ^ (f & 7)) << 4));
+            if (!in) b = u32x4{0u, 0u, 0u, 0u};
+            acc[i][q] = mfma_terms<DT, TERMS>(s, Terms16<DT>(b), acc[i][q]);
+          }
+        }
+      } else if (k0 == 0) {
+        uint32_t rest = (uint32_t)__ballot(mine >= 0);
+        while (rest) {
+          const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctz(rest));
+          const uint32_t members = (uint32_t)__ballot(mine == ad);
+          rest &= ~members;
+          expand_shared<DT, TERMS, NT>(a.ad, ad, members, a.B, a.cols, a.S, tok, col, acc[i]);
+        }
+      }
+      __syncthreads();   // before B, or S, is replaced
+    }
+  }
+}
+
 // WM x WN waves of 32 MT tokens x 32 NT columns.  Both operands come from
 // memory straight into LDS (double buffered, one barrier per step), each lane
 // fetching the chunk that belongs at its place; tokens past the end repeat the
@@ -80,6 +166,12 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
 #pragma unroll
     for (int q = 0; q < NT; ++q) acc[i][q] = floatx16{};
 
+  Places<TM>* pl = reinterpret_cast<Places<TM>*>(smem + 2 * BUF);
+  if (!PARTS && a.S && tid < TM) {
+    const int64_t t = a.ad.token(t0 + tid, a.n);
+    pl->tok[tid] = (int)t;
+    pl->who[tid] = adapter_of(a.ad, t, a.n);
+  }
   load(first);
   for (int s = first; s < all; ++s) {
     // own loads have landed; with every wave here, the other buffer is free
@@ -125,12 +217,13 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
     const int at = j0 + wn + 32 * q + m;
     col[q] = at < a.cols ? at : -1;
   }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t ti = t0 + wm + 32 * i;
-    if (a.S) expand_add<DT, OT == 0 ? 3 : 2, NT>(a.ad, a.B, a.cols, a.S, ti, a.n, col, acc[i]);
-    store_tile<OT, NT>(own, acc[i], a.ad, a.out, ti, a.n, j0 + wn, a.cols, a.ldo, a.vec);
+  if (a.S) {
+    expand_staged<DT, OT == 0 ? 3 : 2, MT, NT, WM, WN>(a, pl, smem, j0, wm, wn, col, acc);
+    __syncthreads();
   }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    store_tile<OT, NT>(own, acc[i], a.ad, a.out, t0 + wm + 32 * i, a.n, j0 + wn, a.cols, a.ldo, a.vec);
 }
 
 template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
@@ -141,7 +234,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(Gemm16 a) {
 
 template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
 void launch_gemm(Gemm16 a, hipStream_t s) {
-  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, LDS = 2 * (TM + TN) * ROWB;
+  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, LDS = 2 * (TM + TN) * ROWB + (PARTS ? 0 : (int)sizeof(Places<TM>));
   static const bool set = [] {   // once, thread-safe
     (void)hipFuncSetAttribute((const void*)gemm_kernel<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
