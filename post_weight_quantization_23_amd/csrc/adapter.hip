@@ -346,19 +346,23 @@ __global__ __launch_bounds__(256) void join_rows_kernel(UpArgs u) {
 // workgroups that each do one piece: they are small, and a launch each took
 // longer than the work.
 
-GPTQ_DEV void transpose_piece(const TransposeArgs& v, int64_t b, uint16_t (&tile)[64][66]) {
+// Two tiles of 64 x 64, by 512 threads each: 16 bytes a load and a store.
+GPTQ_DEV void transpose_piece(const TransposeArgs& v, int64_t b, uint16_t (&tiles)[2][64][72]) {
+  uint16_t (&tile)[64][72] = tiles[threadIdx.x >> 9];
   const int64_t row_tiles = (v.ldd + 63) / 64, ct_n = (v.cols + 63) / 64;
+  b = 2 * b + (threadIdx.x >> 9);
   const int64_t bt = b / row_tiles, rt = b - bt * row_tiles, a = bt / ct_n, ct = bt - a * ct_n;
   const int64_t i0 = rt * 64, j0 = ct * 64;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int r = w; r < 64; r += 16) {
-    const int64_t i = i0 + r, j = j0 + lane;
-    tile[r][lane] = (i < v.rows && j < v.cols) ? v.src[(a * v.rows + i) * v.cols + j] : (uint16_t)0;
-  }
+  const int r = (threadIdx.x & 511) >> 3, k = 8 * (threadIdx.x & 7);
+  u32x4 x = {0u, 0u, 0u, 0u};
+  if (b < v.tiles && i0 + r < v.rows && j0 + k < v.cols)
+    x = load8(v.src + (a * v.rows + i0 + r) * v.cols + j0 + k, (int)min((int64_t)8, v.cols - j0 - k), v.vec);
+  *reinterpret_cast<u32x4*>(&tile[r][k]) = x;
   __syncthreads();
-  for (int r = w; r < 64; r += 16) {
-    const int64_t j = j0 + r, i = i0 + lane;
-    if (j < v.cols && i < v.ldd) v.dst[(a * v.cols + j) * v.ldd + i] = tile[lane][r];
+  if (b < v.tiles && j0 + r < v.cols && i0 + k < v.ldd) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (uint32_t)tile[k + 2 * e][r] | ((uint32_t)tile[k + 2 * e + 1][r] << 16);
+    *reinterpret_cast<u32x4*>(v.dst + (a * v.cols + j0 + r) * v.ldd + i0 + k) = x;
   }
 }
 
@@ -411,7 +415,7 @@ GPTQ_DEV int64_t count_tokens(int64_t n, int (&count)[16], const In& in) {
 }
 
 __global__ __launch_bounds__(1024) void prepare_adapters_kernel(PrepareArgs g) {
-  __shared__ uint16_t tile[64][66];
+  __shared__ __align__(16) uint16_t tile[2][64][72];
   __shared__ int count[16];
   const Adapters& ad = g.ad;
   const int64_t n = g.n;
@@ -456,8 +460,16 @@ __global__ __launch_bounds__(1024) void prepare_adapters_kernel(PrepareArgs g) {
   }
 }
 
+// Place of the k-th term of 16 rank rows and 32 places in the list: a block of 64
+// lanes' operands, each of eight places of one row (lane = row + 16 (place / 8)), so
+// that a wave loads it in one run (rows of whole lists touched 64 places per load).
+GPTQ_DEV int64_t terms_at(int64_t block, int rows, int k, int rank) {
+  return ((block * ((rank + 15) >> 4) + rows) * 3 + k) * 512;
+}
+
 // The rank values in list order, transposed and split into three bf16 terms: the
-// gradients' operand as it is loaded.  One thread per rank row and eight places;
+// gradients' operand as it is loaded; the rows that fill the last 16 stay as they
+// are, their sums are dropped.  One thread per rank row and eight places;
 // it joins the parts that down_tiles_kernel left, and keeps the joined values
 // where `keep` says so.
 __global__ __launch_bounds__(256) void sorted_terms_kernel(TermsArgs g) {
@@ -495,7 +507,8 @@ __global__ __launch_bounds__(256) void sorted_terms_kernel(TermsArgs g) {
   u32x4 k[3];
   split8<3>(v, k);
 #pragma unroll
-  for (int u = 0; u < 3; ++u) *reinterpret_cast<u32x4*>(g.terms[which] + ((int64_t)u * rank + p) * g.places + p8) = k[u];
+  for (int u = 0; u < 3; ++u)
+    *reinterpret_cast<u32x4*>(g.terms[which] + terms_at(p8 >> 5, p >> 4, u, rank) + ((p & 15) + 16 * ((p8 >> 3) & 3)) * 8) = k[u];
 }
 
 // ---------------------------------------------------------------- gradients
@@ -519,14 +532,14 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs g) {
   if (b >= g.p[0].items) b -= g.p[0].items;
   if (b >= q.items) return;
   const int rank = g.ad.rank, splits = q.splits;
-  const int64_t places = g.places, cols = q.cols, ldz = q.ldz;
+  const int64_t cols = q.cols, ldz = q.ldz;
   const uint16_t* terms = q.terms;
   const uint16_t* Z = q.Z;
   const int32_t* order = g.list;
+  const int rb = (int)(b % g.rank_blocks);   // neighbours: they read the same rows of Z
+  b /= g.rank_blocks;
   const int64_t cb = b % q.col_blocks;
   b /= q.col_blocks;
-  const int rb = (int)(b % g.rank_blocks);
-  b /= g.rank_blocks;
   const int split = (int)(b % splits);
   const int a = (int)(b / splits);
   const int64_t first = g.start[a];
@@ -569,8 +582,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradArgs g) {
     for (int p = 0; p < RT; ++p)
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        f.v[p][k] = *reinterpret_cast<const u32x4*>(terms + ((int64_t)k * rank + min(p0 + 16 * p + m, rank - 1)) * places + first +
-                                                    32 * (int64_t)blk + 8 * kq);
+        f.v[p][k] = *reinterpret_cast<const u32x4*>(terms + terms_at((first >> 5) + blk, min(p0 + 16 * p, rank - 1) >> 4, k, rank) + 8 * lane);
     if (blk + 1 < b1) load_tokens(blk + 1);
   };
   auto use = [&](const Operands& f) __attribute__((always_inline)) {
@@ -642,7 +654,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs g) {
 // chip, two steps of 64 at least in each.
 int down_splits(int64_t n, int64_t d) {
   const int64_t tiles = (n + 63) / 64, steps = (d + 63) / 64;
-  int64_t splits = 768 / tiles;
+  int64_t splits = 512 / tiles;
   splits = splits < steps / 2 ? splits : steps / 2;
   return splits < 1 ? 1 : (splits > 8 ? 8 : (int)splits);
 }
@@ -657,7 +669,7 @@ int grad_rows(int rank) { return rank <= 16 ? 16 : 32; }
 int grad_splits(int64_t n, int m, int64_t cols, int rank) {
   if (n == 0 || cols == 0) return 1;
   const int64_t waves = (cols + 127) / 128 * m * ((rank + grad_rows(rank) - 1) / grad_rows(rank));
-  int64_t splits = (2048 + waves - 1) / waves;
+  int64_t splits = (512 + waves - 1) / waves;
   const int64_t most = (n + m - 1) / m / 64;   // two blocks of tokens each
   splits = splits < most ? splits : most;
   return splits < 1 ? 1 : (splits > 16 ? 16 : (int)splits);
@@ -685,7 +697,9 @@ void launch_prepare_adapters(const PrepareArgs& given, hipStream_t s) {
   g.list_blocks = g.list ? g.ad.m : 0;
   int64_t blocks = (int64_t)g.order_blocks + g.list_blocks;
   for (auto& v : g.turn) {
-    v.blocks = v.src ? (v.ldd + 63) / 64 * ((v.cols + 63) / 64) * g.ad.m : 0;
+    v.tiles = v.src ? (v.ldd + 63) / 64 * ((v.cols + 63) / 64) * g.ad.m : 0;
+    v.blocks = (v.tiles + 1) / 2;
+    v.vec = v.src && reinterpret_cast<uintptr_t>(v.src) % 16 == 0 && v.cols % 8 == 0;
     blocks += v.blocks;
   }
   for (auto& v : g.pad) {

@@ -459,7 +459,9 @@ struct TransposeArgs {
   const uint16_t* src;
   int64_t rows, cols;
   uint16_t* dst;
-  int64_t ldd, blocks;
+  int64_t ldd;        // a multiple of 8; dst on 16 bytes
+  int64_t tiles, blocks;   // set by the launch, as vec
+  bool vec;
 };
 struct PadArgs {
   const uint16_t* src;
@@ -499,8 +501,9 @@ struct UpArgs {
 };
 void launch_adapter_up(const UpArgs& u, int xt, int yt, hipStream_t s);
 // gA[a][p][k] = sum over a's tokens of T[t][p] X[t][k] and gB[a][i][p] = ... S[t][p]
-// dY[t][i], from the rank values S[0] = T and S[1] = S in list order: terms[w][k][p][i]
-// is the k-th bf16 term of S[w][list[i]][p] (0 where list[i] is -1).
+// dY[t][i], from the rank values S[0] = T and S[1] = S in list order: terms[w] holds the
+// three bf16 terms of S[w][list[i]][p] (0 where list[i] is -1), rank rows and places in
+// blocks of 16 x 32.
 struct TermsArgs {
   Adapters ad;
   int64_t n, places;
@@ -521,7 +524,6 @@ struct GradProblem {
 };
 struct GradArgs {
   Adapters ad;
-  int64_t places;
   const int32_t *list, *start, *count;
   int rank_blocks;     // set by the launch
   GradProblem p[2];    // gA, gB

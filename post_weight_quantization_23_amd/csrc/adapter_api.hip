@@ -197,7 +197,7 @@ GradSizes grad_sizes(int64_t n, int64_t r, int64_t c, int64_t m, int64_t rank) {
   z.part = align256(gptq::adapter_grad_floats(n, (int)m, r, c, (int)rank) * 4);
   z.places = gptq::list_places(n, m);
   z.lists = align256(z.places * 4) + align256((m + 1) * 4) + align256(m * 4);
-  z.terms = align256(3 * rank * z.places * 2);
+  z.terms = align256(3 * ((rank + 15) / 16 * 16) * z.places * 2);
   z.total = order_bytes(n, rank) + rows_bytes(n, r, rank) + rows_bytes(n, c, rank) + align256(m * rank * pad8(r) * 2) + align256(m * c * rank * 2) + low_bytes(n, c, rank) + low_bytes(n, r, rank) + z.lists + 2 * z.terms + z.part;
   return z;
 }
@@ -517,7 +517,7 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   gptq::TermsArgs v{};
   v.ad = ad;
   v.n = n;
-  v.places = w.places = z.places;
+  v.places = z.places;
   v.list = w.list = g.list;
   v.start = w.start = g.start;
   w.count = g.count;

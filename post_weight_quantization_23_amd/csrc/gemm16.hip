@@ -226,15 +226,22 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
     store_tile<OT, NT>(own, acc[i], a.ad, a.out, t0 + wm + 32 * i, a.n, j0 + wn, a.cols, a.ldo, a.vec);
 }
 
+// LDS of a workgroup, and the waves per SIMD that it leaves room for (the smallest
+// tile three: with registers for two 512 tokens of 4096 x 11008 took 84 us, so 64).
+template <bool PARTS, int TM, int TN>
+constexpr int gemm_lds() { return 2 * (TM + TN) * ROWB + (PARTS ? 0 : (int)sizeof(Places<TM>)); }
+template <bool PARTS, int MT, int NT, int WM, int WN>
+constexpr int gemm_waves() { return WM * WN == 4 && 3 * gemm_lds<PARTS, 32 * MT * WM, 32 * NT * WN>() <= 160 * 1024 ? 3 : 2; }
+
 template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(Gemm16 a) {
+__global__ __launch_bounds__(64 * WM * WN, (gemm_waves<PARTS, MT, NT, WM, WN>())) void gemm_kernel(Gemm16 a) {
   extern __shared__ __align__(16) unsigned char gsm[];
   gemm_body<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>(a, gsm);
 }
 
 template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
 void launch_gemm(Gemm16 a, hipStream_t s) {
-  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, LDS = 2 * (TM + TN) * ROWB + (PARTS ? 0 : (int)sizeof(Places<TM>));
+  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, LDS = gemm_lds<PARTS, TM, TN>();
   static const bool set = [] {   // once, thread-safe
     (void)hipFuncSetAttribute((const void*)gemm_kernel<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
