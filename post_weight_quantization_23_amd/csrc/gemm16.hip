@@ -106,9 +106,10 @@ GPTQ_DEV void expand_staged(const Gemm16& a, const Places<32 * MT * WM>* pl, uns
 // memory straight into LDS (double buffered, one barrier per step), each lane
 // fetching the chunk that belongs at its place; tokens past the end repeat the
 // last one, columns past the end lie outside the descriptor's records and read
-// as zero.  ORDER: tokens by adapter (ad.order).  PARTS: the workgroup takes one of
+// as zero.  LOW: adapters beside the product (1), tokens by adapter too (2: ad.order;
+// without either a 256 x 256 tile keeps all its registers).  PARTS: the workgroup takes one of
 // `splits` parts of the contraction and writes its fp32 sums to part.
-template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
+template <int DT, int OT, int TERMS, int LOW, bool PARTS, int MT, int NT, int WM, int WN>
 GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
   constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, NW = WM * WN, BUF = (TM + TN) * ROWB;
   constexpr int QX = TM / 8 / NW, QW = TN / 8 / NW;   // load instructions per wave: 8 rows each
@@ -129,7 +130,7 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
 #pragma unroll
   for (int q = 0; q < QX; ++q) {
     const int row = 8 * (wave * QX + q) + (lane >> 3), piece = 8 * ((lane & 7) ^ swz(row));
-    if constexpr (ORDER) fromx[q] = a.X + (int64_t)a.ad.order[min(t0 + row, a.n - 1)] * a.ldx + piece;
+    if constexpr (LOW == 2) fromx[q] = a.X + (int64_t)a.ad.order[min(t0 + row, a.n - 1)] * a.ldx + piece;
     else offx[q] = (row * (int)a.ldx + piece) * 2;
   }
 #pragma unroll
@@ -149,7 +150,7 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
     lds_u8* to = lbase + (s & 1) * BUF;
 #pragma unroll
     for (int q = 0; q < QX; ++q) {
-      if constexpr (ORDER)
+      if constexpr (LOW == 2)
         __builtin_amdgcn_global_load_lds((const void __attribute__((address_space(1)))*)(fromx[q] + k0),
                                          (void __attribute__((address_space(3)))*)(to + (wave * QX + q) * 1024), 16, 0, 0);
       else
@@ -167,7 +168,7 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
     for (int q = 0; q < NT; ++q) acc[i][q] = floatx16{};
 
   Places<TM>* pl = reinterpret_cast<Places<TM>*>(smem + 2 * BUF);
-  if (!PARTS && a.S && tid < TM) {
+  if (LOW && tid < TM) {
     const int64_t t = a.ad.token(t0 + tid, a.n);
     pl->tok[tid] = (int)t;
     pl->who[tid] = adapter_of(a.ad, t, a.n);
@@ -217,7 +218,7 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
     const int at = j0 + wn + 32 * q + m;
     col[q] = at < a.cols ? at : -1;
   }
-  if (a.S) {
+  if constexpr (LOW != 0) {
     expand_staged<DT, OT == 0 ? 3 : 2, MT, NT, WM, WN>(a, pl, smem, j0, wm, wn, col, acc);
     __syncthreads();
   }
@@ -228,29 +229,29 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
 
 // LDS of a workgroup, and the waves per SIMD that it leaves room for (the smallest
 // tile three: with registers for two 512 tokens of 4096 x 11008 took 84 us, so 64).
-template <bool PARTS, int TM, int TN>
-constexpr int gemm_lds() { return 2 * (TM + TN) * ROWB + (PARTS ? 0 : (int)sizeof(Places<TM>)); }
-template <bool PARTS, int MT, int NT, int WM, int WN>
-constexpr int gemm_waves() { return WM * WN == 4 && 3 * gemm_lds<PARTS, 32 * MT * WM, 32 * NT * WN>() <= 160 * 1024 ? 3 : 2; }
+template <int LOW, int TM, int TN>
+constexpr int gemm_lds() { return 2 * (TM + TN) * ROWB + (LOW ? (int)sizeof(Places<TM>) : 0); }
+template <int LOW, int MT, int NT, int WM, int WN>
+constexpr int gemm_waves() { return WM * WN == 4 && 3 * gemm_lds<LOW, 32 * MT * WM, 32 * NT * WN>() <= 160 * 1024 ? 3 : 2; }
 
-template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, (gemm_waves<PARTS, MT, NT, WM, WN>())) void gemm_kernel(Gemm16 a) {
+template <int DT, int OT, int TERMS, int LOW, bool PARTS, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, (gemm_waves<LOW, MT, NT, WM, WN>())) void gemm_kernel(Gemm16 a) {
   extern __shared__ __align__(16) unsigned char gsm[];
-  gemm_body<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>(a, gsm);
+  gemm_body<DT, OT, TERMS, LOW, PARTS, MT, NT, WM, WN>(a, gsm);
 }
 
-template <int DT, int OT, int TERMS, bool ORDER, bool PARTS, int MT, int NT, int WM, int WN>
+template <int DT, int OT, int TERMS, int LOW, bool PARTS, int MT, int NT, int WM, int WN>
 void launch_gemm(Gemm16 a, hipStream_t s) {
-  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, LDS = gemm_lds<PARTS, TM, TN>();
+  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, LDS = gemm_lds<LOW, TM, TN>();
   static const bool set = [] {   // once, thread-safe
-    (void)hipFuncSetAttribute((const void*)gemm_kernel<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>,
+    (void)hipFuncSetAttribute((const void*)gemm_kernel<DT, OT, TERMS, LOW, PARTS, MT, NT, WM, WN>,
                               hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     return true;
   }();
   (void)set;
   a.tok_tiles = (int)((a.n + TM - 1) / TM);
   a.col_tiles = (a.cols + TN - 1) / TN;
-  hipLaunchKernelGGL((gemm_kernel<DT, OT, TERMS, ORDER, PARTS, MT, NT, WM, WN>),
+  hipLaunchKernelGGL((gemm_kernel<DT, OT, TERMS, LOW, PARTS, MT, NT, WM, WN>),
                      dim3((unsigned)((int64_t)a.tok_tiles * a.col_tiles * a.splits)), dim3(64 * WM * WN), LDS, s, a);
 }
 
@@ -285,21 +286,22 @@ int gemm16_splits(int64_t n, int64_t cols, int64_t steps) {
   return splits < 3 ? 1 : (splits > 16 ? 16 : (int)splits);
 }
 
-template <int DT, int OT, int TERMS, bool ORDER>
+template <int DT, int OT, int TERMS, int LOW>
 void launch_shape(const Gemm16& a, hipStream_t s) {
   switch (choose_shape(a.n, a.cols)) {
-    case k256: return launch_gemm<DT, OT, TERMS, ORDER, false, 4, 2, 2, 4>(a, s);
-    case k128: return launch_gemm<DT, OT, TERMS, ORDER, false, 2, 2, 2, 2>(a, s);
-    case k96: return launch_gemm<DT, OT, TERMS, ORDER, false, 3, 1, 1, 4>(a, s);
-    case k64: return launch_gemm<DT, OT, TERMS, ORDER, false, 2, 1, 1, 4>(a, s);
+    case k256: return launch_gemm<DT, OT, TERMS, LOW, false, 4, 2, 2, 4>(a, s);
+    case k128: return launch_gemm<DT, OT, TERMS, LOW, false, 2, 2, 2, 2>(a, s);
+    case k96: return launch_gemm<DT, OT, TERMS, LOW, false, 3, 1, 1, 4>(a, s);
+    case k64: return launch_gemm<DT, OT, TERMS, LOW, false, 2, 1, 1, 4>(a, s);
   }
 }
 
 template <int DT, int OT, int TERMS>
 void choose_gemm(const Gemm16& a, hipStream_t s) {
-  if (a.splits > 1) launch_gemm<DT, 0, TERMS, false, true, 2, 2, 2, 2>(a, s);
-  else if (a.ad.order) launch_shape<DT, OT, TERMS, true>(a, s);
-  else launch_shape<DT, OT, TERMS, false>(a, s);
+  if (a.splits > 1) launch_gemm<DT, 0, TERMS, 0, true, 2, 2, 2, 2>(a, s);
+  else if (!a.S) launch_shape<DT, OT, TERMS, 0>(a, s);
+  else if (a.ad.order) launch_shape<DT, OT, TERMS, 2>(a, s);
+  else launch_shape<DT, OT, TERMS, 1>(a, s);
 }
 
 // dst[t][0 .. kp) = src[t][0 .. d) (through perm, entries outside 0 .. d-1
