@@ -59,16 +59,18 @@ extern "C" {
  * Y[t, i] = round_yt( sum_j W_hat[i, j] X[t, src(j)] + delta[t, i] ),
  * src(j) = col_perm[j], or j.  Up to 1023 tokens, and for fp32 results of any
  * number, codes are multiplied as whole numbers and the rulers applied to each
- * group's fp32 sum, so the weights are not rounded:
- * the fp32 result is within about 2^-16 sum_j scale (2 * 2^bits + q + zero)
- * |x_j| of the exact product (a bound; usual errors are far smaller).  |X| must stay below 2^115 (larger bf16 values can
- * overflow a group's sum); a token that holds an infinity or NaN gives NaN.
+ * group's fp32 sum, so the weights are not rounded: the fp32 result is within
+ * about 2^-16 sum_j scale (2 * 2^bits + q + zero) |x_j| of the exact product (a
+ * bound; usual errors are far smaller).  16-bit results of more tokens take
+ * weights rounded once to X's type, as gptq_linear_forward does.  |X| must stay
+ * below 2^115 (larger bf16 values can overflow a group's sum); a token that
+ * holds an infinity or NaN gives infinities or NaN, the others are not touched.
  *
  * X  : n_tok x c of type xt, 16-byte aligned, ldx a multiple of 8 and >= c
  *      (2-byte alignment and any ldx >= c when col_perm is given).
  * Y  : n_tok x r of type yt (GPTQ_F32 or xt), row stride ldy; overlaps no input.
- * ws : gptq_packed_linear_workspace_size(n_tok, c, rank, col_perm != NULL)
- *      bytes, rank 0 without adapters (NULL when that is 0).
+ * ws : gptq_packed_linear_workspace_size() bytes (rank 0 without adapters;
+ *      NULL when that is 0).
  * ------------------------------------------------------------------------ */
 gptq_status gptq_packed_linear_workspace_size(int64_t n_tok, int64_t r, int64_t c, gptq_dtype yt, int64_t rank,
                                               int has_perm, size_t* bytes);

@@ -162,6 +162,8 @@ def packed_linear_backward(dY: torch.Tensor, packed: torch.Tensor, scales: torch
     _rows16(dY, "dY")
     _need(packed, "packed", torch.uint32, 2, on_gpu=False)
     n = dY.shape[0]
+    if bits not in (3, 4):
+        raise ValueError("bits must be 3 or 4")
     c = int(cols) if cols is not None else packed.shape[1] * 32 // int(bits)
     r = _layer(packed, scales, zeros, bits, c, perm)
     if dY.shape[1] != r:

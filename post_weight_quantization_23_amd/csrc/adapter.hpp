@@ -214,13 +214,16 @@ GPTQ_DEV float rank_dot(const float* S, const uint16_t* b, int rank) {
 
 // out[q] += S B_a^T of one adapter's tokens among the Tile::E of a tile (accumulator
 // layout, row = place): a product over all of them, of which only the members'
-// rows are kept.  t: the token of the lane's place, or -1.
+// rows are kept.  It goes on from out, so that a token's sum does not depend on
+// whether it shares its tile.  t: the token of the lane's place, or -1.
 template <int DT, int TERMS, int NT, class Acc>
 GPTQ_DEV void expand_shared(const Adapters& ad, int a, uint32_t members, const uint16_t* B, int64_t rows, const float* S, int64_t t,
                             const int64_t (&row)[NT], Acc (&out)[NT]) {
   using Tile = TileShape<Acc>;
   const int lane = threadIdx.x & 63, kq = lane / Tile::E;
-  Acc acc[NT] = {};
+  Acc acc[NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) acc[q] = out[q];
   for (int k0 = 0; k0 < ad.rank; k0 += Tile::K) {
     const int k = k0 + 8 * kq;
     float v[8] = {};
@@ -239,7 +242,7 @@ GPTQ_DEV void expand_shared(const Adapters& ad, int a, uint32_t members, const u
   for (int q = 0; q < NT; ++q)
 #pragma unroll
     for (int i = 0; i < Tile::C; ++i)
-      if ((members >> Tile::acc_row(lane, i)) & 1) out[q][i] += acc[q][i];
+      out[q][i] = (members >> Tile::acc_row(lane, i)) & 1 ? acc[q][i] : out[q][i];
 }
 
 // out[q] += (S B_a^T) of the tokens at places t0 .. and NT sets of a tile's outputs, in

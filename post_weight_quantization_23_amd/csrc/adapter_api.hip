@@ -121,6 +121,26 @@ gptq_status check_clash(const char* fn, int c) {
   return GPTQ_OK;
 }
 
+// An output against the arrays of a packed layer, and against adapters.
+gptq_status check_clashes(const char* fn, const void* out, int64_t eo, const uint32_t* packed, int64_t r, int64_t c, int bits,
+                          int64_t ld_words, const float* scales, const int32_t* zeros, int64_t ld_groups, int64_t groupsize,
+                          const int32_t* perm) {
+  const int64_t groups = groupsize > 0 && groupsize < c ? (c + groupsize - 1) / groupsize : 1;
+  if (gptq_status st = check_clash(fn, clash(out, eo, packed, r, ld_words, c / 32 * bits, 4))) return st;
+  if (gptq_status st = check_clash(fn, clash(out, eo, scales, r, ld_groups, groups, 4))) return st;
+  if (gptq_status st = check_clash(fn, clash(out, eo, zeros, r, ld_groups, groups, 4))) return st;
+  return perm ? check_clash(fn, clash(out, eo, perm, 1, c, c, 4)) : GPTQ_OK;
+}
+
+gptq_status check_clashes(const char* fn, const void* out, int64_t eo, int64_t n, int64_t r, int64_t c, const void* A, const void* B,
+                          int64_t m, int64_t rank, const int32_t* index, const float* alpha) {
+  if (gptq_status st = check_clash(fn, clash(out, eo, A, m * rank, c, c, 2))) return st;
+  if (gptq_status st = check_clash(fn, clash(out, eo, B, m * r, rank, rank, 2))) return st;
+  if (index)
+    if (gptq_status st = check_clash(fn, clash(out, eo, index, 1, n, n, 4))) return st;
+  return alpha ? check_clash(fn, clash(out, eo, alpha, 1, m, m, 4)) : GPTQ_OK;
+}
+
 // What the packed product's kernels prepare: the gathered activations of a few
 // tokens of an act-order layer, or what many tokens need.
 int64_t forward_bytes(int64_t n, int64_t r, int64_t c, bool perm, int yt) {
@@ -167,7 +187,8 @@ gptq::DownProblem down_problem(const void* X, int64_t n, int64_t d, int64_t ldx,
 
 // Every launch's grid, at the launch helpers' workgroup shapes.
 bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
-  return groups_for(n * (rank > 0 ? rank : 1), 4) <= kMaxGroups256 &&                    // down: a wave per value
+  return n <= kMaxGroups256 &&                                                           // prepared activations: a workgroup each
+         groups_for(2 * n * (rank > 0 ? rank : 1), 4) <= kMaxGroups256 &&                // down: a wave per value, both sides
          groups_for(n, 16) * groups_for(r, 16) <= kMaxGroups256 / 2 &&                   // forward: 512 threads per 16 rows
          groups_for(n, 16) * groups_for(r > c ? r : c, 256) <= kMaxGroups256 &&          // up
          groups_for(n, 32) * groups_for(r > c ? r : c, 128) <= kMaxGroups256 / 16 &&     // tiles, in up to 16 parts
@@ -175,9 +196,9 @@ bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
          groups_for(n * (r / 8 + 8), 256) <= kMaxGroups256 &&                            // padded rows
          groups_for(n * (c / 8), 256) <= kMaxGroups256 &&                                // gather
          n * groups_for(r > c ? r : c, 256) <= kMaxGroups256 * (n > 64 && n > 4 * m ? 32 : 1) &&   // up
-         groups_for(gptq::list_places(n, m) / 8 * (rank > 0 ? rank : 1), 256) <= kMaxGroups256 && gptq::list_places(n, m) < INT_MAX &&  // lists
+         groups_for(2 * (gptq::list_places(n, m) / 8) * (rank > 0 ? rank : 1), 256) <= kMaxGroups256 && gptq::list_places(n, m) < INT_MAX &&  // lists
          m * groups_for(r > c ? r : c, 64) * 5 + groups_for(n * (r + c) / 8 + 16, 1024) <= kMaxGroups256 / 4 &&   // preparation (1024 threads)
-         m * groups_for(r > c ? r : c, 128) * 16 <= kMaxGroups256 &&                     // gradients (16 splits of 4 rank blocks, 4 a group)
+         m * (groups_for(r, 128) + groups_for(c, 128)) * 16 <= kMaxGroups256 &&          // gradients (16 splits of 4 rank blocks, 4 a group)
          groups_for(m * rank * (r > c ? r : c), 1024) <= kMaxGroups256;                  // join
 }
 
@@ -216,6 +237,7 @@ gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t r, int64_t c, g
   if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
   if (rank != 0)
     if (gptq_status st = check_rank(fn, 1, rank)) return st;
+  if (!grids_fit(n, r, c, rank, rank != 0)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank) + rows_bytes(n, c, rank));
   return ok();
 }
@@ -243,11 +265,9 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
   if (!aligned(Y, elem_size(yt))) return fail(GPTQ_EALIGN, fn, "Y misaligned");
   const int64_t ey = extent_bytes(n, ldy, r, (int64_t)elem_size(yt));
   if (gptq_status st = check_clash(fn, clash(Y, ey, X, n, ldx, c, 2))) return st;
-  if (gptq_status st = check_clash(fn, clash(Y, ey, packed, r, ld_words, c / 32 * bits, 4))) return st;
-  if (low) {
-    if (gptq_status st = check_clash(fn, clash(Y, ey, A, m * rank, c, c, 2))) return st;
-    if (gptq_status st = check_clash(fn, clash(Y, ey, B, m * r, rank, rank, 2))) return st;
-  }
+  if (gptq_status st = check_clashes(fn, Y, ey, packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm)) return st;
+  if (low)
+    if (gptq_status st = check_clashes(fn, Y, ey, n, r, c, A, B, m, rank, index, alpha)) return st;
   if (gptq_status st = need_ws(fn, ws, ws_bytes, forward_bytes(n, r, c, perm != nullptr, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank) + rows_bytes(n, c, rank))) return st;
   Carve carve{static_cast<char*>(ws)};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -325,11 +345,9 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
   if (!aligned(dY, 2) || !aligned(dX, elem_size(ot))) return fail(GPTQ_EALIGN, fn, "misaligned pointer");
   const int64_t ex = extent_bytes(n, ldx, c, (int64_t)elem_size(ot));
   if (gptq_status st = check_clash(fn, clash(dX, ex, dY, n, ldy, r, 2))) return st;
-  if (gptq_status st = check_clash(fn, clash(dX, ex, packed, r, ld_words, c / 32 * bits, 4))) return st;
-  if (low) {
-    if (gptq_status st = check_clash(fn, clash(dX, ex, A, m * rank, c, c, 2))) return st;
-    if (gptq_status st = check_clash(fn, clash(dX, ex, B, m * r, rank, rank, 2))) return st;
-  }
+  if (gptq_status st = check_clashes(fn, dX, ex, packed, r, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm)) return st;
+  if (low)
+    if (gptq_status st = check_clashes(fn, dX, ex, n, r, c, A, B, m, rank, index, alpha)) return st;
   const int terms = gptq::gemm16_terms((int)xt, (int)ot);
   const int64_t need = backward_bytes(n, r, c, (int)xt, (int)ot) + align256(m * c * rank * 2) + align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank) +
                        order_bytes(n, rank) + rows_bytes(n, r, rank);
@@ -392,8 +410,7 @@ gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n, int64_t c,
   if (!aligned(X, 2) || !aligned(Y, el) || !aligned(out, el)) return fail(GPTQ_EALIGN, fn, "misaligned pointer");
   const int64_t eo = extent_bytes(n, ldo, r, el);
   if (gptq_status st = check_clash(fn, clash(out, eo, X, n, ldx, c, 2))) return st;
-  if (gptq_status st = check_clash(fn, clash(out, eo, A, m * rank, c, c, 2))) return st;
-  if (gptq_status st = check_clash(fn, clash(out, eo, B, m * r, rank, rank, 2))) return st;
+  if (gptq_status st = check_clashes(fn, out, eo, n, r, c, A, B, m, rank, index, alpha)) return st;
   if (!(out == Y && ldo == ldy))
     if (gptq_status st = check_clash(fn, clash(out, eo, Y, n, ldy, r, el))) return st;
   if (gptq_status st = need_ws(fn, ws, ws_bytes, low_bytes(n, c, rank) + order_bytes(n, rank) + rows_bytes(n, c, rank))) return st;
@@ -452,11 +469,14 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   const int64_t ea = extent_bytes(m * rank, c, c, 4), eb = extent_bytes(m * r, rank, rank, 4);
   const int64_t ed = dX ? extent_bytes(n, ldd, c, el) : 0;
   struct { const void* p; int64_t rows, ld, cols, elem; } in[] = {
-      {dY, n, ldy, r, 2}, {X, n, ldx, c, 2}, {A, m * rank, c, c, 2}, {B, m * r, rank, rank, 2}};
+      {dY, n, ldy, r, 2}, {X, n, ldx, c, 2}};
   for (const auto& v : in)
     for (const auto& o : {std::pair<const void*, int64_t>{gA, ea}, {gB, eb}, {dX, ed}})
       if (o.first)
         if (gptq_status st = check_clash(fn, clash(o.first, o.second, v.p, v.rows, v.ld, v.cols, v.elem))) return st;
+  for (const auto& o : {std::pair<const void*, int64_t>{gA, ea}, {gB, eb}, {dX, ed}})
+    if (o.first)
+      if (gptq_status st = check_clashes(fn, o.first, o.second, n, r, c, A, B, m, rank, index, alpha)) return st;
   if (overlaps(gA, ea, gB, eb) || (dX && ed > 0 && (overlaps(dX, ed, gA, ea) || overlaps(dX, ed, gB, eb))))
     return fail(GPTQ_EINVAL, fn, "outputs overlap");
   if (base && base != dX)

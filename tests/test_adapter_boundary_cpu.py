@@ -212,3 +212,38 @@ def test_python_checks_before_the_device():
         adapter.adapter_backward(v["dY"], v["X"], **low, base=v["X"])
     with pytest.raises(TypeError, match="out"):
         adapter.adapter_backward(v["dY"], v["X"], **low, out={"A": v["A"]})
+    with pytest.raises(ValueError, match="bits"):
+        adapter.packed_linear_backward(v["dY"], v["packed"], v["scales"], v["zeros"], 0, 32)
+
+
+def test_outputs_inside_small_inputs_and_sizes_past_a_grid(lib):
+    """An output may not lie in rulers, permutation, index or factors either; sizes that no grid holds have no workspace."""
+    out = C.c_size_t(7)
+    assert lib.gptq_packed_linear_workspace_size(1 << 30, 1 << 30, 1 << 30, 0, 128, 1, C.byref(out)) == 5
+    assert lib.gptq_packed_linear_workspace_size((1 << 24) + 1, 8, 32, 0, 0, 0, C.byref(out)) == 5
+
+    def packed(back, **kw):
+        v = packed_args(**kw)
+        args = (v["packed"], v["r"], v["c"], v["bits"], v["ldw"], v["s"], v["z"], v["ldg"], v["gs"], v["perm"], v["A"], v["B"],
+                v["m"], v["rank"], v["index"], v["alpha"], v["Y"], v["yt"])
+        if back:
+            return lib.gptq_packed_linear_backward(v["X"], v["xt"], v["n"], 8, *args, 256, v["ws"], v["nws"], None)
+        return lib.gptq_packed_linear(v["X"], v["xt"], v["n"], 256, *args, 8, v["ws"], v["nws"], None)
+
+    low = dict(A=P(5), B=P(6), m=2, rank=8, index=P(7), alpha=P(10))
+    for back in (False, True):
+        assert packed(back, **low) == 6                                  # well-formed but for the workspace
+        for p in (P(2), P(3), P(7), P(10)):
+            assert packed(back, **low, Y=p) == 1
+        assert packed(back, perm=P(4), Y=at(P(4), 64)) == 1
+
+    def add(y):
+        return lib.gptq_adapter_add(P(0), 1, 4, 64, 64, P(1), P(2), 2, 8, 10, P(7), P(8), P(3), 1, 10, y, 10, None, 0, None)
+
+    def grads(gA, gB, dX):
+        return lib.gptq_adapter_backward(P(0), 10, P(1), 64, 1, 4, 10, 64, P(2), P(3), 2, 8, P(7), P(8), gA, gB, None, dX, 1, 64,
+                                         None, 0, None)
+
+    assert add(P(4)) == 6 and add(P(7)) == 1 and add(P(8)) == 1
+    assert grads(P(4), P(5), P(6)) == 6
+    assert grads(P(7), P(5), P(6)) == 1 and grads(P(4), P(8), P(6)) == 1 and grads(P(4), P(5), P(8)) == 1

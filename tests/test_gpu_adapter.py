@@ -401,6 +401,73 @@ def test_order_of_tokens_does_not_matter():
     assert torch.equal(g1["A"], g2["A"]) and torch.equal(g1["B"], g2["B"])
 
 
+# Many tokens, adapters in runs and mixed: tiles that one adapter has to itself
+# beside shared ones, ranks past 64.
+MANY = [(1100, 264, 416, 4, 72, torch.bfloat16), (1030, 1030, 96, 3, 16, torch.float16)]
+
+
+@pytest.mark.parametrize("n,r,c,m,rank,dt", MANY)
+def test_many_tokens_keep_requests_apart(n, r, c, m, rank, dt):
+    L = Layer(r, c, 4, 32, 9, False)
+    X, dY, Y = normal((n, c), 1).to(dt), normal((n, r), 2).to(dt), normal((n, r), 4).to(dt)
+    ad = make_adapters(m, rank, r, c, n, dt, 3, "runs")
+    ad["index"][5::200] = -1
+
+    def run(ad, X, dY, Y):
+        g = gq().adapter_backward(dY, X, **ad, want_dX=True)
+        return [gq().packed_linear(X, *L.args(), **ad), gq().packed_linear(X, *L.args(), **ad, out_dtype=torch.float32),
+                gq().packed_linear_backward(dY, *L.args(), **ad),
+                gq().packed_linear_backward(dY, *L.args(), **ad, out_dtype=torch.float32), gq().adapter_add(Y, X, **ad), g["dX"]]
+
+    clean = run(ad, X, dY, Y)
+    check("Y", clean[0], *forward64(L, X, ad, dt))
+    # shuffled tokens, the same bits
+    sh = torch.randperm(n, device="cuda")
+    moved = run({**ad, "index": ad["index"][sh].contiguous()}, X[sh].contiguous(), dY[sh].contiguous(), Y[sh].contiguous())
+    for a, b in zip(clean, moved):
+        assert torch.equal(a[sh], b)
+    # infinities and NaN of one request
+    bad = {k: v.clone() for k, v in ad.items()}
+    bad["A"][1, 3, 5], bad["B"][1, 7, 1] = float("nan"), float("inf")
+    X2, dY2 = X.clone(), dY.clone()
+    X2[4, 10], dY2[9, 3] = float("inf"), float("nan")
+    got = run(bad, X2, dY2, Y)
+    keep = ad["index"] != 1
+    keep[4] = keep[9] = False
+    for a, b in zip(clean, got):
+        assert torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.parametrize("n,r,c,m,rank,dt", MANY)
+def test_many_tokens_graph_replay(n, r, c, m, rank, dt):
+    """Captured calls replayed with eager work of the same kernels between."""
+    L = Layer(r, c, 3, 32, 29, True)
+    ads = [make_adapters(m, rank, r, c, n, dt, 3 + i, kind) for i, kind in enumerate(("runs", "mixed", "runs"))]
+    Xs, dYs = [normal((n, c), 20 + i).to(dt) for i in range(3)], [normal((n, r), 30 + i).to(dt) for i in range(3)]
+
+    def step(X, dY, ad):
+        g = gq().adapter_backward(dY, X, **ad, want_dX=True)
+        return [gq().packed_linear(X, *L.args(), perm=L.perm, **ad), g["A"], g["B"], g["dX"],
+                gq().packed_linear(X, *L.args(), perm=L.perm, **ad, out_dtype=torch.float32),
+                gq().packed_linear_backward(dY, *L.args(), perm=L.perm, **ad), gq().adapter_add(dY, X, **ad)]
+
+    want = [step(*v) for v in zip(Xs, dYs, ads)]
+    X, dY, ad = Xs[0].clone(), dYs[0].clone(), {k: v.clone() for k, v in ads[0].items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(X, dY, ad)
+    for rep in (1, 2, 0, 1):
+        X.copy_(Xs[rep])
+        dY.copy_(dYs[rep])
+        for k in ad:
+            ad[k].copy_(ads[rep][k])
+        step(Xs[2], dYs[2], ads[2])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[rep], got)), rep
+
+
 def test_offsets_past_32_bits():
     """Rows whose byte and element offsets pass 2^32."""
     n, r, c = 40, 24, 64
