@@ -250,28 +250,32 @@ GPTQ_DEV void add_base(const UpArgs& u, float (&v)[8], int64_t t, int64_t j, int
 }
 
 // Many tokens: a wave takes 32 tokens x 64 outputs on the matrix cores.  Memory
-// bounds it (180 MB for 4099 tokens of 11008 outputs): what the product is added to
-// is asked for first, so that its way from memory runs beside the rank values'
-// (51 us instead of 60).
-template <int DT, int YT>
+// bounds it (180 MB for 4099 tokens of 11008 outputs).  PLAIN: added to rows on 16
+// bytes, of whole eights; these are asked for first, so that their way from
+// memory runs beside the rank values' (48 us, 60 without; a wave of 32 outputs, with
+// more waves in a SIMD: 54).
+template <int DT, int YT, bool PLAIN>
 __global__ __launch_bounds__(256) void up_tiles_kernel(UpArgs u) {
   constexpr int PIECES = YT == 0 ? 2 : 1;   // of 16 bytes in eight outputs
-  __shared__ float turn[4][32 * 68];
+  __shared__ float turn[4][32 * 36];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t tile = blockIdx.x / u.col_tiles, ct = blockIdx.x - tile * u.col_tiles;
-  const int64_t t0 = tile * 32, j0 = ct * 256 + 64 * wave, j = j0 + 8 * (lane & 7);
-  const bool early = u.base && !u.part && u.vec_base && j + 8 <= u.rows;
-  int64_t tok[4];
-  u32x4 base[4][PIECES];
+  const int64_t t0 = tile * 32, j0 = ct * 256 + 64 * wave;
+  // this lane's eight outputs of four places: 32 q + 8 (lane & 3) of place 16 k + lane / 4
+  int64_t tok[2];
+  u32x4 base[2][2][PIECES];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) tok[k] = u.ad.token(t0 + 8 * k + (lane >> 3), u.n);
-  if (early) {
+  for (int k = 0; k < 2; ++k) tok[k] = u.ad.token(t0 + 16 * k + (lane >> 2), u.n);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+  for (int q = 0; q < 2; ++q) {
+    const int64_t j = j0 + 32 * q + 8 * (lane & 3);
+    if (!PLAIN || j >= u.rows) continue;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int p = 0; p < PIECES; ++p)
-        base[k][p] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(u.base) +
-                                                     (max(tok[k], (int64_t)0) * u.ldb + j) * (YT == 0 ? 4 : 2) + 16 * p);
+        base[q][k][p] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(u.base) +
+                                                        (max(tok[k], (int64_t)0) * u.ldb + j) * (YT == 0 ? 4 : 2) + 16 * p);
   }
   int64_t row[2];
   floatx16 acc[2];
@@ -283,27 +287,34 @@ __global__ __launch_bounds__(256) void up_tiles_kernel(UpArgs u) {
   }
   expand_add<DT, YT == 0 ? 3 : 2, 2>(u.ad, u.B, u.rows, u.S, t0, u.n, row, acc);
   float* own = turn[wave];
-  turn_tile<2>(own, acc);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (tok[k] < 0 || j >= u.rows) continue;
-    const int count = (int)min((int64_t)8, u.rows - j);
-    float v[8];
-    load8f(own + (8 * k + (lane >> 3)) * 68 + 8 * (lane & 7), v);
-    if (early) {
+  for (int q = 0; q < 2; ++q) {
+    const int64_t j = j0 + 32 * q + 8 * (lane & 3);
+    const floatx16 half[1] = {acc[q]};
+    turn_tile<1>(own, half);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (YT == 0) {
-          const uint32_t w = base[k][e >> 2][e & 3];
-          v[e] += __builtin_bit_cast(float, w);
-        } else {
-          v[e] += f16_to_f32<YT>((base[k][0][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+    for (int k = 0; k < 2; ++k) {
+      if (tok[k] < 0 || j >= u.rows) continue;
+      float v[8];
+      load8f(own + (16 * k + (lane >> 2)) * 36 + 8 * (lane & 3), v);
+      if constexpr (PLAIN) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (YT == 0) {
+            const uint32_t w = base[q][k][e >> 2][e & 3];
+            v[e] += __builtin_bit_cast(float, w);
+          } else {
+            v[e] += f16_to_f32<YT>((base[q][k][0][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+          }
         }
+        store8<YT>(u.out, tok[k] * u.ldo + j, v, 8, true);
+      } else {
+        const int count = (int)min((int64_t)8, u.rows - j);
+        add_base<YT>(u, v, tok[k], j, count);
+        store8<YT>(u.out, tok[k] * u.ldo + j, v, count, u.vec_out);
       }
-    } else {
-      add_base<YT>(u, v, tok[k], j, count);
     }
-    store8<YT>(u.out, tok[k] * u.ldo + j, v, count, u.vec_out);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the other half replaces it
   }
 }
 
@@ -763,12 +774,13 @@ void launch_adapter_up(const UpArgs& given, int xt, int yt, hipStream_t s) {
     else hipLaunchKernelGGL((join_rows_kernel<kF16>), flat, dim3(256), 0, s, u);
     return;
   }
-  const bool few = by_token(u.n, u.ad.m);
+  const bool few = by_token(u.n, u.ad.m), plain = u.base && !u.part && u.vec_base && u.vec_out && u.rows % 8 == 0;
   const dim3 grid((unsigned)((few ? u.n : (u.n + 31) / 32) * u.col_tiles)), block(256);
 #define GPTQ_UP(D_, Y_)                                                                \
   do {                                                                                 \
     if (few) hipLaunchKernelGGL((up_kernel<D_, Y_>), grid, block, 0, s, u);            \
-    else hipLaunchKernelGGL((up_tiles_kernel<D_, Y_>), grid, block, 0, s, u);          \
+    else if (plain) hipLaunchKernelGGL((up_tiles_kernel<D_, Y_, true>), grid, block, 0, s, u); \
+    else hipLaunchKernelGGL((up_tiles_kernel<D_, Y_, false>), grid, block, 0, s, u);   \
   } while (0)
   if (xt == kBF16) { if (yt == 0) GPTQ_UP(kBF16, 0); else GPTQ_UP(kBF16, kBF16); }
   else { if (yt == 0) GPTQ_UP(kF16, 0); else GPTQ_UP(kF16, kF16); }
