@@ -71,7 +71,8 @@ __global__ __launch_bounds__(256) void down_kernel(DownArgs g) {
 // Steps of 64 come into LDS by loads that write it (double buffered): loading
 // operands straight into registers touches 64 places of 16 bytes per
 // instruction, which the L1 cache takes one a cycle, against 16 here (4096
-// tokens of 11008, rank 64: 37 us, memory's share is 18).  The adapters that
+// tokens of 11008, rank 64: 37 us, memory's share is 18; with 4096 columns beside
+// them 41 us now, 3 TB/s).  The adapters that
 // occur among the tokens are taken in turn; each writes its own tokens' rows.
 // Parts are added by the kernels that read them.
 template <int DT, int RT>
@@ -534,7 +535,8 @@ __global__ __launch_bounds__(256) void sorted_terms_kernel(TermsArgs g) {
 // A wave takes 128 columns x 16 RT rank rows and one of `splits` parts of the
 // adapter's tokens, by itself (four waves joined through LDS spent more time
 // there than on their five blocks of tokens); parts are added in order by
-// join_kernel.
+// join_kernel.  4096 tokens of 11008 and 4096 columns, rank 64, take 57 us, 2.2 TB/s of
+// rows.
 template <int DT, int RT>
 __global__ __launch_bounds__(256) void grad_kernel(GradArgs g) {
   const int lane = threadIdx.x & 63, m = lane & 15, kq = lane >> 4;
@@ -674,9 +676,12 @@ int down_splits(int64_t n, int64_t d) {
 // tile would hold ten and more.
 bool by_token(int64_t n, int m) { return n <= 64 || n <= 4 * (int64_t)m; }
 
-// Rank rows of a gradient wave: 32 (64 would leave one wave per SIMD).
+// Rank rows of a gradient wave: 32 (more do not fit its registers).
 int grad_rows(int rank) { return rank <= 16 ? 16 : 32; }
 
+// Parts of an adapter's tokens, up to 512 waves: more of them write and read more sums
+// than they gain (4096 tokens, five adapters of rank 64 on 11008 x 4096: 113 us with
+// 512 waves, 122 with 1024, 136 with 2048; eight of rank 32 on 8192 x 8192: 53, 69, 81).
 int grad_splits(int64_t n, int m, int64_t cols, int rank) {
   if (n == 0 || cols == 0) return 1;
   const int64_t waves = (cols + 127) / 128 * m * ((rank + grad_rows(rank) - 1) / grad_rows(rank));

@@ -60,7 +60,7 @@ constexpr int steps_ahead(int tg) { return tg == 1 ? 2 : 1; }
 // LDS bytes of a step of one wave: 16 NT rows of words, then tokens of 256 bytes.
 constexpr int step_bytes(int bits, int nt, int quads) { return 256 * bits * nt + 1024 * quads; }
 
-// 16 TG tokens x 16 rows per workgroup.  The waves split the columns in runs of
+// 16 TG tokens x 16 NT rows per workgroup.  The waves split the columns in runs of
 // AHEAD steps of 128 and are joined through LDS in wave order.
 //
 // What a run reads comes through the wave's own part of LDS, by loads that write
@@ -68,8 +68,9 @@ constexpr int step_bytes(int bits, int nt, int quads) { return 256 * bits * nt +
 // operands straight into registers touches 64 places of 16 bytes per
 // instruction, and the L1 cache takes them one a cycle: that, not memory, set the
 // pace (16 tokens of 11008 x 4096 at 3 bits: 22 us, and 40 thousand accesses
-// per CU).  The loads into LDS give 4 (words) or 16 (activations) consecutive
-// lanes one row.
+// per CU; 14 us now).  The loads into LDS give 4 (words) or 16 (activations)
+// consecutive lanes one row.  What bounds it now are the waits for a run and about
+// 140 instructions per step of 128 columns, not memory (1.3 TB/s of words).
 //
 // A lane then holds chunk kq of row m (lane = m + 16 kq); the blocks of codes are
 // transposed, so that product j takes chunk j alone.  Steps, tokens and rows past
