@@ -308,12 +308,12 @@ GPTQ_DEV void turn_tile(float* lds, const floatx16 (&acc)[NT]) {
 template <int OT, int NT>
 GPTQ_DEV void store_tile(float* lds, const floatx16 (&acc)[NT], const Adapters& ad, void* out, int64_t t0, int64_t n, int64_t j0,
                          int64_t cols, int64_t ldo, bool vec) {
-  constexpr int W = 32 * NT, LPR = W / 8, RPP = 64 / LPR;
+  constexpr int W = 32 * NT, RUNS = W / 8;   // of a row
   const int lane = threadIdx.x & 63;
   turn_tile<NT>(lds, acc);
 #pragma unroll
-  for (int k = 0; k < 32 / RPP; ++k) {
-    const int r = RPP * k + lane / LPR, c = 8 * (lane % LPR);
+  for (int k = 0; k < RUNS / 2; ++k) {
+    const int run = 64 * k + lane, r = run / RUNS, c = 8 * (run % RUNS);
     const int64_t t = ad.token(t0 + r, n), j = j0 + c;
     if (t < 0 || j >= cols) continue;
     float v[8];

@@ -40,6 +40,7 @@ GPTQ_DEV void expand_staged(const Gemm16& a, const Places<32 * MT * WM>* pl, uns
   constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, RANKS = 64;
   constexpr int QS = TM / 4 / (WM * WN), QB = TN / 8 / WN;   // load instructions per wave: 4 rows of S, 8 of B
   static_assert(QS * 4 * WM * WN == TM && QB * 8 * WN == TN, "rows divide over the waves");
+  static_assert(TM * 256 + WM * TN * 128 <= 2 * (TM + TN) * ROWB, "S and each wave row's B fit the operands' LDS");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31, h = lane >> 5;
   const int rank = a.ad.rank;
   unsigned char* bs = smem + TM * 256 + (wave / WN) * TN * 128;   // B of the waves with these tokens
@@ -259,20 +260,22 @@ void launch_gemm(Gemm16 a, hipStream_t s) {
                      dim3((unsigned)((int64_t)a.tok_tiles * a.col_tiles * a.splits)), dim3(64 * WM * WN), LDS, s, a);
 }
 
-// Tiles: 256 x 256 (8 waves of 128 x 64), 128 x 128 (4 of 64 x 64), 96 and 64 x 128 (4 of
-// 96 or 64 x 32).  A launch takes as long as its fullest CU, ceil(tiles / 256) of
-// them, and a large tile reads less of LDS for each product.  A call of 1024 tokens
-// of 4096 x 4096 took 101, 59, 60 and 57 us in this order, of 2085 tokens 108, 116, 107
-// and 109, of 8192 254, 302, 331 and 340; the choice was within 12 % of the best
-// on 44 sizes (512 to 8192 tokens, four layers).
-enum Shape { k256, k128, k96, k64 };
+// Tiles: 256 x 256 (8 waves of 128 x 64), 256 x 192 and 192 x 256 (8 of 64 x 96 and 96 x 64),
+// 128 x 128 (4 of 64 x 64), 96 and 64 x 128 (4 of 96 or 64 x 32).  A launch takes as
+// long as its fullest CU, ceil(tiles / 256) of them, and a large tile reads less of
+// LDS for each product.  The input gradient of 2085 tokens of 4096 x 4096 took 107, 95, 96,
+// 114, 107 and 110 us in this order, of 6000 tokens of 11008 x 4096 577, 644, 527, 636, 705
+// and 837, of 1024 tokens of 1024 x 4096 38, 35, 34, 23, 26 and 22; the choice was within
+// 9 % of the best on 84 sizes (300 to 8192 tokens, six layers), 1 % on average.
+enum Shape { k256, k256x192, k192x256, k128, k96, k64, kShapes };
 
-Shape choose_shape(int64_t n, int64_t cols) {
-  const int64_t tm[4] = {256, 128, 96, 64}, tn[4] = {256, 128, 128, 128};
-  const double cost[4] = {0.83, 1.0, 1.08, 1.15};
+Shape choose_shape(int64_t n, int64_t cols, bool low) {
+  constexpr int64_t tm[kShapes] = {256, 256, 192, 128, 96, 64}, tn[kShapes] = {256, 192, 256, 128, 128, 128};
+  constexpr double cost[kShapes] = {0.83, 0.84, 0.84, 1.0, 1.12, 1.15};
   Shape best = k256;
   double least = 1e30;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kShapes; ++i) {
+    if (low && i == k256x192) continue;   // four wave rows, each with an adapter's B, are more than its LDS holds
     const int64_t tiles = (n + tm[i] - 1) / tm[i] * ((cols + tn[i] - 1) / tn[i]);
     const double us = cost[i] * tm[i] * tn[i] * (double)((tiles + 255) / 256);
     if (us < least) least = us, best = (Shape)i;
@@ -292,11 +295,16 @@ int gemm16_splits(int64_t n, int64_t cols, int64_t steps) {
 
 template <int DT, int OT, int TERMS, int LOW>
 void launch_shape(const Gemm16& a, hipStream_t s) {
-  switch (choose_shape(a.n, a.cols)) {
+  switch (choose_shape(a.n, a.cols, LOW != 0)) {
     case k256: return launch_gemm<DT, OT, TERMS, LOW, false, 4, 2, 2, 4>(a, s);
+    case k256x192:
+      if constexpr (LOW == 0) launch_gemm<DT, OT, TERMS, 0, false, 2, 3, 4, 2>(a, s);
+      return;
+    case k192x256: return launch_gemm<DT, OT, TERMS, LOW, false, 3, 2, 2, 4>(a, s);
     case k128: return launch_gemm<DT, OT, TERMS, LOW, false, 2, 2, 2, 2>(a, s);
     case k96: return launch_gemm<DT, OT, TERMS, LOW, false, 3, 1, 1, 4>(a, s);
     case k64: return launch_gemm<DT, OT, TERMS, LOW, false, 2, 1, 1, 4>(a, s);
+    case kShapes: return;
   }
 }
 

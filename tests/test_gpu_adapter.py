@@ -179,6 +179,14 @@ SHAPES = [
     (1151, 1030, 96, 4, 32, True, "fp16", "fp32", (1, 64, "all")),
     (520, 4100, 4128, 4, 128, False, "bf16", "bf16", (3, 16, "runs")),
     (77, 6001, 8224, 3, 32, True, "fp16", "fp16", (2, 40, "mixed")),
+    # every tile of the 16-bit product, with adapters in runs, mixed, and one for all
+    (2085, 4096, 64, 4, -1, False, "bf16", "bf16", (5, 64, "runs")),
+    (2085, 4096, 64, 4, -1, False, "fp16", "fp16", None),
+    (4096, 4096, 64, 3, 32, False, "fp16", "fp16", (3, 72, "mixed")),
+    (4000, 4090, 32, 4, -1, False, "bf16", "bf16", (1, 128, "all")),
+    (1024, 4096, 96, 4, 32, True, "bf16", "bf16", (4, 40, "mixed")),
+    (1050, 2900, 64, 3, -1, False, "fp16", "fp16", (6, 24, "runs")),
+    (1100, 1500, 64, 4, 64, False, "bf16", "bf16", (9, 8, "mixed")),
 ]
 
 
@@ -222,6 +230,20 @@ def test_packed_linear_backward(n, r, c, bits, gs, act, dt, out, low):
     torch.cuda.synchronize()
     assert dX.shape == (n, c) and dX.dtype == DT[out]
     check("dX", dX, *backward64(L, dY, ad, DT[out]))
+
+
+# Large tiles of the 16-bit product, fp32 results in several terms.
+BACKWARD_SHAPES = [
+    (2085, 64, 4096, 4, 128, False, "bf16", "fp32", (5, 64, "runs")),
+    (2085, 40, 4096, 3, 32, True, "fp16", "fp32", None),
+    (4096, 32, 4096, 4, 64, False, "bf16", "bf16", None),
+    (1030, 33, 4064, 4, 32, False, "fp16", "fp32", (2, 16, "mixed")),
+]
+
+
+@pytest.mark.parametrize("n,r,c,bits,gs,act,dt,out,low", BACKWARD_SHAPES)
+def test_packed_linear_backward_shapes(n, r, c, bits, gs, act, dt, out, low):
+    test_packed_linear_backward(n, r, c, bits, gs, act, dt, out, low)
 
 
 ADD = [
