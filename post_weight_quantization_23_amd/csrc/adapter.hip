@@ -319,27 +319,41 @@ __global__ __launch_bounds__(256) void up_tiles_kernel(UpArgs u) {
   }
 }
 
-// A few tokens: a thread takes one output of one token, and its row of that
-// token's adapter (a tile of 32 tokens would take 32 adapters in turn).
-template <int DT, int YT>
+// A few tokens: SHARE threads take one output of one token, and its row of that
+// token's adapter (a tile of 32 tokens would take 32 adapters in turn).  Rows of
+// more than 16 ranks go to four threads, eight ranks each in turn, so that a load
+// touches 16 places instead of 64 (39 tokens, 11008 outputs of rank 88: 18 us,
+// 78 with one); one thread does for shorter ones (32 tokens, 4096 outputs of rank
+// 16: 2.9 us).
+template <int DT, int YT, int SHARE>
 __global__ __launch_bounds__(256) void up_kernel(UpArgs u) {
   const int64_t t = blockIdx.x / u.col_tiles, ct = blockIdx.x - t * u.col_tiles;
-  const int64_t j = ct * 256 + threadIdx.x;
-  if (j >= u.rows) return;
-  float v[8] = {};
+  const int part = threadIdx.x % SHARE, rank = u.ad.rank;
   const int a = adapter_of(u.ad, t, u.n);
-  if (a >= 0) v[0] = rank_dot<DT>(u.S + t * u.ad.rank, u.B + ((int64_t)a * u.rows + j) * u.ad.rank, u.ad.rank);
-  if (u.part) {
-    float w[8] = {};
-    join_parts(u, t, j & ~(int64_t)7, w);
-    float mine = w[0];
 #pragma unroll
-    for (int e = 1; e < 8; ++e) mine = (j & 7) == e ? w[e] : mine;
-    v[0] += mine;
-  } else {
-    add_base<YT>(u, v, t, j, 1);
+  for (int i = 0; i < SHARE; ++i) {
+    const int64_t j = ct * 256 + (256 * i + (int)threadIdx.x) / SHARE;
+    float v[8] = {};
+    if (a >= 0 && j < u.rows) {
+      const float* S = u.S + t * rank;
+      const uint16_t* row = u.B + ((int64_t)a * u.rows + j) * rank;
+      for (int p = 8 * part; p < rank; p += 8 * SHARE) v[0] += rank_dot<DT>(S + p, row + p, 8);
+    }
+#pragma unroll
+    for (int m = 1; m < SHARE; m <<= 1) v[0] += __shfl_xor(v[0], m);
+    if (part || j >= u.rows) continue;
+    if (u.part) {
+      float w[8] = {};
+      join_parts(u, t, j & ~(int64_t)7, w);
+      float mine = w[0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) mine = (j & 7) == e ? w[e] : mine;
+      v[0] += mine;
+    } else {
+      add_base<YT>(u, v, t, j, 1);
+    }
+    store_out<YT>(u.out, t * u.ldo + j, v[0]);
   }
-  store_out<YT>(u.out, t * u.ldo + j, v[0]);
 }
 
 // Parts joined without adapters: a thread takes eight outputs of one token.
@@ -783,7 +797,8 @@ void launch_adapter_up(const UpArgs& given, int xt, int yt, hipStream_t s) {
   const dim3 grid((unsigned)((few ? u.n : (u.n + 31) / 32) * u.col_tiles)), block(256);
 #define GPTQ_UP(D_, Y_)                                                                \
   do {                                                                                 \
-    if (few) hipLaunchKernelGGL((up_kernel<D_, Y_>), grid, block, 0, s, u);            \
+    if (few && u.ad.rank <= 16) hipLaunchKernelGGL((up_kernel<D_, Y_, 1>), grid, block, 0, s, u); \
+    else if (few) hipLaunchKernelGGL((up_kernel<D_, Y_, 4>), grid, block, 0, s, u);    \
     else if (plain) hipLaunchKernelGGL((up_tiles_kernel<D_, Y_, true>), grid, block, 0, s, u); \
     else hipLaunchKernelGGL((up_tiles_kernel<D_, Y_, false>), grid, block, 0, s, u);   \
   } while (0)
