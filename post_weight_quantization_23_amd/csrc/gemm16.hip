@@ -31,7 +31,7 @@ struct Places {
 // adapter after the other, the tile's rows of B come into the operands' LDS in
 // whole runs, 64 ranks at a time: operands loaded straight into registers would
 // touch 32 rows per instruction, at a place a cycle (2085 tokens of 4096 x 4096
-// with rank 64: 110 us, 116 so).  Sets of 32 places that one adapter has to itself take
+// with rank 64 on tiles of 96 x 128: 110 us, 116 so).  Sets of 32 places that one adapter has to itself take
 // its products onto their sums; the others follow by expand_shared, so that a
 // value that is not finite in one request stays there.
 template <int DT, int TERMS, int MT, int NT, int WM, int WN>
