@@ -178,7 +178,7 @@ GPTQ_DEV void gemm_body(const Gemm16& a, unsigned char* smem) {
     pl->tok[tid] = (int)t;
     pl->who[tid] = adapter_of(a.ad, t, a.n);
   }
-  load(first);
+  if (first < all) load(first);   // past the end there are no records to bound it
   for (int s = first; s < all; ++s) {
     // own loads have landed; with every wave here, the other buffer is free
     __builtin_amdgcn_s_waitcnt(0);
@@ -284,13 +284,17 @@ Shape choose_shape(int64_t n, int64_t cols, bool low) {
 }
 
 // Parts of the contraction, while the tiles are too few for the chip (128 x 128
-// then).
+// then).  Each takes ceil(steps / splits) steps, so the last of them could start past
+// the end (13 parts of 9 in 108 steps): as many as hold steps are left.
 int gemm16_splits(int64_t n, int64_t cols, int64_t steps) {
   if (n == 0 || cols == 0) return 1;
   const int64_t tiles = (n + 127) / 128 * ((cols + 127) / 128);
   int64_t splits = 384 / tiles;
   splits = splits < steps / 8 ? splits : steps / 8;
-  return splits < 3 ? 1 : (splits > 16 ? 16 : (int)splits);
+  if (splits < 3) return 1;
+  splits = splits < 16 ? splits : 16;
+  const int64_t each = (steps + splits - 1) / splits;
+  return (int)((steps + each - 1) / each);
 }
 
 template <int DT, int OT, int TERMS, int LOW>
