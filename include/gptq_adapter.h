@@ -43,6 +43,13 @@
  * A token's result never depends on other requests' tokens or adapters, not
  * even where those hold infinities or NaN.
  *
+ * Sizes: a launch holds fewer than 2^32 threads; a call one of whose launches
+ * would pass that is GPTQ_EUNSUPPORTED (also in its query, as far as the query is
+ * told of the adapters).  Activations and results of up to 2^31 elements, and
+ * factors A and B of up to 2^29, in fewer than 2^24 rows each always fit; only where
+ * adapters have few tokens each (n_tok <= 4 n_adapters) n_tok rank has to stay
+ * below 2^25 besides.
+ *
  * Types: activations and gradients are GPTQ_BF16 or GPTQ_F16; results are of
  * that type or GPTQ_F32, rounded once (round-to-nearest-even).
  */

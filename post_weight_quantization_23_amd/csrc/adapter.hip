@@ -717,8 +717,18 @@ int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank) {
 
 int adapter_down_parts(int64_t n, int m, int64_t d) { return by_token(n, m) ? 1 : down_splits(n, d); }
 
+bool adapter_down_fits(int64_t n, int m, int64_t rank, int problems) {
+  if (by_token(n, m)) return grid_fits((problems * n * rank + 3) / 4, 256);
+  return grid_fits(problems * ((n + 63) / 64) * 8, 256) && grid_fits((n * rank / 4 + 255) / 256, 256);
+}
+
 bool adapter_rows_direct(const void* X, int64_t n, int64_t d, int64_t ldx, int m) {
   return (reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0 && d % 8 == 0) || by_token(n, m);
+}
+
+bool prepare_adapters_fits(int64_t n, int64_t m, int64_t rank, int64_t r, int64_t c, int64_t padded) {
+  const int64_t tiles = m * ((rank + 63) / 64) * ((r + 63) / 64 + (c + 63) / 64);
+  return grid_fits(2 * m + 1 + (tiles + 2) / 2 + n * (padded / 8) / 1024 + 2, 1024);
 }
 
 void launch_prepare_adapters(const PrepareArgs& given, hipStream_t s) {
@@ -781,6 +791,12 @@ int launch_adapter_down(const DownArgs& given, int xt, bool join, hipStream_t s)
   return g.p[0].splits;
 }
 
+bool adapter_up_fits(int64_t n, int m, int64_t rows) {
+  return grid_fits((by_token(n, m) ? n : (n + 31) / 32) * ((rows + 255) / 256), 256);
+}
+
+bool join_rows_fits(int64_t n, int64_t rows) { return grid_fits((n * (part_width(rows) / 8) + 255) / 256, 256); }
+
 void launch_adapter_up(const UpArgs& given, int xt, int yt, hipStream_t s) {
   UpArgs u = given;
   u.col_tiles = (u.rows + 255) / 256;
@@ -814,6 +830,15 @@ int64_t adapter_grad_floats(int64_t n, int m, int64_t r, int64_t c, int rank) {
     if (splits > 1) floats += align64(splits * m * rank * cols);
   }
   return floats;
+}
+
+bool adapter_grads_fits(int64_t n, int m, int64_t r, int64_t c, int rank) {
+  const int64_t rank_blocks = (rank + grad_rows(rank) - 1) / grad_rows(rank);
+  int64_t items = 0;
+  for (const int64_t cols : {c, r}) items += (cols + 127) / 128 * rank_blocks * grad_splits(n, m, cols, rank) * m;
+  const int64_t places = list_places(n, m);
+  return places < INT32_MAX && grid_fits((2 * (places / 8) * rank + 255) / 256, 256) && grid_fits((items + 3) / 4, 256) &&
+         grid_fits(((r + c) * rank * m / 4 + 255) / 256, 256);
 }
 
 void launch_adapter_grads(const TermsArgs& terms, const GradArgs& given, int zt, float* gA, float* gB, float* part, hipStream_t s) {

@@ -420,6 +420,11 @@ GPTQ_DEV u32x4 pair_order(u32x4 v) {
 // ---------------------------------------------------------------- launches
 // xt / dt: 1 bf16, 2 fp16; yt: 0 fp32, 1 bf16, 2 fp16.
 
+// Whether the dispatcher takes a grid: its threads are counted in 32 bits.  Each
+// file's *_fits below says so of its launches at a call's sizes, for the host's
+// checks before any of them is enqueued.
+inline bool grid_fits(int64_t groups, int64_t threads) { return groups <= 0xFFFFFFFFll / threads; }
+
 // S[t][p] = alpha sum_k X[t][k] A_a[p][k]: X [n][ldx] (d columns), A [m][rank][lda]
 // on 16 bytes, lda a multiple of 8 and zero past d.  S: n x rank results in
 // adapter_down_floats() of workspace, in which the parts of a split contraction
@@ -443,6 +448,7 @@ struct DownArgs {
   int64_t blocks0; // set by the launch
 };
 int64_t adapter_down_floats(int64_t n, int64_t d, int64_t rank);
+bool adapter_down_fits(int64_t n, int m, int64_t rank, int problems);
 int launch_adapter_down(const DownArgs& g, int xt, bool join, hipStream_t s);
 // The parts that a launch leaves of a problem.
 int adapter_down_parts(int64_t n, int m, int64_t d);
@@ -481,6 +487,9 @@ struct PrepareArgs {
   PadArgs pad[2];
 };
 void launch_prepare_adapters(const PrepareArgs& g, hipStream_t s);
+// With everything that a call may lay out: A and B transposed (their rows r and c, or
+// 0), and rows of `padded` columns in all copied.
+bool prepare_adapters_fits(int64_t n, int64_t m, int64_t rank, int64_t r, int64_t c, int64_t padded);
 
 // out = base + S B^T, of type yt.  base: of the same type (null: 0), or the sum of
 // `splits` parts [n][ldp] fp32 times 2^ex[t] (ex null: 1), ldp = part_width(rows).
@@ -503,6 +512,8 @@ struct UpArgs {
   bool vec_base, vec_out;
 };
 void launch_adapter_up(const UpArgs& u, int xt, int yt, hipStream_t s);
+bool adapter_up_fits(int64_t n, int m, int64_t rows);
+bool join_rows_fits(int64_t n, int64_t rows);
 // gA[a][p][k] = sum over a's tokens of T[t][p] X[t][k] and gB[a][i][p] = ... S[t][p]
 // dY[t][i], from the rank values S[0] = T and S[1] = S in list order: terms[w] holds the
 // three bf16 terms of S[w][list[i]][p] (0 where list[i] is -1), rank rows and places in
@@ -532,6 +543,7 @@ struct GradArgs {
   GradProblem p[2];    // gA, gB
 };
 int64_t adapter_grad_floats(int64_t n, int m, int64_t r, int64_t c, int rank);
+bool adapter_grads_fits(int64_t n, int m, int64_t r, int64_t c, int rank);
 void launch_adapter_grads(const TermsArgs& terms, const GradArgs& g, int zt, float* gA, float* gB, float* part, hipStream_t s);
 
 // out = X W^T (+ S B^T): gemm16.hip.  The contraction has kp columns, a
@@ -558,6 +570,8 @@ struct Gemm16 {
 constexpr int gemm16_terms(int dt, int ot) { return ot != 0 ? 1 : (dt == kBF16 ? 3 : 2); }
 void launch_gemm16(const Gemm16& a, int dt, int ot, hipStream_t s);
 int64_t gemm16_part_floats(int64_t n, int64_t cols, int64_t kp, int dt, int ot);
+// With the copy of rows of kp columns that it may need.
+bool gemm16_fits(int64_t n, int64_t cols, int64_t kp);
 // Whether rows of d values can be its X as they are, and a copy (n x
 // gemm16_depth(d)) that can.
 bool gemm16_takes(const void* X, int64_t d, int64_t ldx);
@@ -568,10 +582,13 @@ void launch_packed_linear(const void* X, int xt, int64_t n, int64_t ldx, const P
                           const float* S, void* Y, int yt, int64_t ldy, hipStream_t s);
 // dst[t][j] = X[t][perm[j]] (entries outside 0 .. c-1 clamped), dst dense.
 void launch_gather_columns(const void* X, int64_t n, int64_t c, int64_t ldx, const int32_t* perm, void* dst, hipStream_t s);
+bool packed_rows_fits(int64_t n, int64_t r, int64_t c);
 // The same for many tokens: packed_tiles.hip.  ws: packed_tiles_bytes().
 bool packed_tiles(int64_t n, int64_t r, int64_t c);
 double packed_rows_us(int64_t n, int64_t r, int64_t c);   // launch_packed_linear's time, as its model has it
 int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt);
+bool packed_tiles_copies(int64_t n, int yt);   // whether through a dequantized copy
+bool packed_tiles_fits(int64_t n, int64_t r, int64_t c, int yt);
 void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad, const float* S,
                          void* Y, int yt, int64_t ldy, void* ws, hipStream_t s);
 // dX = dY W_hat (+ T A): packed_backward.hip.  At: A transposed to [m][c][rank];
@@ -580,5 +597,6 @@ void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const Pa
 void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, const PackedLayer& w, const Adapters& ad,
                             const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, uint16_t* Wt, uint16_t* rows,
                             float* part, hipStream_t s);
+bool packed_backward_fits(int64_t n, int64_t r, int64_t c);
 
 }  // namespace gptq

@@ -185,21 +185,29 @@ gptq::DownProblem down_problem(const void* X, int64_t n, int64_t d, int64_t ldx,
   return q;
 }
 
-// Every launch's grid, at the launch helpers' workgroup shapes.
-bool grids_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
-  return n <= kMaxGroups256 &&                                                           // prepared activations: a workgroup each
-         groups_for(2 * n * (rank > 0 ? rank : 1), 4) <= kMaxGroups256 &&                // down: a wave per value, both sides
-         groups_for(n, 16) * groups_for(r, 16) <= kMaxGroups256 / 2 &&                   // forward: 512 threads per 16 rows
-         groups_for(n, 16) * groups_for(r > c ? r : c, 256) <= kMaxGroups256 &&          // up
-         groups_for(n, 32) * groups_for(r > c ? r : c, 128) <= kMaxGroups256 / 16 &&     // tiles, in up to 16 parts
-         groups_for(r, 64) * groups_for(c, 256) <= kMaxGroups256 &&                      // dequantized copy
-         groups_for(n * (r / 8 + 8), 256) <= kMaxGroups256 &&                            // padded rows
-         groups_for(n * (c / 8), 256) <= kMaxGroups256 &&                                // gather
-         n * groups_for(r > c ? r : c, 256) <= kMaxGroups256 * (n > 64 && n > 4 * m ? 32 : 1) &&   // up
-         groups_for(2 * (gptq::list_places(n, m) / 8) * (rank > 0 ? rank : 1), 256) <= kMaxGroups256 && gptq::list_places(n, m) < INT_MAX &&  // lists
-         m * groups_for(r > c ? r : c, 64) * 5 + groups_for(n * (r + c) / 8 + 16, 1024) <= kMaxGroups256 / 4 &&   // preparation (1024 threads)
-         m * (groups_for(r, 128) + groups_for(c, 128)) * 16 <= kMaxGroups256 &&          // gradients (16 splits of 4 rank blocks, 4 a group)
-         groups_for(m * rank * (r > c ? r : c), 1024) <= kMaxGroups256;                  // join
+// Whether every launch that a call makes at these sizes is one that the
+// dispatcher takes.  up: outputs that a launch of its own adds the adapters to (0: the
+// product does).
+bool low_fits(int64_t n, int64_t d, int64_t rank, int64_t m, int64_t up, int64_t turned_r, int64_t turned_c) {
+  if (rank == 0) return true;
+  return gptq::prepare_adapters_fits(n, m, rank, turned_r, turned_c, gptq::gemm16_depth(d)) &&
+         gptq::adapter_down_fits(n, (int)m, rank, 1) && gptq::adapter_up_fits(n, (int)m, up);
+}
+
+bool forward_fits(int64_t n, int64_t r, int64_t c, int yt, int64_t rank, int64_t m) {
+  const bool tiles = gptq::packed_tiles(n, r, c);
+  if (!(tiles ? gptq::packed_tiles_fits(n, r, c, yt) : gptq::packed_rows_fits(n, r, c))) return false;
+  return low_fits(n, c, rank, m, tiles && !gptq::packed_tiles_copies(n, yt) ? r : 0, 0, 0);
+}
+
+bool backward_fits(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
+  return gptq::packed_backward_fits(n, r, c) && low_fits(n, r, rank, m, 0, pad8(r), c);
+}
+
+bool grads_fit(int64_t n, int64_t r, int64_t c, int64_t rank, int64_t m) {
+  return gptq::prepare_adapters_fits(n, m, rank, pad8(r), c, gptq::gemm16_depth(r) + gptq::gemm16_depth(c)) &&
+         gptq::adapter_down_fits(n, (int)m, rank, 2) && gptq::adapter_up_fits(n, (int)m, c) &&
+         gptq::adapter_grads_fits(n, (int)m, r, c, (int)rank);
 }
 
 // The input gradient's dequantized weights and padded rows of dY.
@@ -237,7 +245,7 @@ gptq_status gptq_packed_linear_workspace_size(int64_t n, int64_t r, int64_t c, g
   if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
   if (rank != 0)
     if (gptq_status st = check_rank(fn, 1, rank)) return st;
-  if (!grids_fit(n, r, c, rank, rank != 0)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (!forward_fits(n, r, c, (int)yt, rank, rank != 0)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   *bytes = (size_t)(forward_bytes(n, r, c, has_perm != 0, (int)yt) + low_bytes(n, c, rank) + order_bytes(n, rank) + rows_bytes(n, c, rank));
   return ok();
 }
@@ -256,7 +264,7 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
   if (yt != GPTQ_F32 && yt != xt) return fail(GPTQ_EDTYPE, fn, "Y must be GPTQ_F32 or of X's type");
   if (low)
     if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
-  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (!forward_fits(n, r, c, (int)yt, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (n == 0 || r == 0) return ok();
   if (gptq_status st = check_packed(fn, packed, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm)) return st;
   if (ldx < c || ldy < r) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
@@ -313,7 +321,7 @@ gptq_status gptq_packed_linear_backward_workspace_size(int64_t n, int64_t r, int
   if (gptq_status st = check_sizes(fn, n, r, c, 32)) return st;
   if (m != 0 || rank != 0)
     if (gptq_status st = check_rank(fn, m, rank)) return st;
-  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (!backward_fits(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
   *bytes = (size_t)(backward_bytes(n, r, c, (int)xt, (int)ot) + align256(m * c * rank * 2) +
                     align256(m * rank * pad8(r) * 2) + low_bytes(n, r, rank) + order_bytes(n, rank) + rows_bytes(n, r, rank));
@@ -335,7 +343,7 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
   if (ot != GPTQ_F32 && ot != xt) return fail(GPTQ_EDTYPE, fn, "dX must be GPTQ_F32 or of dY's type");
   if (low)
     if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
-  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (!backward_fits(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (r == 0) return fail(GPTQ_ESHAPE, fn, "r must be positive");
   if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
   if (n == 0) return ok();
@@ -402,7 +410,7 @@ gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n, int64_t c,
   if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "X must be GPTQ_BF16 or GPTQ_F16");
   if (yt != GPTQ_F32 && yt != xt) return fail(GPTQ_EDTYPE, fn, "Y must be GPTQ_F32 or of X's type");
   if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
-  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (!low_fits(n, c, rank, m, r, 0, 0)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (n == 0 || r == 0) return ok();
   if (ldx < c || ldy < r || ldo < r) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
   if (!X || !Y || !out) return fail(GPTQ_EINVAL, fn, "a required pointer is NULL");
@@ -441,7 +449,7 @@ gptq_status gptq_adapter_backward_workspace_size(int64_t n, int64_t r, int64_t c
   if (!bytes) return fail(GPTQ_EINVAL, fn, "bytes is NULL");
   if (gptq_status st = check_sizes(fn, n, r, c, 8)) return st;
   if (gptq_status st = check_rank(fn, m, rank)) return st;
-  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (!grads_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   *bytes = (size_t)grad_sizes(n, r, c, m, rank).total;
   return ok();
 }
@@ -457,7 +465,7 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   if (ot != GPTQ_F32 && ot != xt) return fail(GPTQ_EDTYPE, fn, "dX must be GPTQ_F32 or of X's type");
   if (r == 0) return fail(GPTQ_ESHAPE, fn, "r must be positive");
   if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
-  if (!grids_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
+  if (!grads_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (ldy < r || ldx < c || (dX && ldd < c)) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
   if (!gA || !gB) return fail(GPTQ_EINVAL, fn, "gA or gB is NULL");
   if (n > 0 && (!dY || !X)) return fail(GPTQ_EINVAL, fn, "dY or X is NULL");

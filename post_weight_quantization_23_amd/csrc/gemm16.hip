@@ -367,6 +367,11 @@ int64_t gemm16_part_floats(int64_t n, int64_t cols, int64_t kp, int dt, int ot) 
   return splits > 1 ? splits * n * part_width(cols) : 0;
 }
 
+// In tiles of 64 x 128 at the smallest; parts are for fewer tiles than the chip takes at once.
+bool gemm16_fits(int64_t n, int64_t cols, int64_t kp) {
+  return grid_fits((n + 63) / 64 * ((cols + 127) / 128), 256) && grid_fits((n * (kp / 8) + 255) / 256, 256);
+}
+
 bool gemm16_takes(const void* X, int64_t d, int64_t ldx) {
   return reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0 && ldx < (int64_t(1) << 22) && d % LK == 0;
 }

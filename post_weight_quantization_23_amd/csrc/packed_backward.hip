@@ -69,6 +69,11 @@ __global__ __launch_bounds__(256) void dequant_t_kernel(PackedLayer w, uint16_t*
 
 }  // namespace
 
+bool packed_backward_fits(int64_t n, int64_t r, int64_t c) {
+  const int64_t kp = gemm16_depth(r);
+  return grid_fits(kp / 64 * ((c + 255) / 256), 256) && gemm16_fits(n, c, kp);
+}
+
 void launch_packed_backward(const void* dY, int xt, int64_t n, int64_t ldy, const PackedLayer& w, const Adapters& ad,
                             const uint16_t* At, const float* T, void* dX, int ot, int64_t ldx, uint16_t* Wt, uint16_t* rows,
                             float* part, hipStream_t s) {

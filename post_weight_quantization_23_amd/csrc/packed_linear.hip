@@ -347,6 +347,12 @@ void launch_forward(const FwdArgs& a, hipStream_t s) {
 
 }  // namespace
 
+bool packed_rows_fits(int64_t n, int64_t r, int64_t c) {
+  const RowsShape p = rows_shape(n, r);
+  return grid_fits((n + 16 * p.tg - 1) / (16 * p.tg) * ((r + 16 * p.nt - 1) / (16 * p.nt)), 64 * WAVES) &&
+         grid_fits((n * (c / 8) + 255) / 256, 256);
+}
+
 double packed_rows_us(int64_t n, int64_t r, int64_t c) { return 2 + rows_shape(n, r).turns * (double)c / 4096; }
 
 void launch_gather_columns(const void* X, int64_t n, int64_t c, int64_t ldx, const int32_t* perm, void* dst, hipStream_t s) {

@@ -26,7 +26,7 @@ typedef __attribute__((address_space(3))) unsigned char lds_u8;
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 
 constexpr int STEP = 128, ROWB = STEP * 2;   // columns of a step, bytes of an LDS row
-constexpr int64_t kCopyTokens = 1024;         // see dequant_first
+constexpr int64_t kCopyTokens = 1024;         // see packed_tiles_copies
 
 struct TileArgs {
   const uint16_t* X;   // prepared activations [n][ldx]
@@ -359,15 +359,15 @@ TilePlan plan_tiles(int64_t n, int64_t r, int64_t c, int chunks) {
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 int64_t tiles_width(int64_t c) { return (c + STEP - 1) / STEP * STEP; }
 
+}  // namespace
+
 // 16-bit results of many tokens: the layer is dequantized once into 16-bit rows
 // (each weight rounded to the activations' type, as gptq_linear_forward does)
 // and multiplied by gemm16.  Its product runs at 1.25 PFLOP/s where the tiles
 // here, which also multiply scales and dequantize for every 128 tokens, reach
 // 0.83, and the copy costs 34 us for 45 million weights: 0.66 against 0.89 ms for
 // 8192 tokens of 11008 x 4096.  Below, the weights stay unrounded.
-bool dequant_first(int64_t n, int yt) { return yt != 0 && n >= kCopyTokens; }
-
-}  // namespace
+bool packed_tiles_copies(int64_t n, int yt) { return yt != 0 && n >= kCopyTokens; }
 
 // Below the tokens of a copy, the kernel for few tokens as long as the models of both
 // say so; tiles take three launches, with what these leave between them in memory
@@ -379,7 +379,7 @@ bool packed_tiles(int64_t n, int64_t r, int64_t c) {
 }
 
 int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt) {
-  if (dequant_first(n, yt))
+  if (packed_tiles_copies(n, yt))
     return align256(n * gemm16_depth(c) * 2) + align256(r * gemm16_depth(c) * 2) + 4 * gemm16_part_floats(n, r, gemm16_depth(c), yt, yt);
   int64_t splits = yt == 0 ? 0 : 1;   // one part of fp32 results is the results
   for (const int chunks : {4, 2, 1}) {
@@ -389,11 +389,24 @@ int64_t packed_tiles_bytes(int64_t n, int64_t r, int64_t c, int yt) {
   return align256(n * tiles_width(c) * 2) + align256(n * 4) + align256(splits * n * part_width(r) * 4);
 }
 
+bool packed_tiles_fits(int64_t n, int64_t r, int64_t c, int yt) {
+  if (packed_tiles_copies(n, yt)) return grid_fits((r + 3) / 4, 256) && gemm16_fits(n, r, gemm16_depth(c));
+  const int64_t row_tiles = (r + 127) / 128;
+  // a workgroup for each token to prepare; the largest tiles, as a bound that plan_tiles needs
+  if (!grid_fits(n, 256) || !grid_fits((n + 127) / 128 * row_tiles, 256)) return false;
+  for (const int chunks : {4, 2, 1}) {
+    const TilePlan p = plan_tiles(n, r, c, chunks);
+    if (!grid_fits((n + 32 * p.mt - 1) / (32 * p.mt) * row_tiles * p.splits, 256)) return false;
+    if ((yt != 0 || p.splits > 1) && !join_rows_fits(n, r)) return false;
+  }
+  return true;
+}
+
 void launch_packed_tiles(const void* X, int xt, int64_t n, int64_t ldx, const PackedLayer& w, const Adapters& ad, const float* S,
                          void* Y, int yt, int64_t ldy, void* ws, hipStream_t s) {
   auto* xp = static_cast<uint16_t*>(ws);
   const dim3 block(256);
-  if (dequant_first(n, yt)) {
+  if (packed_tiles_copies(n, yt)) {
     Gemm16 g{};
     g.kp = gemm16_depth(w.c);
     g.X = static_cast<const uint16_t*>(X);
