@@ -50,6 +50,9 @@
  * adapters have few tokens each (n_tok <= 4 n_adapters) n_tok rank has to stay
  * below 2^25 besides.
  *
+ * n_tok = 0, or r = 0 in the two forward calls, is nothing to do (pointers to what
+ * has no elements may be NULL); gptq_adapter_backward still writes zeros.
+ *
  * Types: activations and gradients are GPTQ_BF16 or GPTQ_F16; results are of
  * that type or GPTQ_F32, rounded once (round-to-nearest-even).
  */

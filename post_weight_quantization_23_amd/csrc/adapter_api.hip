@@ -54,9 +54,7 @@ gptq_status check_rank(const char* fn, int64_t m, int64_t rank) {
   return GPTQ_OK;
 }
 
-gptq_status check_adapters(const char* fn, const void* A, const void* B, int64_t m, int64_t rank, const int32_t* index,
-                           const float* alpha) {
-  if (gptq_status st = check_rank(fn, m, rank)) return st;
+gptq_status check_adapters(const char* fn, const void* A, const void* B, const int32_t* index, const float* alpha) {
   if (!A || !B) return fail(GPTQ_EINVAL, fn, "A or B is NULL");
   if (!aligned(A, 16) || !aligned(B, 16)) return fail(GPTQ_EALIGN, fn, "A and B must be 16-byte aligned");
   if (!aligned(index, 4) || !aligned(alpha, 4)) return fail(GPTQ_EALIGN, fn, "misaligned index or alpha");
@@ -263,9 +261,11 @@ gptq_status gptq_packed_linear(const void* X, gptq_dtype xt, int64_t n, int64_t 
   if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "X must be GPTQ_BF16 or GPTQ_F16");
   if (yt != GPTQ_F32 && yt != xt) return fail(GPTQ_EDTYPE, fn, "Y must be GPTQ_F32 or of X's type");
   if (low)
-    if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
+    if (gptq_status st = check_rank(fn, m, rank)) return st;
   if (!forward_fits(n, r, c, (int)yt, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (n == 0 || r == 0) return ok();
+  if (low)
+    if (gptq_status st = check_adapters(fn, A, B, index, alpha)) return st;
   if (gptq_status st = check_packed(fn, packed, c, bits, ld_words, scales, zeros, ld_groups, groupsize, perm)) return st;
   if (ldx < c || ldy < r) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
   if (!X || !Y) return fail(GPTQ_EINVAL, fn, "a required pointer is NULL");
@@ -341,8 +341,10 @@ gptq_status gptq_packed_linear_backward(const void* dY, gptq_dtype xt, int64_t n
   if (!valid_dtype(xt) || !valid_dtype(ot)) return fail(GPTQ_EINVAL, fn, "xt and ot must be gptq_dtype values");
   if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "dY must be GPTQ_BF16 or GPTQ_F16");
   if (ot != GPTQ_F32 && ot != xt) return fail(GPTQ_EDTYPE, fn, "dX must be GPTQ_F32 or of dY's type");
-  if (low)
-    if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
+  if (low) {
+    if (gptq_status st = check_rank(fn, m, rank)) return st;
+    if (gptq_status st = check_adapters(fn, A, B, index, alpha)) return st;
+  }
   if (!backward_fits(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (r == 0) return fail(GPTQ_ESHAPE, fn, "r must be positive");
   if (r > kMaxDepth) return fail(GPTQ_EUNSUPPORTED, fn, "r too large");
@@ -409,9 +411,10 @@ gptq_status gptq_adapter_add(const void* X, gptq_dtype xt, int64_t n, int64_t c,
   if (!valid_dtype(xt) || !valid_dtype(yt)) return fail(GPTQ_EINVAL, fn, "xt and yt must be gptq_dtype values");
   if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "X must be GPTQ_BF16 or GPTQ_F16");
   if (yt != GPTQ_F32 && yt != xt) return fail(GPTQ_EDTYPE, fn, "Y must be GPTQ_F32 or of X's type");
-  if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
+  if (gptq_status st = check_rank(fn, m, rank)) return st;
   if (!low_fits(n, c, rank, m, r, 0, 0)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (n == 0 || r == 0) return ok();
+  if (gptq_status st = check_adapters(fn, A, B, index, alpha)) return st;
   if (ldx < c || ldy < r || ldo < r) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
   if (!X || !Y || !out) return fail(GPTQ_EINVAL, fn, "a required pointer is NULL");
   const int64_t el = (int64_t)elem_size(yt);
@@ -464,7 +467,8 @@ gptq_status gptq_adapter_backward(const void* dY, int64_t ldy, const void* X, in
   if (xt == GPTQ_F32) return fail(GPTQ_EDTYPE, fn, "dY and X must be GPTQ_BF16 or GPTQ_F16");
   if (ot != GPTQ_F32 && ot != xt) return fail(GPTQ_EDTYPE, fn, "dX must be GPTQ_F32 or of X's type");
   if (r == 0) return fail(GPTQ_ESHAPE, fn, "r must be positive");
-  if (gptq_status st = check_adapters(fn, A, B, m, rank, index, alpha)) return st;
+  if (gptq_status st = check_rank(fn, m, rank)) return st;
+  if (gptq_status st = check_adapters(fn, A, B, index, alpha)) return st;
   if (!grads_fit(n, r, c, rank, m)) return fail(GPTQ_EUNSUPPORTED, fn, "size too large");
   if (ldy < r || ldx < c || (dX && ldd < c)) return fail(GPTQ_ESHAPE, fn, "leading dimension too small");
   if (!gA || !gB) return fail(GPTQ_EINVAL, fn, "gA or gB is NULL");

@@ -84,3 +84,13 @@ def test_launches_past_the_limit_are_refused(lib):
     # the dequantized copy, 64 x 256 weights a workgroup, and tiles of the product
     assert backward(lib, 1 << 12, 1 << 21, 1 << 21) == 5 and backward(lib, 1 << 12, 1 << 20, 1 << 16) == 6
     assert backward(lib, 1 << 29, 1 << 20, 1 << 14) == 5
+
+
+def test_a_layer_without_rows_beside_adapters(lib):
+    """Nothing to do: B has no values then, so its address may be NULL (an empty tensor's is); sizes are still checked."""
+    for n in (0, 4, 2000):
+        for m, rank, want in ((2, 8, 0), (0, 8, 1), (2, 12, 5)):
+            assert lib.gptq_packed_linear(P(0), BF16, n, 64, None, 0, 64, 4, 8, None, None, 2, 32, None, P(4), None, m, rank, None,
+                                          None, None, BF16, 0, None, 0, None) == want
+            assert lib.gptq_adapter_add(P(0), BF16, n, 64, 64, P(1), None, m, rank, 0, None, None, None, BF16, 0, None, 0, None, 0,
+                                        None) == want
