@@ -50,7 +50,7 @@ __global__ __launch_bounds__(256) void dequant_t_kernel(PackedLayer w, uint16_t*
     const int64_t col = w.perm ? min(max(w.perm[j], 0), w.c - 1) : j;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = ((float)((blk[e] >> (BITS * k)) & ((1u << BITS) - 1)) - ze[e]) * sc[e];
+    for (int e = 0; e < 8; ++e) v[e] = weight32<DT>((blk[e] >> (BITS * k)) & ((1u << BITS) - 1), ze[e], sc[e]);
 #pragma unroll
     for (int t = 0; t < TERMS; ++t) {
       u32x4 o;

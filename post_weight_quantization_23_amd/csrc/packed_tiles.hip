@@ -321,8 +321,8 @@ __global__ __launch_bounds__(256) void dequant_rows_kernel(PackedLayer w, uint16
       const uint32_t blk = BITS == 4 ? words[b] : straddling_block(words, b);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float w0 = ((float)((blk >> (2 * BITS * e)) & ((1u << BITS) - 1)) - z) * sc;
-        const float w1 = ((float)((blk >> (2 * BITS * e + BITS)) & ((1u << BITS) - 1)) - z) * sc;
+        const float w0 = weight32<DT>((blk >> (2 * BITS * e)) & ((1u << BITS) - 1), z, sc);
+        const float w1 = weight32<DT>((blk >> (2 * BITS * e + BITS)) & ((1u << BITS) - 1), z, sc);
         o[e] = pack2<DT>(w0, w1);
       }
     }
