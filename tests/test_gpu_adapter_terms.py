@@ -216,3 +216,48 @@ def test_gradients_hold_every_term(n, r, c, dt, m, rank, kind):
     lost = 2 * EPS + 2.0 ** -26 + (2.0 ** -25 if dt == torch.float16 else 0) + 12 * EPS
     near("gA", got["A"], gA, lost * gA.abs())
     near("gB", got["B"], gB, lost * gB.abs())
+
+
+@pytest.mark.parametrize("n,r,c,bits,gs,dt", [(1, 40, 416, 4, 32, "bf16"), (40, 70, 416, 3, 96, "fp16"), (300, 130, 1024, 4, 64, "bf16"),
+                                              (1100, 130, 1024, 3, 128, "fp16"), (1100, 130, 1024, 4, 32, "bf16")])
+def test_zeros_far_from_the_codes(n, r, c, bits, gs, dt):
+    """Zeros of -1000 .. 1000: code less zero has 10 bits, its product with an entry 21, still exact."""
+    L = Layer(r, c, bits, gs, n + r, False)
+    g = torch.Generator().manual_seed(n)
+    zeros = torch.randint(-1000, 1001, L.zeros.shape, generator=g, dtype=torch.int32).cuda()
+    zeros[:2], zeros[2:4] = -1000, 1000
+    of = torch.arange(c, device="cuda") // gs
+    L.W = L.W + L.scales.double()[:, of] * (L.zeros - zeros).double()[:, of]       # s (q - z): 35 bits, exact in float64
+    L.zeros = zeros
+    X, at = single(n, c, DT[dt], n + c)
+    dY, aty = single(n, r, DT[dt], n + r)
+    for out in (DT[dt], torch.float32):
+        W = L.W.float().to(DT[dt]).double() if out != torch.float32 and n >= 1024 else L.W
+        same(f"Y {out}", gq().packed_linear(X, *L.args(), out_dtype=out), (W.T[at] * entry(X, at)).float().to(out))
+    W = L.W.float().to(DT[dt]).double()
+    same("dX", gq().packed_linear_backward(dY, *L.args()), (W[aty] * entry(dY, aty)).float().to(DT[dt]))
+
+
+def test_the_longest_contractions():
+    """Columns past the tiles' 2^22 - 128 (the few-token kernel takes any number of tokens then), and 2^22 - 64 rows."""
+    L = Layer(17, 1 << 22, 4, 128, 5, False)
+    X, at = single(65, 1 << 22, torch.bfloat16, 3)
+    at[::3] = (1 << 22) - 1 - torch.arange(22, device="cuda")
+    X = torch.zeros_like(X).scatter_(1, at.unsqueeze(1), normal((65, 1), 4).bfloat16())
+    for out in (torch.bfloat16, torch.float32):
+        same(f"Y {out}", gq().packed_linear(X, *L.args(), out_dtype=out), (L.W.T[at] * entry(X, at)).float().to(out))
+    dY, aty = single(65, 17, torch.bfloat16, 6)
+    W = L.W.float().bfloat16().double()
+    same("dX", gq().packed_linear_backward(dY, *L.args()), (W[aty] * entry(dY, aty)).float().bfloat16())
+    del L, X, W
+    r = (1 << 22) - 64
+    L = Layer(r, 32, 4, -1, 7, False)
+    dY, aty = single(130, r, torch.bfloat16, 8)
+    aty[::2] = r - 1 - torch.arange(65, device="cuda")
+    dY = torch.zeros_like(dY).scatter_(1, aty.unsqueeze(1), normal((130, 1), 9).bfloat16())
+    W, d = L.W.float().bfloat16().double(), entry(dY, aty)
+    same("dX", gq().packed_linear_backward(dY, *L.args()), (W[aty] * d).float().bfloat16())
+    near("dX fp32", gq().packed_linear_backward(dY, *L.args(), out_dtype=torch.float32), L.W[aty] * d,
+         (EPS + 2.0 ** -26 + 6 * EPS) * (L.W[aty] * d).abs())
+    X, at = single(40, 32, torch.bfloat16, 10)
+    same("Y", gq().packed_linear(X, *L.args()), (L.W.T[at] * entry(X, at)).float().bfloat16())
