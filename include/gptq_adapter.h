@@ -41,7 +41,9 @@
  *           outside 0 .. n_adapters-1 means none.  NULL: adapter 0 for all.
  * alpha   : fp32[n_adapters], the factor of each adapter.  NULL: 1.
  * A token's result never depends on other requests' tokens or adapters, not
- * even where those hold infinities or NaN.
+ * even where those hold infinities or NaN.  A request's own infinities and NaN, in
+ * its tokens, factors or alpha, give infinities or NaN in the results that they enter
+ * (an infinity may come out as NaN: fp32 values go into the matrix cores in terms).
  *
  * Sizes: a launch holds fewer than 2^32 threads; a call one of whose launches
  * would pass that is GPTQ_EUNSUPPORTED (also in its query, as far as the query is
@@ -70,7 +72,7 @@ extern "C" {
  * src(j) = col_perm[j], or j.  Up to 1023 tokens, and for fp32 results of any
  * number, codes are multiplied as whole numbers and the rulers applied to each
  * group's fp32 sum, so the weights are not rounded: the fp32 result is within
- * about 2^-16 sum_j scale (2 * 2^bits + q + zero) |x_j| of the exact product (a
+ * about 2^-16 sum_j scale (2 * 2^bits + q + |zero|) |x_j| of the exact product (a
  * bound; usual errors are far smaller).  16-bit results of more tokens take
  * weights rounded once to X's type, as gptq_linear_forward does.  |X| must stay
  * below 2^115 (larger bf16 values can overflow a group's sum); a token that

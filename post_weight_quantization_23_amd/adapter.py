@@ -132,7 +132,9 @@ def packed_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, z
     alpha_a B_a (A_a x) for each token's adapter a when A and B are given.
 
     X [n, c] bf16 / fp16; packed, scales, zeros, perm as for dequant_gemv; the
-    result [n, r] is of X's type or float32."""
+    result [n, r] is of X's type or float32 (out_dtype).  Weights are not rounded,
+    except for 16-bit results of 1024 tokens or more, which take them rounded to X's
+    type as linear_forward does; float32 results never do."""
     _rows16(X, "X")
     n, c = X.shape
     r = _layer(packed, scales, zeros, bits, c, perm)
@@ -157,8 +159,10 @@ def packed_linear_backward(dY: torch.Tensor, packed: torch.Tensor, scales: torch
     """dX = dY W_hat, plus alpha_a (dY B_a) A_a for each token's adapter: the
     gradient of packed_linear for its input.
 
-    dY [n, r] bf16 / fp16; the result [n, c] is of dY's type or float32.  c is
-    `cols`, or what the packed words hold.  perm must be a permutation."""
+    dY [n, r] bf16 / fp16; the result [n, c] is of dY's type, with weights rounded to
+    it, or float32 (out_dtype), with weights held in as many 16-bit terms as float32
+    has bits.  c is `cols`, or what the packed words hold.  perm must be a
+    permutation."""
     _rows16(dY, "dY")
     _need(packed, "packed", torch.uint32, 2, on_gpu=False)
     n = dY.shape[0]

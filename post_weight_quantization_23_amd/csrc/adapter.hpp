@@ -163,7 +163,8 @@ struct Terms16 {
 };
 
 // c + V Z of an fp32 operand in TERMS terms and a 16-bit one, smallest products
-// first; those below the first term left out of V are left out.
+// first.  The product of both last terms is left out: 2^-16 of two terms (16-bit
+// results), 2^-25 of three, with fp16 Z; with bf16 Z, which is one term, nothing is.
 template <int DT, int TERMS>
 GPTQ_DEV floatx4 mfma_terms(const u32x4 (&v)[TERMS], const Terms16<DT>& z, floatx4 c) {
   if constexpr (TERMS == 3) {

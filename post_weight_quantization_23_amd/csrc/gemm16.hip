@@ -109,9 +109,9 @@ GPTQ_DEV void expand_staged(const Gemm16& a, const Places<32 * MT * WM>* pl, uns
 
 // WM x WN waves of 32 MT tokens x 32 NT columns.  Both operands come from
 // memory straight into LDS (double buffered, one barrier per step), each lane
-// fetching the chunk that belongs at its place; tokens past the end repeat the
-// last one, columns past the end lie outside the descriptor's records and read
-// as zero.  LOW: adapters beside the product (1), tokens by adapter too (2: ad.order;
+// fetching the chunk that belongs at its place; tokens and columns past the end
+// lie outside the descriptors' records and read as zero, except that tokens by
+// adapter, which are fetched by address, repeat the last one.  LOW: adapters beside the product (1), tokens by adapter too (2: ad.order;
 // without either a 256 x 256 tile keeps all its registers).  PARTS: the workgroup takes one of
 // `splits` parts of the contraction and writes its fp32 sums to part.
 template <int DT, int OT, int TERMS, int LOW, bool PARTS, int MT, int NT, int WM, int WN>

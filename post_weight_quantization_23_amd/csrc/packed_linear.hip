@@ -7,8 +7,9 @@
 // exactly, one shift and one and-or for two codes.  With P = sum (2^b + q) x and
 // X_g = sum x over a group (a product with ones, on the matrix cores too), the
 // group's part is s (P - (2^b + z) X_g): the weights are never rounded, and
-// every sum is fp32.  The subtraction costs a factor below 8 in the error of
-// the fp32 sums, three bits of 24.
+// every sum is fp32.  While zeros lie among the codes (0 .. 2^b - 1), the subtraction
+// costs a factor below 8 in the error of the fp32 sums, three bits of 24; zeros
+// far from them, up to 1000, cost as much more as they are larger.
 #include <type_traits>
 
 #include "adapter.hpp"

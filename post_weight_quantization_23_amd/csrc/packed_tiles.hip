@@ -3,8 +3,9 @@
 //
 // Codes become fp16 values q - z exactly, in about nine operations for eight
 // codes (centered).  Activations become fp16 once per call (prepare_tokens): bf16
-// ones are scaled by a power of two per token, which keeps every value within
-// 2^-29 of the token's largest exactly and the others to 2^-40 of it.  A
+// ones are scaled by a power of two per token, its largest value to 2^14 .. 2^15,
+// which keeps every value within 2^-31 of the largest exactly and the others to
+// 2^-39 of it (half of fp16's smallest step, 2^-25).  A
 // group's products are then whole-number weights times activations with fp32
 // sums, and its scale multiplies the sum: the weights are never rounded.
 //
@@ -365,8 +366,13 @@ int64_t tiles_width(int64_t c) { return (c + STEP - 1) / STEP * STEP; }
 // (each weight rounded to the activations' type, as gptq_linear_forward does)
 // and multiplied by gemm16.  Its product runs at 1.25 PFLOP/s where the tiles
 // here, which also multiply scales and dequantize for every 128 tokens, reach
-// 0.83, and the copy costs 34 us for 45 million weights: 0.66 against 0.89 ms for
-// 8192 tokens of 11008 x 4096.  Below, the weights stay unrounded.
+// 0.83, and the copy costs 34 us for 45 million weights: 655 against 950 us for
+// 8192 tokens of 11008 x 4096 in groups of 128 (of 32: 654 and 1271), 109 and 139
+// for 1024.  The two meet at some 600 tokens (4096 x 4096: 512 tokens 44 and 42,
+// 768 54 and 57, 1024 57 and 69) and later in layers of few rows (1024 x 4096: 1024
+// tokens 35 and 31, 1536 35 and 39).  From 1024 tokens on the speed is taken for
+// the rounding; below, and for fp32 results of any number, the weights stay
+// unrounded.
 bool packed_tiles_copies(int64_t n, int yt) { return yt != 0 && n >= kCopyTokens; }
 
 // Below the tokens of a copy, the kernel for few tokens as long as the models of both
