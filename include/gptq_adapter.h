@@ -47,10 +47,10 @@
  *
  * Sizes: a launch holds fewer than 2^32 threads; a call one of whose launches
  * would pass that is GPTQ_EUNSUPPORTED (also in its query, as far as the query is
- * told of the adapters).  Activations and results of up to 2^31 elements, and
- * factors A and B of up to 2^29, in fewer than 2^24 rows each always fit; only where
- * adapters have few tokens each (n_tok <= 4 n_adapters) n_tok rank has to stay
- * below 2^25 besides.
+ * told of the adapters).  Fewer than 2^24 tokens and rows of the layer, activations
+ * and results of up to 2^31 elements, layers of up to 2^37 and factors A and B of up
+ * to 2^29 always fit; only where adapters have few tokens each (n_tok <= 4
+ * n_adapters) n_tok rank has to stay below 2^25 besides.
  *
  * n_tok = 0, or r = 0 in the two forward calls, is nothing to do (pointers to what
  * has no elements may be NULL); gptq_adapter_backward still writes zeros.

@@ -3,6 +3,7 @@ refused for a launch that it makes, and for no other.  Nothing here reaches the
 device: a size that passes goes on to ask for its workspace (status 6)."""
 import ctypes as C
 import os
+import random
 
 import pytest
 
@@ -94,3 +95,20 @@ def test_a_layer_without_rows_beside_adapters(lib):
                                           None, None, BF16, 0, None, 0, None) == want
             assert lib.gptq_adapter_add(P(0), BF16, n, 64, 64, P(1), None, m, rank, 0, None, None, None, BF16, 0, None, 0, None, 0,
                                         None) == want
+
+
+def test_what_the_header_says_always_fits(lib):
+    rng, seen = random.Random(3), 0
+
+    def log2(bits):
+        return min(int(2 ** rng.uniform(0, bits)), 2 ** bits - 1)
+
+    while seen < 5000:
+        n, r, c, m, rank = log2(24), log2(24), max(32, log2(24) // 32 * 32), max(1, log2(20)), 8 * rng.randint(1, 16)
+        if n * max(r, c) > 2 ** 31 or r * c > 2 ** 37 or m * rank * max(r, c) > 2 ** 29 or (n <= 4 * m and n * rank >= 2 ** 25):
+            continue
+        seen += 1
+        for yt in (F32, BF16):
+            assert forward(lib, n, r, c, yt, m, rank) == 6, (n, r, c, m, rank)
+            assert r > 2 ** 22 - 64 or backward(lib, n, r, c, yt, m, rank) == 6, (n, r, c, m, rank)
+        assert add(lib, n, r, c, m, rank) == 6 and grads(lib, n, r, c, m, rank) == 6, (n, r, c, m, rank)
