@@ -91,6 +91,10 @@ BACKWARD = [
     (65, 8256, 1024, 3, 64, True, "bf16", "bf16", (2, 16, "runs")),
     (129, 8570, 160, 4, 32, False, "bf16", "bf16", (5, 72, "mixed")),
     (40, 4096, 640, 4, 128, False, "fp16", "fp16", (40, 8, "runs")),
+    # one part, the largest tiles over many steps
+    (4000, 1030, 4096, 4, 128, False, "bf16", "bf16", (2, 64, "mixed")),
+    (2085, 640, 4096, 3, 64, True, "fp16", "fp32", (4, 24, "runs")),
+    (4096, 832, 4096, 4, 32, False, "bf16", "fp32", None),
 ]
 
 
@@ -105,6 +109,10 @@ FORWARD = [
     (1153, 1, 8320, 3, 64, True, "fp16", None),
     (1030, 200, 5184, 4, 96, False, "bf16", (3, 40, "mixed")),
     (1100, 257, 5120, 4, 128, True, "fp16", (2, 16, "runs")),
+    # one part, the largest tiles over many steps
+    (2085, 4096, 2048, 4, 128, False, "bf16", (5, 64, "runs")),
+    (4096, 4096, 1056, 3, 32, True, "fp16", (3, 72, "mixed")),
+    (4000, 4090, 1024, 4, -1, False, "bf16", (1, 128, "all")),
 ]
 
 
