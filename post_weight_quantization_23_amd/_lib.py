@@ -1,5 +1,5 @@
-"""ctypes loader for libgptq_mi355x.so (the C ABI in include/gptq.h and
-include/gptq_adapter.h).
+"""ctypes loader for libgptq_mi355x.so (the C ABI in include/gptq.h,
+include/gptq_adapter.h and include/gptq_train.h).
 
 There is no fallback: if the library is missing or does not load, every entry
 point raises.  Build it with `python -m post_weight_quantization_23_amd.build`.
@@ -16,7 +16,7 @@ GPTQ_F32, GPTQ_BF16, GPTQ_F16 = 0, 1, 2
 STATUS = {0: "GPTQ_OK", 1: "GPTQ_EINVAL", 2: "GPTQ_EDTYPE", 3: "GPTQ_ESHAPE", 4: "GPTQ_EALIGN",
           5: "GPTQ_EUNSUPPORTED", 6: "GPTQ_EWORKSPACE", 7: "GPTQ_EHIP"}
 
-# name -> (restype, argtypes), mirroring include/gptq.h and include/gptq_adapter.h
+# name -> (restype, argtypes), mirroring include/gptq.h, include/gptq_adapter.h and include/gptq_train.h
 _P = C.c_void_p
 _I64 = C.c_int64
 _SZ = C.c_size_t
@@ -49,6 +49,15 @@ SIGNATURES = {
     "gptq_adapter_backward_workspace_size": (C.c_int, [_I64, _I64, _I64, _I64, _I64, _SZP]),
     "gptq_adapter_backward": (C.c_int, [_P, _I64, _P, _I64, C.c_int, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P,
                                         _P, _P, _P, C.c_int, _I64, _P, _SZ, _P]),
+    # include/gptq_train.h
+    "gptq_linear_cross_entropy_workspace_size": (C.c_int, [_I64, _I64, _I64, _SZP]),
+    "gptq_linear_cross_entropy": (C.c_int, [_P, C.c_int, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "gptq_linear_cross_entropy_backward_workspace_size": (C.c_int, [_I64, _I64, _I64, C.c_int, C.c_int, _SZP]),
+    "gptq_linear_cross_entropy_backward": (C.c_int, [_P, C.c_int, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P,
+                                                     _I64, _P, _SZ, _P]),
+    "gptq_adapter_orthogonalize_workspace_size": (C.c_int, [_I64, _I64, _I64, _I64, C.c_int, _SZP]),
+    "gptq_adapter_orthogonalize": (C.c_int, [_P, _P, C.c_int, _I64, _I64, _I64, _I64, C.c_int, C.c_float, C.c_float, C.c_float,
+                                             C.c_float, _P, _P, C.c_int, _P, _SZ, _P]),
     "gptq_build_id": (C.c_char_p, []),
     "gptq_status_string": (C.c_char_p, [C.c_int]),
     "gptq_last_error": (C.c_char_p, []),

@@ -29,7 +29,8 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 # slowest first: the pool starts them at once
 SOURCES = ["quantize.hip", "linear.hip", "gemm_f32.hip", "syrk.hip", "gemv.hip", "prepare.hip",
            "hadamard.hip", "pack.hip", "packed_linear.hip", "packed_tiles.hip", "packed_backward.hip", "gemm16.hip",
-           "adapter.hip", "gptq_api.hip", "adapter_api.hip", "workspace.hip"]
+           "adapter.hip", "loss_tiles.hip", "orthogonal.hip", "loss.hip", "gptq_api.hip", "adapter_api.hip", "train_api.hip",
+           "workspace.hip"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
@@ -40,10 +41,13 @@ COMMON_FLAGS = [
 
 
 HEADERS = [os.path.join(CSRC, "common.hpp"), os.path.join(CSRC, "kernels.hpp")]
-API_HEADERS = [os.path.join(ROOT, "include", "gptq.h"), os.path.join(ROOT, "include", "gptq_adapter.h")]
+API_HEADERS = [os.path.join(ROOT, "include", f) for f in ("gptq.h", "gptq_adapter.h", "gptq_train.h")]
 # headers that only some sources include
 MORE_HEADERS = {"gptq_api.hip": [os.path.join(CSRC, "api.hpp"), *API_HEADERS],
                 "adapter_api.hip": [os.path.join(CSRC, "api.hpp"), os.path.join(CSRC, "adapter.hpp"), *API_HEADERS],
+                "train_api.hip": [*(os.path.join(CSRC, f) for f in ("api.hpp", "adapter.hpp", "loss.hpp", "orthogonal.hpp")), *API_HEADERS],
+                **{f: [os.path.join(CSRC, "adapter.hpp"), os.path.join(CSRC, "loss.hpp")] for f in ("loss.hip", "loss_tiles.hip")},
+                "orthogonal.hip": [os.path.join(CSRC, "adapter.hpp"), os.path.join(CSRC, "orthogonal.hpp")],
                 **{f: [os.path.join(CSRC, "adapter.hpp")] for f in ("packed_linear.hip", "packed_tiles.hip", "packed_backward.hip", "gemm16.hip",
                                                             "adapter.hip")}}
 

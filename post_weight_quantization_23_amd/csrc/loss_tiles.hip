@@ -1,0 +1,458 @@
+// The matrix products of the loss over a vocabulary: logits, whose tiles leave as
+// softmax statistics or as gradients, and the two products of those gradients.
+// One main loop: 16-bit operands through LDS (double buffered, asynchronous
+// loads, one barrier a step), each either contiguous along the contraction or
+// across it.  Operands across it are read from LDS transposed (ds_read_b64_tr), so
+// that neither W, the rows nor the gradients are ever laid out a second time.
+#include "loss.hpp"
+
+namespace gptq {
+
+namespace {
+
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int LK = 64;   // contraction step
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kOutside = 0x7FFFFFFF;   // an offset past every record
+
+// An operand: E entries (rows of A, columns of B) of a tile and LK values of the
+// contraction.  Along: entry f's LK values are 128 bytes, chunk c (16 bytes)
+// at place c ^ swz(f).  Across: the entries of one k are 2 E bytes, granule g (16
+// entries) at place g ^ turn(k): the eight pieces of 32 bytes that a transposed read
+// of 32 lanes touches (4 k, 2 granules) lie in different banks.
+GPTQ_DEV int swz(int f) { return (f ^ (f >> 3)) & 7; }
+template <int E>
+GPTQ_DEV int turn(int k) { return ((2 * (k & 3)) ^ ((k >> 3) & 1)) & (E / 16 - 1); }
+
+struct Source {
+  const uint16_t* p;
+  int64_t ld;
+  int64_t entries;   // rows of an operand along the contraction, columns of one across it
+  int64_t depth;     // values of the contraction; along it a multiple of 8
+};
+
+template <bool ACROSS, int E, int NW>
+struct Operand {
+  static constexpr int BYTES = E * LK * 2, Q = BYTES / 1024 / NW;   // load instructions per wave
+  static_assert(Q * 1024 * NW == BYTES, "operand divides over the waves");
+  const uint16_t* base;
+  int64_t ld, depth;
+  int left;          // entries of the tile that exist
+  int off[Q];
+
+  GPTQ_DEV void set(const Source& s, int64_t e0, int wave, int lane) {
+    base = ACROSS ? s.p + e0 : s.p + e0 * s.ld;
+    ld = s.ld;
+    depth = s.depth;
+    left = (int)min(s.entries - e0, (int64_t)(ACROSS ? (int64_t)1 << 30 : E));
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if constexpr (ACROSS) {
+        constexpr int CH = E / 8, KR = 64 / CH;   // chunks of a k, k of an instruction
+        const int k = (wave * Q + q) * KR + lane / CH, c = lane % CH;
+        off[q] = (int)((k * ld + 8 * (2 * ((c >> 1) ^ turn<E>(k)) + (c & 1))) * 2);
+      } else {
+        const int row = 8 * (wave * Q + q) + (lane >> 3);
+        off[q] = (int)((row * ld + 8 * ((lane & 7) ^ swz(row))) * 2);
+      }
+    }
+  }
+
+  // Values k0 .. k0 + LK - 1 to LDS; what does not exist reads as zero.
+  GPTQ_DEV void load(lds_u8* to, int64_t k0, int wave, int lane) const {
+    const int ks = (int)min(depth - k0, (int64_t)LK);
+    if constexpr (ACROSS) {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(base + k0 * ld), (short)0, (int)(((ks - 1) * ld + min(left, (int)ld)) * 2), 0x00020000);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to + (wave * Q + q) * 1024, 16, off[q], 0, 0, 0);
+    } else {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(base + k0), (short)0, (int)(((left - 1) * ld + ks) * 2), 0x00020000);
+      if (ks == LK) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to + (wave * Q + q) * 1024, 16, off[q], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int row = 8 * (wave * Q + q) + (lane >> 3);
+          const int at = 8 * ((lane & 7) ^ swz(row)) < ks ? off[q] : kOutside;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to + (wave * Q + q) * 1024, 16, at, 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  // Values 16 k + 8 h .. + 7 of entry f0 + (lane & 31).
+  static GPTQ_DEV u32x4 read(const unsigned char* from, int f0, int k, int lane) {
+    const int h = lane >> 5;
+    if constexpr (ACROSS) {
+      const int i = lane & 15, g = (f0 >> 4) + ((lane >> 4) & 1), k0 = 16 * k + 8 * h + (i >> 2);
+      uint2 v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int kk = k0 + 4 * e;
+        const unsigned char* at = from + kk * (2 * E) + ((g ^ turn<E>(kk)) << 5) + (i & 3) * 8;
+        v[e] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
+      }
+      return u32x4{v[0].x, v[0].y, v[1].x, v[1].y};
+    } else {
+      const int f = f0 + (lane & 31);
+      return *reinterpret_cast<const u32x4*>(from + f * (2 * LK) + (((2 * k + h) ^ swz(f)) << 4));
+    }
+  }
+};
+
+// acc = A B^T of steps first .. last - 1.
+template <int DT, bool TA, bool TB, int MT, int NT, int WM, int WN>
+struct Product {
+  static constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, NW = WM * WN, BUF = (TM + TN) * LK * 2;
+  typedef Operand<TA, TM, NW> OpA;
+  typedef Operand<TB, TN, NW> OpB;
+
+  static GPTQ_DEV void run(const Source& a, const Source& b, int64_t a0, int64_t b0, int64_t first, int64_t last,
+                           unsigned char* smem, floatx16 (&acc)[MT][NT]) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
+    lds_u8* lbase = (lds_u8*)smem;
+    OpA oa;
+    OpB ob;
+    oa.set(a, a0, wave, lane);
+    ob.set(b, b0, wave, lane);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) acc[i][q] = floatx16{};
+    if (first >= last) return;
+    auto load = [&](int64_t s) {
+      lds_u8* to = lbase + (s & 1) * BUF;
+      oa.load(to, s * LK, wave, lane);
+      ob.load(to + OpA::BYTES, s * LK, wave, lane);
+    };
+    load(first);
+    for (int64_t s = first; s < last; ++s) {
+      // own loads have landed; with every wave here, the other buffer is free
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (s + 1 < last) load(s + 1);
+      const unsigned char* ab = smem + (s & 1) * BUF;
+      const unsigned char* bb = ab + OpA::BYTES;
+#pragma unroll
+      for (int k = 0; k < LK / 16; ++k) {
+        u32x4 x[MT], y[NT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) x[i] = OpA::read(ab, wm + 32 * i, k, lane);
+#pragma unroll
+        for (int q = 0; q < NT; ++q) y[q] = OpB::read(bb, wn + 32 * q, k, lane);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int q = 0; q < NT; ++q) acc[i][q] = mfma32<DT>(x[i], y[q], acc[i][q]);
+      }
+    }
+    __syncthreads();   // the last step's operands have been read
+  }
+};
+
+// ---------------------------------------------------------------- softmax statistics
+// The largest of two sets of values and the sum of exponentials against it.  A set
+// that holds nothing is (-inf, 0).
+GPTQ_DEV float2 join_sums(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x), r = m == -INFINITY ? 0.f : m;
+  return float2{m, a.y * __builtin_amdgcn_exp2f((a.x - r) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - r) * kLog2e)};
+}
+
+// ---------------------------------------------------------------- logits
+// Tiles of TM vocabulary entries (rows of the accumulators) x TN kept tokens
+// (columns): a lane holds most of a token's entries itself, so the largest and the sum
+// cost one exchange between lanes.
+template <int DT, bool GRAD, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int tok_tiles, int voc_tiles) {
+  using P = Product<DT, false, false, MT, NT, WM, WN>;
+  extern __shared__ __align__(16) unsigned char lsm[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31;
+  const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
+  const int64_t count = *a.k.count;
+  int tt, vt;
+  tile_of(blockIdx.x, tok_tiles, voc_tiles, tt, vt);
+  const int64_t t0 = (int64_t)tt * P::TN, v0 = (int64_t)vt * P::TM;
+  if (t0 >= count) return;
+  const Source w{a.W + a.v0 * a.ldw, a.ldw, a.width, a.d}, x{a.rows, a.kp, count, a.kp};
+  floatx16 acc[MT][NT];
+  P::run(w, x, v0, t0, 0, a.kp / LK, lsm, acc);
+  const int last = (int)min(a.width - v0, (int64_t)P::TM);   // entries of this tile
+  int row[MT][16];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) row[i][e] = wm + 32 * i + TileShape<floatx16>::acc_row(lane, e);
+
+  if constexpr (!GRAD) {
+    float2* part = reinterpret_cast<float2*>(lsm);   // [WM][TN]
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      const int64_t p = t0 + wn + 32 * q + m;
+      const int64_t y = p < count ? (int64_t)a.k.col[p] - v0 : -1;   // entry of the tile
+      if (last < P::TM) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (row[i][e] >= last) acc[i][q][e] = -INFINITY;
+      }
+      if (__any(y >= wm && y < wm + 32 * MT)) {
+        float z = 0.f;
+        bool mine = false;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (row[i][e] == (int)y) z = acc[i][q][e], mine = true;
+        if (mine && y < last) a.at_target[p] = z;
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][q][e]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum += __builtin_amdgcn_exp2f((acc[i][q][e] - ref) * kLog2e);
+      sum += __shfl_xor(sum, 32);
+      if (lane < 32) part[(wave / WN) * P::TN + wn + 32 * q + m] = float2{top, sum};
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < P::TN; c += 64 * WM * WN) {
+      float2 v = part[c];
+#pragma unroll
+      for (int i = 1; i < WM; ++i) v = join_sums(v, part[i * P::TN + c]);
+      if (t0 + c < count) a.part[(int64_t)vt * a.n + t0 + c] = v;
+    }
+  } else {
+    // a wave's tokens, 32 at a time, as rows of LDS, so that they leave in whole runs
+    constexpr int W = 32 * MT, LD = W + 8, RUNS = W / 8;
+    static_assert(WM * WN * 32 * LD * 2 <= 2 * P::BUF, "results fit the operands' LDS");
+    uint16_t* own = reinterpret_cast<uint16_t*>(lsm) + wave * 32 * LD;
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      const int64_t p = t0 + wn + 32 * q + m;
+      const int64_t y = p < count ? (int64_t)a.k.col[p] - a.v0 - v0 : -1;
+      const float lse = p < count ? a.k.lse[p] : 0.f, g = p < count ? a.k.grad[p] : 0.f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          float v[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const int at = row[i][e + f];
+            v[f] = __builtin_amdgcn_exp2f((acc[i][q][e + f] - lse) * kLog2e);
+            if (at == (int)y) v[f] -= 1.f;
+            v[f] = at < last ? v[f] * g : 0.f;
+          }
+          *reinterpret_cast<uint2*>(own + m * LD + row[i][e] - wm) = uint2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int k = 0; k < RUNS / 2; ++k) {
+        const int run = 64 * k + lane, r = run / RUNS, c = 8 * (run % RUNS);
+        const int64_t at = t0 + wn + 32 * q + r;
+        if (at < count && v0 + wm + c < a.ldp)
+          *reinterpret_cast<u32x4*>(a.P + at * a.ldp + v0 + wm + c) = *reinterpret_cast<const u32x4*>(own + r * LD + c);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+// Stores of a wave's 32 rows x 32 NT columns, turned through its LDS.
+template <int OT, int NT, class F>
+GPTQ_DEV void store_rows(float* lds, const floatx16 (&acc)[NT], int64_t j0, int64_t cols, bool vec, float by, F&& row_at) {
+  constexpr int W = 32 * NT, RUNS = W / 8;
+  const int lane = threadIdx.x & 63;
+  turn_tile<NT>(lds, acc);
+#pragma unroll
+  for (int k = 0; k < RUNS / 2; ++k) {
+    const int run = 64 * k + lane, r = run / RUNS, c = 8 * (run % RUNS);
+    uint16_t* to = row_at(r);
+    if (!to || j0 + c >= cols) continue;
+    float v[8];
+    load8f(lds + r * (W + 4) + c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= by;
+    store8<OT>(to, j0 + c, v, (int)min((int64_t)8, cols - j0 - c), vec);
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// dX: tiles of TM kept tokens x TN columns, contracted over the piece's entries.
+template <int DT, bool PARTS, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void grad_x_kernel(GradXArgs a, int tok_tiles, int col_tiles) {
+  using P = Product<DT, false, true, MT, NT, WM, WN>;
+  extern __shared__ __align__(16) unsigned char lsm[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
+  const int64_t count = *a.k.count;
+  int tt, ct;
+  const int64_t tile = blockIdx.x / a.splits;
+  const int split = (int)(blockIdx.x - tile * a.splits);
+  tile_of(tile, tok_tiles, col_tiles, tt, ct);
+  const int64_t t0 = (int64_t)tt * P::TM, j0 = (int64_t)ct * P::TN;
+  if (t0 >= count) return;
+  const int64_t steps = (a.width + LK - 1) / LK, each = (steps + a.splits - 1) / a.splits;
+  const int64_t first = min(steps, split * each), last = min(steps, first + each);
+  floatx16 acc[MT][NT];
+  P::run(Source{a.P, a.ldp, count, a.ldp}, Source{a.W, a.ldw, a.d, a.width}, t0, j0, first, last, lsm, acc);
+  static_assert(WM * WN * 32 * (32 * NT + 4) * 4 <= 2 * P::BUF, "results fit the operands' LDS");
+  float* own = reinterpret_cast<float*>(lsm) + wave * 32 * (32 * NT + 4);
+  if constexpr (PARTS) {
+    constexpr int W = 32 * NT, RUNS = W / 4;
+    const int lane = threadIdx.x & 63;
+    float* part = a.part + (int64_t)split * a.n * a.d;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      turn_tile<NT>(own, acc[i]);
+#pragma unroll
+      for (int k = 0; k < RUNS / 2; ++k) {
+        const int run = 64 * k + lane, r = run / RUNS, c = 4 * (run % RUNS);
+        const int64_t p = t0 + wm + 32 * i + r, j = j0 + wn + c;
+        if (p >= count || j >= a.d) continue;
+        floatx4 v = *reinterpret_cast<const floatx4*>(own + r * (W + 4) + c);
+        floatx4* to = reinterpret_cast<floatx4*>(part + p * a.d + j);
+        if (a.add) v += *to;
+        *to = v;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  } else {
+    const float down = *a.k.down;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      store_rows<DT, NT>(own, acc[i], j0 + wn, a.d, a.vec, down, [&](int r) -> uint16_t* {
+        const int64_t p = t0 + wm + 32 * i + r;
+        return p < count ? a.dX + (int64_t)a.k.token[p] * a.ldd : nullptr;
+      });
+  }
+}
+
+// dW: tiles of TM vocabulary entries x TN columns, contracted over the kept tokens.
+template <int DT, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void grad_w_kernel(GradWArgs a, int voc_tiles, int col_tiles) {
+  using P = Product<DT, true, true, MT, NT, WM, WN>;
+  extern __shared__ __align__(16) unsigned char lsm[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
+  const int64_t count = *a.k.count;
+  int vt, ct;
+  tile_of(blockIdx.x, voc_tiles, col_tiles, vt, ct);
+  const int64_t v0 = (int64_t)vt * P::TM, j0 = (int64_t)ct * P::TN;
+  floatx16 acc[MT][NT];
+  P::run(Source{a.P, a.ldp, a.ldp, count}, Source{a.rows, a.kp, a.kp, count}, v0, j0, 0, (count + LK - 1) / LK, lsm, acc);
+  float* own = reinterpret_cast<float*>(lsm) + wave * 32 * (32 * NT + 4);
+  const float down = *a.k.down;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    store_rows<DT, NT>(own, acc[i], j0 + wn, a.d, a.vec, down, [&](int r) -> uint16_t* {
+      const int64_t v = v0 + wm + 32 * i + r;
+      return v < a.width ? a.dW + v * a.ldd : nullptr;
+    });
+}
+
+// Dynamic LDS of a kernel, set once (thread-safe).
+template <class K>
+void allow_lds(K kernel, int bytes) {
+  (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
+template <int DT, bool GRAD, int MT, int NT, int WM, int WN>
+void logits(const LossArgs& a, hipStream_t s) {
+  using P = Product<DT, false, false, MT, NT, WM, WN>;
+  static const bool set = (allow_lds(logits_kernel<DT, GRAD, MT, NT, WM, WN>, 2 * P::BUF), true);
+  (void)set;
+  static_assert(P::TM == kLossTile, "partial sums are per tile of kLossTile entries");
+  const int tt = (int)tiles_of(a.n, P::TN), vt = (int)tiles_of(a.width, P::TM);
+  hipLaunchKernelGGL((logits_kernel<DT, GRAD, MT, NT, WM, WN>), dim3((unsigned)((int64_t)tt * vt)), dim3(64 * WM * WN), 2 * P::BUF, s,
+                     a, tt, vt);
+}
+
+template <int DT, bool GRAD>
+void logits_shape(const LossArgs& a, hipStream_t s) {
+  if (a.n > 128) logits<DT, GRAD, 4, 2, 2, 4>(a, s);
+  else if (a.n > 64) logits<DT, GRAD, 2, 2, 4, 2>(a, s);
+  else logits<DT, GRAD, 2, 2, 4, 1>(a, s);
+}
+
+template <int DT, int MT, int NT, int WM, int WN>
+void grad_x(const GradXArgs& a, hipStream_t s) {
+  using P = Product<DT, false, true, MT, NT, WM, WN>;
+  static const bool set = (allow_lds(grad_x_kernel<DT, true, MT, NT, WM, WN>, 2 * P::BUF),
+                           allow_lds(grad_x_kernel<DT, false, MT, NT, WM, WN>, 2 * P::BUF), true);
+  (void)set;
+  const int tt = (int)tiles_of(a.n, P::TM), ct = (int)tiles_of(a.d, P::TN);
+  const dim3 grid((unsigned)((int64_t)tt * ct * a.splits)), block(64 * WM * WN);
+  if (a.part) hipLaunchKernelGGL((grad_x_kernel<DT, true, MT, NT, WM, WN>), grid, block, 2 * P::BUF, s, a, tt, ct);
+  else hipLaunchKernelGGL((grad_x_kernel<DT, false, MT, NT, WM, WN>), grid, block, 2 * P::BUF, s, a, tt, ct);
+}
+
+template <int DT, int MT, int NT, int WM, int WN>
+void grad_w(const GradWArgs& a, hipStream_t s) {
+  using P = Product<DT, true, true, MT, NT, WM, WN>;
+  static const bool set = (allow_lds(grad_w_kernel<DT, MT, NT, WM, WN>, 2 * P::BUF), true);
+  (void)set;
+  const int vt = (int)tiles_of(a.width, P::TM), ct = (int)tiles_of(a.d, P::TN);
+  hipLaunchKernelGGL((grad_w_kernel<DT, MT, NT, WM, WN>), dim3((unsigned)((int64_t)vt * ct)), dim3(64 * WM * WN), 2 * P::BUF, s, a, vt, ct);
+}
+
+}  // namespace
+
+void launch_logits(const LossArgs& a, int dt, bool grad, hipStream_t s) {
+  if (dt == kBF16) grad ? logits_shape<kBF16, true>(a, s) : logits_shape<kBF16, false>(a, s);
+  else grad ? logits_shape<kF16, true>(a, s) : logits_shape<kF16, false>(a, s);
+}
+
+void launch_grad_x(const GradXArgs& a, int dt, hipStream_t s) {
+  if (dt == kBF16) a.n > 128 ? grad_x<kBF16, 4, 2, 2, 4>(a, s) : grad_x<kBF16, 2, 2, 2, 2>(a, s);
+  else a.n > 128 ? grad_x<kF16, 4, 2, 2, 4>(a, s) : grad_x<kF16, 2, 2, 2, 2>(a, s);
+}
+
+void launch_grad_w(const GradWArgs& a, int dt, hipStream_t s) {
+  if (dt == kBF16) grad_w<kBF16, 4, 2, 2, 4>(a, s);
+  else grad_w<kF16, 4, 2, 2, 4>(a, s);
+}
+
+int grad_x_splits(int64_t n, int64_t d, int64_t width) {
+  const int64_t tile = n > 128 ? 256 : 128, tiles = tiles_of(n, tile) * tiles_of(d, tile), steps = tiles_of(width, LK);
+  int64_t splits = (n > 128 ? 256 : 512) / (tiles > 0 ? tiles : 1);
+  splits = splits < steps / 8 ? splits : steps / 8;
+  if (splits < 2) return 1;
+  splits = splits < 16 ? splits : 16;
+  const int64_t each = (steps + splits - 1) / splits;
+  return (int)((steps + each - 1) / each);
+}
+
+// Gradients of a piece are n x width 16-bit values: 512 MB.
+int64_t loss_piece(int64_t n, int64_t vocab) {
+  const int64_t most = (int64_t(1) << 28) / (n > 0 ? n : 1) / kLossTile * kLossTile;
+  return vocab <= most ? vocab : (most > kLossTile ? most : kLossTile);
+}
+
+bool loss_fits(int64_t n, int64_t vocab, int64_t d, bool grad) {
+  const int64_t shortest = n > 128 ? 256 : (n > 64 ? 128 : 64);
+  if (!grid_fits(tiles_of(n, shortest) * loss_tiles(vocab), 512)) return false;
+  if (!grid_fits(tiles_of(n * (gemm16_depth(d) / 8), 256), 256)) return false;
+  if (!grad) return true;
+  const int64_t tile = n > 128 ? 256 : 128;
+  return grid_fits(tiles_of(n, tile) * tiles_of(d, tile) * 16, 512) && grid_fits(loss_tiles(vocab) * tiles_of(d, 256), 512);
+}
+
+}  // namespace gptq

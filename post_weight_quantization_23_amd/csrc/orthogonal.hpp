@@ -1,0 +1,37 @@
+// Launch interface of the orthogonalised adapter updates (orthogonal.hip; internal
+// to the library).
+#pragma once
+#include "adapter.hpp"
+
+namespace gptq {
+
+// One factor of every adapter: m matrices of rows x cols.  p: the shorter side
+// (1 .. 128), q: the longer one; tall: rows > cols.
+struct OrthoProblem {
+  const void* G;
+  void* out;
+  int64_t rows, cols;
+  int64_t q;
+  int p;
+  bool tall;
+  int splits;            // parts of q in S_0
+  double* part;          // [m][splits][tiles][256]
+  double* inv;           // [m]: 1 / (|G|_F + eps)
+  double* steps;         // [m][count][tiles][256]: q(S_k)
+  float* R;              // [m][pp][pp], pp: p rounded up to 16
+};
+struct OrthoArgs {
+  int64_t m;
+  int steps;
+  double a, b, c, eps;
+  OrthoProblem p[2];     // p[1].G null: one
+};
+constexpr int kOrthoRank = 128;
+constexpr int ortho_blocks(int p) { return (p + 15) / 16; }
+constexpr int ortho_tiles(int p) { return ortho_blocks(p) * (ortho_blocks(p) + 1) / 2; }
+int ortho_splits(int64_t m, int64_t q);
+bool ortho_fits(int64_t m, int64_t q);
+// gt / ot: 0 fp32, 1 bf16, 2 fp16.
+void launch_orthogonalize(const OrthoArgs& a, int gt, int ot, hipStream_t s);
+
+}  // namespace gptq
