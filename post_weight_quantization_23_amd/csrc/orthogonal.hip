@@ -33,61 +33,112 @@ GPTQ_DEV void tile_of_index(int t, int B, int& i, int& j) {
 // C[4 e + (lane >> 4)][lane & 15] in component e; A[lane & 15][lane >> 4], B[lane >> 4][lane & 15].
 GPTQ_DEV doublex4 mfma64(double a, double b, doublex4 c) { return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0); }
 
+// ---------------------------------------------------------------- a run of the long side in LDS
+// KS values of the long side in fp32, zeros past the matrix: rows of the shorter side
+// (KS values and padding), or of the longer one where that is how they lie in memory.
+// The paddings keep the lanes of a read, which run along one side and
+// four values of the other, in different banks.
+constexpr int KS = 64;
+
+template <int B, bool TALL>
+struct Run {
+  static constexpr int PP = 16 * B;
+  // gram: lanes along the shorter side; apply: along the longer one
+  static constexpr int GRAM = TALL ? 16 * (B | 1) : KS + 4, APPLY = TALL ? PP + 4 : KS + 16;
+  static constexpr int ROWS = TALL ? KS : PP;
+  static constexpr int FLOATS = ROWS * (GRAM > APPLY ? GRAM : APPLY);
+  static constexpr int PER = PP * KS / 4;   // fours of values
+
+  // Four values of thread's place v of a run: of short row s from long k, or the reverse.
+  static GPTQ_DEV floatx4 fetch(const OrthoProblem& o, int type, int64_t mat, int64_t k0, int v) {
+    const int row = TALL ? v / (PP / 4) : v / (KS / 4), col = 4 * (TALL ? v % (PP / 4) : v % (KS / 4));
+    const int64_t r = TALL ? k0 + row : row, c = TALL ? col : k0 + col;
+    floatx4 x = {0.f, 0.f, 0.f, 0.f};
+    if (r >= o.rows || c >= o.cols) return x;
+    const int64_t at = mat * o.rows * o.cols + r * o.cols + c;
+    if (o.vec) {
+      if (type == 0) return *reinterpret_cast<const floatx4*>(static_cast<const float*>(o.G) + at);
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(o.G) + at);
+      const uint32_t u[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = type == kBF16 ? f16_to_f32<kBF16>(u[e]) : f16_to_f32<kF16>(u[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < o.cols) x[e] = load_value(o.G, at + e, type);
+    }
+    return x;
+  }
+  static GPTQ_DEV void put(float* lds, int stride, int v, floatx4 x) {
+    const int row = TALL ? v / (PP / 4) : v / (KS / 4), col = 4 * (TALL ? v % (PP / 4) : v % (KS / 4));
+    *reinterpret_cast<floatx4*>(lds + row * stride + col) = x;
+  }
+  static GPTQ_DEV float get(const float* lds, int stride, int s, int l) { return TALL ? lds[l * stride + s] : lds[s * stride + l]; }
+};
+
 // ---------------------------------------------------------------- S_0
-// A workgroup takes a run of the long side, 64 values at a time through LDS (fp32,
-// the shorter side contiguous), and writes its part of every tile of G G^T.
-constexpr int KS = 64, LDG = kOrthoRank + 4;
-
-GPTQ_DEV void stage(const OrthoProblem& o, int type, int64_t mat, int64_t k0, int width, float* lds, int threads) {
-  // lds[k][i] = G[i][k0 + k], zero past the matrix
-  const int pp = ortho_blocks(o.p) * 16;
-  for (int e = threadIdx.x; e < width * pp; e += threads) {
-    int i, k;
-    if (o.tall) i = e % pp, k = e / pp;
-    else k = e % width, i = e / width;
-    float v = 0.f;
-    if (i < o.p && k0 + k < o.q)
-      v = load_value(o.G, mat * o.rows * o.cols + (o.tall ? (k0 + k) * o.p + i : i * o.q + k0 + k), type);
-    lds[k * LDG + i] = v;
-  }
-}
-
-__global__ __launch_bounds__(256) void gram_kernel(OrthoArgs a, int type, int64_t blocks0) {
-  __shared__ __align__(16) float g[KS * LDG];
-  const int which = blockIdx.x >= blocks0;
-  const OrthoProblem& o = a.p[which];
-  const int64_t b = blockIdx.x - (which ? blocks0 : 0), mat = b / o.splits;
-  const int split = (int)(b - mat * o.splits), B = ortho_blocks(o.p), tiles = ortho_tiles(o.p);
+// Parts of G G^T over the long side.  A wave holds tile rows i and B-1-i of the upper
+// half, B+1 tiles whatever i is, so a fragment of the run serves several products; with
+// fewer than four such pairs the waves share the run's values out among them.
+template <int B, bool TALL>
+GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, float* lds) {
+  using R = Run<B, TALL>;
+  constexpr int PAIRS = (B + 1) / 2, SHARE = kOrthoShare(B), TILES = ortho_tiles(16 * B), LD = (R::PER + 255) / 256;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
+  const int pair = wave % PAIRS, share = wave / PAIRS, i0 = pair, i1 = B - 1 - pair;
+  const bool works = share < SHARE;
   const int64_t each = ((o.q + o.splits - 1) / o.splits + KS - 1) / KS * KS, first = split * each, last = min(o.q, first + each);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, h = lane >> 4;
-  constexpr int MOST = 9;   // tiles of a wave: 36 / 4
-  doublex4 acc[MOST];
-  int ti[MOST], tj[MOST];
+  doublex4 up[B], low[B];
 #pragma unroll
-  for (int e = 0; e < MOST; ++e) {
-    acc[e] = doublex4{0, 0, 0, 0};
-    const int t = min(wave + 4 * e, tiles - 1);
-    tile_of_index(t, B, ti[e], tj[e]);
-  }
+  for (int t = 0; t < B; ++t) up[t] = low[t] = doublex4{0, 0, 0, 0};
+  floatx4 next[LD];
+  auto fetch = [&](int64_t k0) {
+#pragma unroll
+    for (int e = 0; e < LD; ++e)
+      if (threadIdx.x + 256 * e < R::PER) next[e] = R::fetch(o, type, mat, k0, threadIdx.x + 256 * e);
+  };
+  if (first < last) fetch(first);
   for (int64_t k0 = first; k0 < last; k0 += KS) {
-    __syncthreads();
-    stage(o, type, mat, k0, KS, g, 256);
-    __syncthreads();
-    for (int k = 0; k < KS; k += 4) {
+    __syncthreads();   // the last run has been read
 #pragma unroll
-      for (int e = 0; e < MOST; ++e)
-        if (wave + 4 * e < tiles) {
-          const float* row = g + (k + h) * LDG + r;
-          acc[e] = mfma64((double)row[16 * ti[e]], (double)row[16 * tj[e]], acc[e]);
+    for (int e = 0; e < LD; ++e)
+      if (threadIdx.x + 256 * e < R::PER) R::put(lds, R::GRAM, threadIdx.x + 256 * e, next[e]);
+    __syncthreads();
+    if (k0 + KS < last) fetch(k0 + KS);
+    if (!works) continue;
+    for (int k1 = 0; k1 < KS; k1 += 4 * SHARE) {
+      const int k = k1 + 4 * share;
+      const double a0 = R::get(lds, R::GRAM, 16 * i0 + r, k + h), a1 = R::get(lds, R::GRAM, 16 * i1 + r, k + h);
+#pragma unroll
+      for (int t = 0; t < B; ++t)
+        if (t >= i0) {
+          const double b = R::get(lds, R::GRAM, 16 * t + r, k + h);
+          up[t] = mfma64(a0, b, up[t]);
+          if (t >= i1 && i1 != i0) low[t] = mfma64(a1, b, low[t]);
         }
     }
   }
-  double* part = o.part + (mat * o.splits + split) * tiles * 256;
+  if (!works) return;
+  double* part = o.part + ((mat * o.splits + split) * SHARE + share) * TILES * 256;
 #pragma unroll
-  for (int e = 0; e < MOST; ++e)
-    if (wave + 4 * e < tiles)
+  for (int t = 0; t < B; ++t)
 #pragma unroll
-      for (int f = 0; f < 4; ++f) part[(wave + 4 * e) * 256 + (4 * f + h) * 16 + r] = acc[e][f];
+    for (int e = 0; e < 4; ++e) {
+      if (t >= i0) part[tile_index(i0, t, B) * 256 + (4 * e + h) * 16 + r] = up[t][e];
+      if (t >= i1 && i1 != i0) part[tile_index(i1, t, B) * 256 + (4 * e + h) * 16 + r] = low[t][e];
+    }
+}
+
+template <int B>
+__global__ __launch_bounds__(256) void gram_kernel(OrthoArgs a, int which, int type, int64_t blocks0) {
+  __shared__ __align__(16) float lds[Run<B, true>::FLOATS > Run<B, false>::FLOATS ? Run<B, true>::FLOATS : Run<B, false>::FLOATS];
+  int64_t b = blockIdx.x;
+  if (b >= blocks0) b -= blocks0, which = 1;
+  const OrthoProblem& o = a.p[which];
+  const int64_t mat = b / o.splits;
+  const int split = (int)(b - mat * o.splits);
+  if (o.tall) gram<B, true>(o, type, mat, split, lds);
+  else gram<B, false>(o, type, mat, split, lds);
 }
 
 // ---------------------------------------------------------------- the iteration
@@ -102,6 +153,8 @@ GPTQ_DEV double element(const double* S, int ti, int tj, int i, int j) {
 template <int B>
 struct Chain {
   static constexpr int TILES = B * (B + 1) / 2, WAVES = TILES < 16 ? TILES : 16, MOST = (TILES + WAVES - 1) / WAVES;
+  static constexpr int THREADS = WAVES < 8 ? 512 : 64 * WAVES;   // all of them read the parts of S_0
+  static constexpr bool HOLDS = B <= 6;                          // a third matrix, the product of the steps so far
   int lane, wave, r, h;
   int ti[MOST], tj[MOST];
 
@@ -110,20 +163,34 @@ struct Chain {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     r = lane & 15;
     h = lane >> 4;
+#pragma unroll
     for (int e = 0; e < MOST; ++e) tile_of_index(min(wave + WAVES * e, TILES - 1), B, ti[e], tj[e]);
   }
-  GPTQ_DEV bool has(int e) const { return wave + WAVES * e < TILES; }
+  GPTQ_DEV bool has(int e) const { return wave < WAVES && wave + WAVES * e < TILES; }
 
   // acc = this wave's tiles of X Y (commuting, symmetric).
   GPTQ_DEV void product(const double* X, const double* Y, doublex4 (&acc)[MOST]) const {
 #pragma unroll
-    for (int e = 0; e < MOST; ++e) {
-      acc[e] = doublex4{0, 0, 0, 0};
-      if (!has(e)) continue;
-      for (int tk = 0; tk < B; ++tk)
+    for (int e = 0; e < MOST; ++e) acc[e] = doublex4{0, 0, 0, 0};
+    if (wave >= WAVES) return;
+    for (int tk = 0; tk < B; ++tk) {
+      double x[MOST][4], y[MOST][4];
 #pragma unroll
-        for (int k = 0; k < 16; k += 4)
-          acc[e] = mfma64(element<B>(X, ti[e], tk, r, k + h), element<B>(Y, tk, tj[e], k + h, r), acc[e]);
+      for (int e = 0; e < MOST; ++e) {
+        const bool xu = ti[e] <= tk, yu = tk <= tj[e];   // which half holds the tile
+        const double* xt = X + (xu ? tile_index(ti[e], tk, B) : tile_index(tk, ti[e], B)) * TSIZE + r * (xu ? TROW : 1) + h * (xu ? 1 : TROW);
+        const double* yt = Y + (yu ? tile_index(tk, tj[e], B) : tile_index(tj[e], tk, B)) * TSIZE + r * (yu ? 1 : TROW) + h * (yu ? TROW : 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[e][k] = xt[4 * k * (xu ? 1 : TROW)];
+          y[e][k] = yt[4 * k * (yu ? TROW : 1)];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < MOST; ++e)
+          if (has(e)) acc[e] = mfma64(x[e][k], y[e][k], acc[e]);
     }
   }
   template <class F>
@@ -142,175 +209,226 @@ struct Chain {
 template <int B>
 GPTQ_DEV void iterate(const OrthoArgs& a, const OrthoProblem& o, int64_t mat, double* lds) {
   using C = Chain<B>;
+  constexpr int N = C::TILES * 256, GROUPS = C::THREADS / N > 0 ? C::THREADS / N : 1;
   C c;
   c.set();
-  double *S = lds, *T = lds + C::TILES * TSIZE;
-  __shared__ double norm;
-  doublex4 acc[C::MOST], q[C::MOST];
-  const double* part = o.part + mat * o.splits * C::TILES * 256;
-  c.each([&](int e, int g, int t, int i, int j) {
+  double *S = lds, *T = S + C::TILES * TSIZE, *R = C::HOLDS ? T + C::TILES * TSIZE : T;
+  __shared__ double norm, sums[GROUPS > 1 ? GROUPS * N : 1];
+  // the parts of S_0, in their order
+  const int parts = o.splits * kOrthoShare(B);
+  const double* part = o.part + mat * parts * N;
+  for (int e = threadIdx.x; e < N * GROUPS; e += C::THREADS) {
+    const int at = e % N, group = e / N, each = (parts + GROUPS - 1) / GROUPS, last = min(parts, (group + 1) * each);
     double v = 0;
-    for (int s = 0; s < o.splits; ++s) v += part[((int64_t)s * C::TILES + t) * 256 + i * 16 + j];
-    acc[e][g] = v;
-  });
-  c.write(S, acc);
+#pragma unroll 8
+    for (int s = group * each; s < last; ++s) v += part[(int64_t)s * N + at];
+    if constexpr (GROUPS > 1) sums[e] = v;
+    else S[at / 256 * TSIZE + at % 256 / 16 * TROW + at % 16] = v;
+  }
   __syncthreads();
+  if constexpr (GROUPS > 1) {
+    for (int e = threadIdx.x; e < N; e += C::THREADS) {
+      double v = 0;
+      for (int g = 0; g < GROUPS; ++g) v += sums[g * N + e];
+      S[e / 256 * TSIZE + e % 256 / 16 * TROW + e % 16] = v;
+    }
+    __syncthreads();
+  }
   if (c.wave == 0) {
     double v = 0;
     for (int i = c.lane; i < 16 * B; i += 64) v += S[tile_index(i / 16, i / 16, B) * TSIZE + (i % 16) * (TROW + 1)];
     for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
     if (c.lane == 0) {
-      norm = sqrt(v) + a.eps;
-      o.inv[mat] = 1.0 / norm;
+      norm = 1.0 / (sqrt(v) + a.eps);
+      o.inv[mat] = norm;
     }
   }
   __syncthreads();
-  const double by = 1.0 / norm;
-  c.each([&](int e, int g, int t, int i, int j) { S[t * TSIZE + i * TROW + j] = acc[e][g] * by * by; });
+  const double by = norm;
+  for (int e = threadIdx.x; e < C::TILES * TSIZE; e += C::THREADS) S[e] = S[e] * by * by;
   __syncthreads();
-  double* steps = o.steps + mat * a.steps * C::TILES * 256;
+  doublex4 acc[C::MOST], more[C::MOST];
+  double* steps = o.steps + mat * a.steps * N;
   for (int k = 0; k < a.steps; ++k) {
     c.product(S, S, acc);
-    // q(S) to T and to memory
+    // q(S)
     c.each([&](int e, int g, int t, int i, int j) {
       const double v = a.c * acc[e][g] + a.b * S[t * TSIZE + i * TROW + j] + (c.ti[e] == c.tj[e] && i == j ? a.a : 0.0);
-      q[e][g] = v;
       T[t * TSIZE + i * TROW + j] = v;
-      if (k + 1 < a.steps) steps[((int64_t)k * C::TILES + t) * 256 + i * 16 + j] = v;
+      if (C::HOLDS && k == 0) R[t * TSIZE + i * TROW + j] = v;
+      if (!C::HOLDS && k + 1 < a.steps) steps[(int64_t)k * N + t * 256 + i * 16 + j] = v;
     });
     __syncthreads();
-    if (k + 1 == a.steps) break;
-    c.product(S, T, acc);
+    const bool on = k + 1 < a.steps;
+    if (on) c.product(S, T, acc);
+    if (C::HOLDS && k > 0) c.product(T, R, more);
     __syncthreads();
-    c.write(S, acc);
+    if (on) c.write(S, acc);
+    if (C::HOLDS && k > 0) c.write(R, more);
     __syncthreads();
+    if (!on) break;
     c.product(S, T, acc);
     __syncthreads();
     c.write(S, acc);
     __syncthreads();
   }
-  // T holds the last step's q: the earlier ones follow
-  for (int k = a.steps - 2; k >= 0; --k) {
-    c.each([&](int e, int g, int t, int i, int j) { S[t * TSIZE + i * TROW + j] = steps[((int64_t)k * C::TILES + t) * 256 + i * 16 + j]; });
-    __syncthreads();
-    c.product(T, S, acc);
-    __syncthreads();
-    c.write(T, acc);
-    __syncthreads();
-  }
-  float* R = o.R + mat * (16 * B) * (16 * B);
-  for (int e = threadIdx.x; e < 256 * B * B; e += 64 * C::WAVES) {
+  if constexpr (!C::HOLDS)   // T holds the last step's q: the earlier ones follow
+    for (int k = a.steps - 2; k >= 0; --k) {
+      for (int e = threadIdx.x; e < N; e += C::THREADS) S[e / 256 * TSIZE + e % 256 / 16 * TROW + e % 16] = steps[(int64_t)k * N + e];
+      __syncthreads();
+      c.product(T, S, acc);
+      __syncthreads();
+      c.write(T, acc);
+      __syncthreads();
+    }
+  float* out = o.R + mat * (16 * B) * (16 * B);
+  for (int e = threadIdx.x; e < 256 * B * B; e += C::THREADS) {
     const int i = e / (16 * B), j = e % (16 * B);
-    R[e] = (float)element<B>(T, i / 16, j / 16, i % 16, j % 16);
+    out[e] = (float)element<B>(R, i / 16, j / 16, i % 16, j % 16);
   }
 }
 
 template <int B>
-__global__ __launch_bounds__(64 * Chain<B>::WAVES) void chain_kernel(OrthoArgs a, int which) {
+__global__ __launch_bounds__(Chain<B>::THREADS) void chain_kernel(OrthoArgs a, int which) {
   extern __shared__ __align__(16) double cs[];
-  iterate<B>(a, a.p[which], blockIdx.x, cs);
+  int64_t mat = blockIdx.x;
+  if (mat >= a.m) mat -= a.m, which = 1;
+  iterate<B>(a, a.p[which], mat, cs);
 }
 
 // ---------------------------------------------------------------- result
-// out = R M_0 for a run of 64 values of the long side, each wave 16 of them.  The
-// lanes run along the side that is contiguous in memory; R is symmetric, so either operand order
+// out = R M_0 for runs of the long side.  Wave w holds rows 16 (w % B) .. of R in
+// registers and takes every (waves / B)th set of 16 long values of a run.  The lanes
+// run along the side that is contiguous in memory; R is symmetric, so either operand order
 // holds it.
 GPTQ_DEV floatx4 mfma_f32(float a, float b, floatx4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
-GPTQ_DEV void store_value(void* p, int64_t at, float v, int type) {
-  if (type == 0) static_cast<float*>(p)[at] = v;
-  else static_cast<uint16_t*>(p)[at] = type == kBF16 ? f32_to_16<kBF16>(v) : f32_to_16<kF16>(v);
-}
-
-__global__ __launch_bounds__(256) void apply_kernel(OrthoArgs a, int gt, int ot, int64_t blocks0) {
-  extern __shared__ __align__(16) float as[];
-  const int which = blockIdx.x >= blocks0;
-  const OrthoProblem& o = a.p[which];
-  const int64_t runs = (o.q + KS - 1) / KS, b = blockIdx.x - (which ? blocks0 : 0), mat = b / runs, k0 = (b - mat * runs) * KS;
-  const int B = ortho_blocks(o.p), pp = 16 * B, ldr = pp + 4;
-  float *R = as, *g = as + pp * ldr;
-  for (int e = threadIdx.x; e < pp * pp; e += 256) R[e / pp * ldr + e % pp] = o.R[mat * pp * pp + e];
-  stage(o, gt, mat, k0, KS, g, 256);
-  __syncthreads();
-  const double inv = o.inv[mat];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, h = lane >> 4, at = 16 * wave;
-  floatx4 acc[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < pp; k += 4) {
-    const float m0 = (float)((double)g[(at + r) * LDG + k + h] * inv);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < B) {
-        const float w = R[(16 * i + r) * ldr + k + h];
-        acc[i] = o.tall ? mfma_f32(m0, w, acc[i]) : mfma_f32(w, m0, acc[i]);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < B)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int s = o.tall ? 16 * i + r : 16 * i + 4 * h + e;          // place on the shorter side
-        const int64_t l = k0 + at + (o.tall ? 4 * h + e : r);            // on the longer one
-        if (s < o.p && l < o.q) store_value(o.out, mat * o.rows * o.cols + (o.tall ? l * o.p + s : s * o.q + l), acc[i][e], ot);
-      }
-}
+template <int OT>
+GPTQ_DEV void store_value(void* p, int64_t at, float v) { store_out<OT>(p, at, v); }
 
 template <int B>
-void chain(const OrthoArgs& a, int which, hipStream_t s) {
-  constexpr int LDS = 2 * Chain<B>::TILES * TSIZE * 8;
+struct Apply {
+  static constexpr int SETS = B >= 5 ? 1 : (B >= 3 ? 2 : (B == 2 ? 4 : 4)), THREADS = 64 * B * SETS;
+};
+
+template <int B, bool TALL, int OT>
+GPTQ_DEV void apply(const OrthoProblem& o, int gt, int64_t mat, int64_t first, int64_t last, float* lds) {
+  using R = Run<B, TALL>;
+  constexpr int SETS = Apply<B>::SETS, THREADS = Apply<B>::THREADS, LD = (R::PER + THREADS - 1) / THREADS, PP = 16 * B;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
+  const int row = wave % B, set = wave / B;
+  floatx4 next[LD];
+  auto fetch = [&](int64_t k0) {
+#pragma unroll
+    for (int e = 0; e < LD; ++e)
+      if (threadIdx.x + THREADS * e < R::PER) next[e] = R::fetch(o, gt, mat, k0, threadIdx.x + THREADS * e);
+  };
+  fetch(first);
+  float w[4 * B];
+#pragma unroll
+  for (int k = 0; k < 4 * B; ++k) w[k] = o.R[mat * PP * PP + (16 * row + r) * PP + 4 * k + h];
+  const double inv = o.inv[mat];
+  for (int64_t k0 = first; k0 < last; k0 += KS) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < LD; ++e)
+      if (threadIdx.x + THREADS * e < R::PER) {
+        floatx4 x = next[e];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) x[f] = (float)((double)x[f] * inv);
+        R::put(lds, R::APPLY, threadIdx.x + THREADS * e, x);
+      }
+    __syncthreads();
+    if (k0 + KS < last) fetch(k0 + KS);
+    for (int at = 16 * set; at < KS; at += 16 * SETS) {
+      floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 4 * B; ++k) {
+        const float m0 = R::get(lds, R::APPLY, 4 * k + h, at + r);
+        acc = TALL ? mfma_f32(m0, w[k], acc) : mfma_f32(w[k], m0, acc);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int s = TALL ? 16 * row + r : 16 * row + 4 * h + e;        // place on the shorter side
+        const int64_t l = k0 + at + (TALL ? 4 * h + e : r);              // on the longer one
+        if (s < o.p && l < o.q) store_value<OT>(o.out, mat * o.rows * o.cols + (TALL ? l * o.p + s : s * o.q + l), acc[e]);
+      }
+    }
+  }
+}
+
+template <int B, int OT>
+__global__ __launch_bounds__(Apply<B>::THREADS) void apply_kernel(OrthoArgs a, int which, int gt, int64_t blocks0, int runs) {
+  __shared__ __align__(16) float lds[Run<B, true>::FLOATS > Run<B, false>::FLOATS ? Run<B, true>::FLOATS : Run<B, false>::FLOATS];
+  int64_t b = blockIdx.x;
+  if (b >= blocks0) b -= blocks0, which = 1;
+  const OrthoProblem& o = a.p[which];
+  const int64_t per = (o.q + (int64_t)KS * runs - 1) / ((int64_t)KS * runs), mat = b / per, first = (b - mat * per) * KS * runs;
+  const int64_t last = min(o.q, first + KS * runs);
+  if (o.tall) apply<B, true, OT>(o, gt, mat, first, last, lds);
+  else apply<B, false, OT>(o, gt, mat, first, last, lds);
+}
+
+// One launch of each kernel for the problems of B tile rows: `which` and, if both, the other.
+template <int B>
+void orthogonalize(const OrthoArgs& a, int which, bool both, int gt, int ot, hipStream_t s) {
+  constexpr int LDS = (Chain<B>::HOLDS ? 3 : 2) * Chain<B>::TILES * TSIZE * 8;
   static const bool set = [] {
     (void)hipFuncSetAttribute((const void*)chain_kernel<B>, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     return true;
   }();
   (void)set;
-  hipLaunchKernelGGL(chain_kernel<B>, dim3((unsigned)a.m), dim3(64 * Chain<B>::WAVES), LDS, s, a, which);
+  // runs of a workgroup: four where that leaves two workgroups for each CU
+  int64_t all = 0;
+  for (int w = which; w <= (both ? 1 : which); ++w) all += a.m * ((a.p[w].q + KS - 1) / KS);
+  const int runs = all >= 2048 ? 4 : (all >= 1024 ? 2 : 1);
+  int64_t gram[2] = {0, 0}, apply[2] = {0, 0};
+  for (int w = which; w <= (both ? 1 : which); ++w) {
+    gram[w - which] = a.m * a.p[w].splits;
+    apply[w - which] = a.m * ((a.p[w].q + (int64_t)KS * runs - 1) / ((int64_t)KS * runs));
+  }
+  hipLaunchKernelGGL(gram_kernel<B>, dim3((unsigned)(gram[0] + gram[1])), dim3(256), 0, s, a, which, gt, gram[0]);
+  hipLaunchKernelGGL(chain_kernel<B>, dim3((unsigned)(both ? 2 * a.m : a.m)), dim3(Chain<B>::THREADS), LDS, s, a, which);
+  const dim3 grid((unsigned)(apply[0] + apply[1])), block(Apply<B>::THREADS);
+  if (ot == 0) hipLaunchKernelGGL((apply_kernel<B, 0>), grid, block, 0, s, a, which, gt, apply[0], runs);
+  else if (ot == kBF16) hipLaunchKernelGGL((apply_kernel<B, kBF16>), grid, block, 0, s, a, which, gt, apply[0], runs);
+  else hipLaunchKernelGGL((apply_kernel<B, kF16>), grid, block, 0, s, a, which, gt, apply[0], runs);
+}
+
+void choose(const OrthoArgs& a, int which, bool both, int gt, int ot, hipStream_t s) {
+  switch (ortho_blocks(a.p[which].p)) {
+    case 1: return orthogonalize<1>(a, which, both, gt, ot, s);
+    case 2: return orthogonalize<2>(a, which, both, gt, ot, s);
+    case 3: return orthogonalize<3>(a, which, both, gt, ot, s);
+    case 4: return orthogonalize<4>(a, which, both, gt, ot, s);
+    case 5: return orthogonalize<5>(a, which, both, gt, ot, s);
+    case 6: return orthogonalize<6>(a, which, both, gt, ot, s);
+    case 7: return orthogonalize<7>(a, which, both, gt, ot, s);
+    default: return orthogonalize<8>(a, which, both, gt, ot, s);
+  }
 }
 
 }  // namespace
 
-void launch_orthogonalize(const OrthoArgs& a, int gt, int ot, hipStream_t s) {
-  int64_t gram[2] = {0, 0}, apply[2] = {0, 0};
-  int most = 0;
-  for (int w = 0; w < 2; ++w)
-    if (a.p[w].G) {
-      gram[w] = a.m * a.p[w].splits;
-      apply[w] = a.m * ((a.p[w].q + KS - 1) / KS);
-      most = most > a.p[w].p ? most : a.p[w].p;
-    }
-  hipLaunchKernelGGL(gram_kernel, dim3((unsigned)(gram[0] + gram[1])), dim3(256), 0, s, a, gt, gram[0]);
-  for (int w = 0; w < 2; ++w)
-    if (a.p[w].G) switch (ortho_blocks(a.p[w].p)) {
-      case 1: chain<1>(a, w, s); break;
-      case 2: chain<2>(a, w, s); break;
-      case 3: chain<3>(a, w, s); break;
-      case 4: chain<4>(a, w, s); break;
-      case 5: chain<5>(a, w, s); break;
-      case 6: chain<6>(a, w, s); break;
-      case 7: chain<7>(a, w, s); break;
-      default: chain<8>(a, w, s); break;
-    }
-  const int pp = 16 * ortho_blocks(most), lds = (pp * (pp + 4) + KS * LDG) * 4;
-  static const bool set = [] {
-    (void)hipFuncSetAttribute((const void*)apply_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                              (kOrthoRank * (kOrthoRank + 4) + KS * LDG) * 4);
-    return true;
-  }();
-  (void)set;
-  hipLaunchKernelGGL(apply_kernel, dim3((unsigned)(apply[0] + apply[1])), dim3(256), lds, s, a, gt, ot, apply[0]);
+void launch_orthogonalize(const OrthoArgs& args, int gt, int ot, hipStream_t s) {
+  OrthoArgs a = args;
+  const int64_t e = gt == 0 ? 4 : 2;
+  for (OrthoProblem& o : a.p) o.vec = o.G && reinterpret_cast<uintptr_t>(o.G) % (4 * e) == 0 && o.cols % 4 == 0;
+  const bool two = a.p[1].G != nullptr, same = two && ortho_blocks(a.p[0].p) == ortho_blocks(a.p[1].p);
+  choose(a, 0, same, gt, ot, s);
+  if (two && !same) choose(a, 1, false, gt, ot, s);
 }
 
+// Parts of S_0: enough for a workgroup on every CU, each of one run at least; a matrix's
+// iteration reads them all.
 int ortho_splits(int64_t m, int64_t q) {
   const int64_t runs = (q + KS - 1) / KS, want = 256 / (2 * (m > 0 ? m : 1));
-  int64_t splits = want < 8 ? 8 : want;
+  int64_t splits = want < 4 ? 4 : (want < 32 ? want : 32);
   splits = splits < runs ? splits : runs;
-  splits = splits < 64 ? splits : 64;
-  return (int)(splits > 0 ? splits : 1);
+  const int64_t each = (runs + splits - 1) / splits;
+  return (int)((runs + each - 1) / each);
 }
 
-bool ortho_fits(int64_t m, int64_t q) {
-  return grid_fits(2 * m * ((q + KS - 1) / KS), 256) && grid_fits(m, 1024) && grid_fits(2 * m * 64, 256);
-}
+bool ortho_fits(int64_t m, int64_t q) { return grid_fits(2 * m * ((q + KS - 1) / KS), 512) && grid_fits(2 * m, 1024) && grid_fits(2 * m * 32, 256); }
 
 }  // namespace gptq

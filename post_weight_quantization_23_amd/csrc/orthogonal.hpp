@@ -15,7 +15,8 @@ struct OrthoProblem {
   int p;
   bool tall;
   int splits;            // parts of q in S_0
-  double* part;          // [m][splits][tiles][256]
+  bool vec;              // set by the launch: four values of a row start on their multiple
+  double* part;          // [m][splits][kOrthoShare][tiles][256]
   double* inv;           // [m]: 1 / (|G|_F + eps)
   double* steps;         // [m][count][tiles][256]: q(S_k)
   float* R;              // [m][pp][pp], pp: p rounded up to 16
@@ -29,6 +30,8 @@ struct OrthoArgs {
 constexpr int kOrthoRank = 128;
 constexpr int ortho_blocks(int p) { return (p + 15) / 16; }
 constexpr int ortho_tiles(int p) { return ortho_blocks(p) * (ortho_blocks(p) + 1) / 2; }
+// Waves that share a run of the long side in S_0, at B tile rows.
+constexpr int kOrthoShare(int B) { return B <= 2 ? 4 : (B <= 4 ? 2 : 1); }
 int ortho_splits(int64_t m, int64_t q);
 bool ortho_fits(int64_t m, int64_t q);
 // gt / ot: 0 fp32, 1 bf16, 2 fp16.

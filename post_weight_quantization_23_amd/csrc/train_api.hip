@@ -343,7 +343,7 @@ void take_ortho(Carve& ws, gptq::OrthoProblem& o, int64_t m, int64_t rows, int64
   o.q = o.tall ? rows : cols;
   o.splits = gptq::ortho_splits(m, o.q);
   const int64_t tiles = gptq::ortho_tiles(o.p), pp = 16 * gptq::ortho_blocks(o.p);
-  o.part = ws.take<double>(m * o.splits * tiles * 256);
+  o.part = ws.take<double>(m * o.splits * gptq::kOrthoShare(gptq::ortho_blocks(o.p)) * tiles * 256);
   o.inv = ws.take<double>(m);
   o.steps = ws.take<double>(m * steps * tiles * 256);
   o.R = ws.take<float>(m * pp * pp);
