@@ -78,16 +78,19 @@ struct Run {
 
 // ---------------------------------------------------------------- S_0
 // Parts of G G^T over the long side.  A wave holds tile rows i and B-1-i of the upper
-// half, B+1 tiles whatever i is, so a fragment of the run serves several products; with
-// fewer than four such pairs the waves share the run's values out among them.
+// half, B+1 tiles whatever i is, so a fragment of the run serves several products;
+// the waves with the same rows share the run's values out among them and
+// are added up through LDS in their order.
+constexpr int GRAM_THREADS = 512;
+
 template <int B, bool TALL>
 GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, float* lds) {
   using R = Run<B, TALL>;
-  constexpr int PAIRS = (B + 1) / 2, SHARE = kOrthoShare(B), TILES = ortho_tiles(16 * B), LD = (R::PER + 255) / 256;
+  constexpr int PAIRS = (B + 1) / 2, SHARE = GRAM_THREADS / 64 / PAIRS, TILES = ortho_tiles(16 * B);
+  constexpr int LD = (R::PER + GRAM_THREADS - 1) / GRAM_THREADS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
   const int pair = wave % PAIRS, share = wave / PAIRS, i0 = pair, i1 = B - 1 - pair;
-  const bool works = share < SHARE;
-  const int64_t each = ((o.q + o.splits - 1) / o.splits + KS - 1) / KS * KS, first = split * each, last = min(o.q, first + each);
+  const int64_t run = ((o.q + o.splits - 1) / o.splits + KS - 1) / KS * KS, first = split * run, last = min(o.q, first + run);
   doublex4 up[B], low[B];
 #pragma unroll
   for (int t = 0; t < B; ++t) up[t] = low[t] = doublex4{0, 0, 0, 0};
@@ -95,17 +98,17 @@ GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, floa
   auto fetch = [&](int64_t k0) {
 #pragma unroll
     for (int e = 0; e < LD; ++e)
-      if (threadIdx.x + 256 * e < R::PER) next[e] = R::fetch(o, type, mat, k0, threadIdx.x + 256 * e);
+      if (threadIdx.x + GRAM_THREADS * e < R::PER) next[e] = R::fetch(o, type, mat, k0, threadIdx.x + GRAM_THREADS * e);
   };
   if (first < last) fetch(first);
   for (int64_t k0 = first; k0 < last; k0 += KS) {
     __syncthreads();   // the last run has been read
 #pragma unroll
     for (int e = 0; e < LD; ++e)
-      if (threadIdx.x + 256 * e < R::PER) R::put(lds, R::GRAM, threadIdx.x + 256 * e, next[e]);
+      if (threadIdx.x + GRAM_THREADS * e < R::PER) R::put(lds, R::GRAM, threadIdx.x + GRAM_THREADS * e, next[e]);
     __syncthreads();
     if (k0 + KS < last) fetch(k0 + KS);
-    if (!works) continue;
+    if (share >= SHARE) continue;
     for (int k1 = 0; k1 < KS; k1 += 4 * SHARE) {
       const int k = k1 + 4 * share;
       const double a0 = R::get(lds, R::GRAM, 16 * i0 + r, k + h), a1 = R::get(lds, R::GRAM, 16 * i1 + r, k + h);
@@ -118,20 +121,30 @@ GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, floa
         }
     }
   }
-  if (!works) return;
-  double* part = o.part + ((mat * o.splits + split) * SHARE + share) * TILES * 256;
+  double* sum = reinterpret_cast<double*>(lds);
+  auto each = [&](auto&& f) {
 #pragma unroll
-  for (int t = 0; t < B; ++t)
+    for (int t = 0; t < B; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (t >= i0) part[tile_index(i0, t, B) * 256 + (4 * e + h) * 16 + r] = up[t][e];
-      if (t >= i1 && i1 != i0) part[tile_index(i1, t, B) * 256 + (4 * e + h) * 16 + r] = low[t][e];
-    }
+      for (int e = 0; e < 4; ++e) {
+        if (t >= i0) up[t][e] = f(up[t][e], tile_index(i0, t, B) * 256 + (4 * e + h) * 16 + r);
+        if (t >= i1 && i1 != i0) low[t][e] = f(low[t][e], tile_index(i1, t, B) * 256 + (4 * e + h) * 16 + r);
+      }
+  };
+  for (int w = 1; w < SHARE; ++w) {
+    __syncthreads();
+    if (share == w) each([&](double v, int at) { return sum[at] = v; });
+    __syncthreads();
+    if (share == 0) each([&](double v, int at) { return v + sum[at]; });
+  }
+  double* part = o.part + (mat * o.splits + split) * TILES * 256;
+  if (share == 0) each([&](double v, int at) { return part[at] = v; });
 }
 
 template <int B>
-__global__ __launch_bounds__(256) void gram_kernel(OrthoArgs a, int which, int type, int64_t blocks0) {
-  __shared__ __align__(16) float lds[Run<B, true>::FLOATS > Run<B, false>::FLOATS ? Run<B, true>::FLOATS : Run<B, false>::FLOATS];
+__global__ __launch_bounds__(GRAM_THREADS) void gram_kernel(OrthoArgs a, int which, int type, int64_t blocks0) {
+  constexpr int RUN = Run<B, true>::FLOATS > Run<B, false>::FLOATS ? Run<B, true>::FLOATS : Run<B, false>::FLOATS, SUM = 512 * ortho_tiles(16 * B);
+  __shared__ __align__(16) float lds[RUN > SUM ? RUN : SUM];
   int64_t b = blockIdx.x;
   if (b >= blocks0) b -= blocks0, which = 1;
   const OrthoProblem& o = a.p[which];
@@ -154,7 +167,6 @@ template <int B>
 struct Chain {
   static constexpr int TILES = B * (B + 1) / 2, WAVES = TILES < 16 ? TILES : 16, MOST = (TILES + WAVES - 1) / WAVES;
   static constexpr int THREADS = WAVES < 8 ? 512 : 64 * WAVES;   // all of them read the parts of S_0
-  static constexpr bool HOLDS = B <= 6;                          // a third matrix, the product of the steps so far
   int lane, wave, r, h;
   int ti[MOST], tj[MOST];
 
@@ -212,10 +224,10 @@ GPTQ_DEV void iterate(const OrthoArgs& a, const OrthoProblem& o, int64_t mat, do
   constexpr int N = C::TILES * 256, GROUPS = C::THREADS / N > 0 ? C::THREADS / N : 1;
   C c;
   c.set();
-  double *S = lds, *T = S + C::TILES * TSIZE, *R = C::HOLDS ? T + C::TILES * TSIZE : T;
+  double *S = lds, *T = S + C::TILES * TSIZE, *R = T + C::TILES * TSIZE;   // R: the product of the steps so far
   __shared__ double norm, sums[GROUPS > 1 ? GROUPS * N : 1];
   // the parts of S_0, in their order
-  const int parts = o.splits * kOrthoShare(B);
+  const int parts = o.splits;
   const double* part = o.part + mat * parts * N;
   for (int e = threadIdx.x; e < N * GROUPS; e += C::THREADS) {
     const int at = e % N, group = e / N, each = (parts + GROUPS - 1) / GROUPS, last = min(parts, (group + 1) * each);
@@ -248,23 +260,21 @@ GPTQ_DEV void iterate(const OrthoArgs& a, const OrthoProblem& o, int64_t mat, do
   for (int e = threadIdx.x; e < C::TILES * TSIZE; e += C::THREADS) S[e] = S[e] * by * by;
   __syncthreads();
   doublex4 acc[C::MOST], more[C::MOST];
-  double* steps = o.steps + mat * a.steps * N;
   for (int k = 0; k < a.steps; ++k) {
     c.product(S, S, acc);
     // q(S)
     c.each([&](int e, int g, int t, int i, int j) {
       const double v = a.c * acc[e][g] + a.b * S[t * TSIZE + i * TROW + j] + (c.ti[e] == c.tj[e] && i == j ? a.a : 0.0);
       T[t * TSIZE + i * TROW + j] = v;
-      if (C::HOLDS && k == 0) R[t * TSIZE + i * TROW + j] = v;
-      if (!C::HOLDS && k + 1 < a.steps) steps[(int64_t)k * N + t * 256 + i * 16 + j] = v;
+      if (k == 0) R[t * TSIZE + i * TROW + j] = v;
     });
     __syncthreads();
     const bool on = k + 1 < a.steps;
     if (on) c.product(S, T, acc);
-    if (C::HOLDS && k > 0) c.product(T, R, more);
+    if (k > 0) c.product(T, R, more);
     __syncthreads();
     if (on) c.write(S, acc);
-    if (C::HOLDS && k > 0) c.write(R, more);
+    if (k > 0) c.write(R, more);
     __syncthreads();
     if (!on) break;
     c.product(S, T, acc);
@@ -272,15 +282,6 @@ GPTQ_DEV void iterate(const OrthoArgs& a, const OrthoProblem& o, int64_t mat, do
     c.write(S, acc);
     __syncthreads();
   }
-  if constexpr (!C::HOLDS)   // T holds the last step's q: the earlier ones follow
-    for (int k = a.steps - 2; k >= 0; --k) {
-      for (int e = threadIdx.x; e < N; e += C::THREADS) S[e / 256 * TSIZE + e % 256 / 16 * TROW + e % 16] = steps[(int64_t)k * N + e];
-      __syncthreads();
-      c.product(T, S, acc);
-      __syncthreads();
-      c.write(T, acc);
-      __syncthreads();
-    }
   float* out = o.R + mat * (16 * B) * (16 * B);
   for (int e = threadIdx.x; e < 256 * B * B; e += C::THREADS) {
     const int i = e / (16 * B), j = e % (16 * B);
@@ -290,10 +291,155 @@ GPTQ_DEV void iterate(const OrthoArgs& a, const OrthoProblem& o, int64_t mat, do
 
 template <int B>
 __global__ __launch_bounds__(Chain<B>::THREADS) void chain_kernel(OrthoArgs a, int which) {
-  extern __shared__ __align__(16) double cs[];
+  __shared__ __align__(16) double cs[3 * Chain<B>::TILES * TSIZE];
   int64_t mat = blockIdx.x;
   if (mat >= a.m) mat -= a.m, which = 1;
   iterate<B>(a, a.p[which], mat, cs);
+}
+
+// ---------------------------------------------------------------- the iteration, over many CUs
+// Matrices of more than 64 rows: a launch for each product, a wave for each tile of its
+// upper half, operands and results (both halves) in memory.  One workgroup with its
+// matrix in LDS has the 64-bit products of one CU only: 254 us for 16 matrices of 128.
+// Both operands are symmetric, so each lane reads runs of one row of either, all of
+// them before the first product.
+struct WideArgs {
+  double a, b, c;
+  int64_t m;               // matrices of the first problem
+  int64_t size;            // values of a matrix's buffers
+  double* base[2];         // of either problem
+  struct {
+    int x, y, out;         // buffers: out = x y, or with `step` a + b x + c x x
+  } p[2];                  // p[1].out < 0: one product
+  bool step;
+  int last;                // the product whose result is the last R, -1: none
+  float* R[2];
+};
+enum { kS0, kS1, kT, kQ0, kQ1, kR0, kR1, kWideBuffers };   // ortho_wide's seven
+
+template <int B>
+__global__ __launch_bounds__(256) void wide_kernel(WideArgs a) {
+  constexpr int PP = 16 * B, TILES = ortho_tiles(PP);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
+  const int t = blockIdx.y * 4 + wave, which = blockIdx.z;
+  if (t >= TILES) return;
+  int ti, tj;
+  tile_of_index(t, B, ti, tj);
+  const int64_t mat = blockIdx.x;
+  const int side = mat >= a.m;
+  double* own = a.base[side] + (mat - (side ? a.m : 0)) * a.size;
+  const double* X = own + (int64_t)a.p[which].x * PP * PP + (16 * ti + r) * PP + h * 4 * B;   // contraction in the order h, k
+  const double* Y = own + (int64_t)a.p[which].y * PP * PP + (16 * tj + r) * PP + h * 4 * B;
+  double2 x[2 * B], y[2 * B];
+#pragma unroll
+  for (int k = 0; k < 2 * B; ++k) {
+    x[k] = *reinterpret_cast<const double2*>(X + 2 * k);
+    y[k] = *reinterpret_cast<const double2*>(Y + 2 * k);
+  }
+  double* out = own + (int64_t)a.p[which].out * PP * PP;
+  const double* S = own + (int64_t)a.p[which].x * PP * PP;
+  double at[4];
+  if (a.step)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) at[e] = S[(16 * ti + 4 * e + h) * PP + 16 * tj + r];
+  doublex4 acc[2] = {};
+#pragma unroll
+  for (int k = 0; k < 2 * B; ++k) {
+    acc[0] = mfma64(x[k].x, y[k].x, acc[0]);
+    acc[1] = mfma64(x[k].y, y[k].y, acc[1]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = 16 * ti + 4 * e + h, j = 16 * tj + r;
+    double v = acc[0][e] + acc[1][e];
+    if (a.step) v = a.c * v + a.b * at[e] + (i == j ? a.a : 0.0);
+    if (ti == tj && i > j) continue;   // of a tile on the diagonal one half stands for both
+    if (which == a.last) {
+      float* R = a.R[side] + (mat - (side ? a.m : 0)) * PP * PP;
+      R[i * PP + j] = R[j * PP + i] = (float)v;
+    } else {
+      out[i * PP + j] = out[j * PP + i] = v;
+    }
+  }
+}
+
+// S_0 / |G|^2 from its parts: a workgroup for each tile, each with the trace of all of them.
+template <int B>
+__global__ __launch_bounds__(256) void wide_start_kernel(OrthoArgs a, int which, WideArgs w) {
+  constexpr int PP = 16 * B, N = ortho_tiles(PP) * 256;
+  __shared__ double sums[4];
+  int64_t mat = blockIdx.x;
+  const int side = mat >= w.m;
+  if (side) mat -= w.m, which = 1;
+  const OrthoProblem& o = a.p[which];
+  const double* part = o.part + mat * o.splits * N;
+  const int tid = threadIdx.x, t = blockIdx.y;
+  auto sum = [&](int at) {
+    double v = 0;
+#pragma unroll 8
+    for (int s = 0; s < o.splits; ++s) v += part[(int64_t)s * N + at];
+    return v;
+  };
+  double v = tid < PP ? sum(tile_index(tid / 16, tid / 16, B) * 256 + tid % 16 * 17) : 0;
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+  if ((tid & 63) == 0) sums[tid >> 6] = v;
+  const double mine = sum(t * 256 + tid);
+  __syncthreads();
+  const double by = 1.0 / (sqrt(sums[0] + sums[1] + sums[2] + sums[3]) + a.eps);
+  if (t == 0 && tid == 0) o.inv[mat] = by;
+  int ti, tj;
+  tile_of_index(t, B, ti, tj);
+  double* S = w.base[side] + mat * w.size + (int64_t)kS0 * PP * PP;
+  const int i = 16 * ti + tid / 16, j = 16 * tj + tid % 16;
+  if (ti < tj || i <= j) S[i * PP + j] = S[j * PP + i] = mine * by * by;
+}
+
+template <int B>
+void wide(const OrthoArgs& a, int which, bool both, hipStream_t s) {
+  constexpr int PP = 16 * B, TILES = ortho_tiles(PP);
+  WideArgs w{};
+  w.a = a.a;
+  w.b = a.b;
+  w.c = a.c;
+  w.m = a.m;
+  w.size = (int64_t)kWideBuffers * PP * PP;
+  for (int k = 0; k <= (both ? 1 : 0); ++k) {
+    w.base[k] = a.p[which + k].wide;
+    w.R[k] = a.p[which + k].R;
+  }
+  const int64_t mats = both ? 2 * a.m : a.m;
+  hipLaunchKernelGGL(wide_start_kernel<B>, dim3((unsigned)mats, TILES), dim3(256), 0, s, a, which, w);
+  auto launch = [&](int products) {
+    hipLaunchKernelGGL(wide_kernel<B>, dim3((unsigned)mats, (TILES + 3) / 4, products), dim3(256), 0, s, w);
+  };
+  int S = kS0, R = -1;
+  for (int k = 0; k < a.steps; ++k) {
+    const bool on = k + 1 < a.steps;
+    const int Q = k % 2 ? kQ1 : kQ0, S1 = S == kS0 ? kS1 : kS0;
+    w.step = true;
+    w.last = on || k > 0 ? -1 : 0;
+    w.p[0] = {S, S, Q};
+    launch(1);
+    w.step = false;
+    w.last = -1;
+    int n = 0;
+    if (on) w.p[n++] = {S, Q, kT};
+    if (k > 0) {
+      const int R1 = R == kR0 ? kR1 : kR0;
+      if (!on) w.last = n;
+      w.p[n++] = {Q, R, R1};
+      R = R1;
+    } else {
+      R = Q;
+    }
+    if (n > 0) launch(n);
+    w.last = -1;
+    if (!on) break;
+    w.p[0] = {kT, Q, S1};
+    launch(1);
+    S = S1;
+  }
 }
 
 // ---------------------------------------------------------------- result
@@ -303,12 +449,9 @@ __global__ __launch_bounds__(Chain<B>::THREADS) void chain_kernel(OrthoArgs a, i
 // holds it.
 GPTQ_DEV floatx4 mfma_f32(float a, float b, floatx4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
-template <int OT>
-GPTQ_DEV void store_value(void* p, int64_t at, float v) { store_out<OT>(p, at, v); }
-
 template <int B>
 struct Apply {
-  static constexpr int SETS = B >= 5 ? 1 : (B >= 3 ? 2 : (B == 2 ? 4 : 4)), THREADS = 64 * B * SETS;
+  static constexpr int SETS = B >= 5 ? 1 : 2, THREADS = 64 * B * SETS;
 };
 
 template <int B, bool TALL, int OT>
@@ -340,19 +483,23 @@ GPTQ_DEV void apply(const OrthoProblem& o, int gt, int64_t mat, int64_t first, i
       }
     __syncthreads();
     if (k0 + KS < last) fetch(k0 + KS);
-    for (int at = 16 * set; at < KS; at += 16 * SETS) {
-      floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int at = 32 * set; at < KS; at += 32 * SETS) {   // two sets of 16 at a time
+      floatx4 acc[2] = {};
 #pragma unroll
-      for (int k = 0; k < 4 * B; ++k) {
-        const float m0 = R::get(lds, R::APPLY, 4 * k + h, at + r);
-        acc = TALL ? mfma_f32(m0, w[k], acc) : mfma_f32(w[k], m0, acc);
-      }
+      for (int k = 0; k < 4 * B; ++k)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int s = TALL ? 16 * row + r : 16 * row + 4 * h + e;        // place on the shorter side
-        const int64_t l = k0 + at + (TALL ? 4 * h + e : r);              // on the longer one
-        if (s < o.p && l < o.q) store_value<OT>(o.out, mat * o.rows * o.cols + (TALL ? l * o.p + s : s * o.q + l), acc[e]);
-      }
+        for (int q = 0; q < 2; ++q) {
+          const float m0 = R::get(lds, R::APPLY, 4 * k + h, at + 16 * q + r);
+          acc[q] = TALL ? mfma_f32(m0, w[k], acc[q]) : mfma_f32(w[k], m0, acc[q]);
+        }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int s = TALL ? 16 * row + r : 16 * row + 4 * h + e;               // place on the shorter side
+          const int64_t l = k0 + at + 16 * q + (TALL ? 4 * h + e : r);            // on the longer one
+          if (s < o.p && l < o.q) store_out<OT>(o.out, mat * o.rows * o.cols + (TALL ? l * o.p + s : s * o.q + l), acc[q][e]);
+        }
     }
   }
 }
@@ -372,12 +519,6 @@ __global__ __launch_bounds__(Apply<B>::THREADS) void apply_kernel(OrthoArgs a, i
 // One launch of each kernel for the problems of B tile rows: `which` and, if both, the other.
 template <int B>
 void orthogonalize(const OrthoArgs& a, int which, bool both, int gt, int ot, hipStream_t s) {
-  constexpr int LDS = (Chain<B>::HOLDS ? 3 : 2) * Chain<B>::TILES * TSIZE * 8;
-  static const bool set = [] {
-    (void)hipFuncSetAttribute((const void*)chain_kernel<B>, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
-    return true;
-  }();
-  (void)set;
   // runs of a workgroup: four where that leaves two workgroups for each CU
   int64_t all = 0;
   for (int w = which; w <= (both ? 1 : which); ++w) all += a.m * ((a.p[w].q + KS - 1) / KS);
@@ -387,8 +528,9 @@ void orthogonalize(const OrthoArgs& a, int which, bool both, int gt, int ot, hip
     gram[w - which] = a.m * a.p[w].splits;
     apply[w - which] = a.m * ((a.p[w].q + (int64_t)KS * runs - 1) / ((int64_t)KS * runs));
   }
-  hipLaunchKernelGGL(gram_kernel<B>, dim3((unsigned)(gram[0] + gram[1])), dim3(256), 0, s, a, which, gt, gram[0]);
-  hipLaunchKernelGGL(chain_kernel<B>, dim3((unsigned)(both ? 2 * a.m : a.m)), dim3(Chain<B>::THREADS), LDS, s, a, which);
+  hipLaunchKernelGGL(gram_kernel<B>, dim3((unsigned)(gram[0] + gram[1])), dim3(GRAM_THREADS), 0, s, a, which, gt, gram[0]);
+  if constexpr (B > kOrthoNarrow) wide<B>(a, which, both, s);
+  else hipLaunchKernelGGL(chain_kernel<B>, dim3((unsigned)(both ? 2 * a.m : a.m)), dim3(Chain<B>::THREADS), 0, s, a, which);
   const dim3 grid((unsigned)(apply[0] + apply[1])), block(Apply<B>::THREADS);
   if (ot == 0) hipLaunchKernelGGL((apply_kernel<B, 0>), grid, block, 0, s, a, which, gt, apply[0], runs);
   else if (ot == kBF16) hipLaunchKernelGGL((apply_kernel<B, kBF16>), grid, block, 0, s, a, which, gt, apply[0], runs);
@@ -429,6 +571,6 @@ int ortho_splits(int64_t m, int64_t q) {
   return (int)((runs + each - 1) / each);
 }
 
-bool ortho_fits(int64_t m, int64_t q) { return grid_fits(2 * m * ((q + KS - 1) / KS), 512) && grid_fits(2 * m, 1024) && grid_fits(2 * m * 32, 256); }
+bool ortho_fits(int64_t m, int64_t q) { return grid_fits(2 * m * ((q + KS - 1) / KS), 512) && grid_fits(2 * m, 1024) && grid_fits(2 * m * 32, 512); }
 
 }  // namespace gptq

@@ -16,9 +16,9 @@ struct OrthoProblem {
   bool tall;
   int splits;            // parts of q in S_0
   bool vec;              // set by the launch: four values of a row start on their multiple
-  double* part;          // [m][splits][kOrthoShare][tiles][256]
+  double* part;          // [m][splits][tiles][256]
   double* inv;           // [m]: 1 / (|G|_F + eps)
-  double* steps;         // [m][count][tiles][256]: q(S_k)
+  double* wide;          // [m][ortho_wide]
   float* R;              // [m][pp][pp], pp: p rounded up to 16
 };
 struct OrthoArgs {
@@ -30,8 +30,12 @@ struct OrthoArgs {
 constexpr int kOrthoRank = 128;
 constexpr int ortho_blocks(int p) { return (p + 15) / 16; }
 constexpr int ortho_tiles(int p) { return ortho_blocks(p) * (ortho_blocks(p) + 1) / 2; }
-// Waves that share a run of the long side in S_0, at B tile rows.
-constexpr int kOrthoShare(int B) { return B <= 2 ? 4 : (B <= 4 ? 2 : 1); }
+constexpr int kOrthoNarrow = 4;   // tile rows up to which a workgroup iterates on its own
+// fp64 values of a matrix's buffers in memory, for the iteration over many CUs.
+inline int64_t ortho_wide(int p) {
+  const int64_t pp = 16 * ortho_blocks(p);
+  return ortho_blocks(p) > kOrthoNarrow ? 7 * pp * pp : 0;
+}
 int ortho_splits(int64_t m, int64_t q);
 bool ortho_fits(int64_t m, int64_t q);
 // gt / ot: 0 fp32, 1 bf16, 2 fp16.

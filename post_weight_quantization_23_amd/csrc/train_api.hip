@@ -335,7 +335,7 @@ gptq_status check_ortho_sizes(const char* fn, int64_t m, int64_t rank, int64_t c
 }
 
 // The problem of m matrices of rows x cols.
-void take_ortho(Carve& ws, gptq::OrthoProblem& o, int64_t m, int64_t rows, int64_t cols, int steps) {
+void take_ortho(Carve& ws, gptq::OrthoProblem& o, int64_t m, int64_t rows, int64_t cols) {
   o.rows = rows;
   o.cols = cols;
   o.tall = rows > cols;
@@ -343,9 +343,9 @@ void take_ortho(Carve& ws, gptq::OrthoProblem& o, int64_t m, int64_t rows, int64
   o.q = o.tall ? rows : cols;
   o.splits = gptq::ortho_splits(m, o.q);
   const int64_t tiles = gptq::ortho_tiles(o.p), pp = 16 * gptq::ortho_blocks(o.p);
-  o.part = ws.take<double>(m * o.splits * gptq::kOrthoShare(gptq::ortho_blocks(o.p)) * tiles * 256);
+  o.part = ws.take<double>(m * o.splits * tiles * 256);
   o.inv = ws.take<double>(m);
-  o.steps = ws.take<double>(m * steps * tiles * 256);
+  o.wide = ws.take<double>(m * gptq::ortho_wide(o.p));
   o.R = ws.take<float>(m * pp * pp);
 }
 
@@ -357,8 +357,8 @@ gptq_status gptq_adapter_orthogonalize_workspace_size(int64_t m, int64_t rank, i
   if (gptq_status st = check_ortho_sizes(fn, m, rank, c, r, steps)) return st;
   Carve ws{nullptr, 0};
   gptq::OrthoProblem o{};
-  if (c > 0) take_ortho(ws, o, m, rank, c, steps);
-  if (r > 0) take_ortho(ws, o, m, r, rank, steps);
+  if (c > 0) take_ortho(ws, o, m, rank, c);
+  if (r > 0) take_ortho(ws, o, m, r, rank);
   *bytes = (size_t)ws.used;
   return ok();
 }
@@ -393,13 +393,13 @@ gptq_status gptq_adapter_orthogonalize(const void* G_A, const void* G_B, gptq_dt
       gptq::OrthoProblem& o = args.p[at++];
       o.G = G_A;
       o.out = out_A;
-      take_ortho(carve, o, m, rank, c, steps);
+      take_ortho(carve, o, m, rank, c);
     }
     if (G_B) {
       gptq::OrthoProblem& o = args.p[at++];
       o.G = G_B;
       o.out = out_B;
-      take_ortho(carve, o, m, r, rank, steps);
+      take_ortho(carve, o, m, r, rank);
     }
     if (pass == 0)
       if (gptq_status st = need_ws(fn, ws, ws_bytes, carve.used)) return st;
