@@ -106,7 +106,7 @@ GPTQ_DEV float2 join_sums(float2 a, float2 b) {
 __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a, int tiles, float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ float2 sums[16][17];
   const int tok = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int64_t p = (int64_t)blockIdx.x * 16 + tok, count = *a.k.count;
+  const int64_t p = (int64_t)blockIdx.x * 16 + tok, count = a.target ? a.n : *a.k.count;
   float2 v = {-INFINITY, 0.f};
   if (p < count)
     for (int i = part; i < tiles; i += 16) v = join_sums(v, a.part[(int64_t)i * a.n + p]);
@@ -115,9 +115,10 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a, int tiles, f
   if (part != 0 || p >= count) return;
   for (int i = 1; i < 16; ++i) v = join_sums(v, sums[i][tok]);
   const float all = v.x + logf(v.y);
-  const int64_t t = a.k.token[p];
-  lse[t] = all;
-  loss[t] = all - a.at_target[p];
+  const bool none = a.target && (uint64_t)a.target[p] >= (uint64_t)a.vocab;
+  const int64_t t = a.target ? p : a.k.token[p];
+  lse[t] = none ? 0.f : all;
+  loss[t] = none ? 0.f : all - a.at_target[p];
 }
 
 // ---------------------------------------------------------------- input gradient
@@ -151,7 +152,7 @@ void launch_gather_kept(GatherArgs a, hipStream_t s) {
 }
 
 void launch_loss_join(const LossArgs& a, float* loss, float* lse, hipStream_t s) {
-  hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)((a.n + 15) / 16)), dim3(256), 0, s, a, (int)loss_tiles(a.vocab), loss, lse);
+  hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)((a.n + 15) / 16)), dim3(256), 0, s, a, (int)loss_tiles(a.n, a.vocab), loss, lse);
 }
 
 void launch_join_x(const GradXArgs& a, int dt, hipStream_t s) {

@@ -5,7 +5,14 @@
 
 namespace gptq {
 
-constexpr int kLossTile = 256;   // vocabulary entries of a tile of logits
+// Vocabulary entries of a tile of logits: its part of a token's sums.
+constexpr int64_t kLossTile = 256, kFewTile = 128;
+// Up to as many tokens the largest tiles hold them all, and leaving tokens out
+// saves no work: they are taken as they lie (forward).
+constexpr int64_t kFewTokens = 256;
+// ... and up to as many tiles are of kFewTile entries.
+constexpr int64_t kFewEntries = 128;
+inline int64_t loss_tile(int64_t n) { return n <= kFewEntries ? kFewTile : kLossTile; }
 
 // The tokens that have a target, in order: place p is token token[p] with target
 // col[p]; place_of[t] is token t's place or -1.  count: how many there are.
@@ -43,12 +50,14 @@ struct GatherArgs {
 };
 void launch_gather_kept(GatherArgs a, hipStream_t s);
 
-// Logits of every kept token in tiles of kLossTile entries: of each tile the
+// Logits of every kept token in tiles of loss_tile(n) entries: of each tile the
 // largest and the sum of exponentials against it, and the target's logit.
 struct LossArgs {
   const uint16_t* W;
-  int64_t ldw, vocab, n, d, kp;
-  const uint16_t* rows;    // [n][kp]
+  int64_t ldw, vocab, n, d;
+  const uint16_t* rows;    // [n][ldr], zero past d up to a whole step, or d itself a whole number of them
+  int64_t ldr;
+  const int64_t* target;   // not null: all n tokens as they lie, k unused (forward)
   Kept k;
   float2* part;            // [tiles][n]
   float* at_target;        // [n]
@@ -95,7 +104,9 @@ void launch_grad_w(const GradWArgs& a, int dt, hipStream_t s);
 int grad_x_splits(int64_t n, int64_t d, int64_t width);
 // Entries of a piece.
 int64_t loss_piece(int64_t n, int64_t vocab);
-inline int64_t loss_tiles(int64_t vocab) { return (vocab + kLossTile - 1) / kLossTile; }
+inline int64_t loss_tiles(int64_t n, int64_t vocab) { return (vocab + loss_tile(n) - 1) / loss_tile(n); }
+// Whether rows of X can be taken as they lie.
+bool loss_takes(const void* X, int64_t n, int64_t d, int64_t ldx);
 bool loss_fits(int64_t n, int64_t vocab, int64_t d, bool grad);
 
 }  // namespace gptq

@@ -175,14 +175,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
   extern __shared__ __align__(16) unsigned char lsm[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31;
   const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
-  const int64_t count = *a.k.count;
+  const int64_t count = !GRAD && a.target ? a.n : *a.k.count;
   int tt, vt;
   tile_of(blockIdx.x, tok_tiles, voc_tiles, tt, vt);
   const int64_t t0 = (int64_t)tt * P::TN, v0 = (int64_t)vt * P::TM;
   if (t0 >= count) return;
-  const Source w{a.W + a.v0 * a.ldw, a.ldw, a.width, a.d}, x{a.rows, a.kp, count, a.kp};
+  const int64_t steps = (a.d + LK - 1) / LK;
+  const Source w{a.W + a.v0 * a.ldw, a.ldw, a.width, a.d}, x{a.rows, a.ldr, count, steps * LK};
   floatx16 acc[MT][NT];
-  P::run(w, x, v0, t0, 0, a.kp / LK, lsm, acc);
+  P::run(w, x, v0, t0, 0, steps, lsm, acc);
   const int last = (int)min(a.width - v0, (int64_t)P::TM);   // entries of this tile
   int row[MT][16];
 #pragma unroll
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
       const int64_t p = t0 + wn + 32 * q + m;
-      const int64_t y = p < count ? (int64_t)a.k.col[p] - v0 : -1;   // entry of the tile
+      const int64_t y = p < count ? (a.target ? a.target[p] : (int64_t)a.k.col[p]) - v0 : -1;   // entry of the tile
       if (last < P::TM) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (row[i][e] == (int)y) z = acc[i][q][e], mine = true;
+            if (row[i][e] == y) z = acc[i][q][e], mine = true;
         if (mine && y < last) a.at_target[p] = z;
       }
       float top = -INFINITY;
@@ -379,7 +380,6 @@ void logits(const LossArgs& a, hipStream_t s) {
   using P = Product<DT, false, false, MT, NT, WM, WN>;
   static const bool set = (allow_lds(logits_kernel<DT, GRAD, MT, NT, WM, WN>, 2 * P::BUF), true);
   (void)set;
-  static_assert(P::TM == kLossTile, "partial sums are per tile of kLossTile entries");
   const int tt = (int)tiles_of(a.n, P::TN), vt = (int)tiles_of(a.width, P::TM);
   hipLaunchKernelGGL((logits_kernel<DT, GRAD, MT, NT, WM, WN>), dim3((unsigned)((int64_t)tt * vt)), dim3(64 * WM * WN), 2 * P::BUF, s,
                      a, tt, vt);
@@ -387,9 +387,11 @@ void logits(const LossArgs& a, hipStream_t s) {
 
 template <int DT, bool GRAD>
 void logits_shape(const LossArgs& a, hipStream_t s) {
+  static_assert(kFewEntries == 128 && kFewTile == 128 && kLossTile == 256, "tiles of loss_tile(n) entries");
   if (a.n > 128) logits<DT, GRAD, 4, 2, 2, 4>(a, s);
-  else if (a.n > 64) logits<DT, GRAD, 2, 2, 4, 2>(a, s);
-  else logits<DT, GRAD, 2, 2, 4, 1>(a, s);
+  else if (a.n > 64) logits<DT, GRAD, 2, 2, 2, 2>(a, s);
+  else if (a.n > 32) logits<DT, GRAD, 1, 2, 4, 1>(a, s);
+  else logits<DT, GRAD, 1, 1, 4, 1>(a, s);
 }
 
 template <int DT, int MT, int NT, int WM, int WN>
@@ -446,13 +448,17 @@ int64_t loss_piece(int64_t n, int64_t vocab) {
   return vocab <= most ? vocab : (most > kLossTile ? most : kLossTile);
 }
 
+bool loss_takes(const void* X, int64_t n, int64_t d, int64_t ldx) {
+  return n <= kFewTokens && reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0 && ldx < (int64_t(1) << 22) && d % LK == 0;
+}
+
 bool loss_fits(int64_t n, int64_t vocab, int64_t d, bool grad) {
-  const int64_t shortest = n > 128 ? 256 : (n > 64 ? 128 : 64);
-  if (!grid_fits(tiles_of(n, shortest) * loss_tiles(vocab), 512)) return false;
+  const int64_t shortest = n > 128 ? 256 : (n > 64 ? 128 : (n > 32 ? 64 : 32));
+  if (!grid_fits(tiles_of(n, shortest) * loss_tiles(n, vocab), 512)) return false;
   if (!grid_fits(tiles_of(n * (gemm16_depth(d) / 8), 256), 256)) return false;
   if (!grad) return true;
   const int64_t tile = n > 128 ? 256 : 128;
-  return grid_fits(tiles_of(n, tile) * tiles_of(d, tile) * 16, 512) && grid_fits(loss_tiles(vocab) * tiles_of(d, 256), 512);
+  return grid_fits(tiles_of(n, tile) * tiles_of(d, tile) * 16, 512) && grid_fits(tiles_of(vocab, 256) * tiles_of(d, 256), 512);
 }
 
 }  // namespace gptq

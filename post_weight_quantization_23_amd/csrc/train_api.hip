@@ -108,7 +108,7 @@ LossBuffers take_loss(Carve& c, int64_t n, int64_t d, int64_t vocab) {
   LossBuffers b;
   b.k = take_kept(c, n, false);
   b.rows = c.take<uint16_t>(n * gptq::gemm16_depth(d));
-  b.part = c.take<float2>(n * gptq::loss_tiles(vocab));
+  b.part = c.take<float2>(n * gptq::loss_tiles(n, vocab));
   b.at_target = c.take<float>(n);
   return b;
 }
@@ -168,34 +168,40 @@ gptq_status gptq_linear_cross_entropy(const void* X, gptq_dtype xt, int64_t n, i
   const LossBuffers b = take_loss(c, n, d, vocab);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int dt = xt == GPTQ_BF16 ? gptq::kBF16 : gptq::kF16;
-  gptq::KeepArgs k{};
-  k.target = target;
-  k.n = n;
-  k.vocab = vocab;
-  k.loss = loss;
-  k.lse = lse;
-  k.k = b.k;
-  gptq::launch_keep(k, s);
-  gptq::GatherArgs g{};
-  g.X = static_cast<const uint16_t*>(X);
-  g.n = n;
-  g.d = d;
-  g.ldx = ldx;
-  g.kp = gptq::gemm16_depth(d);
-  g.k = b.k;
-  g.rows = b.rows;
-  gptq::launch_gather_kept(g, s);
   gptq::LossArgs l{};
   l.W = static_cast<const uint16_t*>(W);
   l.ldw = ldw;
   l.vocab = l.width = vocab;
   l.n = n;
   l.d = d;
-  l.kp = g.kp;
-  l.rows = b.rows;
-  l.k = b.k;
   l.part = b.part;
   l.at_target = b.at_target;
+  if (gptq::loss_takes(X, n, d, ldx)) {
+    l.rows = static_cast<const uint16_t*>(X);
+    l.ldr = ldx;
+    l.target = target;
+  } else {
+    gptq::KeepArgs k{};
+    k.target = target;
+    k.n = n;
+    k.vocab = vocab;
+    k.loss = loss;
+    k.lse = lse;
+    k.k = b.k;
+    gptq::launch_keep(k, s);
+    gptq::GatherArgs g{};
+    g.X = static_cast<const uint16_t*>(X);
+    g.n = n;
+    g.d = d;
+    g.ldx = ldx;
+    g.kp = gptq::gemm16_depth(d);
+    g.k = b.k;
+    g.rows = b.rows;
+    gptq::launch_gather_kept(g, s);
+    l.rows = b.rows;
+    l.ldr = g.kp;
+    l.k = b.k;
+  }
   gptq::launch_logits(l, dt, false, s);
   gptq::launch_loss_join(l, loss, lse, s);
   return check_launch(fn);
@@ -264,8 +270,8 @@ gptq_status gptq_linear_cross_entropy_backward(const void* X, gptq_dtype xt, int
   l.vocab = vocab;
   l.n = n;
   l.d = d;
-  l.kp = kp;
   l.rows = b.rows;
+  l.ldr = kp;
   l.k = b.k;
   l.P = b.P;
   l.W = static_cast<const uint16_t*>(W);
