@@ -118,7 +118,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a, int tiles, f
   const bool none = a.target && (uint64_t)a.target[p] >= (uint64_t)a.vocab;
   const int64_t t = a.target ? p : a.k.token[p];
   lse[t] = none ? 0.f : all;
-  loss[t] = none ? 0.f : all - a.at_target[p];
+  loss[t] = none ? 0.f : (v.x - a.at_target[p]) + logf(v.y);   // not lse - z: lse is rounded at its size
 }
 
 // ---------------------------------------------------------------- input gradient

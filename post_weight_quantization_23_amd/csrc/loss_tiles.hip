@@ -13,6 +13,7 @@ namespace {
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
 constexpr int LK = 64;   // contraction step
 constexpr float kLog2e = 1.4426950408889634f;
@@ -63,15 +64,15 @@ struct Operand {
 
   // Values k0 .. k0 + LK - 1 to LDS; what does not exist reads as zero.
   GPTQ_DEV void load(lds_u8* to, int64_t k0, int wave, int lane) const {
-    const int ks = (int)min(depth - k0, (int64_t)LK);
+    const int ks = (int)max((int64_t)0, min(depth - k0, (int64_t)LK));   // none past the end
     if constexpr (ACROSS) {
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(base + k0 * ld), (short)0, (int)(((ks - 1) * ld + min(left, (int)ld)) * 2), 0x00020000);
+          (void*)(base + k0 * ld), (short)0, ks > 0 ? (int)(((ks - 1) * ld + min(left, (int)ld)) * 2) : 0, 0x00020000);
 #pragma unroll
       for (int q = 0; q < Q; ++q) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to + (wave * Q + q) * 1024, 16, off[q], 0, 0, 0);
     } else {
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(base + k0), (short)0, (int)(((left - 1) * ld + ks) * 2), 0x00020000);
+          (void*)(base + k0), (short)0, ks > 0 ? (int)(((left - 1) * ld + ks) * 2) : 0, 0x00020000);
       if (ks == LK) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to + (wave * Q + q) * 1024, 16, off[q], 0, 0, 0);
@@ -86,32 +87,77 @@ struct Operand {
     }
   }
 
-  // Values 16 k + 8 h .. + 7 of entry f0 + (lane & 31).
-  static GPTQ_DEV u32x4 read(const unsigned char* from, int f0, int k, int lane) {
-    const int h = lane >> 5;
-    if constexpr (ACROSS) {
-      const int i = lane & 15, g = (f0 >> 4) + ((lane >> 4) & 1), k0 = 16 * k + 8 * h + (i >> 2);
-      uint2 v[2];
+  // Addresses of the fragments of 32 entries each from f0 on (a multiple of 32; of 32 COUNT
+  // where COUNT is a power of two).  Both places are exclusive ors of
+  // bits of their own, so what changes with the step's values k and
+  // the set i is a constant offset beside few registers:
+  //   along   f * 128 + ((2 k + h) ^ swz(f)) * 16: one for each k, 32 entries 4096 bytes apart
+  //           (their odd sets exclusive or 64, which is another k's)
+  //   across  one for each set, k values 32 E bytes apart
+  template <int COUNT>
+  struct Fragments {
+    static constexpr int REGS = ACROSS ? COUNT : LK / 16, READS = ACROSS ? 2 * COUNT : COUNT;
+    uint32_t at[REGS];
+
+    GPTQ_DEV void set(const lds_u8* from, int f0, int lane) {
+      const uint32_t base = (uint32_t)(uintptr_t)from;
+      const int h = lane >> 5;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int kk = k0 + 4 * e;
-        const unsigned char* at = from + kk * (2 * E) + ((g ^ turn<E>(kk)) << 5) + (i & 3) * 8;
-        v[e] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
+      for (int r = 0; r < REGS; ++r) {
+        if constexpr (ACROSS) {
+          const int i = lane & 15, g = ((f0 + 32 * r) >> 4) + ((lane >> 4) & 1), k = 8 * h + (i >> 2);
+          at[r] = base + k * (2 * E) + ((g ^ turn<E>(k)) << 5) + (i & 3) * 8;
+        } else {
+          const int f = f0 + (lane & 31);
+          at[r] = base + f * (2 * LK) + (((2 * r + h) ^ swz(f)) << 4);
+        }
       }
-      return u32x4{v[0].x, v[0].y, v[1].x, v[1].y};
-    } else {
-      const int f = f0 + (lane & 31);
-      return *reinterpret_cast<const u32x4*>(from + f * (2 * LK) + (((2 * k + h) ^ swz(f)) << 4));
     }
-  }
+    GPTQ_DEV void move(int by) {
+#pragma unroll
+      for (int r = 0; r < REGS; ++r) at[r] += by;
+    }
+    // Values 16 k + 8 h .. + 7 of entry f0 + 32 i + (lane & 31).
+    GPTQ_DEV void read(int k, u32x4 (&v)[COUNT]) const {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) {
+        if constexpr (ACROSS) {
+          const uint32_t p = at[i] + 32 * E * k;
+          const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)p));
+          const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(p + 8 * E)));
+          v[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
+        } else {
+          v[i] = *(const lds_u32x4*)(uintptr_t)(at[(k ^ (2 * (i & 1)))] + 32 * 2 * LK * i);
+        }
+      }
+    }
+  };
 };
 
-// acc = A B^T of steps first .. last - 1.
+// One step of the schedule below for each of READS reads of LDS: the read, then its share of
+// PRODUCTS matrix products.
+template <int READS, int PRODUCTS, int AT = 0>
+GPTQ_DEV void spread() {
+  if constexpr (AT < READS) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    constexpr int SHARE = PRODUCTS * (AT + 1) / READS - PRODUCTS * AT / READS;
+    if constexpr (SHARE > 0) __builtin_amdgcn_sched_group_barrier(0x8, SHARE, 0);
+    spread<READS, PRODUCTS, AT + 1>();
+  }
+}
+
+// acc = A B^T of steps first .. last - 1.  Fragments are read from LDS 16 values of
+// the contraction ahead of their products, also over the end of a step: the barrier stands before
+// the last 16 values' products, when their fragments are in registers, so that the
+// step's buffer takes the step after the next while they run.
 template <int DT, bool TA, bool TB, int MT, int NT, int WM, int WN>
 struct Product {
   static constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN, NW = WM * WN, BUF = (TM + TN) * LK * 2;
   typedef Operand<TA, TM, NW> OpA;
   typedef Operand<TB, TN, NW> OpB;
+  typedef typename OpA::template Fragments<MT> FragA;
+  typedef typename OpB::template Fragments<NT> FragB;
+  static constexpr int READS = FragA::READS + FragB::READS;
 
   static GPTQ_DEV void run(const Source& a, const Source& b, int64_t a0, int64_t b0, int64_t first, int64_t last,
                            unsigned char* smem, floatx16 (&acc)[MT][NT]) {
@@ -132,30 +178,54 @@ struct Product {
       oa.load(to, s * LK, wave, lane);
       ob.load(to + OpA::BYTES, s * LK, wave, lane);
     };
+    FragA fa;
+    FragB fb;
+    fa.set(lbase + (first & 1) * BUF, wm, lane);
+    fb.set(lbase + (first & 1) * BUF + OpA::BYTES, wn, lane);
+    u32x4 x[2][MT], y[2][NT];
+    auto read = [&](int set, int k) {
+      fa.read(k, x[set]);
+      fb.read(k, y[set]);
+    };
+    auto multiply = [&](int set) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[i][q] = mfma32<DT>(x[set][i], y[set][q], acc[i][q]);
+    };
     load(first);
-    for (int64_t s = first; s < last; ++s) {
-      // own loads have landed; with every wave here, the other buffer is free
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    load(first + 1);
+    read(0, 0);
+    auto most = [&]() {   // a step but for its last 16 values
+#pragma unroll
+      for (int k = 0; k < LK / 16 - 1; ++k) {
+        read((k + 1) & 1, k + 1);
+        multiply(k & 1);
+        spread<READS, MT * NT>();
+      }
+    };
+    for (int64_t s = first; s + 1 < last; ++s) {
+      most();
+      // the next step's loads have landed and this one's buffer has been read, by every wave
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
-      if (s + 1 < last) load(s + 1);
-      const unsigned char* ab = smem + (s & 1) * BUF;
-      const unsigned char* bb = ab + OpA::BYTES;
-#pragma unroll
-      for (int k = 0; k < LK / 16; ++k) {
-        u32x4 x[MT], y[NT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) x[i] = OpA::read(ab, wm + 32 * i, k, lane);
-#pragma unroll
-        for (int q = 0; q < NT; ++q) y[q] = OpB::read(bb, wn + 32 * q, k, lane);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int q = 0; q < NT; ++q) acc[i][q] = mfma32<DT>(x[i], y[q], acc[i][q]);
-      }
+      load(s + 2);
+      const int by = s & 1 ? -BUF : BUF;
+      fa.move(by);
+      fb.move(by);
+      read(0, 0);
+      multiply(1);
+      spread<READS, MT * NT>();
     }
+    most();
+    multiply(1);
+    __builtin_amdgcn_s_waitcnt(0);   // what was loaded past the last step
     __syncthreads();   // the last step's operands have been read
   }
 };
+static_assert(LK / 16 % 2 == 0, "a step's last fragments are in set 1");
 
 // ---------------------------------------------------------------- softmax statistics
 // The largest of two sets of values and the sum of exponentials against it.  A set
@@ -185,11 +255,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
   floatx16 acc[MT][NT];
   P::run(w, x, v0, t0, 0, steps, lsm, acc);
   const int last = (int)min(a.width - v0, (int64_t)P::TM);   // entries of this tile
-  int row[MT][16];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) row[i][e] = wm + 32 * i + TileShape<floatx16>::acc_row(lane, e);
+  // entry of a lane's value: lowest + 32 i + within(e)
+  const int lowest = wm + 4 * (lane >> 5);
+  constexpr auto within = [](int e) { return 8 * (e >> 2) + (e & 3); };
 
   if constexpr (!GRAD) {
     float2* part = reinterpret_cast<float2*>(lsm);   // [WM][TN]
@@ -202,17 +270,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (row[i][e] >= last) acc[i][q][e] = -INFINITY;
+            if (32 * i + within(e) >= last - lowest) acc[i][q][e] = -INFINITY;
       }
       if (__any(y >= wm && y < wm + 32 * MT)) {
+        const int own = (int)y - lowest;   // in range where it counts
         float z = 0.f;
         bool mine = false;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (row[i][e] == y) z = acc[i][q][e], mine = true;
-        if (mine && y < last) a.at_target[p] = z;
+            if (32 * i + within(e) == own) z = acc[i][q][e], mine = true;
+        if (mine && y >= 0 && y < last) a.at_target[p] = z;
       }
       float top = -INFINITY;
 #pragma unroll
@@ -245,6 +314,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
     for (int q = 0; q < NT; ++q) {
       const int64_t p = t0 + wn + 32 * q + m;
       const int64_t y = p < count ? (int64_t)a.k.col[p] - a.v0 - v0 : -1;
+      const int own_row = (int)y - lowest;
       const float lse = p < count ? a.k.lse[p] : 0.f, g = p < count ? a.k.grad[p] : 0.f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -253,12 +323,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
           float v[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            const int at = row[i][e + f];
+            const int at = 32 * i + within(e + f);
             v[f] = __builtin_amdgcn_exp2f((acc[i][q][e + f] - lse) * kLog2e);
-            if (at == (int)y) v[f] -= 1.f;
-            v[f] = at < last ? v[f] * g : 0.f;
+            if (at == own_row) v[f] -= 1.f;
+            v[f] = at < last - lowest ? v[f] * g : 0.f;
           }
-          *reinterpret_cast<uint2*>(own + m * LD + row[i][e] - wm) = uint2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+          *reinterpret_cast<uint2*>(own + m * LD + 32 * i + within(e) + 4 * (lane >> 5)) = uint2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
         }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
