@@ -117,22 +117,53 @@ struct Operand {
 #pragma unroll
       for (int r = 0; r < REGS; ++r) at[r] += by;
     }
-    // Values 16 k + 8 h .. + 7 of entry f0 + 32 i + (lane & 31).
-    GPTQ_DEV void read(int k, u32x4 (&v)[COUNT]) const {
+    // Values 16 K + 8 h .. + 7 of entry f0 + 32 i + (lane & 31), of an operand along the contraction.
+    template <int K>
+    GPTQ_DEV void read(u32x4 (&v)[COUNT]) const {
 #pragma unroll
-      for (int i = 0; i < COUNT; ++i) {
-        if constexpr (ACROSS) {
-          const uint32_t p = at[i] + 32 * E * k;
-          const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)p));
-          const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(p + 8 * E)));
-          v[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
-        } else {
-          v[i] = *(const lds_u32x4*)(uintptr_t)(at[(k ^ (2 * (i & 1)))] + 32 * 2 * LK * i);
-        }
-      }
+      for (int i = 0; i < COUNT; ++i) v[i] = *(const lds_u32x4*)(uintptr_t)(at[K ^ (2 * (i & 1))] + 32 * 2 * LK * i);
     }
   };
 };
+
+// The same of operands across it, at the addresses `at`: a lane of 16 gives the address of four
+// values of one k and gets four k of its own entry.  The builtin of this
+// instruction waits for every asynchronous load to LDS in flight, whichever buffer it
+// writes (gradients of 2048 tokens of 32000 x 4096: 907 us); these blocks wait for reads
+// alone, and hold the wait themselves.
+#define GPTQ_TR(out, from, off) "ds_read_b64_tr_b16 %" #out ", %" #from " offset:%" #off "\n\t"
+typedef uint2 Half;   // four values
+GPTQ_DEV u32x4 whole(Half lo, Half hi) { return u32x4{lo.x, lo.y, hi.x, hi.y}; }
+
+template <int E, int K>
+GPTQ_DEV void read_across(const uint32_t (&at)[2], u32x4 (&v)[2]) {
+  Half a, b, c, d;
+  asm volatile(GPTQ_TR(0, 4, 6) GPTQ_TR(1, 4, 7) GPTQ_TR(2, 5, 6) GPTQ_TR(3, 5, 7) "s_waitcnt lgkmcnt(0)"
+               : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+               : "v"(at[0]), "v"(at[1]), "n"(32 * E * K), "n"(32 * E * K + 8 * E)
+               : "memory");
+  v[0] = whole(a, b);
+  v[1] = whole(c, d);
+}
+
+// Both operands: four fragments of E entries and two of F.
+template <int E, int F, int K>
+GPTQ_DEV void read_across(const uint32_t (&at)[4], u32x4 (&v)[4], const uint32_t (&bt)[2], u32x4 (&w)[2]) {
+  Half a[8], b[4];
+  asm volatile(GPTQ_TR(0, 12, 18) GPTQ_TR(1, 12, 19) GPTQ_TR(8, 16, 20) GPTQ_TR(9, 16, 21) GPTQ_TR(10, 17, 20) GPTQ_TR(11, 17, 21)
+               GPTQ_TR(2, 13, 18) GPTQ_TR(3, 13, 19) GPTQ_TR(4, 14, 18) GPTQ_TR(5, 14, 19) GPTQ_TR(6, 15, 18) GPTQ_TR(7, 15, 19)
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(a[0]), "=&v"(a[1]), "=&v"(a[2]), "=&v"(a[3]), "=&v"(a[4]), "=&v"(a[5]), "=&v"(a[6]), "=&v"(a[7]),
+                 "=&v"(b[0]), "=&v"(b[1]), "=&v"(b[2]), "=&v"(b[3])
+               : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(bt[0]), "v"(bt[1]),
+                 "n"(32 * E * K), "n"(32 * E * K + 8 * E), "n"(32 * F * K), "n"(32 * F * K + 8 * F)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = whole(a[2 * i], a[2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = whole(b[2 * i], b[2 * i + 1]);
+}
+#undef GPTQ_TR
 
 // The order of READS reads of LDS and PRODUCTS matrix products: ONCE reads, a product, and so on,
 // then the products that are left.
@@ -147,6 +178,11 @@ GPTQ_DEV void spread() {
   }
 }
 
+template <int K>
+struct At {
+  static constexpr int value = K;
+};
+
 // acc = A B^T of steps first .. last - 1.  Fragments are read from LDS 16 values of
 // the contraction ahead of their products, also over the end of a step: the barrier stands before
 // the last 16 values' products, when their fragments are in registers, so that the
@@ -158,10 +194,10 @@ struct Product {
   typedef Operand<TB, TN, NW> OpB;
   typedef typename OpA::template Fragments<MT> FragA;
   typedef typename OpB::template Fragments<NT> FragB;
-  // Reads ahead of each product: with operands along the contraction four (loss of 8192
-  // tokens of 128000 x 4096: 6.90 ms, with one 7.08), else one (gradients of 2048 tokens of
-  // 32000 x 4096: 907 us, with four 921).
-  static constexpr int READS = FragA::READS + FragB::READS, ONCE = TA || TB ? 1 : 4;
+  // Operands along the contraction are read four fragments ahead of each product (loss of 8192
+  // tokens of 128000 x 4096: 6.90 ms, one ahead 7.08).
+  static constexpr int READS = FragA::READS + FragB::READS, ONCE = 4;
+  static_assert(!TA || TB, "reads of operands across the contraction: of B, or of both");
 
   static GPTQ_DEV void run(const Source& a, const Source& b, int64_t a0, int64_t b0, int64_t first, int64_t last,
                            unsigned char* smem, floatx16 (&acc)[MT][NT]) {
@@ -187,9 +223,15 @@ struct Product {
     fa.set(lbase + (first & 1) * BUF, wm, lane);
     fb.set(lbase + (first & 1) * BUF + OpA::BYTES, wn, lane);
     u32x4 x[2][MT], y[2][NT];
-    auto read = [&](int set, int k) {
-      fa.read(k, x[set]);
-      fb.read(k, y[set]);
+    auto read = [&](auto value, int set) {
+      constexpr int K = decltype(value)::value;
+      if constexpr (TA) {
+        read_across<TM, TN, K>(fa.at, x[set], fb.at, y[set]);
+      } else {
+        fa.template read<K>(x[set]);
+        if constexpr (TB) read_across<TN, K>(fb.at, y[set]);
+        else fb.template read<K>(y[set]);
+      }
     };
     auto multiply = [&](int set) {
 #pragma unroll
@@ -201,14 +243,17 @@ struct Product {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     load(first + 1);
-    read(0, 0);
+    read(At<0>(), 0);
+    auto quarter = [&](auto value) {   // reads values 16 K .., multiplies the ones before them
+      constexpr int K = decltype(value)::value;
+      read(value, K & 1);
+      multiply((K & 1) ^ 1);
+      if constexpr (!TB) spread<READS, MT * NT, ONCE>();
+    };
     auto most = [&]() {   // a step but for its last 16 values
-#pragma unroll
-      for (int k = 0; k < LK / 16 - 1; ++k) {
-        read((k + 1) & 1, k + 1);
-        multiply(k & 1);
-        spread<READS, MT * NT, ONCE>();
-      }
+      quarter(At<1>());
+      quarter(At<2>());
+      quarter(At<3>());
     };
     for (int64_t s = first; s + 1 < last; ++s) {
       most();
@@ -219,9 +264,7 @@ struct Product {
       const int by = s & 1 ? -BUF : BUF;
       fa.move(by);
       fb.move(by);
-      read(0, 0);
-      multiply(1);
-      spread<READS, MT * NT, ONCE>();
+      quarter(At<0>());
     }
     most();
     multiply(1);
@@ -229,7 +272,7 @@ struct Product {
     __syncthreads();   // the last step's operands have been read
   }
 };
-static_assert(LK / 16 % 2 == 0, "a step's last fragments are in set 1");
+static_assert(LK == 64, "a step is four times 16 values, the last of them in set 1");
 
 // ---------------------------------------------------------------- softmax statistics
 // The largest of two sets of values and the sum of exponentials against it.  A set
