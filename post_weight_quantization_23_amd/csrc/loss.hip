@@ -78,6 +78,23 @@ __global__ __launch_bounds__(1024) void keep_kernel(KeepArgs a) {
     for (int64_t p = tid; p < before; p += 1024) a.k.grad[p] = ldexpf(a.k.grad[p], e);
   }
   if (tid == 0) *a.k.down = ldexpf(1.f, -e);
+  if (tid == 0 && a.d > 0) {
+    // Parts of dX's contraction: rounds of tiles over the CUs (two of the smaller
+    // tiles each), at 1.75 us for 64 entries of the vocabulary, against writing and
+    // reading the parts, 5 ns for 1000 values (1536 tokens of 32000 x 4096: two parts
+    // and five both take 451 us).
+    const int64_t tile = a.large ? 256 : 128, slots = a.large ? 256 : 512;
+    const int64_t tiles = (before + tile - 1) / tile * ((a.d + tile - 1) / tile), steps = (a.width + 63) / 64;
+    const float whole = steps * (a.large ? 1.75f : 1.f), join = (float)before * a.d * 5e-6f;
+    int best = 1;
+    float least = whole * ((tiles + slots - 1) / slots);
+    for (int s = 2; s <= kMostSplits && tiles * s <= kMostParts && steps >= 8 * s; ++s) {
+      const float us = whole * ((tiles * s + slots - 1) / slots) / s + join * s;
+      if (us < least) least = us, best = s;
+    }
+    const int64_t each = (steps + best - 1) / best;   // of equal length, none empty
+    *a.k.splits = steps > 0 ? (int)((steps + each - 1) / each) : 1;
+  }
 }
 
 // One thread per eight columns of a token.
@@ -102,22 +119,36 @@ GPTQ_DEV float2 join_sums(float2 a, float2 b) {
   return float2{m, a.y * __builtin_amdgcn_exp2f((a.x - r) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - r) * kLog2e)};
 }
 
-// 16 tokens by 16 threads each: a thread joins every 16th tile.
+// TOKENS tokens by 256 / TOKENS threads each, which join every so many of its tiles: 16 tokens
+// where there are enough of them, else one wave for each.
+template <int TOKENS>
 __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a, int tiles, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float2 sums[16][17];
-  const int tok = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int64_t p = (int64_t)blockIdx.x * 16 + tok, count = a.target ? a.n : *a.k.count;
+  constexpr int PARTS = 256 / TOKENS;
+  __shared__ float2 sums[PARTS][TOKENS + 1];
+  const int tok = TOKENS == 16 ? threadIdx.x & 15 : threadIdx.x / PARTS, part = TOKENS == 16 ? threadIdx.x >> 4 : threadIdx.x % PARTS;
+  const int64_t p = (int64_t)blockIdx.x * TOKENS + tok, count = a.target ? a.n : *a.k.count;
   float2 v = {-INFINITY, 0.f};
   if (p < count)
-    for (int i = part; i < tiles; i += 16) v = join_sums(v, a.part[(int64_t)i * a.n + p]);
-  sums[part][tok] = v;
-  __syncthreads();
-  if (part != 0 || p >= count) return;
-  for (int i = 1; i < 16; ++i) v = join_sums(v, sums[i][tok]);
-  const float all = v.x + logf(v.y);
+    for (int i = part; i < tiles; i += 4 * PARTS) {   // four loads at once
+      float2 u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = i + e * PARTS < tiles ? a.part[(int64_t)(i + e * PARTS) * a.n + p] : float2{-INFINITY, 0.f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v = join_sums(v, u[e]);
+    }
+  if constexpr (PARTS == 64) {
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) v = join_sums(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)});
+    if (part != 0 || p >= count) return;
+  } else {
+    sums[part][tok] = v;
+    __syncthreads();
+    if (part != 0 || p >= count) return;
+    for (int i = 1; i < PARTS; ++i) v = join_sums(v, sums[i][tok]);
+  }
   const bool none = a.target && (uint64_t)a.target[p] >= (uint64_t)a.vocab;
   const int64_t t = a.target ? p : a.k.token[p];
-  lse[t] = none ? 0.f : all;
+  lse[t] = none ? 0.f : v.x + logf(v.y);
   loss[t] = none ? 0.f : (v.x - a.at_target[p]) + logf(v.y);   // not lse - z: lse is rounded at its size
 }
 
@@ -125,14 +156,17 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a, int tiles, f
 template <int DT>
 __global__ __launch_bounds__(256) void join_x_kernel(GradXArgs a) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = a.d >> 3, p = i / per, j = (i - p * per) * 8;
-  if (p >= *a.k.count) return;
+  const int64_t count = *a.k.count;
+  const int splits = *a.k.splits;
+  if (p >= count || (splits == 1 && !a.pieces)) return;
   float v[8] = {};
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = 0; s < splits; ++s) {
     float u[8];
-    load8f(a.part + ((int64_t)s * a.n + p) * a.d + j, u);
+    load8f(a.part + ((int64_t)s * count + p) * a.d + j, u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += u[e];
   }
+  add_row<DT>(a.W0 + a.k.col[p] * a.ldw + j, a.k.rest[p], v);
   const float down = *a.k.down;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] *= down;
@@ -152,7 +186,9 @@ void launch_gather_kept(GatherArgs a, hipStream_t s) {
 }
 
 void launch_loss_join(const LossArgs& a, float* loss, float* lse, hipStream_t s) {
-  hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)((a.n + 15) / 16)), dim3(256), 0, s, a, (int)loss_tiles(a.n, a.vocab), loss, lse);
+  const int tiles = (int)loss_tiles(a.n, a.vocab);
+  if (a.n > 1024) hipLaunchKernelGGL(loss_join_kernel<16>, dim3((unsigned)((a.n + 15) / 16)), dim3(256), 0, s, a, tiles, loss, lse);
+  else hipLaunchKernelGGL(loss_join_kernel<4>, dim3((unsigned)((a.n + 3) / 4)), dim3(256), 0, s, a, tiles, loss, lse);
 }
 
 void launch_join_x(const GradXArgs& a, int dt, hipStream_t s) {

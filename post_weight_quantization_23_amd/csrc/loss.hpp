@@ -5,14 +5,13 @@
 
 namespace gptq {
 
-// Vocabulary entries of a tile of logits: its part of a token's sums.
-constexpr int64_t kLossTile = 256, kFewTile = 128;
-// Up to as many tokens the largest tiles hold them all, and leaving tokens out
-// saves no work: they are taken as they lie (forward).
+// Tiles of logits, entries of the vocabulary x tokens.
+enum LossShape { k256x256, k128x128, k128x64, k128x32 };
+LossShape loss_shape(int64_t n);
+inline int64_t loss_entries(LossShape s) { return s == k256x256 ? 256 : 128; }
+// Up to as many tokens one or two tiles hold them all, and leaving tokens out
+// saves little work: they are taken as they lie (forward).
 constexpr int64_t kFewTokens = 256;
-// ... and up to as many tiles are of kFewTile entries.
-constexpr int64_t kFewEntries = 128;
-inline int64_t loss_tile(int64_t n) { return n <= kFewEntries ? kFewTile : kLossTile; }
 
 // The tokens that have a target, in order: place p is token token[p] with target
 // col[p]; place_of[t] is token t's place or -1.  count: how many there are.
@@ -24,6 +23,8 @@ struct Kept {
   float* grad;
   int32_t* count;
   float* down;      // what results are multiplied by (a power of two, 1 for bf16)
+  float* rest;      // what rounding took from the target's entry of D (backward)
+  int32_t* splits;  // parts of the contraction that dX is computed in
 };
 
 struct KeepArgs {
@@ -32,6 +33,8 @@ struct KeepArgs {
   float *loss, *lse;              // forward: zeroed where there is no target
   const float *lse_in, *dloss;    // backward (dloss null: 1)
   bool half;                      // fp16 gradients
+  int64_t d, width;               // dX: columns, and entries of a piece
+  bool large;                     // ... in tiles of 256 x 256
   Kept k;
 };
 void launch_keep(const KeepArgs& a, hipStream_t s);
@@ -50,7 +53,18 @@ struct GatherArgs {
 };
 void launch_gather_kept(GatherArgs a, hipStream_t s);
 
-// Logits of every kept token in tiles of loss_tile(n) entries: of each tile the
+// v += much x eight 16-bit values (on 16 bytes).
+template <int DT>
+GPTQ_DEV void add_row(const uint16_t* row, float much, float (&v)[8]) {
+  const u32x4 w = *reinterpret_cast<const u32x4*>(row);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __builtin_fmaf(much, f16_to_f32<DT>(w[e] & 0xFFFFu), v[2 * e]);
+    v[2 * e + 1] = __builtin_fmaf(much, f16_to_f32<DT>(w[e] >> 16), v[2 * e + 1]);
+  }
+}
+
+// Logits of every kept token in tiles: of each tile the
 // largest and the sum of exponentials against it, and the target's logit.
 struct LossArgs {
   const uint16_t* W;
@@ -69,17 +83,17 @@ void launch_logits(const LossArgs& a, int dt, bool grad, hipStream_t s);
 
 void launch_loss_join(const LossArgs& a, float* loss, float* lse, hipStream_t s);
 
-// dX[place] = P W over one piece of the vocabulary, in `splits` fp32 parts (added
-// to what earlier pieces left), and their sum.
+// dX[place] = P W over one piece of the vocabulary, in *k.splits fp32 parts (added
+// to what earlier pieces left), and their sum; at once where one piece and part are all.
 struct GradXArgs {
   const uint16_t* P;
   int64_t ldp, width;
   const uint16_t* W;       // the piece's rows
   int64_t ldw, n, d;
   Kept k;
-  int splits;
-  bool add;                // to parts of an earlier piece
-  float* part;             // [splits][n][d]; null: dX is written at once
+  const uint16_t* W0;      // all of W
+  bool pieces, add;        // there are several pieces; this one adds to parts of an earlier one
+  float* part;             // [splits][kept][d]
   uint16_t* dX;
   int64_t ldd;
   bool vec;
@@ -100,11 +114,17 @@ struct GradWArgs {
 };
 void launch_grad_w(const GradWArgs& a, int dt, hipStream_t s);
 
-// The parts of the contraction that dX is computed in, at a piece of `width` entries.
-int grad_x_splits(int64_t n, int64_t d, int64_t width);
+// dX in tiles of 256 x 256, else 128 x 128, and workspace of its parts.
+bool grad_x_large(int64_t n);
+int64_t grad_x_part_floats(int64_t n, int64_t d, bool pieces);
+constexpr int kMostSplits = 16;
+constexpr int64_t kMostParts = 768;   // tiles times parts, where there are several parts
 // Entries of a piece.
 int64_t loss_piece(int64_t n, int64_t vocab);
-inline int64_t loss_tiles(int64_t n, int64_t vocab) { return (vocab + loss_tile(n) - 1) / loss_tile(n); }
+inline int64_t loss_tiles(int64_t n, int64_t vocab) {
+  const int64_t e = loss_entries(loss_shape(n));
+  return (vocab + e - 1) / e;
+}
 // Whether rows of X can be taken as they lie.
 bool loss_takes(const void* X, int64_t n, int64_t d, int64_t ldx);
 bool loss_fits(int64_t n, int64_t vocab, int64_t d, bool grad);

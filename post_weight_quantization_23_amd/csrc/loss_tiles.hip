@@ -282,21 +282,38 @@ GPTQ_DEV float2 join_sums(float2 a, float2 b) {
   return float2{m, a.y * __builtin_amdgcn_exp2f((a.x - r) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - r) * kLog2e)};
 }
 
+// ---------------------------------------------------------------- tile order
+// Place b of the walk over `all` tiles: of 256 workgroups, which the dispatcher deals round
+// robin to the 8 XCDs, each XCD gets 32 consecutive places.  Tiles past the kept
+// tokens' are not among them, so that they leave no XCD with less to do.
+GPTQ_DEV int64_t place_of(int64_t b, int64_t all) {
+  return b < (all & ~(int64_t)255) ? (b & ~(int64_t)255) | ((b & 7) << 5) | ((b & 255) >> 3) : b;
+}
+// Tile of a place: panels of 8 tiles of tokens, walked column by column.
+GPTQ_DEV void tile_at(int64_t place, int tok_tiles, int col_tiles, int& tok, int& col) {
+  const int64_t per = (int64_t)8 * col_tiles;
+  const int panel = (int)(place / per), in = (int)(place - panel * per), h = min(8, tok_tiles - 8 * panel);
+  col = in / h;
+  tok = 8 * panel + in - col * h;
+}
+
 // ---------------------------------------------------------------- logits
 // Tiles of TM vocabulary entries (rows of the accumulators) x TN kept tokens
 // (columns): a lane holds most of a token's entries itself, so the largest and the sum
 // cost one exchange between lanes.
 template <int DT, bool GRAD, int MT, int NT, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int tok_tiles, int voc_tiles) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int voc_tiles) {
   using P = Product<DT, false, false, MT, NT, WM, WN>;
   extern __shared__ __align__(16) unsigned char lsm[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31;
   const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
   const int64_t count = !GRAD && a.target ? a.n : *a.k.count;
+  const int tok_tiles = (int)((count + P::TN - 1) / P::TN);
+  const int64_t all = (int64_t)tok_tiles * voc_tiles;
+  if (blockIdx.x >= all) return;
   int tt, vt;
-  tile_of(blockIdx.x, tok_tiles, voc_tiles, tt, vt);
+  tile_at(place_of(blockIdx.x, all), tok_tiles, voc_tiles, tt, vt);
   const int64_t t0 = (int64_t)tt * P::TN, v0 = (int64_t)vt * P::TM;
-  if (t0 >= count) return;
   const int64_t steps = (a.d + LK - 1) / LK;
   const Source w{a.W + a.v0 * a.ldw, a.ldw, a.width, a.d}, x{a.rows, a.ldr, count, steps * LK};
   floatx16 acc[MT][NT];
@@ -363,6 +380,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
       const int64_t y = p < count ? (int64_t)a.k.col[p] - a.v0 - v0 : -1;
       const int own_row = (int)y - lowest;
       const float lse = p < count ? a.k.lse[p] : 0.f, g = p < count ? a.k.grad[p] : 0.f;
+      float target = 0.f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -374,9 +392,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
             v[f] = __builtin_amdgcn_exp2f((acc[i][q][e + f] - lse) * kLog2e);
             if (at == own_row) v[f] -= 1.f;
             v[f] = at < last - lowest ? v[f] * g : 0.f;
+            target = at == own_row ? v[f] : target;
           }
           *reinterpret_cast<uint2*>(own + m * LD + 32 * i + within(e) + 4 * (lane >> 5)) = uint2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
         }
+      // the lane that holds the target's entry (row 4 h + within() of some set)
+      if (y >= wm && y < wm + 32 * MT && ((int)y >> 2 & 1) == lane >> 5)
+        a.k.rest[p] = target - f16_to_f32<DT>(f32_to_16<DT>(target));
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int k = 0; k < RUNS / 2; ++k) {
@@ -391,7 +413,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
 }
 
 // ---------------------------------------------------------------- gradients
-// Stores of a wave's 32 rows x 32 NT columns, turned through its LDS.
+// Stores of a wave's 32 rows x 32 NT columns times `by`, turned through its LDS.  row_at(r, also, much):
+// the row's place, and optionally a row of 16-bit values `also` of which `much` is added first.
 template <int OT, int NT, class F>
 GPTQ_DEV void store_rows(float* lds, const floatx16 (&acc)[NT], int64_t j0, int64_t cols, bool vec, float by, F&& row_at) {
   constexpr int W = 32 * NT, RUNS = W / 8;
@@ -400,10 +423,13 @@ GPTQ_DEV void store_rows(float* lds, const floatx16 (&acc)[NT], int64_t j0, int6
 #pragma unroll
   for (int k = 0; k < RUNS / 2; ++k) {
     const int run = 64 * k + lane, r = run / RUNS, c = 8 * (run % RUNS);
-    uint16_t* to = row_at(r);
+    const uint16_t* also = nullptr;
+    float much = 0.f;
+    uint16_t* to = row_at(r, also, much);
     if (!to || j0 + c >= cols) continue;
     float v[8];
     load8f(lds + r * (W + 4) + c, v);
+    if (also) add_row<OT>(also + j0 + c, much, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= by;
     store8<OT>(to, j0 + c, v, (int)min((int64_t)8, cols - j0 - c), vec);
@@ -412,29 +438,31 @@ GPTQ_DEV void store_rows(float* lds, const floatx16 (&acc)[NT], int64_t j0, int6
 }
 
 // dX: tiles of TM kept tokens x TN columns, contracted over the piece's entries.
-template <int DT, bool PARTS, int MT, int NT, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void grad_x_kernel(GradXArgs a, int tok_tiles, int col_tiles) {
+template <int DT, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void grad_x_kernel(GradXArgs a, int col_tiles) {
   using P = Product<DT, false, true, MT, NT, WM, WN>;
   extern __shared__ __align__(16) unsigned char lsm[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
   const int64_t count = *a.k.count;
+  const int splits = *a.k.splits, tok_tiles = (int)((count + P::TM - 1) / P::TM);
+  const int64_t tiles = (int64_t)tok_tiles * col_tiles;
+  if (blockIdx.x >= tiles * splits) return;
+  const int64_t place = place_of(blockIdx.x, tiles * splits);
+  const int split = (int)(place / tiles);
   int tt, ct;
-  const int64_t tile = blockIdx.x / a.splits;
-  const int split = (int)(blockIdx.x - tile * a.splits);
-  tile_of(tile, tok_tiles, col_tiles, tt, ct);
+  tile_at(place - split * tiles, tok_tiles, col_tiles, tt, ct);
   const int64_t t0 = (int64_t)tt * P::TM, j0 = (int64_t)ct * P::TN;
-  if (t0 >= count) return;
-  const int64_t steps = (a.width + LK - 1) / LK, each = (steps + a.splits - 1) / a.splits;
+  const int64_t steps = (a.width + LK - 1) / LK, each = (steps + splits - 1) / splits;
   const int64_t first = min(steps, split * each), last = min(steps, first + each);
   floatx16 acc[MT][NT];
   P::run(Source{a.P, a.ldp, count, a.ldp}, Source{a.W, a.ldw, a.d, a.width}, t0, j0, first, last, lsm, acc);
   static_assert(WM * WN * 32 * (32 * NT + 4) * 4 <= 2 * P::BUF, "results fit the operands' LDS");
   float* own = reinterpret_cast<float*>(lsm) + wave * 32 * (32 * NT + 4);
-  if constexpr (PARTS) {
+  if (splits > 1 || a.pieces) {
     constexpr int W = 32 * NT, RUNS = W / 4;
     const int lane = threadIdx.x & 63;
-    float* part = a.part + (int64_t)split * a.n * a.d;
+    float* part = a.part + (int64_t)split * count * a.d;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       turn_tile<NT>(own, acc[i]);
@@ -454,9 +482,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_x_kernel(GradXArgs a, in
     const float down = *a.k.down;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-      store_rows<DT, NT>(own, acc[i], j0 + wn, a.d, a.vec, down, [&](int r) -> uint16_t* {
+      store_rows<DT, NT>(own, acc[i], j0 + wn, a.d, a.vec, down, [&](int r, const uint16_t*& also, float& much) -> uint16_t* {
         const int64_t p = t0 + wm + 32 * i + r;
-        return p < count ? a.dX + (int64_t)a.k.token[p] * a.ldd : nullptr;
+        if (p >= count) return nullptr;
+        also = a.W0 + a.k.col[p] * a.ldw;
+        much = a.k.rest[p];
+        return a.dX + (int64_t)a.k.token[p] * a.ldd;
       });
   }
 }
@@ -470,7 +501,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_w_kernel(GradWArgs a, in
   const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
   const int64_t count = *a.k.count;
   int vt, ct;
-  tile_of(blockIdx.x, voc_tiles, col_tiles, vt, ct);
+  tile_at(place_of(blockIdx.x, (int64_t)voc_tiles * col_tiles), voc_tiles, col_tiles, vt, ct);
   const int64_t v0 = (int64_t)vt * P::TM, j0 = (int64_t)ct * P::TN;
   floatx16 acc[MT][NT];
   P::run(Source{a.P, a.ldp, a.ldp, count}, Source{a.rows, a.kp, a.kp, count}, v0, j0, 0, (count + LK - 1) / LK, lsm, acc);
@@ -478,7 +509,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_w_kernel(GradWArgs a, in
   const float down = *a.k.down;
 #pragma unroll
   for (int i = 0; i < MT; ++i)
-    store_rows<DT, NT>(own, acc[i], j0 + wn, a.d, a.vec, down, [&](int r) -> uint16_t* {
+    store_rows<DT, NT>(own, acc[i], j0 + wn, a.d, a.vec, down, [&](int r, const uint16_t*&, float&) -> uint16_t* {
       const int64_t v = v0 + wm + 32 * i + r;
       return v < a.width ? a.dW + v * a.ldd : nullptr;
     });
@@ -492,35 +523,34 @@ void allow_lds(K kernel, int bytes) {
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 
-template <int DT, bool GRAD, int MT, int NT, int WM, int WN>
+template <int DT, bool GRAD, int MT, int NT, int WM, int WN>   // a tile of 32 MT WM entries x 32 NT WN tokens
 void logits(const LossArgs& a, hipStream_t s) {
   using P = Product<DT, false, false, MT, NT, WM, WN>;
   static const bool set = (allow_lds(logits_kernel<DT, GRAD, MT, NT, WM, WN>, 2 * P::BUF), true);
   (void)set;
   const int tt = (int)tiles_of(a.n, P::TN), vt = (int)tiles_of(a.width, P::TM);
   hipLaunchKernelGGL((logits_kernel<DT, GRAD, MT, NT, WM, WN>), dim3((unsigned)((int64_t)tt * vt)), dim3(64 * WM * WN), 2 * P::BUF, s,
-                     a, tt, vt);
+                     a, vt);
 }
 
 template <int DT, bool GRAD>
 void logits_shape(const LossArgs& a, hipStream_t s) {
-  static_assert(kFewEntries == 128 && kFewTile == 128 && kLossTile == 256, "tiles of loss_tile(n) entries");
-  if (a.n > 128) logits<DT, GRAD, 4, 2, 2, 4>(a, s);
-  else if (a.n > 64) logits<DT, GRAD, 2, 2, 2, 2>(a, s);
-  else if (a.n > 32) logits<DT, GRAD, 1, 2, 4, 1>(a, s);
-  else logits<DT, GRAD, 1, 1, 4, 1>(a, s);
+  switch (loss_shape(a.n)) {
+    case k256x256: return logits<DT, GRAD, 4, 2, 2, 4>(a, s);
+    case k128x128: return logits<DT, GRAD, 2, 2, 2, 2>(a, s);
+    case k128x64: return logits<DT, GRAD, 1, 2, 4, 1>(a, s);
+    case k128x32: return logits<DT, GRAD, 1, 1, 4, 1>(a, s);
+  }
 }
 
 template <int DT, int MT, int NT, int WM, int WN>
 void grad_x(const GradXArgs& a, hipStream_t s) {
   using P = Product<DT, false, true, MT, NT, WM, WN>;
-  static const bool set = (allow_lds(grad_x_kernel<DT, true, MT, NT, WM, WN>, 2 * P::BUF),
-                           allow_lds(grad_x_kernel<DT, false, MT, NT, WM, WN>, 2 * P::BUF), true);
+  static const bool set = (allow_lds(grad_x_kernel<DT, MT, NT, WM, WN>, 2 * P::BUF), true);
   (void)set;
-  const int tt = (int)tiles_of(a.n, P::TM), ct = (int)tiles_of(a.d, P::TN);
-  const dim3 grid((unsigned)((int64_t)tt * ct * a.splits)), block(64 * WM * WN);
-  if (a.part) hipLaunchKernelGGL((grad_x_kernel<DT, true, MT, NT, WM, WN>), grid, block, 2 * P::BUF, s, a, tt, ct);
-  else hipLaunchKernelGGL((grad_x_kernel<DT, false, MT, NT, WM, WN>), grid, block, 2 * P::BUF, s, a, tt, ct);
+  const int64_t tiles = tiles_of(a.n, P::TM) * tiles_of(a.d, P::TN);
+  hipLaunchKernelGGL((grad_x_kernel<DT, MT, NT, WM, WN>), dim3((unsigned)(tiles > kMostParts ? tiles : kMostParts)), dim3(64 * WM * WN),
+                     2 * P::BUF, s, a, (int)tiles_of(a.d, P::TN));
 }
 
 template <int DT, int MT, int NT, int WM, int WN>
@@ -540,8 +570,8 @@ void launch_logits(const LossArgs& a, int dt, bool grad, hipStream_t s) {
 }
 
 void launch_grad_x(const GradXArgs& a, int dt, hipStream_t s) {
-  if (dt == kBF16) a.n > 128 ? grad_x<kBF16, 4, 2, 2, 4>(a, s) : grad_x<kBF16, 2, 2, 2, 2>(a, s);
-  else a.n > 128 ? grad_x<kF16, 4, 2, 2, 4>(a, s) : grad_x<kF16, 2, 2, 2, 2>(a, s);
+  if (dt == kBF16) grad_x_large(a.n) ? grad_x<kBF16, 4, 2, 2, 4>(a, s) : grad_x<kBF16, 2, 2, 2, 2>(a, s);
+  else grad_x_large(a.n) ? grad_x<kF16, 4, 2, 2, 4>(a, s) : grad_x<kF16, 2, 2, 2, 2>(a, s);
 }
 
 void launch_grad_w(const GradWArgs& a, int dt, hipStream_t s) {
@@ -549,20 +579,32 @@ void launch_grad_w(const GradWArgs& a, int dt, hipStream_t s) {
   else grad_w<kF16, 4, 2, 2, 4>(a, s);
 }
 
-int grad_x_splits(int64_t n, int64_t d, int64_t width) {
-  const int64_t tile = n > 128 ? 256 : 128, tiles = tiles_of(n, tile) * tiles_of(d, tile), steps = tiles_of(width, LK);
-  int64_t splits = (n > 128 ? 256 : 512) / (tiles > 0 ? tiles : 1);
-  splits = splits < steps / 8 ? splits : steps / 8;
-  if (splits < 2) return 1;
-  splits = splits < 16 ? splits : 16;
-  const int64_t each = (steps + splits - 1) / splits;
-  return (int)((steps + each - 1) / each);
+// dX of 300 tokens (150 of them kept) of 32000 x 4096: 65 us in tiles of 256 x 256, 80 of 128 x 128.
+bool grad_x_large(int64_t n) { return n > 128; }
+
+// Several parts are of at most kMostParts tiles in all, one part is of all tokens.
+int64_t grad_x_part_floats(int64_t n, int64_t d, bool pieces) {
+  const int64_t tile = grad_x_large(n) ? 256 : 128, all = kMostSplits * n * d, parts = kMostParts * tile * tile;
+  const int64_t several = all < parts ? all : parts;
+  return pieces && several < n * d ? n * d : several;
+}
+
+// Of 128 x 128 tiles a CU holds two, and few tokens leave fewer of its places empty; a
+// 256 x 256 tile reads half as much of LDS for a product.  Logits of 300, 517 and 1000
+// tokens (50, 30 and 10 % of them without a target; 32000 x 4096, 50021 x 4096, 50021
+// x 1024) took 76, 216 and 158 us in the former, 111, 225 and 174 in the latter; of
+// 2048 tokens of 32000 x 4096 645 and 570.  (256 x 128: 91, 268, 170 and 680.)
+LossShape loss_shape(int64_t n) {
+  if (n <= 32) return k128x32;
+  if (n <= 64) return k128x64;
+  return n <= 1024 ? k128x128 : k256x256;
 }
 
 // Gradients of a piece are n x width 16-bit values: 512 MB.
 int64_t loss_piece(int64_t n, int64_t vocab) {
-  const int64_t most = (int64_t(1) << 28) / (n > 0 ? n : 1) / kLossTile * kLossTile;
-  return vocab <= most ? vocab : (most > kLossTile ? most : kLossTile);
+  const int64_t tile = 256, least = (int64_t(1) << 28) / (n > 0 ? n : 1) / tile * tile;
+  const int64_t most = least < tile ? tile : (least < (1 << 21) ? least : 1 << 21);   // rows of it are below 2^22
+  return vocab <= most ? vocab : most;
 }
 
 bool loss_takes(const void* X, int64_t n, int64_t d, int64_t ldx) {
@@ -570,12 +612,12 @@ bool loss_takes(const void* X, int64_t n, int64_t d, int64_t ldx) {
 }
 
 bool loss_fits(int64_t n, int64_t vocab, int64_t d, bool grad) {
-  const int64_t shortest = n > 128 ? 256 : (n > 64 ? 128 : (n > 32 ? 64 : 32));
-  if (!grid_fits(tiles_of(n, shortest) * loss_tiles(n, vocab), 512)) return false;
+  constexpr int64_t tokens[] = {256, 128, 64, 32};
+  if (!grid_fits(tiles_of(n, tokens[loss_shape(n)]) * loss_tiles(n, vocab), 512)) return false;
   if (!grid_fits(tiles_of(n * (gemm16_depth(d) / 8), 256), 256)) return false;
   if (!grad) return true;
-  const int64_t tile = n > 128 ? 256 : 128;
-  return grid_fits(tiles_of(n, tile) * tiles_of(d, tile) * 16, 512) && grid_fits(tiles_of(vocab, 256) * tiles_of(d, 256), 512);
+  const int64_t tile = grad_x_large(n) ? 256 : 128;
+  return grid_fits(tiles_of(n, tile) * tiles_of(d, tile), 512) && grid_fits(tiles_of(vocab, 256) * tiles_of(d, 256), 512);
 }
 
 }  // namespace gptq

@@ -90,7 +90,7 @@ GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, floa
   constexpr int LD = (R::PER + GRAM_THREADS - 1) / GRAM_THREADS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
   const int pair = wave % PAIRS, share = wave / PAIRS, i0 = pair, i1 = B - 1 - pair;
-  const int64_t run = ((o.q + o.splits - 1) / o.splits + KS - 1) / KS * KS, first = split * run, last = min(o.q, first + run);
+  const int64_t run = ((o.q + KS - 1) / KS + o.splits - 1) / o.splits * KS, first = split * run, last = min(o.q, first + run);
   doublex4 up[B], low[B];
 #pragma unroll
   for (int t = 0; t < B; ++t) up[t] = low[t] = doublex4{0, 0, 0, 0};
@@ -298,11 +298,12 @@ __global__ __launch_bounds__(Chain<B>::THREADS) void chain_kernel(OrthoArgs a, i
 }
 
 // ---------------------------------------------------------------- the iteration, over many CUs
-// Matrices of more than 64 rows: a launch for each product, a wave for each tile of its
-// upper half, operands and results (both halves) in memory.  One workgroup with its
-// matrix in LDS has the 64-bit products of one CU only: 254 us for 16 matrices of 128.
-// Both operands are symmetric, so each lane reads runs of one row of either, all of
-// them before the first product.
+// Matrices of more than 64 rows: a launch for each product, a wave for each tile,
+// operands and results in memory.  One workgroup with its matrix in LDS has the
+// 64-bit products of one CU only: 254 us for 16 matrices of 128.  Both operands are
+// symmetric, so each lane reads runs of one row of either, all of them before the
+// first product; both halves of a result are computed, since writing one of them
+// turned takes longer.
 struct WideArgs {
   double a, b, c;
   int64_t m;               // matrices of the first problem
@@ -319,22 +320,20 @@ enum { kS0, kS1, kT, kQ0, kQ1, kR0, kR1, kWideBuffers };   // ortho_wide's seven
 
 template <int B>
 __global__ __launch_bounds__(256) void wide_kernel(WideArgs a) {
-  constexpr int PP = 16 * B, TILES = ortho_tiles(PP);
+  constexpr int PP = 16 * B;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
-  const int t = blockIdx.y * 4 + wave, which = blockIdx.z;
-  if (t >= TILES) return;
-  int ti, tj;
-  tile_of_index(t, B, ti, tj);
+  const int t = blockIdx.y * 4 + wave, which = blockIdx.z, ti = t / B, tj = t % B;
+  if (t >= B * B) return;
   const int64_t mat = blockIdx.x;
   const int side = mat >= a.m;
   double* own = a.base[side] + (mat - (side ? a.m : 0)) * a.size;
-  const double* X = own + (int64_t)a.p[which].x * PP * PP + (16 * ti + r) * PP + h * 4 * B;   // contraction in the order h, k
-  const double* Y = own + (int64_t)a.p[which].y * PP * PP + (16 * tj + r) * PP + h * 4 * B;
+  const double* X = own + (int64_t)a.p[which].x * PP * PP + (16 * ti + r) * PP + 2 * h;   // of eight values of the contraction a lane has two
+  const double* Y = own + (int64_t)a.p[which].y * PP * PP + (16 * tj + r) * PP + 2 * h;
   double2 x[2 * B], y[2 * B];
 #pragma unroll
   for (int k = 0; k < 2 * B; ++k) {
-    x[k] = *reinterpret_cast<const double2*>(X + 2 * k);
-    y[k] = *reinterpret_cast<const double2*>(Y + 2 * k);
+    x[k] = *reinterpret_cast<const double2*>(X + 8 * k);
+    y[k] = *reinterpret_cast<const double2*>(Y + 8 * k);
   }
   double* out = own + (int64_t)a.p[which].out * PP * PP;
   const double* S = own + (int64_t)a.p[which].x * PP * PP;
@@ -353,13 +352,8 @@ __global__ __launch_bounds__(256) void wide_kernel(WideArgs a) {
     const int i = 16 * ti + 4 * e + h, j = 16 * tj + r;
     double v = acc[0][e] + acc[1][e];
     if (a.step) v = a.c * v + a.b * at[e] + (i == j ? a.a : 0.0);
-    if (ti == tj && i > j) continue;   // of a tile on the diagonal one half stands for both
-    if (which == a.last) {
-      float* R = a.R[side] + (mat - (side ? a.m : 0)) * PP * PP;
-      R[i * PP + j] = R[j * PP + i] = (float)v;
-    } else {
-      out[i * PP + j] = out[j * PP + i] = v;
-    }
+    if (which == a.last) a.R[side][(mat - (side ? a.m : 0)) * PP * PP + i * PP + j] = (float)v;
+    else out[i * PP + j] = v;
   }
 }
 
@@ -411,7 +405,7 @@ void wide(const OrthoArgs& a, int which, bool both, hipStream_t s) {
   const int64_t mats = both ? 2 * a.m : a.m;
   hipLaunchKernelGGL(wide_start_kernel<B>, dim3((unsigned)mats, TILES), dim3(256), 0, s, a, which, w);
   auto launch = [&](int products) {
-    hipLaunchKernelGGL(wide_kernel<B>, dim3((unsigned)mats, (TILES + 3) / 4, products), dim3(256), 0, s, w);
+    hipLaunchKernelGGL(wide_kernel<B>, dim3((unsigned)mats, (B * B + 3) / 4, products), dim3(256), 0, s, w);
   };
   int S = kS0, R = -1;
   for (int k = 0; k < a.steps; ++k) {
@@ -469,7 +463,7 @@ GPTQ_DEV void apply(const OrthoProblem& o, int gt, int64_t mat, int64_t first, i
   fetch(first);
   float w[4 * B];
 #pragma unroll
-  for (int k = 0; k < 4 * B; ++k) w[k] = o.R[mat * PP * PP + (16 * row + r) * PP + 4 * k + h];
+  for (int k = 0; k < 4 * B; ++k) w[k] = o.R[mat * PP * PP + (4 * k + h) * PP + 16 * row + r];   // symmetric
   const double inv = o.inv[mat];
   for (int64_t k0 = first; k0 < last; k0 += KS) {
     __syncthreads();
@@ -519,10 +513,11 @@ __global__ __launch_bounds__(Apply<B>::THREADS) void apply_kernel(OrthoArgs a, i
 // One launch of each kernel for the problems of B tile rows: `which` and, if both, the other.
 template <int B>
 void orthogonalize(const OrthoArgs& a, int which, bool both, int gt, int ot, hipStream_t s) {
-  // runs of a workgroup: four where that leaves two workgroups for each CU
+  // runs of a workgroup: the places of two or three workgroups on each CU filled once
   int64_t all = 0;
   for (int w = which; w <= (both ? 1 : which); ++w) all += a.m * ((a.p[w].q + KS - 1) / KS);
-  const int runs = all >= 2048 ? 4 : (all >= 1024 ? 2 : 1);
+  const int64_t slots = B > kOrthoNarrow ? 512 : 768;
+  const int runs = (int)(all <= slots ? 1 : (all + slots - 1) / slots < 16 ? (all + slots - 1) / slots : 16);
   int64_t gram[2] = {0, 0}, apply[2] = {0, 0};
   for (int w = which; w <= (both ? 1 : which); ++w) {
     gram[w - which] = a.m * a.p[w].splits;
@@ -561,13 +556,12 @@ void launch_orthogonalize(const OrthoArgs& args, int gt, int ot, hipStream_t s) 
   if (two && !same) choose(a, 1, false, gt, ot, s);
 }
 
-// Parts of S_0: enough for a workgroup on every CU, each of one run at least; a matrix's
-// iteration reads them all.
-int ortho_splits(int64_t m, int64_t q) {
-  const int64_t runs = (q + KS - 1) / KS, want = 256 / (2 * (m > 0 ? m : 1));
-  int64_t splits = want < 4 ? 4 : (want < 32 ? want : 32);
-  splits = splits < runs ? splits : runs;
-  const int64_t each = (runs + splits - 1) / splits;
+// Parts of S_0: of as many runs each, for both factors together, as one workgroup on every CU
+// takes; a matrix's iteration reads them all.
+int ortho_splits(int64_t m, int64_t q, int64_t both) {
+  const int64_t runs = (q + KS - 1) / KS, all = (m > 0 ? m : 1) * ((both + KS - 1) / KS);
+  int64_t each = (all + 255) / 256;
+  each = each > runs / 32 ? each : (runs + 31) / 32;
   return (int)((runs + each - 1) / each);
 }
 

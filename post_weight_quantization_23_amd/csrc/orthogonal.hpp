@@ -36,7 +36,7 @@ inline int64_t ortho_wide(int p) {
   const int64_t pp = 16 * ortho_blocks(p);
   return ortho_blocks(p) > kOrthoNarrow ? 7 * pp * pp : 0;
 }
-int ortho_splits(int64_t m, int64_t q);
+int ortho_splits(int64_t m, int64_t q, int64_t both);
 bool ortho_fits(int64_t m, int64_t q);
 // gt / ot: 0 fp32, 1 bf16, 2 fp16.
 void launch_orthogonalize(const OrthoArgs& a, int gt, int ot, hipStream_t s);

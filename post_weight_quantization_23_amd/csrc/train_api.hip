@@ -91,9 +91,11 @@ gptq::Kept take_kept(Carve& c, int64_t n, bool grad) {
   k.col = c.take<int32_t>(n);
   k.count = c.take<int32_t>(1);
   k.down = c.take<float>(1);
+  k.splits = c.take<int32_t>(1);
   if (grad) {
     k.lse = c.take<float>(n);
     k.grad = c.take<float>(n);
+    k.rest = c.take<float>(n);
   }
   return k;
 }
@@ -118,19 +120,15 @@ struct GradBuffers {
   uint16_t *rows, *P;
   float* part;
   int64_t piece, ldp;
-  int splits;
 };
 GradBuffers take_grad(Carve& c, int64_t n, int64_t d, int64_t vocab, bool want_dx) {
   GradBuffers b;
   b.piece = gptq::loss_piece(n, vocab);
   b.ldp = gptq::gemm16_depth(b.piece);
-  b.splits = gptq::grad_x_splits(n, d, b.piece);
   b.k = take_kept(c, n, true);
   b.rows = c.take<uint16_t>(n * gptq::gemm16_depth(d));
   b.P = c.take<uint16_t>(n * b.ldp);
-  const bool parts = want_dx && (b.splits > 1 || b.piece < vocab);
-  float* part = c.take<float>(parts ? b.splits * n * d : 0);
-  b.part = parts ? part : nullptr;
+  b.part = c.take<float>(want_dx ? gptq::grad_x_part_floats(n, d, b.piece < vocab) : 0);
   return b;
 }
 
@@ -252,6 +250,9 @@ gptq_status gptq_linear_cross_entropy_backward(const void* X, gptq_dtype xt, int
   k.lse_in = lse;
   k.dloss = dloss;
   k.half = xt == GPTQ_F16;
+  k.d = dX ? d : 0;
+  k.width = b.piece;
+  k.large = gptq::grad_x_large(n);
   k.k = b.k;
   gptq::launch_keep(k, s);
   gptq::GatherArgs g{};
@@ -281,7 +282,8 @@ gptq_status gptq_linear_cross_entropy_backward(const void* X, gptq_dtype xt, int
   x.n = n;
   x.d = d;
   x.k = b.k;
-  x.splits = b.splits;
+  x.W0 = static_cast<const uint16_t*>(W);
+  x.pieces = b.piece < vocab;
   x.part = b.part;
   x.dX = static_cast<uint16_t*>(dX);
   x.ldd = lddx;
@@ -318,7 +320,7 @@ gptq_status gptq_linear_cross_entropy_backward(const void* X, gptq_dtype xt, int
       gptq::launch_grad_w(w, dt, s);
     }
   }
-  if (n > 0 && dX && b.part) gptq::launch_join_x(x, dt, s);
+  if (n > 0 && dX) gptq::launch_join_x(x, dt, s);
   return check_launch(fn);
 }
 
@@ -340,14 +342,17 @@ gptq_status check_ortho_sizes(const char* fn, int64_t m, int64_t rank, int64_t c
   return GPTQ_OK;
 }
 
-// The problem of m matrices of rows x cols.
-void take_ortho(Carve& ws, gptq::OrthoProblem& o, int64_t m, int64_t rows, int64_t cols) {
+// Longer sides of an adapter's matrices, together (0: not wanted).
+int64_t long_sides(int64_t rank, int64_t c, int64_t r) { return (c > rank || c == 0 ? c : rank) + (r > rank || r == 0 ? r : rank); }
+
+// The problem of m matrices of rows x cols; both: long_sides().
+void take_ortho(Carve& ws, gptq::OrthoProblem& o, int64_t m, int64_t rows, int64_t cols, int64_t both) {
   o.rows = rows;
   o.cols = cols;
   o.tall = rows > cols;
   o.p = (int)(o.tall ? cols : rows);
   o.q = o.tall ? rows : cols;
-  o.splits = gptq::ortho_splits(m, o.q);
+  o.splits = gptq::ortho_splits(m, o.q, both);
   const int64_t tiles = gptq::ortho_tiles(o.p), pp = 16 * gptq::ortho_blocks(o.p);
   o.part = ws.take<double>(m * o.splits * tiles * 256);
   o.inv = ws.take<double>(m);
@@ -363,8 +368,8 @@ gptq_status gptq_adapter_orthogonalize_workspace_size(int64_t m, int64_t rank, i
   if (gptq_status st = check_ortho_sizes(fn, m, rank, c, r, steps)) return st;
   Carve ws{nullptr, 0};
   gptq::OrthoProblem o{};
-  if (c > 0) take_ortho(ws, o, m, rank, c);
-  if (r > 0) take_ortho(ws, o, m, r, rank);
+  if (c > 0) take_ortho(ws, o, m, rank, c, long_sides(rank, c, r));
+  if (r > 0) take_ortho(ws, o, m, r, rank, long_sides(rank, c, r));
   *bytes = (size_t)ws.used;
   return ok();
 }
@@ -399,13 +404,13 @@ gptq_status gptq_adapter_orthogonalize(const void* G_A, const void* G_B, gptq_dt
       gptq::OrthoProblem& o = args.p[at++];
       o.G = G_A;
       o.out = out_A;
-      take_ortho(carve, o, m, rank, c);
+      take_ortho(carve, o, m, rank, c, long_sides(rank, c, r));
     }
     if (G_B) {
       gptq::OrthoProblem& o = args.p[at++];
       o.G = G_B;
       o.out = out_B;
-      take_ortho(carve, o, m, r, rank);
+      take_ortho(carve, o, m, r, rank, long_sides(rank, c, r));
     }
     if (pass == 0)
       if (gptq_status st = need_ws(fn, ws, ws_bytes, carve.used)) return st;
