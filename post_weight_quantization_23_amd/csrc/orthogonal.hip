@@ -298,63 +298,85 @@ __global__ __launch_bounds__(Chain<B>::THREADS) void chain_kernel(OrthoArgs a, i
 }
 
 // ---------------------------------------------------------------- the iteration, over many CUs
-// Matrices of more than 64 rows: a launch for each product, a wave for each tile,
-// operands and results in memory.  One workgroup with its matrix in LDS has the
-// 64-bit products of one CU only: 254 us for 16 matrices of 128.  Both operands are
-// symmetric, so each lane reads runs of one row of either, all of them before the
-// first product; both halves of a result are computed, since writing one of them
-// turned takes longer.
+// Matrices of more than 64 rows: a launch for each step, a workgroup for 16 rows of S_k
+// and a wave for each of its tiles.  With all polynomials of S commuting, rows of
+// what a step needs come from the same rows and S alone:
+//   U = S S, Q = a + b S + c U, T = Q S, V = T S, S' = T Q = a T + b V + c V S, R' = Q R
+// so a wave keeps its 16 columns of S (rows, S being symmetric) and R in registers and only rows
+// pass through LDS.  (One workgroup with the matrix in LDS: 254 us for 16 matrices
+// of 128; a launch for each of 14 products: 92 us.)
 struct WideArgs {
   double a, b, c;
   int64_t m;               // matrices of the first problem
   int64_t size;            // values of a matrix's buffers
   double* base[2];         // of either problem
-  struct {
-    int x, y, out;         // buffers: out = x y, or with `step` a + b x + c x x
-  } p[2];                  // p[1].out < 0: one product
-  bool step;
-  int last;                // the product whose result is the last R, -1: none
-  float* R[2];
+  int s, s1, r, r1;        // buffers: S, S', R, R'
+  bool first, last;
+  float* R[2];             // the last R'
 };
-enum { kS0, kS1, kT, kQ0, kQ1, kR0, kR1, kWideBuffers };   // ortho_wide's seven
+enum { kS0, kS1, kR0, kR1, kWideBuffers };   // ortho_wide's four
 
 template <int B>
-__global__ __launch_bounds__(256) void wide_kernel(WideArgs a) {
-  constexpr int PP = 16 * B;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
-  const int t = blockIdx.y * 4 + wave, which = blockIdx.z, ti = t / B, tj = t % B;
-  if (t >= B * B) return;
-  const int64_t mat = blockIdx.x;
+__global__ __launch_bounds__(64 * B) void wide_kernel(WideArgs a) {
+  constexpr int PP = 16 * B, LD = PP + 2;
+  __shared__ __align__(16) double rows[16 * LD];
+  const int lane = threadIdx.x & 63, tj = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4, ti = blockIdx.y;
+  int64_t mat = blockIdx.x;
   const int side = mat >= a.m;
-  double* own = a.base[side] + (mat - (side ? a.m : 0)) * a.size;
-  const double* X = own + (int64_t)a.p[which].x * PP * PP + (16 * ti + r) * PP + 2 * h;   // of eight values of the contraction a lane has two
-  const double* Y = own + (int64_t)a.p[which].y * PP * PP + (16 * tj + r) * PP + 2 * h;
-  double2 x[2 * B], y[2 * B];
+  if (side) mat -= a.m;
+  double* own = a.base[side] + mat * a.size;
+  const double *S = own + a.s * PP * PP, *R = own + a.r * PP * PP;
+  // of eight values of the contraction a lane has two
+  double2 s[2 * B], rr[2 * B];
 #pragma unroll
-  for (int k = 0; k < 2 * B; ++k) {
-    x[k] = *reinterpret_cast<const double2*>(X + 8 * k);
-    y[k] = *reinterpret_cast<const double2*>(Y + 8 * k);
+  for (int k = 0; k < 2 * B; ++k) s[k] = *reinterpret_cast<const double2*>(S + (16 * tj + r) * PP + 8 * k + 2 * h);
+  if (!a.first)
+#pragma unroll
+    for (int k = 0; k < 2 * B; ++k) rr[k] = *reinterpret_cast<const double2*>(R + (16 * tj + r) * PP + 8 * k + 2 * h);
+  auto put = [&](const doublex4& v) {
+    __syncthreads();   // the rows before have been read
+#pragma unroll
+    for (int e = 0; e < 4; ++e) rows[(4 * e + h) * LD + 16 * tj + r] = v[e];
+    __syncthreads();
+  };
+  auto product = [&](const double2 (&y)[2 * B]) {
+    doublex4 acc[2] = {};
+#pragma unroll
+    for (int k = 0; k < 2 * B; ++k) {
+      const double2 x = *reinterpret_cast<const double2*>(rows + r * LD + 8 * k + 2 * h);
+      acc[0] = mfma64(x.x, y[k].x, acc[0]);
+      acc[1] = mfma64(x.y, y[k].y, acc[1]);
+    }
+    return acc[0] + acc[1];
+  };
+  auto write = [&](int buffer, const doublex4& v) {
+    double* to = own + buffer * PP * PP;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[(16 * ti + 4 * e + h) * PP + 16 * tj + r] = v[e];
+  };
+  doublex4 q;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q[e] = S[(16 * ti + 4 * e + h) * PP + 16 * tj + r];
+  put(q);
+  q = a.b * q + a.c * product(s);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (ti == tj && 4 * e + h == r) q[e] += a.a;
+  if (!a.first || !a.last) put(q);
+  doublex4 next = q;
+  if (!a.first) next = product(rr);
+  if (a.last) {
+    float* out = a.R[side] + mat * PP * PP;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[(16 * ti + 4 * e + h) * PP + 16 * tj + r] = (float)next[e];
+    return;
   }
-  double* out = own + (int64_t)a.p[which].out * PP * PP;
-  const double* S = own + (int64_t)a.p[which].x * PP * PP;
-  double at[4];
-  if (a.step)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) at[e] = S[(16 * ti + 4 * e + h) * PP + 16 * tj + r];
-  doublex4 acc[2] = {};
-#pragma unroll
-  for (int k = 0; k < 2 * B; ++k) {
-    acc[0] = mfma64(x[k].x, y[k].x, acc[0]);
-    acc[1] = mfma64(x[k].y, y[k].y, acc[1]);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int i = 16 * ti + 4 * e + h, j = 16 * tj + r;
-    double v = acc[0][e] + acc[1][e];
-    if (a.step) v = a.c * v + a.b * at[e] + (i == j ? a.a : 0.0);
-    if (which == a.last) a.R[side][(mat - (side ? a.m : 0)) * PP * PP + i * PP + j] = (float)v;
-    else out[i * PP + j] = v;
-  }
+  write(a.r1, next);
+  const doublex4 t = product(s);
+  put(t);
+  const doublex4 v = product(s);
+  put(v);
+  write(a.s1, a.a * t + a.b * v + a.c * product(s));
 }
 
 // S_0 / |G|^2 from its parts: a workgroup for each tile, each with the trace of all of them.
@@ -404,35 +426,14 @@ void wide(const OrthoArgs& a, int which, bool both, hipStream_t s) {
   }
   const int64_t mats = both ? 2 * a.m : a.m;
   hipLaunchKernelGGL(wide_start_kernel<B>, dim3((unsigned)mats, TILES), dim3(256), 0, s, a, which, w);
-  auto launch = [&](int products) {
-    hipLaunchKernelGGL(wide_kernel<B>, dim3((unsigned)mats, (B * B + 3) / 4, products), dim3(256), 0, s, w);
-  };
-  int S = kS0, R = -1;
   for (int k = 0; k < a.steps; ++k) {
-    const bool on = k + 1 < a.steps;
-    const int Q = k % 2 ? kQ1 : kQ0, S1 = S == kS0 ? kS1 : kS0;
-    w.step = true;
-    w.last = on || k > 0 ? -1 : 0;
-    w.p[0] = {S, S, Q};
-    launch(1);
-    w.step = false;
-    w.last = -1;
-    int n = 0;
-    if (on) w.p[n++] = {S, Q, kT};
-    if (k > 0) {
-      const int R1 = R == kR0 ? kR1 : kR0;
-      if (!on) w.last = n;
-      w.p[n++] = {Q, R, R1};
-      R = R1;
-    } else {
-      R = Q;
-    }
-    if (n > 0) launch(n);
-    w.last = -1;
-    if (!on) break;
-    w.p[0] = {kT, Q, S1};
-    launch(1);
-    S = S1;
+    w.first = k == 0;
+    w.last = k + 1 == a.steps;
+    w.s = k % 2 ? kS1 : kS0;
+    w.s1 = k % 2 ? kS0 : kS1;
+    w.r = k % 2 ? kR0 : kR1;
+    w.r1 = k % 2 ? kR1 : kR0;
+    hipLaunchKernelGGL(wide_kernel<B>, dim3((unsigned)mats, B), dim3(64 * B), 0, s, w);
   }
 }
 

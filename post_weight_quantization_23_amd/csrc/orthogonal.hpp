@@ -34,7 +34,7 @@ constexpr int kOrthoNarrow = 4;   // tile rows up to which a workgroup iterates 
 // fp64 values of a matrix's buffers in memory, for the iteration over many CUs.
 inline int64_t ortho_wide(int p) {
   const int64_t pp = 16 * ortho_blocks(p);
-  return ortho_blocks(p) > kOrthoNarrow ? 7 * pp * pp : 0;
+  return ortho_blocks(p) > kOrthoNarrow ? 4 * pp * pp : 0;
 }
 int ortho_splits(int64_t m, int64_t q, int64_t both);
 bool ortho_fits(int64_t m, int64_t q);
