@@ -328,7 +328,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
       const int64_t p = t0 + wn + 32 * q + m;
-      const int64_t y = p < count ? (a.target ? a.target[p] : (int64_t)a.k.col[p]) - v0 : -1;   // entry of the tile
+      int64_t y = p < count ? (a.target ? a.target[p] : (int64_t)a.k.col[p]) : -1;
+      y = (uint64_t)y < (uint64_t)a.vocab ? y - v0 : -1;   // entry of the tile
       if (last < P::TM) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
