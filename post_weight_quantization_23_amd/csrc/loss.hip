@@ -78,22 +78,26 @@ __global__ __launch_bounds__(1024) void keep_kernel(KeepArgs a) {
     for (int64_t p = tid; p < before; p += 1024) a.k.grad[p] = ldexpf(a.k.grad[p], e);
   }
   if (tid == 0) *a.k.down = ldexpf(1.f, -e);
-  if (tid == 0 && a.d > 0) {
-    // Parts of dX's contraction: rounds of tiles over the CUs (two of the smaller
-    // tiles each), at 1.75 us for 64 entries of the vocabulary, against writing and
-    // reading the parts, 5 ns for 1000 values (1536 tokens of 32000 x 4096: two parts
-    // and five both take 451 us).
-    const int64_t tile = a.large ? 256 : 128, slots = a.large ? 256 : 512;
+  if (tid < 64 && a.d > 0) {
+    // Parts of dX's contraction, a lane for each number of them: rounds of tiles over the
+    // CUs (two of the smaller tiles each), at 1.75 us for 64 entries of the vocabulary, against
+    // writing and reading the parts, 5 ns for 1000 values (1536 tokens of 32000 x 4096:
+    // two parts and five both take 451 us).
+    const int64_t tile = a.large ? 256 : 128;
+    const float slots = a.large ? 256.f : 512.f, parts = lane + 1;
     const int64_t tiles = (before + tile - 1) / tile * ((a.d + tile - 1) / tile), steps = (a.width + 63) / 64;
-    const float whole = steps * (a.large ? 1.75f : 1.f), join = (float)before * a.d * 5e-6f;
-    int best = 1;
-    float least = whole * ((tiles + slots - 1) / slots);
-    for (int s = 2; s <= kMostSplits && tiles * s <= kMostParts && steps >= 8 * s; ++s) {
-      const float us = whole * ((tiles * s + slots - 1) / slots) / s + join * s;
-      if (us < least) least = us, best = s;
+    const bool can = lane == 0 || (lane < kMostSplits && tiles * (lane + 1) <= kMostParts && steps >= 8 * (lane + 1));
+    const float us = steps * (a.large ? 1.75f : 1.f) * ceilf(tiles * parts / slots) / parts + (lane ? before * a.d * 5e-6f * parts : 0.f);
+    float least = can ? us : INFINITY;
+    int best = lane + 1;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const float other = __shfl_xor(least, o);
+      const int of = __shfl_xor(best, o);
+      if (other < least || (other == least && of < best)) least = other, best = of;
     }
     const int64_t each = (steps + best - 1) / best;   // of equal length, none empty
-    *a.k.splits = steps > 0 ? (int)((steps + each - 1) / each) : 1;
+    if (lane == 0) *a.k.splits = steps > 0 ? (int)((steps + each - 1) / each) : 1;
   }
 }
 

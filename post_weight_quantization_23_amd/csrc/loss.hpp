@@ -6,9 +6,9 @@
 namespace gptq {
 
 // Tiles of logits, entries of the vocabulary x tokens.
-enum LossShape { k256x256, k128x128, k128x64, k128x32 };
-LossShape loss_shape(int64_t n);
-inline int64_t loss_entries(LossShape s) { return s == k256x256 ? 256 : 128; }
+enum LossShape { k256x256, k128x128, k128x64, k128x32, kFew };   // kFew: 32 entries, up to 64 tokens
+LossShape loss_shape(int64_t n, int64_t vocab);
+inline int64_t loss_entries(LossShape s) { return s == k256x256 ? 256 : s == kFew ? 32 : 128; }
 // Up to as many tokens one or two tiles hold them all, and leaving tokens out
 // saves little work: they are taken as they lie (forward).
 constexpr int64_t kFewTokens = 256;
@@ -69,7 +69,7 @@ GPTQ_DEV void add_row(const uint16_t* row, float much, float (&v)[8]) {
 struct LossArgs {
   const uint16_t* W;
   int64_t ldw, vocab, n, d;
-  const uint16_t* rows;    // [n][ldr], zero past d up to a whole step, or d itself a whole number of them
+  const uint16_t* rows;    // [n][ldr], on 16 bytes
   int64_t ldr;
   const int64_t* target;   // not null: all n tokens as they lie, k unused (forward)
   Kept k;
@@ -122,7 +122,7 @@ constexpr int64_t kMostParts = 768;   // tiles times parts, where there are seve
 // Entries of a piece.
 int64_t loss_piece(int64_t n, int64_t vocab);
 inline int64_t loss_tiles(int64_t n, int64_t vocab) {
-  const int64_t e = loss_entries(loss_shape(n));
+  const int64_t e = loss_entries(loss_shape(n, vocab));
   return (vocab + e - 1) / e;
 }
 // Whether rows of X can be taken as they lie.

@@ -298,15 +298,121 @@ GPTQ_DEV void tile_at(int64_t place, int tok_tiles, int col_tiles, int& tok, int
 }
 
 // ---------------------------------------------------------------- logits
-// Tiles of TM vocabulary entries (rows of the accumulators) x TN kept tokens
-// (columns): a lane holds most of a token's entries itself, so the largest and the sum
-// cost one exchange between lanes.
+// What becomes of a tile of WM x WN waves of 32 MT vocabulary entries (rows of the
+// accumulators) x 32 NT tokens (columns): a lane holds most of a token's entries
+// itself, so the largest and the sum cost one exchange between lanes.  A wave's tile starts
+// at entry wm and token wn; lds is free.  Entry of a lane's value: wm + 4 (lane >> 5) + 32 i + within(e).
+GPTQ_DEV constexpr int within(int e) { return 8 * (e >> 2) + (e & 3); }
+
+// Statistics of entries v0 .. of tile vt, and the targets' logits.  Every wave of the
+// workgroup calls it unless WM is 1.
+template <int MT, int NT, int WM, int WN>
+GPTQ_DEV void finish_loss(const LossArgs& a, floatx16 (&acc)[MT][NT], unsigned char* lds, int64_t count, int64_t t0, int64_t v0, int vt,
+                          int wave) {
+  constexpr int TM = 32 * MT * WM, TN = 32 * NT * WN;
+  const int lane = threadIdx.x & 63, m = lane & 31, wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
+  const int lowest = wm + 4 * (lane >> 5), last = (int)min(a.width - v0, (int64_t)TM);   // entries of this tile
+  float2* part = reinterpret_cast<float2*>(lds);   // [WM][TN]
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int64_t p = t0 + wn + 32 * q + m;
+    int64_t y = p < count ? (a.target ? a.target[p] : (int64_t)a.k.col[p]) : -1;
+    y = (uint64_t)y < (uint64_t)a.vocab ? y - v0 : -1;   // entry of the tile
+    if (last < TM) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (32 * i + within(e) >= last - lowest) acc[i][q][e] = -INFINITY;
+    }
+    if (__any(y >= wm && y < wm + 32 * MT)) {
+      const int own = (int)y - lowest;   // in range where it counts
+      float z = 0.f;
+      bool mine = false;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (32 * i + within(e) == own) z = acc[i][q][e], mine = true;
+      if (mine && y >= 0 && y < last) a.at_target[p] = z;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][q][e]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum += __builtin_amdgcn_exp2f((acc[i][q][e] - ref) * kLog2e);
+    sum += __shfl_xor(sum, 32);
+    if (lane >= 32) continue;
+    if constexpr (WM > 1) part[(wave / WN) * TN + wn + 32 * q + m] = float2{top, sum};
+    else if (p < count) a.part[(int64_t)vt * a.n + p] = float2{top, sum};
+  }
+  if constexpr (WM > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < TN; c += 64 * WM * WN) {
+      float2 v = part[c];
+#pragma unroll
+      for (int i = 1; i < WM; ++i) v = join_sums(v, part[i * TN + c]);
+      if (t0 + c < count) a.part[(int64_t)vt * a.n + t0 + c] = v;
+    }
+  }
+}
+
+// Rows of D, rounded, a wave's tokens 32 at a time as rows of its `own` LDS (32 x
+// (32 MT + 8) values), so that they leave in whole runs.
+template <int DT, int MT, int NT, int WM, int WN>
+GPTQ_DEV void finish_grad(const LossArgs& a, const floatx16 (&acc)[MT][NT], uint16_t* own, int64_t count, int64_t t0, int64_t v0, int wave) {
+  constexpr int TM = 32 * MT * WM, W = 32 * MT, LD = W + 8, RUNS = W / 8;
+  const int lane = threadIdx.x & 63, m = lane & 31, wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
+  const int lowest = wm + 4 * (lane >> 5), last = (int)min(a.width - v0, (int64_t)TM);
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int64_t p = t0 + wn + 32 * q + m;
+    const int64_t y = p < count ? (int64_t)a.k.col[p] - a.v0 - v0 : -1;
+    const int own_row = (int)y - lowest;
+    const float lse = p < count ? a.k.lse[p] : 0.f, g = p < count ? a.k.grad[p] : 0.f;
+    float target = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        float v[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const int at = 32 * i + within(e + f);
+          v[f] = __builtin_amdgcn_exp2f((acc[i][q][e + f] - lse) * kLog2e);
+          if (at == own_row) v[f] -= 1.f;
+          v[f] = at < last - lowest ? v[f] * g : 0.f;
+          target = at == own_row ? v[f] : target;
+        }
+        *reinterpret_cast<uint2*>(own + m * LD + 32 * i + within(e) + 4 * (lane >> 5)) = uint2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+      }
+    // the lane that holds the target's entry
+    if (y >= wm && y < wm + 32 * MT && ((int)y >> 2 & 1) == lane >> 5)
+      a.k.rest[p] = target - f16_to_f32<DT>(f32_to_16<DT>(target));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int k = 0; k < RUNS / 2; ++k) {
+      const int run = 64 * k + lane, r = run / RUNS, c = 8 * (run % RUNS);
+      const int64_t at = t0 + wn + 32 * q + r;
+      if (at < count && v0 + wm + c < a.ldp)
+        *reinterpret_cast<u32x4*>(a.P + at * a.ldp + v0 + wm + c) = *reinterpret_cast<const u32x4*>(own + r * LD + c);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
 template <int DT, bool GRAD, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int voc_tiles) {
   using P = Product<DT, false, false, MT, NT, WM, WN>;
   extern __shared__ __align__(16) unsigned char lsm[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31;
-  const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t count = !GRAD && a.target ? a.n : *a.k.count;
   const int tok_tiles = (int)((count + P::TN - 1) / P::TN);
   const int64_t all = (int64_t)tok_tiles * voc_tiles;
@@ -314,103 +420,81 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
   int tt, vt;
   tile_at(place_of(blockIdx.x, all), tok_tiles, voc_tiles, tt, vt);
   const int64_t t0 = (int64_t)tt * P::TN, v0 = (int64_t)vt * P::TM;
-  const int64_t steps = (a.d + LK - 1) / LK;
-  const Source w{a.W + a.v0 * a.ldw, a.ldw, a.width, a.d}, x{a.rows, a.ldr, count, steps * LK};
+  const Source w{a.W + a.v0 * a.ldw, a.ldw, a.width, a.d}, x{a.rows, a.ldr, count, a.d};
   floatx16 acc[MT][NT];
-  P::run(w, x, v0, t0, 0, steps, lsm, acc);
-  const int last = (int)min(a.width - v0, (int64_t)P::TM);   // entries of this tile
-  // entry of a lane's value: lowest + 32 i + within(e)
-  const int lowest = wm + 4 * (lane >> 5);
-  constexpr auto within = [](int e) { return 8 * (e >> 2) + (e & 3); };
-
-  if constexpr (!GRAD) {
-    float2* part = reinterpret_cast<float2*>(lsm);   // [WM][TN]
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      const int64_t p = t0 + wn + 32 * q + m;
-      int64_t y = p < count ? (a.target ? a.target[p] : (int64_t)a.k.col[p]) : -1;
-      y = (uint64_t)y < (uint64_t)a.vocab ? y - v0 : -1;   // entry of the tile
-      if (last < P::TM) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (32 * i + within(e) >= last - lowest) acc[i][q][e] = -INFINITY;
-      }
-      if (__any(y >= wm && y < wm + 32 * MT)) {
-        const int own = (int)y - lowest;   // in range where it counts
-        float z = 0.f;
-        bool mine = false;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (32 * i + within(e) == own) z = acc[i][q][e], mine = true;
-        if (mine && y >= 0 && y < last) a.at_target[p] = z;
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][q][e]);
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float ref = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum += __builtin_amdgcn_exp2f((acc[i][q][e] - ref) * kLog2e);
-      sum += __shfl_xor(sum, 32);
-      if (lane < 32) part[(wave / WN) * P::TN + wn + 32 * q + m] = float2{top, sum};
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < P::TN; c += 64 * WM * WN) {
-      float2 v = part[c];
-#pragma unroll
-      for (int i = 1; i < WM; ++i) v = join_sums(v, part[i * P::TN + c]);
-      if (t0 + c < count) a.part[(int64_t)vt * a.n + t0 + c] = v;
-    }
+  P::run(w, x, v0, t0, 0, (a.d + LK - 1) / LK, lsm, acc);
+  if constexpr (GRAD) {
+    static_assert(WM * WN * 32 * (32 * MT + 8) * 2 <= 2 * P::BUF, "results fit the operands' LDS");
+    finish_grad<DT, MT, NT, WM, WN>(a, acc, reinterpret_cast<uint16_t*>(lsm) + wave * 32 * (32 * MT + 8), count, t0, v0, wave);
   } else {
-    // a wave's tokens, 32 at a time, as rows of LDS, so that they leave in whole runs
-    constexpr int W = 32 * MT, LD = W + 8, RUNS = W / 8;
-    static_assert(WM * WN * 32 * LD * 2 <= 2 * P::BUF, "results fit the operands' LDS");
-    uint16_t* own = reinterpret_cast<uint16_t*>(lsm) + wave * 32 * LD;
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      const int64_t p = t0 + wn + 32 * q + m;
-      const int64_t y = p < count ? (int64_t)a.k.col[p] - a.v0 - v0 : -1;
-      const int own_row = (int)y - lowest;
-      const float lse = p < count ? a.k.lse[p] : 0.f, g = p < count ? a.k.grad[p] : 0.f;
-      float target = 0.f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          float v[4];
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const int at = 32 * i + within(e + f);
-            v[f] = __builtin_amdgcn_exp2f((acc[i][q][e + f] - lse) * kLog2e);
-            if (at == own_row) v[f] -= 1.f;
-            v[f] = at < last - lowest ? v[f] * g : 0.f;
-            target = at == own_row ? v[f] : target;
-          }
-          *reinterpret_cast<uint2*>(own + m * LD + 32 * i + within(e) + 4 * (lane >> 5)) = uint2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-        }
-      // the lane that holds the target's entry (row 4 h + within() of some set)
-      if (y >= wm && y < wm + 32 * MT && ((int)y >> 2 & 1) == lane >> 5)
-        a.k.rest[p] = target - f16_to_f32<DT>(f32_to_16<DT>(target));
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-      for (int k = 0; k < RUNS / 2; ++k) {
-        const int run = 64 * k + lane, r = run / RUNS, c = 8 * (run % RUNS);
-        const int64_t at = t0 + wn + 32 * q + r;
-        if (at < count && v0 + wm + c < a.ldp)
-          *reinterpret_cast<u32x4*>(a.P + at * a.ldp + v0 + wm + c) = *reinterpret_cast<const u32x4*>(own + r * LD + c);
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
+    finish_loss<MT, NT, WM, WN>(a, acc, lsm, count, t0, v0, vt, wave);
   }
+}
+
+// Up to 64 tokens of a vocabulary whose tiles of 128 entries would leave most CUs idle: what
+// bounds those is how long a workgroup walks along the contraction.  Here one takes 32
+// entries, its eight waves share the contraction out among them, straight from memory to
+// registers and without a barrier, and are added up in LDS at the end.  A token of
+// 4000 x 8192 take 26 us instead of 60, both gradients of 6 of 2553 x 6376 52
+// instead of 98; but pieces of 32 bytes of each row are poorer loads than LDS tiles' once there
+// are enough of those.  A call on 1 and 64 tokens of 8000 x 4096 takes 19 and 36 us here, 36 and
+// 41 in tiles; of 12000 x 4096 34 and 60 against 37 and 44.
+constexpr int64_t kFewVocab = 8192;
+constexpr int FEW_WAVES = 8;
+
+template <int DT, bool GRAD, int NT>
+__global__ __launch_bounds__(64 * FEW_WAVES) void few_kernel(LossArgs a) {
+  constexpr int AHEAD = 8 / NT;   // sets of 16 values of the contraction in flight
+  __shared__ __align__(16) float sums[FEW_WAVES - 1][NT][16 * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = lane & 31, h = lane >> 5;
+  const int64_t count = !GRAD && a.target ? a.n : *a.k.count, v0 = (int64_t)blockIdx.x * 32;
+  const int d = (int)a.d;
+  const bool row = v0 + m < a.width;
+  const uint16_t* w = a.W + (a.v0 + min(v0 + m, a.width - 1)) * a.ldw + 8 * h;
+  const uint16_t* x[NT];
+  bool there[NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    there[q] = 32 * q + m < count;
+    x[q] = a.rows + (there[q] ? 32 * q + m : 0) * a.ldr + 8 * h;
+  }
+  floatx16 acc[1][NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) acc[0][q] = floatx16{};
+  for (int k0 = 16 * AHEAD * wave; k0 < d; k0 += 16 * AHEAD * FEW_WAVES) {
+    u32x4 u[AHEAD], v[NT][AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const bool in = k0 + 16 * j + 8 * h < d;
+      u[j] = u32x4{0u, 0u, 0u, 0u};
+      if (row && in) u[j] = *reinterpret_cast<const u32x4*>(w + k0 + 16 * j);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        v[q][j] = u32x4{0u, 0u, 0u, 0u};
+        if (there[q] && in) v[q][j] = *reinterpret_cast<const u32x4*>(x[q] + k0 + 16 * j);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) acc[0][q] = mfma32<DT>(u[j], v[q][j], acc[0][q]);
+  }
+  if (wave > 0)
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sums[wave - 1][q][64 * e + lane] = acc[0][q][e];
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll 1
+  for (int i = 0; i < FEW_WAVES - 1; ++i)
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[0][q][e] += sums[i][q][64 * e + lane];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if constexpr (GRAD) finish_grad<DT, 1, NT, 1, 1>(a, acc, reinterpret_cast<uint16_t*>(&sums[0][0][0]), count, 0, v0, 0);
+  else finish_loss<1, NT, 1, 1>(a, acc, nullptr, count, 0, v0, (int)blockIdx.x, 0);
 }
 
 // ---------------------------------------------------------------- gradients
@@ -536,11 +620,15 @@ void logits(const LossArgs& a, hipStream_t s) {
 
 template <int DT, bool GRAD>
 void logits_shape(const LossArgs& a, hipStream_t s) {
-  switch (loss_shape(a.n)) {
+  switch (loss_shape(a.n, a.vocab)) {
     case k256x256: return logits<DT, GRAD, 4, 2, 2, 4>(a, s);
     case k128x128: return logits<DT, GRAD, 2, 2, 2, 2>(a, s);
     case k128x64: return logits<DT, GRAD, 1, 2, 4, 1>(a, s);
     case k128x32: return logits<DT, GRAD, 1, 1, 4, 1>(a, s);
+    case kFew:
+      const dim3 grid((unsigned)tiles_of(GRAD ? a.ldp : a.width, 32));   // D is read up to its row stride
+      if (a.n > 32) hipLaunchKernelGGL((few_kernel<DT, GRAD, 2>), grid, dim3(64 * FEW_WAVES), 0, s, a);
+      else hipLaunchKernelGGL((few_kernel<DT, GRAD, 1>), grid, dim3(64 * FEW_WAVES), 0, s, a);
   }
 }
 
@@ -595,7 +683,8 @@ int64_t grad_x_part_floats(int64_t n, int64_t d, bool pieces) {
 // tokens (50, 30 and 10 % of them without a target; 32000 x 4096, 50021 x 4096, 50021
 // x 1024) took 76, 216 and 158 us in the former, 111, 225 and 174 in the latter; of
 // 2048 tokens of 32000 x 4096 645 and 570.  (256 x 128: 91, 268, 170 and 680.)
-LossShape loss_shape(int64_t n) {
+LossShape loss_shape(int64_t n, int64_t vocab) {
+  if (n <= 64 && vocab <= kFewVocab) return kFew;
   if (n <= 32) return k128x32;
   if (n <= 64) return k128x64;
   return n <= 1024 ? k128x128 : k256x256;
@@ -609,12 +698,12 @@ int64_t loss_piece(int64_t n, int64_t vocab) {
 }
 
 bool loss_takes(const void* X, int64_t n, int64_t d, int64_t ldx) {
-  return n <= kFewTokens && reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0 && ldx < (int64_t(1) << 22) && d % LK == 0;
+  return n <= kFewTokens && reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx % 8 == 0 && ldx < (int64_t(1) << 22);
 }
 
 bool loss_fits(int64_t n, int64_t vocab, int64_t d, bool grad) {
-  constexpr int64_t tokens[] = {256, 128, 64, 32};
-  if (!grid_fits(tiles_of(n, tokens[loss_shape(n)]) * loss_tiles(n, vocab), 512)) return false;
+  constexpr int64_t tokens[] = {256, 128, 64, 32, 64};
+  if (!grid_fits(tiles_of(n, tokens[loss_shape(n, vocab)]) * loss_tiles(n, vocab), 512)) return false;
   if (!grid_fits(tiles_of(n * (gemm16_depth(d) / 8), 256), 256)) return false;
   if (!grad) return true;
   const int64_t tile = grad_x_large(n) ? 256 : 128;

@@ -120,7 +120,7 @@ def check(name, got, want, bound):
     assert bool(torch.isfinite(got.double()).all()) and worst <= 1.0, (name, worst)
 
 
-SIZES = [(1, 1, 8), (1, 257, 8), (3, 255, 64), (17, 1000, 72), (64, 300, 136), (65, 513, 64), (128, 256, 320), (129, 777, 128),
+SIZES = [(1, 1, 8), (2, 8200, 136), (40, 8193, 72), (33, 5000, 1160), (1, 257, 8), (3, 255, 64), (17, 1000, 72), (64, 300, 136), (65, 513, 64), (128, 256, 320), (129, 777, 128),
          (300, 1031, 520), (513, 2049, 264), (1000, 4099, 96)]
 
 
