@@ -19,7 +19,7 @@ struct Kept {
   int32_t* token;
   int32_t* place_of;
   int32_t* col;
-  float* lse;       // of each place (backward), as grad: dloss, for fp16 times `up`
+  float* lse;       // of each place (backward), as grad: dloss, for fp16 times 1 / *down
   float* grad;
   int32_t* count;
   float* down;      // what results are multiplied by (a power of two, 1 for bf16)
@@ -52,6 +52,15 @@ struct GatherArgs {
   bool vec_dx;
 };
 void launch_gather_kept(GatherArgs a, hipStream_t s);
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The largest of two sets of values and the sum of exponentials against it.  A set
+// that holds nothing is (-inf, 0).
+GPTQ_DEV float2 join_sums(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x), r = m == -INFINITY ? 0.f : m;
+  return float2{m, a.y * __builtin_amdgcn_exp2f((a.x - r) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - r) * kLog2e)};
+}
 
 // v += much x eight 16-bit values (on 16 bytes).
 template <int DT>

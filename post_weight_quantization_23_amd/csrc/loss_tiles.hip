@@ -4,6 +4,9 @@
 // loads, one barrier a step), each either contiguous along the contraction or
 // across it.  Operands across it are read from LDS transposed (ds_read_b64_tr), so
 // that neither W, the rows nor the gradients are ever laid out a second time.
+// Tiles of 256 x 256 run at 1.24 PFLOP/s for statistics (8192 tokens of 128000 x 4096, matrix
+// cores busy 67 % at the 1.75 GHz that the power limit leaves), and of 4096 tokens
+// of 32000 x 4096 at 1.15 for D (its 262 MB written), 1.28 for dX and 1.17 for dW.
 #include "loss.hpp"
 
 namespace gptq {
@@ -16,7 +19,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
 constexpr int LK = 64;   // contraction step
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kOutside = 0x7FFFFFFF;   // an offset past every record
 
 // An operand: E entries (rows of A, columns of B) of a tile and LK values of the
@@ -274,14 +276,6 @@ struct Product {
 };
 static_assert(LK == 64, "a step is four times 16 values, the last of them in set 1");
 
-// ---------------------------------------------------------------- softmax statistics
-// The largest of two sets of values and the sum of exponentials against it.  A set
-// that holds nothing is (-inf, 0).
-GPTQ_DEV float2 join_sums(float2 a, float2 b) {
-  const float m = fmaxf(a.x, b.x), r = m == -INFINITY ? 0.f : m;
-  return float2{m, a.y * __builtin_amdgcn_exp2f((a.x - r) * kLog2e) + b.y * __builtin_amdgcn_exp2f((b.x - r) * kLog2e)};
-}
-
 // ---------------------------------------------------------------- tile order
 // Place b of the walk over `all` tiles: of 256 workgroups, which the dispatcher deals round
 // robin to the 8 XCDs, each XCD gets 32 consecutive places.  Tiles past the kept
@@ -435,7 +429,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void logits_kernel(LossArgs a, int
 // bounds those is how long a workgroup walks along the contraction.  Here one takes 32
 // entries, its eight waves share the contraction out among them, straight from memory to
 // registers and without a barrier, and are added up in LDS at the end.  A token of
-// 4000 x 8192 take 26 us instead of 60, both gradients of 6 of 2553 x 6376 52
+// 4000 x 8192 takes 26 us instead of 60, both gradients of 6 tokens of 2553 x 6376 52
 // instead of 98; but pieces of 32 bytes of each row are poorer loads than LDS tiles' once there
 // are enough of those.  A call on 1 and 64 tokens of 8000 x 4096 takes 19 and 36 us here, 36 and
 // 41 in tiles; of 12000 x 4096 34 and 60 against 37 and 44.
