@@ -49,7 +49,7 @@ __global__ __launch_bounds__(1024) void keep_kernel(KeepArgs a) {
       if (mine) {
         a.k.token[p] = (int32_t)t;
         a.k.col[p] = (int32_t)y[k];
-        if (a.lse_in) {
+        if (a.grad) {
           const float g = a.dloss ? a.dloss[t] : 1.f;
           a.k.lse[p] = a.lse_in[t];
           a.k.grad[p] = g;
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(1024) void keep_kernel(KeepArgs a) {
     __syncthreads();   // before the counts are replaced
   }
   if (tid == 0) *a.k.count = (int32_t)before;
-  if (!a.lse_in) return;
+  if (!a.grad) return;
   int e = 0;   // grad = dloss 2^e
   if (a.half) {
 #pragma unroll

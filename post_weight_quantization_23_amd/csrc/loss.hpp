@@ -31,7 +31,8 @@ struct KeepArgs {
   const int64_t* target;
   int64_t n, vocab;
   float *loss, *lse;              // forward: zeroed where there is no target
-  const float *lse_in, *dloss;    // backward (dloss null: 1)
+  bool grad;                      // backward (also without tokens, and so without pointers)
+  const float *lse_in, *dloss;    // ... (dloss null: 1)
   bool half;                      // fp16 gradients
   int64_t d, width;               // dX: columns, and entries of a piece
   bool large;                     // ... in tiles of 256 x 256

@@ -247,6 +247,7 @@ gptq_status gptq_linear_cross_entropy_backward(const void* X, gptq_dtype xt, int
   k.target = target;
   k.n = n;
   k.vocab = vocab;
+  k.grad = true;
   k.lse_in = lse;
   k.dloss = dloss;
   k.half = xt == GPTQ_F16;
