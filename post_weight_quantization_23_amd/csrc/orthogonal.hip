@@ -104,46 +104,24 @@ GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, floa
     for (int e = 0; e < LD; ++e)
       if (threadIdx.x + GRAM_THREADS * e < R::PER) next[e] = R::fetch(o, type, mat, k0, threadIdx.x + GRAM_THREADS * e);
   };
-  auto put = [&](float* to) {
+  if (first < last) fetch(first);
+  for (int64_t k0 = first; k0 < last; k0 += KS) {
+    __syncthreads();   // the last run has been read
 #pragma unroll
     for (int e = 0; e < LD; ++e)
-      if (threadIdx.x + GRAM_THREADS * e < R::PER) R::put(to, R::GRAM, threadIdx.x + GRAM_THREADS * e, next[e]);
-  };
-  // two buffers: a run goes to LDS while the one before is multiplied, the next is on its way
-  if (first < last) {
-    fetch(first);
-    put(lds);
-    if (first + KS < last) fetch(first + KS);
-  }
-  int at = 0;
-  for (int64_t k0 = first; k0 < last; k0 += KS, at ^= 1) {
-    __syncthreads();   // this run is there, the one before has been read
-    if (k0 + KS < last) {
-      put(lds + (at ^ 1) * R::FLOATS);
-      if (k0 + 2 * KS < last) fetch(k0 + 2 * KS);
-    }
+      if (threadIdx.x + GRAM_THREADS * e < R::PER) R::put(lds, R::GRAM, threadIdx.x + GRAM_THREADS * e, next[e]);
+    __syncthreads();
+    if (k0 + KS < last) fetch(k0 + KS);
     if (share >= SHARE) continue;
-    const float* g = lds + at * R::FLOATS;
-    // fragments of a step are read before the last one's products: behind a tile's condition
-    // each product waited for its own (rank 128: 64 us)
-    float f[B + 2];
-    auto read = [&](int k) {
-#pragma unroll
-      for (int t = 0; t < B; ++t) f[t] = R::get(g, R::GRAM, 16 * t + r, k + h);
-      f[B] = R::get(g, R::GRAM, 16 * i0 + r, k + h);
-      f[B + 1] = R::get(g, R::GRAM, 16 * i1 + r, k + h);
-    };
-    read(4 * share);
     for (int k1 = 0; k1 < KS; k1 += 4 * SHARE) {
-      double b[B + 2];
-#pragma unroll
-      for (int t = 0; t < B + 2; ++t) b[t] = (double)f[t];
-      if (k1 + 4 * SHARE < KS) read(k1 + 4 * SHARE + 4 * share);
+      const int k = k1 + 4 * share;
+      const double a0 = R::get(lds, R::GRAM, 16 * i0 + r, k + h), a1 = R::get(lds, R::GRAM, 16 * i1 + r, k + h);
 #pragma unroll
       for (int t = 0; t < B; ++t)
         if (t >= i0) {
-          up[t] = mfma64(b[B], b[t], up[t]);
-          if (t >= i1 && i1 != i0) low[t] = mfma64(b[B + 1], b[t], low[t]);
+          const double b = R::get(lds, R::GRAM, 16 * t + r, k + h);
+          up[t] = mfma64(a0, b, up[t]);
+          if (t >= i1 && i1 != i0) low[t] = mfma64(a1, b, low[t]);
         }
     }
   }
@@ -169,7 +147,7 @@ GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, floa
 
 template <int B>
 __global__ __launch_bounds__(GRAM_THREADS) void gram_kernel(OrthoArgs a, int which, int type, int64_t blocks0) {
-  constexpr int RUN = 2 * (Run<B, true>::FLOATS > Run<B, false>::FLOATS ? Run<B, true>::FLOATS : Run<B, false>::FLOATS), SUM = 512 * ortho_tiles(16 * B);
+  constexpr int RUN = Run<B, true>::FLOATS > Run<B, false>::FLOATS ? Run<B, true>::FLOATS : Run<B, false>::FLOATS, SUM = 512 * ortho_tiles(16 * B);
   __shared__ __align__(16) float lds[RUN > SUM ? RUN : SUM];
   int64_t b = blockIdx.x;
   if (b >= blocks0) b -= blocks0, which = 1;
@@ -211,7 +189,6 @@ struct Chain {
 #pragma unroll
     for (int e = 0; e < MOST; ++e) acc[e] = doublex4{0, 0, 0, 0};
     if (wave >= WAVES) return;
-#pragma unroll
     for (int tk = 0; tk < B; ++tk) {
       double x[MOST][4], y[MOST][4];
 #pragma unroll
