@@ -93,7 +93,9 @@ gptq_status gptq_linear_cross_entropy_backward(const void* X, gptq_dtype xt, int
  * which is the same), `steps` times; out = M_steps.  The singular vectors stay, the
  * singular values s become p(p(..p(s))), p(s) = a s + b s^3 + c3 s^5.
  * The iteration runs on S in 64 bits: S_{k+1} = S_k q(S_k)^2 with q(S) = a + b S + c3 S^2,
- * out = q(S_{steps-1}) .. q(S_0) M_0, whose last product is in fp32.
+ * out = q(S_{steps-1}) .. q(S_0) M_0.  S is formed again from M_k, also in 64 bits, where an error of it
+ * would have grown by more than 2^16, a^2 a step (after 5 steps of a = 3.4445), so that
+ * matrices of less than full rank stay so.  Nothing is rounded to fewer bits but the result, once.
  *
  * G_A    : m x rank x c of type gt (GPTQ_F32, GPTQ_BF16 or GPTQ_F16), dense, aligned
  *          to its elements; NULL: not wanted (out_A is then ignored).

@@ -5,12 +5,18 @@
 // long side of M is read twice only, for S_0 and for the result
 // q(S_{n-1}) .. q(S_0) M_0.  An error d in S_0 grows by a^2 (11.9 for the usual
 // coefficients) a step and moves singular values s near 1e-3 by 1e7 s d: 32 bits
-// would leave 1e-3 there, so S_0 and the iteration are held in 64.
+// would leave 1e-3 there, so S_0 and the iteration are held in 64.  So are R = q .. q, which is
+// a^n where M has no part, and its product with M_0, where those parts have to cancel
+// (five steps of a row repeated 128 times: off by 4e-4 with R and the product in 32 bits).
+// Rounding leaves eigenvalues of S_0 near -1e-17 where they are zero, and below zero
+// nothing bounds s q(s)^2 (16 steps of such a matrix: values of 1e7).  After as many steps as
+// a^2 may multiply up to 2^16 (five) S is therefore formed again, from M = R M_0, run by
+// run of the long side, and is positive again but for rounding of its own.
 // Launches: parts of S_0 over the long side, the iteration, the result.  Up to 64 rows a
 // workgroup iterates a matrix by itself; above that (more 64-bit products than one
 // CU is quick at) a launch takes a step of all matrices on many.  An adapter of rank
-// 16 beside 4096 x 4096 takes 19 us, five of rank 64 beside 11008 x 4096 79 us (S_0
-// 19, iteration 45, result 16), eight of rank 128 220 us (63, 112 in six launches, 56).
+// 16 beside 4096 x 4096 takes 19 us, five of rank 64 beside 11008 x 4096 87 us (S_0
+// 19, iteration 45, result 25), eight of rank 128 262 us (65, 112 in six launches, 99).
 #include "orthogonal.hpp"
 
 namespace gptq {
@@ -81,13 +87,15 @@ struct Run {
 
 // ---------------------------------------------------------------- S_0
 // Parts of G G^T over the long side; 64-bit products bound it (rank 128: its operations take 33 us
-// at 67 TFLOP/s, the kernel 63).  A wave holds tile rows i and B-1-i of the upper
+// at 67 TFLOP/s, the kernel 65).  A wave holds tile rows i and B-1-i of the upper
 // half, B+1 tiles whatever i is, so a fragment of the run serves several products;
 // the waves with the same rows share the run's values out among them and
 // are added up through LDS in their order.
+// AGAIN: of R G / |G| instead, of which each run is made in LDS first.
 constexpr int GRAM_THREADS = 512;
+constexpr int MADE = KS + 4;   // values of a row of it (banks)
 
-template <int B, bool TALL>
+template <int B, bool TALL, bool AGAIN>
 GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, float* lds) {
   using R = Run<B, TALL>;
   constexpr int PAIRS = (B + 1) / 2, SHARE = GRAM_THREADS / 64 / PAIRS, TILES = ortho_tiles(16 * B);
@@ -99,6 +107,9 @@ GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, floa
 #pragma unroll
   for (int t = 0; t < B; ++t) up[t] = low[t] = doublex4{0, 0, 0, 0};
   floatx4 next[LD];
+  double* made = reinterpret_cast<double*>(lds + R::FLOATS);   // [16 B][MADE]
+  static_assert(R::FLOATS % 2 == 0, "64-bit values behind the run");
+  auto value = [&](int s, int l) { return AGAIN ? made[s * MADE + l] : (double)R::get(lds, R::GRAM, s, l); };
   auto fetch = [&](int64_t k0) {
 #pragma unroll
     for (int e = 0; e < LD; ++e)
@@ -112,14 +123,25 @@ GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, floa
       if (threadIdx.x + GRAM_THREADS * e < R::PER) R::put(lds, R::GRAM, threadIdx.x + GRAM_THREADS * e, next[e]);
     __syncthreads();
     if (k0 + KS < last) fetch(k0 + KS);
+    if constexpr (AGAIN) {
+      const double *by = o.R + mat * o.apart, inv = o.inv[mat];
+      for (int t = wave; t < B * (KS / 16); t += GRAM_THREADS / 64) {
+        const int i = 16 * (t / (KS / 16)), j = 16 * (t % (KS / 16));
+        doublex4 v = {0, 0, 0, 0};
+        for (int k = 0; k < 16 * B; k += 4) v = mfma64(by[(k + h) * 16 * B + i + r], (double)R::get(lds, R::GRAM, k + h, j + r), v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) made[(i + 4 * e + h) * MADE + j + r] = v[e] * inv;
+      }
+      __syncthreads();
+    }
     if (share >= SHARE) continue;
     for (int k1 = 0; k1 < KS; k1 += 4 * SHARE) {
       const int k = k1 + 4 * share;
-      const double a0 = R::get(lds, R::GRAM, 16 * i0 + r, k + h), a1 = R::get(lds, R::GRAM, 16 * i1 + r, k + h);
+      const double a0 = value(16 * i0 + r, k + h), a1 = value(16 * i1 + r, k + h);
 #pragma unroll
       for (int t = 0; t < B; ++t)
         if (t >= i0) {
-          const double b = R::get(lds, R::GRAM, 16 * t + r, k + h);
+          const double b = value(16 * t + r, k + h);
           up[t] = mfma64(a0, b, up[t]);
           if (t >= i1 && i1 != i0) low[t] = mfma64(a1, b, low[t]);
         }
@@ -145,17 +167,18 @@ GPTQ_DEV void gram(const OrthoProblem& o, int type, int64_t mat, int split, floa
   if (share == 0) each([&](double v, int at) { return part[at] = v; });
 }
 
-template <int B>
+template <int B, bool AGAIN>
 __global__ __launch_bounds__(GRAM_THREADS) void gram_kernel(OrthoArgs a, int which, int type, int64_t blocks0) {
-  constexpr int RUN = Run<B, true>::FLOATS > Run<B, false>::FLOATS ? Run<B, true>::FLOATS : Run<B, false>::FLOATS, SUM = 512 * ortho_tiles(16 * B);
+  constexpr int RUN = (Run<B, true>::FLOATS > Run<B, false>::FLOATS ? Run<B, true>::FLOATS : Run<B, false>::FLOATS) + (AGAIN ? 2 * 16 * B * MADE : 0);
+  constexpr int SUM = 512 * ortho_tiles(16 * B);
   __shared__ __align__(16) float lds[RUN > SUM ? RUN : SUM];
   int64_t b = blockIdx.x;
   if (b >= blocks0) b -= blocks0, which = 1;
   const OrthoProblem& o = a.p[which];
   const int64_t mat = b / o.splits;
   const int split = (int)(b - mat * o.splits);
-  if (o.tall) gram<B, true>(o, type, mat, split, lds);
-  else gram<B, false>(o, type, mat, split, lds);
+  if (o.tall) gram<B, true, AGAIN>(o, type, mat, split, lds);
+  else gram<B, false, AGAIN>(o, type, mat, split, lds);
 }
 
 // ---------------------------------------------------------------- the iteration
@@ -255,8 +278,8 @@ GPTQ_DEV void iterate(const OrthoArgs& a, const OrthoProblem& o, int64_t mat, do
     for (int i = c.lane; i < 16 * B; i += 64) v += S[tile_index(i / 16, i / 16, B) * TSIZE + (i % 16) * (TROW + 1)];
     for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
     if (c.lane == 0) {
-      norm = 1.0 / (sqrt(v) + a.eps);
-      o.inv[mat] = norm;
+      norm = a.first ? 1.0 / (sqrt(v) + a.eps) : 1.0;
+      if (a.first) o.inv[mat] = norm;
     }
   }
   __syncthreads();
@@ -286,10 +309,31 @@ GPTQ_DEV void iterate(const OrthoArgs& a, const OrthoProblem& o, int64_t mat, do
     c.write(S, acc);
     __syncthreads();
   }
-  float* out = o.R + mat * (16 * B) * (16 * B);
-  for (int e = threadIdx.x; e < 256 * B * B; e += C::THREADS) {
-    const int i = e / (16 * B), j = e % (16 * B);
-    out[e] = (float)element<B>(R, i / 16, j / 16, i % 16, j % 16);
+  double* all = o.R + mat * o.apart;
+  if (a.first) {
+    for (int e = threadIdx.x; e < 256 * B * B; e += C::THREADS) {
+      const int i = e / (16 * B), j = e % (16 * B);
+      all[e] = element<B>(R, i / 16, j / 16, i % 16, j % 16);
+    }
+    return;
+  }
+  // times the product of the steps before, which was formed of another S and so does not commute
+  constexpr int MORE = (B * B + C::THREADS / 64 - 1) / (C::THREADS / 64);
+  doublex4 total[MORE];
+#pragma unroll
+  for (int e = 0; e < MORE; ++e) {
+    const int t = min(c.wave + C::THREADS / 64 * e, B * B - 1), i = t / B, j = t % B;
+    total[e] = doublex4{0, 0, 0, 0};
+    for (int k = 0; k < 16 * B; k += 4)
+      total[e] = mfma64(element<B>(R, i, k / 16, c.r, k % 16 + c.h), all[(16 * j + c.r) * 16 * B + k + c.h], total[e]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < MORE; ++e) {
+    const int t = c.wave + C::THREADS / 64 * e, i = t / B, j = t % B;
+    if (t < B * B)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) all[(16 * j + c.r) * 16 * B + 16 * i + 4 * g + c.h] = total[e][g];
   }
 }
 
@@ -306,8 +350,8 @@ __global__ __launch_bounds__(Chain<B>::THREADS) void chain_kernel(OrthoArgs a, i
 // and a wave for each of its tiles.  With all polynomials of S commuting, rows of
 // what a step needs come from the same rows and S alone:
 //   U = S S, Q = a + b S + c U, T = Q S, V = T S, S' = T Q = a T + b V + c V S, R' = Q R
-// so a wave keeps its 16 columns of S (rows, S being symmetric) and R in registers and only rows
-// pass through LDS.  (One workgroup with the matrix in LDS: 254 us for 16 matrices
+// so a wave keeps its 16 columns of S (rows, S being symmetric) and R (held transposed) in registers and
+// only rows pass through LDS.  (One workgroup with the matrix in LDS: 254 us for 16 matrices
 // of 128; a launch for each of 14 products: 92 us.)
 struct WideArgs {
   double a, b, c;
@@ -315,8 +359,8 @@ struct WideArgs {
   int64_t size;            // values of a matrix's buffers
   double* base[2];         // of either problem
   int s, s1, r, r1;        // buffers: S, S', R, R'
-  bool first, last;
-  float* R[2];             // the last R'
+  bool first, last;        // R is the identity; no S' is wanted
+  bool again;              // R holds steps of an S formed before, and does not commute with this one
 };
 enum { kS0, kS1, kR0, kR1, kWideBuffers };   // ortho_wide's four
 
@@ -367,15 +411,15 @@ __global__ __launch_bounds__(64 * B) void wide_kernel(WideArgs a) {
   for (int e = 0; e < 4; ++e)
     if (ti == tj && 4 * e + h == r) q[e] += a.a;
   if (!a.first || !a.last) put(q);
-  doublex4 next = q;
-  if (!a.first) next = product(rr);
-  if (a.last) {
-    float* out = a.R[side] + mat * PP * PP;
+  const doublex4 next = a.first ? q : product(rr);
+  if (a.again) {
+    double* to = own + a.r1 * PP * PP;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[(16 * ti + 4 * e + h) * PP + 16 * tj + r] = (float)next[e];
-    return;
+    for (int e = 0; e < 4; ++e) to[(16 * tj + r) * PP + 16 * ti + 4 * e + h] = next[e];
+  } else {
+    write(a.r1, next);
   }
-  write(a.r1, next);
+  if (a.last) return;
   const doublex4 t = product(s);
   put(t);
   const doublex4 v = product(s);
@@ -406,8 +450,8 @@ __global__ __launch_bounds__(256) void wide_start_kernel(OrthoArgs a, int which,
   if ((tid & 63) == 0) sums[tid >> 6] = v;
   const double mine = sum(t * 256 + tid);
   __syncthreads();
-  const double by = 1.0 / (sqrt(sums[0] + sums[1] + sums[2] + sums[3]) + a.eps);
-  if (t == 0 && tid == 0) o.inv[mat] = by;
+  const double by = a.first ? 1.0 / (sqrt(sums[0] + sums[1] + sums[2] + sums[3]) + a.eps) : 1.0;
+  if (a.first && t == 0 && tid == 0) o.inv[mat] = by;
   int ti, tj;
   tile_of_index(t, B, ti, tj);
   double* S = w.base[side] + mat * w.size + (int64_t)kS0 * PP * PP;
@@ -415,8 +459,9 @@ __global__ __launch_bounds__(256) void wide_start_kernel(OrthoArgs a, int which,
   if (ti < tj || i <= j) S[i * PP + j] = S[j * PP + i] = mine * by * by;
 }
 
+// a.steps steps; R of the problems is in buffer `held`, before and after.
 template <int B>
-void wide(const OrthoArgs& a, int which, bool both, hipStream_t s) {
+void wide(OrthoArgs& a, int which, bool both, int& held, hipStream_t s) {
   constexpr int PP = 16 * B, TILES = ortho_tiles(PP);
   WideArgs w{};
   w.a = a.a;
@@ -424,30 +469,35 @@ void wide(const OrthoArgs& a, int which, bool both, hipStream_t s) {
   w.c = a.c;
   w.m = a.m;
   w.size = (int64_t)kWideBuffers * PP * PP;
-  for (int k = 0; k <= (both ? 1 : 0); ++k) {
-    w.base[k] = a.p[which + k].wide;
-    w.R[k] = a.p[which + k].R;
-  }
+  for (int k = 0; k <= (both ? 1 : 0); ++k) w.base[k] = a.p[which + k].wide;
   const int64_t mats = both ? 2 * a.m : a.m;
   hipLaunchKernelGGL(wide_start_kernel<B>, dim3((unsigned)mats, TILES), dim3(256), 0, s, a, which, w);
   for (int k = 0; k < a.steps; ++k) {
-    w.first = k == 0;
+    w.first = a.first && k == 0;
+    w.again = !a.first;
     w.last = k + 1 == a.steps;
     w.s = k % 2 ? kS1 : kS0;
     w.s1 = k % 2 ? kS0 : kS1;
-    w.r = k % 2 ? kR0 : kR1;
-    w.r1 = k % 2 ? kR1 : kR0;
+    w.r = held;
+    w.r1 = held = held == kR0 ? kR1 : kR0;
     hipLaunchKernelGGL(wide_kernel<B>, dim3((unsigned)mats, B), dim3(64 * B), 0, s, w);
   }
+  for (int k = 0; k <= (both ? 1 : 0); ++k) a.p[which + k].R = w.base[k] + held * PP * PP;
 }
 
 // ---------------------------------------------------------------- result
-// out = R M_0 for runs of the long side, with fp32 products: 29 us of operations at 135 TFLOP/s and
-// 26 us of memory for eight adapters of rank 128, which take 56.  Wave w holds rows 16 (w % B) .. of R in
+// out = R G / |G| for runs of the long side, with 64-bit products of G as it is (divided and rounded first,
+// its parts would no longer cancel).  For eight adapters of rank 128 59 us of operations at 67 TFLOP/s and
+// 26 us of memory, which take 99 (rounded to 32 bits 56).  Wave w holds rows 16 (w % B) .. of R / |G| in
 // registers and takes every (waves / B)th set of 16 long values of a run.  The lanes
-// run along the side that is contiguous in memory; R is symmetric, so either operand order
-// holds it.
-GPTQ_DEV floatx4 mfma_f32(float a, float b, floatx4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+// run along the side that is contiguous in memory.
+// Steps from one S formed of M to the next: its error, of which the last of them sees a^2
+// for each step before it, is multiplied by 2^16 at most.
+int steps_at_once(double a, int steps) {
+  int n = 1;
+  for (double by = a * a; n < steps && by <= 65536.0; by *= a * a) ++n;
+  return n;
+}
 
 template <int B>
 struct Apply {
@@ -467,38 +517,33 @@ GPTQ_DEV void apply(const OrthoProblem& o, int gt, int64_t mat, int64_t first, i
       if (threadIdx.x + THREADS * e < R::PER) next[e] = R::fetch(o, gt, mat, k0, threadIdx.x + THREADS * e);
   };
   fetch(first);
-  float w[4 * B];
+  double w[4 * B];
+  const double *by = o.R + mat * o.apart, inv = o.inv[mat];
 #pragma unroll
-  for (int k = 0; k < 4 * B; ++k) w[k] = o.R[mat * PP * PP + (4 * k + h) * PP + 16 * row + r];   // symmetric
-  const double inv = o.inv[mat];
+  for (int k = 0; k < 4 * B; ++k) w[k] = by[(4 * k + h) * PP + 16 * row + r] * inv;
   for (int64_t k0 = first; k0 < last; k0 += KS) {
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < LD; ++e)
-      if (threadIdx.x + THREADS * e < R::PER) {
-        floatx4 x = next[e];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) x[f] = (float)((double)x[f] * inv);
-        R::put(lds, R::APPLY, threadIdx.x + THREADS * e, x);
-      }
+      if (threadIdx.x + THREADS * e < R::PER) R::put(lds, R::APPLY, threadIdx.x + THREADS * e, next[e]);
     __syncthreads();
     if (k0 + KS < last) fetch(k0 + KS);
     for (int at = 32 * set; at < KS; at += 32 * SETS) {   // two sets of 16 at a time
-      floatx4 acc[2] = {};
+      doublex4 acc[2] = {};
 #pragma unroll
       for (int k = 0; k < 4 * B; ++k)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float m0 = R::get(lds, R::APPLY, 4 * k + h, at + 16 * q + r);
-          acc[q] = TALL ? mfma_f32(m0, w[k], acc[q]) : mfma_f32(w[k], m0, acc[q]);
+          const double g = R::get(lds, R::APPLY, 4 * k + h, at + 16 * q + r);
+          acc[q] = TALL ? mfma64(g, w[k], acc[q]) : mfma64(w[k], g, acc[q]);
         }
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int s = TALL ? 16 * row + r : 16 * row + 4 * h + e;               // place on the shorter side
-          const int64_t l = k0 + at + 16 * q + (TALL ? 4 * h + e : r);            // on the longer one
-          if (s < o.p && l < o.q) store_out<OT>(o.out, mat * o.rows * o.cols + (TALL ? l * o.p + s : s * o.q + l), acc[q][e]);
+          const int s = 16 * row + (TALL ? r : 4 * e + h);                        // place on the shorter side
+          const int64_t l = k0 + at + 16 * q + (TALL ? 4 * e + h : r);            // on the longer one
+          if (s < o.p && l < o.q) store_out<OT>(o.out, mat * o.rows * o.cols + (TALL ? l * o.p + s : s * o.q + l), (float)acc[q][e]);
         }
     }
   }
@@ -516,9 +561,10 @@ __global__ __launch_bounds__(Apply<B>::THREADS) void apply_kernel(OrthoArgs a, i
   else apply<B, false, OT>(o, gt, mat, first, last, lds);
 }
 
-// One launch of each kernel for the problems of B tile rows: `which` and, if both, the other.
+// One launch of each kernel for the problems of B tile rows: `which` and, if both, the other;
+// and of S and its steps again while steps are left.
 template <int B>
-void orthogonalize(const OrthoArgs& a, int which, bool both, int gt, int ot, hipStream_t s) {
+void orthogonalize(OrthoArgs a, int which, bool both, int gt, int ot, hipStream_t s) {
   // runs of a workgroup: the places of two or three workgroups on each CU filled once
   int64_t all = 0;
   for (int w = which; w <= (both ? 1 : which); ++w) all += a.m * ((a.p[w].q + KS - 1) / KS);
@@ -529,9 +575,17 @@ void orthogonalize(const OrthoArgs& a, int which, bool both, int gt, int ot, hip
     gram[w - which] = a.m * a.p[w].splits;
     apply[w - which] = a.m * ((a.p[w].q + (int64_t)KS * runs - 1) / ((int64_t)KS * runs));
   }
-  hipLaunchKernelGGL(gram_kernel<B>, dim3((unsigned)(gram[0] + gram[1])), dim3(GRAM_THREADS), 0, s, a, which, gt, gram[0]);
-  if constexpr (B > kOrthoNarrow) wide<B>(a, which, both, s);
-  else hipLaunchKernelGGL(chain_kernel<B>, dim3((unsigned)(both ? 2 * a.m : a.m)), dim3(Chain<B>::THREADS), 0, s, a, which);
+  const int steps = a.steps, most = steps_at_once(a.a, steps);
+  [[maybe_unused]] int held = kR1;
+  for (int done = 0; done < steps; done += most) {
+    a.first = done == 0;
+    a.steps = steps - done < most ? steps - done : most;
+    const dim3 parts((unsigned)(gram[0] + gram[1])), by(GRAM_THREADS);
+    if (a.first) hipLaunchKernelGGL((gram_kernel<B, false>), parts, by, 0, s, a, which, gt, gram[0]);
+    else hipLaunchKernelGGL((gram_kernel<B, true>), parts, by, 0, s, a, which, gt, gram[0]);
+    if constexpr (B > kOrthoNarrow) wide<B>(a, which, both, held, s);
+    else hipLaunchKernelGGL(chain_kernel<B>, dim3((unsigned)(both ? 2 * a.m : a.m)), dim3(Chain<B>::THREADS), 0, s, a, which);
+  }
   const dim3 grid((unsigned)(apply[0] + apply[1])), block(Apply<B>::THREADS);
   if (ot == 0) hipLaunchKernelGGL((apply_kernel<B, 0>), grid, block, 0, s, a, which, gt, apply[0], runs);
   else if (ot == kBF16) hipLaunchKernelGGL((apply_kernel<B, kBF16>), grid, block, 0, s, a, which, gt, apply[0], runs);

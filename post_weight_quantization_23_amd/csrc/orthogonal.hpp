@@ -19,11 +19,13 @@ struct OrthoProblem {
   double* part;          // [m][splits][tiles][256]
   double* inv;           // [m]: 1 / (|G|_F + eps)
   double* wide;          // [m][ortho_wide]
-  float* R;              // [m][pp][pp], pp: p rounded up to 16
+  double* R;             // the products q .. q transposed, pp x pp of each matrix, pp: p rounded up to 16 (in
+  int64_t apart;         // wide where that is used: set by the launch), this many values apart
 };
 struct OrthoArgs {
   int64_t m;
   int steps;
+  bool first;            // S is formed from G, not from R G (set by the launch)
   double a, b, c, eps;
   OrthoProblem p[2];     // p[1].G null: one
 };

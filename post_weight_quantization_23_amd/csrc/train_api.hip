@@ -358,7 +358,11 @@ void take_ortho(Carve& ws, gptq::OrthoProblem& o, int64_t m, int64_t rows, int64
   o.part = ws.take<double>(m * o.splits * tiles * 256);
   o.inv = ws.take<double>(m);
   o.wide = ws.take<double>(m * gptq::ortho_wide(o.p));
-  o.R = ws.take<float>(m * pp * pp);
+  o.R = o.wide;
+  o.apart = gptq::ortho_wide(o.p);
+  if (o.apart > 0) return;
+  o.R = ws.take<double>(m * pp * pp);
+  o.apart = pp * pp;
 }
 
 }  // namespace

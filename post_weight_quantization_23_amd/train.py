@@ -98,7 +98,8 @@ def adapter_orthogonalize(A: torch.Tensor | None = None, B: torch.Tensor | None 
     """Orthogonalised updates from the gradients (or momenta of them) of adapters'
     factors, A [m, rank, c] and B [m, r, rank] as adapter_backward gives them, either
     or both: each matrix is divided by its Frobenius norm + eps and its singular
-    values s go through a s + b s^3 + c s^5 `steps` times (Newton-Schulz).
+    values s go through a s + b s^3 + c s^5 `steps` times (Newton-Schulz; 1 to 16), in
+    64 bits throughout.
 
     Returns {A, B} (None where not given) of the inputs' type (float32, bfloat16 or
     float16) or out_dtype.  The shorter side of a matrix is at most 128."""

@@ -1,9 +1,12 @@
-"""The loss, its gradients and the adapters' update where they can go wrong.  Bounds as in
+"""The loss, its gradients and the adapters' update where they can go wrong: workspaces
+that hold anything, gradients of less than full rank and many steps.  Bounds as in
 test_gpu_train.py unless said."""
+import math
+
 import pytest
 import torch
 
-from test_gpu_train import DT, Head, gq, matrices, normal
+from test_gpu_train import COEF, DT, EPS, Head, check, gq, matrices, normal, update64
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +50,120 @@ def test_results_do_not_depend_on_what_the_workspace_holds(n, dt):
 
     for a, b in zip(step(0xFF), step(0)):
         assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- updates of less than full rank, many steps
+def deficient(kind, m, p, q, seed):
+    if kind == "one row repeated":
+        return normal((m, 1, q), seed).expand(m, p, q).contiguous()
+    k = {"rank 1": 1, "rank 10": 10, "half rank": p // 2}[kind]
+    return normal((m, p, k), seed) @ normal((m, k, q), seed + 1)
+
+
+def single(values):
+    """Coefficients as the C call takes them, in fp32 (2.0315 is then off by 5e-8 of it, a step of the result)."""
+    return tuple(float(torch.tensor(v, dtype=torch.float32)) for v in values)
+
+
+def steps_bound(p, n):
+    """Spectral norm of what the update of a p x q matrix (q up to 1024) may be off after n of Muon's
+    steps, in first order, and so of any of its entries, with e = 2^-53.
+    S is off by at most 64 e (chains of at most 48 sums of products, the norm of |M| |M|^T being at most 1) and
+    by (p + 8) e a step from its own products, of norms below 1.5.  An error of S grows by at most a^2 a
+    step (the slope of s q(s)^2, largest at 0); q(S) is off by (|b| + 2 |c| 1.5) = 11 times it, which
+    meets M of norm below 1.25, and grows by at most 4 a step from there, the largest slope
+    of p(s) = a s + b s^3 + c s^5 up to p's largest value 1.2025.  S is formed again from M after at most 5
+    steps: 2 * 11 * 1.25 * (64 + p + 8) e a^8 at the last of them, twice that for all of them.  The products
+    of R and M are off by (p + 8) e a step, and grow likewise."""
+    e, a = 2.0 ** -53, COEF[0]
+    block = min(n, 5)
+    once = 2 * 2 * 11 * 1.25 * (72 + p) * e * a ** (2 * (block - 1)) + block * (p + 8) * math.sqrt(p) * e * a ** block
+    return sum(once * 4.0 ** max(0, n - block - k) for k in range(0, n, 5))
+
+
+@pytest.mark.parametrize("kind", ["one row repeated", "rank 1", "rank 10", "half rank"])
+@pytest.mark.parametrize("p,q", [(8, 512), (24, 100), (64, 1024), (128, 1000)])
+def test_update_of_less_than_full_rank(p, q, kind):
+    """Gradients of fewer tokens than ranks: S has eigenvalues of zero, whose rounding must not grow."""
+    if kind == "rank 10" and p < 10:
+        pytest.skip("rank 10 of 8 rows")
+    A = deficient(kind, 2, p, q, 11)
+    B = deficient(kind, 2, p, q - 40, 12).transpose(1, 2).contiguous()
+    for steps in (1, 2, 5, 6, 8, 10, 12, 16):
+        got = gq().adapter_orthogonalize(A, B, steps=steps)
+        tau = steps_bound(p, steps)
+        for k, G in (("A", A), ("B", B.transpose(1, 2))):
+            mine = got[k] if k == "A" else got[k].transpose(1, 2)
+            want, _ = update64(G, steps, single(COEF), *single((1e-7,)))
+            norm = float(torch.linalg.matrix_norm(mine.double(), 2).max())
+            print(f"  {kind}, {steps} steps: norm {norm:.4f}, off {float((mine.double() - want).norm() / want.norm()):.2g}", flush=True)
+            check(f"{k}, {steps} steps", mine, want, torch.full_like(want, tau))
+            assert norm < 1.2025 + math.sqrt(p * q) * EPS + tau
+
+
+@pytest.mark.parametrize("p,q", [(16, 300), (72, 300)])
+@pytest.mark.parametrize("coef,steps", [((1.5, -0.5, 0.0), 16), ((2.0, -1.5, 0.5), 16), ((5.0, -20.0, 16.0), 3),
+                                        ((-1.5, 0.5, 0.0), 7), ((1.0, 0.0, 0.0), 1), ((0.0, 0.0, 0.0), 2)])
+def test_update_with_other_coefficients(p, q, coef, steps):
+    """Any coefficients on matrices of full and of half rank.  In first order: every product is off by (p + 72) 2^-53 of
+    its factors' norms, S's errors reach q(S) by |b| + 2 |c| and M by one more factor 2, and each later step multiplies an error by at
+    most L, the largest slope of p, or of p's values over s, up to the largest value reached, found on a grid; S, formed from
+    M again where L^(2 k) would pass 2^16, adds at most that."""
+    a, b, c = coef
+    top, L = 1.0, 1.0
+    for _ in range(steps):
+        s = torch.linspace(1e-3, top, 4000, dtype=torch.float64)
+        L = max(L, float((a + 3 * b * s ** 2 + 5 * c * s ** 4).abs().max()), float((a + b * s ** 2 + c * s ** 4).abs().max()), abs(a))
+        top = max(top, float((a * s + b * s ** 3 + c * s ** 5).abs().max()))
+    tau = steps * (p + 72) * 2.0 ** -53 * max(top, 1.0) ** 3 * 4 * (1 + abs(b) + 2 * abs(c)) * min(L ** (2 * steps), 2.0 ** 16) * L ** steps
+    for G in (matrices(2, p, q, 3, torch.float32), deficient("half rank", 2, p, q, 5)):
+        got = gq().adapter_orthogonalize(A=G, steps=steps, coefficients=coef)["A"]
+        want, _ = update64(G, steps, single(coef), *single((1e-7,)))
+        assert tau < 0.1 * float(want.abs().max()) or float(want.abs().max()) == 0
+        check("update", got, want, torch.full_like(want, tau))
+
+
+@pytest.mark.parametrize("p", [16, 72])
+@pytest.mark.parametrize("a,steps", [(300.0, 3), (1e4, 2), (1e-3, 4)])
+def test_update_of_a_line(p, a, steps):
+    """b = c = 0: M_0 times a^steps, each product off by (p + 72) 2^-53 of its factors' norms."""
+    G = matrices(2, p, 300, 3, torch.float32)
+    got = gq().adapter_orthogonalize(A=G, steps=steps, coefficients=(a, 0.0, 0.0))["A"]
+    a, eps = single((a, 1e-7))
+    M = G.double() / (G.double().square().sum((1, 2), keepdim=True).sqrt() + eps)
+    check("update", got, a ** steps * M, torch.full_like(M, steps * (p + 72) * 2.0 ** -53 * 4 * a ** steps))
+
+
+@pytest.mark.parametrize("gt,ot", [("fp32", "bf16"), ("bf16", "fp32"), ("fp16", "fp16")])
+@pytest.mark.parametrize("rank,c,r", [(72, 40, 500), (72, 200, 80), (16, 8, 300), (40, 64, 33)])
+def test_update_of_many_steps_of_both_factors(rank, c, r, gt, ot):
+    """Matrices of other numbers of tile rows beside each other, lying and standing, in all types."""
+    A, B = normal((3, rank, c), 31).to(DT[gt]), normal((3, r, 2), 32) @ normal((3, 2, rank), 33)
+    B = B.to(DT[gt])
+    got = gq().adapter_orthogonalize(A, B, steps=12, out_dtype=DT[ot])
+    for k, G in (("A", A), ("B", B)):
+        flip = G.shape[1] > G.shape[2]
+        want, _ = update64(G.transpose(1, 2) if flip else G, 12, single(COEF), *single((1e-7,)))
+        check(k, got[k].transpose(1, 2) if flip else got[k], want, torch.full_like(want, steps_bound(min(G.shape[1:]), 12)))
+
+
+@pytest.mark.parametrize("p", [24, 96])
+def test_many_steps_in_a_graph(p):
+    """S formed again within a captured call, replayed on other matrices with eager calls between."""
+    G = deficient("rank 1", 3, p, 400, 41)
+    ws, out = gq().Workspace(), {"A": torch.empty_like(G)}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gq().adapter_orthogonalize(A=G, steps=16, out=out, ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gq().adapter_orthogonalize(A=G, steps=16, out=out, ws=ws)
+    for seed, kind in enumerate(("half rank", "one row repeated", "rank 1")):
+        G.copy_(deficient(kind, 3, p, 400, 50 + seed))
+        want = gq().adapter_orthogonalize(A=G, steps=16)["A"]
+        out["A"].fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out["A"], want), kind
