@@ -116,13 +116,13 @@ __global__ __launch_bounds__(256) void gather_kernel(GatherArgs a) {
 }
 
 // ---------------------------------------------------------------- statistics
-// TOKENS tokens by 256 / TOKENS threads each, which join every so many of its tiles: 16 tokens
+// TOKENS tokens by 256 / TOKENS threads each, which join every so many of its tiles: kJoinTokens
 // where there are enough of them, else one wave for each.
 template <int TOKENS>
 __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a, int tiles, float* __restrict__ loss, float* __restrict__ lse) {
   constexpr int PARTS = 256 / TOKENS;
   __shared__ float2 sums[PARTS][TOKENS + 1];
-  const int tok = TOKENS == 16 ? threadIdx.x & 15 : threadIdx.x / PARTS, part = TOKENS == 16 ? threadIdx.x >> 4 : threadIdx.x % PARTS;
+  const int tok = TOKENS == kJoinTokens ? threadIdx.x % TOKENS : threadIdx.x / PARTS, part = TOKENS == kJoinTokens ? threadIdx.x / TOKENS : threadIdx.x % PARTS;
   const int64_t p = (int64_t)blockIdx.x * TOKENS + tok, count = a.target ? a.n : *a.k.count;
   float2 v = {-INFINITY, 0.f};
   if (p < count)
@@ -184,7 +184,7 @@ void launch_gather_kept(GatherArgs a, hipStream_t s) {
 
 void launch_loss_join(const LossArgs& a, float* loss, float* lse, hipStream_t s) {
   const int tiles = (int)loss_tiles(a.n, a.vocab);
-  if (a.n > 1024) hipLaunchKernelGGL(loss_join_kernel<16>, dim3((unsigned)((a.n + 15) / 16)), dim3(256), 0, s, a, tiles, loss, lse);
+  if (a.n > 1024) hipLaunchKernelGGL(loss_join_kernel<kJoinTokens>, dim3((unsigned)((a.n + kJoinTokens - 1) / kJoinTokens)), dim3(256), 0, s, a, tiles, loss, lse);
   else hipLaunchKernelGGL(loss_join_kernel<4>, dim3((unsigned)((a.n + 3) / 4)), dim3(256), 0, s, a, tiles, loss, lse);
 }
 

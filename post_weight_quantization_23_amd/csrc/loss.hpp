@@ -91,6 +91,7 @@ struct LossArgs {
 };
 void launch_logits(const LossArgs& a, int dt, bool grad, hipStream_t s);
 
+constexpr int kJoinTokens = 16;   // of a workgroup of the join, where there are enough of them
 void launch_loss_join(const LossArgs& a, float* loss, float* lse, hipStream_t s);
 
 // dX[place] = P W over one piece of the vocabulary, in *k.splits fp32 parts (added

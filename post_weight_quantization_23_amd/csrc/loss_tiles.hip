@@ -699,7 +699,7 @@ bool loss_fits(int64_t n, int64_t vocab, int64_t d, bool grad) {
   constexpr int64_t tokens[] = {256, 128, 64, 32, 64};
   if (!grid_fits(tiles_of(n, tokens[loss_shape(n, vocab)]) * loss_tiles(n, vocab), 512)) return false;
   if (!grid_fits(tiles_of(n * (gemm16_depth(d) / 8), 256), 256)) return false;
-  if (!grad) return true;
+  if (!grad) return grid_fits(tiles_of(n, kJoinTokens), 256);
   const int64_t tile = grad_x_large(n) ? 256 : 128;
   return grid_fits(tiles_of(n, tile) * tiles_of(d, tile), 512) && grid_fits(tiles_of(vocab, 256) * tiles_of(d, 256), 512);
 }

@@ -158,3 +158,13 @@ def test_binding_refuses_bad_tensors():
                 dict(out={"A": B}), dict(A=None, out={"A": A}), dict(out={"C": A}), dict(A=A[0]), dict()):
         with pytest.raises(ValueError):
             h(**{**dict(A=A, B=B), **bad})
+
+
+def test_losses_of_more_tokens_than_a_launch_takes_are_refused(lib):
+    """The join of the tiles' sums takes 16 threads for a token: 2^28 tokens and more would pass 2^32."""
+    out = C.c_size_t(7)
+    f, most = lib.gptq_linear_cross_entropy_workspace_size, (1 << 28) - 16
+    assert f(most, 8, 1, C.byref(out)) == 0 and f(most + 1, 8, 1, C.byref(out)) == 5 and f((1 << 28) + 4096, 8, 1, C.byref(out)) == 5
+    v = loss_args(n=(1 << 28) + 4096, d=8, ldx=8, ldw=8, vocab=1)
+    assert lib.gptq_linear_cross_entropy(v["X"], v["xt"], v["n"], v["d"], v["ldx"], v["W"], v["vocab"], v["ldw"], v["y"], v["loss"],
+                                         v["lse"], None, 0, None) == 5
