@@ -1,12 +1,13 @@
 """The loss, its gradients and the adapters' update where they can go wrong: workspaces
-that hold anything, gradients of less than full rank and many steps.  Bounds as in
+that hold anything, tiles of 256 x 256 over many steps of the contraction, many pieces of the
+vocabulary, heads past 2^31 elements, gradients of less than full rank and many steps.  Bounds as in
 test_gpu_train.py unless said."""
 import math
 
 import pytest
 import torch
 
-from test_gpu_train import COEF, DT, EPS, Head, check, gq, matrices, normal, update64
+from test_gpu_train import COEF, DT, EPS, U, Head, check, gq, matrices, normal, targets, update64
 
 pytestmark = pytest.mark.gpu
 
@@ -50,6 +51,89 @@ def test_results_do_not_depend_on_what_the_workspace_holds(n, dt):
 
     for a, b in zip(step(0xFF), step(0)):
         assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- tiles of 256 x 256
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("mask", ["none", "prompt"])
+@pytest.mark.parametrize("n,vocab,d", [(1025, 257, 136), (1100, 1031, 520), (2300, 700, 328), (1537, 513, 1160), (4097, 300, 192)])
+def test_many_tokens_over_many_steps(n, vocab, d, mask, dt):
+    """More than 1024 tokens, of which several tiles of 256 remain, over 3 to 19 steps of 64 values
+    with and without a tail."""
+    h = Head(n, vocab, d, DT[dt], 500 + n, mask).exact()
+    loss, lse = gq().linear_cross_entropy(h.X, h.W, h.y)
+    check("lse", lse, h.keep_lse, h.dlse)
+    check("loss", loss, h.loss, h.dloss_bound)
+    dloss = h.dloss * (4096 if dt == "fp16" else 1)   # results that are normal numbers
+    (dX, bX), (dW, bW) = h.gradients(dloss)
+    got = gq().linear_cross_entropy_backward(h.X, h.W, h.y, lse, dloss, want_dW=True)
+    check("dX", got["X"], dX, bX)
+    check("dW", got["W"], dW, bW)
+    assert bool((got["X"][~h.there] == 0).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("n", [5, 70])
+def test_vocabulary_in_pieces_of_few_tokens(n, dt):
+    """Pieces hold at most 2^21 entries, however few the tokens; targets on both sides of the border."""
+    vocab = (1 << 21) + 300
+    h = Head(n, vocab, 16, DT[dt], 600 + n)
+    h.y[: n // 2] = (1 << 21) - n // 4 + torch.arange(n // 2, device="cuda")
+    h.at = h.y
+    h.exact()
+    loss, lse = gq().linear_cross_entropy(h.X, h.W, h.y)
+    check("lse", lse, h.keep_lse, h.dlse)
+    check("loss", loss, h.loss, h.dloss_bound)
+    dloss = h.dloss * (4096 if dt == "fp16" else 1)   # results that are normal numbers
+    (dX, bX), (dW, bW) = h.gradients(dloss)
+    got = gq().linear_cross_entropy_backward(h.X, h.W, h.y, lse, dloss, want_dW=True)
+    check("dX", got["X"], dX, bX)
+    check("dW", got["W"], dW, bW)
+
+
+# ---------------------------------------------------------------- past 2^31 elements
+@pytest.mark.parametrize("n", [3, 300])
+def test_head_past_32_bits_entry_by_entry(n):
+    """A head, and its gradient, of more than 2^31 elements.  Targets are dealt over the whole
+    vocabulary, a third of them past 2^31 elements, and each token's hidden state leans to its
+    target, so that another row of W in its place is a loss off by a unit or more.  Every bound is
+    entry by entry, and far below the result itself."""
+    vocab, d, dt = 270001, 8192, torch.bfloat16
+    W = torch.empty((vocab, d), dtype=dt, device="cuda")
+    parts = range(0, vocab, 30000)
+    for a in parts:
+        W[a:a + 30000] = normal((min(30000, vocab - a), d), 170 + a, 1 / math.sqrt(d)).to(dt)
+    y = (torch.arange(n, device="cuda") * 7919 + vocab - 1 - 7919 * (n // 3)) % vocab
+    X = (normal((n, d), 172) + 4 * W[y].float()).to(dt)
+    dloss = 1 + normal((n,), 173).abs()
+    loss, lse = gq().linear_cross_entropy(X, W, y)
+    x, zy = X.double(), torch.arange(n, device="cuda")
+    z = torch.cat([x @ W[a:a + 30000].double().T for a in parts], 1)
+    dz = (d + 32) * 2 * EPS * torch.cat([x.abs() @ W[a:a + 30000].double().abs().T for a in parts], 1)
+    want = torch.logsumexp(z, 1)
+    arg = (z.max(1).values - z.min(1).values).clamp_max(90) + 2
+    dlse = dz.max(1).values + arg * 4 * EPS + (64 + 3 * (16 + vocab / 4096)) * 2 * EPS + 4 * EPS * want.abs()
+    check("lse", lse, want, dlse)
+    bound = dlse + dz[zy, y] + 4 * EPS * (want.abs() + z[zy, y].abs())
+    check("loss", loss, want - z[zy, y], bound)
+    assert float(bound.max()) < 0.25       # another row's logit is about N(0, 1) where the target's is 4 higher
+    got = gq().linear_cross_entropy_backward(X, W, y, want.float(), dloss, want_dW=True)
+    p = torch.exp(z - want.unsqueeze(1))
+    D = p.clone()
+    D[zy, y] -= 1
+    D *= dloss.double().unsqueeze(1)
+    off = dloss.double().unsqueeze(1) * p * (dz + EPS * want.abs().unsqueeze(1) + ((z - want.unsqueeze(1)).abs() + 2) * 4 * EPS) + U[dt] * D.abs()
+    dX, bX = torch.zeros_like(x), torch.zeros_like(x)
+    for a in parts:
+        w = W[a:a + 30000].double()
+        dX += D[:, a:a + 30000] @ w
+        bX += (off[:, a:a + 30000] + (vocab / 16 + 64) * 2 * EPS * D[:, a:a + 30000].abs()) @ w.abs()
+    check("dX", got["X"], dX, bX)
+    assert float(bX.norm()) < 0.3 * float(dX.norm())
+    rows = torch.cat([y, (y + 1) % vocab, torch.arange(vocab - 300, vocab, device="cuda"), torch.arange(0, vocab, 997, device="cuda")])
+    dW, bW = D[:, rows].T @ x, (off[:, rows] + (n + 64) * 2 * EPS * D[:, rows].abs()).T @ x.abs()
+    check("dW", got["W"][rows], dW, bW)
+    assert float(bW[:n].norm()) < 0.3 * float(dW[:n].norm())
 
 
 # ---------------------------------------------------------------- updates of less than full rank, many steps
