@@ -62,7 +62,8 @@ gptq_status gptq_linear_cross_entropy(const void* X, gptq_dtype xt, int64_t n_to
  *   dX = D W,   dW = D^T X
  *
  * D enters the products rounded once to xt (GPTQ_F16: scaled by a power of two, so
- * that entries down to 2^-28 of the largest dloss are normal numbers).  Hidden
+ * that entries down to 2^-28 of the largest dloss are normal numbers), the targets' entries
+ * in fp32 for dX and as two values of xt for dW.  Hidden
  * states of tokens without a target enter nothing.  The vocabulary is taken in
  * pieces, so that D takes 512 MB or 512 bytes per token, whichever is more.
  *

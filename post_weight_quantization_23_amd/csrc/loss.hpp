@@ -23,7 +23,7 @@ struct Kept {
   float* grad;
   int32_t* count;
   float* down;      // what results are multiplied by (a power of two, 1 for bf16)
-  float* rest;      // what rounding took from the target's entry of D (backward)
+  float* rest;      // what rounding took from the target's entry of D (backward), for dX and dW
   int32_t* splits;  // parts of the contraction that dX is computed in
 };
 
@@ -112,10 +112,10 @@ struct GradXArgs {
 void launch_grad_x(const GradXArgs& a, int dt, hipStream_t s);
 void launch_join_x(const GradXArgs& a, int dt, hipStream_t s);
 
-// dW rows of one piece of the vocabulary = P^T rows.
+// dW rows of one piece of the vocabulary = P^T rows, and what rounding took from the targets' entries.
 struct GradWArgs {
   const uint16_t* P;
-  int64_t ldp, width;
+  int64_t ldp, v0, width;
   const uint16_t* rows;
   int64_t kp, n, d;
   Kept k;

@@ -571,6 +571,79 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_x_kernel(GradXArgs a, in
   }
 }
 
+// What rounding took from the targets' entries of D, for a wave's 32 MT entries from v0 of the vocabulary on x
+// 32 NT columns from j0: a product over the tokens whose targets are among them, 16 at a time in
+// their order, one entry of a column of its left operand each.  A target's entry is most of a
+// token's row of D, so this is most of what dW would be off by (4096 tokens of 32000 x 4096: 2.4e-3, with
+// it 1.7e-3, that of its own rounding).  The wave looks through all tokens for them: 930 -> 972 us there;
+// 8192 tokens of 1000 x 4096, eight to an entry, 295 -> 390 us.  lds: the wave's own.
+template <int DT, int MT, int NT>
+GPTQ_DEV void add_rest(const GradWArgs& a, floatx16 (&acc)[MT][NT], void* lds, int64_t count, int64_t v0, int64_t j0) {
+  constexpr int SETS = 16, ONCE = 16, ROOM = 64 * SETS + ONCE;   // tokens looked at at once: 64 SETS
+  const int lane = threadIdx.x & 63, m = lane & 31, h = lane >> 5;
+  int32_t *place = static_cast<int32_t*>(lds), *entry = place + ROOM;
+  static_assert(2 * ROOM <= 32 * (32 * NT + 4), "a wave's LDS");
+  int have = 0;
+#pragma unroll 1
+  for (int64_t base = 0; base < count; base += 64 * SETS) {
+    int at[SETS];
+#pragma unroll
+    for (int k = 0; k < SETS; ++k) {
+      at[k] = a.k.col[min(base + 64 * k + lane, count - 1)] - (int)v0;
+    }
+#pragma unroll
+    for (int k = 0; k < SETS; ++k) {
+      const bool mine = base + 64 * k + lane < count && (uint32_t)at[k] < 32u * MT;
+      const uint64_t all = __ballot(mine);
+      if (mine) {
+        const int to = have + __popcll(all & ((1ull << lane) - 1));
+        place[to] = (int32_t)(base + 64 * k + lane);
+        entry[to] = at[k];
+      }
+      have += __popcll(all);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const bool end = base + 64 * SETS >= count;
+    int from = 0;
+#pragma unroll 1
+    for (; end ? from < have : have - from >= ONCE; from += ONCE) {
+      // all loads before the first use: what does not exist is read from the last that does, and meets a
+      // left operand of zero, or columns that are not stored
+      u32x4 left[MT], right[NT];
+      int own[8];
+      float r[8];
+      uint32_t x[NT][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int of = from + 8 * h + e, p = place[min(of, have - 1)];
+        own[e] = of < have ? entry[min(of, have - 1)] : -1;
+        r[e] = a.k.rest[p];
+#pragma unroll
+        for (int q = 0; q < NT; ++q) x[q][e] = a.rows[p * a.kp + min(j0 + 32 * q + m, a.kp - 1)];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          left[i][e] = (own[2 * e] == 32 * i + m ? f32_to_16<DT>(r[2 * e]) : 0u) | (own[2 * e + 1] == 32 * i + m ? (uint32_t)f32_to_16<DT>(r[2 * e + 1]) << 16 : 0u);
+#pragma unroll
+        for (int q = 0; q < NT; ++q) right[q][e] = x[q][2 * e] | x[q][2 * e + 1] << 16;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[i][q] = mfma32<DT>(left[i], right[q], acc[i][q]);
+    }
+    if (end) break;
+    have -= from;   // fewer than 16 go first next time
+    const int32_t p = place[from + (lane & 15)], e = entry[from + (lane & 15)];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (lane < have) place[lane] = p, entry[lane] = e;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // dW: tiles of TM vocabulary entries x TN columns, contracted over the kept tokens.
 template <int DT, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void grad_w_kernel(GradWArgs a, int voc_tiles, int col_tiles) {
@@ -584,7 +657,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_w_kernel(GradWArgs a, in
   const int64_t v0 = (int64_t)vt * P::TM, j0 = (int64_t)ct * P::TN;
   floatx16 acc[MT][NT];
   P::run(Source{a.P, a.ldp, a.ldp, count}, Source{a.rows, a.kp, a.kp, count}, v0, j0, 0, (count + LK - 1) / LK, lsm, acc);
+  static_assert(WM * WN * 32 * (32 * NT + 4) * 4 <= 2 * P::BUF, "results fit the operands' LDS");
   float* own = reinterpret_cast<float*>(lsm) + wave * 32 * (32 * NT + 4);
+  add_rest<DT, MT, NT>(a, acc, own, count, a.v0 + v0 + wm, j0 + wn);
   const float down = *a.k.down;
 #pragma unroll
   for (int i = 0; i < MT; ++i)

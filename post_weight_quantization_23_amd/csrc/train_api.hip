@@ -315,6 +315,7 @@ gptq_status gptq_linear_cross_entropy_backward(const void* X, gptq_dtype xt, int
       gptq::launch_grad_x(x, dt, s);
     }
     if (dW) {
+      w.v0 = v0;
       w.width = width;
       w.ldp = ldp;
       w.dW = static_cast<uint16_t*>(dW) + v0 * lddw;

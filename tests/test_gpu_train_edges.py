@@ -91,6 +91,34 @@ def test_vocabulary_in_pieces_of_few_tokens(n, dt):
     check("dW", got["W"], dW, bW)
 
 
+# ---------------------------------------------------------------- the target's entry
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("mask", ["none", "prompt"])
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("n,vocab,d", [(1, 300, 8), (50, 4000, 72), (60, 9000, 136), (130, 700, 264), (700, 5003, 320), (1500, 20000, 72)])
+def test_gradients_with_the_targets_entry_unrounded(n, vocab, d, same, mask, dt):
+    """Of D the targets' entries enter dX in fp32 and dW in two 16-bit terms: u^2 |D| and the step of the second
+    term instead of u |D|, 4 EPS |D| for the fp32 value itself.  same: a few entries are the targets of all tokens."""
+    h = Head(n, vocab, d, DT[dt], 700 + n, mask)
+    if same:
+        h.y = torch.where(h.there, vocab // 2 + 37 * (torch.arange(n, device="cuda") % 5) % (vocab // 2), h.y)
+        h.at = torch.where(h.there, h.y, 0)
+    h.exact()
+    dloss = h.dloss * (4096 if dt == "fp16" else 1)
+    (dX, bX), (dW, bW) = h.gradients(dloss)
+    g = torch.where(h.there, dloss.double(), 0)
+    D = g * (torch.exp(h.z.gather(1, h.at.unsqueeze(1)).squeeze(1) - h.lse) - 1)
+    less = (U[h.dt] - U[h.dt] ** 2 - 4 * EPS) * D.abs()
+    bX -= less.unsqueeze(1) * h.W[h.at].double().abs()
+    bW.index_add_(0, h.at, -less.unsqueeze(1) * h.X.double().nan_to_num().abs())
+    lse = h.keep_lse.float()
+    got = gq().linear_cross_entropy_backward(h.X, h.W, h.y, lse, dloss, want_dW=True)
+    check("dX", got["X"], dX, bX)
+    check("dW", got["W"], dW, bW)
+    only = gq().linear_cross_entropy_backward(h.X, h.W, h.y, lse, dloss, want_dX=False, want_dW=True)
+    assert torch.equal(only["W"], got["W"])
+
+
 # ---------------------------------------------------------------- past 2^31 elements
 @pytest.mark.parametrize("n", [3, 300])
 def test_head_past_32_bits_entry_by_entry(n):
