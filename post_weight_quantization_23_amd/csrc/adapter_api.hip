@@ -1,7 +1,6 @@
 // C ABI of the packed products for many tokens and of the low-rank adapters
 // (declared in include/gptq_adapter.h).  As in gptq_api.hip every argument is
 // validated on the host before anything is enqueued.
-#include <cstdio>
 #include <utility>
 
 #include "../../include/gptq_adapter.h"
@@ -16,16 +15,7 @@ constexpr int64_t kMaxCols = int64_t(1) << 30;
 constexpr int64_t kMaxDepth = (int64_t(1) << 22) - 64;   // rows of the layer in the input gradient
 constexpr int64_t kMaxAdapters = int64_t(1) << 20;
 
-int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
-
-gptq_status need_ws(const char* fn, const void* ws, size_t have, int64_t need) {
-  char text[80];
-  snprintf(text, sizeof text, "workspace needs %lld bytes", (long long)need);
-  if (need > 0 && (!ws || have < (size_t)need)) return fail(GPTQ_EWORKSPACE, fn, text);
-  if (need > 0 && !aligned(ws, 256)) return fail(GPTQ_EALIGN, fn, "workspace not 256-byte aligned");
-  return GPTQ_OK;
-}
 
 // Pieces of a workspace, each 256-byte aligned.
 struct Carve {

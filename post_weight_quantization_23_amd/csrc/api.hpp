@@ -1,4 +1,4 @@
-// Host-side checks shared by the C entry points (gptq_api.hip, adapter_api.hip).
+// Host-side checks shared by the C entry points (gptq_api.hip, adapter_api.hip, train_api.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -55,6 +55,14 @@ inline int64_t extent_bytes(int64_t rows, int64_t ld, int64_t cols, int64_t elem
 inline bool overlaps(const void* p, int64_t bytes, const void* q, int64_t bytes_q) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return a < b + (uint64_t)bytes_q && b < a + (uint64_t)bytes;
+}
+
+// A workspace of `have` bytes where `need` are needed; its pieces start on 256 bytes.
+inline int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
+inline gptq_status need_ws(const char* fn, const void* ws, size_t have, int64_t need) {
+  if (need > 0 && (!ws || have < (size_t)need)) return fail(GPTQ_EWORKSPACE, fn, "workspace needs " + std::to_string(need) + " bytes");
+  if (need > 0 && !aligned(ws, 256)) return fail(GPTQ_EALIGN, fn, "workspace not 256-byte aligned");
+  return GPTQ_OK;
 }
 
 inline size_t elem_size(gptq_dtype t) { return t == GPTQ_F32 ? 4 : 2; }

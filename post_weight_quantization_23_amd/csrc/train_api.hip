@@ -2,7 +2,6 @@
 // updates (declared in include/gptq_train.h).  Every argument is validated on the
 // host before anything is enqueued.
 #include <cmath>
-#include <cstdio>
 
 #include "../../include/gptq_train.h"
 #include "api.hpp"
@@ -16,8 +15,6 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t(1) << 22) - 64;
 constexpr int64_t kMaxMatrices = int64_t(1) << 20;
 
-int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
-
 // Pieces of a workspace, each 256-byte aligned.
 struct Carve {
   char* base;
@@ -29,14 +26,6 @@ struct Carve {
     return p;
   }
 };
-
-gptq_status need_ws(const char* fn, const void* ws, size_t have, int64_t need) {
-  char text[80];
-  snprintf(text, sizeof text, "workspace needs %lld bytes", (long long)need);
-  if (need > 0 && (!ws || have < (size_t)need)) return fail(GPTQ_EWORKSPACE, fn, text);
-  if (need > 0 && !aligned(ws, 256)) return fail(GPTQ_EALIGN, fn, "workspace not 256-byte aligned");
-  return GPTQ_OK;
-}
 
 // Arrays of a call; an output may overlap nothing else.
 struct Span {
@@ -402,7 +391,6 @@ gptq_status gptq_adapter_orthogonalize(const void* G_A, const void* G_B, gptq_dt
                         {G_A ? out_A : nullptr, m * rank, c, c, eo, true}, {G_B ? out_B : nullptr, m * r, rank, rank, eo, true}};
   if (gptq_status st = check_apart(fn, spans)) return st;
   gptq::OrthoArgs args{};
-  Carve size{nullptr, 0};
   for (int pass = 0; pass < 2; ++pass) {
     Carve carve{pass ? static_cast<char*>(ws) : nullptr, 0};
     int at = 0;
