@@ -35,8 +35,9 @@ extern "C" {
  *   loss[t] = lse[t] - z[t, target[t]]
  *
  * A target outside 0 .. vocab-1 is none (a prompt's token, padding): the token's
- * loss and lse are 0, its hidden state is not looked at, and no work is spent
- * on it.  A token whose own logits hold an infinity or NaN gives infinities or NaN;
+ * loss and lse are 0, and what its hidden state holds reaches no result.  Such tokens are
+ * left out of the products, but for the loss of up to 256 tokens whose rows start on
+ * 16 bytes, which are multiplied as they lie.  A token whose own logits hold an infinity or NaN gives infinities or NaN;
  * the others are not touched.
  *
  * X      : n_tok x d of type xt (GPTQ_BF16 or GPTQ_F16), 2-byte aligned, ldx >= d

@@ -10,7 +10,7 @@ namespace {
 // Places of the tokens that have a target, by one workgroup: 4096 tokens a turn as
 // four sets of 1024, whose waves' counts are summed up by every wave for itself.
 // For fp16 gradients the largest finite |dloss| is brought to 2^14 .. 2^15 by a power
-// of two, so that softmax values down to 2^-29 of it keep their precision.
+// of two, so that entries of D down to 2^-28 of it are normal numbers.
 __global__ __launch_bounds__(1024) void keep_kernel(KeepArgs a) {
   constexpr int SETS = 4, WAVES = 16;
   __shared__ int counts[SETS * WAVES];

@@ -4,9 +4,9 @@
 // loads, one barrier a step), each either contiguous along the contraction or
 // across it.  Operands across it are read from LDS transposed (ds_read_b64_tr), so
 // that neither W, the rows nor the gradients are ever laid out a second time.
-// Tiles of 256 x 256 run at 1.24 PFLOP/s for statistics (8192 tokens of 128000 x 4096, matrix
+// Tiles of 256 x 256 run at 1.26 PFLOP/s for statistics (8192 tokens of 128000 x 4096, matrix
 // cores busy 67 % at the 1.75 GHz that the power limit leaves), and of 4096 tokens
-// of 32000 x 4096 at 1.15 for D (its 262 MB written), 1.28 for dX and 1.17 for dW.
+// of 32000 x 4096 at 1.17 for D (its 262 MB written), 1.28 for dX and 1.10 for dW.
 #include "loss.hpp"
 
 namespace gptq {
@@ -575,8 +575,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void grad_x_kernel(GradXArgs a, in
 // 32 NT columns from j0: a product over the tokens whose targets are among them, 16 at a time in
 // their order, one entry of a column of its left operand each.  A target's entry is most of a
 // token's row of D, so this is most of what dW would be off by (4096 tokens of 32000 x 4096: 2.4e-3, with
-// it 1.7e-3, that of its own rounding).  The wave looks through all tokens for them: 930 -> 972 us there;
-// 8192 tokens of 1000 x 4096, eight to an entry, 295 -> 390 us.  lds: the wave's own.
+// it 1.7e-3, that of its own rounding).  The wave looks through all tokens for them: both gradients take
+// 2772 us there instead of 2760; dW of 8192 tokens of 1000 x 4096, eight to an entry, 390 instead of 295.
+// lds: the wave's own.
 template <int DT, int MT, int NT>
 GPTQ_DEV void add_rest(const GradWArgs& a, floatx16 (&acc)[MT][NT], void* lds, int64_t count, int64_t v0, int64_t j0) {
   constexpr int SETS = 16, ONCE = 16, ROOM = 64 * SETS + ONCE;   // tokens looked at at once: 64 SETS

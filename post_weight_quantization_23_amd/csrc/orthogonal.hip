@@ -16,7 +16,7 @@
 // workgroup iterates a matrix by itself; above that (more 64-bit products than one
 // CU is quick at) a launch takes a step of all matrices on many.  An adapter of rank
 // 16 beside 4096 x 4096 takes 19 us, five of rank 64 beside 11008 x 4096 87 us (S_0
-// 19, iteration 45, result 25), eight of rank 128 262 us (65, 112 in six launches, 99).
+// 18, iteration 45, result 24), eight of rank 128 262 us (62, 108 in six launches, 94).
 #include "orthogonal.hpp"
 
 namespace gptq {
@@ -87,7 +87,7 @@ struct Run {
 
 // ---------------------------------------------------------------- S_0
 // Parts of G G^T over the long side; 64-bit products bound it (rank 128: its operations take 33 us
-// at 67 TFLOP/s, the kernel 65).  A wave holds tile rows i and B-1-i of the upper
+// at 67 TFLOP/s, the kernel 62).  A wave holds tile rows i and B-1-i of the upper
 // half, B+1 tiles whatever i is, so a fragment of the run serves several products;
 // the waves with the same rows share the run's values out among them and
 // are added up through LDS in their order.
@@ -352,7 +352,8 @@ __global__ __launch_bounds__(Chain<B>::THREADS) void chain_kernel(OrthoArgs a, i
 //   U = S S, Q = a + b S + c U, T = Q S, V = T S, S' = T Q = a T + b V + c V S, R' = Q R
 // so a wave keeps its 16 columns of S (rows, S being symmetric) and R (held transposed) in registers and
 // only rows pass through LDS.  (One workgroup with the matrix in LDS: 254 us for 16 matrices
-// of 128; a launch for each of 14 products: 92 us.)
+// of 128, these six launches 108.  A launch for each of 14 products made the call of eight adapters
+// 17 us longer.)
 struct WideArgs {
   double a, b, c;
   int64_t m;               // matrices of the first problem
@@ -488,7 +489,7 @@ void wide(OrthoArgs& a, int which, bool both, int& held, hipStream_t s) {
 // ---------------------------------------------------------------- result
 // out = R G / |G| for runs of the long side, with 64-bit products of G as it is (divided and rounded first,
 // its parts would no longer cancel).  For eight adapters of rank 128 59 us of operations at 67 TFLOP/s and
-// 26 us of memory, which take 99 (rounded to 32 bits 56).  Wave w holds rows 16 (w % B) .. of R / |G| in
+// 26 us of memory, which take 94 (rounded to 32 bits 56).  Wave w holds rows 16 (w % B) .. of R / |G| in
 // registers and takes every (waves / B)th set of 16 long values of a run.  The lanes
 // run along the side that is contiguous in memory.
 // Steps from one S formed of M to the next: its error, of which the last of them sees a^2

@@ -32,7 +32,10 @@ struct OrthoArgs {
 constexpr int kOrthoRank = 128;
 constexpr int ortho_blocks(int p) { return (p + 15) / 16; }
 constexpr int ortho_tiles(int p) { return ortho_blocks(p) * (ortho_blocks(p) + 1) / 2; }
-constexpr int kOrthoNarrow = 4;   // tile rows up to which a workgroup iterates on its own
+// Tile rows up to which a workgroup iterates on its own.  Calls of 1, 5 and 32 adapters beside 11008 x 4096 so and
+// with a launch for each step: rank 48 49, 67 and 192 us against 56, 73 and 195; rank 64 68, 87 and 236 against
+// 65, 84 and 238.
+constexpr int kOrthoNarrow = 4;
 // fp64 values of a matrix's buffers in memory, for the iteration over many CUs.
 inline int64_t ortho_wide(int p) {
   const int64_t pp = 16 * ortho_blocks(p);

@@ -44,7 +44,7 @@ def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
     """(loss, lse), fp32 [n] each, of hidden states X [n, d] under the output head W
     [vocab, d] (both bf16 or both fp16; d a multiple of 8): loss = lse - z[target]
     with z = X W^T, which is never kept.  target int64 [n]; a value outside 0 .. vocab-1
-    (torch's -100) is no target: loss and lse are 0 and no work is spent on it.
+    (torch's -100) is no target: loss and lse are 0, whatever the token's X holds.
 
     The mean over a corpus, exponentiated, is a quantized model's perplexity; W may
     be a quantized head's w_hat rounded by round16."""
